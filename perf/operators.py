@@ -192,10 +192,10 @@ def exact_codes(x, block_rows):
     along = along.scatter_reduce(1, c.expand(rows, cols), x.abs(), "amax")
     top = torch.zeros(-(-rows // block_rows), blocks(cols), device=x.device, dtype=torch.float64)
     top = top.scatter_reduce(0, r[:, None].expand(rows, blocks(cols)), along, "amax")
-    s = torch.maximum(top, torch.full_like(top, TINY)) / TOP
-    q = nearest_e4m3(x / s[r][:, c])
+    top = torch.maximum(top, torch.full_like(top, TINY))
+    q = nearest_e4m3(x * TOP / top[r][:, c])
     kept = -(-cols // 16) * 16
-    return torch.cat([q, q.new_zeros(rows, kept - cols)], 1), s
+    return torch.cat([q, q.new_zeros(rows, kept - cols)], 1), top / TOP
 
 
 def exact(case, seed):
