@@ -75,7 +75,8 @@ extern "C" {
 
 typedef enum {
   SL_F16 = 1,     /* IEEE binary16 */
-  SL_F32 = 2,     /* IEEE binary32 (accepted for nothing but reported) */
+  SL_F32 = 2,     /* IEEE binary32: block scales and the block-scaled product's C and D, inputs of
+                     sl_quantize and sl_orthogonalize */
   SL_F8_E4M3 = 3, /* OCP MX E4M3 (bias 7, max 448, S.1111.111 = NaN) */
   SL_E8M0 = 4,    /* OCP MX E8M0 scale: 2^(b-127), 255 = NaN */
   SL_BF16 = 5,    /* bfloat16: binary32's sign and 8-bit exponent, 7 stored significand bits */
@@ -118,10 +119,13 @@ typedef struct {
   sl_tensor a;     /* (batch?, M, K)  f16, bf16, f8_e4m3 or f4_e2m1 (scaled) */
   sl_tensor b;     /* (batch?, N, K)  same dtype as a                      */
   sl_tensor c;     /* (batch?, M, N)  D's dtype; data == NULL means C = 0  */
-  sl_tensor d;     /* (batch?, M, N)  bf16 for bf16 a/b, else f16 output  */
-  sl_tensor sfa;   /* (batch?, M, ceil(K/block_k)) e8m0 (MXFP8) or f8_e4m3 (NVFP4) */
+  sl_tensor d;     /* (batch?, M, N)  bf16 for bf16 a/b, else f16 output (f16,
+                      bf16 or f32 with f32 scales)                         */
+  sl_tensor sfa;   /* (batch?, M, ceil(K/block_k)) e8m0 (MXFP8), f8_e4m3 (NVFP4)
+                      or f32 (block_k 128; M or ceil(M/128) rows)          */
   sl_tensor sfb;   /* (batch?, N, ceil(K/block_k)) same dtype as sfa       */
-  int32_t block_k; /* 32 for MXFP8, 16 for NVFP4; ignored for f16 / bf16   */
+  int32_t block_k; /* 32 for MXFP8, 16 for NVFP4, 128 with f32 scales;
+                      ignored for f16 / bf16                               */
   void* workspace;          /* device memory for a plan's workspace: split-K
                                fp32 partial sums or decoded NVFP4 operands
                                (NULL when the plan needs none) */
@@ -143,7 +147,10 @@ typedef struct {
                          8 waves when K == 0 or tile 4 is asked for),
                          8 mxfp8 (4 waves, 32x32x64 instruction,
                          LDS ring, scales in registers: scale rows of a
-                         multiple of 16 blocks on 16-byte boundaries) */
+                         multiple of 16 blocks on 16-byte boundaries),
+                         9 e4m3 with fp32 scales per 128 K (256x256 or
+                         128x128 tiles; up to 64 rows of A: tile_m 64, no
+                         LDS tiles, the waves of a workgroup split K) */
   int32_t a_load;     /* 0 K-contiguous vector, 1 M-contiguous vector (register
                          transpose), 2 generic, 3 M-contiguous direct copy into
                          an M-major LDS tile read by transposing reads, 4 NVFP4
@@ -178,6 +185,13 @@ typedef struct {
  * 16-byte boundaries (row strides multiples of 32 (fp4) or 64 (fp6)
  * elements), K % 512 == 0, and scale rows K-contiguous on 16-byte
  * boundaries with row strides multiples of 16.
+ * E4M3 with fp32 scales: a and b SL_F8_E4M3, sfa and sfb SL_F32, block_k
+ * 128: one scale per 128 consecutive K of each row, (batch?, M, ceil(K/128)),
+ * or of each 128 rows, (batch?, ceil(M/128), ceil(K/128)); sfb the same over
+ * N.  d (and c) f16, bf16 or f32.  Each block's sum is formed in the matrix
+ * core, multiplied by its two scales and added up in fp32.  Operands
+ * K-contiguous with rows on 16-byte boundaries and K % 16 == 0, scales of any
+ * strides (sl_quantize writes them).  No workspace.
  * Sizes: M, N, K and the batch count below 2^31 (else SL_ERR_SHAPE).  An
  * operand may span any number of bytes; 256 of its rows (one tile) must
  * span fewer than 2^31 bytes for the vector loaders of 16-bit operands
@@ -209,6 +223,71 @@ sl_status sl_gemm(const sl_gemm_args* args, void* stream);
  */
 #define SL_NO_ALLOC_SCRATCH_BYTES (32LL << 20)
 sl_status sl_gemm_no_alloc(const sl_gemm_args* args, void* stream);
+
+/*
+ * Block quantisation to E4M3.  A block is 128 consecutive values of a row of
+ * x, or 128 x 128 values (block_rows 128); the last block of an axis may be
+ * shorter.  With top = max(max |x|, 2^-100) over a block,
+ *     s = top / 448,   q = the E4M3 value nearest to 448 x / top,
+ * both quotients correctly rounded to fp32, ties of the code to even, so
+ * x ~ q s within half a step of E4M3.  A block holding a NaN or an infinity
+ * gets scale NaN and NaN codes.
+ *   x   (batch?, R, C)  f16, bf16 or f32, any strides
+ *   q   (batch?, R, Cq) f8_e4m3, C <= Cq <= 128 ceil(C / 128); columns from C
+ *       on are written as zeros (a product wants K a multiple of 16)
+ *   s   (batch?, ceil(R / block_rows), ceil(C / 128)) f32, any strides
+ *   qt, st  the same of x's transpose (its rows are x's columns, its blocks
+ *       run along x's rows): (batch?, C, Rq) and (batch?, ceil(C /
+ *       block_rows), ceil(R / 128)).  x is read once for both.
+ * q.data or qt.data NULL: that pair is not wanted (its other fields are
+ * ignored).  q and qt are contiguous along their last axis with rows on
+ * 16-byte boundaries; no output may broadcast or overlap x or another
+ * output.  An empty x is a no-op.  Asynchronous on `stream`, one kernel, no
+ * workspace; errors as sl_gemm, SL_ERR_ARG for another block_rows.
+ * Scales stored with the rows contiguous (strides (1, rows)) are the ones
+ * that sl_gemm's large tiles read fastest.
+ */
+typedef struct {
+  sl_tensor x;
+  sl_tensor q, s;
+  sl_tensor qt, st;
+  int32_t block_rows; /* 1 or 128 */
+} sl_quantize_args;
+sl_status sl_quantize(const sl_quantize_args* args, void* stream);
+
+/*
+ * Newton-Schulz orthogonalisation of an update:
+ *     X_0 = x / (|x|_F + 1e-7),
+ *     G = X_t X_t^T,  X_{t+1} = a X_t + (b G + c G^2) X_t,  d = X_steps,
+ * for each matrix of the batch, with X_t's shorter axis taken as its rows
+ * (a tall x gives the transpose of its transpose's result).
+ *   x  (batch?, M, N) f16, bf16 or f32, any strides
+ *   d  (batch?, M, N) f16 or bf16, any strides that do not broadcast; it may
+ *      be x itself (same pointer, dtype and layout), else not overlap it
+ *   steps         1 to 64
+ *   coefficients  host array of a, b, c for each step, each within 16 in
+ *                 magnitude; NULL: 3.4445, -4.7750, 2.0315 at every step
+ * The matrices between products are fp16 times 2^10 with sums in fp32, the
+ * sum of squares is in 64 bits: an iterate may reach 32 in magnitude (the
+ * default coefficients keep singular values below 1.3), beyond which d holds
+ * infinities or NaN.  An x that holds a NaN or an infinity gives a d of NaN; zero gives
+ * zero.  Results do not vary from call to call.
+ * workspace: device memory of sl_orthogonalize_workspace_bytes() bytes,
+ * 16-byte aligned, apart from x and d, not used by anything else until the
+ * call's kernels have finished on `stream`; its contents do not matter
+ * before or after.  An empty x is a no-op and needs none.  Asynchronous on
+ * `stream`; errors as sl_gemm, SL_ERR_ARG for steps or coefficients.
+ */
+typedef struct {
+  sl_tensor x;
+  sl_tensor d;
+  int32_t steps;
+  const float* coefficients;
+  void* workspace;
+  int64_t workspace_bytes;
+} sl_orthogonalize_args;
+sl_status sl_orthogonalize(const sl_orthogonalize_args* args, void* stream);
+sl_status sl_orthogonalize_workspace_bytes(const sl_orthogonalize_args* args, int64_t* bytes);
 
 /*
  * Planner overrides, read from the environment on every planning call (by

@@ -17,14 +17,15 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libstride_layouts_lds.so")
 
 SL_F16, SL_F32, SL_F8_E4M3, SL_E8M0, SL_BF16, SL_F4_E2M1, SL_F6_E2M3, SL_F6_E3M2 = 1, 2, 3, 4, 5, 6, 7, 8
-K_F16, K_F16_GENERIC, K_MX, K_MX_W8, K_NVFP4, K_MXFP4, K_MXFP6, K_MX_W4R = 1, 2, 3, 4, 5, 6, 7, 8
+K_F16, K_F16_GENERIC, K_MX, K_MX_W8, K_NVFP4, K_MXFP4, K_MXFP6, K_MX_W4R, K_BLOCK8 = 1, 2, 3, 4, 5, 6, 7, 8, 9
 STATUS = {0: "SL_OK", -1: "SL_ERR_NULL", -2: "SL_ERR_DTYPE", -3: "SL_ERR_SHAPE", -4: "SL_ERR_LAYOUT",
           -5: "SL_ERR_ALIGN", -6: "SL_ERR_ALIAS", -7: "SL_ERR_ARCH", -8: "SL_ERR_LAUNCH", -9: "SL_ERR_ARG"}
 
 # every symbol include/sl.h declares
 EXPORTS = ["sl_gemm", "sl_gemm_no_alloc", "sl_gemm_plan", "sl_gemm_workspace_bytes", "sl_status_string", "sl_last_error_message",
            "sl_abi_version", "sl_query_fragment_map", "sl_query_lds_map", "sl_query_fragment_addresses", "sl_probe_mfma",
-           "sl_probe_lds", "sl_layout_op", "sl_describe_plan"]
+           "sl_probe_lds", "sl_layout_op", "sl_describe_plan", "sl_quantize", "sl_orthogonalize",
+           "sl_orthogonalize_workspace_bytes"]
 
 # sl_layout_op operations (include/sl.h)
 LA_OPS = {"parse": 0, "coalesce": 1, "composition": 2, "complement": 3, "right_inverse": 4,
@@ -46,6 +47,17 @@ class sl_tensor(ctypes.Structure):
 class sl_gemm_args(ctypes.Structure):
     _fields_ = [("a", sl_tensor), ("b", sl_tensor), ("c", sl_tensor), ("d", sl_tensor), ("sfa", sl_tensor),
                 ("sfb", sl_tensor), ("block_k", ctypes.c_int32), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64)]
+
+
+class sl_quantize_args(ctypes.Structure):
+    _fields_ = [("x", sl_tensor), ("q", sl_tensor), ("s", sl_tensor), ("qt", sl_tensor), ("st", sl_tensor),
+                ("block_rows", ctypes.c_int32)]
+
+
+class sl_orthogonalize_args(ctypes.Structure):
+    _fields_ = [("x", sl_tensor), ("d", sl_tensor), ("steps", ctypes.c_int32),
+                ("coefficients", ctypes.POINTER(ctypes.c_float)), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_int64)]
 
 
@@ -104,6 +116,12 @@ def lib() -> ctypes.CDLL:
         L.sl_layout_op.argtypes = [i32, ctypes.c_char_p, ctypes.c_char_p, ctypes.c_char_p, i64, P(i64)]
         L.sl_describe_plan.restype = i32
         L.sl_describe_plan.argtypes = [P(sl_gemm_args), ctypes.c_char_p, i64, P(i64)]
+        L.sl_quantize.restype = i32
+        L.sl_quantize.argtypes = [P(sl_quantize_args), vp]
+        L.sl_orthogonalize.restype = i32
+        L.sl_orthogonalize.argtypes = [P(sl_orthogonalize_args), vp]
+        L.sl_orthogonalize_workspace_bytes.restype = i32
+        L.sl_orthogonalize_workspace_bytes.argtypes = [P(sl_orthogonalize_args), P(i64)]
         _lib = L
     return _lib
 
@@ -181,8 +199,8 @@ def make_args(a, b, c=None, d=None, sfa=None, sfb=None, block_k: int = 32, works
     return args
 
 
-def set_workspace(args: sl_gemm_args, workspace) -> None:
-    """Point args at a device tensor's bytes as the split-K workspace (None: none)."""
+def set_workspace(args, workspace) -> None:
+    """Point args at a device tensor's bytes as the call's workspace (None: none)."""
     if workspace is None:
         args.workspace, args.workspace_bytes = None, 0
     else:
@@ -231,24 +249,117 @@ def sl_gemm_plan(args: sl_gemm_args) -> dict:
 
 
 def gemm(a, b, c=None, out=None, sfa=None, sfb=None, block_k: int = 32, stream: Optional[int] = None,
-         workspace=None):
+         workspace=None, dtype=None):
     """D = A B^T + C on torch tensors (any strides).  ``a``: (batch?, M, K)
     fp16, bf16 or float8_e4m3fn; ``b``: (batch?, N, K); ``c``: (batch?, M, N)
     of D's dtype (bf16 for bf16 operands, else fp16) or None; ``sfa``/``sfb``: float8_e8m0fnu scales (batch?, rows, K/32) for
-    the MX form.  A plan's workspace (split-K partial sums, or NVFP4
+    the MX form, or float32 scales (batch?, rows or ceil(rows/128),
+    ceil(K/128)) with ``block_k`` 128 as ``quantize`` writes them, where D and
+    C may be fp16, bf16 or float32 (``dtype``, or ``out``'s).  A plan's workspace (split-K partial sums, or NVFP4
     operands decoded to fp16) is ``workspace`` (a device tensor) or, when
     None, a torch allocation of the size the library asks for.  Returns ``out`` (allocated by torch if None)."""
     import torch
     if out is None:
         batch = max(x.shape[0] if x is not None and x.dim() == 3 else 0 for x in (a, b, c))
         shape = (a.shape[-2], b.shape[-2]) if batch == 0 else (batch, a.shape[-2], b.shape[-2])
-        out = torch.empty(shape, dtype=torch.bfloat16 if a.dtype == torch.bfloat16 else torch.float16,
+        out = torch.empty(shape, dtype=dtype or (torch.bfloat16 if a.dtype == torch.bfloat16 else torch.float16),
                           device=a.device)
     args = make_args(a, b, c, out, sfa, sfb, block_k)
     if workspace is None:
         workspace = workspace_for(args, out.device)
     set_workspace(args, workspace)
     sl_gemm(args, stream)
+    return out
+
+
+def _stream(stream: Optional[int]) -> int:
+    if stream is not None:
+        return stream
+    import torch
+    return torch.cuda.current_stream().cuda_stream
+
+
+def sl_quantize(args: sl_quantize_args, stream: Optional[int] = None) -> None:
+    _check(lib().sl_quantize(ctypes.byref(args), ctypes.c_void_p(_stream(stream))))
+
+
+def sl_orthogonalize(args: sl_orthogonalize_args, stream: Optional[int] = None) -> None:
+    _check(lib().sl_orthogonalize(ctypes.byref(args), ctypes.c_void_p(_stream(stream))))
+
+
+def sl_orthogonalize_workspace_bytes(args: sl_orthogonalize_args) -> int:
+    n = ctypes.c_int64(0)
+    _check(lib().sl_orthogonalize_workspace_bytes(ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def _codes_and_scales(x, rows: int, cols: int, block_rows: int):
+    """Torch tensors for one of quantize's outputs: codes padded to whole
+    16-byte rows, scales stored with the rows contiguous."""
+    import torch
+    batch = tuple(x.shape[:-2])
+    q = torch.empty(batch + (rows, (cols + 15) // 16 * 16), dtype=torch.float8_e4m3fn, device=x.device)
+    s = torch.empty(batch + ((cols + 127) // 128, (rows + block_rows - 1) // block_rows), dtype=torch.float32,
+                    device=x.device)
+    return q, s.transpose(-2, -1)
+
+
+def quantize(x, block_rows: int = 1, transposed: bool = False, direct: bool = True, out=None,
+             stream: Optional[int] = None):
+    """E4M3 codes and float32 scales of a torch tensor ``x`` ((batch?, R, C),
+    fp16, bf16 or float32, any strides): one scale per 128 consecutive values
+    of a row, or per 128 x 128 values (``block_rows`` 128).  Returns (q, s);
+    with ``transposed`` also the codes and scales of x's transpose, blocked
+    along x's rows, from the same pass: (q, s, qt, st), or (qt, st) without
+    ``direct``.  Codes come with their columns padded with zeros to a multiple
+    of 16, ready for ``gemm(..., block_k=128)``.  ``out``: the same tuple of
+    the caller's tensors."""
+    if x.dim() not in (2, 3):
+        raise ValueError("quantize takes a matrix or a batch of matrices")
+    if not (direct or transposed):
+        raise ValueError("nothing to compute: neither direct nor transposed")
+    R, C = x.shape[-2:]
+    if out is None:
+        out = (_codes_and_scales(x, R, C, block_rows) if direct else ()) + \
+              (_codes_and_scales(x, C, R, block_rows) if transposed else ())
+    elif len(out) != 2 * (direct + transposed):
+        raise ValueError(f"out holds {len(out)} tensors, {2 * (direct + transposed)} are written")
+    args = sl_quantize_args()
+    args.x = tensor_desc(x)
+    if direct:
+        args.q, args.s = tensor_desc(out[0]), tensor_desc(out[1])
+    if transposed:
+        args.qt, args.st = tensor_desc(out[-2]), tensor_desc(out[-1])
+    args.block_rows = block_rows
+    sl_quantize(args, stream)
+    return out
+
+
+def orthogonalize(x, out=None, steps: int = 5, coefficients=None, workspace=None, stream: Optional[int] = None):
+    """Newton-Schulz orthogonalisation of each matrix of ``x`` ((batch?, M,
+    N), fp16, bf16 or float32, any strides) as include/sl.h states it.
+    ``coefficients``: (a, b, c) for every step or one triple per step (None:
+    the library's).  ``workspace``: a device tensor of at least
+    sl_orthogonalize_workspace_bytes, or None for a torch allocation.
+    Returns ``out`` (x's dtype, bf16 for float32, if None)."""
+    import torch
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.bfloat16 if x.dtype == torch.float32 else x.dtype, device=x.device)
+    args = sl_orthogonalize_args()
+    args.x, args.d, args.steps = tensor_desc(x), tensor_desc(out), steps
+    if coefficients is not None:
+        flat = np.asarray(coefficients, np.float32)
+        if flat.shape == (3,):
+            flat = np.tile(flat, (max(steps, 0), 1))
+        if flat.shape != (steps, 3):
+            raise ValueError(f"coefficients are (3,) or (steps, 3), got {flat.shape}")
+        flat = np.ascontiguousarray(flat)  # read before the call returns
+        args.coefficients = flat.ctypes.data_as(ctypes.POINTER(ctypes.c_float))
+    if workspace is None:
+        n = sl_orthogonalize_workspace_bytes(args)
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+    set_workspace(args, workspace)
+    sl_orthogonalize(args, stream)
     return out
 
 

@@ -1,0 +1,347 @@
+// gemm_block.hip -- the block-scaled product on E4M3 codes with fp32 scales
+// per 128 K:
+//   D[m,n] = C[m,n] + sum_j SA[m,j] SB[n,j] sum_{k in block j} A[m,k] B[n,k]
+// where a scale row covers one row of its operand or 128 of them.
+//
+// The matrix core sums one K block of 128 exactly as one 128-wide step on a
+// zero accumulator; its result, times the block's scale, is added to the
+// running fp32 sum by the vector unit (the hardware's own scale operands are
+// powers of two and cannot hold these).  A lane of the 16 x 16 result holds
+// four consecutive n of one m, so with SB constant over 128 rows of B that is
+// one multiply-add per value on top of one scale product per 16 rows of A.
+#include "sl_ops.hpp"
+
+#include "sl_device.hpp"
+
+namespace sl {
+namespace {
+
+constexpr int32_t kE4M3 = 0;  // CBSZ / BLGP format code
+
+__device__ __forceinline__ floatx4 mfma_block(const i32x8& a, const i32x8& b) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, floatx4{0.f, 0.f, 0.f, 0.f}, kE4M3, kE4M3, 0, 0, 0, 0);
+}
+
+template <int OT>
+__device__ __forceinline__ float block_load(const void* p, int64_t off) {
+  if constexpr (OT == OT_F32)
+    return ((const float*)p)[off];
+  else
+    return to_f32<OT == OT_F16 ? DT_F16 : DT_BF16>(((const uint16_t*)p)[off]);
+}
+template <int OT>
+__device__ __forceinline__ void block_store(void* p, int64_t off, float v) {
+  if constexpr (OT == OT_F32)
+    ((float*)p)[off] = v;
+  else
+    ((uint16_t*)p)[off] = from_f32<OT == OT_F16 ? DT_F16 : DT_BF16>(v);
+}
+
+// D(m, n .. n + 3) = v + C, where in range
+template <int OT>
+__device__ __forceinline__ void block_store_quad(const BlockGemmParams& p, int64_t batch, int64_t m, int64_t n, floatx4 v) {
+  if (m >= p.M || n >= p.N) return;
+  const bool whole = n + 4 <= p.N;
+  if (p.flags & BF_HAS_C) {
+    const int64_t off = batch * p.c_bs + m * p.c_rs + n * p.c_cs;
+    if (whole && (p.flags & BF_C_VEC)) {
+      if constexpr (OT == OT_F32) {
+        const floatx4 c = *(const floatx4*)((const float*)p.c + off);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] += c[r];
+      } else {
+        const u16x4 c = *(const u16x4*)((const uint16_t*)p.c + off);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] += to_f32<OT == OT_F16 ? DT_F16 : DT_BF16>(c[r]);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n + r < p.N) v[r] += block_load<OT>(p.c, off + r * p.c_cs);
+    }
+  }
+  const int64_t off = batch * p.d_bs + m * p.d_rs + n * p.d_cs;
+  if (whole && (p.flags & BF_D_VEC)) {
+    if constexpr (OT == OT_F32) {
+      *(floatx4*)((float*)p.d + off) = v;
+    } else {
+      constexpr int DT = OT == OT_F16 ? DT_F16 : DT_BF16;
+      *(u16x4*)((uint16_t*)p.d + off) = u16x4{from_f32<DT>(v[0]), from_f32<DT>(v[1]), from_f32<DT>(v[2]), from_f32<DT>(v[3])};
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (n + r < p.N) block_store<OT>(p.d, off + r * p.d_cs, v[r]);
+  }
+}
+
+__device__ __forceinline__ i32x8 join(const u32x4& lo, const u32x4& hi) {
+  return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+// how a tile reads SB: one scale for the wave's columns (128 x 128 blocks), or
+// one per row of B
+constexpr int SB_SQUARE = 0, SB_ROWS = 1;
+
+// BM x BN output tiles, the K-tiles of 128 bytes per row brought straight
+// into LDS two stages deep, as in the MXFP8 kernels.
+template <int BM, int BN, int WM, int WN, int SBK, int OT>
+__global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void gemm_block_kernel(const BlockGemmParams p) {
+  constexpr int NT = WM * WN * 64;
+  constexpr int TM = BM / WM, TN = BN / WN;
+  constexpr int FM = TM / 16, FN = TN / 16;
+  static_assert(128 % TN == 0, "a wave's columns lie in one square block");
+  constexpr int ABYTES = BM * kRowBytes, BBYTES = BN * kRowBytes;
+  constexpr int STAGE = ABYTES + BBYTES;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+
+  const int32_t lane = threadIdx.x & 63;
+  const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t wm = wave % WM, wn = wave / WM;
+  const TileCoord tc = map_tile(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.batch);
+  const int64_t m0 = (int64_t)tc.tm * BM, n0 = (int64_t)tc.tn * BN;
+  const int32_t rows_a = (int32_t)(p.M - m0 < BM ? p.M - m0 : BM);
+  const int32_t rows_b = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
+  LoaderKVec<BM, NT, 0, 1> la(p.a + tc.batch * p.a_bs + m0 * p.a_rs, rows_a, p.a_rs, 1, p.K, wave, lane);
+  LoaderKVec<BN, NT, 0, 1> lb(p.b + tc.batch * p.b_bs + n0 * p.b_rs, rows_b, p.b_rs, 1, p.K, wave, lane);
+  const int32_t a_row0 = wm * TM, b_row0 = wn * TN;
+
+  // scale pointers; rows past the operand read its last one (their results
+  // are not stored)
+  const float* sa_p[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    int64_t m = m0 + a_row0 + 16 * i + (lane & 15);
+    m = m < p.M ? m : p.M - 1;
+    sa_p[i] = p.sa + tc.batch * p.sa_bs + (m >> p.a_shift) * p.sa_rs;
+  }
+  const float* sb_base = p.sb + tc.batch * p.sb_bs;
+  int64_t nw = n0 + b_row0;
+  nw = nw < p.N ? nw : p.N - 1;
+  const float* sb_w = sb_base + (nw >> p.b_shift) * p.sb_rs;
+  int64_t sb_off[SBK == SB_ROWS ? FN : 1][4];
+  if constexpr (SBK == SB_ROWS) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        int64_t n = n0 + b_row0 + 16 * j + 4 * (lane >> 4) + r;
+        n = n < p.N ? n : p.N - 1;
+        sb_off[j][r] = (n >> p.b_shift) * p.sb_rs;
+      }
+  }
+
+  floatx4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+  const int32_t T = p.k_blocks;
+  if (T > 0) {
+    la.issue(0, smem);
+    lb.issue(0, smem + ABYTES);
+    wait_vmem();
+    __syncthreads();
+  }
+  for (int32_t t = 0; t < T; ++t) {
+    char* cur = smem + (t & 1) * STAGE;
+    char* nxt = smem + ((t + 1) & 1) * STAGE;
+    float sa[FM], sb[SBK == SB_ROWS ? FN : 1][4];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) sa[i] = sa_p[i][t * p.sa_ks];
+    if constexpr (SBK == SB_ROWS) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sb[j][r] = sb_base[sb_off[j][r] + t * p.sb_ks];
+    } else {
+      sb[0][0] = sb_w[t * p.sb_ks];
+    }
+    la.issue(t + 1, nxt);
+    lb.issue(t + 1, nxt + ABYTES);
+    i32x8 bf[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      bf[j] = join(*(const u32x4*)(cur + ABYTES + fragment_lds_offset(MFMA16_F8, lane, 0, b_row0 + 16 * j, 0, 0)),
+                   *(const u32x4*)(cur + ABYTES + fragment_lds_offset(MFMA16_F8, lane, 1, b_row0 + 16 * j, 0, 0)));
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const i32x8 af = join(*(const u32x4*)(cur + fragment_lds_offset(MFMA16_F8, lane, 0, a_row0 + 16 * i, 0, 0)),
+                            *(const u32x4*)(cur + fragment_lds_offset(MFMA16_F8, lane, 1, a_row0 + 16 * i, 0, 0)));
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const floatx4 t4 = mfma_block(bf[j], af);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float s = sa[i] * sb[SBK == SB_ROWS ? j : 0][SBK == SB_ROWS ? r : 0];
+          acc[i][j][r] = __builtin_fmaf(t4[r], s, acc[i][j][r]);
+        }
+      }
+    }
+    wait_vmem();
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      block_store_quad<OT>(p, tc.batch, m0 + a_row0 + 16 * i + (lane & 15), n0 + b_row0 + 16 * j + 4 * (lane >> 4), acc[i][j]);
+}
+
+// Few rows of A: the weight B is read once and bounds the call.  A workgroup
+// of 8 waves owns 16 FN rows of B and up to 16 FM rows of A; wave w takes the
+// K blocks w, w + 8, ... straight from memory into registers (a lane 32
+// consecutive bytes of its row; the order of K inside a block is free as long
+// as A and B share it), and the waves' sums meet in LDS.
+template <int FM, int FN, int OT>
+__global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_block_skinny_kernel(const BlockGemmParams p) {
+  __shared__ __attribute__((aligned(16))) float part[kSkinnyWaves - 1][FM * FN][64][4];
+  const int32_t lane = threadIdx.x & 63;
+  const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t id = blockIdx.x;
+  const int32_t tn = id % p.tiles_n, tm = id / p.tiles_n % p.tiles_m;
+  const int64_t batch = id / p.tiles_n / p.tiles_m;
+  const int64_t m0 = (int64_t)tm * kSkinnyRows, n0 = (int64_t)tn * (16 * FN);
+  const int32_t rows_a = (int32_t)(p.M - m0 < 16 * FM ? p.M - m0 : 16 * FM);
+  const int32_t rows_b = (int32_t)(p.N - n0 < 16 * FN ? p.N - n0 : 16 * FN);
+  const __amdgpu_buffer_rsrc_t ra =
+      make_rsrc(p.a + batch * p.a_bs + m0 * p.a_rs, (uint32_t)((rows_a - 1) * p.a_rs + p.K));
+  const __amdgpu_buffer_rsrc_t rb =
+      make_rsrc(p.b + batch * p.b_bs + n0 * p.b_rs, (uint32_t)((rows_b - 1) * p.b_rs + p.K));
+  const int32_t kl = 32 * (lane >> 4);
+  uint32_t off_a[FM], off_b[FN];
+  const float* sa_p[FM];
+  int64_t sb_off[FN][4];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int32_t r = 16 * i + (lane & 15);
+    off_a[i] = r < rows_a ? (uint32_t)(r * p.a_rs + kl) : kOutOfRange;
+    const int64_t m = m0 + (r < rows_a ? r : rows_a - 1);
+    sa_p[i] = p.sa + batch * p.sa_bs + (m >> p.a_shift) * p.sa_rs;
+  }
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int32_t r = 16 * j + (lane & 15);
+    off_b[j] = r < rows_b ? (uint32_t)(r * p.b_rs + kl) : kOutOfRange;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int32_t n = 16 * j + 4 * (lane >> 4) + e;
+      sb_off[j][e] = ((n0 + (n < rows_b ? n : rows_b - 1)) >> p.b_shift) * p.sb_rs;
+    }
+  }
+  const float* sb_base = p.sb + batch * p.sb_bs;
+
+  struct Regs {
+    u32x4 a[FM][2], b[FN][2];
+    float sa[FM], sb[FN][4];
+  };
+  const int32_t T = p.k_blocks;
+  auto load = [&](int32_t t, Regs& x) {
+    const int32_t k = t * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = t < T && k + kl + 16 * h < p.K;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        x.b[j][h] = __builtin_amdgcn_raw_buffer_load_b128(
+            rb, in && off_b[j] != kOutOfRange ? off_b[j] + (uint32_t)(k + 16 * h) : kOutOfRange, 0, 0);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        x.a[i][h] = __builtin_amdgcn_raw_buffer_load_b128(
+            ra, in && off_a[i] != kOutOfRange ? off_a[i] + (uint32_t)(k + 16 * h) : kOutOfRange, 0, 0);
+    }
+    const int64_t ts = t < T ? t : T - 1;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) x.sa[i] = sa_p[i][ts * p.sa_ks];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x.sb[j][e] = sb_base[sb_off[j][e] + ts * p.sb_ks];
+  };
+  floatx4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  auto step = [&](const Regs& x) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const floatx4 t4 = mfma_block(join(x.b[j][0], x.b[j][1]), join(x.a[i][0], x.a[i][1]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(t4[e], x.sa[i] * x.sb[j][e], acc[i][j][e]);
+      }
+  };
+  if (wave < T) {
+    Regs x, y;
+    load(wave, x);
+    for (int32_t t = wave; t < T; t += 2 * kSkinnyWaves) {
+      load(t + kSkinnyWaves, y);
+      step(x);
+      if (t + kSkinnyWaves >= T) break;
+      load(t + 2 * kSkinnyWaves, x);
+      step(y);
+    }
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) *(floatx4*)part[wave - 1][i * FN + j][lane] = acc[i][j];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      floatx4 v = acc[i][j];
+      for (int w = 0; w < kSkinnyWaves - 1; ++w) {
+        const floatx4 o = *(const floatx4*)part[w][i * FN + j][lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += o[e];
+      }
+      block_store_quad<OT>(p, batch, m0 + 16 * i + (lane & 15), n0 + 16 * j + 4 * (lane >> 4), v);
+    }
+}
+
+template <int OT>
+hipError_t go(const BlockGemmParams& p, int32_t tile, hipStream_t s) {
+  const dim3 grid((uint32_t)((int64_t)p.batch * p.tiles_m * p.tiles_n));
+  const bool square = p.b_shift != 0;
+  if (tile == BT_256x256) {
+    if (square) hipLaunchKernelGGL((gemm_block_kernel<256, 256, 2, 4, SB_SQUARE, OT>), grid, dim3(512), 0, s, p);
+    else hipLaunchKernelGGL((gemm_block_kernel<256, 256, 2, 4, SB_ROWS, OT>), grid, dim3(512), 0, s, p);
+  } else if (tile == BT_128x128) {
+    if (square) hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, SB_SQUARE, OT>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, SB_ROWS, OT>), grid, dim3(256), 0, s, p);
+  } else if (tile == BT_SKINNY) {
+    const dim3 block(kSkinnyWaves * 64);
+    const bool wide = skinny_cols(p.M, p.N, p.batch) == 32;
+    const int fm = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
+    if (fm == 1 && wide) hipLaunchKernelGGL((gemm_block_skinny_kernel<1, 2, OT>), grid, block, 0, s, p);
+    if (fm == 1 && !wide) hipLaunchKernelGGL((gemm_block_skinny_kernel<1, 1, OT>), grid, block, 0, s, p);
+    if (fm == 2 && wide) hipLaunchKernelGGL((gemm_block_skinny_kernel<2, 2, OT>), grid, block, 0, s, p);
+    if (fm == 2 && !wide) hipLaunchKernelGGL((gemm_block_skinny_kernel<2, 1, OT>), grid, block, 0, s, p);
+    if (fm == 4 && wide) hipLaunchKernelGGL((gemm_block_skinny_kernel<4, 2, OT>), grid, block, 0, s, p);
+    if (fm == 4 && !wide) hipLaunchKernelGGL((gemm_block_skinny_kernel<4, 1, OT>), grid, block, 0, s, p);
+  } else {
+    return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gemm_block(const BlockGemmParams& p, int32_t tile, hipStream_t s) {
+  switch (p.type) {
+    case OT_F16: return go<OT_F16>(p, tile, s);
+    case OT_BF16: return go<OT_BF16>(p, tile, s);
+    case OT_F32: return go<OT_F32>(p, tile, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace sl

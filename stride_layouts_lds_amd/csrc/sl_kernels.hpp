@@ -27,7 +27,8 @@ enum KernelKind : int32_t {
   K_NVFP4 = 5,        // NVFP4 dequantised to exact fp16 tiles, fp16 MFMA (8 waves)
   K_MXFP4 = 6,        // MXFP4, 8 waves, v_mfma_scale 32x32x64 with E2M1 data
   K_MXFP6 = 7,        // MXFP6, 8 waves, v_mfma_scale 32x32x64 with E2M3 or E3M2 data
-  K_MX_W4R = 8        // MXFP8, 4 waves each 128x128, v_mfma_scale 32x32x64, LDS ring, scales in registers
+  K_MX_W4R = 8,       // MXFP8, 4 waves each 128x128, v_mfma_scale 32x32x64, LDS ring, scales in registers
+  K_BLOCK8 = 9        // E4M3 with fp32 scales per 128 K (sl_ops.hpp)
 };
 
 // Tile configurations the dispatcher can choose: rows of A, rows of B,
