@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence, Tuple
 
 import numpy as np
@@ -135,27 +136,64 @@ def _check(status: int) -> None:
 # descriptors
 # ---------------------------------------------------------------------------
 
+# A call's arguments are packed field by field into their bytes: filling the
+# ctypes structures one attribute at a time took 4 us a descriptor, several
+# times the launch itself.
+_TENSOR = struct.Struct("@Pi4xi4x6q")          # sl_tensor
+_GEMM_TAIL = struct.Struct("@i4xPq")           # sl_gemm_args from block_k
+assert _TENSOR.size == ctypes.sizeof(sl_tensor)
+assert 6 * _TENSOR.size + _GEMM_TAIL.size == ctypes.sizeof(sl_gemm_args)
+_QUANTIZE_TAIL = struct.Struct("@i4x")         # sl_quantize_args from block_rows
+assert 5 * _TENSOR.size + _QUANTIZE_TAIL.size == ctypes.sizeof(sl_quantize_args)
+_pack = _TENSOR.pack
+_ABSENT = _pack(0, 0, 2, 0, 0, 0, 0, 0, 0)
+
+
+def _fields(data: int, dtype: int, shape: Sequence[int], strides: Sequence[int]) -> bytes:
+    """sl_tensor's bytes."""
+    if len(shape) == 2:
+        return _pack(data, dtype, 2, shape[0], shape[1], 0, strides[0], strides[1], 0)
+    if len(shape) == 3:
+        return _pack(data, dtype, 3, *shape, *strides)
+    if len(shape) > 3:
+        raise ValueError(f"a descriptor holds up to 3 axes, got {len(shape)}")
+    pad = [0] * (3 - len(shape))  # the library refuses the rank
+    return _pack(data, dtype, len(shape), *shape, *pad, *strides, *pad)
+
+
 def desc(data: int, dtype: int, shape: Sequence[int], strides: Sequence[int]) -> sl_tensor:
     """A raw descriptor: pointer, sl_dtype, shape and element strides."""
-    t = sl_tensor()
-    t.data = data or None
-    t.dtype = dtype
-    t.layout.rank = len(shape)
-    for i, (n, s) in enumerate(zip(shape, strides)):
-        t.layout.shape[i] = int(n)
-        t.layout.stride[i] = int(s)
-    return t
+    return sl_tensor.from_buffer_copy(_fields(data or 0, dtype, [int(n) for n in shape], [int(n) for n in strides]))
+
+
+_codes: dict = {}  # torch dtype -> sl_dtype
 
 
 def _torch_dtype_code(x, override: Optional[int]) -> int:
-    import torch
     if override is not None:
         return override
-    table = {torch.float16: SL_F16, torch.bfloat16: SL_BF16, torch.float32: SL_F32, torch.float8_e4m3fn: SL_F8_E4M3,
-             torch.float8_e8m0fnu: SL_E8M0}
-    if x.dtype not in table:
+    if not _codes:
+        import torch
+        _codes.update({torch.float16: SL_F16, torch.bfloat16: SL_BF16, torch.float32: SL_F32,
+                       torch.float8_e4m3fn: SL_F8_E4M3, torch.float8_e8m0fnu: SL_E8M0})
+    if x.dtype not in _codes:
         raise TypeError(f"unsupported dtype {x.dtype}")
-    return table[x.dtype]
+    return _codes[x.dtype]
+
+
+def _record(x) -> bytes:
+    """The bytes of the descriptor of a torch tensor, a PackedTensor, None (an
+    absent operand) or a descriptor."""
+    if x is None:
+        return _ABSENT
+    if isinstance(x, sl_tensor):
+        return bytes(x)
+    if isinstance(x, PackedTensor):
+        return bytes(tensor_desc(x))
+    code = _codes.get(x.dtype)
+    if code is None:
+        return bytes(tensor_desc(x))
+    return _fields(x.data_ptr(), code, x.shape, x.stride())
 
 
 class PackedTensor:
@@ -191,11 +229,10 @@ def tensor_desc(x, dtype: Optional[int] = None) -> sl_tensor:
 def make_args(a, b, c=None, d=None, sfa=None, sfb=None, block_k: int = 32, workspace=None) -> sl_gemm_args:
     """Arguments from descriptors (sl_tensor) or torch tensors; ``workspace``
     is a device tensor (its bytes) or None."""
-    args = sl_gemm_args()
-    for name, v in (("a", a), ("b", b), ("c", c), ("d", d), ("sfa", sfa), ("sfb", sfb)):
-        setattr(args, name, v if isinstance(v, sl_tensor) else tensor_desc(v))
-    args.block_k = block_k
-    set_workspace(args, workspace)
+    args = sl_gemm_args.from_buffer_copy(b"".join((_record(a), _record(b), _record(c), _record(d), _record(sfa),
+                                                   _record(sfb), _GEMM_TAIL.pack(block_k, 0, 0))))
+    if workspace is not None:
+        set_workspace(args, workspace)
     return args
 
 
@@ -212,18 +249,21 @@ def set_workspace(args, workspace) -> None:
 # the entry points
 # ---------------------------------------------------------------------------
 
-def sl_gemm(args: sl_gemm_args, stream: Optional[int] = None) -> None:
+def _stream(stream: Optional[int]) -> ctypes.c_void_p:
+    """``stream``, or torch's current one on the current device (its handle
+    alone: building torch's Stream object for it takes 3 us)."""
     if stream is None:
         import torch
-        stream = torch.cuda.current_stream().cuda_stream
-    _check(lib().sl_gemm(ctypes.byref(args), ctypes.c_void_p(stream)))
+        stream = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return ctypes.c_void_p(stream)
+
+
+def sl_gemm(args: sl_gemm_args, stream: Optional[int] = None) -> None:
+    _check(lib().sl_gemm(ctypes.byref(args), _stream(stream)))
 
 
 def sl_gemm_no_alloc(args: sl_gemm_args, stream: Optional[int] = None) -> None:
-    if stream is None:
-        import torch
-        stream = torch.cuda.current_stream().cuda_stream
-    _check(lib().sl_gemm_no_alloc(ctypes.byref(args), ctypes.c_void_p(stream)))
+    _check(lib().sl_gemm_no_alloc(ctypes.byref(args), _stream(stream)))
 
 
 def sl_gemm_workspace_bytes(args: sl_gemm_args) -> int:
@@ -272,19 +312,12 @@ def gemm(a, b, c=None, out=None, sfa=None, sfb=None, block_k: int = 32, stream: 
     return out
 
 
-def _stream(stream: Optional[int]) -> int:
-    if stream is not None:
-        return stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
-
-
 def sl_quantize(args: sl_quantize_args, stream: Optional[int] = None) -> None:
-    _check(lib().sl_quantize(ctypes.byref(args), ctypes.c_void_p(_stream(stream))))
+    _check(lib().sl_quantize(ctypes.byref(args), _stream(stream)))
 
 
 def sl_orthogonalize(args: sl_orthogonalize_args, stream: Optional[int] = None) -> None:
-    _check(lib().sl_orthogonalize(ctypes.byref(args), ctypes.c_void_p(_stream(stream))))
+    _check(lib().sl_orthogonalize(ctypes.byref(args), _stream(stream)))
 
 
 def sl_orthogonalize_workspace_bytes(args: sl_orthogonalize_args) -> int:
@@ -298,10 +331,11 @@ def _codes_and_scales(x, rows: int, cols: int, block_rows: int):
     16-byte rows, scales stored with the rows contiguous."""
     import torch
     batch = tuple(x.shape[:-2])
+    blocks, scale_rows = (cols + 127) // 128, (rows + block_rows - 1) // block_rows
     q = torch.empty(batch + (rows, (cols + 15) // 16 * 16), dtype=torch.float8_e4m3fn, device=x.device)
-    s = torch.empty(batch + ((cols + 127) // 128, (rows + block_rows - 1) // block_rows), dtype=torch.float32,
-                    device=x.device)
-    return q, s.transpose(-2, -1)
+    s = torch.empty_strided(batch + (scale_rows, blocks), (blocks * scale_rows,) * len(batch) + (1, scale_rows),
+                            dtype=torch.float32, device=x.device)
+    return q, s
 
 
 def quantize(x, block_rows: int = 1, transposed: bool = False, direct: bool = True, out=None,
@@ -324,14 +358,9 @@ def quantize(x, block_rows: int = 1, transposed: bool = False, direct: bool = Tr
               (_codes_and_scales(x, C, R, block_rows) if transposed else ())
     elif len(out) != 2 * (direct + transposed):
         raise ValueError(f"out holds {len(out)} tensors, {2 * (direct + transposed)} are written")
-    args = sl_quantize_args()
-    args.x = tensor_desc(x)
-    if direct:
-        args.q, args.s = tensor_desc(out[0]), tensor_desc(out[1])
-    if transposed:
-        args.qt, args.st = tensor_desc(out[-2]), tensor_desc(out[-1])
-    args.block_rows = block_rows
-    sl_quantize(args, stream)
+    pair = lambda wanted, at: (_record(out[at]), _record(out[at + 1])) if wanted else (_ABSENT, _ABSENT)
+    sl_quantize(sl_quantize_args.from_buffer_copy(b"".join((_record(x), *pair(direct, 0), *pair(transposed, -2),
+                                                            _QUANTIZE_TAIL.pack(block_rows)))), stream)
     return out
 
 
