@@ -189,7 +189,9 @@ typedef struct {
  * 128: one scale per 128 consecutive K of each row, (batch?, M, ceil(K/128)),
  * or of each 128 rows, (batch?, ceil(M/128), ceil(K/128)); sfb the same over
  * N.  d (and c) f16, bf16 or f32.  Each block's sum is formed in the matrix
- * core, multiplied by its two scales and added up in fp32.  Operands
+ * core, multiplied by its two scales and added up in fp32; for f16 and bf16 d
+ * the block's sum keeps bits down to about 2^-16 of its largest product (the
+ * 8-bit instruction), for f32 d it is an fp32 sum of exact products.  Operands
  * K-contiguous with rows on 16-byte boundaries and K % 16 == 0, scales of any
  * strides (sl_quantize writes them).  No workspace.
  * Sizes: M, N, K and the batch count below 2^31 (else SL_ERR_SHAPE).  An
@@ -267,8 +269,9 @@ sl_status sl_quantize(const sl_quantize_args* args, void* stream);
  *   steps         1 to 64
  *   coefficients  host array of a, b, c for each step, each within 16 in
  *                 magnitude; NULL: 3.4445, -4.7750, 2.0315 at every step
- * The matrices between products are fp16 times 2^10 with sums in fp32, the
- * sum of squares is in 64 bits: an iterate may reach 32 in magnitude (the
+ * The matrices between products are fp16 times 2^10 (for f16 d pairs of fp16,
+ * the value and what its rounding left) with sums in fp32, the sum of squares
+ * is in 64 bits: an iterate may reach 32 in magnitude (the
  * default coefficients keep singular values below 1.3), beyond which d holds
  * infinities or NaN.  An x that holds a NaN or an infinity gives a d of NaN; zero gives
  * zero.  Results do not vary from call to call.

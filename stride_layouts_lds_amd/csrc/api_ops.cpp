@@ -49,9 +49,11 @@ static bool overlap(const View& x, const View& y, int64_t batch) {
 // The tile: up to 64 rows of A stream the weight once (the skinny kernel);
 // otherwise the tile with the least (workgroup rounds over the 256 CUs) x
 // (work of a tile), the 128 x 128 tile two to a CU and moving twice the
-// operand bytes per product.
-static int32_t choose_tile(int64_t batch, int64_t M, int64_t N) {
+// operand bytes per product.  fp32 results: 128 x 128 (the fp16 fragments of
+// the larger tile do not fit the registers: 4096 x 4096 x 8192 took 836 us).
+static int32_t choose_tile(int64_t batch, int64_t M, int64_t N, int32_t type) {
   if (M <= kSkinnyRows) return BT_SKINNY;
+  if (type == OT_F32) return BT_128x128;
   int32_t best = BT_256x256;
   double least = 1e300;
   for (int32_t t : {(int32_t)BT_256x256, (int32_t)BT_128x128}) {
@@ -152,7 +154,7 @@ sl_status plan_block(const sl_gemm_args* args, BlockPlan* out) {
   };
   p.flags = (has_c ? BF_HAS_C : 0) | (quads(D) ? BF_D_VEC : 0) | (has_c && quads(C) ? BF_C_VEC : 0);
 
-  P.tile = choose_tile(batch, M, N);
+  P.tile = choose_tile(batch, M, N, type);
   BlockTileShape ts = kBlockTiles[P.tile];
   if (P.tile == BT_SKINNY) ts.bn = skinny_cols(M, N, batch);
   p.tiles_m = (int32_t)ceil_div(M, ts.bm), p.tiles_n = (int32_t)ceil_div(N, ts.bn);
@@ -309,7 +311,7 @@ sl_status plan_orthogonalize(const sl_orthogonalize_args* args, OrthoPlan* P) {
   p.steps = args->steps;
   p.x = args->x.data, p.d = args->d.data;
   if (!sl::orthogonalize_grid_ok(X.batch, p.m, p.n)) return fail(SL_ERR_SHAPE, "x is too large");
-  P->ws_bytes = sl::orthogonalize_workspace(X.batch, p.m, p.n);
+  P->ws_bytes = sl::orthogonalize_workspace(X.batch, p.m, p.n, p.d_type);
   return SL_OK;
 }
 

@@ -3,12 +3,20 @@
 //   D[m,n] = C[m,n] + sum_j SA[m,j] SB[n,j] sum_{k in block j} A[m,k] B[n,k]
 // where a scale row covers one row of its operand or 128 of them.
 //
-// The matrix core sums one K block of 128 exactly as one 128-wide step on a
-// zero accumulator; its result, times the block's scale, is added to the
-// running fp32 sum by the vector unit (the hardware's own scale operands are
-// powers of two and cannot hold these).  A lane of the 16 x 16 result holds
-// four consecutive n of one m, so with SB constant over 128 rows of B that is
-// one multiply-add per value on top of one scale product per 16 rows of A.
+// The matrix core sums one K block of 128 on a zero accumulator; its result,
+// times the block's scale, is added to the running fp32 sum by the vector
+// unit (the hardware's own scale operands are powers of two and cannot hold
+// these).  A lane of the 16 x 16 result holds four consecutive n of one m, so
+// with SB constant over 128 rows of B that is one multiply-add per value on
+// top of one scale product per 16 rows of A.
+//
+// 16-bit results: one 128-wide step of the 8-bit instruction per K block.  It
+// aligns a block's products to the largest and drops bits below about 2^-16
+// of it (measured on normally distributed codes: 1.5e-5 of the result, every
+// 8-bit instruction alike), a tenth of fp16's rounding.  fp32 results would
+// show that, so for them the codes become fp16 in registers (exact) and four
+// steps of the fp16 instruction, at half the rate, sum the block (measured
+// 1e-8 of the result).
 #include "sl_ops.hpp"
 
 #include "sl_device.hpp"
@@ -18,8 +26,47 @@ namespace {
 
 constexpr int32_t kE4M3 = 0;  // CBSZ / BLGP format code
 
-__device__ __forceinline__ floatx4 mfma_block(const i32x8& a, const i32x8& b) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, floatx4{0.f, 0.f, 0.f, 0.f}, kE4M3, kE4M3, 0, 0, 0, 0);
+// A lane's 32 codes of one K block, as the instruction takes them.
+struct FragF8 {
+  i32x8 v;
+  __device__ __forceinline__ FragF8() {}
+  __device__ __forceinline__ FragF8(const u32x4& lo, const u32x4& hi)
+      : v{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]} {}
+};
+struct FragF16 {
+  half8 v[4];
+  __device__ __forceinline__ FragF16() {}
+  __device__ __forceinline__ FragF16(const u32x4& lo, const u32x4& hi) {
+    typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t w0 = q < 2 ? lo[2 * q] : hi[2 * q - 4], w1 = q < 2 ? lo[2 * q + 1] : hi[2 * q - 3];
+      const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, false);
+      const half2v b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, true);
+      const half2v c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, false);
+      const half2v d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, true);
+      v[q] = half8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    }
+  }
+};
+template <int OT>
+struct FragOf {
+  typedef FragF8 type;
+};
+template <>
+struct FragOf<OT_F32> {
+  typedef FragF16 type;
+};
+
+__device__ __forceinline__ floatx4 mfma_block(const FragF8& a, const FragF8& b) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, floatx4{0.f, 0.f, 0.f, 0.f}, kE4M3, kE4M3, 0, 0, 0, 0);
+}
+// the order of K inside a block is free as long as both operands share it
+__device__ __forceinline__ floatx4 mfma_block(const FragF16& a, const FragF16& b) {
+  floatx4 t = mfma16<DT_F16>(a.v[0], b.v[0], floatx4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+  for (int q = 1; q < 4; ++q) t = mfma16<DT_F16>(a.v[q], b.v[q], t);
+  return t;
 }
 
 template <int OT>
@@ -75,10 +122,6 @@ __device__ __forceinline__ void block_store_quad(const BlockGemmParams& p, int64
   }
 }
 
-__device__ __forceinline__ i32x8 join(const u32x4& lo, const u32x4& hi) {
-  return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-}
-
 // how a tile reads SB: one scale for the wave's columns (128 x 128 blocks), or
 // one per row of B
 constexpr int SB_SQUARE = 0, SB_ROWS = 1;
@@ -87,6 +130,7 @@ constexpr int SB_SQUARE = 0, SB_ROWS = 1;
 // into LDS two stages deep, as in the MXFP8 kernels.
 template <int BM, int BN, int WM, int WN, int SBK, int OT>
 __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void gemm_block_kernel(const BlockGemmParams p) {
+  typedef typename FragOf<OT>::type Frag;
   constexpr int NT = WM * WN * 64;
   constexpr int TM = BM / WM, TN = BN / WN;
   constexpr int FM = TM / 16, FN = TN / 16;
@@ -160,15 +204,15 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void gemm_block_kernel(con
     }
     la.issue(t + 1, nxt);
     lb.issue(t + 1, nxt + ABYTES);
-    i32x8 bf[FN];
+    Frag bf[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j)
-      bf[j] = join(*(const u32x4*)(cur + ABYTES + fragment_lds_offset(MFMA16_F8, lane, 0, b_row0 + 16 * j, 0, 0)),
+      bf[j] = Frag(*(const u32x4*)(cur + ABYTES + fragment_lds_offset(MFMA16_F8, lane, 0, b_row0 + 16 * j, 0, 0)),
                    *(const u32x4*)(cur + ABYTES + fragment_lds_offset(MFMA16_F8, lane, 1, b_row0 + 16 * j, 0, 0)));
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const i32x8 af = join(*(const u32x4*)(cur + fragment_lds_offset(MFMA16_F8, lane, 0, a_row0 + 16 * i, 0, 0)),
-                            *(const u32x4*)(cur + fragment_lds_offset(MFMA16_F8, lane, 1, a_row0 + 16 * i, 0, 0)));
+      const Frag af(*(const u32x4*)(cur + fragment_lds_offset(MFMA16_F8, lane, 0, a_row0 + 16 * i, 0, 0)),
+                    *(const u32x4*)(cur + fragment_lds_offset(MFMA16_F8, lane, 1, a_row0 + 16 * i, 0, 0)));
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const floatx4 t4 = mfma_block(bf[j], af);
@@ -265,14 +309,20 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_block_skinny_kernel(co
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
   auto step = [&](const Regs& x) {
+    typedef typename FragOf<OT>::type Frag;
+    Frag bf[FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int j = 0; j < FN; ++j) bf[j] = Frag(x.b[j][0], x.b[j][1]);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const Frag af(x.a[i][0], x.a[i][1]);
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const floatx4 t4 = mfma_block(join(x.b[j][0], x.b[j][1]), join(x.a[i][0], x.a[i][1]));
+        const floatx4 t4 = mfma_block(bf[j], af);
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(t4[e], x.sa[i] * x.sb[j][e], acc[i][j][e]);
       }
+    }
   };
   if (wave < T) {
     Regs x, y;
@@ -311,9 +361,10 @@ template <int OT>
 hipError_t go(const BlockGemmParams& p, int32_t tile, hipStream_t s) {
   const dim3 grid((uint32_t)((int64_t)p.batch * p.tiles_m * p.tiles_n));
   const bool square = p.b_shift != 0;
-  if (tile == BT_256x256) {
-    if (square) hipLaunchKernelGGL((gemm_block_kernel<256, 256, 2, 4, SB_SQUARE, OT>), grid, dim3(512), 0, s, p);
-    else hipLaunchKernelGGL((gemm_block_kernel<256, 256, 2, 4, SB_ROWS, OT>), grid, dim3(512), 0, s, p);
+  if (tile == BT_256x256 && OT != OT_F32) {
+    constexpr int OT2 = OT == OT_F32 ? OT_F16 : OT;  // fp32 results have no such tile
+    if (square) hipLaunchKernelGGL((gemm_block_kernel<256, 256, 2, 4, SB_SQUARE, OT2>), grid, dim3(512), 0, s, p);
+    else hipLaunchKernelGGL((gemm_block_kernel<256, 256, 2, 4, SB_ROWS, OT2>), grid, dim3(512), 0, s, p);
   } else if (tile == BT_128x128) {
     if (square) hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, SB_SQUARE, OT>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, SB_ROWS, OT>), grid, dim3(256), 0, s, p);

@@ -5,11 +5,11 @@
 // strides).
 //
 // Three matrix products a step, all on the fp16 matrix cores with fp32 sums.
-// Between products X, G and B are kept as fp16 times 2^10: X's and G's values
+// Between products X, G and B are kept as fp16 times 2^10 (one plane), or for
+// fp16 results as that and what the rounding left (two): X's and G's values
 // stay below 2 and B's below 64 in magnitude for iterates of spectral norm
 // below 1.4, so nothing overflows, and a value keeps fp16's 11 bits down to
-// 2^-24; bf16's 8 bits would double the error of a 16-bit result.  x's sum of
-// squares is held in 64 bits and added up in a fixed order.
+// 2^-24.  x's sum of squares is held in 64 bits and added up in a fixed order.
 //
 // Every product reads both operands along their contiguous axis: G and B are
 // symmetric, and the product that makes X writes it in both orientations, so
@@ -67,12 +67,13 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(const OrthoParams p, do
   if (threadIdx.x == 0) parts[b * kNormParts + blockIdx.x] = s;
 }
 
-// X = 2^10 x / (|x| + 1e-7) as fp16, m x n and n x m, zero to the padded sizes
-template <int T>
+// X = 2^10 x / (|x| + 1e-7) as fp16, m x n and n x m, zero to the padded
+// sizes; with two planes also what the rounding left
+template <int T, int PLANES>
 __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, const double* parts, uint16_t* X,
                                                           uint16_t* XT, int32_t tiles_m, int32_t tiles_n) {
   __shared__ double lds[4];
-  __shared__ uint16_t tile[64][66];
+  __shared__ uint16_t tile[PLANES][64][66];
   const uint32_t id = blockIdx.x;
   const int32_t tn = id % tiles_n, tm = id / tiles_n % tiles_m;
   const int64_t b = id / tiles_n / tiles_m;
@@ -88,25 +89,35 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, c
     const int64_t i = i0 + il, j = j0 + jl;
     float v = 0.f;
     if (i < p.m && j < p.n) v = (float)(load_any<T>(p.x, b * p.x_bs + i * p.x_rs + j * p.x_cs) * f);
-    tile[il][jl] = from_f32<DT_F16>(v);
+#pragma unroll
+    for (int q = 0; q < PLANES; ++q) {
+      const uint16_t h = from_f32<DT_F16>(v);
+      tile[q][il][jl] = h;
+      v -= to_f32<DT_F16>(h);
+    }
   }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
-    const int32_t q = 4 * k + w;
-    X[b * mp * np + (i0 + q) * np + j0 + u] = tile[q][u];
-    XT[b * mp * np + (j0 + q) * mp + i0 + u] = tile[u][q];
+    const int32_t r = 4 * k + w;
+#pragma unroll
+    for (int q = 0; q < PLANES; ++q) {
+      X[PLANES * (b * mp * np + (i0 + r) * np) + q * np + j0 + u] = tile[q][r][u];
+      XT[PLANES * (b * mp * np + (j0 + r) * mp) + q * mp + i0 + u] = tile[q][u][r];
+    }
   }
 }
 
-// D = alpha P Q^T + beta E on fp16 operands with contiguous K
+// D = alpha P Q^T + beta E on fp16 operands with contiguous K.  `planes` 2: a
+// row of every matrix is its values rounded to fp16 and, behind them, what
+// that left, so the product is P0 Q0 + P0 Q1 + P1 Q0 and loses 2^-22.
 struct OrthoGemm {
-  const uint16_t *P, *Q, *E;   // (m, k), (n, k), (m, n)
+  const uint16_t *P, *Q, *E;   // (m, planes k), (n, planes k), (m, planes n)
   int64_t P_bs, Q_bs, E_bs;
   int32_t m, n, k;             // padded: multiples of 64
   float alpha, beta;
-  uint16_t* O;                 // (m, n), or NULL
-  uint16_t* OT;                // (n, m), or NULL
+  uint16_t* O;                 // (m, planes n), or NULL
+  uint16_t* OT;                // (n, planes m), or NULL
   int64_t O_bs;
   int32_t sym;                 // only tiles on and above the diagonal, each stored twice (O = OT)
   int32_t tiles_m, tiles_n, batch;
@@ -134,7 +145,7 @@ __device__ __forceinline__ void ortho_tile(const OrthoGemm& g, uint32_t id, int3
   }
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int PLANES>
 __global__ __launch_bounds__(WM* WN * 64) void ortho_gemm_kernel(const OrthoGemm g) {
   constexpr int NT = WM * WN * 64;
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
@@ -149,24 +160,28 @@ __global__ __launch_bounds__(WM* WN * 64) void ortho_gemm_kernel(const OrthoGemm
   ortho_tile(g, blockIdx.x, batch, tm, tn);
   const int32_t m0 = tm * BM, n0 = tn * BN;
   const int32_t rows_a = g.m - m0 < BM ? g.m - m0 : BM, rows_b = g.n - n0 < BN ? g.n - n0 : BN;
-  LoaderKVec<BM, NT, 0, 2> la(g.P + batch * g.P_bs + (int64_t)m0 * g.k, rows_a, g.k, 1, g.k, wave, lane);
-  LoaderKVec<BN, NT, 0, 2> lb(g.Q + batch * g.Q_bs + (int64_t)n0 * g.k, rows_b, g.k, 1, g.k, wave, lane);
+  const int32_t kp = PLANES * g.k;
+  LoaderKVec<BM, NT, 0, 2> la(g.P + batch * g.P_bs + (int64_t)m0 * kp, rows_a, kp, 1, kp, wave, lane);
+  LoaderKVec<BN, NT, 0, 2> lb(g.Q + batch * g.Q_bs + (int64_t)n0 * kp, rows_b, kp, 1, kp, wave, lane);
   const int32_t a_row0 = wm * TM, b_row0 = wn * TN;
   floatx4 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-  const int32_t T = g.k / 64;
-  la.issue(0, smem);
-  lb.issue(0, smem + ABYTES);
+  // K-tiles: P0 Q0, with two planes then P0 Q1 and P1 Q0
+  const int32_t T1 = g.k / 64, T = PLANES == 2 ? 3 * T1 : T1;
+  auto issue = [&](int32_t t, char* at) {  // past the last K-tile: not read
+    la.issue(PLANES == 2 && t >= T1 ? t - T1 : t, at);
+    lb.issue(PLANES == 2 && t >= 2 * T1 ? t - 2 * T1 : t, at + ABYTES);
+  };
+  issue(0, smem);
   wait_vmem();
   __syncthreads();
   for (int32_t t = 0; t < T; ++t) {
     char* cur = smem + (t & 1) * STAGE;
     char* nxt = smem + ((t + 1) & 1) * STAGE;
-    la.issue(t + 1, nxt);  // past the last K-tile: out of range, zeros
-    lb.issue(t + 1, nxt + ABYTES);
+    issue(t + 1, nxt);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       half8 af[FM], bf[FN];
@@ -188,81 +203,111 @@ __global__ __launch_bounds__(WM* WN * 64) void ortho_gemm_kernel(const OrthoGemm
   const bool mirror = g.sym && tm != tn;
   const bool transposed = g.d ? g.d_rs == 1 && g.d_cs != 1 : g.OT && (!g.sym || mirror);
   uint16_t* region = (uint16_t*)smem + wave * (TN * PITCH);
+  const int64_t np = (int64_t)PLANES * g.n, mp = (int64_t)PLANES * g.m;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int32_t ml = 16 * i + (lane & 15), m = m0 + a_row0 + ml;
+    const int32_t m = m0 + a_row0 + 16 * i + (lane & 15);
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
-      const int32_t nl = 16 * j + 4 * (lane >> 4), n = n0 + b_row0 + nl;
-      const bool in = m < g.m && n < g.n;
+      const int32_t n = n0 + b_row0 + 16 * j + 4 * (lane >> 4);
       floatx4 v = acc[i][j];
 #pragma unroll
       for (int r = 0; r < 4; ++r) v[r] *= g.alpha;
-      if (g.E && in) {
-        const u16x4 e = *(const u16x4*)(g.E + batch * g.E_bs + (int64_t)m * g.n + n);
+      if (g.E && m < g.m && n < g.n) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(g.beta, to_f32<DT_F16>(e[r]), v[r]);
-      }
-      u16x4 h;
-      if (g.d && g.d_type == OT_BF16)
-        h = u16x4{from_f32<DT_BF16>(v[0]), from_f32<DT_BF16>(v[1]), from_f32<DT_BF16>(v[2]), from_f32<DT_BF16>(v[3])};
-      else
-        h = u16x4{from_f32<DT_F16>(v[0]), from_f32<DT_F16>(v[1]), from_f32<DT_F16>(v[2]), from_f32<DT_F16>(v[3])};
-      if (transposed) {
+        for (int q = PLANES - 1; q >= 0; --q) {
+          const u16x4 e = *(const u16x4*)(g.E + batch * g.E_bs + m * np + q * g.n + n);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) region[(nl + r) * PITCH + ml] = h[r];
-      }
-      if (g.d) {
-        if (!transposed) {
-          uint16_t* D = (uint16_t*)g.d + batch * g.d_bs + m * g.d_rs;
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (m < g.rows && n + r < g.cols) D[(n + r) * g.d_cs] = h[r];
+          for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(g.beta, to_f32<DT_F16>(e[r]), v[r]);
         }
-      } else if (g.O && in) {
-        *(u16x4*)(g.O + batch * g.O_bs + (int64_t)m * g.n + n) = h;
       }
+      acc[i][j] = v;
     }
   }
-  if (!transposed) return;
-  // each wave reads back only its own region: the compiler's wait on the
-  // LDS writes is enough
-  constexpr int LPR = TM / 8, RPI = 64 / LPR;  // lanes per row of the region, rows per instruction
 #pragma unroll
-  for (int k = 0; k < TN / RPI; ++k) {
-    const int32_t nl = RPI * k + lane / LPR, ml = 8 * (lane % LPR);
-    const int32_t n = n0 + b_row0 + nl, m = m0 + a_row0 + ml;
-    const u16x8 h = *(const u16x8*)(region + nl * PITCH + ml);
-    if (g.d) {
-      uint16_t* D = (uint16_t*)g.d + batch * g.d_bs + n * g.d_cs + m;
+  for (int q = 0; q < PLANES; ++q) {
+    if (q > 0 && g.d) break;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (n < g.cols && m + e < g.rows) D[e] = h[e];
-    } else if (n < g.n && m < g.m) {
-      *(u16x8*)(g.OT + batch * g.O_bs + (int64_t)n * g.m + m) = h;
+    for (int i = 0; i < FM; ++i) {
+      const int32_t ml = 16 * i + (lane & 15), m = m0 + a_row0 + ml;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int32_t nl = 16 * j + 4 * (lane >> 4), n = n0 + b_row0 + nl;
+        const floatx4 v = acc[i][j];
+        u16x4 h;
+        if (g.d && g.d_type == OT_BF16) {
+          h = u16x4{from_f32<DT_BF16>(v[0]), from_f32<DT_BF16>(v[1]), from_f32<DT_BF16>(v[2]), from_f32<DT_BF16>(v[3])};
+        } else {
+          h = u16x4{from_f32<DT_F16>(v[0]), from_f32<DT_F16>(v[1]), from_f32<DT_F16>(v[2]), from_f32<DT_F16>(v[3])};
+          if (q + 1 < PLANES) {  // the next plane's: what this rounding left
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][j][r] = v[r] - to_f32<DT_F16>(h[r]);
+          }
+        }
+        if (transposed) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) region[(nl + r) * PITCH + ml] = h[r];
+        }
+        if (g.d) {
+          if (!transposed) {
+            uint16_t* D = (uint16_t*)g.d + batch * g.d_bs + m * g.d_rs;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (m < g.rows && n + r < g.cols) D[(n + r) * g.d_cs] = h[r];
+          }
+        } else if (g.O && m < g.m && n < g.n) {
+          *(u16x4*)(g.O + batch * g.O_bs + m * np + q * g.n + n) = h;
+        }
+      }
+    }
+    if (!transposed) continue;
+    // each wave reads back only its own region: the compiler's wait on the
+    // LDS writes is enough
+    constexpr int LPR = TM / 8, RPI = 64 / LPR;  // lanes per row of the region, rows per instruction
+#pragma unroll
+    for (int k = 0; k < TN / RPI; ++k) {
+      const int32_t nl = RPI * k + lane / LPR, ml = 8 * (lane % LPR);
+      const int32_t n = n0 + b_row0 + nl, m = m0 + a_row0 + ml;
+      const u16x8 h = *(const u16x8*)(region + nl * PITCH + ml);
+      if (g.d) {
+        uint16_t* D = (uint16_t*)g.d + batch * g.d_bs + n * g.d_cs + m;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n < g.cols && m + e < g.rows) D[e] = h[e];
+      } else if (n < g.n && m < g.m) {
+        *(u16x8*)(g.OT + batch * g.O_bs + n * mp + q * g.m + m) = h;
+      }
     }
   }
 }
 
-hipError_t run_gemm(OrthoGemm g, hipStream_t s) {
+hipError_t run_gemm(OrthoGemm g, int32_t planes, hipStream_t s) {
   g.tiles_m = (g.m + 127) / 128, g.tiles_n = (g.n + 127) / 128;
   const int64_t tiles = g.sym ? (int64_t)g.tiles_n * (g.tiles_n + 1) / 2 : (int64_t)g.tiles_m * g.tiles_n;
-  hipLaunchKernelGGL((ortho_gemm_kernel<128, 128, 2, 2>), dim3((uint32_t)(tiles * g.batch)), dim3(256), 0, s, g);
+  const dim3 grid((uint32_t)(tiles * g.batch));
+  if (planes == 2)
+    hipLaunchKernelGGL((ortho_gemm_kernel<128, 128, 2, 2, 2>), grid, dim3(256), 0, s, g);
+  else
+    hipLaunchKernelGGL((ortho_gemm_kernel<128, 128, 2, 2, 1>), grid, dim3(256), 0, s, g);
   return hipGetLastError();
 }
 
 template <int T>
-hipError_t start(const OrthoParams& p, double* parts, uint16_t* X, uint16_t* XT, int32_t tm, int32_t tn, hipStream_t s) {
+hipError_t start(int32_t planes, const OrthoParams& p, double* parts, uint16_t* X, uint16_t* XT, int32_t tm, int32_t tn, hipStream_t s) {
   hipLaunchKernelGGL(ortho_norm_kernel<T>, dim3(kNormParts, p.batch), dim3(256), 0, s, p, parts);
-  hipLaunchKernelGGL(ortho_start_kernel<T>, dim3((uint32_t)((int64_t)p.batch * tm * tn)), dim3(256), 0, s, p, parts, X, XT, tm, tn);
+  const dim3 grid((uint32_t)((int64_t)p.batch * tm * tn));
+  if (planes == 2)
+    hipLaunchKernelGGL((ortho_start_kernel<T, 2>), grid, dim3(256), 0, s, p, parts, X, XT, tm, tn);
+  else
+    hipLaunchKernelGGL((ortho_start_kernel<T, 1>), grid, dim3(256), 0, s, p, parts, X, XT, tm, tn);
   return hipGetLastError();
 }
 
 struct Places {
   size_t x, xt0, xt1, g, b, total;  // byte offsets behind the partial sums
 };
-Places places(int64_t batch, int64_t m, int64_t n) {
-  const size_t mn = (size_t)batch * pad64(m) * pad64(n) * 2, mm = (size_t)batch * pad64(m) * pad64(m) * 2;
+Places places(int64_t batch, int64_t m, int64_t n, int32_t planes) {
+  const size_t mn = (size_t)batch * pad64(m) * pad64(n) * 2 * planes, mm = (size_t)batch * pad64(m) * pad64(m) * 2 * planes;
   Places q;
   q.x = ((size_t)batch * kNormParts * 8 + 255) & ~(size_t)255;
   q.xt0 = q.x + mn;
@@ -275,29 +320,41 @@ Places places(int64_t batch, int64_t m, int64_t n) {
 
 }  // namespace
 
-size_t orthogonalize_workspace(int64_t batch, int64_t m, int64_t n) { return places(batch, m, n).total; }
+// fp16 results take two planes: with one, every matrix between products
+// rounded to fp16 costs them 1.1e-3 to 1.8e-3 (relative, 2-norm; 64-bit
+// simulation at 16 x 16 to 1000 x 1000), five times their own rounding of
+// 2.1e-4, with two 3e-7 at three times the products.  A bf16 result's own
+// rounding is 1.7e-3.
+namespace {
+int32_t planes_for(int32_t d_type) { return d_type == OT_F16 ? 2 : 1; }
+}  // namespace
+
+size_t orthogonalize_workspace(int64_t batch, int64_t m, int64_t n, int32_t d_type) {
+  return places(batch, m, n, planes_for(d_type)).total;
+}
 
 // every launch below fits a grid, and a 128-row tile 32-bit offsets
 bool orthogonalize_grid_ok(int64_t batch, int64_t m, int64_t n) {
   const int64_t lim = (int64_t)1 << 31;
   if (batch >= 65536 || m >= lim || n >= lim) return false;
-  return (double)batch * (double)(pad64(m) / 64) * (double)(pad64(n) / 64) < 0x1p31 && 256 * pad64(n) * 2 < lim;
+  return (double)batch * (double)(pad64(m) / 64) * (double)(pad64(n) / 64) < 0x1p31 && 256 * pad64(n) * 4 < lim;
 }
 
 hipError_t launch_orthogonalize(const OrthoParams& p, hipStream_t s) {
-  const Places q = places(p.batch, p.m, p.n);
+  const int32_t planes = planes_for(p.d_type);
+  const Places q = places(p.batch, p.m, p.n, planes);
   double* parts = (double*)p.ws;
   uint16_t* X = (uint16_t*)(p.ws + q.x);
   uint16_t* XT[2] = {(uint16_t*)(p.ws + q.xt0), (uint16_t*)(p.ws + q.xt1)};
   uint16_t* G = (uint16_t*)(p.ws + q.g);
   uint16_t* B = (uint16_t*)(p.ws + q.b);
   const int32_t mp = (int32_t)pad64(p.m), np = (int32_t)pad64(p.n);
-  const int64_t mn = (int64_t)mp * np, mm = (int64_t)mp * mp;
+  const int64_t mn = (int64_t)mp * np * planes, mm = (int64_t)mp * mp * planes;
   hipError_t e;
   switch (p.x_type) {
-    case OT_F16: e = start<OT_F16>(p, parts, X, XT[0], mp / 64, np / 64, s); break;
-    case OT_BF16: e = start<OT_BF16>(p, parts, X, XT[0], mp / 64, np / 64, s); break;
-    default: e = start<OT_F32>(p, parts, X, XT[0], mp / 64, np / 64, s); break;
+    case OT_F16: e = start<OT_F16>(planes, p, parts, X, XT[0], mp / 64, np / 64, s); break;
+    case OT_BF16: e = start<OT_BF16>(planes, p, parts, X, XT[0], mp / 64, np / 64, s); break;
+    default: e = start<OT_F32>(planes, p, parts, X, XT[0], mp / 64, np / 64, s); break;
   }
   for (int32_t k = 0; k < p.steps && e == hipSuccess; ++k) {
     const float a = p.coefficients[3 * k], b = p.coefficients[3 * k + 1], c = p.coefficients[3 * k + 2];
@@ -308,11 +365,11 @@ hipError_t launch_orthogonalize(const OrthoParams& p, hipStream_t s) {
     g.P = X, g.Q = X, g.P_bs = g.Q_bs = mn;
     g.m = g.n = mp, g.k = np, g.alpha = kDown;
     g.O = g.OT = G, g.O_bs = mm, g.sym = 1;
-    if ((e = run_gemm(g, s)) != hipSuccess) break;
+    if ((e = run_gemm(g, planes, s)) != hipSuccess) break;
     g.P = G, g.Q = G, g.E = G, g.P_bs = g.Q_bs = g.E_bs = mm;
     g.k = mp, g.alpha = c * kDown, g.beta = b;
     g.O = g.OT = B;
-    if ((e = run_gemm(g, s)) != hipSuccess) break;
+    if ((e = run_gemm(g, planes, s)) != hipSuccess) break;
     g.P = B, g.Q = XT[k & 1], g.E = X, g.Q_bs = g.E_bs = mn;
     g.n = np, g.alpha = kDown, g.beta = a, g.sym = 0;
     g.O = X, g.OT = XT[(k + 1) & 1], g.O_bs = mn;
@@ -321,7 +378,7 @@ hipError_t launch_orthogonalize(const OrthoParams& p, hipStream_t s) {
       g.d = p.d, g.d_type = p.d_type, g.rows = p.m, g.cols = p.n;
       g.d_bs = p.d_bs, g.d_rs = p.d_rs, g.d_cs = p.d_cs;
     }
-    e = run_gemm(g, s);
+    e = run_gemm(g, planes, s);
   }
   return e;
 }

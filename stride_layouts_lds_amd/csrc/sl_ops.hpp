@@ -84,8 +84,9 @@ hipError_t launch_gemm_block(const BlockGemmParams& p, int32_t tile, hipStream_t
 
 // ---------------------------------------------------------------------------
 // The orthogonalised update.  x is taken with m <= n (a tall x by its
-// strides, transposed); every matrix of the iteration is fp16, scaled by
-// 2^10, in the workspace, its sizes padded with zeros to multiples of 64.
+// strides, transposed); every matrix of the iteration is fp16 (for fp16
+// results two such planes), scaled by 2^10, in the workspace, its sizes
+// padded with zeros to multiples of 64.
 // ---------------------------------------------------------------------------
 struct OrthoParams {
   const void* x;               // (b, i, j), i < m, j < n
@@ -98,7 +99,7 @@ struct OrthoParams {
   char* ws;
 };
 constexpr int32_t kOrthoMaxSteps = 64;
-size_t orthogonalize_workspace(int64_t batch, int64_t m, int64_t n);
+size_t orthogonalize_workspace(int64_t batch, int64_t m, int64_t n, int32_t d_type);
 bool orthogonalize_grid_ok(int64_t batch, int64_t m, int64_t n);
 hipError_t launch_orthogonalize(const OrthoParams& p, hipStream_t stream);
 

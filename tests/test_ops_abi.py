@@ -1,0 +1,238 @@
+"""sl_quantize, sl_orthogonalize and the block-scaled form of sl_gemm on the
+host (no GPU): every check of their arguments runs before any HIP call, so a
+refusal is seen here; what passes the checks is planned, not run."""
+
+import ctypes
+import os
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def api():
+    from stride_layouts_lds_amd import api as A
+    if not os.path.exists(A.LIB_PATH):
+        from stride_layouts_lds_amd import build
+        build.build(verbose=False)
+    A.lib()
+    return A
+
+
+F16, F32, F8, E8M0, BF16 = 1, 2, 3, 4, 5
+X, Q, S, QT, ST, D, WS = (i << 36 for i in range(1, 8))
+
+
+def rm(ptr, shape, dtype, strides=None):
+    """A row-major descriptor's fields, or one with the given strides."""
+    if strides is None:
+        strides, acc = [0] * len(shape), 1
+        for i in reversed(range(len(shape))):
+            strides[i], acc = acc, acc * shape[i]
+    return ptr, dtype, shape, strides
+
+
+def refused(api, call, args, what):
+    with pytest.raises(api.SLError) as e:
+        call(args, 0)
+    assert api.STATUS[e.value.status] == what, str(e.value)
+    assert str(e.value)
+
+
+# ------------------------------------------------------------------ quantize
+
+def quantize_args(api, x, q=None, s=None, qt=None, st=None, block_rows=1):
+    a = api.sl_quantize_args()
+    for name, v in (("x", x), ("q", q), ("s", s), ("qt", qt), ("st", st)):
+        if v is not None:
+            setattr(a, name, api.desc(*v))
+        else:
+            getattr(a, name).layout.rank = 2
+    a.block_rows = block_rows
+    return a
+
+
+GOOD_Q = dict(x=rm(X, (256, 512), F16), q=rm(Q, (256, 512), F8), s=rm(S, (256, 4), F32),
+              qt=rm(QT, (512, 256), F8), st=rm(ST, (512, 2), F32))
+
+
+@pytest.mark.parametrize("change,what", [
+    (dict(x=rm(X, (256, 512), F8)), "SL_ERR_DTYPE"),
+    (dict(q=rm(Q, (256, 512), F16)), "SL_ERR_DTYPE"),
+    (dict(s=rm(S, (256, 4), F16)), "SL_ERR_DTYPE"),
+    (dict(block_rows=64), "SL_ERR_ARG"),
+    (dict(block_rows=0), "SL_ERR_ARG"),
+    (dict(x=rm(X, (512,), F16)), "SL_ERR_LAYOUT"),
+    (dict(x=rm(X, (256, 512), F16, (-512, 1))), "SL_ERR_LAYOUT"),
+    (dict(x=rm(X, (256, -512), F16, (512, 1))), "SL_ERR_SHAPE"),
+    (dict(q=rm(Q, (256, 496), F8)), "SL_ERR_SHAPE"),                     # fewer columns than x
+    (dict(q=rm(Q, (256, 528), F8)), "SL_ERR_SHAPE"),                     # past the last block
+    (dict(q=rm(Q, (255, 512), F8)), "SL_ERR_SHAPE"),
+    (dict(s=rm(S, (256, 3), F32)), "SL_ERR_SHAPE"),
+    (dict(s=rm(S, (2, 4), F32)), "SL_ERR_SHAPE"),                        # the square blocks' shape
+    (dict(qt=rm(QT, (256, 512), F8)), "SL_ERR_SHAPE"),                   # not transposed
+    (dict(st=rm(ST, (4, 256), F32)), "SL_ERR_SHAPE"),
+    (dict(q=rm(Q, (1, 256, 512), F8), x=rm(X, (2, 256, 512), F16)), "SL_ERR_SHAPE"),
+    (dict(x=rm(0, (256, 512), F16)), "SL_ERR_NULL"),
+    (dict(q=rm(0, (256, 512), F8), qt=rm(0, (512, 256), F8)), "SL_ERR_NULL"),
+    (dict(s=rm(0, (256, 4), F32)), "SL_ERR_NULL"),
+    (dict(x=rm(X + 1, (256, 512), F16)), "SL_ERR_ALIGN"),
+    (dict(s=rm(S + 2, (256, 4), F32)), "SL_ERR_ALIGN"),
+    (dict(q=rm(Q, (256, 512), F8, (1, 256))), "SL_ERR_LAYOUT"),          # columns not contiguous
+    (dict(q=rm(Q, (256, 512), F8, (520, 1))), "SL_ERR_LAYOUT"),          # rows off 16 bytes
+    (dict(q=rm(Q + 8, (256, 512), F8)), "SL_ERR_LAYOUT"),
+    (dict(q=rm(Q, (256, 512), F8, (0, 1))), "SL_ERR_LAYOUT"),            # broadcast output
+    (dict(s=rm(S, (256, 4), F32, (1, 0))), "SL_ERR_LAYOUT"),
+    (dict(q=rm(X, (256, 512), F8)), "SL_ERR_ALIAS"),
+    (dict(qt=rm(Q + 4096, (512, 256), F8)), "SL_ERR_ALIAS"),
+    (dict(st=rm(S + 16, (512, 2), F32)), "SL_ERR_ALIAS"),
+    (dict(x=rm(X, ((1 << 31) - 128, 1), F16)), "SL_ERR_SHAPE"),
+])
+def test_quantize_refuses(api, change, what):
+    refused(api, api.sl_quantize, quantize_args(api, **{**GOOD_Q, **change}), what)
+
+
+def test_quantize_null_args_and_empty(api):
+    assert api.lib().sl_quantize(None, None) == -1
+    for shape in ((0, 512), (256, 0)):
+        R, C = shape
+        kb = lambda n: (n + 127) // 128
+        api.sl_quantize(quantize_args(api, rm(0, shape, F16), rm(0, shape, F8), rm(0, (R, kb(C)), F32)), 0)
+        api.sl_quantize(quantize_args(api, rm(X, shape, F16), rm(Q, shape, F8), rm(S, (R, kb(C)), F32),
+                                      rm(QT, (C, R), F8), rm(ST, (C, kb(R)), F32)), 0)
+
+
+def test_quantize_python_refuses(api):
+    import torch
+    with pytest.raises(ValueError):
+        api.quantize(torch.zeros(128))
+    with pytest.raises(ValueError):
+        api.quantize(torch.zeros(4, 128), direct=False)
+    with pytest.raises(ValueError):
+        api.quantize(torch.zeros(4, 128), out=(1, 2, 3, 4))
+    with pytest.raises(TypeError):
+        api.quantize(torch.zeros(4, 128, dtype=torch.float64))
+
+
+# ------------------------------------------------------------ orthogonalize
+
+def ortho_args(api, x, d, steps=5, coefficients=None, ws=WS, ws_bytes=1 << 40):
+    a = api.sl_orthogonalize_args()
+    a.x, a.d, a.steps = api.desc(*x), api.desc(*d), steps
+    if coefficients is not None:
+        a.keep = (ctypes.c_float * len(coefficients))(*coefficients)
+        a.coefficients = ctypes.cast(a.keep, ctypes.POINTER(ctypes.c_float))
+    a.workspace, a.workspace_bytes = ws, ws_bytes
+    return a
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("change,what", [
+    (dict(x=rm(X, (96, 128), F8)), "SL_ERR_DTYPE"),
+    (dict(d=rm(D, (96, 128), F32)), "SL_ERR_DTYPE"),
+    (dict(steps=0), "SL_ERR_ARG"),
+    (dict(steps=65), "SL_ERR_ARG"),
+    (dict(steps=1, coefficients=(1.0, NAN, 0.0)), "SL_ERR_ARG"),
+    (dict(steps=1, coefficients=(INF, 0.0, 0.0)), "SL_ERR_ARG"),
+    (dict(steps=1, coefficients=(17.0, 0.0, 0.0)), "SL_ERR_ARG"),
+    (dict(d=rm(D, (128, 96), BF16)), "SL_ERR_SHAPE"),
+    (dict(d=rm(D, (2, 96, 128), BF16)), "SL_ERR_SHAPE"),
+    (dict(d=rm(D, (96, 128), BF16, (0, 1))), "SL_ERR_LAYOUT"),
+    (dict(d=rm(D, (96, 128), BF16, (1, 1))), "SL_ERR_LAYOUT"),
+    (dict(x=rm(X, (96, 128), BF16, (-128, 1))), "SL_ERR_LAYOUT"),
+    (dict(x=rm(0, (96, 128), BF16)), "SL_ERR_NULL"),
+    (dict(d=rm(0, (96, 128), BF16)), "SL_ERR_NULL"),
+    (dict(x=rm(X + 1, (96, 128), BF16)), "SL_ERR_ALIGN"),
+    (dict(d=rm(X + 2, (96, 128), BF16)), "SL_ERR_ALIAS"),                 # neither x itself nor apart from it
+    (dict(d=rm(X, (96, 128), BF16), x=rm(X, (96, 128), F32)), "SL_ERR_ALIAS"),
+    (dict(ws=0), "SL_ERR_NULL"),
+    (dict(ws_bytes=64), "SL_ERR_SHAPE"),
+    (dict(ws_bytes=-1), "SL_ERR_SHAPE"),
+    (dict(ws=WS + 8), "SL_ERR_ALIGN"),
+    (dict(ws=X), "SL_ERR_ALIAS"),
+    (dict(ws=D), "SL_ERR_ALIAS"),
+    (dict(x=rm(X, (70000, 4, 4), BF16), d=rm(D, (70000, 4, 4), BF16)), "SL_ERR_SHAPE"),
+])
+def test_orthogonalize_refuses(api, change, what):
+    good = dict(x=rm(X, (96, 128), BF16), d=rm(D, (96, 128), BF16))
+    refused(api, api.sl_orthogonalize, ortho_args(api, **{**good, **change}), what)
+
+
+def test_orthogonalize_null_empty_and_workspace(api):
+    assert api.lib().sl_orthogonalize(None, None) == -1
+    assert api.lib().sl_orthogonalize_workspace_bytes(None, None) == -1
+    empty = ortho_args(api, rm(0, (0, 128), BF16), rm(0, (0, 128), BF16), ws=0, ws_bytes=0)
+    assert api.sl_orthogonalize_workspace_bytes(empty) == 0
+    api.sl_orthogonalize(empty, 0)
+    size = lambda m, n, t=BF16: api.sl_orthogonalize_workspace_bytes(ortho_args(api, rm(X, (m, n), t), rm(D, (m, n), t)))
+    assert size(1000, 520) == size(520, 1000)  # a tall x is worked on transposed
+    assert size(2048, 4096) > size(1024, 4096) > 0
+
+
+def test_orthogonalize_python_refuses(api):
+    import torch
+    for c in ((1.0, 2.0), [(1.0, 2.0, 3.0)] * 4):
+        with pytest.raises(ValueError):
+            api.orthogonalize(torch.zeros(4, 4, dtype=torch.bfloat16), coefficients=c, steps=5)
+
+
+# ------------------------------------------------- the block-scaled product
+
+def gemm_args(api, a, b, d, sfa, sfb, c=None, block_k=128):
+    D_ = lambda v: api.desc(*v) if v is not None else None
+    return api.make_args(D_(a), D_(b), D_(c), D_(d), D_(sfa), D_(sfb), block_k)
+
+
+GOOD_P = dict(a=rm(X, (300, 512), F8), b=rm(Q, (200, 512), F8), d=rm(D, (300, 200), BF16), sfa=rm(S, (300, 4), F32),
+              sfb=rm(ST, (2, 4), F32))
+
+
+@pytest.mark.parametrize("change,what", [
+    (dict(b=rm(Q, (200, 512), F16)), "SL_ERR_DTYPE"),
+    (dict(sfb=rm(ST, (200, 4), E8M0)), "SL_ERR_DTYPE"),
+    (dict(d=rm(D, (300, 200), F8)), "SL_ERR_DTYPE"),
+    (dict(c=rm(QT, (300, 200), F16)), "SL_ERR_DTYPE"),
+    (dict(block_k=32), "SL_ERR_SHAPE"),
+    (dict(b=rm(Q, (200, 528), F8)), "SL_ERR_SHAPE"),
+    (dict(d=rm(D, (200, 300), BF16)), "SL_ERR_SHAPE"),
+    (dict(c=rm(QT, (300, 100), BF16)), "SL_ERR_SHAPE"),
+    (dict(sfa=rm(S, (300, 5), F32)), "SL_ERR_SHAPE"),
+    (dict(sfa=rm(S, (2, 4), F32)), "SL_ERR_SHAPE"),                        # 3 blocks of rows
+    (dict(sfb=rm(ST, (3, 4), F32)), "SL_ERR_SHAPE"),
+    (dict(a=rm(X, (2, 300, 512), F8)), "SL_ERR_SHAPE"),                    # d has one batch
+    (dict(a=rm(0, (300, 512), F8)), "SL_ERR_NULL"),
+    (dict(sfa=rm(0, (300, 4), F32)), "SL_ERR_NULL"),
+    (dict(d=rm(0, (300, 200), BF16)), "SL_ERR_NULL"),
+    (dict(d=rm(D + 1, (300, 200), BF16)), "SL_ERR_ALIGN"),
+    (dict(sfb=rm(ST + 2, (2, 4), F32)), "SL_ERR_ALIGN"),
+    (dict(a=rm(X, (300, 512), F8, (1, 300))), "SL_ERR_LAYOUT"),
+    (dict(a=rm(X, (300, 512), F8, (520, 1))), "SL_ERR_LAYOUT"),
+    (dict(a=rm(X + 8, (300, 512), F8)), "SL_ERR_LAYOUT"),
+    (dict(a=rm(X, (300, 504), F8, (512, 1)), b=rm(Q, (200, 504), F8, (512, 1))), "SL_ERR_LAYOUT"),
+    (dict(d=rm(D, (300, 200), BF16, (0, 1))), "SL_ERR_LAYOUT"),
+    (dict(d=rm(X, (300, 200), BF16)), "SL_ERR_ALIAS"),
+    (dict(d=rm(ST, (300, 200), BF16)), "SL_ERR_ALIAS"),
+    (dict(c=rm(D + 2, (300, 200), BF16)), "SL_ERR_ALIAS"),
+    (dict(a=rm(X, (300, 512), F8, (1 << 24, 1))), "SL_ERR_SHAPE"),         # a tile spans 2^31 bytes
+])
+def test_block_product_refuses(api, change, what):
+    args = gemm_args(api, **{**GOOD_P, **change})
+    for call in (api.sl_gemm, api.sl_gemm_no_alloc):
+        refused(api, call, args, what)
+
+
+def test_block_product_plans(api):
+    p = api.sl_gemm_plan(gemm_args(api, **GOOD_P))
+    assert p["kernel"] == api.K_BLOCK8 and p["tile_k"] == 128 and p["m"] == 300 and p["n"] == 200
+    # C may be D itself, broadcast, or absent; K = 0 and empty products are planned
+    api.sl_gemm_plan(gemm_args(api, **{**GOOD_P, "c": GOOD_P["d"]}))
+    api.sl_gemm_plan(gemm_args(api, **{**GOOD_P, "c": rm(QT, (300, 200), BF16, (0, 1))}))
+    api.sl_gemm_plan(gemm_args(api, rm(0, (300, 0), F8), rm(0, (200, 0), F8), GOOD_P["d"], rm(0, (300, 0), F32),
+                               rm(0, (2, 0), F32)))
+    api.sl_gemm(gemm_args(api, rm(X, (0, 512), F8), GOOD_P["b"], rm(D, (0, 200), BF16), rm(S, (0, 4), F32),
+                          GOOD_P["sfb"]), 0)
+    # the other 8-bit form is as before
+    mx = gemm_args(api, GOOD_P["a"], GOOD_P["b"], rm(D, (300, 200), F16), rm(S, (300, 16), E8M0),
+                   rm(ST, (200, 16), E8M0), block_k=32)
+    assert api.sl_gemm_plan(mx)["kernel"] in (api.K_MX, api.K_MX_W8, api.K_MX_W4R)
