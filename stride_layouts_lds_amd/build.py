@@ -20,7 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libstride_layouts_lds.so")
 SOURCES = ["api.cpp", "api_ops.cpp", "describe.cpp", "layout_algebra.cpp", "gemm_f16.hip", "gemm_mx.hip",
-           "gemm_block.hip", "quantize.hip", "orthogonalize.hip", "probes.hip", "scratch.hip"]
+           "gemm_block.hip", "quantize.hip", "orthogonalize.hip",
+           "ortho_gram.hip", "probes.hip", "scratch.hip"]
 HEADERS = ["sl_maps.hpp", "sl_kernels.hpp", "sl_ops.hpp", "sl_device.hpp", "layout_algebra.hpp", "describe.hpp",
            "api_common.hpp", "api_ops.hpp"]
 ARCH = "gfx950"

@@ -311,7 +311,8 @@ sl_status plan_orthogonalize(const sl_orthogonalize_args* args, OrthoPlan* P) {
   p.steps = args->steps;
   p.x = args->x.data, p.d = args->d.data;
   if (!sl::orthogonalize_grid_ok(X.batch, p.m, p.n)) return fail(SL_ERR_SHAPE, "x is too large");
-  P->ws_bytes = sl::orthogonalize_workspace(X.batch, p.m, p.n, p.d_type);
+  p.coefficients = P->coefficients;
+  P->ws_bytes = sl::orthogonalize_workspace(p);
   return SL_OK;
 }
 
@@ -352,7 +353,6 @@ sl_status sl_orthogonalize(const sl_orthogonalize_args* args, void* stream) {
   }
   if ((s = check_arch()) != SL_OK) return s;
   P.p.ws = (char*)args->workspace;
-  P.p.coefficients = P.coefficients;
   const hipError_t e = sl::launch_orthogonalize(P.p, (hipStream_t)stream);
   if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
   return SL_OK;

@@ -88,7 +88,7 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, c
     const int32_t il = along_rows ? u : 4 * k + w, jl = along_rows ? 4 * k + w : u;
     const int64_t i = i0 + il, j = j0 + jl;
     float v = 0.f;
-    if (i < p.m && j < p.n) v = (float)(load_any<T>(p.x, b * p.x_bs + i * p.x_rs + j * p.x_cs) * f);
+    if (i < p.m && j < p.n) v = as_computed((float)(load_any<T>(p.x, b * p.x_bs + i * p.x_rs + j * p.x_cs) * f));
 #pragma unroll
     for (int q = 0; q < PLANES; ++q) {
       const uint16_t h = from_f32<DT_F16>(v);
@@ -221,7 +221,8 @@ __global__ __launch_bounds__(WM* WN * 64) void ortho_gemm_kernel(const OrthoGemm
           for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(g.beta, to_f32<DT_F16>(e[r]), v[r]);
         }
       }
-      acc[i][j] = v;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = as_computed(v[r]);
     }
   }
 #pragma unroll
@@ -241,7 +242,7 @@ __global__ __launch_bounds__(WM* WN * 64) void ortho_gemm_kernel(const OrthoGemm
           h = u16x4{from_f32<DT_F16>(v[0]), from_f32<DT_F16>(v[1]), from_f32<DT_F16>(v[2]), from_f32<DT_F16>(v[3])};
           if (q + 1 < PLANES) {  // the next plane's: what this rounding left
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][j][r] = v[r] - to_f32<DT_F16>(h[r]);
+            for (int r = 0; r < 4; ++r) acc[i][j][r] = as_computed(v[r] - to_f32<DT_F16>(h[r]));
           }
         }
         if (transposed) {
@@ -329,8 +330,18 @@ namespace {
 int32_t planes_for(int32_t d_type) { return d_type == OT_F16 ? 2 : 1; }
 }  // namespace
 
-size_t orthogonalize_workspace(int64_t batch, int64_t m, int64_t n, int32_t d_type) {
-  return places(batch, m, n, planes_for(d_type)).total;
+// Up to 128 rows the Gram matrix's three launches (96 x 128: 123 us with the
+// launches below), unless the steps amplify too much for it.
+namespace {
+bool through_gram(const OrthoParams& p) {
+  float growth = 1.f;
+  for (int32_t t = 0; t < p.steps; ++t) growth *= fmaxf(1.f, fabsf(p.coefficients[3 * t]));
+  return p.m <= kGramRows && growth <= kGramGrowth;
+}
+}  // namespace
+
+size_t orthogonalize_workspace(const OrthoParams& p) {
+  return through_gram(p) ? ortho_gram_workspace(p) : places(p.batch, p.m, p.n, planes_for(p.d_type)).total;
 }
 
 // every launch below fits a grid, and a 128-row tile 32-bit offsets
@@ -341,6 +352,7 @@ bool orthogonalize_grid_ok(int64_t batch, int64_t m, int64_t n) {
 }
 
 hipError_t launch_orthogonalize(const OrthoParams& p, hipStream_t s) {
+  if (through_gram(p)) return launch_ortho_gram(p, s);
   const int32_t planes = planes_for(p.d_type);
   const Places q = places(p.batch, p.m, p.n, planes);
   double* parts = (double*)p.ws;

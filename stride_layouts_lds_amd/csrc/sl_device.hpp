@@ -51,6 +51,16 @@ __device__ __forceinline__ uint16_t from_f32(float v) {
     return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// A value both rounded to fp16 and used as it is: the compiler may otherwise
+// fuse the multiplication that made it into one rounding (a mixed-precision
+// multiply-add) for one of the two uses, and what is computed as left over by
+// the rounding then belongs to another one (off by a whole step of fp16, for
+// values next to a tie).
+__device__ __forceinline__ float as_computed(float v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
 using lds_void_t = __attribute__((address_space(3))) void;
 
 // A buffer load whose offset is at or beyond the resource's byte count

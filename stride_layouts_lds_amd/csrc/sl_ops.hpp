@@ -99,8 +99,30 @@ struct OrthoParams {
   char* ws;
 };
 constexpr int32_t kOrthoMaxSteps = 64;
-size_t orthogonalize_workspace(int64_t batch, int64_t m, int64_t n, int32_t d_type);
+size_t orthogonalize_workspace(const OrthoParams& p);
 bool orthogonalize_grid_ok(int64_t batch, int64_t m, int64_t n);
 hipError_t launch_orthogonalize(const OrthoParams& p, hipStream_t stream);
+
+// Through the Gram matrix (ortho_gram.hip): up to kGramRows rows, and steps
+// whose polynomials multiply to at most kGramGrowth at zero (that product is
+// Q's largest value, kept in fp16 times 2^6).
+constexpr int64_t kGramRows = 128;
+constexpr float kGramGrowth = 512.f;
+struct OrthoGramPlan {
+  int32_t rows;          // m padded: 32, 64, 96 or 128
+  int32_t splits, cols;  // ranges of columns, and the columns of one
+};
+OrthoGramPlan ortho_gram_plan(int64_t m, int64_t n);
+size_t ortho_gram_workspace(const OrthoParams& p);
+hipError_t launch_ortho_gram(const OrthoParams& p, hipStream_t stream);
+
+template <int T>
+struct OrthoElem {
+  typedef uint16_t type;
+};
+template <>
+struct OrthoElem<OT_F32> {
+  typedef uint32_t type;
+};
 
 }  // namespace sl
