@@ -8,7 +8,7 @@
 //   gram    a workgroup per range of columns: x's values times a power of two
 //           of its own (exact in fp16; fp32 values as a pair of fp16), their
 //           products on the fp16 matrix cores into fp32 partial sums.
-//   steps   one workgroup of 16 waves per matrix: sums the partials, takes
+//   steps   one workgroup of 8 waves per matrix: sums the partials, takes
 //           |x| from G's trace in 64 bits, and runs all steps in LDS.
 //   apply   a workgroup per 128 columns: d = Q X.
 //
@@ -212,12 +212,17 @@ __global__ __launch_bounds__(512) void gram_kernel(const OrthoParams p, const Or
 template <int MP>
 struct PairMatrix {
   static constexpr int PITCH = 4 * MP + 32, BYTES = MP * PITCH;
-  // the fragment of rows row0 .. + 15, K 32 ks .. + 31
+  // the fragment of rows row0 .. + 15, K 32 ks .. + 31, of a matrix in
+  // address space AS (3: LDS, 1: memory; a pointer that may be either would
+  // make every access wait for both)
+  template <int AS>
   static __device__ __forceinline__ half8 frag(const char* p, int32_t lane, int32_t row0, int32_t ks, int32_t plane) {
-    return *(const half8*)(p + (row0 + (lane & 15)) * PITCH + 2 * MP * plane + 64 * ks + 16 * (lane >> 4));
+    typedef const __attribute__((address_space(AS))) half8 elem;
+    return *(elem*)(p + (row0 + (lane & 15)) * PITCH + 2 * MP * plane + 64 * ks + 16 * (lane >> 4));
   }
-  // four consecutive values of a row, as a pair, at `scale`
-  static __device__ __forceinline__ void store(char* p, int32_t m, int32_t n, floatx4 v) {
+  // four consecutive values of a row, as a pair, and where asked for the
+  // mirrored four
+  static __device__ __forceinline__ void store_both(char* p, int32_t m, int32_t n, floatx4 v, bool mirror) {
     u16x4 h, l;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -227,6 +232,12 @@ struct PairMatrix {
     }
     *(u16x4*)(p + m * PITCH + 2 * n) = h;
     *(u16x4*)(p + m * PITCH + 2 * MP + 2 * n) = l;
+    if (!mirror) return;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      *(uint16_t*)(p + (n + r) * PITCH + 2 * m) = h[r];
+      *(uint16_t*)(p + (n + r) * PITCH + 2 * MP + 2 * m) = l[r];
+    }
   }
   static __device__ __forceinline__ floatx4 read(const char* p, int32_t m, int32_t n) {
     const u16x4 h = *(const u16x4*)(p + m * PITCH + 2 * n), l = *(const u16x4*)(p + m * PITCH + 2 * MP + 2 * n);
@@ -237,36 +248,46 @@ struct PairMatrix {
   }
 };
 
-// rows and columns of a wave's block
+// A product's blocks on and above the diagonal, dealt to the waves in turn
+constexpr int kStepWaves = 8;
 template <int MP>
 struct StepBlock {
-  static constexpr int F = MP <= 64 ? 1 : 2, BS = 16 * F, PER = MP / BS, N = PER * PER;
-  static_assert(N <= 16, "a block per wave");
+  static constexpr int F = MP <= 64 ? 1 : 2, BS = 16 * F, PER = MP / BS, N = PER * (PER + 1) / 2;
+  static constexpr int ONE = (N + kStepWaves - 1) / kStepWaves, TWO = (2 * N + kStepWaves - 1) / kStepWaves;  // blocks of a wave
 };
 
 // acc = the block of A B^T at rows m0 of A and n0 of B
-template <int MP, int F>
+template <int MP, int F, int BS = 3>
 __device__ __forceinline__ void pair_product(const char* A, const char* B, int32_t lane, int32_t m0, int32_t n0, floatx4 (&acc)[F][F]) {
   typedef PairMatrix<MP> M;
+  constexpr int KS = MP / 32;
 #pragma unroll
   for (int i = 0; i < F; ++i)
 #pragma unroll
     for (int j = 0; j < F; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  // the fragments of KC slices of 32 are requested together: one wave has
+  // little else to cover LDS latency with
+  constexpr int KC = KS <= 3 ? KS : 2;
 #pragma unroll
-  for (int ks = 0; ks < MP / 32; ++ks) {
-    half8 a[F][2], b[F][2];
+  for (int k0 = 0; k0 < KS; k0 += KC) {
+    half8 a[KC][F][2], b[KC][F][2];
 #pragma unroll
-    for (int i = 0; i < F; ++i)
+    for (int k = 0; k < KC; ++k)
 #pragma unroll
-      for (int z = 0; z < 2; ++z) a[i][z] = M::frag(A, lane, m0 + 16 * i, ks, z), b[i][z] = M::frag(B, lane, n0 + 16 * i, ks, z);
+      for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int i = 0; i < F; ++i)
+        for (int z = 0; z < 2; ++z) {
+          a[k][i][z] = M::template frag<3>(A, lane, m0 + 16 * i, k0 + k, z);
+          b[k][i][z] = M::template frag<BS>(B, lane, n0 + 16 * i, k0 + k, z);
+        }
 #pragma unroll
-      for (int j = 0; j < F; ++j) {
-        acc[i][j] = mfma16<DT_F16>(b[j][0], a[i][0], acc[i][j]);
-        acc[i][j] = mfma16<DT_F16>(b[j][1], a[i][0], acc[i][j]);
-        acc[i][j] = mfma16<DT_F16>(b[j][0], a[i][1], acc[i][j]);
-      }
+    for (int k = 0; k < KC; ++k)
+#pragma unroll
+      for (int z = 0; z < 3; ++z)  // P0 Q0, P0 Q1, P1 Q0
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+          for (int j = 0; j < F; ++j) acc[i][j] = mfma16<DT_F16>(b[k][j][z == 1], a[k][i][z == 2], acc[i][j]);
   }
 }
 
@@ -275,18 +296,18 @@ struct StepCoefficients {
 };
 
 // Q is the third matrix in LDS, or for MP = 128, where three do not fit, the
-// result's place in memory (read back through L1 by the workgroup that
-// wrote it).
+// result's place in memory: written once a step from P's place in LDS, when P
+// is no longer read, and read back by the workgroup that wrote it.
 template <int MP>
-__global__ __launch_bounds__(1024) void gram_steps_kernel(const OrthoParams p, const OrthoGramPlan pl, const float* parts,
+__global__ __launch_bounds__(64 * kStepWaves) void gram_steps_kernel(const OrthoParams p, const OrthoGramPlan pl, const float* parts,
                                                           const int32_t* exps, const StepCoefficients co, char* q_all,
                                                           double* norms) {
   typedef PairMatrix<MP> M;
   typedef StepBlock<MP> S;
-  constexpr int R = MP / 16, NT = R * (R + 1) / 2, TPW = (NT + 15) / 16;
+  constexpr int R = MP / 16, NT = R * (R + 1) / 2, TPW = (NT + kStepWaves - 1) / kStepWaves;
   constexpr bool Q_LDS = 3 * M::BYTES <= 150 * 1024;
   __shared__ __attribute__((aligned(16))) char smem[(Q_LDS ? 3 : 2) * M::BYTES];
-  __shared__ double traces[16];
+  __shared__ double traces[kStepWaves];
   char* G = smem;                 // G, then H = P G, then the next G
   char* P = smem + M::BYTES;
   const int64_t b = blockIdx.x;
@@ -303,7 +324,7 @@ __global__ __launch_bounds__(1024) void gram_steps_kernel(const OrthoParams p, c
   double trace = 0;
 #pragma unroll
   for (int u = 0; u < TPW; ++u) {
-    const int32_t id = wave + 16 * u;
+    const int32_t id = wave + kStepWaves * u;
     int32_t c = 0;
     while (tri(0, c + 1) <= id) ++c;
     tn[u] = c, tm[u] = id - tri(0, c);
@@ -325,7 +346,7 @@ __global__ __launch_bounds__(1024) void gram_steps_kernel(const OrthoParams p, c
   __syncthreads();
   trace = 0;
 #pragma unroll
-  for (int w = 0; w < 16; ++w) trace += traces[w];
+  for (int w = 0; w < kStepWaves; ++w) trace += traces[w];
   const double norm = ldexp(sqrt(trace), ex - kTop);
   const double f = ex < 128 ? 1.0 / (norm + 1e-7) : __builtin_nan("");
   if (threadIdx.x == 0) norms[b] = f;
@@ -333,30 +354,30 @@ __global__ __launch_bounds__(1024) void gram_steps_kernel(const OrthoParams p, c
   const float fg = (float)(fx * fx * (double)kGScale);
 #pragma unroll
   for (int u = 0; u < TPW; ++u) {
-    if (wave + 16 * u >= NT) continue;
+    if (wave + kStepWaves * u >= NT) continue;
     // lane: row lane % 16, columns 4 (lane / 16) .. + 3; and mirrored
     const int32_t m = 16 * tm[u] + (lane & 15), n = 16 * tn[u] + 4 * (lane >> 4);
     floatx4 v = g[u];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = as_computed(v[r] * fg);
-    M::store(G, m, n, v);
-    if (tm[u] != tn[u]) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint16_t h = from_f32<DT_F16>(v[r]);
-        *(uint16_t*)(G + (n + r) * M::PITCH + 2 * m) = h;
-        *(uint16_t*)(G + (n + r) * M::PITCH + 2 * MP + 2 * m) = from_f32<DT_F16>(v[r] - to_f32<DT_F16>(h));
-      }
-    }
+    for (int r = 0; r < 4; ++r) v[r] *= fg;
+    M::store_both(G, m, n, v, tm[u] != tn[u]);
   }
   __syncthreads();
 
-  constexpr int F = S::F;
-  const bool busy = wave < S::N;
-  const int32_t m0 = wave % S::PER * S::BS, n0 = wave / S::PER * S::BS;
-  const int32_t ml = m0 + (lane & 15), nl = n0 + 4 * (lane >> 4);
-  floatx4 acc[F][F], accq[F][F];
-  auto put = [&](char* to, const floatx4 (&x)[F][F], float scale) {
+  // Every product is symmetric: its blocks on and above the diagonal are
+  // computed, and those above stored a second time, mirrored.  H = P G and the
+  // next Q = P Q are computed at the same time.  Results wait in registers
+  // for the barrier after which their place is no longer read.
+  constexpr int F = S::F, N = S::N;
+  int32_t bm[S::TWO], bn[S::TWO];  // rows and columns of block (wave + 8 u) mod N
+#pragma unroll
+  for (int u = 0; u < S::TWO; ++u) {
+    const int32_t id = (wave + kStepWaves * u) % N;
+    int32_t c = 0;
+    while (tri(0, c + 1) <= id) ++c;
+    bm[u] = (id - tri(0, c)) * S::BS, bn[u] = c * S::BS;
+  }
+  auto put = [&](char* to, int u, const floatx4 (&x)[F][F], float scale) {
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
@@ -364,43 +385,80 @@ __global__ __launch_bounds__(1024) void gram_steps_kernel(const OrthoParams p, c
         floatx4 v = x[i][j];
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[r] *= scale;
-        M::store(to, ml + 16 * i, nl + 16 * j, v);
+        M::store_both(to, bm[u] + 16 * i + (lane & 15), bn[u] + 16 * j + 4 * (lane >> 4), v, bm[u] != bn[u]);
       }
   };
+  // a matrix in LDS to Q's place in memory
+  auto copy_out = [&](const char* from) {
+    for (int32_t i = threadIdx.x; i < M::BYTES / 16; i += 64 * kStepWaves) ((u32x4*)q_out)[i] = ((const u32x4*)from)[i];
+  };
+  floatx4 acc[S::TWO][F][F];
   for (int32_t t = 0; t < p.steps; ++t) {
     const bool last = t + 1 == p.steps;
     const float ca = co.v[3 * t], cb = co.v[3 * t + 1], cc = co.v[3 * t + 2];
-    if (busy) {
-      pair_product<MP, F>(G, G, lane, m0, n0, acc);
+#pragma unroll
+    for (int u = 0; u < S::ONE; ++u) {
+      if (wave + kStepWaves * u >= N) break;
+      pair_product<MP, F>(G, G, lane, bm[u], bn[u], acc[u]);
 #pragma unroll
       for (int i = 0; i < F; ++i)
 #pragma unroll
         for (int j = 0; j < F; ++j) {
-          const int32_t m = ml + 16 * i, n = nl + 16 * j;
+          const int32_t m = bm[u] + 16 * i + (lane & 15), n = bn[u] + 16 * j + 4 * (lane >> 4);
           const floatx4 e = M::read(G, m, n);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            float v = acc[i][j][r] * (cc * (kPScale / (kGScale * kGScale)));
+            float v = acc[u][i][j][r] * (cc * (kPScale / (kGScale * kGScale)));
             v = __builtin_fmaf(cb * (kPScale / kGScale), e[r], v);
-            acc[i][j][r] = m == n + r ? v + ca * kPScale : v;
+            acc[u][i][j][r] = m == n + r ? v + ca * kPScale : v;
           }
         }
-      if (!last || t > 0) put(P, acc, 1.f);
-      if (t == 0) put(last ? q_out : Q, acc, 1.f);
+      put(P, u, acc[u], 1.f);
+      if (Q_LDS && t == 0) put(Q, u, acc[u], 1.f);
     }
     __syncthreads();
-    if (t > 0 && busy) pair_product<MP, F>(P, Q, lane, m0, n0, accq);
-    if (!last && busy) pair_product<MP, F>(P, G, lane, m0, n0, acc);
+    if (!Q_LDS && t == 0) copy_out(P);
+    // blocks 0 .. N - 1 of H, then (from the second step on) those of Q
+    const int32_t h = last ? 0 : N, jobs = t > 0 ? h + N : h;
+#pragma unroll
+    for (int u = 0; u < S::TWO; ++u) {
+      const int32_t id = wave + kStepWaves * u;
+      if (id < h)
+        pair_product<MP, F>(P, G, lane, bm[u], bn[u], acc[u]);
+      else if (id < jobs)
+        pair_product<MP, F, Q_LDS ? 3 : 1>(P, Q, lane, bm[u], bn[u], acc[u]);
+    }
     __syncthreads();
-    if (t > 0 && busy) put(last ? q_out : Q, accq, 1.f / kPScale);
+#pragma unroll
+    for (int u = 0; u < S::TWO; ++u) {
+      const int32_t id = wave + kStepWaves * u;
+      if (id < h)
+        put(G, u, acc[u], 1.f / kGScale);
+      else if (id < jobs && (Q_LDS || last))
+        put(Q_LDS ? Q : P, u, acc[u], 1.f / kPScale);
+    }
+    __syncthreads();
     if (last) break;
-    if (busy) put(G, acc, 1.f / kGScale);
+    floatx4 next[S::ONE][F][F];
+#pragma unroll
+    for (int u = 0; u < S::ONE; ++u)
+      if (wave + kStepWaves * u < N) pair_product<MP, F>(G, P, lane, bm[u], bn[u], next[u]);
     __syncthreads();
-    if (busy) pair_product<MP, F>(G, P, lane, m0, n0, acc);
-    __syncthreads();
-    if (busy) put(G, acc, kGScale / (kPScale * kPScale));
+#pragma unroll
+    for (int u = 0; u < S::ONE; ++u)
+      if (wave + kStepWaves * u < N) put(G, u, next[u], kGScale / (kPScale * kPScale));
+    if (!Q_LDS && t > 0) {
+#pragma unroll
+      for (int u = 0; u < S::TWO; ++u) {
+        const int32_t id = wave + kStepWaves * u;
+        if (id >= h && id < jobs) put(P, u, acc[u], 1.f / kPScale);
+      }
+      __syncthreads();
+      copy_out(P);
+    }
     __syncthreads();
   }
+  if (Q_LDS || p.steps > 1) copy_out(Q_LDS ? Q : P);
 }
 
 // ---------------------------------------------------------------------------
@@ -429,6 +487,16 @@ __global__ __launch_bounds__(256) void gram_apply_kernel(const OrthoParams p, co
   uint32_t top = 0;
 #pragma unroll
   for (int q = 0; q < PPT; ++q) load8<T>(p, b, row_of(q), j0 + col_of(q), p.n, along_rows, v[q]);
+  // Q's fragments, all in flight before x's values are used
+  const char* Q = q_all + b * M::BYTES;
+  const int32_t m0 = wave % WM * (16 * FM), n0 = wave / WM * (16 * FN);
+  half8 a[MP / 32][FM][2];
+#pragma unroll
+  for (int ks = 0; ks < MP / 32; ++ks)
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) a[ks][i][z] = M::template frag<1>(Q, lane, m0 + 16 * i, ks, z);
 #pragma unroll
   for (int q = 0; q < PPT; ++q) top = top8(v[q], top);
   const int32_t ex = top_exponent(block_top<4>(top, tops));
@@ -447,8 +515,6 @@ __global__ __launch_bounds__(256) void gram_apply_kernel(const OrthoParams p, co
     }
   }
   __syncthreads();
-  const char* Q = q_all + b * M::BYTES;
-  const int32_t m0 = wave % WM * (16 * FM), n0 = wave / WM * (16 * FN);
   floatx4 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -456,11 +522,6 @@ __global__ __launch_bounds__(256) void gram_apply_kernel(const OrthoParams p, co
     for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int ks = 0; ks < MP / 32; ++ks) {
-    half8 a[FM][2];
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int z = 0; z < 2; ++z) a[i][z] = M::frag(Q, lane, m0 + 16 * i, ks, z);
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       half8 x[PX];
@@ -468,9 +529,9 @@ __global__ __launch_bounds__(256) void gram_apply_kernel(const OrthoParams p, co
       for (int z = 0; z < PX; ++z) x[z] = read_frag<LOAD_MNDMA, 128, 0>(smem + z * PLANE, lane, n0 + 16 * j, ks);
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        acc[i][j] = mfma16<DT_F16>(x[0], a[i][0], acc[i][j]);
-        acc[i][j] = mfma16<DT_F16>(x[0], a[i][1], acc[i][j]);
-        if constexpr (PX == 2) acc[i][j] = mfma16<DT_F16>(x[1], a[i][0], acc[i][j]);
+        acc[i][j] = mfma16<DT_F16>(x[0], a[ks][i][0], acc[i][j]);
+        acc[i][j] = mfma16<DT_F16>(x[0], a[ks][i][1], acc[i][j]);
+        if constexpr (PX == 2) acc[i][j] = mfma16<DT_F16>(x[1], a[ks][i][0], acc[i][j]);
       }
     }
   }
@@ -492,9 +553,25 @@ __global__ __launch_bounds__(256) void gram_apply_kernel(const OrthoParams p, co
   __syncthreads();
   uint16_t* d = (uint16_t*)p.d + b * p.d_bs;
   const bool d_rows = p.d_rs == 1 && p.d_cs != 1;
-  for (int32_t t = threadIdx.x; t < MP * 128; t += 256) {
-    const int32_t m = d_rows ? t % MP : t / 128, n = d_rows ? t / MP : t % 128;
-    if (m < p.m && j0 + n < p.n) d[m * p.d_rs + (j0 + n) * p.d_cs] = D[m * DP + n];
+  typedef uint16_t out8 __attribute__((ext_vector_type(8), aligned(2)));
+#pragma unroll
+  for (int q = 0; q < PPT; ++q) {
+    // eight consecutive of d's contiguous axis
+    const int32_t t = threadIdx.x + 256 * q;
+    const int32_t m = d_rows ? 8 * (t % (MP / 8)) : t / 16, n = d_rows ? t / (MP / 8) : 8 * (t % 16);
+    if (m >= p.m || j0 + n >= p.n) continue;
+    uint16_t* to = d + m * p.d_rs + (j0 + n) * p.d_cs;
+    const int64_t step = d_rows ? p.d_rs : p.d_cs, left = d_rows ? p.m - m : p.n - j0 - n;
+    uint16_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = D[(d_rows ? m + e : m) * DP + (d_rows ? n : n + e)];
+    if (step == 1 && left >= 8) {
+      *(out8*)to = out8{w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) to[e * step] = w[e];
+    }
   }
 }
 
@@ -523,7 +600,7 @@ hipError_t go(const OrthoParams& p, const OrthoGramPlan& pl, hipStream_t s) {
   for (int32_t i = 0; i < 3 * p.steps; ++i) co.v[i] = p.coefficients[i];
   const uint32_t tiles_n = (uint32_t)((p.n + 127) / 128);
   hipLaunchKernelGGL((gram_kernel<T, MP>), dim3((uint32_t)(p.batch * pl.splits)), dim3(512), 0, s, p, pl, parts, exps);
-  hipLaunchKernelGGL((gram_steps_kernel<MP>), dim3(p.batch), dim3(1024), 0, s, p, pl, parts, exps, co, q, norms);
+  hipLaunchKernelGGL((gram_steps_kernel<MP>), dim3(p.batch), dim3(64 * kStepWaves), 0, s, p, pl, parts, exps, co, q, norms);
   hipLaunchKernelGGL((gram_apply_kernel<T, MP>), dim3(tiles_n * p.batch), dim3(256), 0, s, p, q, norms, tiles_n);
   return hipGetLastError();
 }
