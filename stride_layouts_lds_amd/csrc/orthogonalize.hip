@@ -2,19 +2,26 @@
 //   X <- x / (|x|_F + 1e-7), then per step
 //   G = X X^T,  B = b G + c G^2,  X <- a X + B X,
 // x taken with no more rows than columns (a tall one transposed by its
-// strides).
+// strides).  Three ways, chosen by through_gram() below:
 //
-// Three matrix products a step, all on the fp16 matrix cores with fp32 sums.
-// Between products X, G and B are kept as fp16 times 2^10 (one plane), or for
-// fp16 results as that and what the rounding left (two): X's and G's values
-// stay below 2 and B's below 64 in magnitude for iterates of spectral norm
-// below 1.4, so nothing overflows, and a value keeps fp16's 11 bits down to
-// 2^-24.  x's sum of squares is held in 64 bits and added up in a fixed order.
+//   up to 128 rows     ortho_gram.hip: three launches
+//   Gram matrix        the same iteration on m x m matrices alone (G, P = a I
+//                      + b G + c G^2, Q <- P Q, G <- P G P, d = Q x), every one
+//                      a pair of fp16 planes; x times a power of two
+//   direct             the formula above; X one fp16 plane or, for fp16
+//                      results, a pair
 //
-// Every product reads both operands along their contiguous axis: G and B are
-// symmetric, and the product that makes X writes it in both orientations, so
-// none of them gathers.  G and G^2 are symmetric, so only the tiles on and
-// above the diagonal are computed; each is stored a second time, transposed.
+// All on the fp16 matrix cores with fp32 sums.  A plane holds values times a
+// power of two (2^10 for X, G and B of the direct way, 2^12 and 2^6 for the
+// other), so nothing overflows while the singular values of every iterate
+// stay below 2; a pair is a value rounded to fp16 and what that left, and its
+// products are P0 Q0 + P1 Q0 + P0 Q1.  x's sum of squares is held in 64 bits
+// and added up in a fixed order.
+//
+// G, B, P, Q and H = P G are symmetric (polynomials in G): only tiles on and
+// above the diagonal are computed, each stored a second time, transposed.  A
+// product with X as its second operand reads X along its contiguous axis n by
+// transposing LDS reads, so no transpose of X is kept.
 #include "sl_ops.hpp"
 
 #include "sl_device.hpp"
@@ -22,7 +29,6 @@
 namespace sl {
 namespace {
 
-constexpr float kDown = 0x1p-10f;  // what a stored value times it stands for
 constexpr int32_t kNormParts = 256;               // partial sums of squares of one matrix
 constexpr int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 
@@ -67,11 +73,19 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(const OrthoParams p, do
   if (threadIdx.x == 0) parts[b * kNormParts + blockIdx.x] = s;
 }
 
-// X = 2^10 x / (|x| + 1e-7) as fp16, m x n and n x m, zero to the padded
-// sizes; with two planes also what the rounding left
-template <int T, int PLANES>
+// What the products multiply by, one of each for every matrix.
+struct OrthoScales {
+  float gram;   // of x's planes' Gram matrix, to make G's plane (2^12 G)
+  float apply;  // of Q's plane times x's, to make d
+};
+
+// The planes that the products read: m x n, zero to the padded sizes.
+// EXACT: x times the power of two that brings |x| to 2^14 (to 2^15): exact in
+// fp16 but for what lies 2^-38 below |x|; the scales follow.  Else 2^10 x /
+// (|x| + 1e-7), rounded.  With two planes also what the rounding left.
+template <int T, int PLANES, bool EXACT>
 __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, const double* parts, uint16_t* X,
-                                                          uint16_t* XT, int32_t tiles_m, int32_t tiles_n) {
+                                                          OrthoScales* scales, int32_t tiles_m, int32_t tiles_n) {
   __shared__ double lds[4];
   __shared__ uint16_t tile[PLANES][64][66];
   const uint32_t id = blockIdx.x;
@@ -79,7 +93,15 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, c
   const int64_t b = id / tiles_n / tiles_m;
   const int64_t mp = 64 * (int64_t)tiles_m, np = 64 * (int64_t)tiles_n;
   const double sum = block_sum(parts[b * kNormParts + threadIdx.x], lds);
-  const double f = 1024.0 / (sqrt(sum) + 1e-7);
+  const double norm = sqrt(sum), inv = 1.0 / (norm + 1e-7);
+  double f = 1024.0 * inv;
+  if constexpr (EXACT) {
+    // infinite or NaN norms make every scale NaN
+    const int32_t e = norm > 0.0 && norm < __builtin_inf() ? ilogb(norm) : 0;
+    f = ldexp(1.0, 14 - e);
+    const double fx = norm < __builtin_inf() ? inv / f : __builtin_nan("");
+    if (tm == 0 && tn == 0 && threadIdx.x == 0) scales[b] = OrthoScales{(float)(fx * fx * 4096.0), (float)(fx / 64.0)};
+  }
   const int64_t i0 = 64 * (int64_t)tm, j0 = 64 * (int64_t)tn;
   const bool along_rows = p.x_rs == 1 && p.x_cs != 1;
   const int32_t u = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -101,298 +123,498 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, c
   for (int k = 0; k < 16; ++k) {
     const int32_t r = 4 * k + w;
 #pragma unroll
-    for (int q = 0; q < PLANES; ++q) {
-      X[PLANES * (b * mp * np + (i0 + r) * np) + q * np + j0 + u] = tile[q][r][u];
-      XT[PLANES * (b * mp * np + (j0 + r) * mp) + q * mp + i0 + u] = tile[q][u][r];
-    }
+    for (int q = 0; q < PLANES; ++q) X[PLANES * (b * mp * np + (i0 + r) * np) + q * np + j0 + u] = tile[q][r][u];
   }
 }
 
-// D = alpha P Q^T + beta E on fp16 operands with contiguous K.  `planes` 2: a
-// row of every matrix is its values rounded to fp16 and, behind them, what
-// that left, so the product is P0 Q0 + P0 Q1 + P1 Q0 and loses 2^-22.
+// D = alpha P Q^T + beta E + diag I (with `scaled`, alpha times the matrix's
+// own scale), P's planes K-contiguous, Q K-contiguous or (n_major) stored as
+// (k, n).  A row of a matrix of two planes is its first plane's values and
+// behind them the second's.  One or two products of the same P in one launch.
 struct OrthoGemm {
-  const uint16_t *P, *Q, *E;   // (m, planes k), (n, planes k), (m, planes n)
-  int64_t P_bs, Q_bs, E_bs;
-  int32_t m, n, k;             // padded: multiples of 64
-  float alpha, beta;
-  uint16_t* O;                 // (m, planes n), or NULL
-  uint16_t* OT;                // (n, planes m), or NULL
-  int64_t O_bs;
-  int32_t sym;                 // only tiles on and above the diagonal, each stored twice (O = OT)
+  const uint16_t* P;             // (m, PP k)
+  const uint16_t* Q[2];          // (n, PQ k), or (k, PQ n)
+  const uint16_t* E;             // (m, OP n), or NULL
+  uint16_t* O[2];                // (m, OP n); sym: and its transpose
+  int64_t P_bs, Q_bs, E_bs, O_bs;
+  int32_t m, n, k;               // padded: multiples of 64
+  float alpha[2], beta, diag;
+  const OrthoScales* scales;     // or NULL
+  int32_t scale_apply;           // which of them
+  int32_t sym;
+  int32_t products;              // 1 or 2
   int32_t tiles_m, tiles_n, batch;
-  // the last step's result instead of O and OT
+  // the last step's result instead of O
   void* d;
   int64_t rows, cols, d_bs, d_rs, d_cs;
   int32_t d_type;
 };
 
-// the tile of workgroup `id`: row-major, or for symmetric results the pairs
-// tm <= tn, column by column
-__device__ __forceinline__ void ortho_tile(const OrthoGemm& g, uint32_t id, int32_t& batch, int32_t& tm, int32_t& tn) {
+struct OrthoTile {
+  int32_t product, batch, tm, tn;
+  float alpha;
+};
+
+// the tile of workgroup `id`: for symmetric results the pairs tm <= tn,
+// column by column
+__device__ __forceinline__ OrthoTile ortho_tile(const OrthoGemm& g) {
+  OrthoTile o;
+  uint32_t id = blockIdx.x, total = gridDim.x / g.products;
+  o.product = id >= total;
+  id -= o.product * total;
   if (g.sym) {
     const uint32_t per = (uint32_t)g.tiles_n * (g.tiles_n + 1) / 2;
-    batch = id / per;
+    o.batch = id / per;
     const uint32_t t = id % per;
     int32_t c = (int32_t)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
     while ((uint32_t)c * (c + 1) / 2 > t) --c;
     while ((uint32_t)(c + 1) * (c + 2) / 2 <= t) ++c;
-    tn = c;
-    tm = (int32_t)(t - (uint32_t)c * (c + 1) / 2);
+    o.tn = c;
+    o.tm = (int32_t)(t - (uint32_t)c * (c + 1) / 2);
   } else {
-    const TileCoord tc = map_tile(id, gridDim.x, g.tiles_m, g.tiles_n, 8, g.batch);
-    batch = tc.batch, tm = tc.tm, tn = tc.tn;
+    const TileCoord tc = map_tile(id, total, g.tiles_m, g.tiles_n, 8, g.batch);
+    o.batch = tc.batch, o.tm = tc.tm, o.tn = tc.tn;
+  }
+  o.alpha = o.product ? g.alpha[1] : g.alpha[0];
+  if (g.scales) o.alpha *= g.scale_apply ? g.scales[o.batch].apply : g.scales[o.batch].gram;
+  return o;
+}
+
+// W consecutive values of D at (m, n ..), added to and stored; v: what is
+// stored in the mirrored place
+template <int OP, int W>
+__device__ __forceinline__ void ortho_emit(const OrthoGemm& g, const OrthoTile& o, int32_t m, int32_t n, float (&v)[W]) {
+  typedef uint16_t vec __attribute__((ext_vector_type(W)));
+  const int64_t at = o.batch * g.O_bs + (int64_t)m * (OP * (int64_t)g.n) + n;
+#pragma unroll
+  for (int e = 0; e < W; ++e) v[e] *= o.alpha;
+  if (g.E) {
+    const uint16_t* E = g.E + o.batch * g.E_bs + (int64_t)m * (OP * (int64_t)g.n) + n;
+#pragma unroll
+    for (int q = OP - 1; q >= 0; --q) {
+      const vec x = *(const vec*)(E + q * (int64_t)g.n);
+#pragma unroll
+      for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(g.beta, to_f32<DT_F16>(x[e]), v[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < W; ++e) v[e] = as_computed(m == n + e ? v[e] + g.diag : v[e]);
+  if (g.d) {
+    if (m >= g.rows) return;
+    uint16_t* D = (uint16_t*)g.d + o.batch * g.d_bs + m * g.d_rs + n * g.d_cs;
+    vec x;
+#pragma unroll
+    for (int e = 0; e < W; ++e) x[e] = g.d_type == OT_BF16 ? from_f32<DT_BF16>(v[e]) : from_f32<DT_F16>(v[e]);
+    typedef uint16_t loose __attribute__((ext_vector_type(W), aligned(2)));
+    if (g.d_cs == 1 && n + W <= g.cols) {
+      *(loose*)D = x;
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e)
+        if (n + e < g.cols) D[e * g.d_cs] = x[e];
+    }
+    return;
+  }
+  float r[W];
+#pragma unroll
+  for (int e = 0; e < W; ++e) r[e] = v[e];
+#pragma unroll
+  for (int q = 0; q < OP; ++q) {
+    vec x;
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      x[e] = from_f32<DT_F16>(r[e]);
+      r[e] = as_computed(r[e] - to_f32<DT_F16>(x[e]));
+    }
+    *(vec*)((o.product ? g.O[1] : g.O[0]) + at + q * (int64_t)g.n) = x;
   }
 }
 
-template <int BM, int BN, int WM, int WN, int PLANES>
-__global__ __launch_bounds__(WM* WN * 64) void ortho_gemm_kernel(const OrthoGemm g) {
-  constexpr int NT = WM * WN * 64;
-  constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+// W consecutive m of D's finished values at column n, to the mirrored place
+// or d stored column after column
+template <int OP, int W>
+__device__ __forceinline__ void ortho_emit_column(const OrthoGemm& g, const OrthoTile& o, int32_t m, int32_t n, float (&v)[W]) {
+  typedef uint16_t vec __attribute__((ext_vector_type(W)));
+  typedef uint16_t loose __attribute__((ext_vector_type(W), aligned(2)));
+  if (g.d) {
+    if (n >= g.cols) return;
+    uint16_t* D = (uint16_t*)g.d + o.batch * g.d_bs + n * g.d_cs + m;
+    vec x;
+#pragma unroll
+    for (int e = 0; e < W; ++e) x[e] = g.d_type == OT_BF16 ? from_f32<DT_BF16>(v[e]) : from_f32<DT_F16>(v[e]);
+    if (m + W <= g.rows) {
+      *(loose*)D = x;
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e)
+        if (m + e < g.rows) D[e] = x[e];
+    }
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < OP; ++q) {
+    vec x;
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      x[e] = from_f32<DT_F16>(v[e]);
+      v[e] = as_computed(v[e] - to_f32<DT_F16>(x[e]));
+    }
+    *(vec*)((o.product ? g.O[1] : g.O[0]) + o.batch * g.O_bs + (int64_t)n * (OP * (int64_t)g.m) + q * (int64_t)g.m + m) = x;
+  }
+}
+
+// d stored column after column: the row pass only computes
+__device__ __forceinline__ bool ortho_columns(const OrthoGemm& g) { return g.d && g.d_rs == 1 && g.d_cs != 1; }
+
+// The K-tiles: P0 Q0, then P1 Q0, then P0 Q1, T1 of 64 each.
+template <int PP, int PQ>
+struct OrthoPasses {
+  static constexpr int N = PP + PQ - 1;
+  static __device__ __forceinline__ int32_t of_p(int32_t t, int32_t T1) {
+    return PP == 2 && t < 2 * T1 ? t : PP == 2 ? t - 2 * T1 : t < T1 ? t : t - T1;
+  }
+  // Q K-contiguous: plane 1 behind plane 0
+  static __device__ __forceinline__ int32_t of_q(int32_t t, int32_t T1) {
+    return t < T1 ? t : PP == 2 ? t - T1 : t;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Outputs too small for 256 x 256 tiles to fill the chip: BM x BN tiles, KG
+// groups of four waves that take the K-tiles in turn (their sums meet in
+// LDS), each with a ring of STAGES K-tiles in LDS so that a copy has STAGES -
+// 2 K-tiles of compute to land.  One barrier a K-tile.
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int KG, int STAGES, bool N_MAJOR, int PP, int PQ, int OP>
+__global__ __launch_bounds__(256 * KG) void ortho_gemm_kernel(const OrthoGemm g) {
+  typedef OrthoPasses<PP, PQ> Pass;
+  constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
   constexpr int ABYTES = BM * kRowBytes, BBYTES = BN * kRowBytes, STAGE = ABYTES + BBYTES;
-  constexpr int PITCH = TM + 8;  // halves per row of the transposing region
-  static_assert(WM * WN * TN * PITCH * 2 <= 2 * STAGE, "the transposed tile fits the stages");
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  constexpr int PITCH = BN + 1;  // floats a row of the finished tile
+  constexpr int LDS = KG * STAGES * STAGE;
+  static_assert(BM * PITCH * 4 <= LDS && LDS <= 160 * 1024, "LDS");
+  __shared__ __attribute__((aligned(1024))) char smem[LDS];
   const int32_t lane = threadIdx.x & 63;
-  const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t wm = wave % WM, wn = wave / WM;
-  int32_t batch, tm, tn;
-  ortho_tile(g, blockIdx.x, batch, tm, tn);
-  const int32_t m0 = tm * BM, n0 = tn * BN;
+  const int32_t wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
+  const int32_t group = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  const OrthoTile o = ortho_tile(g);
+  const int32_t m0 = o.tm * BM, n0 = o.tn * BN;
   const int32_t rows_a = g.m - m0 < BM ? g.m - m0 : BM, rows_b = g.n - n0 < BN ? g.n - n0 : BN;
-  const int32_t kp = PLANES * g.k;
-  LoaderKVec<BM, NT, 0, 2> la(g.P + batch * g.P_bs + (int64_t)m0 * kp, rows_a, kp, 1, kp, wave, lane);
-  LoaderKVec<BN, NT, 0, 2> lb(g.Q + batch * g.Q_bs + (int64_t)n0 * kp, rows_b, kp, 1, kp, wave, lane);
-  const int32_t a_row0 = wm * TM, b_row0 = wn * TN;
+  const int64_t pk = (int64_t)PP * g.k, qk = N_MAJOR ? (int64_t)PQ * g.n : (int64_t)PQ * g.k;
+  LoaderKVec<BM, 256, 0, 2> la(g.P + o.batch * g.P_bs + m0 * pk, rows_a, pk, 1, pk, wave, lane);
+  const uint16_t* qb = (o.product ? g.Q[1] : g.Q[0]) + o.batch * g.Q_bs;
+  auto make_b = [&](int plane) {
+    if constexpr (N_MAJOR)
+      return LoaderMNDma<BN, 256>(qb + n0 + plane * (int64_t)g.n, rows_b, 1, qk, g.k, wave, lane);
+    else
+      return LoaderKVec<BN, 256, 0, 2>(qb + n0 * qk, rows_b, qk, 1, qk, wave, lane);
+  };
+  auto lb = make_b(0);
+  auto lb1 = make_b(N_MAJOR && PQ == 2 ? 1 : 0);  // used where a plane is not a range of K
+  constexpr int LOADS = decltype(la)::ITERS + decltype(lb)::ITERS;
+  const int32_t a_row0 = (wave & 1) * TM, b_row0 = (wave >> 1) * TN;
+  char* ring = smem + group * (STAGES * STAGE);
+
   floatx4 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-  // K-tiles: P0 Q0, with two planes then P0 Q1 and P1 Q0
-  const int32_t T1 = g.k / 64, T = PLANES == 2 ? 3 * T1 : T1;
-  auto issue = [&](int32_t t, char* at) {  // past the last K-tile: not read
-    la.issue(PLANES == 2 && t >= T1 ? t - T1 : t, at);
-    lb.issue(PLANES == 2 && t >= 2 * T1 ? t - 2 * T1 : t, at + ABYTES);
+  const int32_t T1 = g.k / 64, T = Pass::N * T1, rounds = (T + KG - 1) / KG;
+  constexpr int32_t kPast = 1 << 24;  // a K-tile past every K: zeros
+  auto issue = [&](int32_t i) {
+    const int32_t t = i * KG + group;
+    char* at = ring + i % STAGES * STAGE;
+    la.issue(t < T ? Pass::of_p(t, T1) : kPast, at);
+    if (N_MAJOR && PQ == 2 && t >= PP * T1)
+      lb1.issue(t < T ? t - PP * T1 : kPast, at + ABYTES);
+    else if (N_MAJOR)
+      lb.issue(t < T ? (t < T1 ? t : t - T1) : kPast, at + ABYTES);
+    else
+      lb.issue(t < T ? Pass::of_q(t, T1) : kPast, at + ABYTES);
   };
-  issue(0, smem);
-  wait_vmem();
-  __syncthreads();
-  for (int32_t t = 0; t < T; ++t) {
-    char* cur = smem + (t & 1) * STAGE;
-    char* nxt = smem + ((t + 1) & 1) * STAGE;
-    issue(t + 1, nxt);
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) issue(i);
+  for (int32_t i = 0; i < rounds; ++i) {
+    wait_vmem_n<(STAGES - 2) * LOADS>();
+    phase_barrier();
+    issue(i + STAGES - 1);
+    const char* cur = ring + i % STAGES * STAGE;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       half8 af[FM], bf[FN];
 #pragma unroll
-      for (int i = 0; i < FM; ++i) af[i] = *(const half8*)(cur + fragment_lds_offset(MFMA16_F16, lane, 0, a_row0 + 16 * i, ks, 0));
+      for (int a = 0; a < FM; ++a) af[a] = read_frag<LOAD_KVEC, BM, 0>(cur, lane, a_row0 + 16 * a, ks);
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-        bf[j] = *(const half8*)(cur + ABYTES + fragment_lds_offset(MFMA16_F16, lane, 0, b_row0 + 16 * j, ks, 0));
+      for (int b = 0; b < FN; ++b) bf[b] = read_frag<N_MAJOR ? LOAD_MNDMA : LOAD_KVEC, BN, 0>(cur + ABYTES, lane, b_row0 + 16 * b, ks);
+#pragma unroll
+      for (int a = 0; a < FM; ++a)
+#pragma unroll
+        for (int b = 0; b < FN; ++b) acc[a][b] = mfma16<DT_F16>(bf[b], af[a], acc[a][b]);
+    }
+  }
+  wait_vmem();
+  __syncthreads();
+
+  // the groups' sums, one after the other, into the finished tile
+  float* tile = (float*)smem;
+#pragma unroll
+  for (int k = KG - 1; k >= 0; --k) {
+    if (group == k) {
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mfma16<DT_F16>(bf[j], af[i], acc[i][j]);
+        for (int j = 0; j < FN; ++j) {
+          float* to = tile + (a_row0 + 16 * i + (lane & 15)) * PITCH + b_row0 + 16 * j + 4 * (lane >> 4);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) to[r] = k < KG - 1 ? to[r] + acc[i][j][r] : acc[i][j][r];
+        }
     }
-    wait_vmem();
     __syncthreads();
   }
-
-  // lane: m = lane % 16 of tile i, n = 4 (lane / 16) + r of tile j
-  const bool mirror = g.sym && tm != tn;
-  const bool transposed = g.d ? g.d_rs == 1 && g.d_cs != 1 : g.OT && (!g.sym || mirror);
-  uint16_t* region = (uint16_t*)smem + wave * (TN * PITCH);
-  const int64_t np = (int64_t)PLANES * g.n, mp = (int64_t)PLANES * g.m;
+  const bool mirror = g.sym && o.tm != o.tn, columns = ortho_columns(g);
+  constexpr int PIECES = BM * BN / 8 / (256 * KG);
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int32_t m = m0 + a_row0 + 16 * i + (lane & 15);
+  for (int q = 0; q < PIECES; ++q) {
+    const int32_t t = threadIdx.x + 256 * KG * q, ml = t / (BN / 8), nl = 8 * (t % (BN / 8));
+    float* at = tile + ml * PITCH + nl;
+    float v[8];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int32_t n = n0 + b_row0 + 16 * j + 4 * (lane >> 4);
-      floatx4 v = acc[i][j];
+    for (int e = 0; e < 8; ++e) v[e] = at[e];
+    if (m0 + ml < g.m && n0 + nl < g.n) {
+      if (columns) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] *= g.alpha;
-      if (g.E && m < g.m && n < g.n) {
+        for (int e = 0; e < 8; ++e) v[e] *= o.alpha;
+        if (g.E) {
 #pragma unroll
-        for (int q = PLANES - 1; q >= 0; --q) {
-          const u16x4 e = *(const u16x4*)(g.E + batch * g.E_bs + m * np + q * g.n + n);
+          for (int z = OP - 1; z >= 0; --z) {
+            const u16x8 x = *(const u16x8*)(g.E + o.batch * g.E_bs + (m0 + ml) * (OP * (int64_t)g.n) + z * (int64_t)g.n + n0 + nl);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(g.beta, to_f32<DT_F16>(e[r]), v[r]);
+            for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(g.beta, to_f32<DT_F16>(x[e]), v[e]);
+          }
         }
+      } else {
+        ortho_emit<OP, 8>(g, o, m0 + ml, n0 + nl, v);
       }
+    }
+    if (mirror || columns) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[i][j][r] = as_computed(v[r]);
+      for (int e = 0; e < 8; ++e) at[e] = v[e];
     }
   }
+  if (!mirror && !columns) return;
+  __syncthreads();
 #pragma unroll
-  for (int q = 0; q < PLANES; ++q) {
-    if (q > 0 && g.d) break;
+  for (int q = 0; q < PIECES; ++q) {
+    const int32_t t = threadIdx.x + 256 * KG * q, ml = 8 * (t % (BM / 8)), nl = t / (BM / 8);
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int32_t ml = 16 * i + (lane & 15), m = m0 + a_row0 + ml;
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int32_t nl = 16 * j + 4 * (lane >> 4), n = n0 + b_row0 + nl;
-        const floatx4 v = acc[i][j];
-        u16x4 h;
-        if (g.d && g.d_type == OT_BF16) {
-          h = u16x4{from_f32<DT_BF16>(v[0]), from_f32<DT_BF16>(v[1]), from_f32<DT_BF16>(v[2]), from_f32<DT_BF16>(v[3])};
-        } else {
-          h = u16x4{from_f32<DT_F16>(v[0]), from_f32<DT_F16>(v[1]), from_f32<DT_F16>(v[2]), from_f32<DT_F16>(v[3])};
-          if (q + 1 < PLANES) {  // the next plane's: what this rounding left
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][j][r] = as_computed(v[r] - to_f32<DT_F16>(h[r]));
-          }
-        }
-        if (transposed) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) region[(nl + r) * PITCH + ml] = h[r];
-        }
-        if (g.d) {
-          if (!transposed) {
-            uint16_t* D = (uint16_t*)g.d + batch * g.d_bs + m * g.d_rs;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (m < g.rows && n + r < g.cols) D[(n + r) * g.d_cs] = h[r];
-          }
-        } else if (g.O && m < g.m && n < g.n) {
-          *(u16x4*)(g.O + batch * g.O_bs + m * np + q * g.n + n) = h;
-        }
-      }
-    }
-    if (!transposed) continue;
-    // each wave reads back only its own region: the compiler's wait on the
-    // LDS writes is enough
-    constexpr int LPR = TM / 8, RPI = 64 / LPR;  // lanes per row of the region, rows per instruction
-#pragma unroll
-    for (int k = 0; k < TN / RPI; ++k) {
-      const int32_t nl = RPI * k + lane / LPR, ml = 8 * (lane % LPR);
-      const int32_t n = n0 + b_row0 + nl, m = m0 + a_row0 + ml;
-      const u16x8 h = *(const u16x8*)(region + nl * PITCH + ml);
-      if (g.d) {
-        uint16_t* D = (uint16_t*)g.d + batch * g.d_bs + n * g.d_cs + m;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (n < g.cols && m + e < g.rows) D[e] = h[e];
-      } else if (n < g.n && m < g.m) {
-        *(u16x8*)(g.OT + batch * g.O_bs + n * mp + q * g.m + m) = h;
-      }
-    }
+    for (int e = 0; e < 8; ++e) v[e] = tile[(ml + e) * PITCH + nl];
+    if (m0 + ml < g.m && n0 + nl < g.n) ortho_emit_column<OP, 8>(g, o, m0 + ml, n0 + nl, v);
   }
 }
 
-hipError_t run_gemm(OrthoGemm g, int32_t planes, hipStream_t s) {
-  g.tiles_m = (g.m + 127) / 128, g.tiles_n = (g.n + 127) / 128;
+template <int BM, int BN, int KG, int STAGES, bool NM, int PP, int PQ, int OP>
+hipError_t run_tiles(OrthoGemm g, hipStream_t s) {
+  g.tiles_m = (g.m + BM - 1) / BM, g.tiles_n = (g.n + BN - 1) / BN;
   const int64_t tiles = g.sym ? (int64_t)g.tiles_n * (g.tiles_n + 1) / 2 : (int64_t)g.tiles_m * g.tiles_n;
-  const dim3 grid((uint32_t)(tiles * g.batch));
-  if (planes == 2)
-    hipLaunchKernelGGL((ortho_gemm_kernel<128, 128, 2, 2, 2>), grid, dim3(256), 0, s, g);
-  else
-    hipLaunchKernelGGL((ortho_gemm_kernel<128, 128, 2, 2, 1>), grid, dim3(256), 0, s, g);
+  hipLaunchKernelGGL((ortho_gemm_kernel<BM, BN, KG, STAGES, NM, PP, PQ, OP>), dim3((uint32_t)(tiles * g.batch * g.products)),
+                     dim3(256 * KG), 0, s, g);
   return hipGetLastError();
+}
+
+// Q K-contiguous, a symmetric result
+template <int PP, int PQ, int OP>
+hipError_t run_sym(const OrthoGemm& g, hipStream_t s) {
+  const int64_t t = (g.m + 127) / 128, tiles = t * (t + 1) / 2 * g.batch * g.products;
+  if (tiles >= 160) return run_tiles<128, 128, 1, 4, false, PP, PQ, OP>(g, s);
+  return run_tiles<64, 64, 2, 4, false, PP, PQ, OP>(g, s);
+}
+// Q stored as (k, n)
+template <int PP, int PQ, int OP>
+hipError_t run_wide(const OrthoGemm& g, hipStream_t s) {
+  const int64_t tiles = (int64_t)((g.m + 127) / 128) * ((g.n + 127) / 128) * g.batch;
+  if (tiles >= 160) return run_tiles<128, 128, 1, 4, true, PP, PQ, OP>(g, s);
+  return run_tiles<64, 128, 2, 3, true, PP, PQ, OP>(g, s);
 }
 
 template <int T>
-hipError_t start(int32_t planes, const OrthoParams& p, double* parts, uint16_t* X, uint16_t* XT, int32_t tm, int32_t tn, hipStream_t s) {
+hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, OrthoScales* scales, hipStream_t s) {
+  const int32_t tm = (int32_t)(pad64(p.m) / 64), tn = (int32_t)(pad64(p.n) / 64);
   hipLaunchKernelGGL(ortho_norm_kernel<T>, dim3(kNormParts, p.batch), dim3(256), 0, s, p, parts);
-  const dim3 grid((uint32_t)((int64_t)p.batch * tm * tn));
-  if (planes == 2)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 2>), grid, dim3(256), 0, s, p, parts, X, XT, tm, tn);
+  const dim3 grid((uint32_t)((int64_t)p.batch * tm * tn)), block(256);
+  if (exact && planes == 2)
+    hipLaunchKernelGGL((ortho_start_kernel<T, 2, true>), grid, block, 0, s, p, parts, X, scales, tm, tn);
+  else if (exact)
+    hipLaunchKernelGGL((ortho_start_kernel<T, 1, true>), grid, block, 0, s, p, parts, X, scales, tm, tn);
+  else if (planes == 2)
+    hipLaunchKernelGGL((ortho_start_kernel<T, 2, false>), grid, block, 0, s, p, parts, X, scales, tm, tn);
   else
-    hipLaunchKernelGGL((ortho_start_kernel<T, 1>), grid, dim3(256), 0, s, p, parts, X, XT, tm, tn);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 1, false>), grid, block, 0, s, p, parts, X, scales, tm, tn);
   return hipGetLastError();
+}
+hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, OrthoScales* scales, hipStream_t s) {
+  switch (p.x_type) {
+    case OT_F16: return start<OT_F16>(p, planes, exact, parts, X, scales, s);
+    case OT_BF16: return start<OT_BF16>(p, planes, exact, parts, X, scales, s);
+    default: return start<OT_F32>(p, planes, exact, parts, X, scales, s);
+  }
+}
+
+enum Way { kSmallGram, kGram, kDirect };
+
+// The Gram matrix's way multiplies pairs, 54 m^3 + 3 m^2 n and up to 2 m^2 n
+// more multiply-adds for five steps, but for small sizes where launches
+// count; the direct one 15 m^2 n + 5 m^3 on single planes, three times that
+// on pairs.
+Way way_of(const OrthoParams& p) {
+  float growth = 1.f;
+  for (int32_t t = 0; t < p.steps; ++t) growth *= fmaxf(1.f, fabsf(p.coefficients[3 * t]));
+  if (growth > kGramGrowth) return kDirect;
+  if (p.m <= kGramRows) return kSmallGram;
+  return p.d_type == OT_F16 || p.n > 4 * p.m ? kGram : kDirect;
+}
+
+// fp16 results of the direct way take pairs: with one plane, every matrix
+// between products rounded to fp16 costs them 1.1e-3 to 1.8e-3 (relative,
+// 2-norm; 64-bit simulation at 16 x 16 to 1000 x 1000), five times their own
+// rounding of 2.1e-4, with pairs 3e-7.  A bf16 result's own rounding is
+// 1.7e-3.  The Gram matrix's way keeps x itself, exactly, in one plane unless
+// it is fp32.
+int32_t x_planes(const OrthoParams& p, Way way) {
+  if (way == kGram) return p.x_type == OT_F32 && p.d_type == OT_F16 ? 2 : 1;
+  return p.d_type == OT_F16 ? 2 : 1;
 }
 
 struct Places {
-  size_t x, xt0, xt1, g, b, total;  // byte offsets behind the partial sums
+  size_t scales, x[2], mm[5], total;  // byte offsets behind the partial sums
 };
-Places places(int64_t batch, int64_t m, int64_t n, int32_t planes) {
-  const size_t mn = (size_t)batch * pad64(m) * pad64(n) * 2 * planes, mm = (size_t)batch * pad64(m) * pad64(m) * 2 * planes;
+Places places(const OrthoParams& p, Way way) {
+  const int32_t xp = x_planes(p, way), mp = way == kGram ? 2 : xp;
+  const size_t mn = (size_t)p.batch * pad64(p.m) * pad64(p.n) * 2 * xp, mm = (size_t)p.batch * pad64(p.m) * pad64(p.m) * 2 * mp;
+  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   Places q;
-  q.x = ((size_t)batch * kNormParts * 8 + 255) & ~(size_t)255;
-  q.xt0 = q.x + mn;
-  q.xt1 = q.xt0 + mn;
-  q.g = q.xt1 + mn;
-  q.b = q.g + mm;
-  q.total = q.b + mm;
+  q.scales = up((size_t)p.batch * kNormParts * 8);
+  q.x[0] = q.scales + up((size_t)p.batch * sizeof(OrthoScales));
+  q.x[1] = way == kGram ? q.x[0] : q.x[0] + mn;
+  size_t at = q.x[1] + mn;
+  for (int i = 0; i < 5; ++i) {
+    q.mm[i] = at;
+    if (way == kGram || i < 2) at += mm;
+  }
+  q.total = at;
   return q;
 }
 
-}  // namespace
-
-// fp16 results take two planes: with one, every matrix between products
-// rounded to fp16 costs them 1.1e-3 to 1.8e-3 (relative, 2-norm; 64-bit
-// simulation at 16 x 16 to 1000 x 1000), five times their own rounding of
-// 2.1e-4, with two 3e-7 at three times the products.  A bf16 result's own
-// rounding is 1.7e-3.
-namespace {
-int32_t planes_for(int32_t d_type) { return d_type == OT_F16 ? 2 : 1; }
-}  // namespace
-
-// Up to 128 rows the Gram matrix's three launches (96 x 128: 123 us with the
-// launches below), unless the steps amplify too much for it.
-namespace {
-bool through_gram(const OrthoParams& p) {
-  float growth = 1.f;
-  for (int32_t t = 0; t < p.steps; ++t) growth *= fmaxf(1.f, fabsf(p.coefficients[3 * t]));
-  return p.m <= kGramRows && growth <= kGramGrowth;
+void to_result(const OrthoParams& p, OrthoGemm* g) {
+  g->d = p.d, g->d_type = p.d_type, g->rows = p.m, g->cols = p.n;
+  g->d_bs = p.d_bs, g->d_rs = p.d_rs, g->d_cs = p.d_cs;
 }
+
+template <int PL>
+hipError_t direct(const OrthoParams& p, hipStream_t s) {
+  const Places q = places(p, kDirect);
+  uint16_t* X[2] = {(uint16_t*)(p.ws + q.x[0]), (uint16_t*)(p.ws + q.x[1])};
+  uint16_t *G = (uint16_t*)(p.ws + q.mm[0]), *B = (uint16_t*)(p.ws + q.mm[1]);
+  const int32_t mp = (int32_t)pad64(p.m), np = (int32_t)pad64(p.n);
+  const int64_t mn = (int64_t)mp * np * PL, mm = (int64_t)mp * mp * PL;
+  constexpr float kDown = 0x1p-10f;  // what a stored value times it stands for
+  hipError_t e = start(p, PL, false, (double*)p.ws, X[0], nullptr, s);
+  for (int32_t k = 0; k < p.steps && e == hipSuccess; ++k) {
+    const float a = p.coefficients[3 * k], b = p.coefficients[3 * k + 1], c = p.coefficients[3 * k + 2];
+    // stored values carry 2^10, products of two 2^20
+    OrthoGemm g{};
+    g.batch = p.batch, g.products = 1;
+    g.P = g.Q[0] = X[k & 1], g.P_bs = g.Q_bs = mn;
+    g.m = g.n = mp, g.k = np, g.alpha[0] = kDown, g.sym = 1;
+    g.O[0] = G, g.O_bs = mm;
+    if ((e = run_sym<PL, PL, PL>(g, s)) != hipSuccess) break;
+    g.P = g.Q[0] = g.E = G, g.P_bs = g.Q_bs = g.E_bs = mm;
+    g.k = mp, g.alpha[0] = c * kDown, g.beta = b;
+    g.O[0] = B;
+    if ((e = run_sym<PL, PL, PL>(g, s)) != hipSuccess) break;
+    g.P = B, g.Q[0] = g.E = X[k & 1], g.Q_bs = g.E_bs = mn;
+    g.n = np, g.alpha[0] = kDown, g.beta = a, g.sym = 0;
+    g.O[0] = X[(k + 1) & 1], g.O_bs = mn;
+    if (k + 1 == p.steps) {
+      g.alpha[0] *= kDown, g.beta *= kDown;
+      to_result(p, &g);
+    }
+    e = run_wide<PL, PL, PL>(g, s);
+  }
+  return e;
+}
+
+// PX: planes of x
+template <int PX>
+hipError_t gram(const OrthoParams& p, hipStream_t s) {
+  const Places q = places(p, kGram);
+  OrthoScales* scales = (OrthoScales*)(p.ws + q.scales);
+  uint16_t* X = (uint16_t*)(p.ws + q.x[0]);
+  uint16_t* M[5];
+  for (int i = 0; i < 5; ++i) M[i] = (uint16_t*)(p.ws + q.mm[i]);
+  uint16_t *G = M[0], *P = M[1], *H = M[2], *Q = nullptr;
+  const int32_t mp = (int32_t)pad64(p.m), np = (int32_t)pad64(p.n);
+  const int64_t mn = (int64_t)mp * np * PX, mm = (int64_t)mp * mp * 2;
+  constexpr float kG = 0x1p12f, kP = 0x1p6f;  // what G's planes, and those of P, H and Q, are multiplied by
+  hipError_t e = start(p, PX, true, (double*)p.ws, X, scales, s);
+  if (e != hipSuccess) return e;
+  OrthoGemm g{};
+  g.batch = p.batch, g.products = 1, g.sym = 1;
+  g.P = g.Q[0] = X, g.P_bs = g.Q_bs = mn;
+  g.m = g.n = mp, g.k = np, g.alpha[0] = 1.f, g.scales = scales;
+  g.O[0] = G, g.O_bs = mm;
+  if ((e = run_sym<PX, PX, 2>(g, s)) != hipSuccess) return e;
+  g.scales = nullptr, g.P_bs = g.Q_bs = g.E_bs = mm, g.k = mp;
+  for (int32_t k = 0; k < p.steps; ++k) {
+    const float a = p.coefficients[3 * k], b = p.coefficients[3 * k + 1], c = p.coefficients[3 * k + 2];
+    const bool last = k + 1 == p.steps;
+    // P = a I + b G + c G^2; the first is Q as well
+    uint16_t* Pk = k == 0 ? M[3] : P;
+    g.P = g.Q[0] = g.E = G, g.alpha[0] = c * (kP / (kG * kG)), g.beta = b * (kP / kG), g.diag = a * kP;
+    g.O[0] = Pk;
+    if ((e = run_sym<2, 2, 2>(g, s)) != hipSuccess) return e;
+    g.E = nullptr, g.diag = 0.f;
+    uint16_t* next = Q == M[3] ? M[4] : M[3];
+    g.P = Pk;
+    g.products = (last ? 0 : 1) + (k > 0 ? 1 : 0);
+    int i = 0;
+    if (!last) g.Q[i] = G, g.O[i] = H, g.alpha[i] = 1.f / kG, ++i;
+    if (k > 0) g.Q[i] = Q, g.O[i] = next, g.alpha[i] = 1.f / kP;
+    if (g.products > 0 && (e = run_sym<2, 2, 2>(g, s)) != hipSuccess) return e;
+    g.products = 1;
+    Q = k > 0 ? next : M[3];
+    if (last) break;
+    g.P = H, g.Q[0] = Pk, g.O[0] = G, g.alpha[0] = kG / (kP * kP);
+    if ((e = run_sym<2, 2, 2>(g, s)) != hipSuccess) return e;
+  }
+  g.P = Q, g.Q[0] = X, g.Q_bs = mn, g.n = np, g.sym = 0, g.alpha[0] = 1.f;
+  g.scales = scales, g.scale_apply = 1;
+  to_result(p, &g);
+  return run_wide<2, PX, 1>(g, s);
+}
+
 }  // namespace
 
 size_t orthogonalize_workspace(const OrthoParams& p) {
-  return through_gram(p) ? ortho_gram_workspace(p) : places(p.batch, p.m, p.n, planes_for(p.d_type)).total;
+  const Way way = way_of(p);
+  return way == kSmallGram ? ortho_gram_workspace(p) : places(p, way).total;
 }
 
-// every launch below fits a grid, and a 128-row tile 32-bit offsets
+// every launch fits a grid, and a matrix's planes 32-bit offsets
 bool orthogonalize_grid_ok(int64_t batch, int64_t m, int64_t n) {
   const int64_t lim = (int64_t)1 << 31;
   if (batch >= 65536 || m >= lim || n >= lim) return false;
-  return (double)batch * (double)(pad64(m) / 64) * (double)(pad64(n) / 64) < 0x1p31 && 256 * pad64(n) * 4 < lim;
+  if ((double)batch * (double)(pad64(m) / 64) * (double)(pad64(n) / 64) >= 0x1p30) return false;
+  return m <= kGramRows || (double)pad64(m) * (double)pad64(n) * 4 < 0x1p31;
 }
 
 hipError_t launch_orthogonalize(const OrthoParams& p, hipStream_t s) {
-  if (through_gram(p)) return launch_ortho_gram(p, s);
-  const int32_t planes = planes_for(p.d_type);
-  const Places q = places(p.batch, p.m, p.n, planes);
-  double* parts = (double*)p.ws;
-  uint16_t* X = (uint16_t*)(p.ws + q.x);
-  uint16_t* XT[2] = {(uint16_t*)(p.ws + q.xt0), (uint16_t*)(p.ws + q.xt1)};
-  uint16_t* G = (uint16_t*)(p.ws + q.g);
-  uint16_t* B = (uint16_t*)(p.ws + q.b);
-  const int32_t mp = (int32_t)pad64(p.m), np = (int32_t)pad64(p.n);
-  const int64_t mn = (int64_t)mp * np * planes, mm = (int64_t)mp * mp * planes;
-  hipError_t e;
-  switch (p.x_type) {
-    case OT_F16: e = start<OT_F16>(planes, p, parts, X, XT[0], mp / 64, np / 64, s); break;
-    case OT_BF16: e = start<OT_BF16>(planes, p, parts, X, XT[0], mp / 64, np / 64, s); break;
-    default: e = start<OT_F32>(planes, p, parts, X, XT[0], mp / 64, np / 64, s); break;
+  switch (way_of(p)) {
+    case kSmallGram: return launch_ortho_gram(p, s);
+    case kGram: return x_planes(p, kGram) == 2 ? gram<2>(p, s) : gram<1>(p, s);
+    default: return x_planes(p, kDirect) == 2 ? direct<2>(p, s) : direct<1>(p, s);
   }
-  for (int32_t k = 0; k < p.steps && e == hipSuccess; ++k) {
-    const float a = p.coefficients[3 * k], b = p.coefficients[3 * k + 1], c = p.coefficients[3 * k + 2];
-    const bool last = k + 1 == p.steps;
-    // stored values carry 2^10, products of two 2^20
-    OrthoGemm g{};
-    g.batch = p.batch;
-    g.P = X, g.Q = X, g.P_bs = g.Q_bs = mn;
-    g.m = g.n = mp, g.k = np, g.alpha = kDown;
-    g.O = g.OT = G, g.O_bs = mm, g.sym = 1;
-    if ((e = run_gemm(g, planes, s)) != hipSuccess) break;
-    g.P = G, g.Q = G, g.E = G, g.P_bs = g.Q_bs = g.E_bs = mm;
-    g.k = mp, g.alpha = c * kDown, g.beta = b;
-    g.O = g.OT = B;
-    if ((e = run_gemm(g, planes, s)) != hipSuccess) break;
-    g.P = B, g.Q = XT[k & 1], g.E = X, g.Q_bs = g.E_bs = mn;
-    g.n = np, g.alpha = kDown, g.beta = a, g.sym = 0;
-    g.O = X, g.OT = XT[(k + 1) & 1], g.O_bs = mn;
-    if (last) {
-      g.alpha *= kDown, g.beta *= kDown;
-      g.d = p.d, g.d_type = p.d_type, g.rows = p.m, g.cols = p.n;
-      g.d_bs = p.d_bs, g.d_rs = p.d_rs, g.d_cs = p.d_cs;
-    }
-    e = run_gemm(g, planes, s);
-  }
-  return e;
 }
 
 }  // namespace sl
