@@ -19,9 +19,10 @@
 // and added up in a fixed order.
 //
 // G, B, P, Q and H = P G are symmetric (polynomials in G): only tiles on and
-// above the diagonal are computed, each stored a second time, transposed.  A
-// product with X as its second operand reads X along its contiguous axis n by
-// transposing LDS reads, so no transpose of X is kept.
+// above the diagonal are computed, each stored a second time, transposed.
+// Every product reads both operands along K: X is kept in both orientations
+// (read as it lies, by transposing LDS reads, it cost a product of 8192^3
+// half as much again).
 #include "sl_ops.hpp"
 
 #include "sl_device.hpp"
@@ -79,13 +80,14 @@ struct OrthoScales {
   float apply;  // of Q's plane times x's, to make d
 };
 
-// The planes that the products read: m x n, zero to the padded sizes.
+// The planes that the products read: m x n and n x m, zero to the padded
+// sizes.
 // EXACT: x times the power of two that brings |x| to 2^14 (to 2^15): exact in
 // fp16 but for what lies 2^-38 below |x|; the scales follow.  Else 2^10 x /
 // (|x| + 1e-7), rounded.  With two planes also what the rounding left.
 template <int T, int PLANES, bool EXACT>
 __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, const double* parts, uint16_t* X,
-                                                          OrthoScales* scales, int32_t tiles_m, int32_t tiles_n) {
+                                                          uint16_t* XT, OrthoScales* scales, int32_t tiles_m, int32_t tiles_n) {
   __shared__ double lds[4];
   __shared__ uint16_t tile[PLANES][64][66];
   const uint32_t id = blockIdx.x;
@@ -123,19 +125,23 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, c
   for (int k = 0; k < 16; ++k) {
     const int32_t r = 4 * k + w;
 #pragma unroll
-    for (int q = 0; q < PLANES; ++q) X[PLANES * (b * mp * np + (i0 + r) * np) + q * np + j0 + u] = tile[q][r][u];
+    for (int q = 0; q < PLANES; ++q) {
+      X[PLANES * (b * mp * np + (i0 + r) * np) + q * np + j0 + u] = tile[q][r][u];
+      XT[PLANES * (b * mp * np + (j0 + r) * mp) + q * mp + i0 + u] = tile[q][u][r];
+    }
   }
 }
 
-// D = alpha P Q^T + beta E + diag I (with `scaled`, alpha times the matrix's
-// own scale), P's planes K-contiguous, Q K-contiguous or (n_major) stored as
-// (k, n).  A row of a matrix of two planes is its first plane's values and
-// behind them the second's.  One or two products of the same P in one launch.
+// D = alpha P Q^T + beta E + diag I (with `scales`, alpha times the matrix's
+// own), K contiguous in P and Q.  A row of a matrix of two planes is its
+// first plane's values and behind them the second's.  One or two products of
+// the same P in one launch.
 struct OrthoGemm {
   const uint16_t* P;             // (m, PP k)
-  const uint16_t* Q[2];          // (n, PQ k), or (k, PQ n)
+  const uint16_t* Q[2];          // (n, PQ k)
   const uint16_t* E;             // (m, OP n), or NULL
-  uint16_t* O[2];                // (m, OP n); sym: and its transpose
+  uint16_t* O[2];                // (m, OP n); sym: its transpose as well
+  uint16_t* OT;                  // (n, OP m), or NULL
   int64_t P_bs, Q_bs, E_bs, O_bs;
   int32_t m, n, k;               // padded: multiples of 64
   float alpha[2], beta, diag;
@@ -151,41 +157,54 @@ struct OrthoGemm {
 };
 
 struct OrthoTile {
-  int32_t product, batch, tm, tn;
+  int32_t batch, product, tm, tn;
   float alpha;
 };
 
-// the tile of workgroup `id`: for symmetric results the pairs tm <= tn,
-// column by column
+// The tile of a workgroup.  Workgroups go to the 8 XCDs in turn: each XCD
+// takes a contiguous range of (matrix, product, tile), the tiles of a matrix
+// in groups of eight tile rows, so that what runs on one XCD at a time shares
+// rows of both operands in its L2 (without it 16 x 1000 x 520's products ran
+// at the Infinity Cache's rate).  Symmetric results: the tiles tm <= tn.
 __device__ __forceinline__ OrthoTile ortho_tile(const OrthoGemm& g) {
+  constexpr uint32_t GR = 8;
   OrthoTile o;
-  uint32_t id = blockIdx.x, total = gridDim.x / g.products;
-  o.product = id >= total;
-  id -= o.product * total;
+  const uint32_t total = gridDim.x, x = blockIdx.x & 7, q = total >> 3, r = total & 7;
+  const uint32_t id = x * q + (x < r ? x : r) + (blockIdx.x >> 3);
+  const uint32_t nt = (uint32_t)g.tiles_n, per = g.sym ? nt * (nt + 1) / 2 : nt * (uint32_t)g.tiles_m;
+  o.batch = id / (per * g.products);
+  uint32_t t = id % (per * g.products);
+  o.product = t >= per;
+  t -= o.product * per;
   if (g.sym) {
-    const uint32_t per = (uint32_t)g.tiles_n * (g.tiles_n + 1) / 2;
-    o.batch = id / per;
-    const uint32_t t = id % per;
-    int32_t c = (int32_t)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
-    while ((uint32_t)c * (c + 1) / 2 > t) --c;
-    while ((uint32_t)(c + 1) * (c + 2) / 2 <= t) ++c;
-    o.tn = c;
-    o.tm = (int32_t)(t - (uint32_t)c * (c + 1) / 2);
+    uint32_t g0 = 0, R, tri;
+    for (;; g0 += GR) {
+      R = nt - g0 < GR ? nt - g0 : GR, tri = R * (R + 1) / 2;
+      const uint32_t count = tri + R * (nt - g0 - R);
+      if (t < count) break;
+      t -= count;
+    }
+    if (t < tri) {
+      uint32_t c = 0;
+      while ((c + 1) * (c + 2) / 2 <= t) ++c;
+      o.tn = g0 + c, o.tm = g0 + t - c * (c + 1) / 2;
+    } else {
+      o.tn = g0 + R + (t - tri) / R, o.tm = g0 + (t - tri) % R;
+    }
   } else {
-    const TileCoord tc = map_tile(id, total, g.tiles_m, g.tiles_n, 8, g.batch);
-    o.batch = tc.batch, o.tm = tc.tm, o.tn = tc.tn;
+    const uint32_t span = GR * nt, first = t / span * GR, left = g.tiles_m - first;
+    const uint32_t R = left < GR ? left : GR, in = t % span;
+    o.tm = first + in % R, o.tn = in / R;
   }
   o.alpha = o.product ? g.alpha[1] : g.alpha[0];
   if (g.scales) o.alpha *= g.scale_apply ? g.scales[o.batch].apply : g.scales[o.batch].gram;
   return o;
 }
 
-// W consecutive values of D at (m, n ..), added to and stored; v: what is
-// stored in the mirrored place
+// W consecutive values of D at (m, n ..) from the sums
 template <int OP, int W>
-__device__ __forceinline__ void ortho_emit(const OrthoGemm& g, const OrthoTile& o, int32_t m, int32_t n, float (&v)[W]) {
+__device__ __forceinline__ void ortho_value(const OrthoGemm& g, const OrthoTile& o, int32_t m, int32_t n, float (&v)[W]) {
   typedef uint16_t vec __attribute__((ext_vector_type(W)));
-  const int64_t at = o.batch * g.O_bs + (int64_t)m * (OP * (int64_t)g.n) + n;
 #pragma unroll
   for (int e = 0; e < W; ++e) v[e] *= o.alpha;
   if (g.E) {
@@ -199,22 +218,12 @@ __device__ __forceinline__ void ortho_emit(const OrthoGemm& g, const OrthoTile& 
   }
 #pragma unroll
   for (int e = 0; e < W; ++e) v[e] = as_computed(m == n + e ? v[e] + g.diag : v[e]);
-  if (g.d) {
-    if (m >= g.rows) return;
-    uint16_t* D = (uint16_t*)g.d + o.batch * g.d_bs + m * g.d_rs + n * g.d_cs;
-    vec x;
-#pragma unroll
-    for (int e = 0; e < W; ++e) x[e] = g.d_type == OT_BF16 ? from_f32<DT_BF16>(v[e]) : from_f32<DT_F16>(v[e]);
-    typedef uint16_t loose __attribute__((ext_vector_type(W), aligned(2)));
-    if (g.d_cs == 1 && n + W <= g.cols) {
-      *(loose*)D = x;
-    } else {
-#pragma unroll
-      for (int e = 0; e < W; ++e)
-        if (n + e < g.cols) D[e * g.d_cs] = x[e];
-    }
-    return;
-  }
+}
+
+// ... stored along a row: as planes with `rs` values a plane's row
+template <int OP, int W>
+__device__ __forceinline__ void ortho_store(uint16_t* row, int64_t plane, float (&v)[W]) {
+  typedef uint16_t vec __attribute__((ext_vector_type(W)));
   float r[W];
 #pragma unroll
   for (int e = 0; e < W; ++e) r[e] = v[e];
@@ -226,68 +235,70 @@ __device__ __forceinline__ void ortho_emit(const OrthoGemm& g, const OrthoTile& 
       x[e] = from_f32<DT_F16>(r[e]);
       r[e] = as_computed(r[e] - to_f32<DT_F16>(x[e]));
     }
-    *(vec*)((o.product ? g.O[1] : g.O[0]) + at + q * (int64_t)g.n) = x;
+    *(vec*)(row + q * plane) = x;
   }
 }
-
-// W consecutive m of D's finished values at column n, to the mirrored place
-// or d stored column after column
-template <int OP, int W>
-__device__ __forceinline__ void ortho_emit_column(const OrthoGemm& g, const OrthoTile& o, int32_t m, int32_t n, float (&v)[W]) {
-  typedef uint16_t vec __attribute__((ext_vector_type(W)));
+// ... to the result's type, `left` of them, `step` apart
+template <int W>
+__device__ __forceinline__ void ortho_result(const OrthoGemm& g, uint16_t* d, int64_t step, int64_t left, const float (&v)[W]) {
   typedef uint16_t loose __attribute__((ext_vector_type(W), aligned(2)));
-  if (g.d) {
-    if (n >= g.cols) return;
-    uint16_t* D = (uint16_t*)g.d + o.batch * g.d_bs + n * g.d_cs + m;
-    vec x;
+  loose x;
 #pragma unroll
-    for (int e = 0; e < W; ++e) x[e] = g.d_type == OT_BF16 ? from_f32<DT_BF16>(v[e]) : from_f32<DT_F16>(v[e]);
-    if (m + W <= g.rows) {
-      *(loose*)D = x;
-    } else {
+  for (int e = 0; e < W; ++e) x[e] = g.d_type == OT_BF16 ? from_f32<DT_BF16>(v[e]) : from_f32<DT_F16>(v[e]);
+  if (step == 1 && left >= W) {
+    *(loose*)d = x;
+  } else {
 #pragma unroll
-      for (int e = 0; e < W; ++e)
-        if (m + e < g.rows) D[e] = x[e];
-    }
-    return;
-  }
-#pragma unroll
-  for (int q = 0; q < OP; ++q) {
-    vec x;
-#pragma unroll
-    for (int e = 0; e < W; ++e) {
-      x[e] = from_f32<DT_F16>(v[e]);
-      v[e] = as_computed(v[e] - to_f32<DT_F16>(x[e]));
-    }
-    *(vec*)((o.product ? g.O[1] : g.O[0]) + o.batch * g.O_bs + (int64_t)n * (OP * (int64_t)g.m) + q * (int64_t)g.m + m) = x;
+    for (int e = 0; e < W; ++e)
+      if (e < left) d[e * step] = x[e];
   }
 }
 
-// d stored column after column: the row pass only computes
-__device__ __forceinline__ bool ortho_columns(const OrthoGemm& g) { return g.d && g.d_rs == 1 && g.d_cs != 1; }
+// what a tile's second pass, along its columns, stores
+__device__ __forceinline__ bool ortho_columns(const OrthoGemm& g, const OrthoTile& o) {
+  return g.d ? g.d_rs == 1 && g.d_cs != 1 : (g.sym && o.tm != o.tn) || g.OT;
+}
+// W consecutive n of row m
+template <int OP, int W>
+__device__ __forceinline__ void ortho_row(const OrthoGemm& g, const OrthoTile& o, bool columns, int32_t m, int32_t n, float (&v)[W]) {
+  ortho_value<OP, W>(g, o, m, n, v);
+  if (!g.d)
+    ortho_store<OP, W>((o.product ? g.O[1] : g.O[0]) + o.batch * g.O_bs + (int64_t)m * (OP * (int64_t)g.n) + n, g.n, v);
+  else if (!columns && m < g.rows)
+    ortho_result<W>(g, (uint16_t*)g.d + o.batch * g.d_bs + m * g.d_rs + n * g.d_cs, g.d_cs, g.cols - n, v);
+}
+// W consecutive m of column n
+template <int OP, int W>
+__device__ __forceinline__ void ortho_column(const OrthoGemm& g, const OrthoTile& o, int32_t m, int32_t n, float (&v)[W]) {
+  if (!g.d)
+    ortho_store<OP, W>((g.OT ? g.OT : o.product ? g.O[1] : g.O[0]) + o.batch * g.O_bs + (int64_t)n * (OP * (int64_t)g.m) + m, g.m, v);
+  else if (n < g.cols)
+    ortho_result<W>(g, (uint16_t*)g.d + o.batch * g.d_bs + m + n * g.d_cs, 1, g.rows - m, v);
+}
 
 // The K-tiles: P0 Q0, then P1 Q0, then P0 Q1, T1 of 64 each.
 template <int PP, int PQ>
 struct OrthoPasses {
   static constexpr int N = PP + PQ - 1;
   static __device__ __forceinline__ int32_t of_p(int32_t t, int32_t T1) {
-    return PP == 2 && t < 2 * T1 ? t : PP == 2 ? t - 2 * T1 : t < T1 ? t : t - T1;
+    return t < PP * T1 ? t : t - PP * T1;
   }
-  // Q K-contiguous: plane 1 behind plane 0
   static __device__ __forceinline__ int32_t of_q(int32_t t, int32_t T1) {
-    return t < T1 ? t : PP == 2 ? t - T1 : t;
+    return PP == 2 && t >= T1 ? t - T1 : t;
   }
 };
 
 // ---------------------------------------------------------------------------
 // Outputs too small for 256 x 256 tiles to fill the chip: BM x BN tiles, KG
 // groups of four waves that take the K-tiles in turn (their sums meet in
-// LDS), each with a ring of STAGES K-tiles in LDS so that a copy has STAGES -
-// 2 K-tiles of compute to land.  One barrier a K-tile.
+// LDS), each with a ring of four K-tiles in LDS, so that a copy has two
+// K-tiles of compute to land.  A slice's fragments are read while the slice
+// before it computes, across the one barrier of a K-tile too.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int KG, int STAGES, bool N_MAJOR, int PP, int PQ, int OP>
+template <int BM, int BN, int KG, int PP, int PQ, int OP>
 __global__ __launch_bounds__(256 * KG) void ortho_gemm_kernel(const OrthoGemm g) {
   typedef OrthoPasses<PP, PQ> Pass;
+  constexpr int STAGES = 4;
   constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
   constexpr int ABYTES = BM * kRowBytes, BBYTES = BN * kRowBytes, STAGE = ABYTES + BBYTES;
   constexpr int PITCH = BN + 1;  // floats a row of the finished tile
@@ -300,17 +311,9 @@ __global__ __launch_bounds__(256 * KG) void ortho_gemm_kernel(const OrthoGemm g)
   const OrthoTile o = ortho_tile(g);
   const int32_t m0 = o.tm * BM, n0 = o.tn * BN;
   const int32_t rows_a = g.m - m0 < BM ? g.m - m0 : BM, rows_b = g.n - n0 < BN ? g.n - n0 : BN;
-  const int64_t pk = (int64_t)PP * g.k, qk = N_MAJOR ? (int64_t)PQ * g.n : (int64_t)PQ * g.k;
+  const int64_t pk = (int64_t)PP * g.k, qk = (int64_t)PQ * g.k;
   LoaderKVec<BM, 256, 0, 2> la(g.P + o.batch * g.P_bs + m0 * pk, rows_a, pk, 1, pk, wave, lane);
-  const uint16_t* qb = (o.product ? g.Q[1] : g.Q[0]) + o.batch * g.Q_bs;
-  auto make_b = [&](int plane) {
-    if constexpr (N_MAJOR)
-      return LoaderMNDma<BN, 256>(qb + n0 + plane * (int64_t)g.n, rows_b, 1, qk, g.k, wave, lane);
-    else
-      return LoaderKVec<BN, 256, 0, 2>(qb + n0 * qk, rows_b, qk, 1, qk, wave, lane);
-  };
-  auto lb = make_b(0);
-  auto lb1 = make_b(N_MAJOR && PQ == 2 ? 1 : 0);  // used where a plane is not a range of K
+  LoaderKVec<BN, 256, 0, 2> lb((o.product ? g.Q[1] : g.Q[0]) + o.batch * g.Q_bs + n0 * qk, rows_b, qk, 1, qk, wave, lane);
   constexpr int LOADS = decltype(la)::ITERS + decltype(lb)::ITERS;
   const int32_t a_row0 = (wave & 1) * TM, b_row0 = (wave >> 1) * TN;
   char* ring = smem + group * (STAGES * STAGE);
@@ -324,34 +327,41 @@ __global__ __launch_bounds__(256 * KG) void ortho_gemm_kernel(const OrthoGemm g)
   constexpr int32_t kPast = 1 << 24;  // a K-tile past every K: zeros
   auto issue = [&](int32_t i) {
     const int32_t t = i * KG + group;
-    char* at = ring + i % STAGES * STAGE;
+    char* at = ring + (i & (STAGES - 1)) * STAGE;
     la.issue(t < T ? Pass::of_p(t, T1) : kPast, at);
-    if (N_MAJOR && PQ == 2 && t >= PP * T1)
-      lb1.issue(t < T ? t - PP * T1 : kPast, at + ABYTES);
-    else if (N_MAJOR)
-      lb.issue(t < T ? (t < T1 ? t : t - T1) : kPast, at + ABYTES);
-    else
-      lb.issue(t < T ? Pass::of_q(t, T1) : kPast, at + ABYTES);
+    lb.issue(t < T ? Pass::of_q(t, T1) : kPast, at + ABYTES);
+  };
+  half8 af[2][FM], bf[2][FN];
+  auto read = [&](int32_t i, int ks) {
+    const char* cur = ring + (i & (STAGES - 1)) * STAGE;
+#pragma unroll
+    for (int a = 0; a < FM; ++a) af[ks][a] = read_frag<LOAD_KVEC, BM, 0>(cur, lane, a_row0 + 16 * a, ks);
+#pragma unroll
+    for (int b = 0; b < FN; ++b) bf[ks][b] = read_frag<LOAD_KVEC, BN, 0>(cur + ABYTES, lane, b_row0 + 16 * b, ks);
+  };
+  auto multiply = [&](int ks) {
+#pragma unroll
+    for (int a = 0; a < FM; ++a)
+#pragma unroll
+      for (int b = 0; b < FN; ++b) acc[a][b] = mfma16<DT_F16>(bf[ks][b], af[ks][a], acc[a][b]);
   };
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) issue(i);
+  wait_vmem_n<(STAGES - 2) * LOADS>();
+  phase_barrier();
+  read(0, 0);
   for (int32_t i = 0; i < rounds; ++i) {
-    wait_vmem_n<(STAGES - 2) * LOADS>();
-    phase_barrier();
+    wait_vmem_n<(STAGES - 3) * LOADS>();  // K-tile i + 1 has landed
+    phase_barrier();                      // for every wave, and K-tile i - 1 is no longer read
     issue(i + STAGES - 1);
-    const char* cur = ring + i % STAGES * STAGE;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      half8 af[FM], bf[FN];
-#pragma unroll
-      for (int a = 0; a < FM; ++a) af[a] = read_frag<LOAD_KVEC, BM, 0>(cur, lane, a_row0 + 16 * a, ks);
-#pragma unroll
-      for (int b = 0; b < FN; ++b) bf[b] = read_frag<N_MAJOR ? LOAD_MNDMA : LOAD_KVEC, BN, 0>(cur + ABYTES, lane, b_row0 + 16 * b, ks);
-#pragma unroll
-      for (int a = 0; a < FM; ++a)
-#pragma unroll
-        for (int b = 0; b < FN; ++b) acc[a][b] = mfma16<DT_F16>(bf[b], af[a], acc[a][b]);
-    }
+    read(i, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(0);
+    __builtin_amdgcn_sched_barrier(0);
+    read(i + 1, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(1);
+    __builtin_amdgcn_sched_barrier(0);
   }
   wait_vmem();
   __syncthreads();
@@ -372,92 +382,245 @@ __global__ __launch_bounds__(256 * KG) void ortho_gemm_kernel(const OrthoGemm g)
     }
     __syncthreads();
   }
-  const bool mirror = g.sym && o.tm != o.tn, columns = ortho_columns(g);
+  const bool columns = ortho_columns(g, o);
   constexpr int PIECES = BM * BN / 8 / (256 * KG);
 #pragma unroll
   for (int q = 0; q < PIECES; ++q) {
     const int32_t t = threadIdx.x + 256 * KG * q, ml = t / (BN / 8), nl = 8 * (t % (BN / 8));
     float* at = tile + ml * PITCH + nl;
+    if (m0 + ml >= g.m || n0 + nl >= g.n) continue;
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = at[e];
-    if (m0 + ml < g.m && n0 + nl < g.n) {
-      if (columns) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= o.alpha;
-        if (g.E) {
-#pragma unroll
-          for (int z = OP - 1; z >= 0; --z) {
-            const u16x8 x = *(const u16x8*)(g.E + o.batch * g.E_bs + (m0 + ml) * (OP * (int64_t)g.n) + z * (int64_t)g.n + n0 + nl);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(g.beta, to_f32<DT_F16>(x[e]), v[e]);
-          }
-        }
-      } else {
-        ortho_emit<OP, 8>(g, o, m0 + ml, n0 + nl, v);
-      }
-    }
-    if (mirror || columns) {
+    ortho_row<OP, 8>(g, o, columns, m0 + ml, n0 + nl, v);
+    if (columns) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) at[e] = v[e];
     }
   }
-  if (!mirror && !columns) return;
+  if (!columns) return;
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < PIECES; ++q) {
     const int32_t t = threadIdx.x + 256 * KG * q, ml = 8 * (t % (BM / 8)), nl = t / (BM / 8);
+    if (m0 + ml >= g.m || n0 + nl >= g.n) continue;
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = tile[(ml + e) * PITCH + nl];
-    if (m0 + ml < g.m && n0 + nl < g.n) ortho_emit_column<OP, 8>(g, o, m0 + ml, n0 + nl, v);
+    ortho_column<OP, 8>(g, o, m0 + ml, n0 + nl, v);
   }
 }
 
-template <int BM, int BN, int KG, int STAGES, bool NM, int PP, int PQ, int OP>
-hipError_t run_tiles(OrthoGemm g, hipStream_t s) {
-  g.tiles_m = (g.m + BM - 1) / BM, g.tiles_n = (g.n + BN - 1) / BN;
-  const int64_t tiles = g.sym ? (int64_t)g.tiles_n * (g.tiles_n + 1) / 2 : (int64_t)g.tiles_m * g.tiles_n;
-  hipLaunchKernelGGL((ortho_gemm_kernel<BM, BN, KG, STAGES, NM, PP, PQ, OP>), dim3((uint32_t)(tiles * g.batch * g.products)),
-                     dim3(256 * KG), 0, s, g);
+// ---------------------------------------------------------------------------
+// 256 x 256 tiles: four waves, one per SIMD, each a 128 x 128 block with its
+// accumulators in AGPRs, and a ring of five operand K-tiles in LDS, on the
+// schedule of gemm_f16_w4r_kernel (gemm_f16.hip), which see: operand tile q
+// (P's K-tile q / 2 for even q, Q's for odd q) in slot q % 5; per K-tile the
+// reads of slice 0 beside the second half of the last slice, slice 0 beside
+// the reads of slice 1, half of slice 1, one barrier.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void mfma_agpr(floatx4& c, const half8& a, const half8& b) {
+  asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+
+template <int PP, int PQ, int OP>
+__global__ __launch_bounds__(256, 1) void ortho_ring_kernel(const OrthoGemm g) {
+  typedef OrthoPasses<PP, PQ> Pass;
+  constexpr int F = 8, SLOT = 256 * kRowBytes, LOADS = 8;
+  __shared__ __attribute__((aligned(1024))) char smem[5 * SLOT];
+  const int32_t lane = threadIdx.x & 63;
+  const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const OrthoTile o = ortho_tile(g);
+  const int32_t m0 = o.tm * 256, n0 = o.tn * 256;
+  const int32_t rows_a = g.m - m0 < 256 ? g.m - m0 : 256, rows_b = g.n - n0 < 256 ? g.n - n0 : 256;
+  const int64_t pk = (int64_t)PP * g.k, qk = (int64_t)PQ * g.k;
+  LoaderKVec<256, 256, 0, 2> la(g.P + o.batch * g.P_bs + m0 * pk, rows_a, pk, 1, pk, wave, lane);
+  LoaderKVec<256, 256, 0, 2> lb((o.product ? g.Q[1] : g.Q[0]) + o.batch * g.Q_bs + n0 * qk, rows_b, qk, 1, qk, wave, lane);
+  floatx4 acc[F][F];
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < F; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  const int32_t a_row0 = (wave & 1) * 128, b_row0 = (wave >> 1) * 128;
+  const int32_t T1 = g.k / 64, T = Pass::N * T1;
+  __builtin_assume(T >= 1);
+  // past the last K-tile the look-ahead copies repeat it and are not read
+  auto kt = [&](int32_t u) { return u < T ? u : T - 1; };
+  auto slot = [&](int32_t q) { return smem + q * SLOT; };
+  auto copy_a = [&](int32_t u, char* dst, int j) { la.issue_full(Pass::of_p(kt(u), T1), dst, j); };
+  auto copy_b = [&](int32_t u, char* dst, int j) { lb.issue_full(Pass::of_q(kt(u), T1), dst, j); };
+  half8 fa0[F], fb0[F], fa1[F], fb1[F];
+  typedef __attribute__((address_space(3))) const half8 lds_h8;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)smem;
+  uint32_t offA[2][2], offB[2][2], bA[2][2], bB[2][2];
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+    for (int par = 0; par < 2; ++par) {
+      offA[ks][par] = lds0 + (uint32_t)fragment_lds_offset(MFMA16_F16, lane, 0, a_row0 + 16 * par, ks, 0);
+      offB[ks][par] = lds0 + (uint32_t)fragment_lds_offset(MFMA16_F16, lane, 0, b_row0 + 16 * par, ks, 0);
+    }
+  auto bases = [&](int32_t qa, int32_t qb) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int par = 0; par < 2; ++par) {
+        bA[ks][par] = offA[ks][par] + (uint32_t)(qa * SLOT);
+        bB[ks][par] = offB[ks][par] + (uint32_t)(qb * SLOT);
+      }
+    // computed here, not next to the reads
+    asm volatile("" : "+v"(bA[0][0]), "+v"(bA[0][1]), "+v"(bA[1][0]), "+v"(bA[1][1]));
+    asm volatile("" : "+v"(bB[0][0]), "+v"(bB[0][1]), "+v"(bB[1][0]), "+v"(bB[1][1]));
+  };
+  auto read = [&](int r, int ks, half8(&fa)[F], half8(&fb)[F]) {
+    if (r < F)
+      fb[r] = *(lds_h8*)(uintptr_t)(bB[ks][r & 1] + 4096u * (uint32_t)(r >> 1));
+    else
+      fa[r - F] = *(lds_h8*)(uintptr_t)(bA[ks][r & 1] + 4096u * (uint32_t)((r - F) >> 1));
+  };
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j) copy_a(0, slot(0), j);
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j) copy_b(0, slot(1), j);
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j) copy_a(1, slot(2), j);
+  // the first tile's first part computes with zero fragments (adds nothing)
+#pragma unroll
+  for (int i = 0; i < F; ++i) fa1[i] = half8{}, fb1[i] = half8{};
+  wait_vmem_n<LOADS>();
+  phase_barrier();
+  int32_t sa = 0;  // slot of P's K-tile t; Q's in the next one
+  int32_t t = 0;
+  bases(0, 1);
+  // one copy of the loop body: a peeled or unswitched copy would give the
+  // accumulators a second path to the epilogue
+#pragma clang loop unroll(disable)
+  do {
+    const int32_t s3 = sa + 3 >= 5 ? sa - 2 : sa + 3, s4 = sa == 0 ? 4 : sa - 1;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      read(q, 0, fa0, fb0);
+      if (!(q & 1)) copy_b(t + 1, slot(s3), q >> 1);
+#pragma unroll
+      for (int e = 2 * q; e < 2 * q + 2; ++e) mfma_agpr(acc[F / 2 + e / F][e % F], fb1[e % F], fa1[F / 2 + e / F]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      read(q, 1, fa1, fb1);
+      if (q & 1) copy_a(t + 2, slot(s4), q >> 1);
+#pragma unroll
+      for (int e = 4 * q; e < 4 * q + 4; ++e) mfma_agpr(acc[e / F][e % F], fb0[e % F], fa0[e / F]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < F / 2; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j) mfma_agpr(acc[i][j], fb1[j], fa1[i]);
+    const int32_t na = sa + 2 >= 5 ? sa - 3 : sa + 2;
+    bases(na, na == 4 ? 0 : na + 1);
+    wait_vmem_n<LOADS>();  // in flight after this: P's K-tile t + 2
+    phase_barrier();
+    sa = na;
+  } while (++t < T);
+#pragma unroll
+  for (int i = F / 2; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < F; ++j) mfma_agpr(acc[i][j], fb1[j], fa1[i]);
+  wait_vmem();
+  // The MFMAs are inline assembly, so the compiler inserts no wait states
+  // before their results are read: empty volatile statements that re-define
+  // every accumulator hold the MFMAs before an idle of 32 cycles and every
+  // read after it.
+  auto pin = [&] {
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; j += 2) asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));
+  };
+  pin();
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+  pin();
+  // every wave's copies have landed and its reads of the ring are done
+  __syncthreads();
+  // the wave's block through its own 32 KiB of LDS, 64 rows at a time
+  const bool columns = ortho_columns(g, o);
+  char* region = smem + wave * 32768;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+        *(floatx4*)(region + rows_chunk(16 * i + (lane & 15), 4 * j + (lane >> 4))) = acc[4 * h + i][j];
+    const int32_t mb = m0 + a_row0 + 64 * h, nb = n0 + b_row0;
+#pragma unroll 8
+    for (int it = 0; it < 32; ++it) {
+      const int32_t r = 2 * it + (lane >> 5), q = lane & 31;
+      floatx4* at = (floatx4*)(region + rows_chunk(r, q));
+      if (mb + r >= g.m || nb + 4 * q >= g.n) continue;
+      const floatx4 x = *at;
+      float v[4] = {x[0], x[1], x[2], x[3]};
+      ortho_row<OP, 4>(g, o, columns, mb + r, nb + 4 * q, v);
+      if (columns) *at = floatx4{v[0], v[1], v[2], v[3]};
+    }
+    if (columns) {
+#pragma unroll 4
+      for (int it = 0; it < 32; ++it) {
+        const int32_t n = 4 * it + (lane >> 4), m = 4 * (lane & 15);
+        if (mb + m >= g.m || nb + n >= g.n) continue;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = *(const float*)(region + rows_chunk(m + e, n >> 2) + 4 * (n & 3));
+        ortho_column<OP, 4>(g, o, mb + m, nb + n, v);
+      }
+    }
+  }
+}
+
+// Workgroups of tiles of `side`
+int64_t ortho_tiles(const OrthoGemm& g, int64_t side) {
+  const int64_t tm = (g.m + side - 1) / side, tn = (g.n + side - 1) / side;
+  return (g.sym ? tn * (tn + 1) / 2 : tm * tn) * g.batch * g.products;
+}
+
+// The tile: the largest whose workgroups still fill the 256 CUs.
+template <int PP, int PQ, int OP>
+hipError_t run_gemm(OrthoGemm g, hipStream_t s) {
+  const int32_t side = ortho_tiles(g, 256) >= 200 ? 256 : ortho_tiles(g, 128) >= 160 ? 128 : 64;
+  g.tiles_m = (g.m + side - 1) / side, g.tiles_n = (g.n + side - 1) / side;
+  const dim3 grid((uint32_t)ortho_tiles(g, side));
+  if (side == 256)
+    hipLaunchKernelGGL((ortho_ring_kernel<PP, PQ, OP>), grid, dim3(256), 0, s, g);
+  else if (side == 128)
+    hipLaunchKernelGGL((ortho_gemm_kernel<128, 128, 1, PP, PQ, OP>), grid, dim3(256), 0, s, g);
+  else
+    hipLaunchKernelGGL((ortho_gemm_kernel<64, 64, 2, PP, PQ, OP>), grid, dim3(512), 0, s, g);
   return hipGetLastError();
 }
 
-// Q K-contiguous, a symmetric result
-template <int PP, int PQ, int OP>
-hipError_t run_sym(const OrthoGemm& g, hipStream_t s) {
-  const int64_t t = (g.m + 127) / 128, tiles = t * (t + 1) / 2 * g.batch * g.products;
-  if (tiles >= 160) return run_tiles<128, 128, 1, 4, false, PP, PQ, OP>(g, s);
-  return run_tiles<64, 64, 2, 4, false, PP, PQ, OP>(g, s);
-}
-// Q stored as (k, n)
-template <int PP, int PQ, int OP>
-hipError_t run_wide(const OrthoGemm& g, hipStream_t s) {
-  const int64_t tiles = (int64_t)((g.m + 127) / 128) * ((g.n + 127) / 128) * g.batch;
-  if (tiles >= 160) return run_tiles<128, 128, 1, 4, true, PP, PQ, OP>(g, s);
-  return run_tiles<64, 128, 2, 3, true, PP, PQ, OP>(g, s);
-}
-
 template <int T>
-hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, OrthoScales* scales, hipStream_t s) {
+hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, uint16_t* XT, OrthoScales* scales,
+                 hipStream_t s) {
   const int32_t tm = (int32_t)(pad64(p.m) / 64), tn = (int32_t)(pad64(p.n) / 64);
   hipLaunchKernelGGL(ortho_norm_kernel<T>, dim3(kNormParts, p.batch), dim3(256), 0, s, p, parts);
   const dim3 grid((uint32_t)((int64_t)p.batch * tm * tn)), block(256);
   if (exact && planes == 2)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 2, true>), grid, block, 0, s, p, parts, X, scales, tm, tn);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 2, true>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn);
   else if (exact)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 1, true>), grid, block, 0, s, p, parts, X, scales, tm, tn);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 1, true>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn);
   else if (planes == 2)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 2, false>), grid, block, 0, s, p, parts, X, scales, tm, tn);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 2, false>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn);
   else
-    hipLaunchKernelGGL((ortho_start_kernel<T, 1, false>), grid, block, 0, s, p, parts, X, scales, tm, tn);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 1, false>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn);
   return hipGetLastError();
 }
-hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, OrthoScales* scales, hipStream_t s) {
+hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, uint16_t* XT, OrthoScales* scales,
+                 hipStream_t s) {
   switch (p.x_type) {
-    case OT_F16: return start<OT_F16>(p, planes, exact, parts, X, scales, s);
-    case OT_BF16: return start<OT_BF16>(p, planes, exact, parts, X, scales, s);
-    default: return start<OT_F32>(p, planes, exact, parts, X, scales, s);
+    case OT_F16: return start<OT_F16>(p, planes, exact, parts, X, XT, scales, s);
+    case OT_BF16: return start<OT_BF16>(p, planes, exact, parts, X, XT, scales, s);
+    default: return start<OT_F32>(p, planes, exact, parts, X, XT, scales, s);
   }
 }
 
@@ -487,7 +650,7 @@ int32_t x_planes(const OrthoParams& p, Way way) {
 }
 
 struct Places {
-  size_t scales, x[2], mm[5], total;  // byte offsets behind the partial sums
+  size_t scales, x, xt[2], mm[5], total;  // byte offsets behind the partial sums
 };
 Places places(const OrthoParams& p, Way way) {
   const int32_t xp = x_planes(p, way), mp = way == kGram ? 2 : xp;
@@ -495,9 +658,10 @@ Places places(const OrthoParams& p, Way way) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   Places q;
   q.scales = up((size_t)p.batch * kNormParts * 8);
-  q.x[0] = q.scales + up((size_t)p.batch * sizeof(OrthoScales));
-  q.x[1] = way == kGram ? q.x[0] : q.x[0] + mn;
-  size_t at = q.x[1] + mn;
+  q.x = q.scales + up((size_t)p.batch * sizeof(OrthoScales));
+  q.xt[0] = q.x + mn;
+  q.xt[1] = way == kGram ? q.xt[0] : q.xt[0] + mn;
+  size_t at = q.xt[1] + mn;
   for (int i = 0; i < 5; ++i) {
     q.mm[i] = at;
     if (way == kGram || i < 2) at += mm;
@@ -514,33 +678,34 @@ void to_result(const OrthoParams& p, OrthoGemm* g) {
 template <int PL>
 hipError_t direct(const OrthoParams& p, hipStream_t s) {
   const Places q = places(p, kDirect);
-  uint16_t* X[2] = {(uint16_t*)(p.ws + q.x[0]), (uint16_t*)(p.ws + q.x[1])};
+  uint16_t* X = (uint16_t*)(p.ws + q.x);
+  uint16_t* XT[2] = {(uint16_t*)(p.ws + q.xt[0]), (uint16_t*)(p.ws + q.xt[1])};
   uint16_t *G = (uint16_t*)(p.ws + q.mm[0]), *B = (uint16_t*)(p.ws + q.mm[1]);
   const int32_t mp = (int32_t)pad64(p.m), np = (int32_t)pad64(p.n);
   const int64_t mn = (int64_t)mp * np * PL, mm = (int64_t)mp * mp * PL;
   constexpr float kDown = 0x1p-10f;  // what a stored value times it stands for
-  hipError_t e = start(p, PL, false, (double*)p.ws, X[0], nullptr, s);
+  hipError_t e = start(p, PL, false, (double*)p.ws, X, XT[0], nullptr, s);
   for (int32_t k = 0; k < p.steps && e == hipSuccess; ++k) {
     const float a = p.coefficients[3 * k], b = p.coefficients[3 * k + 1], c = p.coefficients[3 * k + 2];
     // stored values carry 2^10, products of two 2^20
     OrthoGemm g{};
     g.batch = p.batch, g.products = 1;
-    g.P = g.Q[0] = X[k & 1], g.P_bs = g.Q_bs = mn;
+    g.P = g.Q[0] = X, g.P_bs = g.Q_bs = mn;
     g.m = g.n = mp, g.k = np, g.alpha[0] = kDown, g.sym = 1;
     g.O[0] = G, g.O_bs = mm;
-    if ((e = run_sym<PL, PL, PL>(g, s)) != hipSuccess) break;
+    if ((e = run_gemm<PL, PL, PL>(g, s)) != hipSuccess) break;
     g.P = g.Q[0] = g.E = G, g.P_bs = g.Q_bs = g.E_bs = mm;
     g.k = mp, g.alpha[0] = c * kDown, g.beta = b;
     g.O[0] = B;
-    if ((e = run_sym<PL, PL, PL>(g, s)) != hipSuccess) break;
-    g.P = B, g.Q[0] = g.E = X[k & 1], g.Q_bs = g.E_bs = mn;
+    if ((e = run_gemm<PL, PL, PL>(g, s)) != hipSuccess) break;
+    g.P = B, g.Q[0] = XT[k & 1], g.E = X, g.Q_bs = g.E_bs = mn;
     g.n = np, g.alpha[0] = kDown, g.beta = a, g.sym = 0;
-    g.O[0] = X[(k + 1) & 1], g.O_bs = mn;
+    g.O[0] = X, g.OT = XT[(k + 1) & 1], g.O_bs = mn;
     if (k + 1 == p.steps) {
       g.alpha[0] *= kDown, g.beta *= kDown;
       to_result(p, &g);
     }
-    e = run_wide<PL, PL, PL>(g, s);
+    e = run_gemm<PL, PL, PL>(g, s);
   }
   return e;
 }
@@ -550,21 +715,21 @@ template <int PX>
 hipError_t gram(const OrthoParams& p, hipStream_t s) {
   const Places q = places(p, kGram);
   OrthoScales* scales = (OrthoScales*)(p.ws + q.scales);
-  uint16_t* X = (uint16_t*)(p.ws + q.x[0]);
+  uint16_t *X = (uint16_t*)(p.ws + q.x), *XT = (uint16_t*)(p.ws + q.xt[0]);
   uint16_t* M[5];
   for (int i = 0; i < 5; ++i) M[i] = (uint16_t*)(p.ws + q.mm[i]);
   uint16_t *G = M[0], *P = M[1], *H = M[2], *Q = nullptr;
   const int32_t mp = (int32_t)pad64(p.m), np = (int32_t)pad64(p.n);
   const int64_t mn = (int64_t)mp * np * PX, mm = (int64_t)mp * mp * 2;
   constexpr float kG = 0x1p12f, kP = 0x1p6f;  // what G's planes, and those of P, H and Q, are multiplied by
-  hipError_t e = start(p, PX, true, (double*)p.ws, X, scales, s);
+  hipError_t e = start(p, PX, true, (double*)p.ws, X, XT, scales, s);
   if (e != hipSuccess) return e;
   OrthoGemm g{};
   g.batch = p.batch, g.products = 1, g.sym = 1;
   g.P = g.Q[0] = X, g.P_bs = g.Q_bs = mn;
   g.m = g.n = mp, g.k = np, g.alpha[0] = 1.f, g.scales = scales;
   g.O[0] = G, g.O_bs = mm;
-  if ((e = run_sym<PX, PX, 2>(g, s)) != hipSuccess) return e;
+  if ((e = run_gemm<PX, PX, 2>(g, s)) != hipSuccess) return e;
   g.scales = nullptr, g.P_bs = g.Q_bs = g.E_bs = mm, g.k = mp;
   for (int32_t k = 0; k < p.steps; ++k) {
     const float a = p.coefficients[3 * k], b = p.coefficients[3 * k + 1], c = p.coefficients[3 * k + 2];
@@ -573,7 +738,7 @@ hipError_t gram(const OrthoParams& p, hipStream_t s) {
     uint16_t* Pk = k == 0 ? M[3] : P;
     g.P = g.Q[0] = g.E = G, g.alpha[0] = c * (kP / (kG * kG)), g.beta = b * (kP / kG), g.diag = a * kP;
     g.O[0] = Pk;
-    if ((e = run_sym<2, 2, 2>(g, s)) != hipSuccess) return e;
+    if ((e = run_gemm<2, 2, 2>(g, s)) != hipSuccess) return e;
     g.E = nullptr, g.diag = 0.f;
     uint16_t* next = Q == M[3] ? M[4] : M[3];
     g.P = Pk;
@@ -581,17 +746,17 @@ hipError_t gram(const OrthoParams& p, hipStream_t s) {
     int i = 0;
     if (!last) g.Q[i] = G, g.O[i] = H, g.alpha[i] = 1.f / kG, ++i;
     if (k > 0) g.Q[i] = Q, g.O[i] = next, g.alpha[i] = 1.f / kP;
-    if (g.products > 0 && (e = run_sym<2, 2, 2>(g, s)) != hipSuccess) return e;
+    if (g.products > 0 && (e = run_gemm<2, 2, 2>(g, s)) != hipSuccess) return e;
     g.products = 1;
     Q = k > 0 ? next : M[3];
     if (last) break;
     g.P = H, g.Q[0] = Pk, g.O[0] = G, g.alpha[0] = kG / (kP * kP);
-    if ((e = run_sym<2, 2, 2>(g, s)) != hipSuccess) return e;
+    if ((e = run_gemm<2, 2, 2>(g, s)) != hipSuccess) return e;
   }
-  g.P = Q, g.Q[0] = X, g.Q_bs = mn, g.n = np, g.sym = 0, g.alpha[0] = 1.f;
+  g.P = Q, g.Q[0] = XT, g.Q_bs = mn, g.n = np, g.sym = 0, g.alpha[0] = 1.f;
   g.scales = scales, g.scale_apply = 1;
   to_result(p, &g);
-  return run_wide<2, PX, 1>(g, s);
+  return run_gemm<2, PX, 1>(g, s);
 }
 
 }  // namespace
