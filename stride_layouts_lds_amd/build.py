@@ -23,7 +23,7 @@ SOURCES = ["api.cpp", "api_ops.cpp", "describe.cpp", "layout_algebra.cpp", "gemm
            "gemm_block.hip", "quantize.hip", "orthogonalize.hip",
            "ortho_gram.hip", "probes.hip", "scratch.hip"]
 HEADERS = ["sl_maps.hpp", "sl_kernels.hpp", "sl_ops.hpp", "sl_device.hpp", "layout_algebra.hpp", "describe.hpp",
-           "api_common.hpp", "api_ops.hpp"]
+           "api_common.hpp", "api_ops.hpp", "ortho_device.hpp"]
 ARCH = "gfx950"
 
 

@@ -233,6 +233,139 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void gemm_block_kernel(con
       block_store_quad<OT>(p, tc.batch, m0 + a_row0 + 16 * i + (lane & 15), n0 + b_row0 + 16 * j + 4 * (lane >> 4), acc[i][j]);
 }
 
+// 256 x 256 tiles for 16-bit results: 8 waves, two per SIMD, each 128 x 64,
+// and five slots for operand K-tiles (32 KiB each) in LDS: A and B of K-tiles
+// t and t + 1, and a free one.  One barrier, in the middle of K-tile t: K-tile
+// t + 1 has landed then, so the first fragments of t + 1 are read while t's
+// last products run, and the copies of t + 2 (A into the free slot, B into
+// B(t)'s, which is in registers) have a whole K-tile to land.  A block's sums
+// are scaled and added while the next ones run in the matrix core.
+template <int SBK, int OT>
+__global__ __launch_bounds__(512, 2) void gemm_block_ring_kernel(const BlockGemmParams p) {
+  typedef FragF8 Frag;
+  constexpr int FM = 8, FN = 4, SLOT = 256 * kRowBytes;
+  __shared__ __attribute__((aligned(1024))) char smem[5 * SLOT];
+  const int32_t lane = threadIdx.x & 63;
+  const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const TileCoord tc = map_tile(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.batch);
+  const int64_t m0 = (int64_t)tc.tm * 256, n0 = (int64_t)tc.tn * 256;
+  const int32_t rows_a = (int32_t)(p.M - m0 < 256 ? p.M - m0 : 256);
+  const int32_t rows_b = (int32_t)(p.N - n0 < 256 ? p.N - n0 : 256);
+  const LoaderKVec<256, 512, 0, 1> la(p.a + tc.batch * p.a_bs + m0 * p.a_rs, rows_a, p.a_rs, 1, p.K, wave, lane);
+  const LoaderKVec<256, 512, 0, 1> lb(p.b + tc.batch * p.b_bs + n0 * p.b_rs, rows_b, p.b_rs, 1, p.K, wave, lane);
+  constexpr int LOADS = decltype(la)::ITERS;
+  const int32_t a_row0 = wave % 2 * 128, b_row0 = wave / 2 * 64;
+
+  // A lane holds the scales of rows lane and lane + 64 of the wave's A and of
+  // row lane of its B (rows past the operand: its last one's; their results
+  // are not stored), and takes those that a result needs from the lanes that
+  // hold them.
+  auto row_scale = [&](const float* base, int64_t row, int64_t rows, int32_t shift, int64_t rs) {
+    return base + ((row < rows ? row : rows - 1) >> shift) * rs;
+  };
+  const float* sa_base = p.sa + tc.batch * p.sa_bs;
+  const float* sa0 = row_scale(sa_base, m0 + a_row0 + lane, p.M, p.a_shift, p.sa_rs);
+  const float* sa1 = row_scale(sa_base, m0 + a_row0 + 64 + lane, p.M, p.a_shift, p.sa_rs);
+  const float* sb0 = row_scale(p.sb + tc.batch * p.sb_bs, n0 + b_row0 + (SBK == SB_ROWS ? lane : 0), p.N, p.b_shift, p.sb_rs);
+  struct Scales {
+    float a[2], b;
+  };
+  const int32_t T = p.k_blocks;
+  auto load_scales = [&](Scales& s, bool more) {
+    s.a[0] = *sa0, s.a[1] = *sa1, s.b = *sb0;
+    if (more) sa0 += p.sa_ks, sa1 += p.sa_ks, sb0 += p.sb_ks;
+  };
+  auto from_lane = [](float v, int32_t l) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(4 * l, __builtin_bit_cast(int32_t, v)));
+  };
+
+  floatx4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  if (T > 0) {
+    auto read = [&](int32_t slot, int32_t row0) {
+      const char* at = smem + slot * SLOT;
+      return Frag(*(const u32x4*)(at + fragment_lds_offset(MFMA16_F8, lane, 0, row0, 0, 0)),
+                  *(const u32x4*)(at + fragment_lds_offset(MFMA16_F8, lane, 1, row0, 0, 0)));
+    };
+    Scales cur, nxt;
+    load_scales(cur, T > 1);
+    la.issue(0, smem);
+    lb.issue(0, smem + SLOT);
+    la.issue(1, smem + 2 * SLOT);
+    lb.issue(1, smem + 3 * SLOT);
+    wait_vmem_n<2 * LOADS>();
+    phase_barrier();
+    // slots of A(t), B(t), A(t + 1), B(t + 1), and the free one
+    int32_t sa = 0, sb = 1, na = 2, nb = 3, fr = 4;
+    Frag bf[FN], af[2];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) bf[j] = read(sb, b_row0 + 16 * j);
+    af[0] = read(sa, a_row0);
+    for (int32_t t = 0; t < T; ++t) {
+      float sbv[SBK == SB_ROWS ? FN * 4 : 1];
+      if constexpr (SBK == SB_ROWS) {
+#pragma unroll
+        for (int j = 0; j < FN * 4; ++j) sbv[j] = from_lane(cur.b, 16 * (j / 4) + 4 * (lane >> 4) + j % 4);
+      } else {
+        sbv[0] = cur.b;
+      }
+      auto a_scale = [&](int i) { return from_lane(cur.a[i / 4], 16 * (i % 4) + (lane & 15)); };
+      float sav[3], sai = 0.f;
+      sav[0] = a_scale(0);
+      // product e of the wave's 32, its sums added LAG products later
+      constexpr int LAG = 3;
+      floatx4 sums[LAG + 1];
+#pragma unroll
+      for (int e = 0; e < FM * FN + LAG; ++e) {
+        const int i = e / FN, j = e % FN;
+        if (e == FM * FN / 2) {
+          // K-tile t + 1 has landed, for every wave, and B(t), read whole,
+          // is free.  LDS reads may be in flight: those of A(t), which is
+          // not, and the compiler waits for them where they are used.
+          __builtin_amdgcn_sched_barrier(0);
+          wait_vmem();
+          asm volatile("s_barrier" ::: "memory");
+          load_scales(nxt, t + 2 < T);
+          la.issue(t + 2, smem + fr * SLOT);
+          lb.issue(t + 2, smem + sb * SLOT);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (e < FM * FN) {
+          if (j == 0) {
+            af[(i + 1) & 1] = i + 1 < FM ? read(sa, a_row0 + 16 * (i + 1)) : read(na, a_row0);
+            if (i + 1 < FM) sav[(i + 1) % 3] = a_scale(i + 1);
+          }
+          sums[e % (LAG + 1)] = mfma_block(bf[j], af[i & 1]);
+          if (i + 1 == FM) bf[j] = read(nb, b_row0 + 16 * j);
+        }
+        if (e >= LAG) {
+          const int u = (e - LAG) / FN, w = (e - LAG) % FN;
+          if (w == 0) sai = SBK == SB_ROWS ? sav[u % 3] : sav[u % 3] * sbv[0];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float s = SBK == SB_ROWS ? sai * sbv[SBK == SB_ROWS ? 4 * w + r : 0] : sai;
+            acc[u][w][r] = __builtin_fmaf(sums[(e - LAG) % (LAG + 1)][r], s, acc[u][w][r]);
+          }
+        }
+        // left to itself, the compiler moved each read next to its use
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      cur = nxt;
+      const int32_t was_a = sa, was_b = sb;
+      sa = na, sb = nb, na = fr, nb = was_b, fr = was_a;
+    }
+    wait_vmem();
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      block_store_quad<OT>(p, tc.batch, m0 + a_row0 + 16 * i + (lane & 15), n0 + b_row0 + 16 * j + 4 * (lane >> 4), acc[i][j]);
+}
+
 // Few rows of A: the weight B is read once and bounds the call.  A workgroup
 // of 8 waves owns 16 FN rows of B and up to 16 FM rows of A; wave w takes the
 // K blocks w, w + 8, ... straight from memory into registers (a lane 32
@@ -363,8 +496,8 @@ hipError_t go(const BlockGemmParams& p, int32_t tile, hipStream_t s) {
   const bool square = p.b_shift != 0;
   if (tile == BT_256x256 && OT != OT_F32) {
     constexpr int OT2 = OT == OT_F32 ? OT_F16 : OT;  // fp32 results have no such tile
-    if (square) hipLaunchKernelGGL((gemm_block_kernel<256, 256, 2, 4, SB_SQUARE, OT2>), grid, dim3(512), 0, s, p);
-    else hipLaunchKernelGGL((gemm_block_kernel<256, 256, 2, 4, SB_ROWS, OT2>), grid, dim3(512), 0, s, p);
+    if (square) hipLaunchKernelGGL((gemm_block_ring_kernel<SB_SQUARE, OT2>), grid, dim3(512), 0, s, p);
+    else hipLaunchKernelGGL((gemm_block_ring_kernel<SB_ROWS, OT2>), grid, dim3(512), 0, s, p);
   } else if (tile == BT_128x128) {
     if (square) hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, SB_SQUARE, OT>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, SB_ROWS, OT>), grid, dim3(256), 0, s, p);

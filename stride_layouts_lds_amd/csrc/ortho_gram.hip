@@ -22,46 +22,13 @@
 // P's products commute, so G and Q stay symmetric and every operand is read
 // along its rows.  Bound by latency: at 96 x 128 a step is three products of
 // 96^3 and three barriers.
-#include "sl_ops.hpp"
-
-#include "sl_device.hpp"
+#include "ortho_device.hpp"
 
 namespace sl {
 namespace {
 
 constexpr float kGScale = 0x1p12f, kPScale = 0x1p6f;  // what the planes of G, and of P, H and Q, are multiplied by
 constexpr int32_t kTop = 14;                           // a range's largest magnitude becomes 2^14 to 2^15
-
-template <int T>
-__device__ __forceinline__ float ortho_widen(typename OrthoElem<T>::type v) {
-  if constexpr (T == OT_F32)
-    return __builtin_bit_cast(float, v);
-  else
-    return to_f32<T == OT_F16 ? DT_F16 : DT_BF16>(v);
-}
-
-// eight values of x at rows i .. (along_rows) or columns j .., zero outside
-// m x n
-template <int T>
-__device__ __forceinline__ void load8(const OrthoParams& p, int64_t b, int64_t i, int64_t j, int64_t j_end, bool along_rows,
-                                      float (&v)[8]) {
-  typedef typename OrthoElem<T>::type E;
-  typedef E vec8 __attribute__((ext_vector_type(8), aligned(sizeof(E))));
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = 0.f;
-  if (i >= p.m || j >= j_end) return;
-  const E* x = (const E*)p.x + b * p.x_bs + i * p.x_rs + j * p.x_cs;
-  const int64_t step = along_rows ? p.x_rs : p.x_cs, left = along_rows ? p.m - i : j_end - j;
-  if (step == 1 && left >= 8) {
-    const vec8 w = *(const vec8*)x;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = ortho_widen<T>(w[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) v[e] = ortho_widen<T>(x[e * step]);
-  }
-}
 
 __device__ __forceinline__ uint32_t top8(const float (&v)[8], uint32_t m) {
 #pragma unroll
@@ -135,7 +102,7 @@ __global__ __launch_bounds__(512) void gram_kernel(const OrthoParams p, const Or
 #pragma unroll
     for (int q = 0; q < PPT; ++q)
       if (PPT * 512 == MP * 8 || (int)threadIdx.x + 512 * q < MP * 8)
-        load8<T>(p, b, row_of(q), j + col_of(q), j1, along_rows, v[q]);
+        ortho_load8<T>(p, b, row_of(q), j + col_of(q), j1, along_rows, v[q]);
   };
 #pragma unroll
   for (int q = 0; q < PPT; ++q)
@@ -486,7 +453,7 @@ __global__ __launch_bounds__(256) void gram_apply_kernel(const OrthoParams p, co
   auto col_of = [&](int q) { const int32_t t = threadIdx.x + 256 * q; return along_rows ? t / (MP / 8) : 8 * (t % 16); };
   uint32_t top = 0;
 #pragma unroll
-  for (int q = 0; q < PPT; ++q) load8<T>(p, b, row_of(q), j0 + col_of(q), p.n, along_rows, v[q]);
+  for (int q = 0; q < PPT; ++q) ortho_load8<T>(p, b, row_of(q), j0 + col_of(q), p.n, along_rows, v[q]);
   // Q's fragments, all in flight before x's values are used
   const char* Q = q_all + b * M::BYTES;
   const int32_t m0 = wave % WM * (16 * FM), n0 = wave / WM * (16 * FN);

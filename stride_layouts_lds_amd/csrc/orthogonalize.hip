@@ -23,9 +23,7 @@
 // Every product reads both operands along K: X is kept in both orientations
 // (read as it lies, by transposing LDS reads, it cost a product of 8192^3
 // half as much again).
-#include "sl_ops.hpp"
-
-#include "sl_device.hpp"
+#include "ortho_device.hpp"
 
 namespace sl {
 namespace {
@@ -33,41 +31,35 @@ namespace {
 constexpr int32_t kNormParts = 256;               // partial sums of squares of one matrix
 constexpr int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 
-template <int T>
-__device__ __forceinline__ float load_any(const void* p, int64_t off) {
-  if constexpr (T == OT_F32)
-    return ((const float*)p)[off];
-  else
-    return to_f32<T == OT_F16 ? DT_F16 : DT_BF16>(((const uint16_t*)p)[off]);
-}
+constexpr int kNormWaves = 16;
 
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
-  return ((lds[0] + lds[1]) + lds[2]) + lds[3];
+  v = 0;
+  for (uint32_t w = 0; w < blockDim.x / 64; ++w) v += lds[w];
+  return v;
 }
 
-// sum of squares of part blockIdx.x of matrix blockIdx.y: the 64 x 64 tiles
-// blockIdx.x, + kNormParts, ...
+// sum of squares of part blockIdx.x of matrix blockIdx.y: lines along x's
+// contiguous axis, `across` threads (a power of two) to a line
 template <int T>
-__global__ __launch_bounds__(256) void ortho_norm_kernel(const OrthoParams p, double* parts) {
-  __shared__ double lds[4];
+__global__ __launch_bounds__(64 * kNormWaves) void ortho_norm_kernel(const OrthoParams p, double* parts, int32_t across) {
+  __shared__ double lds[kNormWaves];
   const int64_t b = blockIdx.y;
-  const int32_t tiles_n = (int32_t)((p.n + 63) / 64), tiles = (int32_t)((p.m + 63) / 64) * tiles_n;
-  const bool along_rows = p.x_rs == 1 && p.x_cs != 1;  // the lanes' axis: the contiguous one
-  const int32_t u = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const bool along_rows = p.x_rs == 1 && p.x_cs != 1;
+  const int64_t lines = along_rows ? p.n : p.m, length = along_rows ? p.m : p.n;
+  const int64_t u = threadIdx.x & (across - 1), w = threadIdx.x / across, at_once = 64 * kNormWaves / across;
   double s = 0;
-  for (int32_t t = blockIdx.x; t < tiles; t += kNormParts) {
-    const int64_t i0 = (int64_t)(t / tiles_n) * 64, j0 = (int64_t)(t % tiles_n) * 64;
+  for (int64_t c = 8 * u; c < length; c += 8 * across) {
+#pragma unroll 4
+    for (int64_t r = blockIdx.x * at_once + w; r < lines; r += kNormParts * at_once) {
+      float v[8];
+      ortho_load8<T>(p, b, along_rows ? c : r, along_rows ? r : c, p.n, along_rows, v);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int64_t i = i0 + (along_rows ? u : 4 * k + w), j = j0 + (along_rows ? 4 * k + w : u);
-      if (i < p.m && j < p.n) {
-        const double v = load_any<T>(p.x, b * p.x_bs + i * p.x_rs + j * p.x_cs);
-        s += v * v;
-      }
+      for (int e = 0; e < 8; ++e) s = __builtin_fma((double)v[e], (double)v[e], s);
     }
   }
   s = block_sum(s, lds);
@@ -106,28 +98,35 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, c
   }
   const int64_t i0 = 64 * (int64_t)tm, j0 = 64 * (int64_t)tn;
   const bool along_rows = p.x_rs == 1 && p.x_cs != 1;
-  const int32_t u = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int32_t u = threadIdx.x & 7, w = threadIdx.x >> 3;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int32_t il = along_rows ? u : 4 * k + w, jl = along_rows ? 4 * k + w : u;
-    const int64_t i = i0 + il, j = j0 + jl;
-    float v = 0.f;
-    if (i < p.m && j < p.n) v = as_computed((float)(load_any<T>(p.x, b * p.x_bs + i * p.x_rs + j * p.x_cs) * f));
+  for (int k = 0; k < 2; ++k) {
+    // eight along x's contiguous axis
+    const int32_t il = along_rows ? 8 * u : 32 * k + w, jl = along_rows ? 32 * k + w : 8 * u;
+    float v[8];
+    ortho_load8<T>(p, b, i0 + il, j0 + jl, p.n, along_rows, v);
 #pragma unroll
-    for (int q = 0; q < PLANES; ++q) {
-      const uint16_t h = from_f32<DT_F16>(v);
-      tile[q][il][jl] = h;
-      v -= to_f32<DT_F16>(h);
+    for (int e = 0; e < 8; ++e) {
+      float y = as_computed((float)(v[e] * f));
+#pragma unroll
+      for (int q = 0; q < PLANES; ++q) {
+        const uint16_t h = from_f32<DT_F16>(y);
+        tile[q][along_rows ? il + e : il][along_rows ? jl : jl + e] = h;
+        y -= to_f32<DT_F16>(h);
+      }
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int32_t r = 4 * k + w;
+  for (int k = 0; k < 2; ++k) {
+    const int32_t r = 32 * k + w;
 #pragma unroll
     for (int q = 0; q < PLANES; ++q) {
-      X[PLANES * (b * mp * np + (i0 + r) * np) + q * np + j0 + u] = tile[q][r][u];
-      XT[PLANES * (b * mp * np + (j0 + r) * mp) + q * mp + i0 + u] = tile[q][u][r];
+      u16x8 row, col;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) row[e] = tile[q][r][8 * u + e], col[e] = tile[q][8 * u + e][r];
+      *(u16x8*)(X + PLANES * (b * mp * np + (i0 + r) * np) + q * np + j0 + 8 * u) = row;
+      *(u16x8*)(XT + PLANES * (b * mp * np + (j0 + r) * mp) + q * mp + i0 + 8 * u) = col;
     }
   }
 }
@@ -150,6 +149,7 @@ struct OrthoGemm {
   int32_t sym;
   int32_t products;              // 1 or 2
   int32_t tiles_m, tiles_n, batch;
+  int32_t first, parts;          // tiles from this one on, each in parts x parts workgroups
   // the last step's result instead of O
   void* d;
   int64_t rows, cols, d_bs, d_rs, d_cs;
@@ -158,6 +158,7 @@ struct OrthoGemm {
 
 struct OrthoTile {
   int32_t batch, product, tm, tn;
+  bool mirror;  // off the diagonal of a symmetric result
   float alpha;
 };
 
@@ -170,7 +171,8 @@ __device__ __forceinline__ OrthoTile ortho_tile(const OrthoGemm& g) {
   constexpr uint32_t GR = 8;
   OrthoTile o;
   const uint32_t total = gridDim.x, x = blockIdx.x & 7, q = total >> 3, r = total & 7;
-  const uint32_t id = x * q + (x < r ? x : r) + (blockIdx.x >> 3);
+  const uint32_t at = x * q + (x < r ? x : r) + (blockIdx.x >> 3), parts = g.parts * g.parts;
+  const uint32_t id = g.first + at / parts, part = at % parts;
   const uint32_t nt = (uint32_t)g.tiles_n, per = g.sym ? nt * (nt + 1) / 2 : nt * (uint32_t)g.tiles_m;
   o.batch = id / (per * g.products);
   uint32_t t = id % (per * g.products);
@@ -196,6 +198,8 @@ __device__ __forceinline__ OrthoTile ortho_tile(const OrthoGemm& g) {
     const uint32_t R = left < GR ? left : GR, in = t % span;
     o.tm = first + in % R, o.tn = in / R;
   }
+  o.mirror = g.sym && o.tm != o.tn;
+  o.tm = o.tm * g.parts + part % g.parts, o.tn = o.tn * g.parts + part / g.parts;
   o.alpha = o.product ? g.alpha[1] : g.alpha[0];
   if (g.scales) o.alpha *= g.scale_apply ? g.scales[o.batch].apply : g.scales[o.batch].gram;
   return o;
@@ -256,7 +260,7 @@ __device__ __forceinline__ void ortho_result(const OrthoGemm& g, uint16_t* d, in
 
 // what a tile's second pass, along its columns, stores
 __device__ __forceinline__ bool ortho_columns(const OrthoGemm& g, const OrthoTile& o) {
-  return g.d ? g.d_rs == 1 && g.d_cs != 1 : (g.sym && o.tm != o.tn) || g.OT;
+  return g.d ? g.d_rs == 1 && g.d_cs != 1 : o.mirror || g.OT;
 }
 // W consecutive n of row m
 template <int OP, int W>
@@ -288,6 +292,28 @@ struct OrthoPasses {
   }
 };
 
+// An MFMA whose accumulator stays in AGPRs.  The statement is opaque to the
+// compiler: results are read only after agprs_settled.
+__device__ __forceinline__ void mfma_agpr(floatx4& c, const half8& a, const half8& b) {
+  asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+// The MFMAs above are inline assembly, so the compiler inserts no wait states
+// before their results are read: empty volatile statements that re-define
+// every accumulator hold the MFMAs before an idle of 32 cycles and every read
+// after it.
+template <int FM, int FN>
+__device__ __forceinline__ void agprs_settled(floatx4 (&acc)[FM][FN]) {
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; j += 2) asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; j += 2) asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));
+}
+
 // ---------------------------------------------------------------------------
 // Outputs too small for 256 x 256 tiles to fill the chip: BM x BN tiles, KG
 // groups of four waves that take the K-tiles in turn (their sums meet in
@@ -296,12 +322,16 @@ struct OrthoPasses {
 // before it computes, across the one barrier of a K-tile too.
 // ---------------------------------------------------------------------------
 template <int BM, int BN, int KG, int PP, int PQ, int OP>
-__global__ __launch_bounds__(256 * KG) void ortho_gemm_kernel(const OrthoGemm g) {
+__global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGemm g) {
   typedef OrthoPasses<PP, PQ> Pass;
   constexpr int STAGES = 4;
   constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
   constexpr int ABYTES = BM * kRowBytes, BBYTES = BN * kRowBytes, STAGE = ABYTES + BBYTES;
   constexpr int PITCH = BN + 1;  // floats a row of the finished tile
+  // sixteen accumulators: left to it, the compiler moved them between
+  // register files in every K-tile (and an accumulator comes up again only
+  // after fifteen others)
+  constexpr bool AGPR = FM * FN >= 16;
   constexpr int LDS = KG * STAGES * STAGE;
   static_assert(BM * PITCH * 4 <= LDS && LDS <= 160 * 1024, "LDS");
   __shared__ __attribute__((aligned(1024))) char smem[LDS];
@@ -310,6 +340,7 @@ __global__ __launch_bounds__(256 * KG) void ortho_gemm_kernel(const OrthoGemm g)
   const int32_t group = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
   const OrthoTile o = ortho_tile(g);
   const int32_t m0 = o.tm * BM, n0 = o.tn * BN;
+  if (m0 >= g.m || n0 >= g.n) return;  // a part of a tile at the edge
   const int32_t rows_a = g.m - m0 < BM ? g.m - m0 : BM, rows_b = g.n - n0 < BN ? g.n - n0 : BN;
   const int64_t pk = (int64_t)PP * g.k, qk = (int64_t)PQ * g.k;
   LoaderKVec<BM, 256, 0, 2> la(g.P + o.batch * g.P_bs + m0 * pk, rows_a, pk, 1, pk, wave, lane);
@@ -343,14 +374,19 @@ __global__ __launch_bounds__(256 * KG) void ortho_gemm_kernel(const OrthoGemm g)
 #pragma unroll
     for (int a = 0; a < FM; ++a)
 #pragma unroll
-      for (int b = 0; b < FN; ++b) acc[a][b] = mfma16<DT_F16>(bf[ks][b], af[ks][a], acc[a][b]);
+      for (int b = 0; b < FN; ++b) {
+        if constexpr (AGPR) mfma_agpr(acc[a][b], bf[ks][b], af[ks][a]);
+        else acc[a][b] = mfma16<DT_F16>(bf[ks][b], af[ks][a], acc[a][b]);
+      }
   };
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) issue(i);
   wait_vmem_n<(STAGES - 2) * LOADS>();
   phase_barrier();
   read(0, 0);
-  for (int32_t i = 0; i < rounds; ++i) {
+  int32_t i = 0;
+#pragma clang loop unroll(disable)
+  do {
     wait_vmem_n<(STAGES - 3) * LOADS>();  // K-tile i + 1 has landed
     phase_barrier();                      // for every wave, and K-tile i - 1 is no longer read
     issue(i + STAGES - 1);
@@ -362,8 +398,9 @@ __global__ __launch_bounds__(256 * KG) void ortho_gemm_kernel(const OrthoGemm g)
     __builtin_amdgcn_sched_barrier(0);
     multiply(1);
     __builtin_amdgcn_sched_barrier(0);
-  }
+  } while (++i < rounds);
   wait_vmem();
+  if constexpr (AGPR) agprs_settled(acc);
   __syncthreads();
 
   // the groups' sums, one after the other, into the finished tile
@@ -419,10 +456,6 @@ __global__ __launch_bounds__(256 * KG) void ortho_gemm_kernel(const OrthoGemm g)
 // reads of slice 0 beside the second half of the last slice, slice 0 beside
 // the reads of slice 1, half of slice 1, one barrier.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void mfma_agpr(floatx4& c, const half8& a, const half8& b) {
-  asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-}
-
 template <int PP, int PQ, int OP>
 __global__ __launch_bounds__(256, 1) void ortho_ring_kernel(const OrthoGemm g) {
   typedef OrthoPasses<PP, PQ> Pass;
@@ -528,19 +561,7 @@ __global__ __launch_bounds__(256, 1) void ortho_ring_kernel(const OrthoGemm g) {
 #pragma unroll
     for (int j = 0; j < F; ++j) mfma_agpr(acc[i][j], fb1[j], fa1[i]);
   wait_vmem();
-  // The MFMAs are inline assembly, so the compiler inserts no wait states
-  // before their results are read: empty volatile statements that re-define
-  // every accumulator hold the MFMAs before an idle of 32 cycles and every
-  // read after it.
-  auto pin = [&] {
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-      for (int j = 0; j < F; j += 2) asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));
-  };
-  pin();
-  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
-  pin();
+  agprs_settled(acc);
   // every wave's copies have landed and its reads of the ring are done
   __syncthreads();
   // the wave's block through its own 32 KiB of LDS, 64 rows at a time
@@ -584,18 +605,34 @@ int64_t ortho_tiles(const OrthoGemm& g, int64_t side) {
   return (g.sym ? tn * (tn + 1) / 2 : tm * tn) * g.batch * g.products;
 }
 
-// The tile: the largest whose workgroups still fill the 256 CUs.
 template <int PP, int PQ, int OP>
-hipError_t run_gemm(OrthoGemm g, hipStream_t s) {
-  const int32_t side = ortho_tiles(g, 256) >= 200 ? 256 : ortho_tiles(g, 128) >= 160 ? 128 : 64;
-  g.tiles_m = (g.m + side - 1) / side, g.tiles_n = (g.n + side - 1) / side;
-  const dim3 grid((uint32_t)ortho_tiles(g, side));
+void launch_tiles(OrthoGemm g, int32_t side, int64_t first, int64_t count, hipStream_t s) {
+  const dim3 grid((uint32_t)(count * g.parts * g.parts));
+  g.first = (int32_t)first;
+  g.tiles_m = (g.m + side * g.parts - 1) / (side * g.parts), g.tiles_n = (g.n + side * g.parts - 1) / (side * g.parts);
   if (side == 256)
     hipLaunchKernelGGL((ortho_ring_kernel<PP, PQ, OP>), grid, dim3(256), 0, s, g);
   else if (side == 128)
     hipLaunchKernelGGL((ortho_gemm_kernel<128, 128, 1, PP, PQ, OP>), grid, dim3(256), 0, s, g);
   else
     hipLaunchKernelGGL((ortho_gemm_kernel<64, 64, 2, PP, PQ, OP>), grid, dim3(512), 0, s, g);
+}
+
+// The tile: the largest whose workgroups still fill the 256 CUs.  What a last
+// round of 256 x 256 tiles would leave most CUs without goes to 64 x 64
+// tiles: a symmetric 8192 x 8192 result has 528 tiles, and a third round for
+// 16 of them took 180 of 596 us.
+template <int PP, int PQ, int OP>
+hipError_t run_gemm(OrthoGemm g, hipStream_t s) {
+  const int32_t side = ortho_tiles(g, 256) >= 200 ? 256 : ortho_tiles(g, 128) >= 160 ? 128 : 64;
+  const int64_t all = ortho_tiles(g, side), rest = all % 256;
+  const int64_t whole = side == 256 && all > 256 && rest <= 64 ? all - rest : all;
+  g.parts = 1;
+  launch_tiles<PP, PQ, OP>(g, side, 0, whole, s);
+  if (whole < all) {
+    g.parts = 4;
+    launch_tiles<PP, PQ, OP>(g, 64, whole, all - whole, s);
+  }
   return hipGetLastError();
 }
 
@@ -603,7 +640,10 @@ template <int T>
 hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, uint16_t* XT, OrthoScales* scales,
                  hipStream_t s) {
   const int32_t tm = (int32_t)(pad64(p.m) / 64), tn = (int32_t)(pad64(p.n) / 64);
-  hipLaunchKernelGGL(ortho_norm_kernel<T>, dim3(kNormParts, p.batch), dim3(256), 0, s, p, parts);
+  const int64_t length = p.x_rs == 1 && p.x_cs != 1 ? p.m : p.n;
+  int32_t across = 64 * kNormWaves;
+  while (across > 1 && 4 * (int64_t)across >= length) across /= 2;
+  hipLaunchKernelGGL(ortho_norm_kernel<T>, dim3(kNormParts, p.batch), dim3(64 * kNormWaves), 0, s, p, parts, across);
   const dim3 grid((uint32_t)((int64_t)p.batch * tm * tn)), block(256);
   if (exact && planes == 2)
     hipLaunchKernelGGL((ortho_start_kernel<T, 2, true>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn);
