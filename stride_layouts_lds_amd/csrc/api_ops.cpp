@@ -162,7 +162,7 @@ sl_status plan_block(const sl_gemm_args* args, BlockPlan* out) {
   if (total >= kLim) return fail(SL_ERR_SHAPE, "too many output tiles (%lld)", (long long)total);
   P.pub.a_load = P.pub.b_load = LOAD_KVEC;
   P.pub.tile_m = ts.bm, P.pub.tile_n = ts.bn, P.pub.tile_k = kScaleBlock;
-  P.pub.threads = P.tile == BT_SKINNY ? kSkinnyWaves * 64 : ts.wm * ts.wn * 64;
+  P.pub.threads = P.tile == BT_SKINNY ? (M <= 16 ? kSkinnyWaves : kStreamWaves) * 64 : ts.wm * ts.wn * 64;
   P.pub.workgroups = total;
   P.pub.lds_bytes = ts.stages * (ts.bm + ts.bn) * kScaleBlock;
   return SL_OK;

@@ -17,6 +17,8 @@
 // show that, so for them the codes become fp16 in registers (exact) and four
 // steps of the fp16 instruction, at half the rate, sum the block (measured
 // 1e-8 of the result).
+#include <type_traits>
+
 #include "sl_ops.hpp"
 
 #include "sl_device.hpp"
@@ -122,6 +124,16 @@ __device__ __forceinline__ void block_store_quad(const BlockGemmParams& p, int64
   }
 }
 
+// A lane holds the scale of one row of its wave's A or B (of the operand's
+// last row, past it: those results are not stored); the lanes that need it
+// take it from there.
+__device__ __forceinline__ const float* row_scale(const float* base, int64_t row, int64_t rows, int32_t shift, int64_t rs) {
+  return base + ((row < rows ? row : rows - 1) >> shift) * rs;
+}
+__device__ __forceinline__ float from_lane(float v, int32_t l) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(4 * l, __builtin_bit_cast(int32_t, v)));
+}
+
 // how a tile reads SB: one scale for the wave's columns (128 x 128 blocks), or
 // one per row of B
 constexpr int SB_SQUARE = 0, SB_ROWS = 1;
@@ -150,30 +162,9 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void gemm_block_kernel(con
   LoaderKVec<BN, NT, 0, 1> lb(p.b + tc.batch * p.b_bs + n0 * p.b_rs, rows_b, p.b_rs, 1, p.K, wave, lane);
   const int32_t a_row0 = wm * TM, b_row0 = wn * TN;
 
-  // scale pointers; rows past the operand read its last one (their results
-  // are not stored)
-  const float* sa_p[FM];
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    int64_t m = m0 + a_row0 + 16 * i + (lane & 15);
-    m = m < p.M ? m : p.M - 1;
-    sa_p[i] = p.sa + tc.batch * p.sa_bs + (m >> p.a_shift) * p.sa_rs;
-  }
-  const float* sb_base = p.sb + tc.batch * p.sb_bs;
-  int64_t nw = n0 + b_row0;
-  nw = nw < p.N ? nw : p.N - 1;
-  const float* sb_w = sb_base + (nw >> p.b_shift) * p.sb_rs;
-  int64_t sb_off[SBK == SB_ROWS ? FN : 1][4];
-  if constexpr (SBK == SB_ROWS) {
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        int64_t n = n0 + b_row0 + 16 * j + 4 * (lane >> 4) + r;
-        n = n < p.N ? n : p.N - 1;
-        sb_off[j][r] = (n >> p.b_shift) * p.sb_rs;
-      }
-  }
+  static_assert(TM == 64 && TN == 64, "a lane holds one row's scale");
+  const float* sa_p = row_scale(p.sa + tc.batch * p.sa_bs, m0 + a_row0 + lane, p.M, p.a_shift, p.sa_rs);
+  const float* sb_p = row_scale(p.sb + tc.batch * p.sb_bs, n0 + b_row0 + lane, p.N, p.b_shift, p.sb_rs);
 
   floatx4 acc[FM][FN];
 #pragma unroll
@@ -182,7 +173,9 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void gemm_block_kernel(con
     for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
   const int32_t T = p.k_blocks;
+  float sa_next = 0.f, sb_next = 0.f;
   if (T > 0) {
+    sa_next = *sa_p, sb_next = *sb_p;
     la.issue(0, smem);
     lb.issue(0, smem + ABYTES);
     wait_vmem();
@@ -191,16 +184,21 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void gemm_block_kernel(con
   for (int32_t t = 0; t < T; ++t) {
     char* cur = smem + (t & 1) * STAGE;
     char* nxt = smem + ((t + 1) & 1) * STAGE;
+    const float sa_own = sa_next, sb_own = sb_next;
+    if (t + 1 < T) {
+      sa_p += p.sa_ks, sb_p += p.sb_ks;
+      sa_next = *sa_p, sb_next = *sb_p;
+    }
     float sa[FM], sb[SBK == SB_ROWS ? FN : 1][4];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) sa[i] = sa_p[i][t * p.sa_ks];
+    for (int i = 0; i < FM; ++i) sa[i] = from_lane(sa_own, 16 * i + (lane & 15));
     if constexpr (SBK == SB_ROWS) {
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sb[j][r] = sb_base[sb_off[j][r] + t * p.sb_ks];
+        for (int r = 0; r < 4; ++r) sb[j][r] = from_lane(sb_own, 16 * j + 4 * (lane >> 4) + r);
     } else {
-      sb[0][0] = sb_w[t * p.sb_ks];
+      sb[0][0] = sb_own;  // the wave's columns lie in one block
     }
     la.issue(t + 1, nxt);
     lb.issue(t + 1, nxt + ABYTES);
@@ -257,12 +255,7 @@ __global__ __launch_bounds__(512, 2) void gemm_block_ring_kernel(const BlockGemm
   const int32_t a_row0 = wave % 2 * 128, b_row0 = wave / 2 * 64;
 
   // A lane holds the scales of rows lane and lane + 64 of the wave's A and of
-  // row lane of its B (rows past the operand: its last one's; their results
-  // are not stored), and takes those that a result needs from the lanes that
-  // hold them.
-  auto row_scale = [&](const float* base, int64_t row, int64_t rows, int32_t shift, int64_t rs) {
-    return base + ((row < rows ? row : rows - 1) >> shift) * rs;
-  };
+  // row lane of its B.
   const float* sa_base = p.sa + tc.batch * p.sa_bs;
   const float* sa0 = row_scale(sa_base, m0 + a_row0 + lane, p.M, p.a_shift, p.sa_rs);
   const float* sa1 = row_scale(sa_base, m0 + a_row0 + 64 + lane, p.M, p.a_shift, p.sa_rs);
@@ -274,9 +267,6 @@ __global__ __launch_bounds__(512, 2) void gemm_block_ring_kernel(const BlockGemm
   auto load_scales = [&](Scales& s, bool more) {
     s.a[0] = *sa0, s.a[1] = *sa1, s.b = *sb0;
     if (more) sa0 += p.sa_ks, sa1 += p.sa_ks, sb0 += p.sb_ks;
-  };
-  auto from_lane = [](float v, int32_t l) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(4 * l, __builtin_bit_cast(int32_t, v)));
   };
 
   floatx4 acc[FM][FN];
@@ -366,13 +356,14 @@ __global__ __launch_bounds__(512, 2) void gemm_block_ring_kernel(const BlockGemm
       block_store_quad<OT>(p, tc.batch, m0 + a_row0 + 16 * i + (lane & 15), n0 + b_row0 + 16 * j + 4 * (lane >> 4), acc[i][j]);
 }
 
-// Few rows of A: the weight B is read once and bounds the call.  A workgroup
-// of 8 waves owns 16 FN rows of B and up to 16 FM rows of A; wave w takes the
-// K blocks w, w + 8, ... straight from memory into registers (a lane 32
-// consecutive bytes of its row; the order of K inside a block is free as long
-// as A and B share it), and the waves' sums meet in LDS.
-template <int FM, int FN, int OT>
+// Up to 16 rows of A: the weight B is read once and bounds the call.  A
+// workgroup of 8 waves owns 16 FN rows of B; wave w takes the
+// K blocks w, w + 8, ... straight from memory into registers (four lanes read
+// 64 consecutive bytes of a row; the order of K inside a block is free as
+// long as A and B share it), and the waves' sums meet in LDS.
+template <int FN, int SBK, int OT>
 __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_block_skinny_kernel(const BlockGemmParams p) {
+  constexpr int FM = 1;
   __shared__ __attribute__((aligned(16))) float part[kSkinnyWaves - 1][FM * FN][64][4];
   const int32_t lane = threadIdx.x & 63;
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -386,10 +377,12 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_block_skinny_kernel(co
       make_rsrc(p.a + batch * p.a_bs + m0 * p.a_rs, (uint32_t)((rows_a - 1) * p.a_rs + p.K));
   const __amdgpu_buffer_rsrc_t rb =
       make_rsrc(p.b + batch * p.b_bs + n0 * p.b_rs, (uint32_t)((rows_b - 1) * p.b_rs + p.K));
-  const int32_t kl = 32 * (lane >> 4);
+  const int32_t kl = 16 * (lane >> 4);
   uint32_t off_a[FM], off_b[FN];
   const float* sa_p[FM];
-  int64_t sb_off[FN][4];
+  constexpr int NSB = SBK == SB_ROWS ? FN : 0;  // square blocks: one scale for the workgroup's columns
+  int64_t sb_off[SBK == SB_ROWS ? FN : 1][4];
+  sb_off[0][0] = (n0 >> p.b_shift) * p.sb_rs;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int32_t r = 16 * i + (lane & 15);
@@ -402,7 +395,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_block_skinny_kernel(co
     const int32_t r = 16 * j + (lane & 15);
     off_b[j] = r < rows_b ? (uint32_t)(r * p.b_rs + kl) : kOutOfRange;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < (SBK == SB_ROWS ? 4 : 0); ++e) {
       const int32_t n = 16 * j + 4 * (lane >> 4) + e;
       sb_off[j][e] = ((n0 + (n < rows_b ? n : rows_b - 1)) >> p.b_shift) * p.sb_rs;
     }
@@ -411,30 +404,31 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_block_skinny_kernel(co
 
   struct Regs {
     u32x4 a[FM][2], b[FN][2];
-    float sa[FM], sb[FN][4];
+    float sa[FM], sb[SBK == SB_ROWS ? FN : 1][4];
   };
   const int32_t T = p.k_blocks;
   auto load = [&](int32_t t, Regs& x) {
     const int32_t k = t * 128;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const bool in = t < T && k + kl + 16 * h < p.K;
+      const bool in = t < T && k + kl + 64 * h < p.K;
 #pragma unroll
       for (int j = 0; j < FN; ++j)
         x.b[j][h] = __builtin_amdgcn_raw_buffer_load_b128(
-            rb, in && off_b[j] != kOutOfRange ? off_b[j] + (uint32_t)(k + 16 * h) : kOutOfRange, 0, 0);
+            rb, in && off_b[j] != kOutOfRange ? off_b[j] + (uint32_t)(k + 64 * h) : kOutOfRange, 0, 0);
 #pragma unroll
       for (int i = 0; i < FM; ++i)
         x.a[i][h] = __builtin_amdgcn_raw_buffer_load_b128(
-            ra, in && off_a[i] != kOutOfRange ? off_a[i] + (uint32_t)(k + 16 * h) : kOutOfRange, 0, 0);
+            ra, in && off_a[i] != kOutOfRange ? off_a[i] + (uint32_t)(k + 64 * h) : kOutOfRange, 0, 0);
     }
     const int64_t ts = t < T ? t : T - 1;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) x.sa[i] = sa_p[i][ts * p.sa_ks];
+    for (int i = 0; i < FM; ++i) x.sa[i] = t < T ? sa_p[i][ts * p.sa_ks] : 0.f;  // past the last block: adds 0
+    if constexpr (SBK == SB_SQUARE) x.sb[0][0] = t < T ? sb_base[sb_off[0][0] + ts * p.sb_ks] : 0.f;
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+    for (int j = 0; j < NSB; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x.sb[j][e] = sb_base[sb_off[j][e] + ts * p.sb_ks];
+      for (int e = 0; e < 4; ++e) x.sb[j][e] = t < T ? sb_base[sb_off[j][e] + ts * p.sb_ks] : 0.f;
   };
   floatx4 acc[FM][FN];
 #pragma unroll
@@ -453,19 +447,24 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_block_skinny_kernel(co
       for (int j = 0; j < FN; ++j) {
         const floatx4 t4 = mfma_block(bf[j], af);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(t4[e], x.sa[i] * x.sb[j][e], acc[i][j][e]);
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(t4[e], x.sa[i] * x.sb[SBK == SB_ROWS ? j : 0][SBK == SB_ROWS ? e : 0], acc[i][j][e]);
       }
     }
   };
+  // DEPTH blocks requested ahead: a wave has few of them (8 at K = 8192), and
+  // two ahead left the call waiting for memory
+  constexpr int DEPTH = 4;
   if (wave < T) {
-    Regs x, y;
-    load(wave, x);
-    for (int32_t t = wave; t < T; t += 2 * kSkinnyWaves) {
-      load(t + kSkinnyWaves, y);
-      step(x);
-      if (t + kSkinnyWaves >= T) break;
-      load(t + 2 * kSkinnyWaves, x);
-      step(y);
+    Regs x[DEPTH];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(wave + d * kSkinnyWaves, x[d]);
+    for (int32_t t = wave; t < T; t += DEPTH * kSkinnyWaves) {
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        step(x[d]);
+        load(t + (d + DEPTH) * kSkinnyWaves, x[d]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
   if (wave > 0) {
@@ -490,6 +489,115 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_block_skinny_kernel(co
     }
 }
 
+// 17 to 64 rows of A: the same with the K blocks of a wave copied straight
+// into its own part of LDS, STAGES deep (in registers two blocks filled the
+// file: 48 x 8192 x 8192 took 26 us).  Four waves split K; no barrier until
+// their sums meet.
+template <int FM, int FN, int SBK, int OT>
+__global__ __launch_bounds__(kStreamWaves * 64, 1) void gemm_block_stream_kernel(const BlockGemmParams p) {
+  typedef typename FragOf<OT>::type Frag;
+  constexpr int STAGES = FM == 4 ? 3 : 4;
+  constexpr int ABYTES = 16 * FM * kRowBytes, STAGE = ABYTES + 16 * FN * kRowBytes;
+  __shared__ __attribute__((aligned(1024))) char smem[kStreamWaves * STAGES * STAGE];
+  static_assert((kStreamWaves - 1) * FM * FN * 1024 <= (int)sizeof smem, "the sums fit");
+  const int32_t lane = threadIdx.x & 63;
+  const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t id = blockIdx.x;
+  const int32_t tn = id % p.tiles_n, tm = id / p.tiles_n % p.tiles_m;
+  const int64_t batch = id / p.tiles_n / p.tiles_m;
+  const int64_t m0 = (int64_t)tm * kSkinnyRows, n0 = (int64_t)tn * (16 * FN);
+  const int32_t rows_a = (int32_t)(p.M - m0 < 16 * FM ? p.M - m0 : 16 * FM);
+  const int32_t rows_b = (int32_t)(p.N - n0 < 16 * FN ? p.N - n0 : 16 * FN);
+  const LoaderKVec<16 * FM, 64, 0, 1> la(p.a + batch * p.a_bs + m0 * p.a_rs, rows_a, p.a_rs, 1, p.K, 0, lane);
+  const LoaderKVec<16 * FN, 64, 0, 1> lb(p.b + batch * p.b_bs + n0 * p.b_rs, rows_b, p.b_rs, 1, p.K, 0, lane);
+  constexpr int LOADS = decltype(la)::ITERS + decltype(lb)::ITERS + 2;
+  const float* sa_p = row_scale(p.sa + batch * p.sa_bs, m0 + lane, p.M, p.a_shift, p.sa_rs);
+  const float* sb_p = row_scale(p.sb + batch * p.sb_bs, n0 + (lane & (16 * FN - 1)), p.N, p.b_shift, p.sb_rs);
+  char* ring = smem + wave * (STAGES * STAGE);
+  const int32_t T = p.k_blocks;
+  float sa[STAGES], sb[STAGES];  // of the rows `lane` of A and B
+  auto request = [&](int32_t t, int d) {
+    const int64_t at = t < T ? t : T - 1;
+    sa[d] = sa_p[at * p.sa_ks];
+    sb[d] = sb_p[at * p.sb_ks];
+    la.issue(t, ring + d * STAGE);  // past the last block: zeros
+    lb.issue(t, ring + d * STAGE + ABYTES);
+  };
+  floatx4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  auto step = [&](int32_t t, int d) {
+    const char* at = ring + d * STAGE;
+    auto read = [&](const char* x, int32_t row0) {
+      return Frag(*(const u32x4*)(x + fragment_lds_offset(MFMA16_F8, lane, 0, row0, 0, 0)),
+                  *(const u32x4*)(x + fragment_lds_offset(MFMA16_F8, lane, 1, row0, 0, 0)));
+    };
+    Frag bf[FN];
+    float sbv[FN][4];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      bf[j] = read(at + ABYTES, 16 * j);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sbv[j][r] = SBK == SB_ROWS ? from_lane(sb[d], 16 * j + 4 * (lane >> 4) + r) : sb[d];
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const Frag af = read(at, 16 * i);
+      const float sai = from_lane(sa[d], 16 * i + (lane & 15));
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const floatx4 t4 = mfma_block(bf[j], af);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(t4[r], sai * sbv[j][r], acc[i][j][r]);
+      }
+    }
+  };
+  if (wave < T) {
+#pragma unroll
+    for (int d = 0; d < STAGES - 1; ++d) request(wave + d * kStreamWaves, d);
+    for (int32_t t = wave; t < T; t += STAGES * kStreamWaves) {
+#pragma unroll
+      for (int d = 0; d < STAGES; ++d) {
+        // into the stage of the block before, whose reads are done
+        asm volatile("" ::: "memory");
+        request(t + (d + STAGES - 1) * kStreamWaves, (d + STAGES - 1) % STAGES);
+        wait_vmem_n<(STAGES - 1) * LOADS>();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        if (t + d * kStreamWaves < T) step(t + d * kStreamWaves, d);
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this block's reads
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  wait_vmem();
+  __syncthreads();
+  floatx4* part = (floatx4*)smem;  // [wave - 1][tile][lane]
+  if (wave > 0) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) part[((wave - 1) * FM * FN + i * FN + j) * 64 + lane] = acc[i][j];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      floatx4 v = acc[i][j];
+#pragma unroll
+      for (int w = 0; w < kStreamWaves - 1; ++w) {
+        const floatx4 o = part[(w * FM * FN + i * FN + j) * 64 + lane];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] += o[r];
+      }
+      block_store_quad<OT>(p, batch, m0 + 16 * i + (lane & 15), n0 + 16 * j + 4 * (lane >> 4), v);
+    }
+}
+
 template <int OT>
 hipError_t go(const BlockGemmParams& p, int32_t tile, hipStream_t s) {
   const dim3 grid((uint32_t)((int64_t)p.batch * p.tiles_m * p.tiles_n));
@@ -502,15 +610,23 @@ hipError_t go(const BlockGemmParams& p, int32_t tile, hipStream_t s) {
     if (square) hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, SB_SQUARE, OT>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, SB_ROWS, OT>), grid, dim3(256), 0, s, p);
   } else if (tile == BT_SKINNY) {
-    const dim3 block(kSkinnyWaves * 64);
     const bool wide = skinny_cols(p.M, p.N, p.batch) == 32;
-    const int fm = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
-    if (fm == 1 && wide) hipLaunchKernelGGL((gemm_block_skinny_kernel<1, 2, OT>), grid, block, 0, s, p);
-    if (fm == 1 && !wide) hipLaunchKernelGGL((gemm_block_skinny_kernel<1, 1, OT>), grid, block, 0, s, p);
-    if (fm == 2 && wide) hipLaunchKernelGGL((gemm_block_skinny_kernel<2, 2, OT>), grid, block, 0, s, p);
-    if (fm == 2 && !wide) hipLaunchKernelGGL((gemm_block_skinny_kernel<2, 1, OT>), grid, block, 0, s, p);
-    if (fm == 4 && wide) hipLaunchKernelGGL((gemm_block_skinny_kernel<4, 2, OT>), grid, block, 0, s, p);
-    if (fm == 4 && !wide) hipLaunchKernelGGL((gemm_block_skinny_kernel<4, 1, OT>), grid, block, 0, s, p);
+    auto skinny = [&](auto fm_c, auto fn_c, auto sb_c) {
+      constexpr int FM = decltype(fm_c)::value, FN = decltype(fn_c)::value, SBK = decltype(sb_c)::value;
+      if constexpr (FM == 1)
+        hipLaunchKernelGGL((gemm_block_skinny_kernel<FN, SBK, OT>), grid, dim3(kSkinnyWaves * 64), 0, s, p);
+      else
+        hipLaunchKernelGGL((gemm_block_stream_kernel<FM, FN, SBK, OT>), grid, dim3(kStreamWaves * 64), 0, s, p);
+    };
+    auto by_cols = [&](auto fm_c, auto sb_c) {
+      wide ? skinny(fm_c, std::integral_constant<int, 2>{}, sb_c) : skinny(fm_c, std::integral_constant<int, 1>{}, sb_c);
+    };
+    auto by_rows = [&](auto sb_c) {
+      if (p.M <= 16) by_cols(std::integral_constant<int, 1>{}, sb_c);
+      else if (p.M <= 32) by_cols(std::integral_constant<int, 2>{}, sb_c);
+      else by_cols(std::integral_constant<int, 4>{}, sb_c);
+    };
+    square ? by_rows(std::integral_constant<int, SB_SQUARE>{}) : by_rows(std::integral_constant<int, SB_ROWS>{});
   } else {
     return hipErrorInvalidValue;
   }

@@ -75,7 +75,8 @@ struct BlockTileShape {
 };
 constexpr BlockTileShape kBlockTiles[3] = {{256, 256, 2, 4, 2}, {128, 128, 2, 2, 2}, {64, 32, 1, 1, 0}};
 constexpr int32_t kSkinnyRows = 64;   // most rows of A of one skinny workgroup
-constexpr int32_t kSkinnyWaves = 8;
+constexpr int32_t kSkinnyWaves = 8;    // up to 16 rows of A
+constexpr int32_t kStreamWaves = 4;    // 17 to 64
 // rows of B of a skinny workgroup: 32 when that still gives every CU one
 inline int32_t skinny_cols(int64_t M, int64_t N, int64_t batch) {
   return batch * ((M + kSkinnyRows - 1) / kSkinnyRows) * ((N + 31) / 32) >= 256 ? 32 : 16;
