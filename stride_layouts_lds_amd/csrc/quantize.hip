@@ -38,8 +38,14 @@ struct BlockScale {
   __device__ __forceinline__ explicit BlockScale(uint32_t top_bits) {
     const float top = fmaxf(__builtin_bit_cast(float, top_bits), 0x1p-100f);
     d = top * 0x1p-10f;
-    r = 1.0f / d;
-    s = top / 448.0f;
+    // 1 / d: the hardware's reciprocal and one Newton step; top / 448: a
+    // product with the rounded 1 / 448 and one residual step (top is at least
+    // 2^-100, so nothing here is subnormal)
+    const float r0 = __builtin_amdgcn_rcpf(d);
+    r = __builtin_fmaf(__builtin_fmaf(-d, r0, 1.f), r0, r0);
+    constexpr float k = 1.f / 448.f;
+    const float s0 = top * k;
+    s = __builtin_fmaf(__builtin_fmaf(-448.f, s0, top), k, s0);
     if (top_bits >= kInfBits) d = r = s = __builtin_nanf("");
   }
   __device__ __forceinline__ float quotient(float x) const {
@@ -73,22 +79,22 @@ __device__ __forceinline__ float widen(typename Elem<T>::type v) {
 // eight consecutive columns of a row from column c0 (zero at and past
 // `cols`); CONTIG: unit column stride, one wide load that needs no more
 // than the element's own alignment
-template <int T, bool CONTIG>
+template <int T, bool CONTIG, bool WHOLE = false>
 __device__ __forceinline__ void load8(const typename Elem<T>::type* row, int64_t cs, int64_t c0, int64_t cols,
                                       bool row_ok, float (&v)[8]) {
   typedef typename Elem<T>::type E;
   typedef E vec8 __attribute__((ext_vector_type(8), aligned(sizeof(E))));
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = 0.f;
-  if (!row_ok) return;
-  if (CONTIG && c0 + 8 <= cols) {
+  if (!WHOLE && !row_ok) return;
+  if (CONTIG && (WHOLE || c0 + 8 <= cols)) {
     const vec8 x = *(const vec8*)(row + c0);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = widen<T>(x[e]);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (c0 + e < cols) v[e] = widen<T>(row[(c0 + e) * cs]);
+      if (WHOLE || c0 + e < cols) v[e] = widen<T>(row[(c0 + e) * cs]);
   }
 }
 
@@ -150,20 +156,29 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeParams
   }
 }
 
-// thread t of a tile: columns 8 (t % 16) .. + 7 of rows 8 (t / 16) .. + 7
-template <int T, bool CONTIG, bool SQUARE>
-__global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeParams p, uint32_t blocks_c, uint32_t blocks_r) {
+// The values as new ones: the compiler would otherwise keep what one stage
+// computed of each (its magnitude, 7/16 of it) for the next, another 64
+// registers.
+__device__ __forceinline__ void renew(float (&v)[8][8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(v[i][e]));
+}
+
+// thread t of a tile: columns 8 (t % 16) .. + 7 of rows 8 (t / 16) .. + 7.
+// WHOLE: 128 x 128 values in x and codes in every output, so nothing is
+// checked.
+template <int T, bool CONTIG, bool SQUARE, bool WHOLE>
+__device__ __forceinline__ void quantize_tile(const QuantizeParams& p, int64_t bc, int64_t br, int64_t b, char* codes,
+                                              uint32_t (*tops)[128]) {
   typedef typename Elem<T>::type E;
-  __shared__ __attribute__((aligned(16))) char codes[128 * 128];
-  __shared__ uint32_t tops[4][128];
-  const uint32_t id = blockIdx.x;
-  const int64_t bc = id % blocks_c, br = id / blocks_c % blocks_r, b = id / blocks_c / blocks_r;
   const int32_t g = threadIdx.x >> 4, l = threadIdx.x & 15, wave = threadIdx.x >> 6;
   const int64_t r0 = br * 128 + 8 * g, c0 = bc * 128 + 8 * l;
   const E* X = (const E*)p.x + b * p.x_bs;
   float v[8][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) load8<T, CONTIG>(X + (r0 + i) * p.x_rs, p.x_cs, c0, p.cols, r0 + i < p.rows, v[i]);
+  for (int i = 0; i < 8; ++i) load8<T, CONTIG, WHOLE>(X + (r0 + i) * p.x_rs, p.x_cs, c0, p.cols, WHOLE || r0 + i < p.rows, v[i]);
 
   uint32_t row_top[8], col_top[8];
 #pragma unroll
@@ -187,6 +202,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeParams
 #pragma unroll
     for (int i = 0; i < 8; ++i) row_top[i] = max16(row_top[i]);
     if (p.qt) {
+      renew(v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         uint32_t m = 0;
@@ -213,21 +229,23 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeParams
     }
   }
 
+  renew(v);
   const BlockScale whole(row_top[0]);  // SQUARE: the block's
   if (p.q) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t r = r0 + i;
+      __builtin_amdgcn_sched_barrier(0);  // one row's scale and codes at a time: registers for four waves a SIMD
       const BlockScale bs = SQUARE ? whole : BlockScale(row_top[i]);
-      if (r >= p.rows) continue;
+      if (!WHOLE && r >= p.rows) continue;
       if (SQUARE ? threadIdx.x == 0 && i == 0 : l == 0)
         p.s[b * p.s_bs + (SQUARE ? br : r) * p.s_rs + bc * p.s_cs] = bs.s;
       uint8_t* Q = p.q + b * p.q_bs + r * p.q_rs + c0;
       float q[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = c0 + e < p.cols ? bs.quotient(v[i][e]) : 0.f;
+      for (int e = 0; e < 8; ++e) q[e] = WHOLE || c0 + e < p.cols ? bs.quotient(v[i][e]) : 0.f;
       const u32x2 w = u32x2{pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7])};
-      if (c0 + 8 <= p.q_cols) {
+      if (WHOLE || c0 + 8 <= p.q_cols) {
         *(u32x2*)Q = w;
       } else {
 #pragma unroll
@@ -237,17 +255,19 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeParams
     }
   }
   if (p.qt) {
+    renew(v);
     // column c's 128 codes as 16 pieces of 8 bytes, piece g at g ^ (c / 8):
     // a wave's 64 stores of one register then spread over the pieces
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
+      __builtin_amdgcn_sched_barrier(0);
       const BlockScale bs = SQUARE ? whole : BlockScale(col_top[e]);
       float q[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = r0 + i < p.rows ? bs.quotient(v[i][e]) : 0.f;
+      for (int i = 0; i < 8; ++i) q[i] = WHOLE || r0 + i < p.rows ? bs.quotient(v[i][e]) : 0.f;
       *(u32x2*)(codes + (8 * l + e) * 128 + 8 * (g ^ l)) =
           u32x2{pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7])};
-      if (SQUARE ? threadIdx.x == 0 && e == 0 : g == 0 && c0 + e < p.cols)
+      if (SQUARE ? threadIdx.x == 0 && e == 0 : g == 0 && (WHOLE || c0 + e < p.cols))
         p.st[b * p.st_bs + (SQUARE ? bc : c0 + e) * p.st_rs + br * p.st_cs] = bs.s;
     }
     __syncthreads();
@@ -257,9 +277,9 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeParams
       const int32_t cl = 16 * e + g;
       const int64_t c = bc * 128 + cl, r = br * 128 + 8 * l;
       const u32x2 w = *(const u32x2*)(codes + cl * 128 + 8 * (l ^ (cl >> 3)));
-      if (c >= p.cols) continue;
+      if (!WHOLE && c >= p.cols) continue;
       uint8_t* Q = p.qt + b * p.qt_bs + c * p.qt_rs + r;
-      if (r + 8 <= p.qt_cols) {
+      if (WHOLE || r + 8 <= p.qt_cols) {
         *(u32x2*)Q = w;
       } else {
 #pragma unroll
@@ -268,6 +288,18 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantizeParams
       }
     }
   }
+}
+
+template <int T, bool CONTIG, bool SQUARE>
+__global__ __launch_bounds__(256, 4) void quantize_tile_kernel(const QuantizeParams p, uint32_t blocks_c, uint32_t blocks_r) {
+  __shared__ __attribute__((aligned(16))) char codes[128 * 128];
+  __shared__ uint32_t tops[4][128];
+  const uint32_t id = blockIdx.x;
+  const int64_t bc = id % blocks_c, br = id / blocks_c % blocks_r, b = id / blocks_c / blocks_r;
+  if ((bc + 1) * 128 <= p.cols && (br + 1) * 128 <= p.rows)
+    quantize_tile<T, CONTIG, SQUARE, true>(p, bc, br, b, codes, tops);
+  else
+    quantize_tile<T, CONTIG, SQUARE, false>(p, bc, br, b, codes, tops);
 }
 
 bool rows_only(const QuantizeParams& p) { return !p.qt && !p.square; }
