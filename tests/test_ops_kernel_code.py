@@ -1,0 +1,20 @@
+"""The orthogonalisation's kernels that issue their MFMAs as inline assembly on
+accumulators in AGPRs (256 x 256 and 128 x 128 tiles), under the checks that
+test_kernel_code.py makes of the GEMM's ring kernels."""
+
+import pytest
+
+import test_kernel_code as K
+from test_kernel_code import code_objects  # noqa: F401
+
+# symbol, MFMAs of one K-loop iteration, MFMAs after the loop
+NAMES = {}
+for pp, pq, op in ((1, 1, 1), (1, 1, 2), (2, 2, 1), (2, 2, 2), (2, 1, 1)):
+    NAMES[f"ortho_ring_{pp}{pq}{op}"] = (f"_ZN2sl12_GLOBAL__N_117ortho_ring_kernelILi{pp}ELi{pq}ELi{op}EEEvNS0_9OrthoGemmE", 128, 32)
+    NAMES[f"ortho_128_{pp}{pq}{op}"] = (f"_ZN2sl12_GLOBAL__N_117ortho_gemm_kernelILi128ELi128ELi1ELi{pp}ELi{pq}ELi{op}EEEvNS0_9OrthoGemmE", 32, 0)
+K.KERNELS.update(NAMES)
+
+
+@pytest.mark.parametrize("name", sorted(NAMES))
+def test_ortho_kernel_accumulator_discipline(code_objects, name):  # noqa: F811
+    K.test_ring_kernel_accumulator_discipline(code_objects, name)
