@@ -23,6 +23,8 @@
 // Every product reads both operands along K: X is kept in both orientations
 // (read as it lies, by transposing LDS reads, it cost a product of 8192^3
 // half as much again).
+#include <utility>
+
 #include "ortho_device.hpp"
 
 namespace sl {
@@ -66,6 +68,15 @@ __global__ __launch_bounds__(64 * kNormWaves) void ortho_norm_kernel(const Ortho
   if (threadIdx.x == 0) parts[b * kNormParts + blockIdx.x] = s;
 }
 
+// Where value (row, col) of a matrix with rows of `cols` lies.  Pairs: 32
+// values of the first plane, then the same 32 of the second, so that one
+// 128-byte K-tile of a row holds both planes of 32 values and three products
+// come from one copy.
+template <int PLANES>
+__device__ __forceinline__ int64_t plane_at(int64_t row, int64_t cols, int64_t col) {
+  return PLANES == 2 ? row * 2 * cols + (col >> 5) * 64 + (col & 31) : row * cols + col;
+}
+
 // What the products multiply by, one of each for every matrix.
 struct OrthoScales {
   float gram;   // of x's planes' Gram matrix, to make G's plane (2^12 G)
@@ -75,7 +86,8 @@ struct OrthoScales {
 // The planes that the products read: m x n and n x m, zero to the padded
 // sizes.
 // EXACT: x times the power of two that brings |x| to 2^14 (to 2^15): exact in
-// fp16 but for what lies 2^-38 below |x|; the scales follow.  Else 2^10 x /
+// fp16 but for what lies 2^-38 below |x|; the scales follow, and the
+// transpose is a pair in any case (its second plane zero).  Else 2^10 x /
 // (|x| + 1e-7), rounded.  With two planes also what the rounding left.
 template <int T, int PLANES, bool EXACT>
 __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, const double* parts, uint16_t* X,
@@ -125,22 +137,24 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, c
       u16x8 row, col;
 #pragma unroll
       for (int e = 0; e < 8; ++e) row[e] = tile[q][r][8 * u + e], col[e] = tile[q][8 * u + e][r];
-      *(u16x8*)(X + PLANES * (b * mp * np + (i0 + r) * np) + q * np + j0 + 8 * u) = row;
-      *(u16x8*)(XT + PLANES * (b * mp * np + (j0 + r) * mp) + q * mp + i0 + 8 * u) = col;
+      *(u16x8*)(X + plane_at<PLANES>(b * mp + i0 + r, np, j0 + 8 * u) + 32 * q) = row;
+      *(u16x8*)(XT + plane_at<EXACT ? 2 : PLANES>(b * np + j0 + r, mp, i0 + 8 * u) + 32 * q) = col;
     }
+    if constexpr (EXACT && PLANES == 1) *(u16x8*)(XT + plane_at<2>(b * np + j0 + r, mp, i0 + 8 * u) + 32) = u16x8{0, 0, 0, 0, 0, 0, 0, 0};
   }
 }
 
 // D = alpha P Q^T + beta E + diag I (with `scales`, alpha times the matrix's
-// own), K contiguous in P and Q.  A row of a matrix of two planes is its
-// first plane's values and behind them the second's.  One or two products of
-// the same P in one launch.
+// own), K contiguous in P and Q.  One or two products of the same P in one
+// launch.  The kernels' MODE: P and Q of one plane; pairs, P0 Q0 + P1 Q0 +
+// P0 Q1; or pairs with P1 = 0.  OP: planes of E and of the result.
+constexpr int kPlain = 0, kPairs = 1, kPlainByPair = 2;
 struct OrthoGemm {
-  const uint16_t* P;             // (m, PP k)
-  const uint16_t* Q[2];          // (n, PQ k)
-  const uint16_t* E;             // (m, OP n), or NULL
-  uint16_t* O[2];                // (m, OP n); sym: its transpose as well
-  uint16_t* OT;                  // (n, OP m), or NULL
+  const uint16_t* P;             // (m, k)
+  const uint16_t* Q[2];          // (n, k)
+  const uint16_t* E;             // (m, n), or NULL
+  uint16_t* O[2];                // (m, n); sym: its transpose as well
+  uint16_t* OT;                  // (n, m), or NULL
   int64_t P_bs, Q_bs, E_bs, O_bs;
   int32_t m, n, k;               // padded: multiples of 64
   float alpha[2], beta, diag;
@@ -212,10 +226,10 @@ __device__ __forceinline__ void ortho_value(const OrthoGemm& g, const OrthoTile&
 #pragma unroll
   for (int e = 0; e < W; ++e) v[e] *= o.alpha;
   if (g.E) {
-    const uint16_t* E = g.E + o.batch * g.E_bs + (int64_t)m * (OP * (int64_t)g.n) + n;
+    const uint16_t* E = g.E + o.batch * g.E_bs + plane_at<OP>(m, g.n, n);
 #pragma unroll
     for (int q = OP - 1; q >= 0; --q) {
-      const vec x = *(const vec*)(E + q * (int64_t)g.n);
+      const vec x = *(const vec*)(E + 32 * q);
 #pragma unroll
       for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(g.beta, to_f32<DT_F16>(x[e]), v[e]);
     }
@@ -224,9 +238,9 @@ __device__ __forceinline__ void ortho_value(const OrthoGemm& g, const OrthoTile&
   for (int e = 0; e < W; ++e) v[e] = as_computed(m == n + e ? v[e] + g.diag : v[e]);
 }
 
-// ... stored along a row: as planes with `rs` values a plane's row
+// ... stored along a row
 template <int OP, int W>
-__device__ __forceinline__ void ortho_store(uint16_t* row, int64_t plane, float (&v)[W]) {
+__device__ __forceinline__ void ortho_store(uint16_t* row, const float (&v)[W]) {
   typedef uint16_t vec __attribute__((ext_vector_type(W)));
   float r[W];
 #pragma unroll
@@ -239,7 +253,7 @@ __device__ __forceinline__ void ortho_store(uint16_t* row, int64_t plane, float 
       x[e] = from_f32<DT_F16>(r[e]);
       r[e] = as_computed(r[e] - to_f32<DT_F16>(x[e]));
     }
-    *(vec*)(row + q * plane) = x;
+    *(vec*)(row + 32 * q) = x;
   }
 }
 // ... to the result's type, `left` of them, `step` apart
@@ -267,7 +281,7 @@ template <int OP, int W>
 __device__ __forceinline__ void ortho_row(const OrthoGemm& g, const OrthoTile& o, bool columns, int32_t m, int32_t n, float (&v)[W]) {
   ortho_value<OP, W>(g, o, m, n, v);
   if (!g.d)
-    ortho_store<OP, W>((o.product ? g.O[1] : g.O[0]) + o.batch * g.O_bs + (int64_t)m * (OP * (int64_t)g.n) + n, g.n, v);
+    ortho_store<OP, W>((o.product ? g.O[1] : g.O[0]) + o.batch * g.O_bs + plane_at<OP>(m, g.n, n), v);
   else if (!columns && m < g.rows)
     ortho_result<W>(g, (uint16_t*)g.d + o.batch * g.d_bs + m * g.d_rs + n * g.d_cs, g.d_cs, g.cols - n, v);
 }
@@ -275,22 +289,10 @@ __device__ __forceinline__ void ortho_row(const OrthoGemm& g, const OrthoTile& o
 template <int OP, int W>
 __device__ __forceinline__ void ortho_column(const OrthoGemm& g, const OrthoTile& o, int32_t m, int32_t n, float (&v)[W]) {
   if (!g.d)
-    ortho_store<OP, W>((g.OT ? g.OT : o.product ? g.O[1] : g.O[0]) + o.batch * g.O_bs + (int64_t)n * (OP * (int64_t)g.m) + m, g.m, v);
+    ortho_store<OP, W>((g.OT ? g.OT : o.product ? g.O[1] : g.O[0]) + o.batch * g.O_bs + plane_at<OP>(n, g.m, m), v);
   else if (n < g.cols)
     ortho_result<W>(g, (uint16_t*)g.d + o.batch * g.d_bs + m + n * g.d_cs, 1, g.rows - m, v);
 }
-
-// The K-tiles: P0 Q0, then P1 Q0, then P0 Q1, T1 of 64 each.
-template <int PP, int PQ>
-struct OrthoPasses {
-  static constexpr int N = PP + PQ - 1;
-  static __device__ __forceinline__ int32_t of_p(int32_t t, int32_t T1) {
-    return t < PP * T1 ? t : t - PP * T1;
-  }
-  static __device__ __forceinline__ int32_t of_q(int32_t t, int32_t T1) {
-    return PP == 2 && t >= T1 ? t - T1 : t;
-  }
-};
 
 // An MFMA whose accumulator stays in AGPRs.  The statement is opaque to the
 // compiler: results are read only after agprs_settled.
@@ -318,12 +320,11 @@ __device__ __forceinline__ void agprs_settled(floatx4 (&acc)[FM][FN]) {
 // Outputs too small for 256 x 256 tiles to fill the chip: BM x BN tiles, KG
 // groups of four waves that take the K-tiles in turn (their sums meet in
 // LDS), each with a ring of four K-tiles in LDS, so that a copy has two
-// K-tiles of compute to land.  A slice's fragments are read while the slice
-// before it computes, across the one barrier of a K-tile too.
+// K-tiles of compute to land.  Fragments are read while the products before
+// theirs run, across the one barrier of a K-tile too.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int KG, int PP, int PQ, int OP>
+template <int BM, int BN, int KG, int MODE, int OP>
 __global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGemm g) {
-  typedef OrthoPasses<PP, PQ> Pass;
   constexpr int STAGES = 4;
   constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
   constexpr int ABYTES = BM * kRowBytes, BBYTES = BN * kRowBytes, STAGE = ABYTES + BBYTES;
@@ -342,9 +343,9 @@ __global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGem
   const int32_t m0 = o.tm * BM, n0 = o.tn * BN;
   if (m0 >= g.m || n0 >= g.n) return;  // a part of a tile at the edge
   const int32_t rows_a = g.m - m0 < BM ? g.m - m0 : BM, rows_b = g.n - n0 < BN ? g.n - n0 : BN;
-  const int64_t pk = (int64_t)PP * g.k, qk = (int64_t)PQ * g.k;
-  LoaderKVec<BM, 256, 0, 2> la(g.P + o.batch * g.P_bs + m0 * pk, rows_a, pk, 1, pk, wave, lane);
-  LoaderKVec<BN, 256, 0, 2> lb((o.product ? g.Q[1] : g.Q[0]) + o.batch * g.Q_bs + n0 * qk, rows_b, qk, 1, qk, wave, lane);
+  const int64_t row = MODE == kPlain ? g.k : 2 * (int64_t)g.k;
+  LoaderKVec<BM, 256, 0, 2> la(g.P + o.batch * g.P_bs + m0 * row, rows_a, row, 1, row, wave, lane);
+  LoaderKVec<BN, 256, 0, 2> lb((o.product ? g.Q[1] : g.Q[0]) + o.batch * g.Q_bs + n0 * row, rows_b, row, 1, row, wave, lane);
   constexpr int LOADS = decltype(la)::ITERS + decltype(lb)::ITERS;
   const int32_t a_row0 = (wave & 1) * TM, b_row0 = (wave >> 1) * TN;
   char* ring = smem + group * (STAGES * STAGE);
@@ -354,57 +355,72 @@ __global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGem
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-  const int32_t T1 = g.k / 64, T = Pass::N * T1, rounds = (T + KG - 1) / KG;
+  const int32_t T = (int32_t)(row / 64), rounds = (T + KG - 1) / KG;
   constexpr int32_t kPast = 1 << 24;  // a K-tile past every K: zeros
   auto issue = [&](int32_t i) {
     const int32_t t = i * KG + group;
     char* at = ring + (i & (STAGES - 1)) * STAGE;
-    la.issue(t < T ? Pass::of_p(t, T1) : kPast, at);
-    lb.issue(t < T ? Pass::of_q(t, T1) : kPast, at + ABYTES);
+    la.issue(t < T ? t : kPast, at);
+    lb.issue(t < T ? t : kPast, at + ABYTES);
   };
-  half8 af[2][FM], bf[2][FN];
-  auto read = [&](int32_t i, int ks) {
+  // the two halves of a K-tile: 32 values each, or the planes of 32 values
+  struct Half {
+    half8 a[FM], b[FN];
+  };
+  auto read = [&](int32_t i, int half, Half& h) {
     const char* cur = ring + (i & (STAGES - 1)) * STAGE;
 #pragma unroll
-    for (int a = 0; a < FM; ++a) af[ks][a] = read_frag<LOAD_KVEC, BM, 0>(cur, lane, a_row0 + 16 * a, ks);
+    for (int a = 0; a < FM; ++a)
+      if (MODE != kPlainByPair || half == 0) h.a[a] = read_frag<LOAD_KVEC, BM, 0>(cur, lane, a_row0 + 16 * a, half);
 #pragma unroll
-    for (int b = 0; b < FN; ++b) bf[ks][b] = read_frag<LOAD_KVEC, BN, 0>(cur + ABYTES, lane, b_row0 + 16 * b, ks);
+    for (int b = 0; b < FN; ++b) h.b[b] = read_frag<LOAD_KVEC, BN, 0>(cur + ABYTES, lane, b_row0 + 16 * b, half);
   };
-  auto multiply = [&](int ks) {
+  auto multiply = [&](const half8(&x)[FM], const half8(&y)[FN]) {
 #pragma unroll
     for (int a = 0; a < FM; ++a)
 #pragma unroll
       for (int b = 0; b < FN; ++b) {
-        if constexpr (AGPR) mfma_agpr(acc[a][b], bf[ks][b], af[ks][a]);
-        else acc[a][b] = mfma16<DT_F16>(bf[ks][b], af[ks][a], acc[a][b]);
+        if constexpr (AGPR) mfma_agpr(acc[a][b], y[b], x[a]);
+        else acc[a][b] = mfma16<DT_F16>(y[b], x[a], acc[a][b]);
       }
   };
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) issue(i);
   wait_vmem_n<(STAGES - 2) * LOADS>();
   phase_barrier();
-  read(0, 0);
-  int32_t i = 0;
-#pragma clang loop unroll(disable)
-  do {
+  Half first, second, other;
+  read(0, 0, first);
+  // K-tile i, its first half in `x`; the next one's goes to `y`
+  auto tile = [&](int32_t i, Half& x, Half& y) {
     wait_vmem_n<(STAGES - 3) * LOADS>();  // K-tile i + 1 has landed
     phase_barrier();                      // for every wave, and K-tile i - 1 is no longer read
     issue(i + STAGES - 1);
-    read(i, 1);
+    read(i, 1, second);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(0);
+    multiply(x.a, x.b);
     __builtin_amdgcn_sched_barrier(0);
-    read(i + 1, 0);
+    read(i + 1, 0, y);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(1);
+    if constexpr (MODE == kPlain) multiply(second.a, second.b);
+    if constexpr (MODE == kPairs) multiply(second.a, x.b);
+    if constexpr (MODE != kPlain) multiply(x.a, second.b);
     __builtin_amdgcn_sched_barrier(0);
-  } while (++i < rounds);
+  };
+  int32_t i = 0;
+#pragma clang loop unroll(disable)
+  do {
+    tile(i, first, other);
+    // (with one group the sum over an odd number of K-tiles ends on a K-tile
+    // of zeros)
+    tile(i + 1, other, first);
+    i += 2;
+  } while (i < rounds);
   wait_vmem();
   if constexpr (AGPR) agprs_settled(acc);
   __syncthreads();
 
   // the groups' sums, one after the other, into the finished tile
-  float* tile = (float*)smem;
+  float* done = (float*)smem;
 #pragma unroll
   for (int k = KG - 1; k >= 0; --k) {
     if (group == k) {
@@ -412,7 +428,7 @@ __global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGem
       for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-          float* to = tile + (a_row0 + 16 * i + (lane & 15)) * PITCH + b_row0 + 16 * j + 4 * (lane >> 4);
+          float* to = done + (a_row0 + 16 * i + (lane & 15)) * PITCH + b_row0 + 16 * j + 4 * (lane >> 4);
 #pragma unroll
           for (int r = 0; r < 4; ++r) to[r] = k < KG - 1 ? to[r] + acc[i][j][r] : acc[i][j][r];
         }
@@ -424,7 +440,7 @@ __global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGem
 #pragma unroll
   for (int q = 0; q < PIECES; ++q) {
     const int32_t t = threadIdx.x + 256 * KG * q, ml = t / (BN / 8), nl = 8 * (t % (BN / 8));
-    float* at = tile + ml * PITCH + nl;
+    float* at = done + ml * PITCH + nl;
     if (m0 + ml >= g.m || n0 + nl >= g.n) continue;
     float v[8];
 #pragma unroll
@@ -443,7 +459,7 @@ __global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGem
     if (m0 + ml >= g.m || n0 + nl >= g.n) continue;
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = tile[(ml + e) * PITCH + nl];
+    for (int e = 0; e < 8; ++e) v[e] = done[(ml + e) * PITCH + nl];
     ortho_column<OP, 8>(g, o, m0 + ml, n0 + nl, v);
   }
 }
@@ -453,12 +469,12 @@ __global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGem
 // accumulators in AGPRs, and a ring of five operand K-tiles in LDS, on the
 // schedule of gemm_f16_w4r_kernel (gemm_f16.hip), which see: operand tile q
 // (P's K-tile q / 2 for even q, Q's for odd q) in slot q % 5; per K-tile the
-// reads of slice 0 beside the second half of the last slice, slice 0 beside
-// the reads of slice 1, half of slice 1, one barrier.
+// reads of its first half beside the last products of the K-tile before, the
+// first half's products beside the reads of the second, all but the last of
+// the second half's, one barrier.
 // ---------------------------------------------------------------------------
-template <int PP, int PQ, int OP>
+template <int MODE, int OP>
 __global__ __launch_bounds__(256, 1) void ortho_ring_kernel(const OrthoGemm g) {
-  typedef OrthoPasses<PP, PQ> Pass;
   constexpr int F = 8, SLOT = 256 * kRowBytes, LOADS = 8;
   __shared__ __attribute__((aligned(1024))) char smem[5 * SLOT];
   const int32_t lane = threadIdx.x & 63;
@@ -466,22 +482,22 @@ __global__ __launch_bounds__(256, 1) void ortho_ring_kernel(const OrthoGemm g) {
   const OrthoTile o = ortho_tile(g);
   const int32_t m0 = o.tm * 256, n0 = o.tn * 256;
   const int32_t rows_a = g.m - m0 < 256 ? g.m - m0 : 256, rows_b = g.n - n0 < 256 ? g.n - n0 : 256;
-  const int64_t pk = (int64_t)PP * g.k, qk = (int64_t)PQ * g.k;
-  LoaderKVec<256, 256, 0, 2> la(g.P + o.batch * g.P_bs + m0 * pk, rows_a, pk, 1, pk, wave, lane);
-  LoaderKVec<256, 256, 0, 2> lb((o.product ? g.Q[1] : g.Q[0]) + o.batch * g.Q_bs + n0 * qk, rows_b, qk, 1, qk, wave, lane);
+  const int64_t row = MODE == kPlain ? g.k : 2 * (int64_t)g.k;
+  LoaderKVec<256, 256, 0, 2> la(g.P + o.batch * g.P_bs + m0 * row, rows_a, row, 1, row, wave, lane);
+  LoaderKVec<256, 256, 0, 2> lb((o.product ? g.Q[1] : g.Q[0]) + o.batch * g.Q_bs + n0 * row, rows_b, row, 1, row, wave, lane);
   floatx4 acc[F][F];
 #pragma unroll
   for (int i = 0; i < F; ++i)
 #pragma unroll
     for (int j = 0; j < F; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
   const int32_t a_row0 = (wave & 1) * 128, b_row0 = (wave >> 1) * 128;
-  const int32_t T1 = g.k / 64, T = Pass::N * T1;
+  const int32_t T = (int32_t)(row / 64);
   __builtin_assume(T >= 1);
   // past the last K-tile the look-ahead copies repeat it and are not read
   auto kt = [&](int32_t u) { return u < T ? u : T - 1; };
   auto slot = [&](int32_t q) { return smem + q * SLOT; };
-  auto copy_a = [&](int32_t u, char* dst, int j) { la.issue_full(Pass::of_p(kt(u), T1), dst, j); };
-  auto copy_b = [&](int32_t u, char* dst, int j) { lb.issue_full(Pass::of_q(kt(u), T1), dst, j); };
+  auto copy_a = [&](int32_t u, char* dst, int j) { la.issue_full(kt(u), dst, j); };
+  auto copy_b = [&](int32_t u, char* dst, int j) { lb.issue_full(kt(u), dst, j); };
   half8 fa0[F], fb0[F], fa1[F], fb1[F];
   typedef __attribute__((address_space(3))) const half8 lds_h8;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)smem;
@@ -519,7 +535,13 @@ __global__ __launch_bounds__(256, 1) void ortho_ring_kernel(const OrthoGemm g) {
   for (int j = 0; j < LOADS; ++j) copy_a(1, slot(2), j);
   // the first tile's first part computes with zero fragments (adds nothing)
 #pragma unroll
-  for (int i = 0; i < F; ++i) fa1[i] = half8{}, fb1[i] = half8{};
+  for (int i = 0; i < F; ++i) fa0[i] = fa1[i] = half8{}, fb1[i] = half8{};
+  // rows i0 .. i0 + 3 of the block, products of the first (0) or second half,
+  // or across them (pairs), step q of 16
+  auto products = [&](int i0, int q, const half8(&fa)[F], const half8(&fb)[F]) {
+#pragma unroll
+    for (int e = 2 * q; e < 2 * q + 2; ++e) mfma_agpr(acc[i0 + e / F][e % F], fb[e % F], fa[i0 + e / F]);
+  };
   wait_vmem_n<LOADS>();
   phase_barrier();
   int32_t sa = 0;  // slot of P's K-tile t; Q's in the next one
@@ -530,26 +552,54 @@ __global__ __launch_bounds__(256, 1) void ortho_ring_kernel(const OrthoGemm g) {
 #pragma clang loop unroll(disable)
   do {
     const int32_t s3 = sa + 3 >= 5 ? sa - 2 : sa + 3, s4 = sa == 0 ? 4 : sa - 1;
+    if constexpr (MODE == kPlain) {
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      read(q, 0, fa0, fb0);
-      if (!(q & 1)) copy_b(t + 1, slot(s3), q >> 1);
+      for (int q = 0; q < 16; ++q) {
+        read(q, 0, fa0, fb0);
+        if (!(q & 1)) copy_b(t + 1, slot(s3), q >> 1);
+        products(F / 2, q, fa1, fb1);  // K-tile t - 1's
+        __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
-      for (int e = 2 * q; e < 2 * q + 2; ++e) mfma_agpr(acc[F / 2 + e / F][e % F], fb1[e % F], fa1[F / 2 + e / F]);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int q = 0; q < 16; ++q) {
+        read(q, 1, fa1, fb1);
+        if (q & 1) copy_a(t + 2, slot(s4), q >> 1);
+        products(q < 8 ? 0 : F / 2, 2 * (q & 7), fa0, fb0);
+        products(q < 8 ? 0 : F / 2, 2 * (q & 7) + 1, fa0, fb0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int q = 0; q < 16; ++q) products(0, q, fa1, fb1);
+    } else {
+      // P0 of K-tile t - 1 times its Q1, rows 4 to 7, is what is left of it:
+      // Q0 and the first rows of P0 are free
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        if (q < 12) read(q, 0, fa0, fb0);
+        if (!(q & 1)) copy_b(t + 1, slot(s3), q >> 1);
+        products(F / 2, q, fa0, fb1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        if (q < 4) read(12 + q, 0, fa0, fb0);
+        if (q & 1) copy_a(t + 2, slot(s4), q >> 1);
+        products(0, q, fa0, fb0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        if (MODE == kPairs || q < F) read(q, 1, fa1, fb1);
+        products(F / 2, q, fa0, fb0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (MODE == kPairs) {
+#pragma unroll
+        for (int q = 0; q < 32; ++q) products(q < 16 ? 0 : F / 2, q & 15, fa1, fb0);
+      }
+#pragma unroll
+      for (int q = 0; q < 16; ++q) products(0, q, fa0, fb1);
     }
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      read(q, 1, fa1, fb1);
-      if (q & 1) copy_a(t + 2, slot(s4), q >> 1);
-#pragma unroll
-      for (int e = 4 * q; e < 4 * q + 4; ++e) mfma_agpr(acc[e / F][e % F], fb0[e % F], fa0[e / F]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int i = 0; i < F / 2; ++i)
-#pragma unroll
-      for (int j = 0; j < F; ++j) mfma_agpr(acc[i][j], fb1[j], fa1[i]);
     const int32_t na = sa + 2 >= 5 ? sa - 3 : sa + 2;
     bases(na, na == 4 ? 0 : na + 1);
     wait_vmem_n<LOADS>();  // in flight after this: P's K-tile t + 2
@@ -557,9 +607,10 @@ __global__ __launch_bounds__(256, 1) void ortho_ring_kernel(const OrthoGemm g) {
     sa = na;
   } while (++t < T);
 #pragma unroll
-  for (int i = F / 2; i < F; ++i)
-#pragma unroll
-    for (int j = 0; j < F; ++j) mfma_agpr(acc[i][j], fb1[j], fa1[i]);
+  for (int q = 0; q < 16; ++q) {
+    if constexpr (MODE == kPlain) products(F / 2, q, fa1, fb1);
+    else products(F / 2, q, fa0, fb1);
+  }
   wait_vmem();
   agprs_settled(acc);
   // every wave's copies have landed and its reads of the ring are done
@@ -605,33 +656,33 @@ int64_t ortho_tiles(const OrthoGemm& g, int64_t side) {
   return (g.sym ? tn * (tn + 1) / 2 : tm * tn) * g.batch * g.products;
 }
 
-template <int PP, int PQ, int OP>
+template <int MODE, int OP>
 void launch_tiles(OrthoGemm g, int32_t side, int64_t first, int64_t count, hipStream_t s) {
   const dim3 grid((uint32_t)(count * g.parts * g.parts));
   g.first = (int32_t)first;
   g.tiles_m = (g.m + side * g.parts - 1) / (side * g.parts), g.tiles_n = (g.n + side * g.parts - 1) / (side * g.parts);
   if (side == 256)
-    hipLaunchKernelGGL((ortho_ring_kernel<PP, PQ, OP>), grid, dim3(256), 0, s, g);
+    hipLaunchKernelGGL((ortho_ring_kernel<MODE, OP>), grid, dim3(256), 0, s, g);
   else if (side == 128)
-    hipLaunchKernelGGL((ortho_gemm_kernel<128, 128, 1, PP, PQ, OP>), grid, dim3(256), 0, s, g);
+    hipLaunchKernelGGL((ortho_gemm_kernel<128, 128, 1, MODE, OP>), grid, dim3(256), 0, s, g);
   else
-    hipLaunchKernelGGL((ortho_gemm_kernel<64, 64, 2, PP, PQ, OP>), grid, dim3(512), 0, s, g);
+    hipLaunchKernelGGL((ortho_gemm_kernel<64, 64, 2, MODE, OP>), grid, dim3(512), 0, s, g);
 }
 
 // The tile: the largest whose workgroups still fill the 256 CUs.  What a last
 // round of 256 x 256 tiles would leave most CUs without goes to 64 x 64
 // tiles: a symmetric 8192 x 8192 result has 528 tiles, and a third round for
 // 16 of them took 180 of 596 us.
-template <int PP, int PQ, int OP>
+template <int MODE, int OP>
 hipError_t run_gemm(OrthoGemm g, hipStream_t s) {
   const int32_t side = ortho_tiles(g, 256) >= 200 ? 256 : ortho_tiles(g, 128) >= 160 ? 128 : 64;
   const int64_t all = ortho_tiles(g, side), rest = all % 256;
   const int64_t whole = side == 256 && all > 256 && rest <= 64 ? all - rest : all;
   g.parts = 1;
-  launch_tiles<PP, PQ, OP>(g, side, 0, whole, s);
+  launch_tiles<MODE, OP>(g, side, 0, whole, s);
   if (whole < all) {
     g.parts = 4;
-    launch_tiles<PP, PQ, OP>(g, 64, whole, all - whole, s);
+    launch_tiles<MODE, OP>(g, 64, whole, all - whole, s);
   }
   return hipGetLastError();
 }
@@ -700,8 +751,9 @@ Places places(const OrthoParams& p, Way way) {
   q.scales = up((size_t)p.batch * kNormParts * 8);
   q.x = q.scales + up((size_t)p.batch * sizeof(OrthoScales));
   q.xt[0] = q.x + mn;
-  q.xt[1] = way == kGram ? q.xt[0] : q.xt[0] + mn;
-  size_t at = q.xt[1] + mn;
+  const size_t xt = way == kGram ? mn / xp * 2 : mn;  // the Gram way's is a pair
+  q.xt[1] = way == kGram ? q.xt[0] : q.xt[0] + xt;
+  size_t at = q.xt[1] + xt;
   for (int i = 0; i < 5; ++i) {
     q.mm[i] = at;
     if (way == kGram || i < 2) at += mm;
@@ -733,11 +785,11 @@ hipError_t direct(const OrthoParams& p, hipStream_t s) {
     g.P = g.Q[0] = X, g.P_bs = g.Q_bs = mn;
     g.m = g.n = mp, g.k = np, g.alpha[0] = kDown, g.sym = 1;
     g.O[0] = G, g.O_bs = mm;
-    if ((e = run_gemm<PL, PL, PL>(g, s)) != hipSuccess) break;
+    if ((e = run_gemm<PL == 2 ? kPairs : kPlain, PL>(g, s)) != hipSuccess) break;
     g.P = g.Q[0] = g.E = G, g.P_bs = g.Q_bs = g.E_bs = mm;
     g.k = mp, g.alpha[0] = c * kDown, g.beta = b;
     g.O[0] = B;
-    if ((e = run_gemm<PL, PL, PL>(g, s)) != hipSuccess) break;
+    if ((e = run_gemm<PL == 2 ? kPairs : kPlain, PL>(g, s)) != hipSuccess) break;
     g.P = B, g.Q[0] = XT[k & 1], g.E = X, g.Q_bs = g.E_bs = mn;
     g.n = np, g.alpha[0] = kDown, g.beta = a, g.sym = 0;
     g.O[0] = X, g.OT = XT[(k + 1) & 1], g.O_bs = mn;
@@ -745,7 +797,7 @@ hipError_t direct(const OrthoParams& p, hipStream_t s) {
       g.alpha[0] *= kDown, g.beta *= kDown;
       to_result(p, &g);
     }
-    e = run_gemm<PL, PL, PL>(g, s);
+    e = run_gemm<PL == 2 ? kPairs : kPlain, PL>(g, s);
   }
   return e;
 }
@@ -769,7 +821,7 @@ hipError_t gram(const OrthoParams& p, hipStream_t s) {
   g.P = g.Q[0] = X, g.P_bs = g.Q_bs = mn;
   g.m = g.n = mp, g.k = np, g.alpha[0] = 1.f, g.scales = scales;
   g.O[0] = G, g.O_bs = mm;
-  if ((e = run_gemm<PX, PX, 2>(g, s)) != hipSuccess) return e;
+  if ((e = run_gemm<PX == 2 ? kPairs : kPlain, 2>(g, s)) != hipSuccess) return e;
   g.scales = nullptr, g.P_bs = g.Q_bs = g.E_bs = mm, g.k = mp;
   for (int32_t k = 0; k < p.steps; ++k) {
     const float a = p.coefficients[3 * k], b = p.coefficients[3 * k + 1], c = p.coefficients[3 * k + 2];
@@ -778,7 +830,7 @@ hipError_t gram(const OrthoParams& p, hipStream_t s) {
     uint16_t* Pk = k == 0 ? M[3] : P;
     g.P = g.Q[0] = g.E = G, g.alpha[0] = c * (kP / (kG * kG)), g.beta = b * (kP / kG), g.diag = a * kP;
     g.O[0] = Pk;
-    if ((e = run_gemm<2, 2, 2>(g, s)) != hipSuccess) return e;
+    if ((e = run_gemm<kPairs, 2>(g, s)) != hipSuccess) return e;
     g.E = nullptr, g.diag = 0.f;
     uint16_t* next = Q == M[3] ? M[4] : M[3];
     g.P = Pk;
@@ -786,17 +838,21 @@ hipError_t gram(const OrthoParams& p, hipStream_t s) {
     int i = 0;
     if (!last) g.Q[i] = G, g.O[i] = H, g.alpha[i] = 1.f / kG, ++i;
     if (k > 0) g.Q[i] = Q, g.O[i] = next, g.alpha[i] = 1.f / kP;
-    if (g.products > 0 && (e = run_gemm<2, 2, 2>(g, s)) != hipSuccess) return e;
+    if (g.products > 0 && (e = run_gemm<kPairs, 2>(g, s)) != hipSuccess) return e;
     g.products = 1;
     Q = k > 0 ? next : M[3];
     if (last) break;
     g.P = H, g.Q[0] = Pk, g.O[0] = G, g.alpha[0] = kG / (kP * kP);
-    if ((e = run_gemm<2, 2, 2>(g, s)) != hipSuccess) return e;
+    if ((e = run_gemm<kPairs, 2>(g, s)) != hipSuccess) return e;
   }
-  g.P = Q, g.Q[0] = XT, g.Q_bs = mn, g.n = np, g.sym = 0, g.alpha[0] = 1.f;
+  // d's transpose: x^T Q, Q being symmetric, so that the pair is the second
+  // operand
+  g.P = XT, g.P_bs = 2 * (int64_t)mp * np, g.Q[0] = Q, g.Q_bs = mm;
+  g.m = np, g.sym = 0, g.alpha[0] = 1.f;
   g.scales = scales, g.scale_apply = 1;
   to_result(p, &g);
-  return run_gemm<2, PX, 1>(g, s);
+  std::swap(g.rows, g.cols), std::swap(g.d_rs, g.d_cs);
+  return run_gemm<PX == 2 ? kPairs : kPlainByPair, 1>(g, s);
 }
 
 }  // namespace

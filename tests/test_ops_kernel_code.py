@@ -9,9 +9,10 @@ from test_kernel_code import code_objects  # noqa: F401
 
 # symbol, MFMAs of one K-loop iteration, MFMAs after the loop
 NAMES = {}
-for pp, pq, op in ((1, 1, 1), (1, 1, 2), (2, 2, 1), (2, 2, 2), (2, 1, 1)):
-    NAMES[f"ortho_ring_{pp}{pq}{op}"] = (f"_ZN2sl12_GLOBAL__N_117ortho_ring_kernelILi{pp}ELi{pq}ELi{op}EEEvNS0_9OrthoGemmE", 128, 32)
-    NAMES[f"ortho_128_{pp}{pq}{op}"] = (f"_ZN2sl12_GLOBAL__N_117ortho_gemm_kernelILi128ELi128ELi1ELi{pp}ELi{pq}ELi{op}EEEvNS0_9OrthoGemmE", 32, 0)
+for mode, op, loop in ((0, 1, 128), (0, 2, 128), (1, 1, 192), (1, 2, 192), (2, 1, 128)):
+    NAMES[f"ortho_ring_{mode}{op}"] = (f"_ZN2sl12_GLOBAL__N_117ortho_ring_kernelILi{mode}ELi{op}EEEvNS0_9OrthoGemmE", loop, 32)
+    NAMES[f"ortho_128_{mode}{op}"] = (f"_ZN2sl12_GLOBAL__N_117ortho_gemm_kernelILi128ELi128ELi1ELi{mode}ELi{op}EEEvNS0_9OrthoGemmE",
+                                      {0: 64, 1: 96, 2: 64}[mode], 0)
 K.KERNELS.update(NAMES)
 
 
