@@ -30,7 +30,7 @@
 namespace sl {
 namespace {
 
-constexpr int32_t kNormParts = 256;               // partial sums of squares of one matrix
+constexpr int32_t kNormParts = 256;               // most partial sums of squares of one matrix
 constexpr int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 
 constexpr int kNormWaves = 16;
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(64 * kNormWaves) void ortho_norm_kernel(const Ortho
   double s = 0;
   for (int64_t c = 8 * u; c < length; c += 8 * across) {
 #pragma unroll 4
-    for (int64_t r = blockIdx.x * at_once + w; r < lines; r += kNormParts * at_once) {
+    for (int64_t r = blockIdx.x * at_once + w; r < lines; r += gridDim.x * at_once) {
       float v[8];
       ortho_load8<T>(p, b, along_rows ? c : r, along_rows ? r : c, p.n, along_rows, v);
 #pragma unroll
@@ -91,14 +91,15 @@ struct OrthoScales {
 // (|x| + 1e-7), rounded.  With two planes also what the rounding left.
 template <int T, int PLANES, bool EXACT>
 __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, const double* parts, uint16_t* X,
-                                                          uint16_t* XT, OrthoScales* scales, int32_t tiles_m, int32_t tiles_n) {
+                                                          uint16_t* XT, OrthoScales* scales, int32_t tiles_m, int32_t tiles_n,
+                                                          int32_t sums) {
   __shared__ double lds[4];
   __shared__ uint16_t tile[PLANES][64][66];
   const uint32_t id = blockIdx.x;
   const int32_t tn = id % tiles_n, tm = id / tiles_n % tiles_m;
   const int64_t b = id / tiles_n / tiles_m;
   const int64_t mp = 64 * (int64_t)tiles_m, np = 64 * (int64_t)tiles_n;
-  const double sum = block_sum(parts[b * kNormParts + threadIdx.x], lds);
+  const double sum = block_sum((int32_t)threadIdx.x < sums ? parts[b * kNormParts + threadIdx.x] : 0.0, lds);
   const double norm = sqrt(sum), inv = 1.0 / (norm + 1e-7);
   double f = 1024.0 * inv;
   if constexpr (EXACT) {
@@ -219,20 +220,29 @@ __device__ __forceinline__ OrthoTile ortho_tile(const OrthoGemm& g) {
   return o;
 }
 
-// W consecutive values of D at (m, n ..) from the sums
-template <int OP, int W>
-__device__ __forceinline__ void ortho_value(const OrthoGemm& g, const OrthoTile& o, int32_t m, int32_t n, float (&v)[W]) {
+template <int W>
+struct Halves {
   typedef uint16_t vec __attribute__((ext_vector_type(W)));
+};
+// W consecutive values of E at (m, n ..)
+template <int OP, int W>
+__device__ __forceinline__ void ortho_load(const OrthoGemm& g, const OrthoTile& o, int32_t m, int32_t n,
+                                           typename Halves<W>::vec (&x)[OP]) {
+  const uint16_t* E = g.E + o.batch * g.E_bs + plane_at<OP>(m, g.n, n);
+#pragma unroll
+  for (int q = 0; q < OP; ++q) x[q] = *(const typename Halves<W>::vec*)(E + 32 * q);
+}
+// W consecutive values of D at (m, n ..) from the sums and E's
+template <int OP, int W>
+__device__ __forceinline__ void ortho_value(const OrthoGemm& g, const OrthoTile& o, int32_t m, int32_t n,
+                                            const typename Halves<W>::vec (&x)[OP], float (&v)[W]) {
 #pragma unroll
   for (int e = 0; e < W; ++e) v[e] *= o.alpha;
   if (g.E) {
-    const uint16_t* E = g.E + o.batch * g.E_bs + plane_at<OP>(m, g.n, n);
 #pragma unroll
-    for (int q = OP - 1; q >= 0; --q) {
-      const vec x = *(const vec*)(E + 32 * q);
+    for (int q = OP - 1; q >= 0; --q)
 #pragma unroll
-      for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(g.beta, to_f32<DT_F16>(x[e]), v[e]);
-    }
+      for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(g.beta, to_f32<DT_F16>(x[q][e]), v[e]);
   }
 #pragma unroll
   for (int e = 0; e < W; ++e) v[e] = as_computed(m == n + e ? v[e] + g.diag : v[e]);
@@ -278,8 +288,9 @@ __device__ __forceinline__ bool ortho_columns(const OrthoGemm& g, const OrthoTil
 }
 // W consecutive n of row m
 template <int OP, int W>
-__device__ __forceinline__ void ortho_row(const OrthoGemm& g, const OrthoTile& o, bool columns, int32_t m, int32_t n, float (&v)[W]) {
-  ortho_value<OP, W>(g, o, m, n, v);
+__device__ __forceinline__ void ortho_row(const OrthoGemm& g, const OrthoTile& o, bool columns, int32_t m, int32_t n,
+                                          const typename Halves<W>::vec (&x)[OP], float (&v)[W]) {
+  ortho_value<OP, W>(g, o, m, n, x, v);
   if (!g.d)
     ortho_store<OP, W>((o.product ? g.O[1] : g.O[0]) + o.batch * g.O_bs + plane_at<OP>(m, g.n, n), v);
   else if (!columns && m < g.rows)
@@ -328,7 +339,7 @@ __global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGem
   constexpr int STAGES = 4;
   constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
   constexpr int ABYTES = BM * kRowBytes, BBYTES = BN * kRowBytes, STAGE = ABYTES + BBYTES;
-  constexpr int PITCH = BN + 1;  // floats a row of the finished tile
+  constexpr int PITCH = BN + 4;  // floats a row of the finished tile
   // sixteen accumulators: left to it, the compiler moved them between
   // register files in every K-tile (and an accumulator comes up again only
   // after fifteen others)
@@ -419,6 +430,17 @@ __global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGem
   if constexpr (AGPR) agprs_settled(acc);
   __syncthreads();
 
+  // E's values, all requested before any is used
+  const bool columns = ortho_columns(g, o);
+  constexpr int PIECES = BM * BN / 8 / (256 * KG);
+  auto row_of = [](int q) { return (int32_t)(threadIdx.x + 256 * KG * q) / (BN / 8); };
+  auto col_of = [](int q) { return 8 * ((int32_t)(threadIdx.x + 256 * KG * q) % (BN / 8)); };
+  u16x8 ev[PIECES][OP];
+  if (g.E) {
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q)
+      if (m0 + row_of(q) < g.m && n0 + col_of(q) < g.n) ortho_load<OP, 8>(g, o, m0 + row_of(q), n0 + col_of(q), ev[q]);
+  }
   // the groups' sums, one after the other, into the finished tile
   float* done = (float*)smem;
 #pragma unroll
@@ -428,34 +450,29 @@ __global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGem
       for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-          float* to = done + (a_row0 + 16 * i + (lane & 15)) * PITCH + b_row0 + 16 * j + 4 * (lane >> 4);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) to[r] = k < KG - 1 ? to[r] + acc[i][j][r] : acc[i][j][r];
+          floatx4* to = (floatx4*)(done + (a_row0 + 16 * i + (lane & 15)) * PITCH + b_row0 + 16 * j + 4 * (lane >> 4));
+          *to = k < KG - 1 ? *to + acc[i][j] : acc[i][j];
         }
     }
     __syncthreads();
   }
-  const bool columns = ortho_columns(g, o);
-  constexpr int PIECES = BM * BN / 8 / (256 * KG);
 #pragma unroll
   for (int q = 0; q < PIECES; ++q) {
-    const int32_t t = threadIdx.x + 256 * KG * q, ml = t / (BN / 8), nl = 8 * (t % (BN / 8));
-    float* at = done + ml * PITCH + nl;
+    const int32_t ml = row_of(q), nl = col_of(q);
+    floatx4* at = (floatx4*)(done + ml * PITCH + nl);
     if (m0 + ml >= g.m || n0 + nl >= g.n) continue;
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = at[e];
-    ortho_row<OP, 8>(g, o, columns, m0 + ml, n0 + nl, v);
-    if (columns) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) at[e] = v[e];
-    }
+    const floatx4 lo = at[0], hi = at[1];
+    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    ortho_row<OP, 8>(g, o, columns, m0 + ml, n0 + nl, ev[q], v);
+    if (columns) at[0] = floatx4{v[0], v[1], v[2], v[3]}, at[1] = floatx4{v[4], v[5], v[6], v[7]};
   }
   if (!columns) return;
   __syncthreads();
+  // sixteen columns by four groups of 8 rows to a wave's reads: two lanes to a bank,
+  // and 64 bytes of every column stored together
 #pragma unroll
   for (int q = 0; q < PIECES; ++q) {
-    const int32_t t = threadIdx.x + 256 * KG * q, ml = 8 * (t % (BM / 8)), nl = t / (BM / 8);
+    const int32_t t = threadIdx.x + 256 * KG * q, ml = 8 * (t / 16 % (BM / 8)), nl = t % 16 + 16 * (t / (2 * BM));
     if (m0 + ml >= g.m || n0 + nl >= g.n) continue;
     float v[8];
 #pragma unroll
@@ -631,9 +648,11 @@ __global__ __launch_bounds__(256, 1) void ortho_ring_kernel(const OrthoGemm g) {
       const int32_t r = 2 * it + (lane >> 5), q = lane & 31;
       floatx4* at = (floatx4*)(region + rows_chunk(r, q));
       if (mb + r >= g.m || nb + 4 * q >= g.n) continue;
+      u16x4 e[OP];
+      if (g.E) ortho_load<OP, 4>(g, o, mb + r, nb + 4 * q, e);
       const floatx4 x = *at;
       float v[4] = {x[0], x[1], x[2], x[3]};
-      ortho_row<OP, 4>(g, o, columns, mb + r, nb + 4 * q, v);
+      ortho_row<OP, 4>(g, o, columns, mb + r, nb + 4 * q, e, v);
       if (columns) *at = floatx4{v[0], v[1], v[2], v[3]};
     }
     if (columns) {
@@ -694,16 +713,19 @@ hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts
   const int64_t length = p.x_rs == 1 && p.x_cs != 1 ? p.m : p.n;
   int32_t across = 64 * kNormWaves;
   while (across > 1 && 4 * (int64_t)across >= length) across /= 2;
-  hipLaunchKernelGGL(ortho_norm_kernel<T>, dim3(kNormParts, p.batch), dim3(64 * kNormWaves), 0, s, p, parts, across);
+  // 16384 values to a workgroup
+  const int64_t want = (p.m * p.n + 16383) / 16384;
+  const int32_t sums = (int32_t)(want < kNormParts ? want : kNormParts);
+  hipLaunchKernelGGL(ortho_norm_kernel<T>, dim3(sums, p.batch), dim3(64 * kNormWaves), 0, s, p, parts, across);
   const dim3 grid((uint32_t)((int64_t)p.batch * tm * tn)), block(256);
   if (exact && planes == 2)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 2, true>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 2, true>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn, sums);
   else if (exact)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 1, true>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 1, true>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn, sums);
   else if (planes == 2)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 2, false>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 2, false>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn, sums);
   else
-    hipLaunchKernelGGL((ortho_start_kernel<T, 1, false>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 1, false>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn, sums);
   return hipGetLastError();
 }
 hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, uint16_t* XT, OrthoScales* scales,
