@@ -46,13 +46,17 @@ static bool overlap(const View& x, const View& y, int64_t batch) {
   return xl < yh && yl < xh;
 }
 
-// The tile: up to 64 rows of A stream the weight once (the skinny kernel);
+// The tile: up to 64 rows of A stream the weight once (the skinny kernels),
+// and so do products of up to 64 tiles of 128 x 128, which would leave most
+// CUs without work (128 x 512 x 8192: 75 us in those tiles, 14 us in 64 x 16;
+// 512 x 2048 x 4096, 64 tiles: 41 and 23 us; 1024 x 2048 x 4096, 128 tiles: 43
+// both ways, and x 512: 12 and 20 us);
 // otherwise the tile with the least (workgroup rounds over the 256 CUs) x
 // (work of a tile), the 128 x 128 tile two to a CU and moving twice the
 // operand bytes per product.  fp32 results: 128 x 128 (the fp16 fragments of
 // the larger tile do not fit the registers: 4096 x 4096 x 8192 took 836 us).
 static int32_t choose_tile(int64_t batch, int64_t M, int64_t N, int32_t type) {
-  if (M <= kSkinnyRows) return BT_SKINNY;
+  if (M <= kSkinnyRows || batch * ceil_div(M, 128) * ceil_div(N, 128) <= 64) return BT_SKINNY;
   if (type == OT_F32) return BT_128x128;
   int32_t best = BT_256x256;
   double least = 1e300;

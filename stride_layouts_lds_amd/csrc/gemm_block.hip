@@ -139,9 +139,10 @@ __device__ __forceinline__ float from_lane(float v, int32_t l) {
 constexpr int SB_SQUARE = 0, SB_ROWS = 1;
 
 // BM x BN output tiles, the K-tiles of 128 bytes per row brought straight
-// into LDS two stages deep, as in the MXFP8 kernels.
-template <int BM, int BN, int WM, int WN, int SBK, int OT>
-__global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void gemm_block_kernel(const BlockGemmParams p) {
+// into LDS, STAGES deep: two, and two workgroups to a CU, or, where there is
+// not more than one for each, four.
+template <int BM, int BN, int WM, int WN, int STAGES, int SBK, int OT>
+__global__ __launch_bounds__(WM* WN * 64, STAGES == 2 ? 2 : 1) void gemm_block_kernel(const BlockGemmParams p) {
   typedef typename FragOf<OT>::type Frag;
   constexpr int NT = WM * WN * 64;
   constexpr int TM = BM / WM, TN = BN / WN;
@@ -149,7 +150,7 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void gemm_block_kernel(con
   static_assert(128 % TN == 0, "a wave's columns lie in one square block");
   constexpr int ABYTES = BM * kRowBytes, BBYTES = BN * kRowBytes;
   constexpr int STAGE = ABYTES + BBYTES;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  __shared__ __attribute__((aligned(1024))) char smem[STAGES * STAGE];
 
   const int32_t lane = threadIdx.x & 63;
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -173,35 +174,27 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void gemm_block_kernel(con
     for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
   const int32_t T = p.k_blocks;
-  float sa_next = 0.f, sb_next = 0.f;
-  if (T > 0) {
-    sa_next = *sa_p, sb_next = *sb_p;
-    la.issue(0, smem);
-    lb.issue(0, smem + ABYTES);
-    wait_vmem();
-    __syncthreads();
-  }
-  for (int32_t t = 0; t < T; ++t) {
-    char* cur = smem + (t & 1) * STAGE;
-    char* nxt = smem + ((t + 1) & 1) * STAGE;
-    const float sa_own = sa_next, sb_own = sb_next;
-    if (t + 1 < T) {
-      sa_p += p.sa_ks, sb_p += p.sb_ks;
-      sa_next = *sa_p, sb_next = *sb_p;
-    }
+  constexpr int LOADS = decltype(la)::ITERS + decltype(lb)::ITERS + 2;
+  float sa_own[STAGES], sb_own[STAGES];
+  auto request = [&](int32_t t, int d) {
+    const int64_t at = t < T ? t : T - 1;
+    sa_own[d] = sa_p[at * p.sa_ks], sb_own[d] = sb_p[at * p.sb_ks];
+    la.issue(t, smem + d * STAGE);  // past the last K-tile: zeros, not read
+    lb.issue(t, smem + d * STAGE + ABYTES);
+  };
+  auto multiply = [&](int d) {
+    const char* cur = smem + d * STAGE;
     float sa[FM], sb[SBK == SB_ROWS ? FN : 1][4];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) sa[i] = from_lane(sa_own, 16 * i + (lane & 15));
+    for (int i = 0; i < FM; ++i) sa[i] = from_lane(sa_own[d], 16 * i + (lane & 15));
     if constexpr (SBK == SB_ROWS) {
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sb[j][r] = from_lane(sb_own, 16 * j + 4 * (lane >> 4) + r);
+        for (int r = 0; r < 4; ++r) sb[j][r] = from_lane(sb_own[d], 16 * j + 4 * (lane >> 4) + r);
     } else {
-      sb[0][0] = sb_own;  // the wave's columns lie in one block
+      sb[0][0] = sb_own[d];  // the wave's columns lie in one block
     }
-    la.issue(t + 1, nxt);
-    lb.issue(t + 1, nxt + ABYTES);
     Frag bf[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j)
@@ -221,8 +214,20 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void gemm_block_kernel(con
         }
       }
     }
+  };
+  if (T > 0) {
+#pragma unroll
+    for (int d = 0; d < STAGES - 1; ++d) request(d, d);
+    for (int32_t t = 0; t < T; t += STAGES) {
+#pragma unroll
+      for (int d = 0; d < STAGES; ++d) {
+        wait_vmem_n<(STAGES - 2) * LOADS>();  // K-tile t + d has landed
+        phase_barrier();                      // for every wave, and the one before is no longer read
+        request(t + d + STAGES - 1, (d + STAGES - 1) % STAGES);
+        if (t + d < T) multiply(d);
+      }
+    }
     wait_vmem();
-    __syncthreads();
   }
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -606,9 +611,12 @@ hipError_t go(const BlockGemmParams& p, int32_t tile, hipStream_t s) {
     constexpr int OT2 = OT == OT_F32 ? OT_F16 : OT;  // fp32 results have no such tile
     if (square) hipLaunchKernelGGL((gemm_block_ring_kernel<SB_SQUARE, OT2>), grid, dim3(512), 0, s, p);
     else hipLaunchKernelGGL((gemm_block_ring_kernel<SB_ROWS, OT2>), grid, dim3(512), 0, s, p);
+  } else if (tile == BT_128x128 && grid.x > 256) {
+    if (square) hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, 2, SB_SQUARE, OT>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, 2, SB_ROWS, OT>), grid, dim3(256), 0, s, p);
   } else if (tile == BT_128x128) {
-    if (square) hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, SB_SQUARE, OT>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, SB_ROWS, OT>), grid, dim3(256), 0, s, p);
+    if (square) hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, 4, SB_SQUARE, OT>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((gemm_block_kernel<128, 128, 2, 2, 4, SB_ROWS, OT>), grid, dim3(256), 0, s, p);
   } else if (tile == BT_SKINNY) {
     const bool wide = skinny_cols(p.M, p.N, p.batch) == 32;
     auto skinny = [&](auto fm_c, auto fn_c, auto sb_c) {

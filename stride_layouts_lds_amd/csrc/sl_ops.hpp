@@ -68,7 +68,7 @@ constexpr int32_t BF_C_VEC = 4;   // ... of C
 enum BlockTile : int32_t {
   BT_256x256 = 0,  // 8 waves, each 128 x 64
   BT_128x128 = 1,  // 4 waves, each 64 x 64
-  BT_SKINNY = 2,   // up to 64 rows of A x 16 or 32 of B, the waves of a workgroup splitting K
+  BT_SKINNY = 2,   // 64 rows of A x 16 or 32 of B, the waves of a workgroup splitting K
 };
 struct BlockTileShape {
   int32_t bm, bn, wm, wn, stages;
