@@ -149,8 +149,8 @@ typedef struct {
                          LDS ring, scales in registers: scale rows of a
                          multiple of 16 blocks on 16-byte boundaries),
                          9 e4m3 with fp32 scales per 128 K (256x256 or
-                         128x128 tiles; up to 64 rows of A: tile_m 64, no
-                         LDS tiles, the waves of a workgroup split K) */
+                         128x128 tiles; few rows of A or few tiles: tile_m
+                         64, the waves of a workgroup split K) */
   int32_t a_load;     /* 0 K-contiguous vector, 1 M-contiguous vector (register
                          transpose), 2 generic, 3 M-contiguous direct copy into
                          an M-major LDS tile read by transposing reads, 4 NVFP4
@@ -269,10 +269,15 @@ sl_status sl_quantize(const sl_quantize_args* args, void* stream);
  *   steps         1 to 64
  *   coefficients  host array of a, b, c for each step, each within 16 in
  *                 magnitude; NULL: 3.4445, -4.7750, 2.0315 at every step
- * The matrices between products are fp16 times 2^10 (for f16 d pairs of fp16,
- * the value and what its rounding left) with sums in fp32, the sum of squares
- * is in 64 bits: an iterate may reach 32 in magnitude (the
- * default coefficients keep singular values below 1.3), beyond which d holds
+ * All products are on fp16 values times powers of two with sums in fp32, the
+ * sum of squares is in 64 bits (up to 128 rows: a matrix's trace in 64 bits
+ * over fp32 sums).  A matrix between products is a pair of fp16, a value and
+ * what its rounding left; for bf16 d with more than 128 and no more than four
+ * times as many columns as rows it is one fp16 (1.1e-3 to 1.8e-3 of the
+ * result, 2-norm; a bf16 result's own rounding is 1.7e-3).  Pairs: 5e-6 to
+ * 1.3e-4 on noise with a few strong directions, 4e-4 where singular values
+ * span five decades.  The singular values of every iterate are to stay below
+ * 2 (the default coefficients keep them below 1.3); beyond that d may hold
  * infinities or NaN.  An x that holds a NaN or an infinity gives a d of NaN; zero gives
  * zero.  Results do not vary from call to call.
  * workspace: device memory of sl_orthogonalize_workspace_bytes() bytes,

@@ -168,7 +168,10 @@ sl_status plan_block(const sl_gemm_args* args, BlockPlan* out) {
   P.pub.tile_m = ts.bm, P.pub.tile_n = ts.bn, P.pub.tile_k = kScaleBlock;
   P.pub.threads = P.tile == BT_SKINNY ? (M <= 16 ? kSkinnyWaves : kStreamWaves) * 64 : ts.wm * ts.wn * 64;
   P.pub.workgroups = total;
-  P.pub.lds_bytes = ts.stages * (ts.bm + ts.bn) * kScaleBlock;
+  if (P.tile == BT_256x256) P.pub.lds_bytes = 5 * 256 * kScaleBlock;
+  else if (P.tile == BT_128x128) P.pub.lds_bytes = (total > 256 ? 2 : 4) * 256 * kScaleBlock;
+  else if (M <= 16) P.pub.lds_bytes = (kSkinnyWaves - 1) * (ts.bn / 16) * 1024;
+  else P.pub.lds_bytes = kStreamWaves * (M <= 32 ? 4 : 3) * ((M <= 32 ? 32 : 64) + ts.bn) * kScaleBlock;
   return SL_OK;
 }
 

@@ -71,9 +71,9 @@ enum BlockTile : int32_t {
   BT_SKINNY = 2,   // 64 rows of A x 16 or 32 of B, the waves of a workgroup splitting K
 };
 struct BlockTileShape {
-  int32_t bm, bn, wm, wn, stages;
+  int32_t bm, bn, wm, wn;
 };
-constexpr BlockTileShape kBlockTiles[3] = {{256, 256, 2, 4, 2}, {128, 128, 2, 2, 2}, {64, 32, 1, 1, 0}};
+constexpr BlockTileShape kBlockTiles[3] = {{256, 256, 2, 4}, {128, 128, 2, 2}, {64, 32, 1, 1}};
 constexpr int32_t kSkinnyRows = 64;   // most rows of A of one skinny workgroup
 constexpr int32_t kSkinnyWaves = 8;    // up to 16 rows of A
 constexpr int32_t kStreamWaves = 4;    // 17 to 64
@@ -85,9 +85,8 @@ hipError_t launch_gemm_block(const BlockGemmParams& p, int32_t tile, hipStream_t
 
 // ---------------------------------------------------------------------------
 // The orthogonalised update.  x is taken with m <= n (a tall x by its
-// strides, transposed); every matrix of the iteration is fp16 (for fp16
-// results two such planes), scaled by 2^10, in the workspace, its sizes
-// padded with zeros to multiples of 64.
+// strides, transposed); the matrices of the iteration are one or two planes of
+// fp16 in the workspace, their sizes padded with zeros to multiples of 64.
 // ---------------------------------------------------------------------------
 struct OrthoParams {
   const void* x;               // (b, i, j), i < m, j < n
