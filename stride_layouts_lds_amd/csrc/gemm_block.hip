@@ -140,7 +140,9 @@ constexpr int SB_SQUARE = 0, SB_ROWS = 1;
 
 // BM x BN output tiles, the K-tiles of 128 bytes per row brought straight
 // into LDS, STAGES deep: two, and two workgroups to a CU, or, where there is
-// not more than one for each, four.
+// not more than one for each, four.  Measured: 4096 x 4096 x 8192 + C into
+// fp32 300 us (916 TFLOP/s; 360 vector instructions a K-tile beside 64
+// MFMAs), 1024 x 2048 x 4096 into bf16 31 us.
 template <int BM, int BN, int WM, int WN, int STAGES, int SBK, int OT>
 __global__ __launch_bounds__(WM* WN * 64, STAGES == 2 ? 2 : 1) void gemm_block_kernel(const BlockGemmParams p) {
   typedef typename FragOf<OT>::type Frag;
@@ -256,7 +258,8 @@ __global__ __launch_bounds__(WM* WN * 64, STAGES == 2 ? 2 : 1) void gemm_block_k
 // t + 1 has landed then, so the first fragments of t + 1 are read while t's
 // last products run, and the copies of t + 2 (A into the free slot, B into
 // B(t)'s, which is in registers) have a whole K-tile to land.  A block's sums
-// are scaled and added while the next ones run in the matrix core.
+// are scaled and added while the next ones run in the matrix core.  Measured:
+// 8192^3, bf16 D, square blocks of B: 527 us, 2.09 PFLOP/s (MXFP8: 403).
 template <int SBK, int OT>
 __global__ __launch_bounds__(512, 2) void gemm_block_ring_kernel(const BlockGemmParams p) {
   typedef FragF8 Frag;
@@ -510,8 +513,9 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_block_skinny_kernel(co
 
 // 17 to 64 rows of A: the same with the K blocks of a wave copied straight
 // into its own part of LDS, STAGES deep (in registers two blocks filled the
-// file: 48 x 8192 x 8192 took 26 us).  Four waves split K; no barrier until
-// their sums meet.
+// file: 48 x 8192 x 8192 took 26 us, here 23, 2.9 TB/s).  Four waves split K;
+// no barrier until their sums meet.  Also for more rows, 64 to a workgroup,
+// where 128 x 128 tiles would be few.
 template <int FM, int FN, int SBK, int OT>
 __global__ __launch_bounds__(kStreamWaves * 64, 1) void gemm_block_stream_kernel(const BlockGemmParams p) {
   typedef typename FragOf<OT>::type Frag;

@@ -20,8 +20,10 @@
 // values span five decades; with one plane it is 1e-2 and more.
 //
 // P's products commute, so G and Q stay symmetric and every operand is read
-// along its rows.  Bound by latency: at 96 x 128 a step is three products of
-// 96^3 and three barriers.
+// along its rows.  Bound by latency: a step is three dependent rounds of
+// products with two barriers each.  Measured at 96 x 128 (bf16, five steps):
+// gram 6, steps 27, apply 8 us; the steps take 0.9 us each at 32 rows, 2.5 at
+// 64, 5.2 at 96 and 10.5 at 128.
 #include "ortho_device.hpp"
 
 namespace sl {
