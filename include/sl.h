@@ -283,7 +283,11 @@ sl_status sl_quantize(const sl_quantize_args* args, void* stream);
  * workspace: device memory of sl_orthogonalize_workspace_bytes() bytes,
  * 16-byte aligned, apart from x and d, not used by anything else until the
  * call's kernels have finished on `stream`; its contents do not matter
- * before or after.  An empty x is a no-op and needs none.  Asynchronous on
+ * before or after.  An empty x is a no-op and needs none.  Sizes: fewer than
+ * 65536 matrices, and each (its sizes rounded up to multiples of 64) fewer
+ * than 2^29 values, but for up to 128 rows or columns and coefficients whose
+ * a's multiply to at most 512, where 2^30 tiles of 64 x 64 in all are the
+ * limit (else SL_ERR_SHAPE).  Asynchronous on
  * `stream`; errors as sl_gemm, SL_ERR_ARG for steps or coefficients.
  */
 typedef struct {

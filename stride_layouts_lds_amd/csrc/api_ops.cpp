@@ -274,6 +274,7 @@ sl_status sl_quantize(const sl_quantize_args* args, void* stream) {
 
 namespace {
 
+constexpr int64_t kOrthoMaxBatch = 65536;
 constexpr float kDefaultCoefficients[3] = {3.4445f, -4.7750f, 2.0315f};
 
 struct OrthoPlan {
@@ -314,11 +315,12 @@ sl_status plan_orthogonalize(const sl_orthogonalize_args* args, OrthoPlan* P) {
   p.m = tall ? X.cols : X.rows, p.n = tall ? X.rows : X.cols;
   p.x_bs = batch_stride(X), p.x_rs = tall ? X.cs : X.rs, p.x_cs = tall ? X.rs : X.cs;
   p.d_bs = batch_stride(D), p.d_rs = tall ? D.cs : D.rs, p.d_cs = tall ? D.rs : D.cs;
+  if (X.batch >= kOrthoMaxBatch) return fail(SL_ERR_SHAPE, "x has %lld matrices, fewer than %lld are taken", (long long)X.batch, (long long)kOrthoMaxBatch);
   p.batch = (int32_t)X.batch;
   p.steps = args->steps;
   p.x = args->x.data, p.d = args->d.data;
-  if (!sl::orthogonalize_grid_ok(X.batch, p.m, p.n)) return fail(SL_ERR_SHAPE, "x is too large");
   p.coefficients = P->coefficients;
+  if (!sl::orthogonalize_grid_ok(p)) return fail(SL_ERR_SHAPE, "x is too large");
   P->ws_bytes = sl::orthogonalize_workspace(p);
   return SL_OK;
 }

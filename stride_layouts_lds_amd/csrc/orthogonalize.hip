@@ -890,11 +890,11 @@ size_t orthogonalize_workspace(const OrthoParams& p) {
 }
 
 // every launch fits a grid, and a matrix's planes 32-bit offsets
-bool orthogonalize_grid_ok(int64_t batch, int64_t m, int64_t n) {
+bool orthogonalize_grid_ok(const OrthoParams& p) {
   const int64_t lim = (int64_t)1 << 31;
-  if (batch >= 65536 || m >= lim || n >= lim) return false;
-  if ((double)batch * (double)(pad64(m) / 64) * (double)(pad64(n) / 64) >= 0x1p30) return false;
-  return m <= kGramRows || (double)pad64(m) * (double)pad64(n) * 4 < 0x1p31;
+  if (p.batch >= 65536 || p.m >= lim || p.n >= lim) return false;
+  if ((double)p.batch * (double)(pad64(p.m) / 64) * (double)(pad64(p.n) / 64) >= 0x1p30) return false;
+  return way_of(p) == kSmallGram || (double)pad64(p.m) * (double)pad64(p.n) * 4 < 0x1p31;
 }
 
 hipError_t launch_orthogonalize(const OrthoParams& p, hipStream_t s) {

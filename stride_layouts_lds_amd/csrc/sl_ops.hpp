@@ -100,7 +100,7 @@ struct OrthoParams {
 };
 constexpr int32_t kOrthoMaxSteps = 64;
 size_t orthogonalize_workspace(const OrthoParams& p);
-bool orthogonalize_grid_ok(int64_t batch, int64_t m, int64_t n);
+bool orthogonalize_grid_ok(const OrthoParams& p);
 hipError_t launch_orthogonalize(const OrthoParams& p, hipStream_t stream);
 
 // Through the Gram matrix (ortho_gram.hip): up to kGramRows rows, and steps

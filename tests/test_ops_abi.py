@@ -153,6 +153,10 @@ NAN, INF = float("nan"), float("inf")
     (dict(ws=X), "SL_ERR_ALIAS"),
     (dict(ws=D), "SL_ERR_ALIAS"),
     (dict(x=rm(X, (70000, 4, 4), BF16), d=rm(D, (70000, 4, 4), BF16)), "SL_ERR_SHAPE"),
+    # more bytes than a product's 32-bit offsets reach: 20 default steps amplify
+    # too much for the Gram matrix, so this goes the direct way
+    (dict(x=rm(X, (128, 1 << 24), BF16), d=rm(D, (128, 1 << 24), BF16), steps=20), "SL_ERR_SHAPE"),
+    (dict(x=rm(X, (129, 1 << 23), BF16), d=rm(D, (129, 1 << 23), BF16)), "SL_ERR_SHAPE"),
 ])
 def test_orthogonalize_refuses(api, change, what):
     good = dict(x=rm(X, (96, 128), BF16), d=rm(D, (96, 128), BF16))
