@@ -540,3 +540,69 @@ def test_orthogonalize_in_a_graph(api):
             assert same_bytes(got, ref)
         assert torch.equal(y, api.gemm(wq[0], wq[0], sfa=wq[1], sfb=wq[1], block_k=128, dtype=torch.float32))
         torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# the tiles of large results
+# ---------------------------------------------------------------------------
+
+# 256 x 256 tiles (16-bit D) and 128 x 128 ones two to a CU; 128 x 128 tiles
+# four K-tiles deep
+@pytest.mark.parametrize("shape", [(2100, 4300, 16), (2100, 4300, 400), (4090, 2310, 2064), (1290, 1500, 128),
+                                   (1290, 1500, 1040), (1025, 1030, 656)])
+@pytest.mark.parametrize("out", OUTS)
+@pytest.mark.parametrize("rb", [1, 128])
+def test_product_large_tiles(api, shape, out, rb):
+    import torch
+    M, N, K = shape
+    dt = getattr(torch, out)
+    a, b = int_codes((M, K), 111, 2), int_codes((N, K), 112, 2)
+    sa, sb = scales((), M, K, 1, 113), scales((), N, K, rb, 114)
+    c = torch.randint(-8, 9, (M, N), generator=gen(115), device="cuda").to(dt)
+    want = product64(a, sa, 1, b, sb, rb, c)[0].float().to(dt)
+    d = torch.zeros((M, N), dtype=dt, device="cuda")
+    plan = api.sl_gemm_plan(api.make_args(a, b, c, d, sa, sb, 128))
+    assert plan["tile_m"] in (128, 256)
+    assert torch.equal(api.gemm(a, b, c, out=d, sfa=sa, sfb=sb, block_k=128), want)
+    t = strided(torch.zeros((M, N), dtype=dt, device="cuda"), "cols")
+    api.gemm(a, b, strided(c, "cols"), out=t, sfa=sa, sfb=sb, block_k=128)
+    assert torch.equal(t, want)
+    # codes over their whole range, and a NaN's row
+    wide = (torch.randn((M, K), generator=gen(116), device="cuda") * 60).clamp(-TOP, TOP)
+    wide[7, 3] = float("nan")
+    got = api.gemm(wide.to(torch.float8_e4m3fn), b, sfa=sa, sfb=sb, block_k=128, dtype=dt).double()
+    ref, size = product64(wide.to(torch.float8_e4m3fn), sa, 1, b, sb, rb, None)
+    assert bool(torch.isnan(got[7]).all())
+    rest = torch.arange(M, device="cuda") != 7
+    share = 2.0 ** -11 if out != "float32" else (8 + 2 * blocks(K)) * 2.0 ** -24
+    bound = torch.finfo(dt).eps / 2 * ref.abs() + share * size * (1 + torch.finfo(dt).eps)
+    over = torch.isinf(got) & (got.sign() == ref.sign()) & (ref.abs() + bound > torch.finfo(dt).max)
+    assert bool((((got - ref).abs() <= bound) | over)[rest].all())
+
+
+@pytest.mark.parametrize("shape,dtype,out", [
+    ((3900, 4090), "bfloat16", "bfloat16"),   # direct, one plane: ring tiles, edges and what is left of a round
+    ((4090, 3900), "float16", "float16"),     # Gram, pairs, ring tiles, x and d tall
+    ((3840, 4200), "float32", "float16"),     # x itself a pair
+    ((1100, 5000), "bfloat16", "bfloat16"),   # Gram for a wide matrix
+    ((2, 2050, 2100), "float16", "float16"),
+])
+def test_orthogonalize_large_tiles(api, shape, dtype, out):
+    import torch
+    dt = getattr(torch, out)
+    x = gradient_like(shape, 121, dtype)
+    d = api.orthogonalize(x, out=torch.empty(shape, dtype=dt, device="cuda"))
+    want = orthogonalize64(x)
+    for b in range(shape[0] if len(shape) == 3 else 1):
+        g, w = (d[b], want[b]) if len(shape) == 3 else (d, want)
+        assert float((g.double() - w).norm() / w.norm()) <= ortho_tolerance(dt)
+
+
+def test_orthogonalize_large_direct_pairs(api):
+    """Steps that amplify too much for the Gram matrix, on ring tiles."""
+    import torch
+    x = gradient_like((3900, 4090), 131, "float16")
+    co = [DEFAULT] * 6
+    d = api.orthogonalize(x, steps=6, coefficients=co)
+    want = orthogonalize64(x, 6, co)
+    assert float((d.double() - want).norm() / want.norm()) <= 4 * ortho_tolerance(torch.float16)
