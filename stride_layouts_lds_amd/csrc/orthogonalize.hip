@@ -8,8 +8,10 @@
 //   Gram matrix        the same iteration on m x m matrices alone (G, P = a I
 //                      + b G + c G^2, Q <- P Q, G <- P G P, d = Q x), every one
 //                      a pair of fp16 planes; x times a power of two
-//   direct             the formula above; X one fp16 plane or, for fp16
-//                      results, a pair
+//   direct             the formula above; every matrix a pair of fp16 planes,
+//                      or, for bf16 results and steps that amplify little, X
+//                      a pair of which the products read the first plane, G
+//                      and B one plane
 //
 // All on the fp16 matrix cores with fp32 sums.  A plane holds values times a
 // power of two (2^10 for X, G and B of the direct way, 2^12 and 2^6 for the
@@ -88,13 +90,15 @@ struct OrthoScales {
 // EXACT: x times the power of two that brings |x| to 2^14 (to 2^15): exact in
 // fp16 but for what lies 2^-38 below |x|; the scales follow, and the
 // transpose is a pair in any case (its second plane zero).  Else 2^10 x /
-// (|x| + 1e-7), rounded.  With two planes also what the rounding left.
+// (|x| + 1e-7), rounded, and what the rounding left: the second plane, or,
+// with one plane, XL (m x n).
 template <int T, int PLANES, bool EXACT>
 __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, const double* parts, uint16_t* X,
-                                                          uint16_t* XT, OrthoScales* scales, int32_t tiles_m, int32_t tiles_n,
-                                                          int32_t sums) {
+                                                          uint16_t* XT, uint16_t* XL, OrthoScales* scales, int32_t tiles_m,
+                                                          int32_t tiles_n, int32_t sums) {
+  constexpr int KEPT = EXACT ? PLANES : 2;
   __shared__ double lds[4];
-  __shared__ uint16_t tile[PLANES][64][66];
+  __shared__ uint16_t tile[KEPT][64][66];
   const uint32_t id = blockIdx.x;
   const int32_t tn = id % tiles_n, tm = id / tiles_n % tiles_m;
   const int64_t b = id / tiles_n / tiles_m;
@@ -122,7 +126,7 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, c
     for (int e = 0; e < 8; ++e) {
       float y = as_computed((float)(v[e] * f));
 #pragma unroll
-      for (int q = 0; q < PLANES; ++q) {
+      for (int q = 0; q < KEPT; ++q) {
         const uint16_t h = from_f32<DT_F16>(y);
         tile[q][along_rows ? il + e : il][along_rows ? jl : jl + e] = h;
         y -= to_f32<DT_F16>(h);
@@ -141,6 +145,12 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, c
       *(u16x8*)(X + plane_at<PLANES>(b * mp + i0 + r, np, j0 + 8 * u) + 32 * q) = row;
       *(u16x8*)(XT + plane_at<EXACT ? 2 : PLANES>(b * np + j0 + r, mp, i0 + 8 * u) + 32 * q) = col;
     }
+    if constexpr (KEPT > PLANES) {
+      u16x8 row;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) row[e] = tile[1][r][8 * u + e];
+      *(u16x8*)(XL + (b * mp + i0 + r) * np + j0 + 8 * u) = row;
+    }
     if constexpr (EXACT && PLANES == 1) *(u16x8*)(XT + plane_at<2>(b * np + j0 + r, mp, i0 + 8 * u) + 32) = u16x8{0, 0, 0, 0, 0, 0, 0, 0};
   }
 }
@@ -155,6 +165,7 @@ struct OrthoGemm {
   const uint16_t* Q[2];          // (n, k)
   const uint16_t* E;             // (m, n), or NULL
   uint16_t* O[2];                // (m, n); sym: its transpose as well
+  uint16_t* low;                 // OP 1: the second plane of E and of O, apart from them and in place, or NULL
   uint16_t* OT;                  // (n, m), or NULL
   int64_t P_bs, Q_bs, E_bs, O_bs;
   int32_t m, n, k;               // padded: multiples of 64
@@ -224,23 +235,30 @@ template <int W>
 struct Halves {
   typedef uint16_t vec __attribute__((ext_vector_type(W)));
 };
-// W consecutive values of E at (m, n ..)
+// W consecutive values of E at (m, n ..): both planes, the second zero where
+// there is none
 template <int OP, int W>
 __device__ __forceinline__ void ortho_load(const OrthoGemm& g, const OrthoTile& o, int32_t m, int32_t n,
-                                           typename Halves<W>::vec (&x)[OP]) {
-  const uint16_t* E = g.E + o.batch * g.E_bs + plane_at<OP>(m, g.n, n);
-#pragma unroll
-  for (int q = 0; q < OP; ++q) x[q] = *(const typename Halves<W>::vec*)(E + 32 * q);
+                                           typename Halves<W>::vec (&x)[2]) {
+  typedef typename Halves<W>::vec vec;
+  const int64_t at = o.batch * g.E_bs + plane_at<OP>(m, g.n, n);
+  x[0] = *(const vec*)(g.E + at);
+  if constexpr (OP == 2)
+    x[1] = *(const vec*)(g.E + at + 32);
+  else if (g.low)
+    x[1] = *(const vec*)(g.low + at);
+  else
+    x[1] = vec{};
 }
 // W consecutive values of D at (m, n ..) from the sums and E's
-template <int OP, int W>
+template <int W>
 __device__ __forceinline__ void ortho_value(const OrthoGemm& g, const OrthoTile& o, int32_t m, int32_t n,
-                                            const typename Halves<W>::vec (&x)[OP], float (&v)[W]) {
+                                            const typename Halves<W>::vec (&x)[2], float (&v)[W]) {
 #pragma unroll
   for (int e = 0; e < W; ++e) v[e] *= o.alpha;
   if (g.E) {
 #pragma unroll
-    for (int q = OP - 1; q >= 0; --q)
+    for (int q = 1; q >= 0; --q)
 #pragma unroll
       for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(g.beta, to_f32<DT_F16>(x[q][e]), v[e]);
   }
@@ -289,11 +307,18 @@ __device__ __forceinline__ bool ortho_columns(const OrthoGemm& g, const OrthoTil
 // W consecutive n of row m
 template <int OP, int W>
 __device__ __forceinline__ void ortho_row(const OrthoGemm& g, const OrthoTile& o, bool columns, int32_t m, int32_t n,
-                                          const typename Halves<W>::vec (&x)[OP], float (&v)[W]) {
-  ortho_value<OP, W>(g, o, m, n, x, v);
-  if (!g.d)
-    ortho_store<OP, W>((o.product ? g.O[1] : g.O[0]) + o.batch * g.O_bs + plane_at<OP>(m, g.n, n), v);
-  else if (!columns && m < g.rows)
+                                          const typename Halves<W>::vec (&x)[2], float (&v)[W]) {
+  ortho_value<W>(g, o, m, n, x, v);
+  if (!g.d) {
+    const int64_t at = o.batch * g.O_bs + plane_at<OP>(m, g.n, n);
+    ortho_store<OP, W>((o.product ? g.O[1] : g.O[0]) + at, v);
+    if (OP == 1 && g.low) {
+      float left[W];
+#pragma unroll
+      for (int e = 0; e < W; ++e) left[e] = v[e] - to_f32<DT_F16>(from_f32<DT_F16>(v[e]));
+      ortho_store<1, W>(g.low + at, left);
+    }
+  } else if (!columns && m < g.rows)
     ortho_result<W>(g, (uint16_t*)g.d + o.batch * g.d_bs + m * g.d_rs + n * g.d_cs, g.d_cs, g.cols - n, v);
 }
 // W consecutive m of column n
@@ -438,7 +463,7 @@ __global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGem
   constexpr int PIECES = BM * BN / 8 / (256 * KG);
   auto row_of = [](int q) { return (int32_t)(threadIdx.x + 256 * KG * q) / (BN / 8); };
   auto col_of = [](int q) { return 8 * ((int32_t)(threadIdx.x + 256 * KG * q) % (BN / 8)); };
-  u16x8 ev[PIECES][OP];
+  u16x8 ev[PIECES][2];
   if (g.E) {
 #pragma unroll
     for (int q = 0; q < PIECES; ++q)
@@ -653,7 +678,7 @@ __global__ __launch_bounds__(256, 1) void ortho_ring_kernel(const OrthoGemm g) {
       const int32_t r = 2 * it + (lane >> 5), q = lane & 31;
       floatx4* at = (floatx4*)(region + rows_chunk(r, q));
       if (mb + r >= g.m || nb + 4 * q >= g.n) continue;
-      u16x4 e[OP];
+      u16x4 e[2];
       if (g.E) ortho_load<OP, 4>(g, o, mb + r, nb + 4 * q, e);
       const floatx4 x = *at;
       float v[4] = {x[0], x[1], x[2], x[3]};
@@ -712,8 +737,8 @@ hipError_t run_gemm(OrthoGemm g, hipStream_t s) {
 }
 
 template <int T>
-hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, uint16_t* XT, OrthoScales* scales,
-                 hipStream_t s) {
+hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, uint16_t* XT, uint16_t* XL,
+                 OrthoScales* scales, hipStream_t s) {
   const int32_t tm = (int32_t)(pad64(p.m) / 64), tn = (int32_t)(pad64(p.n) / 64);
   const int64_t length = p.x_rs == 1 && p.x_cs != 1 ? p.m : p.n;
   int32_t across = 64 * kNormWaves;
@@ -724,51 +749,92 @@ hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts
   hipLaunchKernelGGL(ortho_norm_kernel<T>, dim3(sums, p.batch), dim3(64 * kNormWaves), 0, s, p, parts, across);
   const dim3 grid((uint32_t)((int64_t)p.batch * tm * tn)), block(256);
   if (exact && planes == 2)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 2, true>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn, sums);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 2, true>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums);
   else if (exact)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 1, true>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn, sums);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 1, true>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums);
   else if (planes == 2)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 2, false>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn, sums);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 2, false>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums);
   else
-    hipLaunchKernelGGL((ortho_start_kernel<T, 1, false>), grid, block, 0, s, p, parts, X, XT, scales, tm, tn, sums);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 1, false>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums);
   return hipGetLastError();
 }
-hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, uint16_t* XT, OrthoScales* scales,
-                 hipStream_t s) {
+hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, uint16_t* XT, uint16_t* XL,
+                 OrthoScales* scales, hipStream_t s) {
   switch (p.x_type) {
-    case OT_F16: return start<OT_F16>(p, planes, exact, parts, X, XT, scales, s);
-    case OT_BF16: return start<OT_BF16>(p, planes, exact, parts, X, XT, scales, s);
-    default: return start<OT_F32>(p, planes, exact, parts, X, XT, scales, s);
+    case OT_F16: return start<OT_F16>(p, planes, exact, parts, X, XT, XL, scales, s);
+    case OT_BF16: return start<OT_BF16>(p, planes, exact, parts, X, XT, XL, scales, s);
+    default: return start<OT_F32>(p, planes, exact, parts, X, XT, XL, scales, s);
   }
 }
 
 enum Way { kSmallGram, kGram, kDirect };
+
+// How much the steps amplify where x has (almost) nothing: by a each.
+float growth_of(const OrthoParams& p) {
+  float growth = 1.f;
+  for (int32_t t = 0; t < p.steps; ++t) growth *= fmaxf(1.f, fabsf(p.coefficients[3 * t]));
+  return growth;
+}
+
+// How much the steps amplify anywhere: a rounding in X grows in a step by at
+// most the largest slope of s -> a s + b s^3 + c s^5 over the singular values
+// that can occur, 0 to r, r being 1 at first and then what the step makes of
+// it.  (Five default steps: 855, six 3400.)
+float slope_of(const OrthoParams& p) {
+  float slope = 1.f, r = 1.f;
+  for (int32_t t = 0; t < p.steps; ++t) {
+    const float a = p.coefficients[3 * t], b = p.coefficients[3 * t + 1], c = p.coefficients[3 * t + 2];
+    const float top = r * r;
+    float most = fabsf(a), next = 0.f;  // over the ends and where the slope, or the value, turns, in squares of s
+    auto slope_at = [&](float g) { return a + g * (3.f * b + 5.f * c * g); };
+    auto take_value = [&](float g) {
+      if (g > 0.f && g <= top) next = fmaxf(next, fabsf(sqrtf(g) * (a + g * (b + c * g))));
+    };
+    most = fmaxf(most, fabsf(slope_at(top)));
+    take_value(top);
+    if (c != 0.f) {
+      const float turn = -0.3f * b / c, in = 9.f * b * b - 20.f * a * c;
+      if (turn > 0.f && turn < top) most = fmaxf(most, fabsf(slope_at(turn)));
+      if (in >= 0.f) take_value((-3.f * b + sqrtf(in)) / (10.f * c)), take_value((-3.f * b - sqrtf(in)) / (10.f * c));
+    } else if (b != 0.f) {
+      take_value(-a / (3.f * b));
+    }
+    slope *= fmaxf(1.f, most), r = next;
+  }
+  return slope;
+}
 
 // The Gram matrix's way multiplies pairs, 54 m^3 + 3 m^2 n and up to 2 m^2 n
 // more multiply-adds for five steps, but for small sizes where launches
 // count; the direct one 15 m^2 n + 5 m^3 on single planes, three times that
 // on pairs.
 Way way_of(const OrthoParams& p) {
-  float growth = 1.f;
-  for (int32_t t = 0; t < p.steps; ++t) growth *= fmaxf(1.f, fabsf(p.coefficients[3 * t]));
-  if (growth > kGramGrowth) return kDirect;
+  if (growth_of(p) > kGramGrowth) return kDirect;
   if (p.m <= kGramRows) return kSmallGram;
   return p.d_type == OT_F16 || p.n > 4 * p.m ? kGram : kDirect;
 }
 
-// fp16 results of the direct way take pairs: with one plane, every matrix
-// between products rounded to fp16 costs them 1.1e-3 to 1.8e-3 (relative,
-// 2-norm; 64-bit simulation at 16 x 16 to 1000 x 1000), five times their own
-// rounding of 2.1e-4, with pairs 3e-7.  A bf16 result's own rounding is
-// 1.7e-3.  The Gram matrix's way keeps x itself, exactly, in one plane unless
-// it is fp32.
+// X's planes in the products of the direct way.  One for bf16 results and
+// steps that amplify up to kSingleSlope times: X is a pair all the same and a
+// X comes from both planes; what is rounded to fp16 is X as a factor, G and B.
+// (X as one plane was wrong: what its rounding leaves in directions where x
+// has nothing grows by a each step, 4e-2 of a result of rank 8.)  64-bit
+// simulation of these roundings, relative 2-norm, 256 x 256 to 1000 x 1000,
+// five default steps: noise 1.1e-3 to 1.4e-3, rank 1 to 64 1e-4 to 1e-3,
+// singular values over two or four decades 7e-4 to 1.2e-3, a few equal rows
+// among zeros up to 2.8e-3; a bf16 result's own rounding is 1.7e-3.  Steps
+// that amplify more (slope 3e4: 1e-2 of a result of rank 8) and fp16 results
+// (own rounding 2.1e-4) take pairs: 1e-7 to 1e-4.  8192 x 8192 takes 9.6 ms
+// with one plane and 23.5 with pairs, 1000 x 1000 145 and 195 us.  The Gram
+// matrix's way keeps x itself, exactly, in one plane unless it is fp32.
+constexpr float kSingleSlope = 1024.f;
 int32_t x_planes(const OrthoParams& p, Way way) {
   if (way == kGram) return p.x_type == OT_F32 && p.d_type == OT_F16 ? 2 : 1;
-  return p.d_type == OT_F16 ? 2 : 1;
+  return p.d_type == OT_F16 || growth_of(p) > kGramGrowth || !(slope_of(p) <= kSingleSlope) ? 2 : 1;
 }
 
 struct Places {
-  size_t scales, x, xt[2], mm[5], total;  // byte offsets behind the partial sums
+  size_t scales, x, xt[2], low, mm[5], total;  // byte offsets behind the partial sums
 };
 Places places(const OrthoParams& p, Way way) {
   const int32_t xp = x_planes(p, way), mp = way == kGram ? 2 : xp;
@@ -780,7 +846,8 @@ Places places(const OrthoParams& p, Way way) {
   q.xt[0] = q.x + mn;
   const size_t xt = way == kGram ? mn / xp * 2 : mn;  // the Gram way's is a pair
   q.xt[1] = way == kGram ? q.xt[0] : q.xt[0] + xt;
-  size_t at = q.xt[1] + xt;
+  q.low = q.xt[1] + xt;
+  size_t at = q.low + (way == kDirect && xp == 1 ? mn : 0);
   for (int i = 0; i < 5; ++i) {
     q.mm[i] = at;
     if (way == kGram || i < 2) at += mm;
@@ -800,10 +867,11 @@ hipError_t direct(const OrthoParams& p, hipStream_t s) {
   uint16_t* X = (uint16_t*)(p.ws + q.x);
   uint16_t* XT[2] = {(uint16_t*)(p.ws + q.xt[0]), (uint16_t*)(p.ws + q.xt[1])};
   uint16_t *G = (uint16_t*)(p.ws + q.mm[0]), *B = (uint16_t*)(p.ws + q.mm[1]);
+  uint16_t* XL = PL == 1 ? (uint16_t*)(p.ws + q.low) : nullptr;
   const int32_t mp = (int32_t)pad64(p.m), np = (int32_t)pad64(p.n);
   const int64_t mn = (int64_t)mp * np * PL, mm = (int64_t)mp * mp * PL;
   constexpr float kDown = 0x1p-10f;  // what a stored value times it stands for
-  hipError_t e = start(p, PL, false, (double*)p.ws, X, XT[0], nullptr, s);
+  hipError_t e = start(p, PL, false, (double*)p.ws, X, XT[0], XL, nullptr, s);
   for (int32_t k = 0; k < p.steps && e == hipSuccess; ++k) {
     const float a = p.coefficients[3 * k], b = p.coefficients[3 * k + 1], c = p.coefficients[3 * k + 2];
     // stored values carry 2^10, products of two 2^20
@@ -819,7 +887,7 @@ hipError_t direct(const OrthoParams& p, hipStream_t s) {
     if ((e = run_gemm<PL == 2 ? kPairs : kPlain, PL>(g, s)) != hipSuccess) break;
     g.P = B, g.Q[0] = XT[k & 1], g.E = X, g.Q_bs = g.E_bs = mn;
     g.n = np, g.alpha[0] = kDown, g.beta = a, g.sym = 0;
-    g.O[0] = X, g.OT = XT[(k + 1) & 1], g.O_bs = mn;
+    g.O[0] = X, g.OT = XT[(k + 1) & 1], g.low = XL, g.O_bs = mn;
     if (k + 1 == p.steps) {
       g.alpha[0] *= kDown, g.beta *= kDown;
       to_result(p, &g);
@@ -841,7 +909,7 @@ hipError_t gram(const OrthoParams& p, hipStream_t s) {
   const int32_t mp = (int32_t)pad64(p.m), np = (int32_t)pad64(p.n);
   const int64_t mn = (int64_t)mp * np * PX, mm = (int64_t)mp * mp * 2;
   constexpr float kG = 0x1p12f, kP = 0x1p6f;  // what G's planes, and those of P, H and Q, are multiplied by
-  hipError_t e = start(p, PX, true, (double*)p.ws, X, XT, scales, s);
+  hipError_t e = start(p, PX, true, (double*)p.ws, X, XT, nullptr, scales, s);
   if (e != hipSuccess) return e;
   OrthoGemm g{};
   g.batch = p.batch, g.products = 1, g.sym = 1;

@@ -606,3 +606,47 @@ def test_orthogonalize_large_direct_pairs(api):
     d = api.orthogonalize(x, steps=6, coefficients=co)
     want = orthogonalize64(x, 6, co)
     assert float((d.double() - want).norm() / want.norm()) <= 4 * ortho_tolerance(torch.float16)
+
+
+# ---------------------------------------------------------------------------
+# inputs with directions in which x has (almost) nothing
+# ---------------------------------------------------------------------------
+
+def poor_rank(kind, shape, seed, dtype):
+    """Of few strong directions, of singular values over decades, or with most
+    rows zero."""
+    import torch
+    m, n = shape
+    normal = lambda s, *shp: torch.randn(shp, generator=gen(s), device="cuda", dtype=torch.float64)
+    if kind.startswith("rank"):
+        r = int(kind[4:])
+        x = torch.matmul(normal(seed, m, r), normal(seed + 1, r, n))
+    elif kind.startswith("decades"):
+        k = min(m, n)
+        u, _ = torch.linalg.qr(normal(seed, m, k))
+        v, _ = torch.linalg.qr(normal(seed + 1, n, k))
+        x = torch.matmul(u * torch.logspace(0, -int(kind[7:]), k, device="cuda", dtype=torch.float64), v.t().contiguous())
+    else:
+        x = normal(seed, m, n)
+        x[m // 8:] = 0
+    return (x * 1e-3).to(getattr(torch, dtype))
+
+
+# 2-norm, relative.  A bf16 result's rounding is uniform within half a step, which is at most 2^-8 of
+# the value: 2^-8 / sqrt(3) = 2.26e-3 at most.  Next to it stand, for five default steps, what a 64-bit
+# simulation of the fp16 roundings of X (as a factor), G and B gave, 2.8e-3 at most (few equal rows
+# among zeros), and, for steps that amplify more and run on pairs, 1e-4.
+BF16_ROUNDING = 2.0 ** -8 / 3 ** 0.5
+
+
+@pytest.mark.parametrize("kind", ["rank1", "rank8", "rank64", "decades2", "decades4", "rows"])
+@pytest.mark.parametrize("shape,dtype", [((300, 400), "bfloat16"), ((300, 400), "float32"), ((1000, 1000), "bfloat16"),
+                                         ((2100, 530), "float32"), ((3900, 4090), "bfloat16")])
+@pytest.mark.parametrize("steps", [5, 6])
+def test_orthogonalize_poor_rank(api, kind, shape, dtype, steps):
+    import torch
+    x = poor_rank(kind, shape, 141, dtype)
+    d = api.orthogonalize(x, out=torch.empty(shape, dtype=torch.bfloat16, device="cuda"), steps=steps)
+    want = orthogonalize64(x, steps)
+    inside = 2.9e-3 if steps == 5 else 1.1e-4
+    assert float((d.double() - want).norm() / want.norm()) <= (BF16_ROUNDING ** 2 + inside ** 2) ** 0.5
