@@ -81,21 +81,23 @@ __device__ __forceinline__ int64_t plane_at(int64_t row, int64_t cols, int64_t c
 
 // What the products multiply by, one of each for every matrix.
 struct OrthoScales {
-  float gram;   // of x's planes' Gram matrix, to make G's plane (2^12 G)
-  float apply;  // of Q's plane times x's, to make d
+  float gram;   // of X's planes' Gram matrix, to make G's plane
+  float apply;  // of Q's plane times x's, or of the direct way's last step, to make d
 };
 
 // The planes that the products read: m x n and n x m, zero to the padded
 // sizes.
 // EXACT: x times the power of two that brings |x| to 2^14 (to 2^15): exact in
 // fp16 but for what lies 2^-38 below |x|; the scales follow, and the
-// transpose is a pair in any case (its second plane zero).  Else 2^10 x /
-// (|x| + 1e-7), rounded, and what the rounding left: the second plane, or,
-// with one plane, XL (m x n).
+// transpose is a pair in any case (its second plane zero).  Else 2^(10 + e)
+// X_0, X_0 = x / (|x| + 1e-7), rounded, and what the rounding left: the second
+// plane, or, with one plane, XL (m x n).  e is zero but where |x| lies so far
+// below 1e-7 that no iterate passes 1 (|X_0| below 2^knee): 2^10 X would fall
+// out of fp16's range there, and 2^(10 + e) X stays below 2^15 throughout.
 template <int T, int PLANES, bool EXACT>
 __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, const double* parts, uint16_t* X,
                                                           uint16_t* XT, uint16_t* XL, OrthoScales* scales, int32_t tiles_m,
-                                                          int32_t tiles_n, int32_t sums) {
+                                                          int32_t tiles_n, int32_t sums, int32_t knee) {
   constexpr int KEPT = EXACT ? PLANES : 2;
   __shared__ double lds[4];
   __shared__ uint16_t tile[KEPT][64][66];
@@ -105,8 +107,14 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, c
   const int64_t mp = 64 * (int64_t)tiles_m, np = 64 * (int64_t)tiles_n;
   const double sum = block_sum((int32_t)threadIdx.x < sums ? parts[b * kNormParts + threadIdx.x] : 0.0, lds);
   const double norm = sqrt(sum), inv = 1.0 / (norm + 1e-7);
-  double f = 1024.0 * inv;
-  if constexpr (EXACT) {
+  double f;
+  if constexpr (!EXACT) {
+    const double x0 = norm * inv;
+    const int32_t k = x0 > 0.0 ? ilogb(x0) + 1 : 0;                           // |X_0| < 2^k
+    const int32_t e = x0 > 0.0 && k <= knee ? min(5 + knee - k, 100) : 0;  // (NaN: 0)
+    f = ldexp(inv, 10 + e);
+    if (tm == 0 && tn == 0 && threadIdx.x == 0) scales[b] = OrthoScales{ldexpf(1.f, -2 * e), ldexpf(1.f, -e)};
+  } else {
     // infinite or NaN norms make every scale NaN
     const int32_t e = norm > 0.0 && norm < __builtin_inf() ? ilogb(norm) : 0;
     f = ldexp(1.0, 14 - e);
@@ -169,7 +177,7 @@ struct OrthoGemm {
   uint16_t* OT;                  // (n, m), or NULL
   int64_t P_bs, Q_bs, E_bs, O_bs;
   int32_t m, n, k;               // padded: multiples of 64
-  float alpha[2], beta, diag;
+  float alpha[2], beta, diag;    // with scales: alpha and beta times one of the matrix's
   const OrthoScales* scales;     // or NULL
   int32_t scale_apply;           // which of them
   int32_t sym;
@@ -185,7 +193,7 @@ struct OrthoGemm {
 struct OrthoTile {
   int32_t batch, product, tm, tn;
   bool mirror;  // off the diagonal of a symmetric result
-  float alpha;
+  float alpha, beta;
 };
 
 // The tile of a workgroup.  Workgroups go to the 8 XCDs in turn: each XCD
@@ -227,7 +235,11 @@ __device__ __forceinline__ OrthoTile ortho_tile(const OrthoGemm& g) {
   o.mirror = g.sym && o.tm != o.tn;
   o.tm = o.tm * g.parts + part % g.parts, o.tn = o.tn * g.parts + part / g.parts;
   o.alpha = o.product ? g.alpha[1] : g.alpha[0];
-  if (g.scales) o.alpha *= g.scale_apply ? g.scales[o.batch].apply : g.scales[o.batch].gram;
+  o.beta = g.beta;
+  if (g.scales) {
+    const float s = g.scale_apply ? g.scales[o.batch].apply : g.scales[o.batch].gram;
+    o.alpha *= s, o.beta *= s;
+  }
   return o;
 }
 
@@ -260,7 +272,7 @@ __device__ __forceinline__ void ortho_value(const OrthoGemm& g, const OrthoTile&
 #pragma unroll
     for (int q = 1; q >= 0; --q)
 #pragma unroll
-      for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(g.beta, to_f32<DT_F16>(x[q][e]), v[e]);
+      for (int e = 0; e < W; ++e) v[e] = __builtin_fmaf(o.beta, to_f32<DT_F16>(x[q][e]), v[e]);
   }
 #pragma unroll
   for (int e = 0; e < W; ++e) v[e] = as_computed(m == n + e ? v[e] + g.diag : v[e]);
@@ -738,7 +750,7 @@ hipError_t run_gemm(OrthoGemm g, hipStream_t s) {
 
 template <int T>
 hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, uint16_t* XT, uint16_t* XL,
-                 OrthoScales* scales, hipStream_t s) {
+                 OrthoScales* scales, int32_t knee, hipStream_t s) {
   const int32_t tm = (int32_t)(pad64(p.m) / 64), tn = (int32_t)(pad64(p.n) / 64);
   const int64_t length = p.x_rs == 1 && p.x_cs != 1 ? p.m : p.n;
   int32_t across = 64 * kNormWaves;
@@ -749,21 +761,21 @@ hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts
   hipLaunchKernelGGL(ortho_norm_kernel<T>, dim3(sums, p.batch), dim3(64 * kNormWaves), 0, s, p, parts, across);
   const dim3 grid((uint32_t)((int64_t)p.batch * tm * tn)), block(256);
   if (exact && planes == 2)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 2, true>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 2, true>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums, knee);
   else if (exact)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 1, true>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 1, true>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums, knee);
   else if (planes == 2)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 2, false>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 2, false>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums, knee);
   else
-    hipLaunchKernelGGL((ortho_start_kernel<T, 1, false>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums);
+    hipLaunchKernelGGL((ortho_start_kernel<T, 1, false>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums, knee);
   return hipGetLastError();
 }
 hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, uint16_t* XT, uint16_t* XL,
-                 OrthoScales* scales, hipStream_t s) {
+                 OrthoScales* scales, int32_t knee, hipStream_t s) {
   switch (p.x_type) {
-    case OT_F16: return start<OT_F16>(p, planes, exact, parts, X, XT, XL, scales, s);
-    case OT_BF16: return start<OT_BF16>(p, planes, exact, parts, X, XT, XL, scales, s);
-    default: return start<OT_F32>(p, planes, exact, parts, X, XT, XL, scales, s);
+    case OT_F16: return start<OT_F16>(p, planes, exact, parts, X, XT, XL, scales, knee, s);
+    case OT_BF16: return start<OT_BF16>(p, planes, exact, parts, X, XT, XL, scales, knee, s);
+    default: return start<OT_F32>(p, planes, exact, parts, X, XT, XL, scales, knee, s);
   }
 }
 
@@ -802,6 +814,18 @@ float slope_of(const OrthoParams& p) {
     slope *= fmaxf(1.f, most), r = next;
   }
   return slope;
+}
+
+// Where |X_0| is below two to this power no iterate passes 1, and |X| grows
+// at most in proportion to |X_0|: by |a| + |b| |X|^2 + |c| |X|^4 a step.
+int32_t knee_of(const OrthoParams& p) {
+  for (int32_t k = 0; k > -160; --k) {
+    double u = ldexp(1.0, k);
+    for (int32_t t = 0; t < p.steps && u <= 1.0; ++t)
+      u *= fmax(1.0, fabs(p.coefficients[3 * t]) + u * u * (fabs(p.coefficients[3 * t + 1]) + u * u * fabs(p.coefficients[3 * t + 2])));
+    if (u <= 1.0) return k;
+  }
+  return -160;
 }
 
 // The Gram matrix's way multiplies pairs, 54 m^3 + 3 m^2 n and up to 2 m^2 n
@@ -867,11 +891,12 @@ hipError_t direct(const OrthoParams& p, hipStream_t s) {
   uint16_t* X = (uint16_t*)(p.ws + q.x);
   uint16_t* XT[2] = {(uint16_t*)(p.ws + q.xt[0]), (uint16_t*)(p.ws + q.xt[1])};
   uint16_t *G = (uint16_t*)(p.ws + q.mm[0]), *B = (uint16_t*)(p.ws + q.mm[1]);
+  OrthoScales* scales = (OrthoScales*)(p.ws + q.scales);
   uint16_t* XL = PL == 1 ? (uint16_t*)(p.ws + q.low) : nullptr;
   const int32_t mp = (int32_t)pad64(p.m), np = (int32_t)pad64(p.n);
   const int64_t mn = (int64_t)mp * np * PL, mm = (int64_t)mp * mp * PL;
   constexpr float kDown = 0x1p-10f;  // what a stored value times it stands for
-  hipError_t e = start(p, PL, false, (double*)p.ws, X, XT[0], XL, nullptr, s);
+  hipError_t e = start(p, PL, false, (double*)p.ws, X, XT[0], XL, scales, knee_of(p), s);
   for (int32_t k = 0; k < p.steps && e == hipSuccess; ++k) {
     const float a = p.coefficients[3 * k], b = p.coefficients[3 * k + 1], c = p.coefficients[3 * k + 2];
     // stored values carry 2^10, products of two 2^20
@@ -879,8 +904,9 @@ hipError_t direct(const OrthoParams& p, hipStream_t s) {
     g.batch = p.batch, g.products = 1;
     g.P = g.Q[0] = X, g.P_bs = g.Q_bs = mn;
     g.m = g.n = mp, g.k = np, g.alpha[0] = kDown, g.sym = 1;
-    g.O[0] = G, g.O_bs = mm;
+    g.O[0] = G, g.O_bs = mm, g.scales = scales;
     if ((e = run_gemm<PL == 2 ? kPairs : kPlain, PL>(g, s)) != hipSuccess) break;
+    g.scales = nullptr;
     g.P = g.Q[0] = g.E = G, g.P_bs = g.Q_bs = g.E_bs = mm;
     g.k = mp, g.alpha[0] = c * kDown, g.beta = b;
     g.O[0] = B;
@@ -889,7 +915,7 @@ hipError_t direct(const OrthoParams& p, hipStream_t s) {
     g.n = np, g.alpha[0] = kDown, g.beta = a, g.sym = 0;
     g.O[0] = X, g.OT = XT[(k + 1) & 1], g.low = XL, g.O_bs = mn;
     if (k + 1 == p.steps) {
-      g.alpha[0] *= kDown, g.beta *= kDown;
+      g.alpha[0] *= kDown, g.beta *= kDown, g.scales = scales, g.scale_apply = 1;
       to_result(p, &g);
     }
     e = run_gemm<PL == 2 ? kPairs : kPlain, PL>(g, s);
@@ -909,7 +935,7 @@ hipError_t gram(const OrthoParams& p, hipStream_t s) {
   const int32_t mp = (int32_t)pad64(p.m), np = (int32_t)pad64(p.n);
   const int64_t mn = (int64_t)mp * np * PX, mm = (int64_t)mp * mp * 2;
   constexpr float kG = 0x1p12f, kP = 0x1p6f;  // what G's planes, and those of P, H and Q, are multiplied by
-  hipError_t e = start(p, PX, true, (double*)p.ws, X, XT, nullptr, scales, s);
+  hipError_t e = start(p, PX, true, (double*)p.ws, X, XT, nullptr, scales, 0, s);
   if (e != hipSuccess) return e;
   OrthoGemm g{};
   g.batch = p.batch, g.products = 1, g.sym = 1;

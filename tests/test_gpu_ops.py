@@ -650,3 +650,19 @@ def test_orthogonalize_poor_rank(api, kind, shape, dtype, steps):
     want = orthogonalize64(x, steps)
     inside = 2.9e-3 if steps == 5 else 1.1e-4
     assert float((d.double() - want).norm() / want.norm()) <= (BF16_ROUNDING ** 2 + inside ** 2) ** 0.5
+
+
+@pytest.mark.parametrize("norm", [1e-6, 1e-8, 3e-10, 1e-11, 1e-13, 1e-16, 1e-24, 1e-33])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("shape,steps", [((96, 128), 5), ((300, 400), 5), ((300, 400), 6), ((140, 1000), 5), ((1500, 1600), 5)])
+def test_orthogonalize_small_norms(api, norm, dtype, shape, steps):
+    """Norms about and far below the 1e-7 that is added to them: the result is
+    small then, and as accurate as any other."""
+    import torch
+    x = torch.randn((2,) + shape, generator=gen(151), device="cuda", dtype=torch.float64)
+    x[0] *= norm / x[0].norm()  # the other matrix is ordinary
+    x = x.to(getattr(torch, dtype))
+    d = api.orthogonalize(x, out=torch.empty(x.shape, dtype=torch.bfloat16, device="cuda"), steps=steps)
+    want = orthogonalize64(x, steps)
+    for b in range(2):
+        assert float((d[b].double() - want[b]).norm() / want[b].norm()) <= (BF16_ROUNDING ** 2 + 2.9e-3 ** 2) ** 0.5
