@@ -194,7 +194,8 @@ typedef struct {
  * 8-bit instruction), for f32 d it is an fp32 sum of exact products.  Operands
  * K-contiguous with rows on 16-byte boundaries and K % 16 == 0, scales of any
  * strides (sl_quantize writes them).  No workspace.
- * Sizes: M, N, K and the batch count below 2^31 (else SL_ERR_SHAPE).  An
+ * Sizes: M, N, K and the batch count below 2^31, and the plan's workgroups
+ * times their threads below 2^32 (else SL_ERR_SHAPE).  An
  * operand may span any number of bytes; 256 of its rows (one tile) must
  * span fewer than 2^31 bytes for the vector loaders of 16-bit operands
  * (else the slower element loader runs), and for packed 4/6-bit data and
@@ -245,7 +246,9 @@ sl_status sl_gemm_no_alloc(const sl_gemm_args* args, void* stream);
  * ignored).  q and qt are contiguous along their last axis with rows on
  * 16-byte boundaries; no output may broadcast or overlap x or another
  * output.  An empty x is a no-op.  Asynchronous on `stream`, one kernel, no
- * workspace; errors as sl_gemm, SL_ERR_ARG for another block_rows.
+ * workspace; errors as sl_gemm, SL_ERR_ARG for another block_rows, SL_ERR_SHAPE
+ * from 2^24 workgroups on (64 rows x 128 columns of x each for q alone with
+ * block_rows 1, else 128 x 128).
  * Scales stored with the rows contiguous (strides (1, rows)) are the ones
  * that sl_gemm's large tiles read fastest.
  */
@@ -291,9 +294,10 @@ sl_status sl_quantize(const sl_quantize_args* args, void* stream);
  * call's kernels have finished on `stream`; its contents do not matter
  * before or after.  An empty x is a no-op and needs none.  Sizes: fewer than
  * 65536 matrices, and each (its sizes rounded up to multiples of 64) fewer
- * than 2^29 values, but for up to 128 rows or columns and coefficients whose
- * a's multiply to at most 512, where 2^30 tiles of 64 x 64 in all are the
- * limit (else SL_ERR_SHAPE).  Asynchronous on
+ * than 2^29 values, with fewer than 2^24 tiles of 64 x 64 in all; for up to 128
+ * rows or columns and coefficients whose a's multiply to at most 512 instead
+ * fewer than 2^24 pieces of 128 along the longer axis in all
+ * (else SL_ERR_SHAPE).  Asynchronous on
  * `stream`; errors as sl_gemm, SL_ERR_ARG for steps or coefficients.
  */
 typedef struct {

@@ -490,8 +490,9 @@ sl_status plan_gemm(const sl_gemm_args* args, Plan* out, bool allow_decode = tru
   P.tile = tile;
   p.tiles_m = (int32_t)((M + ts.bm - 1) / ts.bm);
   p.tiles_n = (int32_t)((N + ts.bn - 1) / ts.bn);
+  if (!grid_fits(batch * p.splits, p.tiles_m, p.tiles_n, ts.wm * ts.wn * 64))
+    return fail(SL_ERR_SHAPE, "too many output tiles (%lld x %d x %d)", (long long)batch, p.tiles_m, p.tiles_n);
   const int64_t total = batch * p.tiles_m * p.tiles_n * p.splits;
-  if (total >= lim) return fail(SL_ERR_SHAPE, "too many output tiles (%lld)", (long long)total);
   P.pub.tile_m = ts.bm;
   P.pub.tile_n = ts.bn;
   P.pub.threads = ts.wm * ts.wn * 64;

@@ -120,6 +120,12 @@ inline bool same_layout(const sl_tensor& x, const sl_tensor& y) {
   return true;
 }
 
+// HIP's limit: a launch has fewer than 2^32 work items along its grid.  (In
+// floating point: the product of three counts can pass 64 bits.)
+inline bool grid_fits(int64_t batch, int64_t tiles_m, int64_t tiles_n, int32_t threads) {
+  return (double)batch * (double)tiles_m * (double)tiles_n * (double)threads < 0x1p32;
+}
+
 // gfx950 check, cached per device
 inline sl_status check_arch() {
   static std::mutex mu;

@@ -160,15 +160,18 @@ sl_status plan_block(const sl_gemm_args* args, BlockPlan* out) {
   };
   p.flags = (has_c ? BF_HAS_C : 0) | (quads(D) ? BF_D_VEC : 0) | (has_c && quads(C) ? BF_C_VEC : 0);
 
+  if (!grid_fits(batch, ceil_div(M, 256), ceil_div(N, 256), 256))  // in the largest tiles
+    return fail(SL_ERR_SHAPE, "too many output tiles (batch %lld of %lld x %lld)", (long long)batch, (long long)M, (long long)N);
   P.tile = choose_tile(batch, M, N, type);
   BlockTileShape ts = kBlockTiles[P.tile];
   if (P.tile == BT_SKINNY) ts.bn = skinny_cols(M, N, batch);
   p.tiles_m = (int32_t)ceil_div(M, ts.bm), p.tiles_n = (int32_t)ceil_div(N, ts.bn);
   const int64_t total = batch * p.tiles_m * p.tiles_n;
-  if (total >= kLim) return fail(SL_ERR_SHAPE, "too many output tiles (%lld)", (long long)total);
   P.pub.a_load = P.pub.b_load = LOAD_KVEC;
   P.pub.tile_m = ts.bm, P.pub.tile_n = ts.bn, P.pub.tile_k = kScaleBlock;
   P.pub.threads = P.tile == BT_SKINNY ? (M <= 16 ? kSkinnyWaves : kStreamWaves) * 64 : ts.wm * ts.wn * 64;
+  if (!grid_fits(batch, p.tiles_m, p.tiles_n, P.pub.threads))
+    return fail(SL_ERR_SHAPE, "too many output tiles (%lld)", (long long)total);
   P.pub.workgroups = total;
   if (P.tile == BT_256x256) P.pub.lds_bytes = 5 * 256 * kScaleBlock;
   else if (P.tile == BT_128x128) P.pub.lds_bytes = (total > 256 ? 2 : 4) * 256 * kScaleBlock;
@@ -265,7 +268,8 @@ sl_status sl_quantize(const sl_quantize_args* args, void* stream) {
     std::swap(p.q_cols, p.qt_cols), std::swap(p.q_bs, p.qt_bs), std::swap(p.q_rs, p.qt_rs);
     std::swap(p.s_bs, p.st_bs), std::swap(p.s_rs, p.st_rs), std::swap(p.s_cs, p.st_cs);
   }
-  if (sl::quantize_workgroups(p) >= kLim) return fail(SL_ERR_SHAPE, "too many blocks (%lld)", (long long)sl::quantize_workgroups(p));
+  if (!grid_fits(batch, ceil_div(p.rows, sl::quantize_rows(p)), ceil_div(p.cols, 128), sl::kQuantizeThreads))
+    return fail(SL_ERR_SHAPE, "too many blocks (batch %lld of %lld x %lld)", (long long)batch, (long long)R, (long long)C);
   if ((s = check_arch()) != SL_OK) return s;
   const hipError_t e = sl::launch_quantize(p, (hipStream_t)stream);
   if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));

@@ -983,12 +983,18 @@ size_t orthogonalize_workspace(const OrthoParams& p) {
   return way == kSmallGram ? ortho_gram_workspace(p) : places(p, way).total;
 }
 
-// every launch fits a grid, and a matrix's planes 32-bit offsets
+// Every launch fits a grid (fewer than 2^32 work items along its x, 65536
+// matrices along its y), and a matrix's planes 32-bit offsets.  The largest
+// grids: up to 128 rows, the last launch's 256 threads for each 128 columns
+// (the first one's 512 for up to 64 ranges of columns stay below 2^31);
+// otherwise the start's 256 threads for each 64 x 64 values (the products' tiles
+// are larger, or a few).
 bool orthogonalize_grid_ok(const OrthoParams& p) {
   const int64_t lim = (int64_t)1 << 31;
   if (p.batch >= 65536 || p.m >= lim || p.n >= lim) return false;
-  if ((double)p.batch * (double)(pad64(p.m) / 64) * (double)(pad64(p.n) / 64) >= 0x1p30) return false;
-  return way_of(p) == kSmallGram || (double)pad64(p.m) * (double)pad64(p.n) * 4 < 0x1p31;
+  if (way_of(p) == kSmallGram) return (double)p.batch * (double)((p.n + 127) / 128) < 0x1p24;
+  return (double)p.batch * (double)(pad64(p.m) / 64) * (double)(pad64(p.n) / 64) < 0x1p24 &&
+         (double)pad64(p.m) * (double)pad64(p.n) * 4 < 0x1p31;
 }
 
 hipError_t launch_orthogonalize(const OrthoParams& p, hipStream_t s) {

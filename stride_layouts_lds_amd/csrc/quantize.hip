@@ -309,7 +309,8 @@ bool rows_only(const QuantizeParams& p) { return !p.qt && !p.square; }
 template <int T, bool CONTIG>
 void go(const QuantizeParams& p, hipStream_t s) {
   const uint32_t bc = (uint32_t)((p.cols + 127) / 128), br = (uint32_t)((p.rows + 127) / 128);
-  const dim3 grid((uint32_t)quantize_workgroups(p)), block(256);
+  const int64_t rows = quantize_rows(p);
+  const dim3 grid((uint32_t)(p.batch * ((p.rows + rows - 1) / rows) * bc)), block(kQuantizeThreads);
   if (rows_only(p))
     hipLaunchKernelGGL((quantize_rows_kernel<T, CONTIG>), grid, block, 0, s, p, bc,
                        (uint32_t)((p.rows + kRowTile - 1) / kRowTile));
@@ -321,10 +322,7 @@ void go(const QuantizeParams& p, hipStream_t s) {
 
 }  // namespace
 
-int64_t quantize_workgroups(const QuantizeParams& p) {
-  const int64_t rows = rows_only(p) ? kRowTile : 128;
-  return (int64_t)p.batch * ((p.rows + rows - 1) / rows) * ((p.cols + 127) / 128);
-}
+int32_t quantize_rows(const QuantizeParams& p) { return rows_only(p) ? kRowTile : 128; }
 
 hipError_t launch_quantize(const QuantizeParams& p, hipStream_t s) {
   const bool contig = p.x_cs == 1;

@@ -35,7 +35,8 @@ struct QuantizeParams {
   float* st;
   int64_t qt_cols, qt_bs, qt_rs, st_bs, st_rs, st_cs;
 };
-int64_t quantize_workgroups(const QuantizeParams& p);
+constexpr int32_t kQuantizeThreads = 256;
+int32_t quantize_rows(const QuantizeParams& p);  // of a workgroup; 128 columns
 hipError_t launch_quantize(const QuantizeParams& p, hipStream_t stream);
 
 // ---------------------------------------------------------------------------

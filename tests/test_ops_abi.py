@@ -240,3 +240,51 @@ def test_block_product_plans(api):
     mx = gemm_args(api, GOOD_P["a"], GOOD_P["b"], rm(D, (300, 200), F16), rm(S, (300, 16), E8M0),
                    rm(ST, (200, 16), E8M0), block_k=32)
     assert api.sl_gemm_plan(mx)["kernel"] in (api.K_MX, api.K_MX_W8, api.K_MX_W4R)
+
+
+# ------------------------------------------- a launch's grid: below 2^32 work items
+
+def test_quantize_grid_limit(api):
+    # 2^24 workgroups of 256 threads: 64 rows x 128 columns each, or tiles of 128 x 128
+    R = 1 << 30
+    refused(api, api.sl_quantize, quantize_args(api, rm(X, (R, 1), F16), rm(1 << 50, (R, 16), F8), rm(1 << 51, (R, 1), F32)),
+            "SL_ERR_SHAPE")
+    refused(api, api.sl_quantize, quantize_args(api, rm(X, (2, R, 1), F16), qt=rm(1 << 52, (2, 1, R), F8),
+                                                st=rm(1 << 53, (2, 1, R // 128), F32)), "SL_ERR_SHAPE")
+    refused(api, api.sl_quantize, quantize_args(api, rm(X, (2, R, 1), F16), rm(1 << 50, (2, R, 16), F8),
+                                                rm(1 << 51, (2, R // 128, 1), F32), block_rows=128), "SL_ERR_SHAPE")
+
+
+def test_orthogonalize_grid_limit(api):
+    size = lambda shape, **kw: api.sl_orthogonalize_workspace_bytes(ortho_args(api, rm(X, shape, BF16), rm(D, shape, BF16), **kw))
+    # up to 128 rows: 128 columns a workgroup of 256 threads
+    assert size((65535, 1, 32767)) > 0 and size((1, (1 << 31) - 128)) > 0
+    # 64 x 64 values a workgroup of 256 threads
+    assert size((255, 200, 64 * 16383)) > 0
+    for shape in ((65535, 1, 65536), (65535, 128, 32769), (1, (1 << 31) - 1), (257, 200, 64 * 16384)):
+        with pytest.raises(api.SLError) as e:
+            size(shape)
+        assert e.value.name == "SL_ERR_SHAPE", shape
+
+
+def test_product_grid_limit(api):
+    def block(M, N, K=16):
+        return gemm_args(api, rm(X, (M, K), F8), rm(Q, (N, K), F8), rm(D, (M, N), BF16, (N, 1)), rm(S, (M, 1), F32, (1, 1)),
+                         rm(ST, (-(-N // 128), 1), F32, (1, 1)))
+    # one row: 32 columns a workgroup of 512 threads; 40 rows: of 256
+    ok = api.sl_gemm_plan(block(1, (1 << 28) - 32))
+    assert ok["workgroups"] * ok["threads"] == (1 << 32) - 512
+    ok = api.sl_gemm_plan(block(40, (1 << 29) - 32))
+    assert ok["workgroups"] * ok["threads"] < 1 << 32
+    for M, N in ((1, 1 << 28), (40, 1 << 29), (1 << 21, 1 << 20)):
+        with pytest.raises(api.SLError) as e:
+            api.sl_gemm_plan(block(M, N))
+        assert e.value.name == "SL_ERR_SHAPE"
+    # the other forms
+    f16 = lambda M, N: api.sl_gemm_plan(gemm_args(api, rm(X, (M, 64), F16), rm(Q, (N, 64), F16), rm(D, (M, N), F16, (N, 1)),
+                                                  None, None))
+    ok = f16(1 << 21, 1 << 18)
+    assert ok["workgroups"] * ok["threads"] < 1 << 32
+    with pytest.raises(api.SLError) as e:
+        f16(1 << 21, 1 << 20)
+    assert e.value.name == "SL_ERR_SHAPE"
