@@ -7,6 +7,7 @@ is not built, every call raises; there is no fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -258,6 +259,19 @@ def _stream(stream: Optional[int]) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream)
 
 
+def _allocating_on(stream: Optional[int], device):
+    """A context whose torch allocations belong to ``stream`` (None: torch's
+    current one).  What a call on another stream than torch's current one
+    writes must not come from the current one's pool: earlier work there may
+    still use the block, and it is handed out again there as soon as the
+    tensor is dropped, with the call's kernels still to run."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
+                             else torch.cuda.default_stream(device))
+
+
 def sl_gemm(args: sl_gemm_args, stream: Optional[int] = None) -> None:
     _check(lib().sl_gemm(ctypes.byref(args), _stream(stream)))
 
@@ -297,16 +311,20 @@ def gemm(a, b, c=None, out=None, sfa=None, sfb=None, block_k: int = 32, stream: 
     ceil(K/128)) with ``block_k`` 128 as ``quantize`` writes them, where D and
     C may be fp16, bf16 or float32 (``dtype``, or ``out``'s).  A plan's workspace (split-K partial sums, or NVFP4
     operands decoded to fp16) is ``workspace`` (a device tensor) or, when
-    None, a torch allocation of the size the library asks for.  Returns ``out`` (allocated by torch if None)."""
+    None, a torch allocation of the size the library asks for.  Returns ``out`` (allocated by torch if None).
+    With ``stream`` (a stream's handle) the call runs there, and what it
+    allocates belongs to that stream, as under ``torch.cuda.stream``."""
     import torch
     if out is None:
         batch = max(x.shape[0] if x is not None and x.dim() == 3 else 0 for x in (a, b, c))
         shape = (a.shape[-2], b.shape[-2]) if batch == 0 else (batch, a.shape[-2], b.shape[-2])
-        out = torch.empty(shape, dtype=dtype or (torch.bfloat16 if a.dtype == torch.bfloat16 else torch.float16),
-                          device=a.device)
+        with _allocating_on(stream, a.device):
+            out = torch.empty(shape, dtype=dtype or (torch.bfloat16 if a.dtype == torch.bfloat16 else torch.float16),
+                              device=a.device)
     args = make_args(a, b, c, out, sfa, sfb, block_k)
     if workspace is None:
-        workspace = workspace_for(args, out.device)
+        with _allocating_on(stream, out.device):
+            workspace = workspace_for(args, out.device)
     set_workspace(args, workspace)
     sl_gemm(args, stream)
     return out
@@ -347,15 +365,16 @@ def quantize(x, block_rows: int = 1, transposed: bool = False, direct: bool = Tr
     along x's rows, from the same pass: (q, s, qt, st), or (qt, st) without
     ``direct``.  Codes come with their columns padded with zeros to a multiple
     of 16, ready for ``gemm(..., block_k=128)``.  ``out``: the same tuple of
-    the caller's tensors."""
+    the caller's tensors.  ``stream`` as for ``gemm``."""
     if x.dim() not in (2, 3):
         raise ValueError("quantize takes a matrix or a batch of matrices")
     if not (direct or transposed):
         raise ValueError("nothing to compute: neither direct nor transposed")
     R, C = x.shape[-2:]
     if out is None:
-        out = (_codes_and_scales(x, R, C, block_rows) if direct else ()) + \
-              (_codes_and_scales(x, C, R, block_rows) if transposed else ())
+        with _allocating_on(stream, x.device):
+            out = (_codes_and_scales(x, R, C, block_rows) if direct else ()) + \
+                  (_codes_and_scales(x, C, R, block_rows) if transposed else ())
     elif len(out) != 2 * (direct + transposed):
         raise ValueError(f"out holds {len(out)} tensors, {2 * (direct + transposed)} are written")
     pair = lambda wanted, at: (_record(out[at]), _record(out[at + 1])) if wanted else (_ABSENT, _ABSENT)
@@ -370,10 +389,12 @@ def orthogonalize(x, out=None, steps: int = 5, coefficients=None, workspace=None
     ``coefficients``: (a, b, c) for every step or one triple per step (None:
     the library's).  ``workspace``: a device tensor of at least
     sl_orthogonalize_workspace_bytes, or None for a torch allocation.
-    Returns ``out`` (x's dtype, bf16 for float32, if None)."""
+    Returns ``out`` (x's dtype, bf16 for float32, if None).  ``stream`` as for
+    ``gemm``."""
     import torch
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16 if x.dtype == torch.float32 else x.dtype, device=x.device)
+        with _allocating_on(stream, x.device):
+            out = torch.empty(x.shape, dtype=torch.bfloat16 if x.dtype == torch.float32 else x.dtype, device=x.device)
     args = sl_orthogonalize_args()
     args.x, args.d, args.steps = tensor_desc(x), tensor_desc(out), steps
     if coefficients is not None:
@@ -386,7 +407,8 @@ def orthogonalize(x, out=None, steps: int = 5, coefficients=None, workspace=None
         args.coefficients = flat.ctypes.data_as(ctypes.POINTER(ctypes.c_float))
     if workspace is None:
         n = sl_orthogonalize_workspace_bytes(args)
-        workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+        with _allocating_on(stream, x.device):
+            workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
     set_workspace(args, workspace)
     sl_orthogonalize(args, stream)
     return out

@@ -666,3 +666,46 @@ def test_orthogonalize_small_norms(api, norm, dtype, shape, steps):
     want = orthogonalize64(x, steps)
     for b in range(2):
         assert float((d[b].double() - want[b]).norm() / want[b].norm()) <= (BF16_ROUNDING ** 2 + 2.9e-3 ** 2) ** 0.5
+
+
+# ---------------------------------------------------------------------------
+# the `stream` argument
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("op", ["orthogonalize", "gemm", "quantize"])
+def test_allocations_belong_to_the_stream(api, op, monkeypatch):
+    """A call on another stream than torch's current one takes what it
+    allocates from that stream's pool: while its kernels wait there, tensors
+    of the same size allocated on the current stream are other memory."""
+    import torch
+    x = gradient_like((300, 400), 161, "bfloat16")
+    a, b = (torch.randn(s, generator=gen(162), device="cuda").half() for s in ((64, 8192), (64, 8192)))
+    seen = []
+    keep = api.set_workspace
+
+    def record(args, workspace):
+        seen.append((workspace.data_ptr(), workspace.numel()))
+        keep(args, workspace)
+    monkeypatch.setattr(api, "set_workspace", record)
+    call = {"orthogonalize": lambda **kw: api.orthogonalize(x, **kw), "gemm": lambda **kw: api.gemm(a, b, **kw),
+            "quantize": lambda **kw: api.quantize(x, transposed=True, **kw)}[op]
+    want = call()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side.cuda_stream, 0):
+        seen.clear()
+        with torch.cuda.stream(side if stream else torch.cuda.default_stream()):
+            torch.cuda._sleep(20_000_000)  # some milliseconds; the call's kernels run after it
+        other = torch.cuda.Stream()
+        with torch.cuda.stream(other):
+            got = call(stream=stream)
+            assert (len(seen) > 0) == (op != "quantize")
+            outs = got if isinstance(got, tuple) else (got,)
+            taken = seen + [(t.data_ptr(), t.numel() * t.element_size()) for t in outs]
+            fill = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _, n in taken for _ in range(3)]
+            for f in fill:
+                for at, n in taken:
+                    assert f.data_ptr() + f.numel() <= at or at + n <= f.data_ptr()
+        torch.cuda.synchronize()
+        for g, w in zip(outs, want if isinstance(want, tuple) else (want,)):
+            assert same_bytes(g, w)
