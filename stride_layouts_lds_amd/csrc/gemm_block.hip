@@ -176,7 +176,10 @@ __global__ __launch_bounds__(WM* WN * 64, STAGES == 2 ? 2 : 1) void gemm_block_k
     for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
   const int32_t T = p.k_blocks;
-  constexpr int LOADS = decltype(la)::ITERS + decltype(lb)::ITERS + 2;
+  // Copies of a request.  Its two scale loads are not counted on: the compiler
+  // may move them among the copies, and a count that holds in any order leaves
+  // no more operations in flight than there are copies behind the K-tile.
+  constexpr int LOADS = decltype(la)::ITERS + decltype(lb)::ITERS;
   float sa_own[STAGES], sb_own[STAGES];
   auto request = [&](int32_t t, int d) {
     const int64_t at = t < T ? t : T - 1;
@@ -533,7 +536,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, 1) void gemm_block_stream_kernel
   const int32_t rows_b = (int32_t)(p.N - n0 < 16 * FN ? p.N - n0 : 16 * FN);
   const LoaderKVec<16 * FM, 64, 0, 1> la(p.a + batch * p.a_bs + m0 * p.a_rs, rows_a, p.a_rs, 1, p.K, 0, lane);
   const LoaderKVec<16 * FN, 64, 0, 1> lb(p.b + batch * p.b_bs + n0 * p.b_rs, rows_b, p.b_rs, 1, p.K, 0, lane);
-  constexpr int LOADS = decltype(la)::ITERS + decltype(lb)::ITERS + 2;
+  constexpr int LOADS = decltype(la)::ITERS + decltype(lb)::ITERS;  // copies of a request: as in gemm_block_kernel
   const float* sa_p = row_scale(p.sa + batch * p.sa_bs, m0 + lane, p.M, p.a_shift, p.sa_rs);
   const float* sb_p = row_scale(p.sb + batch * p.sb_bs, n0 + (lane & (16 * FN - 1)), p.N, p.b_shift, p.sb_rs);
   char* ring = smem + wave * (STAGES * STAGE);
