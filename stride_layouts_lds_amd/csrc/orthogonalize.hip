@@ -850,10 +850,12 @@ Way way_of(const OrthoParams& p) {
 // that amplify more (slope 3e4: 1e-2 of a result of rank 8) and fp16 results
 // (own rounding 2.1e-4) take pairs: 1e-7 to 1e-4.  8192 x 8192 takes 9.6 ms
 // with one plane and 23.5 with pairs, 1000 x 1000 145 and 195 us.  The Gram
-// matrix's way keeps x itself, exactly, in one plane unless it is fp32.
+// matrix's way keeps x itself: exactly in one plane, fp32 as a pair (whatever d
+// is: rounded to one plane, a 140 x 1000 x of rank 8 was off by
+// 3.3e-2).
 constexpr float kSingleSlope = 1024.f;
 int32_t x_planes(const OrthoParams& p, Way way) {
-  if (way == kGram) return p.x_type == OT_F32 && p.d_type == OT_F16 ? 2 : 1;
+  if (way == kGram) return p.x_type == OT_F32 ? 2 : 1;
   return p.d_type == OT_F16 || growth_of(p) > kGramGrowth || !(slope_of(p) <= kSingleSlope) ? 2 : 1;
 }
 

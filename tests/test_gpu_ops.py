@@ -709,3 +709,16 @@ def test_allocations_belong_to_the_stream(api, op, monkeypatch):
         torch.cuda.synchronize()
         for g, w in zip(outs, want if isinstance(want, tuple) else (want,)):
             assert same_bytes(g, w)
+
+
+@pytest.mark.parametrize("kind", ["rank64", "decades4"])
+@pytest.mark.parametrize("shape", [(140, 1000), (5000, 1100)])
+def test_orthogonalize_wide_float32(api, kind, shape):
+    """fp32 values with bf16 results, through the Gram matrix: pairs of fp16,
+    4e-4 next to the rounding."""
+    import torch
+    x = poor_rank(kind, shape, 181, "float32")
+    d = api.orthogonalize(x)
+    want = orthogonalize64(x)
+    assert d.dtype == torch.bfloat16
+    assert float((d.double() - want).norm() / want.norm()) <= (BF16_ROUNDING ** 2 + 4e-4 ** 2) ** 0.5
