@@ -275,16 +275,16 @@ sl_status sl_quantize(const sl_quantize_args* args, void* stream);
  * All products are on fp16 values times powers of two with sums in fp32, the
  * sum of squares is in 64 bits (up to 128 rows: a matrix's trace in 64 bits
  * over fp32 sums).  A matrix between products is a pair of fp16, a value and
- * what its rounding left: 5e-6 to 1.7e-4 (4096 x 4096) of the result, 2-norm,
- * on noise with a few strong directions, 4e-4 where singular values span five
- * decades.  Less is kept in one case, large bf16 results: with more than 128
- * rows and no more than four times as many columns, and steps whose a's
- * multiply to at most 512 and that amplify a difference of X by at most 1024
- * (five default steps do by 855, six by 3400), X is a pair, but as a factor of
- * a product, like G and b G + c G^2, one fp16.  That costs 1e-4 to 1.4e-3, 2.8e-3
- * where a few equal rows stand among zeros; a bf16 result's own rounding is
- * 1.7e-3.  An fp16 d, or coefficients that amplify more, take pairs.  In
- * directions where x has nothing, whatever a rounding leaves grows by a each
+ * what its rounding left (up to 128 rows X between cycles of steps: fp32), so
+ * that the result is as near as the same iteration in 32 bits, within small
+ * factors: 1e-6 to 2e-4 of it, 2-norm, for five default steps, noise to rank 1.
+ * Less is kept in one case, large bf16 results: with more than 128
+ * rows and no more than four times as many columns, and steps that amplify a
+ * difference of X by at most 1024 (five default steps do by 855, six by 3400),
+ * X is a pair, but as a factor of a product, like G and b G + c G^2, one fp16.
+ * That costs 1e-4 to 1.4e-3, 2.8e-3 where a few equal rows stand among zeros;
+ * a bf16 result's own rounding is 1.7e-3.  An fp16 d takes pairs throughout.
+ * In directions where x has nothing, whatever a rounding leaves grows by a each
  * step, in any precision.  The singular values of every iterate are to stay below
  * 2 (the default coefficients keep them below 1.3); beyond that d may hold
  * infinities or NaN.  An x that holds a NaN or an infinity gives a d of NaN; zero gives

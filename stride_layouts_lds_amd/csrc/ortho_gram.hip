@@ -2,25 +2,26 @@
 // (x taken with no more rows than columns), through their Gram matrix:
 //   G = X X^T,  P = a I + b G + c G^2,  Q <- P Q,  G <- P G P,  d = Q X.
 // Every iterate is a polynomial in G times the first X, so the steps run on
-// m x m matrices alone and x's n columns are read twice, whatever the number
-// of steps.  Three launches:
+// m x m matrices alone and x's n columns are read twice a cycle, as many steps
+// as amplify little (ortho_cycle: three default ones); between cycles X is kept
+// in fp32.  Three launches a cycle:
 //
 //   gram    a workgroup per range of columns: x's values times a power of two
 //           of its own (exact in fp16; fp32 values as a pair of fp16), their
 //           products on the fp16 matrix cores into fp32 partial sums.
 //   steps   one workgroup of 8 waves per matrix: sums the partials, takes
 //           |x| from G's trace in 64 bits, and runs all steps in LDS.
-//   apply   a workgroup per 128 columns: d = Q X.
+//   apply   a workgroup per 128 columns: d, or the next X, = Q X.
 //
 // Between products a matrix is a pair of fp16 planes, its value times a power
 // of two and what that rounding left, and a product of pairs is P0 Q0 + P0 Q1
-// + P1 Q0: squaring the singular values leaves no bits to spare.  Measured in
-// a simulation of these roundings: 5e-6 to 9e-5 (relative, 2-norm) on noise
-// with a few strong directions, 16 x 16 to 128 x 4096, and 4e-4 where singular
-// values span five decades; with one plane it is 1e-2 and more.
+// + P1 Q0: squaring the singular values leaves no bits to spare.  In a
+// simulation of these roundings and of fp32 sums, relative 2-norm, five
+// default steps in two cycles: noise 4e-6 to 7e-6, singular values over four
+// decades 9e-6, rank 8 2e-5, rank 1 1e-4; with one plane 1e-2 and more.
 //
-// P's products commute, so G and Q stay symmetric and every operand is read
-// along its rows.  Bound by latency: a step is three dependent rounds of
+// P's products commute, so G and Q stay symmetric, up to their rounding, and
+// every operand is read along its rows.  Bound by latency: a step is three dependent rounds of
 // products with two barriers each.  Measured at 96 x 128 (bf16, five steps):
 // gram 6, steps 27, apply 8 us; the steps take 0.9 us each at 32 rows, 2.5 at
 // 64, 5.2 at 96 and 10.5 at 128.
@@ -270,7 +271,7 @@ struct StepCoefficients {
 template <int MP>
 __global__ __launch_bounds__(64 * kStepWaves) void gram_steps_kernel(const OrthoParams p, const OrthoGramPlan pl, const float* parts,
                                                           const int32_t* exps, const StepCoefficients co, char* q_all,
-                                                          double* norms) {
+                                                          double* norms, bool kept) {
   typedef PairMatrix<MP> M;
   typedef StepBlock<MP> S;
   constexpr int R = MP / 16, NT = R * (R + 1) / 2, TPW = (NT + kStepWaves - 1) / kStepWaves;
@@ -317,7 +318,7 @@ __global__ __launch_bounds__(64 * kStepWaves) void gram_steps_kernel(const Ortho
 #pragma unroll
   for (int w = 0; w < kStepWaves; ++w) trace += traces[w];
   const double norm = ldexp(sqrt(trace), ex - kTop);
-  const double f = ex < 128 ? 1.0 / (norm + 1e-7) : __builtin_nan("");
+  const double f = ex < 128 ? (kept ? 1.0 : 1.0 / (norm + 1e-7)) : __builtin_nan("");  // kept: x is an iterate
   if (threadIdx.x == 0) norms[b] = f;
   const double fx = ldexp(f, ex - kTop);
   const float fg = (float)(fx * fx * (double)kGScale);
@@ -431,14 +432,15 @@ __global__ __launch_bounds__(64 * kStepWaves) void gram_steps_kernel(const Ortho
 }
 
 // ---------------------------------------------------------------------------
-// d = Q X on 128 columns: X's values go, exactly as in gram_kernel, into an
+// d = Q X on 128 columns (`keep`: into fp32 rows of `pitch` there, which x may
+// be: the workgroup reads its columns first): X's values go, exactly as in gram_kernel, into an
 // LDS tile of MP K-rows of 128, read by transposing reads; Q's fragments come
 // from memory; the result passes through LDS to be stored along d's
 // contiguous axis.
 // ---------------------------------------------------------------------------
-template <int T, int MP>
+template <int T, int MP, bool KEEP>
 __global__ __launch_bounds__(256) void gram_apply_kernel(const OrthoParams p, const char* q_all, const double* norms,
-                                                         uint32_t tiles_n) {
+                                                         uint32_t tiles_n, float* keep, int64_t pitch) {
   typedef PairMatrix<MP> M;
   constexpr int PX = T == OT_F32 ? 2 : 1, PPT = MP * 16 / 256;
   constexpr int WM = MP == 32 ? 1 : 2, WN = 4 / WM, FM = MP / 16 / WM, FN = 8 / WN;
@@ -504,8 +506,21 @@ __global__ __launch_bounds__(256) void gram_apply_kernel(const OrthoParams p, co
       }
     }
   }
-  __syncthreads();
   const float f = (float)(ldexp(norms[b], ex - kTop) * (1.0 / kPScale));
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int32_t m = m0 + 16 * i + (lane & 15);
+        const int64_t n = j0 + n0 + 16 * j + 4 * (lane >> 4);
+        if (m < p.m && n < p.n)  // (the row's last quad ends inside the pitch)
+          *(floatx4*)(keep + (b * p.m + m) * pitch + n) =
+              floatx4{acc[i][j][0] * f, acc[i][j][1] * f, acc[i][j][2] * f, acc[i][j][3] * f};
+      }
+    return;
+  }
+  __syncthreads();
   uint16_t* D = (uint16_t*)smem;
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -545,8 +560,9 @@ __global__ __launch_bounds__(256) void gram_apply_kernel(const OrthoParams p, co
 }
 
 struct GramPlaces {
-  size_t exps, norms, q, total;  // byte offsets behind the partial sums
+  size_t exps, norms, q, x, total;  // byte offsets behind the partial sums
 };
+constexpr int64_t kept_pitch(int64_t n) { return (n + 3) / 4 * 4; }
 GramPlaces gram_places(const OrthoParams& p, const OrthoGramPlan& pl) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   const size_t r = pl.rows / 16, sums = (size_t)p.batch * pl.splits;
@@ -554,33 +570,40 @@ GramPlaces gram_places(const OrthoParams& p, const OrthoGramPlan& pl) {
   g.exps = up(sums * (r * (r + 1) / 2) * 1024);
   g.norms = g.exps + up(sums * 4);
   g.q = g.norms + up((size_t)p.batch * 8);
-  g.total = g.q + (size_t)p.batch * pl.rows * (4 * pl.rows + 32);
+  g.x = g.q + up((size_t)p.batch * pl.rows * (4 * pl.rows + 32));
+  g.total = g.x + (ortho_cycle(p, 0) < p.steps ? (size_t)p.batch * p.m * kept_pitch(p.n) * 4 : 0);
   return g;
 }
 
+// one cycle of p's steps; `kept`: x is what the cycle before left, `keep`: so is
+// what this one makes
 template <int T, int MP>
-hipError_t go(const OrthoParams& p, const OrthoGramPlan& pl, hipStream_t s) {
-  const GramPlaces g = gram_places(p, pl);
+hipError_t go(const OrthoParams& p, const OrthoGramPlan& pl, const GramPlaces& g, bool kept, bool keep, hipStream_t s) {
   float* parts = (float*)p.ws;
   int32_t* exps = (int32_t*)(p.ws + g.exps);
   double* norms = (double*)(p.ws + g.norms);
   char* q = p.ws + g.q;
+  float* x = (float*)(p.ws + g.x);
   StepCoefficients co{};
   for (int32_t i = 0; i < 3 * p.steps; ++i) co.v[i] = p.coefficients[i];
   const uint32_t tiles_n = (uint32_t)((p.n + 127) / 128);
+  const dim3 columns(tiles_n * p.batch);
   hipLaunchKernelGGL((gram_kernel<T, MP>), dim3((uint32_t)(p.batch * pl.splits)), dim3(512), 0, s, p, pl, parts, exps);
-  hipLaunchKernelGGL((gram_steps_kernel<MP>), dim3(p.batch), dim3(64 * kStepWaves), 0, s, p, pl, parts, exps, co, q, norms);
-  hipLaunchKernelGGL((gram_apply_kernel<T, MP>), dim3(tiles_n * p.batch), dim3(256), 0, s, p, q, norms, tiles_n);
+  hipLaunchKernelGGL((gram_steps_kernel<MP>), dim3(p.batch), dim3(64 * kStepWaves), 0, s, p, pl, parts, exps, co, q, norms, kept);
+  if (keep)
+    hipLaunchKernelGGL((gram_apply_kernel<T, MP, true>), columns, dim3(256), 0, s, p, q, norms, tiles_n, x, kept_pitch(p.n));
+  else
+    hipLaunchKernelGGL((gram_apply_kernel<T, MP, false>), columns, dim3(256), 0, s, p, q, norms, tiles_n, x, kept_pitch(p.n));
   return hipGetLastError();
 }
 
 template <int T>
-hipError_t by_rows(const OrthoParams& p, const OrthoGramPlan& pl, hipStream_t s) {
+hipError_t by_rows(const OrthoParams& p, const OrthoGramPlan& pl, const GramPlaces& g, bool kept, bool keep, hipStream_t s) {
   switch (pl.rows) {
-    case 32: return go<T, 32>(p, pl, s);
-    case 64: return go<T, 64>(p, pl, s);
-    case 96: return go<T, 96>(p, pl, s);
-    case 128: return go<T, 128>(p, pl, s);
+    case 32: return go<T, 32>(p, pl, g, kept, keep, s);
+    case 64: return go<T, 64>(p, pl, g, kept, keep, s);
+    case 96: return go<T, 96>(p, pl, g, kept, keep, s);
+    case 128: return go<T, 128>(p, pl, g, kept, keep, s);
     default: return hipErrorInvalidValue;
   }
 }
@@ -606,11 +629,25 @@ size_t ortho_gram_workspace(const OrthoParams& p) { return gram_places(p, ortho_
 
 hipError_t launch_ortho_gram(const OrthoParams& p, hipStream_t s) {
   const OrthoGramPlan pl = ortho_gram_plan(p.m, p.n);
-  switch (p.x_type) {
-    case OT_F16: return by_rows<OT_F16>(p, pl, s);
-    case OT_BF16: return by_rows<OT_BF16>(p, pl, s);
-    default: return by_rows<OT_F32>(p, pl, s);
+  const GramPlaces g = gram_places(p, pl);
+  OrthoParams c = p;
+  for (int32_t k = 0; k < p.steps; k += c.steps) {
+    c.coefficients = p.coefficients + 3 * k;
+    c.steps = ortho_cycle(p, k);
+    const bool kept = k > 0, keep = k + c.steps < p.steps;
+    if (kept) {
+      c.x = p.ws + g.x, c.x_type = OT_F32;
+      c.x_rs = kept_pitch(p.n), c.x_cs = 1, c.x_bs = p.m * c.x_rs;
+    }
+    hipError_t e;
+    switch (c.x_type) {
+      case OT_F16: e = by_rows<OT_F16>(c, pl, g, kept, keep, s); break;
+      case OT_BF16: e = by_rows<OT_BF16>(c, pl, g, kept, keep, s); break;
+      default: e = by_rows<OT_F32>(c, pl, g, kept, keep, s); break;
+    }
+    if (e != hipSuccess) return e;
   }
+  return hipSuccess;
 }
 
 }  // namespace sl

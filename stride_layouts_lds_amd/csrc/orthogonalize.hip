@@ -2,16 +2,17 @@
 //   X <- x / (|x|_F + 1e-7), then per step
 //   G = X X^T,  B = b G + c G^2,  X <- a X + B X,
 // x taken with no more rows than columns (a tall one transposed by its
-// strides).  Three ways, chosen by through_gram() below:
+// strides).  Three ways, chosen by way_of() below:
 //
-//   up to 128 rows     ortho_gram.hip: three launches
+//   up to 128 rows     ortho_gram.hip: three launches a cycle of steps
 //   Gram matrix        the same iteration on m x m matrices alone (G, P = a I
-//                      + b G + c G^2, Q <- P Q, G <- P G P, d = Q x), every one
-//                      a pair of fp16 planes; x times a power of two
-//   direct             the formula above; every matrix a pair of fp16 planes,
-//                      or, for bf16 results and steps that amplify little, X
-//                      a pair of which the products read the first plane, G
-//                      and B one plane
+//                      + b G + c G^2, Q <- P Q, G <- P G P, X <- Q X), every one
+//                      a pair of fp16 planes; x times a power of two.  In
+//                      cycles of steps: X <- Q X and a new G after as many as
+//                      amplify little
+//   direct             the formula above, for bf16 results and steps that
+//                      amplify little: X a pair of which the products read
+//                      the first plane, G and B one plane
 //
 // All on the fp16 matrix cores with fp32 sums.  A plane holds values times a
 // power of two (2^10 for X, G and B of the direct way, 2^12 and 2^6 for the
@@ -79,21 +80,23 @@ __device__ __forceinline__ int64_t plane_at(int64_t row, int64_t cols, int64_t c
   return PLANES == 2 ? row * 2 * cols + (col >> 5) * 64 + (col & 31) : row * cols + col;
 }
 
-// What the products multiply by, one of each for every matrix.
+// What products multiply by, one of each for every matrix: the Gram matrix of
+// x's planes to make G's, Q's planes times x's to make d or the planes that X is
+// kept in, and the first two of those.  (Direct way: the first two.)
+enum OrthoScale : int32_t { kScaleGram, kScaleResult, kScaleKeep, kScaleGramKept, kScaleResultKept, kScaleCount };
 struct OrthoScales {
-  float gram;   // of X's planes' Gram matrix, to make G's plane
-  float apply;  // of Q's plane times x's, or of the direct way's last step, to make d
+  float v[kScaleCount];
 };
 
 // The planes that the products read: m x n and n x m, zero to the padded
 // sizes.
 // EXACT: x times the power of two that brings |x| to 2^14 (to 2^15): exact in
-// fp16 but for what lies 2^-38 below |x|; the scales follow, and the
-// transpose is a pair in any case (its second plane zero).  Else 2^(10 + e)
-// X_0, X_0 = x / (|x| + 1e-7), rounded, and what the rounding left: the second
-// plane, or, with one plane, XL (m x n).  e is zero but where |x| lies so far
-// below 1e-7 that no iterate passes 1 (|X_0| below 2^knee): 2^10 X would fall
-// out of fp16's range there, and 2^(10 + e) X stays below 2^15 throughout.
+// fp16 but for what lies 2^-38 below |x|; the transpose is a pair in any case
+// (its second plane zero).  Else 2^(10 + e) X_0, X_0 = x / (|x| + 1e-7),
+// rounded, and in XL (m x n) what the rounding left.  e, for an X between
+// steps, is zero but where |x| lies so far below 1e-7 that no iterate passes 1
+// (|X_0| below 2^knee): 2^10 X would fall out of fp16's range there, and
+// 2^(10 + e) X stays below 2^15 throughout.
 template <int T, int PLANES, bool EXACT>
 __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, const double* parts, uint16_t* X,
                                                           uint16_t* XT, uint16_t* XL, OrthoScales* scales, int32_t tiles_m,
@@ -107,19 +110,24 @@ __global__ __launch_bounds__(256) void ortho_start_kernel(const OrthoParams p, c
   const int64_t mp = 64 * (int64_t)tiles_m, np = 64 * (int64_t)tiles_n;
   const double sum = block_sum((int32_t)threadIdx.x < sums ? parts[b * kNormParts + threadIdx.x] : 0.0, lds);
   const double norm = sqrt(sum), inv = 1.0 / (norm + 1e-7);
+  const double x0 = norm * inv;
+  const int32_t k = x0 > 0.0 ? ilogb(x0) + 1 : 0;                        // |X_0| < 2^k
+  const int32_t e = x0 > 0.0 && k <= knee ? min(5 + knee - k, 100) : 0;  // (NaN: 0)
+  const bool writes_scales = tm == 0 && tn == 0 && threadIdx.x == 0;
   double f;
   if constexpr (!EXACT) {
-    const double x0 = norm * inv;
-    const int32_t k = x0 > 0.0 ? ilogb(x0) + 1 : 0;                           // |X_0| < 2^k
-    const int32_t e = x0 > 0.0 && k <= knee ? min(5 + knee - k, 100) : 0;  // (NaN: 0)
     f = ldexp(inv, 10 + e);
-    if (tm == 0 && tn == 0 && threadIdx.x == 0) scales[b] = OrthoScales{ldexpf(1.f, -2 * e), ldexpf(1.f, -e)};
+    if (writes_scales) scales[b].v[kScaleGram] = ldexpf(1.f, -2 * e), scales[b].v[kScaleResult] = ldexpf(1.f, -e);
   } else {
     // infinite or NaN norms make every scale NaN
-    const int32_t e = norm > 0.0 && norm < __builtin_inf() ? ilogb(norm) : 0;
-    f = ldexp(1.0, 14 - e);
+    const int32_t en = norm > 0.0 && norm < __builtin_inf() ? ilogb(norm) : 0;
+    f = ldexp(1.0, 14 - en);
     const double fx = norm < __builtin_inf() ? inv / f : __builtin_nan("");
-    if (tm == 0 && tn == 0 && threadIdx.x == 0) scales[b] = OrthoScales{(float)(fx * fx * 4096.0), (float)(fx / 64.0)};
+    if (writes_scales) {
+      scales[b].v[kScaleGram] = (float)(fx * fx * 4096.0), scales[b].v[kScaleResult] = (float)(fx / 64.0);
+      scales[b].v[kScaleKeep] = (float)ldexp(fx / 64.0, 10 + e);
+      scales[b].v[kScaleGramKept] = ldexpf(1.f, 12 - 2 * (10 + e)), scales[b].v[kScaleResultKept] = ldexpf(1.f, -6 - (10 + e));
+    }
   }
   const int64_t i0 = 64 * (int64_t)tm, j0 = 64 * (int64_t)tn;
   const bool along_rows = p.x_rs == 1 && p.x_cs != 1;
@@ -179,7 +187,7 @@ struct OrthoGemm {
   int32_t m, n, k;               // padded: multiples of 64
   float alpha[2], beta, diag;    // with scales: alpha and beta times one of the matrix's
   const OrthoScales* scales;     // or NULL
-  int32_t scale_apply;           // which of them
+  int32_t scale;                 // which of them
   int32_t sym;
   int32_t products;              // 1 or 2
   int32_t tiles_m, tiles_n, batch;
@@ -237,7 +245,7 @@ __device__ __forceinline__ OrthoTile ortho_tile(const OrthoGemm& g) {
   o.alpha = o.product ? g.alpha[1] : g.alpha[0];
   o.beta = g.beta;
   if (g.scales) {
-    const float s = g.scale_apply ? g.scales[o.batch].apply : g.scales[o.batch].gram;
+    const float s = g.scales[o.batch].v[g.scale];
     o.alpha *= s, o.beta *= s;
   }
   return o;
@@ -748,8 +756,11 @@ hipError_t run_gemm(OrthoGemm g, hipStream_t s) {
   return hipGetLastError();
 }
 
+// planes that hold x on the Gram matrix's way
+constexpr int x_planes(int type) { return type == OT_F32 ? 2 : 1; }
+
 template <int T>
-hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, uint16_t* XT, uint16_t* XL,
+hipError_t start(const OrthoParams& p, bool exact, double* parts, uint16_t* X, uint16_t* XT, uint16_t* XL,
                  OrthoScales* scales, int32_t knee, hipStream_t s) {
   const int32_t tm = (int32_t)(pad64(p.m) / 64), tn = (int32_t)(pad64(p.n) / 64);
   const int64_t length = p.x_rs == 1 && p.x_cs != 1 ? p.m : p.n;
@@ -760,33 +771,23 @@ hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts
   const int32_t sums = (int32_t)(want < kNormParts ? want : kNormParts);
   hipLaunchKernelGGL(ortho_norm_kernel<T>, dim3(sums, p.batch), dim3(64 * kNormWaves), 0, s, p, parts, across);
   const dim3 grid((uint32_t)((int64_t)p.batch * tm * tn)), block(256);
-  if (exact && planes == 2)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 2, true>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums, knee);
-  else if (exact)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 1, true>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums, knee);
-  else if (planes == 2)
-    hipLaunchKernelGGL((ortho_start_kernel<T, 2, false>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums, knee);
+  if (exact)
+    hipLaunchKernelGGL((ortho_start_kernel<T, x_planes(T), true>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums,
+                       knee);
   else
     hipLaunchKernelGGL((ortho_start_kernel<T, 1, false>), grid, block, 0, s, p, parts, X, XT, XL, scales, tm, tn, sums, knee);
   return hipGetLastError();
 }
-hipError_t start(const OrthoParams& p, int32_t planes, bool exact, double* parts, uint16_t* X, uint16_t* XT, uint16_t* XL,
+hipError_t start(const OrthoParams& p, bool exact, double* parts, uint16_t* X, uint16_t* XT, uint16_t* XL,
                  OrthoScales* scales, int32_t knee, hipStream_t s) {
   switch (p.x_type) {
-    case OT_F16: return start<OT_F16>(p, planes, exact, parts, X, XT, XL, scales, knee, s);
-    case OT_BF16: return start<OT_BF16>(p, planes, exact, parts, X, XT, XL, scales, knee, s);
-    default: return start<OT_F32>(p, planes, exact, parts, X, XT, XL, scales, knee, s);
+    case OT_F16: return start<OT_F16>(p, exact, parts, X, XT, XL, scales, knee, s);
+    case OT_BF16: return start<OT_BF16>(p, exact, parts, X, XT, XL, scales, knee, s);
+    default: return start<OT_F32>(p, exact, parts, X, XT, XL, scales, knee, s);
   }
 }
 
 enum Way { kSmallGram, kGram, kDirect };
-
-// How much the steps amplify where x has (almost) nothing: by a each.
-float growth_of(const OrthoParams& p) {
-  float growth = 1.f;
-  for (int32_t t = 0; t < p.steps; ++t) growth *= fmaxf(1.f, fabsf(p.coefficients[3 * t]));
-  return growth;
-}
 
 // How much the steps amplify anywhere: a rounding in X grows in a step by at
 // most the largest slope of s -> a s + b s^3 + c s^5 over the singular values
@@ -828,55 +829,49 @@ int32_t knee_of(const OrthoParams& p) {
   return -160;
 }
 
-// The Gram matrix's way multiplies pairs, 54 m^3 + 3 m^2 n and up to 2 m^2 n
-// more multiply-adds for five steps, but for small sizes where launches
-// count; the direct one 15 m^2 n + 5 m^3 on single planes, three times that
-// on pairs.
-Way way_of(const OrthoParams& p) {
-  if (growth_of(p) > kGramGrowth) return kDirect;
-  if (p.m <= kGramRows) return kSmallGram;
-  return p.d_type == OT_F16 || p.n > 4 * p.m ? kGram : kDirect;
-}
-
-// X's planes in the products of the direct way.  One for bf16 results and
-// steps that amplify up to kSingleSlope times: X is a pair all the same and a
-// X comes from both planes; what is rounded to fp16 is X as a factor, G and B.
-// (X as one plane was wrong: what its rounding leaves in directions where x
-// has nothing grows by a each step, 4e-2 of a result of rank 8.)  64-bit
-// simulation of these roundings, relative 2-norm, 256 x 256 to 1000 x 1000,
-// five default steps: noise 1.1e-3 to 1.4e-3, rank 1 to 64 1e-4 to 1e-3,
-// singular values over two or four decades 7e-4 to 1.2e-3, a few equal rows
-// among zeros up to 2.8e-3; a bf16 result's own rounding is 1.7e-3.  Steps
-// that amplify more (slope 3e4: 1e-2 of a result of rank 8) and fp16 results
-// (own rounding 2.1e-4) take pairs: 1e-7 to 1e-4.  8192 x 8192 takes 9.6 ms
-// with one plane and 23.5 with pairs, 1000 x 1000 145 and 195 us.  The Gram
-// matrix's way keeps x itself: exactly in one plane, fp32 as a pair (whatever d
-// is: rounded to one plane, a 140 x 1000 x of rank 8 was off by
-// 3.3e-2).
+// Up to 128 rows: the Gram matrix's way in few launches.  Otherwise bf16
+// results whose steps amplify a rounding of X by no more than kSingleSlope go
+// the direct way, 15 m^2 n + 5 m^3 operations for five steps, where they have no
+// more than four times as many columns as rows; the Gram matrix's multiplies
+// pairs, 42 m^3 + 14 m^2 n in two cycles, and is the more accurate one.  Direct
+// and Gram: 1000 x 1000 147 and 213 us, 1024 x 4096 241 and 282, x 8192 370 and
+// 363, x 16384 631 and 498, 8192 x 8192 9.4 and 21.6 ms.
+//
+// The direct way keeps X as a pair, and a X comes from both planes; what is
+// rounded to fp16 is X as a factor, G and B.  (X as one plane was wrong: what
+// its rounding leaves in directions where x has nothing grows by a each step,
+// 4e-2 of a result of rank 8.)  64-bit simulation of these roundings,
+// relative 2-norm, 256 x 256 to 1000 x 1000, five default steps: noise 1.1e-3
+// to 1.4e-3, rank 1 to 64 1e-4 to 1e-3, singular values over two or four decades
+// 7e-4 to 1.2e-3, a few equal rows among zeros up to 2.8e-3; a bf16 result's own
+// rounding is 1.7e-3.  Steps that amplify more (slope 3e4: 1e-2 of a result of
+// rank 8) and fp16 results (own rounding 2.1e-4) take the pairs.
 constexpr float kSingleSlope = 1024.f;
-int32_t x_planes(const OrthoParams& p, Way way) {
-  if (way == kGram) return p.x_type == OT_F32 ? 2 : 1;
-  return p.d_type == OT_F16 || growth_of(p) > kGramGrowth || !(slope_of(p) <= kSingleSlope) ? 2 : 1;
+constexpr int64_t kDirectColumns = 4;  // times the rows
+Way way_of(const OrthoParams& p) {
+  if (p.m <= kGramRows) return kSmallGram;
+  // (not <= kSingleSlope: infinite or NaN as well)
+  return p.d_type == OT_F16 || p.n > kDirectColumns * p.m || !(slope_of(p) <= kSingleSlope) ? kGram : kDirect;
 }
 
 struct Places {
   size_t scales, x, xt[2], low, mm[5], total;  // byte offsets behind the partial sums
 };
 Places places(const OrthoParams& p, Way way) {
-  const int32_t xp = x_planes(p, way), mp = way == kGram ? 2 : xp;
-  const size_t mn = (size_t)p.batch * pad64(p.m) * pad64(p.n) * 2 * xp, mm = (size_t)p.batch * pad64(p.m) * pad64(p.m) * 2 * mp;
+  const bool gram = way == kGram, cycles = gram && ortho_cycle(p, 0) < p.steps;
+  const size_t plane = (size_t)p.batch * pad64(p.m) * pad64(p.n) * 2, mm = (size_t)p.batch * pad64(p.m) * pad64(p.m) * 2;
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   Places q;
   q.scales = up((size_t)p.batch * kNormParts * 8);
   q.x = q.scales + up((size_t)p.batch * sizeof(OrthoScales));
-  q.xt[0] = q.x + mn;
-  const size_t xt = way == kGram ? mn / xp * 2 : mn;  // the Gram way's is a pair
-  q.xt[1] = way == kGram ? q.xt[0] : q.xt[0] + xt;
-  q.low = q.xt[1] + xt;
-  size_t at = q.low + (way == kDirect && xp == 1 ? mn : 0);
+  // Gram: X a pair from the second cycle on, its transpose in any case
+  q.xt[0] = q.x + plane * (cycles ? 2 : gram ? x_planes(p.x_type) : 1);
+  q.xt[1] = q.xt[0] + plane * (gram ? 2 : 1);
+  q.low = q.xt[1] + plane * (gram ? (cycles ? 2 : 0) : 1);
+  size_t at = q.low + (gram ? 0 : plane);
   for (int i = 0; i < 5; ++i) {
     q.mm[i] = at;
-    if (way == kGram || i < 2) at += mm;
+    if (gram || i < 2) at += mm * (gram ? 2 : 1);
   }
   q.total = at;
   return q;
@@ -887,18 +882,17 @@ void to_result(const OrthoParams& p, OrthoGemm* g) {
   g->d_bs = p.d_bs, g->d_rs = p.d_rs, g->d_cs = p.d_cs;
 }
 
-template <int PL>
 hipError_t direct(const OrthoParams& p, hipStream_t s) {
   const Places q = places(p, kDirect);
   uint16_t* X = (uint16_t*)(p.ws + q.x);
   uint16_t* XT[2] = {(uint16_t*)(p.ws + q.xt[0]), (uint16_t*)(p.ws + q.xt[1])};
+  uint16_t* XL = (uint16_t*)(p.ws + q.low);
   uint16_t *G = (uint16_t*)(p.ws + q.mm[0]), *B = (uint16_t*)(p.ws + q.mm[1]);
   OrthoScales* scales = (OrthoScales*)(p.ws + q.scales);
-  uint16_t* XL = PL == 1 ? (uint16_t*)(p.ws + q.low) : nullptr;
   const int32_t mp = (int32_t)pad64(p.m), np = (int32_t)pad64(p.n);
-  const int64_t mn = (int64_t)mp * np * PL, mm = (int64_t)mp * mp * PL;
+  const int64_t mn = (int64_t)mp * np, mm = (int64_t)mp * mp;
   constexpr float kDown = 0x1p-10f;  // what a stored value times it stands for
-  hipError_t e = start(p, PL, false, (double*)p.ws, X, XT[0], XL, scales, knee_of(p), s);
+  hipError_t e = start(p, false, (double*)p.ws, X, XT[0], XL, scales, knee_of(p), s);
   for (int32_t k = 0; k < p.steps && e == hipSuccess; ++k) {
     const float a = p.coefficients[3 * k], b = p.coefficients[3 * k + 1], c = p.coefficients[3 * k + 2];
     // stored values carry 2^10, products of two 2^20
@@ -906,21 +900,21 @@ hipError_t direct(const OrthoParams& p, hipStream_t s) {
     g.batch = p.batch, g.products = 1;
     g.P = g.Q[0] = X, g.P_bs = g.Q_bs = mn;
     g.m = g.n = mp, g.k = np, g.alpha[0] = kDown, g.sym = 1;
-    g.O[0] = G, g.O_bs = mm, g.scales = scales;
-    if ((e = run_gemm<PL == 2 ? kPairs : kPlain, PL>(g, s)) != hipSuccess) break;
+    g.O[0] = G, g.O_bs = mm, g.scales = scales, g.scale = kScaleGram;
+    if ((e = run_gemm<kPlain, 1>(g, s)) != hipSuccess) break;
     g.scales = nullptr;
     g.P = g.Q[0] = g.E = G, g.P_bs = g.Q_bs = g.E_bs = mm;
     g.k = mp, g.alpha[0] = c * kDown, g.beta = b;
     g.O[0] = B;
-    if ((e = run_gemm<PL == 2 ? kPairs : kPlain, PL>(g, s)) != hipSuccess) break;
+    if ((e = run_gemm<kPlain, 1>(g, s)) != hipSuccess) break;
     g.P = B, g.Q[0] = XT[k & 1], g.E = X, g.Q_bs = g.E_bs = mn;
     g.n = np, g.alpha[0] = kDown, g.beta = a, g.sym = 0;
     g.O[0] = X, g.OT = XT[(k + 1) & 1], g.low = XL, g.O_bs = mn;
     if (k + 1 == p.steps) {
-      g.alpha[0] *= kDown, g.beta *= kDown, g.scales = scales, g.scale_apply = 1;
+      g.alpha[0] *= kDown, g.beta *= kDown, g.scales = scales, g.scale = kScaleResult;
       to_result(p, &g);
     }
-    e = run_gemm<PL == 2 ? kPairs : kPlain, PL>(g, s);
+    e = run_gemm<kPlain, 1>(g, s);
   }
   return e;
 }
@@ -930,55 +924,87 @@ template <int PX>
 hipError_t gram(const OrthoParams& p, hipStream_t s) {
   const Places q = places(p, kGram);
   OrthoScales* scales = (OrthoScales*)(p.ws + q.scales);
-  uint16_t *X = (uint16_t*)(p.ws + q.x), *XT = (uint16_t*)(p.ws + q.xt[0]);
+  uint16_t *X = (uint16_t*)(p.ws + q.x), *XT[2] = {(uint16_t*)(p.ws + q.xt[0]), (uint16_t*)(p.ws + q.xt[1])};
   uint16_t* M[5];
   for (int i = 0; i < 5; ++i) M[i] = (uint16_t*)(p.ws + q.mm[i]);
-  uint16_t *G = M[0], *P = M[1], *H = M[2], *Q = nullptr;
+  uint16_t *G = M[0], *P = M[1], *H = M[2];
   const int32_t mp = (int32_t)pad64(p.m), np = (int32_t)pad64(p.n);
-  const int64_t mn = (int64_t)mp * np * PX, mm = (int64_t)mp * mp * 2;
+  const int64_t mn = (int64_t)mp * np, mm = (int64_t)mp * mp * 2;
   constexpr float kG = 0x1p12f, kP = 0x1p6f;  // what G's planes, and those of P, H and Q, are multiplied by
-  hipError_t e = start(p, PX, true, (double*)p.ws, X, XT, nullptr, scales, 0, s);
+  hipError_t e = start(p, true, (double*)p.ws, X, XT[0], nullptr, scales, knee_of(p), s);
   if (e != hipSuccess) return e;
-  OrthoGemm g{};
-  g.batch = p.batch, g.products = 1, g.sym = 1;
-  g.P = g.Q[0] = X, g.P_bs = g.Q_bs = mn;
-  g.m = g.n = mp, g.k = np, g.alpha[0] = 1.f, g.scales = scales;
-  g.O[0] = G, g.O_bs = mm;
-  if ((e = run_gemm<PX == 2 ? kPairs : kPlain, 2>(g, s)) != hipSuccess) return e;
-  g.scales = nullptr, g.P_bs = g.Q_bs = g.E_bs = mm, g.k = mp;
-  for (int32_t k = 0; k < p.steps; ++k) {
-    const float a = p.coefficients[3 * k], b = p.coefficients[3 * k + 1], c = p.coefficients[3 * k + 2];
-    const bool last = k + 1 == p.steps;
-    // P = a I + b G + c G^2; the first is Q as well
-    uint16_t* Pk = k == 0 ? M[3] : P;
-    g.P = g.Q[0] = g.E = G, g.alpha[0] = c * (kP / (kG * kG)), g.beta = b * (kP / kG), g.diag = a * kP;
-    g.O[0] = Pk;
-    if ((e = run_gemm<kPairs, 2>(g, s)) != hipSuccess) return e;
-    g.E = nullptr, g.diag = 0.f;
-    uint16_t* next = Q == M[3] ? M[4] : M[3];
-    g.P = Pk;
-    g.products = (last ? 0 : 1) + (k > 0 ? 1 : 0);
-    int i = 0;
-    if (!last) g.Q[i] = G, g.O[i] = H, g.alpha[i] = 1.f / kG, ++i;
-    if (k > 0) g.Q[i] = Q, g.O[i] = next, g.alpha[i] = 1.f / kP;
-    if (g.products > 0 && (e = run_gemm<kPairs, 2>(g, s)) != hipSuccess) return e;
-    g.products = 1;
-    Q = k > 0 ? next : M[3];
-    if (last) break;
-    g.P = H, g.Q[0] = Pk, g.O[0] = G, g.alpha[0] = kG / (kP * kP);
-    if ((e = run_gemm<kPairs, 2>(g, s)) != hipSuccess) return e;
+  for (int32_t k = 0, cycle = 0; k < p.steps; ++cycle) {
+    const int32_t end = k + ortho_cycle(p, k);
+    const bool kept = cycle > 0;  // X is a pair that the cycle before made
+    OrthoGemm g{};
+    g.batch = p.batch, g.products = 1, g.sym = 1;
+    g.P = g.Q[0] = X, g.P_bs = g.Q_bs = mn * (kept ? 2 : PX);
+    g.m = g.n = mp, g.k = np, g.alpha[0] = 1.f, g.scales = scales, g.scale = kept ? kScaleGramKept : kScaleGram;
+    g.O[0] = G, g.O_bs = mm;
+    e = kept || PX == 2 ? run_gemm<kPairs, 2>(g, s) : run_gemm<kPlain, 2>(g, s);
+    if (e != hipSuccess) return e;
+    g.scales = nullptr, g.P_bs = g.Q_bs = g.E_bs = mm, g.k = mp;
+    uint16_t* Q = nullptr;
+    for (; k < end; ++k) {
+      const float a = p.coefficients[3 * k], b = p.coefficients[3 * k + 1], c = p.coefficients[3 * k + 2];
+      const bool first = Q == nullptr, last = k + 1 == end;
+      // P = a I + b G + c G^2; the cycle's first is Q as well
+      uint16_t* Pk = first ? M[3] : P;
+      g.P = g.Q[0] = g.E = G, g.alpha[0] = c * (kP / (kG * kG)), g.beta = b * (kP / kG), g.diag = a * kP;
+      g.O[0] = Pk;
+      if ((e = run_gemm<kPairs, 2>(g, s)) != hipSuccess) return e;
+      g.E = nullptr, g.diag = 0.f;
+      uint16_t* next = Q == M[3] ? M[4] : M[3];
+      g.P = Pk;
+      g.products = (last ? 0 : 1) + (first ? 0 : 1);
+      int i = 0;
+      if (!last) g.Q[i] = G, g.O[i] = H, g.alpha[i] = 1.f / kG, ++i;
+      if (!first) g.Q[i] = Q, g.O[i] = next, g.alpha[i] = 1.f / kP;
+      if (g.products > 0 && (e = run_gemm<kPairs, 2>(g, s)) != hipSuccess) return e;
+      g.products = 1;
+      Q = first ? M[3] : next;
+      if (last) continue;
+      g.P = H, g.Q[0] = Pk, g.O[0] = G, g.alpha[0] = kG / (kP * kP);
+      if ((e = run_gemm<kPairs, 2>(g, s)) != hipSuccess) return e;
+    }
+    // the transpose of Q X: X^T Q, Q being symmetric, so that the pair is the
+    // second operand
+    g.P = XT[cycle & 1], g.P_bs = 2 * mn, g.Q[0] = Q, g.Q_bs = mm;
+    g.m = np, g.sym = 0, g.alpha[0] = 1.f, g.scales = scales;
+    if (k == p.steps) {
+      g.scale = kept ? kScaleResultKept : kScaleResult;
+      to_result(p, &g);
+      std::swap(g.rows, g.cols), std::swap(g.d_rs, g.d_cs);
+      return kept || PX == 2 ? run_gemm<kPairs, 1>(g, s) : run_gemm<kPlainByPair, 1>(g, s);
+    }
+    g.O[0] = XT[(cycle + 1) & 1], g.OT = X, g.O_bs = 2 * mn;
+    if (kept) g.scales = nullptr, g.alpha[0] = 1.f / kP;
+    else g.scale = kScaleKeep;
+    e = kept || PX == 2 ? run_gemm<kPairs, 2>(g, s) : run_gemm<kPlainByPair, 2>(g, s);
+    if (e != hipSuccess) return e;
   }
-  // d's transpose: x^T Q, Q being symmetric, so that the pair is the second
-  // operand
-  g.P = XT, g.P_bs = 2 * (int64_t)mp * np, g.Q[0] = Q, g.Q_bs = mm;
-  g.m = np, g.sym = 0, g.alpha[0] = 1.f;
-  g.scales = scales, g.scale_apply = 1;
-  to_result(p, &g);
-  std::swap(g.rows, g.cols), std::swap(g.d_rs, g.d_cs);
-  return run_gemm<PX == 2 ? kPairs : kPlainByPair, 1>(g, s);
+  return e;
 }
 
 }  // namespace
+
+// Q's nonzero part is of the size of 1 while it holds directions in which X has
+// nothing times the product of the a's, and G's errors there grow by a^2 a
+// step: products of Q, P and G are symmetric only up to their rounding, and
+// mirroring them mixes the two.  A 64-bit simulation with fp32 sums and
+// mirrored tiles of 32 (96 x 128; the same on the card): rank 1 3.2e-2, rank 8
+// 8e-3 for five default steps in one cycle, 1.0e-4 and 2.3e-5 in cycles of
+// three, as the iteration itself in 32 bits (7e-5, 1.7e-5).
+int32_t ortho_cycle(const OrthoParams& p, int32_t first) {
+  constexpr float kCycleGrowth = 48.f;
+  float growth = 1.f;
+  int32_t n = 0;
+  for (; first + n < p.steps; ++n) {
+    growth *= fmaxf(1.f, fabsf(p.coefficients[3 * (first + n)]));
+    if (n > 0 && growth > kCycleGrowth) break;
+  }
+  return n;
+}
 
 size_t orthogonalize_workspace(const OrthoParams& p) {
   const Way way = way_of(p);
@@ -990,11 +1016,14 @@ size_t orthogonalize_workspace(const OrthoParams& p) {
 // grids: up to 128 rows, the last launch's 256 threads for each 128 columns
 // (the first one's 512 for up to 64 ranges of columns stay below 2^31);
 // otherwise the start's 256 threads for each 64 x 64 values (the products' tiles
-// are larger, or a few).
+// are larger, or a few).  Up to 128 rows there is no limit of 32-bit offsets,
+// but an X kept between cycles is to stay below 8 GiB of workspace a matrix.
 bool orthogonalize_grid_ok(const OrthoParams& p) {
   const int64_t lim = (int64_t)1 << 31;
   if (p.batch >= 65536 || p.m >= lim || p.n >= lim) return false;
-  if (way_of(p) == kSmallGram) return (double)p.batch * (double)((p.n + 127) / 128) < 0x1p24;
+  if (way_of(p) == kSmallGram)
+    return (double)p.batch * (double)((p.n + 127) / 128) < 0x1p24 &&
+           (ortho_cycle(p, 0) == p.steps || (double)p.m * (double)p.n < 0x1p31);
   return (double)p.batch * (double)(pad64(p.m) / 64) * (double)(pad64(p.n) / 64) < 0x1p24 &&
          (double)pad64(p.m) * (double)pad64(p.n) * 4 < 0x1p31;
 }
@@ -1002,8 +1031,8 @@ bool orthogonalize_grid_ok(const OrthoParams& p) {
 hipError_t launch_orthogonalize(const OrthoParams& p, hipStream_t s) {
   switch (way_of(p)) {
     case kSmallGram: return launch_ortho_gram(p, s);
-    case kGram: return x_planes(p, kGram) == 2 ? gram<2>(p, s) : gram<1>(p, s);
-    default: return x_planes(p, kDirect) == 2 ? direct<2>(p, s) : direct<1>(p, s);
+    case kGram: return x_planes(p.x_type) == 2 ? gram<2>(p, s) : gram<1>(p, s);
+    default: return direct(p, s);
   }
 }
 

@@ -104,11 +104,10 @@ size_t orthogonalize_workspace(const OrthoParams& p);
 bool orthogonalize_grid_ok(const OrthoParams& p);
 hipError_t launch_orthogonalize(const OrthoParams& p, hipStream_t stream);
 
-// Through the Gram matrix (ortho_gram.hip): up to kGramRows rows, and steps
-// whose polynomials multiply to at most kGramGrowth at zero (that product is
-// Q's largest value, kept in fp16 times 2^6).
+// Through the Gram matrix the steps go in cycles: those from `first` on that
+// one cycle takes.  ortho_gram.hip: up to kGramRows rows.
+int32_t ortho_cycle(const OrthoParams& p, int32_t first);
 constexpr int64_t kGramRows = 128;
-constexpr float kGramGrowth = 512.f;
 struct OrthoGramPlan {
   int32_t rows;          // m padded: 32, 64, 96 or 128
   int32_t splits, cols;  // ranges of columns, and the columns of one

@@ -722,3 +722,19 @@ def test_orthogonalize_wide_float32(api, kind, shape):
     want = orthogonalize64(x)
     assert d.dtype == torch.bfloat16
     assert float((d.double() - want).norm() / want.norm()) <= (BF16_ROUNDING ** 2 + 4e-4 ** 2) ** 0.5
+
+
+@pytest.mark.parametrize("kind", ["rank1", "rank8", "rank64", "decades4", "rows"])
+@pytest.mark.parametrize("shape", [(140, 1000), (5000, 1100), (40, 500)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("out", ["bfloat16", "float16"])
+def test_orthogonalize_poor_rank_wide(api, kind, shape, dtype, out):
+    """Through the Gram matrix (small, wide, or fp16 results): pairs of fp16,
+    4e-4 next to the rounding."""
+    import torch
+    dt = getattr(torch, out)
+    x = poor_rank(kind, shape, 181, dtype)
+    d = api.orthogonalize(x, out=torch.empty(shape, dtype=dt, device="cuda"))
+    want = orthogonalize64(x)
+    bound = ((torch.finfo(dt).eps / 2) ** 2 / 3 + 4e-4 ** 2) ** 0.5
+    assert float((d.double() - want).norm() / want.norm()) <= bound

@@ -74,3 +74,16 @@ def test_counted_waits(code_objects, name):  # noqa: F811
             tile += 1
     assert tile == 3 * stages and len(copy_at) == (stages - 1 + 3 * stages) * copies
     assert max(counts) <= ahead * copies, counts
+
+
+# an X between two cycles, from x's one plane: the result a pair, both ways round
+AGAIN = {
+    "ortho_ring_22": ("_ZN2sl12_GLOBAL__N_117ortho_ring_kernelILi2ELi2EEEvNS0_9OrthoGemmE", 128, 32),
+    "ortho_128_22": ("_ZN2sl12_GLOBAL__N_117ortho_gemm_kernelILi128ELi128ELi1ELi2ELi2EEEvNS0_9OrthoGemmE", 64, 0),
+}
+K.KERNELS.update(AGAIN)
+
+
+@pytest.mark.parametrize("name", sorted(AGAIN))
+def test_kept_iterate_accumulator_discipline(code_objects, name):  # noqa: F811
+    K.test_ring_kernel_accumulator_discipline(code_objects, name)
