@@ -270,8 +270,8 @@ sl_status sl_quantize(const sl_quantize_args* args, void* stream);
  *   d  (batch?, M, N) f16 or bf16, any strides that do not broadcast; it may
  *      be x itself (same pointer, dtype and layout), else not overlap it
  *   steps         1 to 64
- *   coefficients  host array of a, b, c for each step, each within 16 in
- *                 magnitude; NULL: 3.4445, -4.7750, 2.0315 at every step
+ *   coefficients  host array of a, b, c for each step, a within 16, b and c
+ *                 within 64 in magnitude; NULL: 3.4445, -4.7750, 2.0315 at every step
  * All products are on fp16 values times powers of two with sums in fp32, the
  * sum of squares is in 64 bits (up to 128 rows: a matrix's trace in 64 bits
  * over fp32 sums).  A matrix between products is a pair of fp16, a value and

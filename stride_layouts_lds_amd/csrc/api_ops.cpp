@@ -312,7 +312,10 @@ sl_status plan_orthogonalize(const sl_orthogonalize_args* args, OrthoPlan* P) {
                 (long long)D.cols, (long long)X.batch, (long long)X.rows, (long long)X.cols);
   for (int i = 0; i < 3 * args->steps; ++i) {
     const float c = args->coefficients ? args->coefficients[i] : kDefaultCoefficients[i % 3];
-    if (!(std::fabs(c) <= 16.f)) return fail(SL_ERR_ARG, "coefficient %d is not within 16 in magnitude", i);
+    // (While the iterates' singular values s stay below 2, |a + b s^2 + c s^4| is below 2 / s: nothing that the
+    // kernels hold in fp16 grows with b or c.)
+    const float most = i % 3 == 0 ? 16.f : 64.f;
+    if (!(std::fabs(c) <= most)) return fail(SL_ERR_ARG, "coefficient %d is not within %g in magnitude", i, most);
     P->coefficients[i] = c;
   }
   P->empty = X.batch == 0 || X.rows == 0 || X.cols == 0;

@@ -738,3 +738,30 @@ def test_orthogonalize_poor_rank_wide(api, kind, shape, dtype, out):
     want = orthogonalize64(x)
     bound = ((torch.finfo(dt).eps / 2) ** 2 / 3 + 4e-4 ** 2) ** 0.5
     assert float((d.double() - want).norm() / want.norm()) <= bound
+
+
+# ---------------------------------------------------------------------------
+# schedules: other coefficients each step, steep ones first
+# ---------------------------------------------------------------------------
+
+SCHEDULE = [(8.287212, -23.595887, 17.300387), (4.107059, -2.947850, 0.544843), (3.948691, -2.908902, 0.551819),
+            (3.318420, -2.488488, 0.510049), (2.300652, -1.668904, 0.418807), (1.891301, -1.267996, 0.376804),
+            (1.875, -1.25, 0.375), (1.875, -1.25, 0.375)]
+
+
+@pytest.mark.parametrize("kind", ["rank8", "decades4", "rows"])
+@pytest.mark.parametrize("shape", [(96, 128), (300, 400), (1000, 140)])
+@pytest.mark.parametrize("out", ["bfloat16", "float16"])
+@pytest.mark.parametrize("steps", [3, 4, 8])
+def test_orthogonalize_schedules(api, kind, shape, out, steps):
+    """Steps that amplify a lot run on pairs of fp16 with fp32 sums: next to
+    the result's rounding (uniform within half a step) an iteration in 32 bits
+    alone is off by up to 2.4e-4 for these coefficients; twice that."""
+    import torch
+    dt = getattr(torch, out)
+    x = poor_rank(kind, shape, 171, "float32")
+    co = [tuple(torch.tensor(c, dtype=torch.float32).tolist()) for c in SCHEDULE[:steps]]  # as the library takes them
+    d = api.orthogonalize(x, out=torch.empty(shape, dtype=dt, device="cuda"), steps=steps, coefficients=co)
+    want = orthogonalize64(x, steps, co)
+    bound = ((torch.finfo(dt).eps / 2) ** 2 / 3 + 4.8e-4 ** 2) ** 0.5
+    assert float((d.double() - want).norm() / want.norm()) <= bound

@@ -288,3 +288,13 @@ def test_product_grid_limit(api):
     with pytest.raises(api.SLError) as e:
         f16(1 << 21, 1 << 20)
     assert e.value.name == "SL_ERR_SHAPE"
+
+
+def test_orthogonalize_coefficient_limits(api):
+    size = lambda *co: api.sl_orthogonalize_workspace_bytes(ortho_args(api, rm(X, (96, 128), BF16), rm(D, (96, 128), BF16),
+                                                                       steps=len(co) // 3, coefficients=co))
+    assert size(8.2872, -23.5959, 17.3004) > 0 and size(16.0, -64.0, 64.0) > 0
+    for co in ((16.5, 0.0, 0.0), (1.0, 64.5, 0.0), (1.0, 0.0, -65.0), (1.0, 0.0, NAN)):
+        with pytest.raises(api.SLError) as e:
+            size(*co)
+        assert e.value.name == "SL_ERR_ARG"
