@@ -518,7 +518,9 @@ sl_status sl_layout_op(int32_t op, const char* a, const char* b, char* out, int6
  *   A_wave, A_lane0  the wave's (lane, ((slot), repeat, K slice)) partition
  *                    of the LDS tile, and lane 0's part of it
  *   A_frag           fragment_like of one K slice: the lane's registers
- *   (B the same), SFA / SFB / scale_instr for scaled formats,
+ *   (B the same), SFA / SFB for scaled formats and scale_instr for those whose
+ *   instruction takes the scales; with few rows of A (kernel 9) no operand goes
+ *   through LDS and the stages between A_tiles and A_frag are not there,
  *   D_instr, acc, D_lane0   accumulator TV map, register order, and the D
  *                    elements of lane 0's registers
  *   D, C, D_tiles, tile_order, workgroup_tile, workspace (split-K).

@@ -853,7 +853,59 @@ sl_status sl_layout_op(int32_t op, const char* a, const char* b, char* out, int6
   return emit_text(r, out, capacity, needed);
 }
 
+// the trace's text, or what went wrong with it
+static sl_status emit_description(const sl::DescribeInput& in, char* out, int64_t capacity, int64_t* needed) {
+  std::string text;
+  try {
+    text = sl::describe_plan(in);
+  } catch (const std::exception& e) {
+    return fail(SL_ERR_LAYOUT, "%s", e.what());
+  }
+  return emit_text(text, out, capacity, needed);
+}
+
+static sl_status describe_block(const sl_gemm_args* args, char* out, int64_t capacity, int64_t* needed) {
+  BlockPlan P;
+  const sl_status s = plan_block(args, &P);
+  if (s != SL_OK) return s;
+  if (P.empty) return emit_text("# empty product: nothing is launched\n", out, capacity, needed);
+  const sl::BlockGemmParams& p = P.p;
+  const sl::BlockTileShape& ts = sl::kBlockTiles[P.tile];
+  sl::DescribeInput in{};
+  in.kernel = P.pub.kernel;
+  in.a_load = P.pub.a_load, in.b_load = P.pub.b_load;
+  in.bm = P.pub.tile_m, in.bn = P.pub.tile_n, in.bk = P.pub.tile_k;
+  in.wm = ts.wm, in.wn = ts.wn;
+  in.stages = P.tile == sl::BT_128x128 ? P.pub.lds_bytes / (256 * sl::kScaleBlock) : 2;
+  in.ring = P.tile == sl::BT_256x256;
+  if (P.tile == sl::BT_SKINNY) {
+    // the rows of A that the kernel covers, and its waves and stages
+    in.bm = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
+    in.from_memory = p.M <= 16;
+    in.k_waves = P.pub.threads / 64;
+    in.stages = in.bm == 64 ? 3 : 4;
+  }
+  in.splits = 1, in.group_m = p.group_m;
+  in.tiles_m = p.tiles_m, in.tiles_n = p.tiles_n;
+  in.workgroups = P.pub.workgroups, in.batch = P.pub.batch, in.M = p.M, in.N = p.N, in.K = p.K;
+  in.a_bs = p.a_bs, in.a_rs = p.a_rs, in.a_cs = 1;
+  in.b_bs = p.b_bs, in.b_rs = p.b_rs, in.b_cs = 1;
+  in.c_bs = p.c_bs, in.c_rs = p.c_rs, in.c_cs = p.c_cs;
+  in.d_bs = p.d_bs, in.d_rs = p.d_rs, in.d_cs = p.d_cs;
+  in.sa_rs = p.sa_rs, in.sa_cs = p.sa_ks, in.sb_rs = p.sb_rs, in.sb_cs = p.sb_ks;
+  in.sa_shift = p.a_shift, in.sb_shift = p.b_shift;
+  in.d_bytes = elem_size(args->d.dtype);
+  in.a_batched = args->a.layout.rank == 3, in.b_batched = args->b.layout.rank == 3;
+  in.c_batched = args->c.layout.rank == 3, in.d_batched = args->d.layout.rank == 3;
+  in.has_c = (p.flags & sl::BF_HAS_C) != 0;
+  in.flags = ((p.flags & sl::BF_D_VEC) ? sl::F_D_VEC : 0) | ((p.flags & sl::BF_C_VEC) ? sl::F_C_VEC : 0);
+  in.block_k = args->block_k;
+  in.lds_bytes = P.pub.lds_bytes;
+  return emit_description(in, out, capacity, needed);
+}
+
 sl_status sl_describe_plan(const sl_gemm_args* args, char* out, int64_t capacity, int64_t* needed) {
+  if (is_block_gemm(args)) return describe_block(args, out, capacity, needed);
   Plan P;
   const sl_status s = plan_gemm(args, &P);
   if (s != SL_OK) return s;
@@ -882,13 +934,7 @@ sl_status sl_describe_plan(const sl_gemm_args* args, char* out, int64_t capacity
   in.flags = p.flags;
   in.block_k = args->block_k;
   in.lds_bytes = P.pub.lds_bytes;
-  std::string text;
-  try {
-    text = sl::describe_plan(in);
-  } catch (const std::exception& e) {
-    return fail(SL_ERR_LAYOUT, "%s", e.what());
-  }
-  return emit_text(text, out, capacity, needed);
+  return emit_description(in, out, capacity, needed);
 }
 
 }  // extern "C"

@@ -79,6 +79,7 @@ struct InstrInfo {
 InstrInfo instr_of(const DescribeInput& in) {
   const bool bf16 = in.flags & F_BF16;
   switch (in.kernel) {
+    case K_BLOCK8: return {MFMA16_F8, "v_mfma_scale_f32_16x16x128_f8f6f4 (E4M3 data, unit scales)", 16, 128, 16};
     case K_MX: return {MFMA16_F8, "v_mfma_scale_f32_16x16x128_f8f6f4 (E4M3 data, E8M0 scales)", 16, 128, 16};
     case K_MX_W8:
     case K_MX_W4R: return {MFMA32_F8, "v_mfma_scale_f32_32x32x64_f8f6f4 (E4M3 data, E8M0 scales)", 32, 64, 16};
@@ -142,6 +143,7 @@ const char* kernel_name(int32_t k) {
     case K_MXFP4: return "MXFP4 GEMM, scaled 32x32x64 instruction on E2M1 data";
     case K_MXFP6: return "MXFP6 GEMM, scaled 32x32x64 instruction on 6-bit data";
     case K_MX_W4R: return "MXFP8 GEMM, 4 waves, scales loaded into registers";
+    case K_BLOCK8: return "E4M3 GEMM with fp32 scales per 128 K";
     default: return "?";
   }
 }
@@ -164,7 +166,7 @@ void operand(Out& o, const DescribeInput& in, const InstrInfo& I, char name, int
   const int32_t KS = in.bk / I.k;                         // K slices per K-tile
   const bool fp4 = in.kernel == K_MXFP4;
   const bool fp6 = in.kernel == K_MXFP6;
-  const bool fp8 = in.kernel == K_MX || in.kernel == K_MX_W8 || in.kernel == K_MX_W4R;
+  const bool fp8 = in.kernel == K_MX || in.kernel == K_MX_W8 || in.kernel == K_MX_W4R || in.kernel == K_BLOCK8;
   // the 4-wave MX kernel packs 6-bit K-tiles: rows 96 bytes apart in LDS
   // (LoaderFP6Packed); the 8-wave one pads them to 128-byte rows
   const bool packed = fp6 && in.ring;
@@ -177,6 +179,11 @@ void operand(Out& o, const DescribeInput& in, const InstrInfo& I, char name, int
           fmt("zipped_divide by the %dx%d workgroup tile: ((tile), (tile index)); a ragged last tile is "
               "completed with zeros by the loads",
               BR, in.bk));
+  if (in.from_memory) {
+    o.note(n + " loader: each lane's two 16-byte pieces of a row's K block straight from memory into registers");
+    o.line(n + "_frag", T({T({S(16, 1), S(2, 16)}), S(F, 32)}), fmt("registers: the lane's 32 codes of a K block (32 values x %d)", F));
+    return;
+  }
   o.note(n + " loader: " + load_name(load));
 
   const bool mmajor = load == LOAD_MNDMA;
@@ -253,6 +260,11 @@ void operand(Out& o, const DescribeInput& in, const InstrInfo& I, char name, int
 
 void workgroup_map(Out& o, const DescribeInput& in) {
   const int64_t total = in.workgroups;
+  if (in.k_waves > 1) {
+    o.line("workgroup_tile", T({R(in.tiles_n, in.tiles_m), R(in.tiles_m, 1), R(in.batch, (int64_t)in.tiles_m * in.tiles_n)}),
+           "workgroup (b % tiles_n, b / tiles_n % tiles_m, matrix) -> tm + tiles_m*tn + tiles_m*tiles_n*matrix");
+    return;
+  }
   const int64_t q = total / 8;
   o.note(fmt("workgroup b -> XCD x = b %% 8 takes the contiguous range x*%lld.. of the tile order; the order walks "
              "groups of %d tile-rows column by column",
@@ -282,9 +294,10 @@ void accumulators(Out& o, const DescribeInput& in, const InstrInfo& I) {
           fmt("D elements of lane 0's (r, i, j) from the wave's corner; lane l adds row l %% %d and column "
               "4 (l / %d)",
               I.rows, I.rows));
+  const int32_t quad = 4 * in.d_bytes;
   o.note(std::string("epilogue: 4 consecutive n of one m per store; ") +
-         ((in.flags & F_D_VEC) ? "one 8-byte store (D rows contiguous and aligned)" : "element stores") +
-         (in.has_c ? ((in.flags & F_C_VEC) ? ", C read as 8 bytes" : ", C read by elements") : ", no C"));
+         ((in.flags & F_D_VEC) ? fmt("one %d-byte store (D rows contiguous and aligned)", quad) : "element stores") +
+         (in.has_c ? ((in.flags & F_C_VEC) ? fmt(", C read as %d bytes", quad) : ", C read by elements") : ", no C"));
 }
 
 }  // namespace
@@ -292,8 +305,18 @@ void accumulators(Out& o, const DescribeInput& in, const InstrInfo& I) {
 std::string describe_plan(const DescribeInput& in) {
   Out o;
   const InstrInfo I = instr_of(in);
-  const int32_t NT = in.wm * in.wn * 64;
-  if (in.ring)
+  const int32_t NT = in.wm * in.wn * in.k_waves * 64;
+  if (in.kernel == K_BLOCK8 && in.k_waves > 1)
+    o.note(fmt("kernel %d: %s; tile %dx%dx%d, %d waves that split K (wave w takes K blocks w, w + %d, ...; their sums meet in "
+               "LDS)%s, %d LDS bytes",
+               in.kernel, kernel_name(in.kernel), in.bm, in.bn, in.bk, in.k_waves, in.k_waves,
+               in.from_memory ? "" : fmt(", each with %d LDS stages of its own", in.stages).c_str(), in.lds_bytes));
+  else if (in.kernel == K_BLOCK8 && in.ring)
+    o.note(fmt("kernel %d: %s; tile %dx%dx%d, %d waves (%d x %d), wave tile %dx%d; LDS five operand K-tiles (A and B of "
+               "K-tiles t and t + 1, and a free one), %d LDS bytes",
+               in.kernel, kernel_name(in.kernel), in.bm, in.bn, in.bk, NT / 64, in.wm, in.wn, in.bm / in.wm, in.bn / in.wn,
+               in.lds_bytes));
+  else if (in.ring)
     o.note(fmt("kernel %d: %s; tile %dx%dx%d, %d waves (%d x %d), wave tile %dx%d with accumulators in AGPRs; LDS "
                "a ring of five operand K-tiles (operand tile q = A of K-tile q/2 for even q, B for odd q, in slot "
                "q %% 5), %d LDS bytes",
@@ -343,6 +366,18 @@ std::string describe_plan(const DescribeInput& in) {
       else
         o.note("scales: byte loads from HBM per K-tile");
     }
+  }
+  if (in.kernel == K_BLOCK8) {
+    const int64_t kb = (in.K + 127) / 128;
+    auto rows = [](int64_t n, int32_t shift, int64_t rs) {
+      return shift ? T({S(int64_t(1) << shift, 0), R((n + (int64_t(1) << shift) - 1) >> shift, rs)}) : R(n, rs);
+    };
+    o.line("SFA", T({rows(in.M, in.sa_shift, in.sa_rs), R(kb, in.sa_cs)}), "fp32 scale of A(m, 128 j .. 128 j + 127)");
+    o.line("SFB", T({rows(in.N, in.sb_shift, in.sb_rs), R(kb, in.sb_cs)}), "fp32 scale of B(n, block)");
+    o.note("scales: a K block's sum, formed on a zero accumulator, times SFA SFB is added to acc");
+    if (in.d_bytes == 4)
+      o.note("fp32 D: the lane's 32 codes become fp16 in registers and four v_mfma_f32_16x16x32_f16 sum the block, 8 of them "
+             "at a time");
   }
   accumulators(o, in, I);
   o.line("D", view(in.M, in.N, in.d_rs, in.d_cs, in.d_batched, in.batch, in.d_bs), "element (m, n[, batch])");

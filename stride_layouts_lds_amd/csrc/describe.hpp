@@ -22,6 +22,10 @@ struct DescribeInput {
   int32_t block_k;  // scale block (MX 32, NVFP4 16)
   int32_t lds_bytes;
   bool ring;  // LDS as a ring of five operand K-tiles (the 4-wave 256x256 kernel)
+  // fp32 block scales (kernel 9): 1 << shift rows of an operand share a scale
+  // row, bytes of a D element, and the waves that split K (1: none do)
+  int32_t sa_shift, sb_shift, d_bytes = 2, k_waves = 1;
+  bool from_memory = false;  // fragments go from memory to registers: no operand tile in LDS
   bool nv_decoded;  // NVFP4 operands decoded to fp16 rows in the workspace by a first kernel
 };
 

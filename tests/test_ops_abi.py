@@ -298,3 +298,52 @@ def test_orthogonalize_coefficient_limits(api):
         with pytest.raises(api.SLError) as e:
             size(*co)
         assert e.value.name == "SL_ERR_ARG"
+
+
+@pytest.mark.parametrize("M,N,out", [(1, 4096, BF16), (48, 8192, F16), (48, 8192, F32), (30, 100, BF16), (300, 200, F16),
+                                     (1290, 1500, BF16), (1290, 1500, F32), (8192, 8192, BF16), (4000, 3000, F32)])
+@pytest.mark.parametrize("b_rows", [1, 128])
+def test_block_product_is_described(api, M, N, out, b_rows):
+    """The trace of every kernel of the block-scaled form: of the plan that
+    sl_gemm_plan gives, its layouts ones that the algebra reads back."""
+    K = 2064
+    kb = 17
+    args = gemm_args(api, rm(X, (M, K), F8), rm(Q, (N, K), F8), rm(D, (M, N), out), rm(S, (M, kb), F32, (1, M)),
+                     rm(ST, (-(-N // b_rows), kb), F32), c=rm(QT, (M, N), out))
+    plan = api.sl_gemm_plan(args)
+    text = api.describe_plan(args)
+    stages = api.describe_stages(text)
+    assert text.startswith(f"# kernel {api.K_BLOCK8}:")
+    assert f"{plan['workgroups']} workgroups of {plan['threads']} threads" in text
+    assert f"{plan['lds_bytes']} LDS bytes" in text
+    for name in ("A_instr", "A", "A_tiles", "B", "B_tiles", "A_frag", "B_frag", "SFA", "SFB", "D_instr", "acc", "D_lane0", "D", "C",
+                 "D_tiles"):
+        api.layout_op("parse", stages[name])
+    assert ("A_lds" in stages) == (M > 16)
+    size = lambda l: int(api.layout_op("size", l))
+    assert size(stages["A"]) == M * K and size(stages["B"]) == N * K and size(stages["D"]) == M * N
+    # m, block -> offset of the scale: one row of scales for each row of A, b_rows of B's share one
+    at = lambda l, row, rows, j: int(api.layout_op("eval", l, str(row + rows * j)))
+    assert at(stages["SFA"], M - 1, M, 3) == M - 1 + 3 * M
+    rows_b = N if b_rows == 1 else -(-N // 128) * 128
+    for n in (0, N // 2, N - 1):
+        assert at(stages["SFB"], n, rows_b, 5) == n // b_rows * kb + 5
+    # a lane's 32 codes, twice 16 in a row 64 apart
+    assert [int(api.layout_op("eval", stages["A_instr"], str(64 * v))) // 16 for v in (0, 15, 16, 31)] == [0, 15, 64, 79]
+    assert ("v_mfma_f32_16x16x32_f16" in text) == (out == F32)
+    # accumulators: as many fp32 registers as the tile's part of a lane
+    tile_m = plan["tile_m"] if plan["tile_m"] != 64 else (16 if M <= 16 else 32 if M <= 32 else 64)
+    waves = plan["threads"] // 64 if plan["tile_m"] != 64 else 1
+    assert size(stages["acc"]) == tile_m * plan["tile_n"] // 64 // waves
+
+
+def test_block_product_description_refuses(api):
+    for change, what in ((dict(block_k=32), "SL_ERR_SHAPE"), (dict(sfb=rm(ST, (3, 4), F32)), "SL_ERR_SHAPE"),
+                         (dict(a=rm(X, (300, 512), F8, (520, 1))), "SL_ERR_LAYOUT")):
+        with pytest.raises(api.SLError) as e:
+            api.describe_plan(gemm_args(api, **{**GOOD_P, **change}))
+        assert e.value.name == what
+    empty = gemm_args(api, rm(X, (0, 512), F8), GOOD_P["b"], rm(D, (0, 200), BF16), rm(S, (0, 4), F32), GOOD_P["sfb"])
+    assert "nothing is launched" in api.describe_plan(empty)
+    no_k = gemm_args(api, rm(0, (300, 0), F8), rm(0, (200, 0), F8), GOOD_P["d"], rm(0, (300, 0), F32), rm(0, (2, 0), F32))
+    assert api.describe_plan(no_k).startswith("# kernel 9")
