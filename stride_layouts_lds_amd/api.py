@@ -252,10 +252,11 @@ def set_workspace(args, workspace) -> None:
 
 def _stream(stream: Optional[int]) -> ctypes.c_void_p:
     """``stream``, or torch's current one on the current device (its handle
-    alone: building torch's Stream object for it takes 3 us)."""
+    alone, where torch gives that: building its Stream object takes 3 us)."""
     if stream is None:
         import torch
-        stream = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        stream = torch.cuda.current_stream().cuda_stream if handle is None else handle(torch.cuda.current_device())
     return ctypes.c_void_p(stream)
 
 

@@ -347,3 +347,17 @@ def test_block_product_description_refuses(api):
     assert "nothing is launched" in api.describe_plan(empty)
     no_k = gemm_args(api, rm(0, (300, 0), F8), rm(0, (200, 0), F8), GOOD_P["d"], rm(0, (300, 0), F32), rm(0, (2, 0), F32))
     assert api.describe_plan(no_k).startswith("# kernel 9")
+
+
+def test_current_stream_without_torchs_private_call(api, monkeypatch):
+    """torch's private call for a stream's handle is a short cut, not needed."""
+    import torch
+
+    class Stream:
+        cuda_stream = 4711
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 100 + device, raising=False)
+    assert api._stream(None).value == 103 and api._stream(7).value == 7 and not api._stream(0).value
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert api._stream(None).value == 4711
