@@ -7,7 +7,6 @@ is not built, every call raises; there is no fallback.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import struct
@@ -44,6 +43,7 @@ class sl_layout(ctypes.Structure):
 
 class sl_tensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("layout", sl_layout)]
+    is_cuda = True  # as far as anyone here can tell
 
 
 class sl_gemm_args(ctypes.Structure):
@@ -205,6 +205,14 @@ class PackedTensor:
     def __init__(self, storage, dtype: int, shape, strides):
         self.storage, self.dtype, self.shape, self.strides = storage, dtype, tuple(shape), tuple(strides)
 
+    @property
+    def device(self):
+        return self.storage.device
+
+    @property
+    def is_cuda(self):
+        return self.storage.is_cuda
+
 
 def tensor_desc(x, dtype: Optional[int] = None) -> sl_tensor:
     """Descriptor of a torch tensor or PackedTensor (None: absent operand)."""
@@ -225,6 +233,13 @@ def tensor_desc(x, dtype: Optional[int] = None) -> sl_tensor:
         strides = tuple(2 * s for s in x.stride()[:-1]) + (1,)
         return desc(x.data_ptr(), SL_F4_E2M1, shape, strides)
     return desc(x.data_ptr(), _torch_dtype_code(x, dtype), tuple(x.shape), tuple(x.stride()))
+
+
+def _check_devices(*operands) -> None:
+    """Host memory would fault the GPU: the library takes addresses as given."""
+    for x in operands:
+        if x is not None and not x.is_cuda:
+            raise ValueError(f"an operand is on {x.device}: they are GPU tensors")
 
 
 def make_args(a, b, c=None, d=None, sfa=None, sfb=None, block_k: int = 32, workspace=None) -> sl_gemm_args:
@@ -260,17 +275,15 @@ def _stream(stream: Optional[int]) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream)
 
 
-def _allocating_on(stream: Optional[int], device):
-    """A context whose torch allocations belong to ``stream`` (None: torch's
-    current one).  What a call on another stream than torch's current one
+def _allocated(stream: int, device, make):
+    """What make() allocates with torch, belonging to ``stream``.  What a call on another stream than torch's current one
     writes must not come from the current one's pool: earlier work there may
     still use the block, and it is handed out again there as soon as the
     tensor is dropped, with the call's kernels still to run."""
-    if stream is None:
-        return contextlib.nullcontext()
     import torch
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
-                             else torch.cuda.default_stream(device))
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
+                           else torch.cuda.default_stream(device)):
+        return make()
 
 
 def sl_gemm(args: sl_gemm_args, stream: Optional[int] = None) -> None:
@@ -319,13 +332,14 @@ def gemm(a, b, c=None, out=None, sfa=None, sfb=None, block_k: int = 32, stream: 
     if out is None:
         batch = max(x.shape[0] if x is not None and x.dim() == 3 else 0 for x in (a, b, c))
         shape = (a.shape[-2], b.shape[-2]) if batch == 0 else (batch, a.shape[-2], b.shape[-2])
-        with _allocating_on(stream, a.device):
-            out = torch.empty(shape, dtype=dtype or (torch.bfloat16 if a.dtype == torch.bfloat16 else torch.float16),
-                              device=a.device)
+        dtype = dtype or (torch.bfloat16 if a.dtype == torch.bfloat16 else torch.float16)
+        out = (torch.empty(shape, dtype=dtype, device=a.device) if stream is None else
+               _allocated(stream, a.device, lambda: torch.empty(shape, dtype=dtype, device=a.device)))
     args = make_args(a, b, c, out, sfa, sfb, block_k)
+    _check_devices(a, b, c, out, sfa, sfb, workspace)
     if workspace is None:
-        with _allocating_on(stream, out.device):
-            workspace = workspace_for(args, out.device)
+        workspace = (workspace_for(args, out.device) if stream is None else
+                     _allocated(stream, out.device, lambda: workspace_for(args, out.device)))
     set_workspace(args, workspace)
     sl_gemm(args, stream)
     return out
@@ -373,14 +387,16 @@ def quantize(x, block_rows: int = 1, transposed: bool = False, direct: bool = Tr
         raise ValueError("nothing to compute: neither direct nor transposed")
     R, C = x.shape[-2:]
     if out is None:
-        with _allocating_on(stream, x.device):
-            out = (_codes_and_scales(x, R, C, block_rows) if direct else ()) + \
-                  (_codes_and_scales(x, C, R, block_rows) if transposed else ())
+        make = lambda: ((_codes_and_scales(x, R, C, block_rows) if direct else ()) +
+                        (_codes_and_scales(x, C, R, block_rows) if transposed else ()))
+        out = make() if stream is None else _allocated(stream, x.device, make)
     elif len(out) != 2 * (direct + transposed):
         raise ValueError(f"out holds {len(out)} tensors, {2 * (direct + transposed)} are written")
     pair = lambda wanted, at: (_record(out[at]), _record(out[at + 1])) if wanted else (_ABSENT, _ABSENT)
-    sl_quantize(sl_quantize_args.from_buffer_copy(b"".join((_record(x), *pair(direct, 0), *pair(transposed, -2),
-                                                            _QUANTIZE_TAIL.pack(block_rows)))), stream)
+    args = sl_quantize_args.from_buffer_copy(b"".join((_record(x), *pair(direct, 0), *pair(transposed, -2),
+                                                       _QUANTIZE_TAIL.pack(block_rows))))
+    _check_devices(x, *out)
+    sl_quantize(args, stream)
     return out
 
 
@@ -394,8 +410,9 @@ def orthogonalize(x, out=None, steps: int = 5, coefficients=None, workspace=None
     ``gemm``."""
     import torch
     if out is None:
-        with _allocating_on(stream, x.device):
-            out = torch.empty(x.shape, dtype=torch.bfloat16 if x.dtype == torch.float32 else x.dtype, device=x.device)
+        dtype = torch.bfloat16 if x.dtype == torch.float32 else x.dtype
+        make = lambda: torch.empty(x.shape, dtype=dtype, device=x.device)
+        out = make() if stream is None else _allocated(stream, x.device, make)
     args = sl_orthogonalize_args()
     args.x, args.d, args.steps = tensor_desc(x), tensor_desc(out), steps
     if coefficients is not None:
@@ -406,10 +423,11 @@ def orthogonalize(x, out=None, steps: int = 5, coefficients=None, workspace=None
             raise ValueError(f"coefficients are (3,) or (steps, 3), got {flat.shape}")
         flat = np.ascontiguousarray(flat)  # read before the call returns
         args.coefficients = flat.ctypes.data_as(ctypes.POINTER(ctypes.c_float))
+    _check_devices(x, out, workspace)
     if workspace is None:
         n = sl_orthogonalize_workspace_bytes(args)
-        with _allocating_on(stream, x.device):
-            workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+        make = lambda: torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+        workspace = make() if stream is None else _allocated(stream, x.device, make)
     set_workspace(args, workspace)
     sl_orthogonalize(args, stream)
     return out

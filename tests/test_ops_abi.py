@@ -361,3 +361,17 @@ def test_current_stream_without_torchs_private_call(api, monkeypatch):
     assert api._stream(None).value == 103 and api._stream(7).value == 7 and not api._stream(0).value
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
     assert api._stream(None).value == 4711
+
+
+def test_host_tensors_are_refused(api):
+    """Before any call: a kernel that reads host memory faults the GPU."""
+    import torch
+    h, q, s = torch.zeros(64, 128).half(), torch.zeros(64, 128).to(torch.float8_e4m3fn), torch.ones(64, 1)
+    for call in (lambda **kw: api.gemm(h, h, **kw), lambda **kw: api.gemm(q, q, sfa=s, sfb=s, block_k=128, **kw),
+                 lambda **kw: api.quantize(h, **kw), lambda **kw: api.quantize(h, transposed=True, **kw),
+                 lambda **kw: api.orthogonalize(h, **kw)):
+        with pytest.raises(ValueError, match="GPU tensors"):
+            call()
+    packed = api.PackedTensor(torch.zeros(64 * 96, dtype=torch.uint8), api.SL_F6_E2M3, (64, 128), (128, 1))
+    with pytest.raises(ValueError, match="GPU tensors"):
+        api.gemm(packed, packed, out=h)
