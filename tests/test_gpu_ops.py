@@ -765,3 +765,80 @@ def test_orthogonalize_schedules(api, kind, shape, out, steps):
     want = orthogonalize64(x, steps, co)
     bound = ((torch.finfo(dt).eps / 2) ** 2 / 3 + 4.8e-4 ** 2) ** 0.5
     assert float((d.double() - want).norm() / want.norm()) <= bound
+
+
+# ---------------------------------------------------------------------------
+# codes of 16-bit values, bit for bit
+# ---------------------------------------------------------------------------
+
+def exact_codes64(x, block_rows):
+    """The nearest E4M3 value to 448 x / top in 64 bits, ties to even.  With
+    16-bit x the quotient, if it is not a tie, is further from one than its
+    rounding to fp32 moves it: 448 x and the tie times top are whole multiples
+    of one unit and have at most 16 bits."""
+    import torch
+    x = x.double()
+    v = x * TOP / spread_scales(block_tops(x, block_rows), block_rows, *x.shape[-2:])
+    step = e4m3_steps(v)
+    return (torch.round(v / step) * step).clamp(-TOP, TOP)
+
+
+def tie_rows(dtype):
+    """Rows whose largest value is 7 j 2^e and whose others are m j 2^i: 448
+    times such a quotient is m 2^i', for odd m from 17 to 31 halfway between two
+    codes, and below 2^-6, where the codes are 2^-9 apart, for every odd m."""
+    import torch
+    dt = getattr(torch, dtype)
+    rows = []
+    for j in (1, 3, 5, 7, 9, 11, 13, 29, 33, 61, 65):
+        for e in (-9, -3, 0, 4):
+            row = [7.0 * j * 2.0 ** e]
+            for m in range(1, 32, 2):
+                for i in range(-17, 3):
+                    for sign in (1, -1):
+                        v = sign * m * j * 2.0 ** (e + i)
+                        if abs(v) <= row[0] and float(torch.tensor(v, dtype=torch.float64).to(dt)) == v:
+                            row.append(v)
+            if float(torch.tensor(row[0], dtype=torch.float64).to(dt)) == row[0]:
+                rows += [([row[0]] + row[1 + at:128 + at]) for at in range(0, len(row) - 1, 127)]
+    x = torch.zeros((len(rows), 128), dtype=torch.float64)
+    for r, row in enumerate(rows):
+        x[r, :len(row)] = torch.tensor(row, dtype=torch.float64)
+    return x.to(dt).cuda()
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_quantize_ties(api, dtype):
+    import torch
+    x = tie_rows(dtype)
+    v = x.double() * TOP / spread_scales(block_tops(x.double(), 1), 1, *x.shape)
+    step = e4m3_steps(v)
+    ties = (v / step - torch.floor(v / step)) == 0.5
+    assert int(ties.sum()) > 1000
+    want = exact_codes64(x, 1)
+    q, s = api.quantize(x)
+    assert torch.equal(q[:, :128].double(), want)
+    # both outputs of one pass, along the rows and of the transpose
+    q, s, qt, st = api.quantize(x.t().contiguous(), transposed=True)
+    assert torch.equal(qt[:, :128].double(), want)
+    square = torch.zeros((128 * len(x), 128), dtype=x.dtype, device="cuda")
+    square[::128] = x
+    q, s = api.quantize(square, block_rows=128)
+    assert torch.equal(q[::128, :128].double(), want)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_codes_exact(api, dtype, block_rows):
+    """Few bits, so that ties are many, and values over the whole range."""
+    import torch
+    dt = getattr(torch, dtype)
+    for seed, x in ((191, torch.randint(-255, 256, (700, 900), generator=gen(191), device="cuda").to(dt)),
+                    (192, torch.randn((700, 900), generator=gen(192), device="cuda").to(dt)),
+                    (193, (torch.randn((700, 900), generator=gen(193), device="cuda") *
+                           torch.exp(3 * torch.randn((700, 900), generator=gen(194), device="cuda"))).clamp(-6e4, 6e4).to(dt))):
+        q, s, qt, st = api.quantize(x, block_rows=block_rows, transposed=True)
+        assert torch.equal(q[:, :900].double(), exact_codes64(x, block_rows)), seed
+        assert torch.equal(qt[:, :700].double(), exact_codes64(x.t(), block_rows)), seed
+        q1, s1 = api.quantize(x, block_rows=block_rows)
+        assert same_bytes(q1, q) and torch.equal(s1, s)
