@@ -738,15 +738,43 @@ void launch_tiles(OrthoGemm g, int32_t side, int64_t first, int64_t count, hipSt
     hipLaunchKernelGGL((ortho_gemm_kernel<64, 64, 2, MODE, OP>), grid, dim3(512), 0, s, g);
 }
 
-// The tile: the largest whose workgroups still fill the 256 CUs.  What a last
-// round of 256 x 256 tiles would leave most CUs without goes to 64 x 64
-// tiles: a symmetric 8192 x 8192 result has 528 tiles, and a third round for
-// 16 of them took 180 of 596 us.
+// What a last round of 256 x 256 tiles would leave most CUs without goes to 64
+// x 64 tiles: a symmetric 8192 x 8192 result has 528 tiles, and a third round
+// for 16 of them took 180 of 596 us.
+int64_t whole_tiles(int32_t side, int64_t all) {
+  const int64_t rest = all % 256;
+  return side == 256 && all > 256 && rest <= 64 ? all - rest : all;
+}
+
+// The tile with the least time: rounds over the 256 CUs (a workgroup to each)
+// times a tile's start and end and its K-loop (`products` of K values), padding
+// included.  The constants are a fit to whole calls with each tile forced, 25
+// sizes and batches in fp16 and bf16, most within 10%.  256, 128 and 64 forced, us:
+// 256 x (200 x 400) bf16 1056, 865, 1174; 256 x (320 x 640) fp16 2699, 2065, 2505;
+// 100 x (300 x 300) fp16 1119, 799, 743; 1024 x 4096 bf16 995, 398, 268;
+// 2100 x 2300 bf16 1069, 533, 558; 8192 x 8192 bf16 9626, 13021, 18972.
+int32_t choose_side(const OrthoGemm& g, int32_t products) {
+  struct {
+    int32_t side;
+    double start, k;  // us a tile, ns a value of K
+  } constexpr tiles[3] = {{256, 27.0, 18.0}, {128, 6.3, 7.3}, {64, 3.1, 2.5}};
+  const double k = (double)g.k * products * 1e-3;
+  int32_t best = 0;
+  double least = 0.0;
+  for (const auto& t : tiles) {
+    const int64_t all = ortho_tiles(g, t.side), whole = whole_tiles(t.side, all);
+    if (all >= (int64_t)1 << 23) continue;  // 512 threads each would not fit a grid
+    double cost = (double)((whole + 255) / 256) * (t.start + k * t.k);
+    if (whole < all) cost += (double)((16 * (all - whole) + 255) / 256) * (tiles[2].start + k * tiles[2].k);
+    if (best == 0 || cost < least) best = t.side, least = cost;
+  }
+  return best;
+}
+
 template <int MODE, int OP>
 hipError_t run_gemm(OrthoGemm g, hipStream_t s) {
-  const int32_t side = ortho_tiles(g, 256) >= 200 ? 256 : ortho_tiles(g, 128) >= 160 ? 128 : 64;
-  const int64_t all = ortho_tiles(g, side), rest = all % 256;
-  const int64_t whole = side == 256 && all > 256 && rest <= 64 ? all - rest : all;
+  const int32_t side = choose_side(g, MODE == kPairs ? 3 : MODE == kPlainByPair ? 2 : 1);
+  const int64_t all = ortho_tiles(g, side), whole = whole_tiles(side, all);
   g.parts = 1;
   launch_tiles<MODE, OP>(g, side, 0, whole, s);
   if (whole < all) {
