@@ -191,7 +191,9 @@ typedef struct {
  * N.  d (and c) f16, bf16 or f32.  Each block's sum is formed in the matrix
  * core, multiplied by its two scales and added up in fp32; for f16 and bf16 d
  * the block's sum keeps bits down to about 2^-16 of its largest product (the
- * 8-bit instruction), for f32 d it is an fp32 sum of exact products.  Operands
+ * 8-bit instruction), for f32 d it is an fp32 sum of exact products.  The two
+ * scales are multiplied first, in fp32: where their product leaves 2^-126 ..
+ * 2^128 it loses bits, or is infinite (and a block's sum of zero times it NaN).  Operands
  * K-contiguous with rows on 16-byte boundaries and K % 16 == 0, scales of any
  * strides (sl_quantize writes them).  No workspace.
  * Sizes: M, N, K and the batch count below 2^31, and the plan's workgroups

@@ -2,7 +2,9 @@
 
 Argument marshalling only: every step of the GEMM runs in the HIP library.
 PyTorch supplies device memory and the current HIP stream.  If the library
-is not built, every call raises; there is no fallback.
+is not built, every call raises; there is no fallback.  Nothing here is
+recorded by autograd: results of tensors that require gradients do not (the
+backward pass of a product is two more products).
 """
 
 from __future__ import annotations

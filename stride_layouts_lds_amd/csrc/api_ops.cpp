@@ -48,14 +48,16 @@ static bool overlap(const View& x, const View& y, int64_t batch) {
 
 // The tile: up to 64 rows of A stream the weight once (the skinny kernels),
 // and so do products of up to 64 tiles of 128 x 128, which would leave most
-// CUs without work (128 x 512 x 8192: 75 us in those tiles, 14 us in 64 x 16;
-// 512 x 2048 x 4096, 64 tiles: 41 and 23 us; 1024 x 2048 x 4096, 128 tiles: 43
-// both ways, and x 512: 12 and 20 us);
+// CUs without work (128 x 512 x 8192: 54 us in those tiles, 14 us streamed in 64
+// x 16; 512 x 2048 x 4096, 64 tiles: 30 and 21 us; 640 x 2048 x 4096, 80 tiles:
+// 30 both ways; 1024 x 2048 x 4096: 30 and 41, and x 512: 9 and 19.  The rule
+// loses where A is tall and B narrow, so that each row of A is read several
+// times: 8192 x 100 x 4096 29 and 39);
 // otherwise the tile with the least (workgroup rounds over the 256 CUs) x
 // (work of a tile), the 128 x 128 tile two to a CU and moving twice the
-// operand bytes per product (measured with either forced: 4096^3 81 and 94 us,
-// 3000 x 5000 x 4096, 240 tiles of 256 x 256, 73 and 84, 4000 x 3000 x 2064 55
-// and 65; equal from 128 such tiles down).  fp32 results: 128 x 128 (the fp16 fragments of
+// operand bytes per product (256 x 256 and 128 x 128 forced: 4096^3 67 and 79 us,
+// 3000 x 5000 x 4096 65 and 75, 4000 x 3000 x 2064 39 and 48, 2048 x 4096 x 4096
+// 66 and 42, 1536 x 4096 x 4096 66 and 41).  fp32 results: 128 x 128 (the fp16 fragments of
 // the larger tile do not fit the registers: 4096 x 4096 x 8192 took 836 us).
 static int32_t choose_tile(int64_t batch, int64_t M, int64_t N, int32_t type) {
   if (M <= kSkinnyRows || batch * ceil_div(M, 128) * ceil_div(N, 128) <= 64) return BT_SKINNY;

@@ -141,8 +141,8 @@ constexpr int SB_SQUARE = 0, SB_ROWS = 1;
 // BM x BN output tiles, the K-tiles of 128 bytes per row brought straight
 // into LDS, STAGES deep: two, and two workgroups to a CU, or, where there is
 // not more than one for each, four.  Measured: 4096 x 4096 x 8192 + C into
-// fp32 300 us (916 TFLOP/s; 360 vector instructions a K-tile beside 64
-// MFMAs), 1024 x 2048 x 4096 into bf16 31 us.
+// fp32 300 us a pass (916 TFLOP/s; 360 vector instructions a K-tile beside 64
+// MFMAs; MFMA busy 40%), 1024 x 2048 x 4096 into bf16 30 us.
 template <int BM, int BN, int WM, int WN, int STAGES, int SBK, int OT>
 __global__ __launch_bounds__(WM* WN * 64, STAGES == 2 ? 2 : 1) void gemm_block_kernel(const BlockGemmParams p) {
   typedef typename FragOf<OT>::type Frag;
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(WM* WN * 64, STAGES == 2 ? 2 : 1) void gemm_block_k
         }
       }
       // left to itself, the compiler moved each read next to its use (1024 x
-      // 2048 x 4096: 39 us; 31 in this order.  With fp16 fragments its own
+      // 2048 x 4096: 39 us; 30 in this order.  With fp16 fragments its own
       // order is 4% faster)
       if constexpr (OT != OT_F32) __builtin_amdgcn_sched_barrier(0);
     }
@@ -262,7 +262,8 @@ __global__ __launch_bounds__(WM* WN * 64, STAGES == 2 ? 2 : 1) void gemm_block_k
 // last products run, and the copies of t + 2 (A into the free slot, B into
 // B(t)'s, which is in registers) have a whole K-tile to land.  A block's sums
 // are scaled and added while the next ones run in the matrix core.  Measured:
-// 8192^3, bf16 D, square blocks of B: 527 us, 2.09 PFLOP/s (MXFP8: 403).
+// 8192^3, bf16 D, square blocks of B: 520 to 535 us a pass, 2.05 to 2.12 PFLOP/s
+// (MXFP8: 403); MFMA busy 45%, 5.9 vector instructions beside each.
 template <int SBK, int OT>
 __global__ __launch_bounds__(512, 2) void gemm_block_ring_kernel(const BlockGemmParams p) {
   typedef FragF8 Frag;

@@ -22,9 +22,9 @@
 //
 // P's products commute, so G and Q stay symmetric, up to their rounding, and
 // every operand is read along its rows.  Bound by latency: a step is three dependent rounds of
-// products with two barriers each.  Measured at 96 x 128 (bf16, five steps):
-// gram 6, steps 27, apply 8 us; the steps take 0.9 us each at 32 rows, 2.5 at
-// 64, 5.2 at 96 and 10.5 at 128.
+// products with two barriers each.  Measured at 96 x 128 (bf16, five steps in
+// two cycles): gram 6 and 7, steps 17 and 12, apply 7 and 9 us; the steps take
+// 0.9 us each at 32 rows, 2.5 at 64, 5.2 at 96 and 10.5 at 128.
 #include "ortho_device.hpp"
 
 namespace sl {

@@ -378,9 +378,8 @@ __device__ __forceinline__ void agprs_settled(floatx4 (&acc)[FM][FN]) {
 // LDS), each with a ring of four K-tiles in LDS, so that a copy has two
 // K-tiles of compute to land.  Fragments are read while the products before
 // theirs run, across the one barrier of a K-tile too.  Measured: 128 x 128
-// tiles, 240 workgroups (16 x 520^2 from pairs, 18 K-tiles) 23 us, of which
-// 11 go to the tile's start and end; 64 x 64 tiles, 136 workgroups (1024^2
-// from K = 4096) 14 us, 0.33 a round of two K-tiles.
+// tiles, 240 workgroups (16 x 520^2 from pairs, 18 K-tiles) 24 us; 64 x 64 tiles,
+// 136 workgroups (1024^2 from K = 4096) 15 us, from K = 1024 7.5.
 // ---------------------------------------------------------------------------
 template <int BM, int BN, int KG, int MODE, int OP>
 __global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGemm g) {
@@ -537,8 +536,9 @@ __global__ __launch_bounds__(256 * KG, KG) void ortho_gemm_kernel(const OrthoGem
 // reads of its first half beside the last products of the K-tile before, the
 // first half's products beside the reads of the second, all but the last of
 // the second half's, one barrier.  Measured: 512 tiles of a symmetric 8192^2
-// from K = 8192 in 400 to 450 us (1.2 to 1.3 PFLOP/s), 1024 tiles of an 8192^2
-// stored in both orientations in 930 us (1.18).
+// from K = 8192 in 410 to 450 us (1.2 to 1.3 PFLOP/s; MFMA busy 66%), 1024 tiles
+// of an 8192^2 stored in both orientations and with its second plane in 935 to
+// 990 us (1.11 to 1.18; 56%).
 // ---------------------------------------------------------------------------
 template <int MODE, int OP>
 __global__ __launch_bounds__(256, 1) void ortho_ring_kernel(const OrthoGemm g) {
@@ -862,8 +862,8 @@ int32_t knee_of(const OrthoParams& p) {
 // the direct way, 15 m^2 n + 5 m^3 operations for five steps, where they have no
 // more than four times as many columns as rows; the Gram matrix's multiplies
 // pairs, 42 m^3 + 14 m^2 n in two cycles, and is the more accurate one.  Direct
-// and Gram: 1000 x 1000 147 and 213 us, 1024 x 4096 241 and 282, x 8192 370 and
-// 363, x 16384 631 and 498, 8192 x 8192 9.4 and 21.6 ms.
+// and Gram: 1000 x 1000 147 and 215 us, 1024 x 4096 240 and 281, x 8192 371 and
+// 367, x 16384 634 and 501, 4096 x 4096 1.7 and 3.7 ms, 8192 x 8192 9.3 and 21.8.
 //
 // The direct way keeps X as a pair, and a X comes from both planes; what is
 // rounded to fp16 is X as a factor, G and B.  (X as one plane was wrong: what
