@@ -1016,13 +1016,14 @@ hipError_t gram(const OrthoParams& p, hipStream_t s) {
 
 }  // namespace
 
-// Q's nonzero part is of the size of 1 while it holds directions in which X has
-// nothing times the product of the a's, and G's errors there grow by a^2 a
-// step: products of Q, P and G are symmetric only up to their rounding, and
-// mirroring them mixes the two.  A 64-bit simulation with fp32 sums and
-// mirrored tiles of 32 (96 x 128; the same on the card): rank 1 3.2e-2, rank 8
-// 8e-3 for five default steps in one cycle, 1.0e-4 and 2.3e-5 in cycles of
-// three, as the iteration itself in 32 bits (7e-5, 1.7e-5).
+// As many steps as multiply to 48 in their a's.  In directions where X has
+// nothing Q grows with that product, next to parts of the size of 1, and G's
+// errors there grow by a^2 a step; products of Q, P and G are symmetric only up
+// to their rounding, and mirroring them mixes the one into the other.  A 64-bit
+// simulation with fp32 sums and mirrored tiles of 32 (96 x 128; the same on the
+// card): rank 1 3.2e-2, rank 8 8e-3 for five default steps in one cycle, 1.0e-4
+// and 2.3e-5 in cycles of three, about as the iteration itself in 32 bits (7e-5,
+// 1.7e-5).
 int32_t ortho_cycle(const OrthoParams& p, int32_t first) {
   constexpr float kCycleGrowth = 48.f;
   float growth = 1.f;
