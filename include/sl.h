@@ -75,8 +75,8 @@ extern "C" {
 
 typedef enum {
   SL_F16 = 1,     /* IEEE binary16 */
-  SL_F32 = 2,     /* IEEE binary32: block scales and the block-scaled product's C and D, inputs of
-                     sl_quantize and sl_orthogonalize */
+  SL_F32 = 2,     /* IEEE binary32: fp32 scales and C and D of the products that take them, inputs of
+                     sl_quantize, sl_quantize_rows and sl_orthogonalize */
   SL_F8_E4M3 = 3, /* OCP MX E4M3 (bias 7, max 448, S.1111.111 = NaN) */
   SL_E8M0 = 4,    /* OCP MX E8M0 scale: 2^(b-127), 255 = NaN */
   SL_BF16 = 5,    /* bfloat16: binary32's sign and 8-bit exponent, 7 stored significand bits */
@@ -85,7 +85,8 @@ typedef enum {
   SL_F6_E2M3 = 7, /* OCP MX FP6 E2M3 (bias 1, 3 significand bits, max 7.5), packed as one
                      little-endian bit stream along the unit-stride (K) axis: element offset
                      o occupies bits 6o .. 6o+5, bit 0 = least significant bit of byte 0 */
-  SL_F6_E3M2 = 8  /* OCP MX FP6 E3M2 (bias 3, 2 significand bits, max 28), packed as E2M3 */
+  SL_F6_E3M2 = 8, /* OCP MX FP6 E3M2 (bias 3, 2 significand bits, max 28), packed as E2M3 */
+  SL_I8 = 9       /* 8-bit two's complement integer */
 } sl_dtype;
 
 typedef enum {
@@ -116,16 +117,17 @@ typedef struct {
 } sl_tensor;
 
 typedef struct {
-  sl_tensor a;     /* (batch?, M, K)  f16, bf16, f8_e4m3 or f4_e2m1 (scaled) */
+  sl_tensor a;     /* (batch?, M, K)  f16, bf16, f8_e4m3, f4_e2m1 or i8 (scaled) */
   sl_tensor b;     /* (batch?, N, K)  same dtype as a                      */
   sl_tensor c;     /* (batch?, M, N)  D's dtype; data == NULL means C = 0  */
   sl_tensor d;     /* (batch?, M, N)  bf16 for bf16 a/b, else f16 output (f16,
-                      bf16 or f32 with f32 scales)                         */
+                      bf16 or f32 with f32 scales, so for i8 too)          */
   sl_tensor sfa;   /* (batch?, M, ceil(K/block_k)) e8m0 (MXFP8), f8_e4m3 (NVFP4)
-                      or f32 (block_k 128; M or ceil(M/128) rows)          */
+                      or f32 (block_k 128; M or ceil(M/128) rows);
+                      (batch?, M, 1) f32 for i8                            */
   sl_tensor sfb;   /* (batch?, N, ceil(K/block_k)) same dtype as sfa       */
   int32_t block_k; /* 32 for MXFP8, 16 for NVFP4, 128 with f32 scales;
-                      ignored for f16 / bf16                               */
+                      ignored for f16 / bf16 and i8                        */
   void* workspace;          /* device memory for a plan's workspace: split-K
                                fp32 partial sums or decoded NVFP4 operands
                                (NULL when the plan needs none) */
@@ -150,7 +152,10 @@ typedef struct {
                          multiple of 16 blocks on 16-byte boundaries),
                          9 e4m3 with fp32 scales per 128 K (256x256 or
                          128x128 tiles; few rows of A or few tiles: tile_m
-                         64, the waves of a workgroup split K) */
+                         64, the waves of a workgroup split K), 10 int8
+                         (256x256 on an LDS ring, or 128x128; few rows of A
+                         or few tiles: tile_m 16, 32 or 64, the waves of a
+                         workgroup split K) */
   int32_t a_load;     /* 0 K-contiguous vector, 1 M-contiguous vector (register
                          transpose), 2 generic, 3 M-contiguous direct copy into
                          an M-major LDS tile read by transposing reads, 4 NVFP4
@@ -196,6 +201,14 @@ typedef struct {
  * 2^128 it loses bits, or is infinite (and a block's sum of zero times it NaN).  Operands
  * K-contiguous with rows on 16-byte boundaries and K % 16 == 0, scales of any
  * strides (sl_quantize writes them).  No workspace.
+ * 8-bit integers: a and b SL_I8, sfa (batch?, M, 1) and sfb (batch?, N, 1)
+ * SL_F32, one scale per row (a token's, an output channel's), d (and c) f16,
+ * bf16 or f32:
+ *     D[m,n] = C[m,n] + sfa[m] sfb[n] sum_k a[m,k] b[n,k].
+ * The sum is exact in 32-bit integers, so K is below 131072 (else
+ * SL_ERR_SHAPE); it is rounded to fp32, multiplied by sfa, then by sfb, and C
+ * added, in fp32, and rounded to d's type.  Operands as for E4M3 with fp32 scales
+ * (sl_quantize_rows writes them), scales of any strides.  No workspace.
  * Sizes: M, N, K and the batch count below 2^31, and the plan's workgroups
  * times their threads below 2^32 (else SL_ERR_SHAPE).  An
  * operand may span any number of bytes; 256 of its rows (one tile) must
@@ -312,6 +325,103 @@ typedef struct {
 } sl_orthogonalize_args;
 sl_status sl_orthogonalize(const sl_orthogonalize_args* args, void* stream);
 sl_status sl_orthogonalize_workspace_bytes(const sl_orthogonalize_args* args, int64_t* bytes);
+
+/*
+ * Row quantisation to 8-bit integers.  Per row of x, with top = max(max |x|,
+ * 2^-100),
+ *     s = top / 127,   q = the integer nearest to 127 x / top,
+ * s correctly rounded to fp32, ties of the code to even, so x ~ q s within half
+ * of s.  A row holding a NaN or an infinity gets scale NaN and codes 0 (any
+ * product with it is NaN).
+ *   x   (batch?, R, C)  f16, bf16 or f32, any strides
+ *   q   (batch?, R, Cq) i8, C <= Cq <= 128 ceil(C / 128); columns from C on are
+ *       written as zeros (a product wants K a multiple of 16); contiguous along
+ *       its last axis with rows on 16-byte boundaries
+ *   s   (batch?, R, 1)  f32, any strides
+ * No output may broadcast or overlap x or the other.  An x without rows is a
+ * no-op; without columns every scale is 2^-100 / 127.  Asynchronous on
+ * `stream`, one kernel, no workspace; errors as sl_gemm, SL_ERR_SHAPE from 2^24
+ * rows on in all (2^26 with up to 1024 columns or, from 1024 rows on, up to
+ * 4096; where x's columns lie apart 64 rows x 2^22).
+ */
+typedef struct {
+  sl_tensor x;
+  sl_tensor q, s;
+} sl_quantize_rows_args;
+sl_status sl_quantize_rows(const sl_quantize_rows_args* args, void* stream);
+
+/*
+ * The gated feed-forward block: both projections, the activation and the
+ * product in one kernel,
+ *     g = x w_gate^T,   u = x w_up^T,   h = act(g) u  (elementwise).
+ *   x       (batch?, M, K)  f16, bf16 or i8
+ *   w_gate, w_up  (batch?, F, K) of x's type; rank 2: the same weights for every
+ *           matrix of the batch
+ *   sx      (batch?, M, 1) f32, s_gate and s_up (batch?, F, 1) f32, with i8: g =
+ *           sx[m] s_gate[f] sum_k x w_gate, as sl_gemm's (K below 131072)
+ *   h       (batch?, M, F)  x's type; for i8 f16, bf16 or f32
+ *   gate, up  (batch?, M, F) of h's type, both or neither (data NULL): g and u,
+ *           which sl_gated_backward reads
+ *   activation  SL_SILU v / (1 + e^-v), SL_GELU v Phi(v), SL_GELU_TANH 0.5 v (1 +
+ *           tanh(sqrt(2/pi) (v + 0.044715 v^3))), SL_RELU max(v, 0)
+ * Sums, scales, activation and product are in fp32 (i8 sums exact); g, u and h
+ * are each rounded once (SL_SILU and SL_GELU_TANH are v s with an s between 0 and
+ * 1, taken as 0 below 2^-126).  16-bit operands may have any strides: those whose
+ * rows are not K-contiguous on 16-byte boundaries (all of them, where K is not a
+ * multiple of 8) are first copied to such rows in the workspace
+ * (sl_gated_workspace_bytes(), often 0; rules as for sl_gemm's).  i8 operands
+ * are K-contiguous with rows on 16-byte boundaries and K % 16 == 0.
+ * Outputs may have any strides that do not broadcast and overlap nothing; gate
+ * and up may be the two halves of one matrix (of its rows or its columns).
+ * M or F or the batch 0: a no-op; K 0: zeros.  Asynchronous on `stream`; errors
+ * as sl_gemm, SL_ERR_ARG for another activation.
+ */
+typedef enum { SL_SILU = 1, SL_GELU = 2, SL_GELU_TANH = 3, SL_RELU = 4 } sl_activation;
+
+typedef struct {
+  sl_tensor x;
+  sl_tensor w_gate, w_up;
+  sl_tensor sx, s_gate, s_up;
+  sl_tensor h;
+  sl_tensor gate, up;
+  int32_t activation; /* sl_activation */
+  void* workspace;
+  int64_t workspace_bytes;
+} sl_gated_args;
+sl_status sl_gated(const sl_gated_args* args, void* stream);
+sl_status sl_gated_workspace_bytes(const sl_gated_args* args, int64_t* bytes);
+
+/*
+ * Its backward pass: from dh, what the forward call read and the g and u it
+ * kept,
+ *     dg = dh u act'(g),   du = dh act(g),
+ *     dx = dg w_gate + du w_up,   dw_gate = dg^T x,   dw_up = du^T x,
+ * act' being 0 at 0 for SL_RELU.  dg and du are rounded to the operands' type, in
+ * which they are multiplied; sums are in fp32, each gradient rounded once.
+ *   dh, gate, up  (batch?, M, F), x (batch?, M, K), w_gate and w_up (batch?, F,
+ *           K): all f16 or all bf16, any strides
+ *   dx      (batch?, M, K), or data NULL: not wanted
+ *   dw_gate, dw_up  w_gate's and w_up's shape, or both data NULL.  Where the
+ *           weights are rank 2 and x is a batch they are summed over it.
+ * The batch is dh's; x's rank is dh's.  Gradients may have any strides that do
+ * not broadcast and overlap nothing (dw_gate and dw_up may be halves as gate and
+ * up).  Without tokens (M or the batch 0) the
+ * weights' gradients are zeros; with F 0 dx is.  Workspace as sl_gated: 16-bit
+ * copies of dg and du both ways and of x's and the weights' transposes, and what
+ * sl_gemm's plan for the three products asks for.  Asynchronous on `stream`;
+ * results do not vary from call to call.
+ */
+typedef struct {
+  sl_tensor dh;
+  sl_tensor x, w_gate, w_up;
+  sl_tensor gate, up;
+  sl_tensor dx, dw_gate, dw_up;
+  int32_t activation;
+  void* workspace;
+  int64_t workspace_bytes;
+} sl_gated_backward_args;
+sl_status sl_gated_backward(const sl_gated_backward_args* args, void* stream);
+sl_status sl_gated_backward_workspace_bytes(const sl_gated_backward_args* args, int64_t* bytes);
 
 /*
  * Planner overrides, read from the environment on every planning call (by

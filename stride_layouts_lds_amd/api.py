@@ -19,8 +19,9 @@ import numpy as np
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libstride_layouts_lds.so")
 
-SL_F16, SL_F32, SL_F8_E4M3, SL_E8M0, SL_BF16, SL_F4_E2M1, SL_F6_E2M3, SL_F6_E3M2 = 1, 2, 3, 4, 5, 6, 7, 8
-K_F16, K_F16_GENERIC, K_MX, K_MX_W8, K_NVFP4, K_MXFP4, K_MXFP6, K_MX_W4R, K_BLOCK8 = 1, 2, 3, 4, 5, 6, 7, 8, 9
+SL_F16, SL_F32, SL_F8_E4M3, SL_E8M0, SL_BF16, SL_F4_E2M1, SL_F6_E2M3, SL_F6_E3M2, SL_I8 = 1, 2, 3, 4, 5, 6, 7, 8, 9
+K_F16, K_F16_GENERIC, K_MX, K_MX_W8, K_NVFP4, K_MXFP4, K_MXFP6, K_MX_W4R, K_BLOCK8, K_I8 = 1, 2, 3, 4, 5, 6, 7, 8, 9, 10
+ACTIVATIONS = {"silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}  # sl_activation
 STATUS = {0: "SL_OK", -1: "SL_ERR_NULL", -2: "SL_ERR_DTYPE", -3: "SL_ERR_SHAPE", -4: "SL_ERR_LAYOUT",
           -5: "SL_ERR_ALIGN", -6: "SL_ERR_ALIAS", -7: "SL_ERR_ARCH", -8: "SL_ERR_LAUNCH", -9: "SL_ERR_ARG"}
 
@@ -28,7 +29,8 @@ STATUS = {0: "SL_OK", -1: "SL_ERR_NULL", -2: "SL_ERR_DTYPE", -3: "SL_ERR_SHAPE",
 EXPORTS = ["sl_gemm", "sl_gemm_no_alloc", "sl_gemm_plan", "sl_gemm_workspace_bytes", "sl_status_string", "sl_last_error_message",
            "sl_abi_version", "sl_query_fragment_map", "sl_query_lds_map", "sl_query_fragment_addresses", "sl_probe_mfma",
            "sl_probe_lds", "sl_layout_op", "sl_describe_plan", "sl_quantize", "sl_orthogonalize",
-           "sl_orthogonalize_workspace_bytes"]
+           "sl_orthogonalize_workspace_bytes", "sl_quantize_rows", "sl_gated", "sl_gated_workspace_bytes", "sl_gated_backward",
+           "sl_gated_backward_workspace_bytes"]
 
 # sl_layout_op operations (include/sl.h)
 LA_OPS = {"parse": 0, "coalesce": 1, "composition": 2, "complement": 3, "right_inverse": 4,
@@ -63,6 +65,20 @@ class sl_orthogonalize_args(ctypes.Structure):
     _fields_ = [("x", sl_tensor), ("d", sl_tensor), ("steps", ctypes.c_int32),
                 ("coefficients", ctypes.POINTER(ctypes.c_float)), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_int64)]
+
+
+class sl_quantize_rows_args(ctypes.Structure):
+    _fields_ = [("x", sl_tensor), ("q", sl_tensor), ("s", sl_tensor)]
+
+
+class sl_gated_args(ctypes.Structure):
+    _fields_ = [(n, sl_tensor) for n in ("x", "w_gate", "w_up", "sx", "s_gate", "s_up", "h", "gate", "up")] + [
+        ("activation", ctypes.c_int32), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class sl_gated_backward_args(ctypes.Structure):
+    _fields_ = [(n, sl_tensor) for n in ("dh", "x", "w_gate", "w_up", "gate", "up", "dx", "dw_gate", "dw_up")] + [
+        ("activation", ctypes.c_int32), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
 class sl_plan(ctypes.Structure):
@@ -126,6 +142,14 @@ def lib() -> ctypes.CDLL:
         L.sl_orthogonalize.argtypes = [P(sl_orthogonalize_args), vp]
         L.sl_orthogonalize_workspace_bytes.restype = i32
         L.sl_orthogonalize_workspace_bytes.argtypes = [P(sl_orthogonalize_args), P(i64)]
+        for name, args in (("sl_quantize_rows", sl_quantize_rows_args), ("sl_gated", sl_gated_args),
+                           ("sl_gated_backward", sl_gated_backward_args)):
+            getattr(L, name).restype = i32
+            getattr(L, name).argtypes = [P(args), vp]
+        for name, args in (("sl_gated_workspace_bytes", sl_gated_args),
+                           ("sl_gated_backward_workspace_bytes", sl_gated_backward_args)):
+            getattr(L, name).restype = i32
+            getattr(L, name).argtypes = [P(args), P(i64)]
         _lib = L
     return _lib
 
@@ -148,6 +172,9 @@ assert _TENSOR.size == ctypes.sizeof(sl_tensor)
 assert 6 * _TENSOR.size + _GEMM_TAIL.size == ctypes.sizeof(sl_gemm_args)
 _QUANTIZE_TAIL = struct.Struct("@i4x")         # sl_quantize_args from block_rows
 assert 5 * _TENSOR.size + _QUANTIZE_TAIL.size == ctypes.sizeof(sl_quantize_args)
+_GATED_TAIL = struct.Struct("@i4xPq")          # sl_gated_args and sl_gated_backward_args from activation
+assert 9 * _TENSOR.size + _GATED_TAIL.size == ctypes.sizeof(sl_gated_args) == ctypes.sizeof(sl_gated_backward_args)
+assert 3 * _TENSOR.size == ctypes.sizeof(sl_quantize_rows_args)
 _pack = _TENSOR.pack
 _ABSENT = _pack(0, 0, 2, 0, 0, 0, 0, 0, 0)
 
@@ -178,7 +205,7 @@ def _torch_dtype_code(x, override: Optional[int]) -> int:
     if not _codes:
         import torch
         _codes.update({torch.float16: SL_F16, torch.bfloat16: SL_BF16, torch.float32: SL_F32,
-                       torch.float8_e4m3fn: SL_F8_E4M3, torch.float8_e8m0fnu: SL_E8M0})
+                       torch.float8_e4m3fn: SL_F8_E4M3, torch.float8_e8m0fnu: SL_E8M0, torch.int8: SL_I8})
     if x.dtype not in _codes:
         raise TypeError(f"unsupported dtype {x.dtype}")
     return _codes[x.dtype]
@@ -242,6 +269,21 @@ def _check_devices(*operands) -> None:
     for x in operands:
         if x is not None and not x.is_cuda:
             raise ValueError(f"an operand is on {x.device}: they are GPU tensors")
+
+
+def _check_one_device(*operands) -> None:
+    """GPU tensors of the current device: its stream is the one the call runs
+    on, and its address space the one the kernels see."""
+    _check_devices(*operands)
+    import torch
+    here = None
+    for x in operands:
+        if x is None or isinstance(x, sl_tensor):
+            continue
+        if here is None:
+            here = torch.cuda.current_device()
+        if x.device.index != here:
+            raise ValueError(f"an operand is on {x.device}, the current device is cuda:{here}")
 
 
 def make_args(a, b, c=None, d=None, sfa=None, sfb=None, block_k: int = 32, workspace=None) -> sl_gemm_args:
@@ -325,7 +367,9 @@ def gemm(a, b, c=None, out=None, sfa=None, sfb=None, block_k: int = 32, stream: 
     of D's dtype (bf16 for bf16 operands, else fp16) or None; ``sfa``/``sfb``: float8_e8m0fnu scales (batch?, rows, K/32) for
     the MX form, or float32 scales (batch?, rows or ceil(rows/128),
     ceil(K/128)) with ``block_k`` 128 as ``quantize`` writes them, where D and
-    C may be fp16, bf16 or float32 (``dtype``, or ``out``'s).  A plan's workspace (split-K partial sums, or NVFP4
+    C may be fp16, bf16 or float32 (``dtype``, or ``out``'s).  int8 ``a`` and
+    ``b`` take one float32 scale per row, (batch?, rows, 1), as
+    ``quantize_rows`` writes them; D and C as with those.  A plan's workspace (split-K partial sums, or NVFP4
     operands decoded to fp16) is ``workspace`` (a device tensor) or, when
     None, a torch allocation of the size the library asks for.  Returns ``out`` (allocated by torch if None).
     With ``stream`` (a stream's handle) the call runs there, and what it
@@ -339,6 +383,10 @@ def gemm(a, b, c=None, out=None, sfa=None, sfb=None, block_k: int = 32, stream: 
                _allocated(stream, a.device, lambda: torch.empty(shape, dtype=dtype, device=a.device)))
     args = make_args(a, b, c, out, sfa, sfb, block_k)
     _check_devices(a, b, c, out, sfa, sfb, workspace)
+    if args.a.dtype == SL_I8:  # plans without a workspace
+        _check_one_device(a, b, c, out, sfa, sfb)
+        sl_gemm(args, stream)
+        return out
     if workspace is None:
         workspace = (workspace_for(args, out.device) if stream is None else
                      _allocated(stream, out.device, lambda: workspace_for(args, out.device)))
@@ -432,6 +480,133 @@ def orthogonalize(x, out=None, steps: int = 5, coefficients=None, workspace=None
         workspace = make() if stream is None else _allocated(stream, x.device, make)
     set_workspace(args, workspace)
     sl_orthogonalize(args, stream)
+    return out
+
+
+def sl_quantize_rows(args: sl_quantize_rows_args, stream: Optional[int] = None) -> None:
+    _check(lib().sl_quantize_rows(ctypes.byref(args), _stream(stream)))
+
+
+def sl_gated(args: sl_gated_args, stream: Optional[int] = None) -> None:
+    _check(lib().sl_gated(ctypes.byref(args), _stream(stream)))
+
+
+def sl_gated_workspace_bytes(args: sl_gated_args) -> int:
+    n = ctypes.c_int64(0)
+    _check(lib().sl_gated_workspace_bytes(ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def sl_gated_backward(args: sl_gated_backward_args, stream: Optional[int] = None) -> None:
+    _check(lib().sl_gated_backward(ctypes.byref(args), _stream(stream)))
+
+
+def sl_gated_backward_workspace_bytes(args: sl_gated_backward_args) -> int:
+    n = ctypes.c_int64(0)
+    _check(lib().sl_gated_backward_workspace_bytes(ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def _activation(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation {name!r}: one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+def _workspace(workspace, n: int, device, stream: Optional[int]):
+    """The caller's workspace, or ``n`` bytes of the call's stream (0: none)."""
+    if workspace is not None or n == 0:
+        return workspace
+    import torch
+    make = lambda: torch.empty(n, dtype=torch.uint8, device=device)
+    return make() if stream is None else _allocated(stream, device, make)
+
+
+def quantize_rows(x, out=None, stream: Optional[int] = None):
+    """int8 codes and float32 scales of a torch tensor ``x`` ((batch?, R, C),
+    fp16, bf16 or float32, any strides), one scale per row: a token's, or an
+    output channel's of a weight (out, in).  Returns (q, s): q (batch?, R, C
+    padded with zeros to a multiple of 16), s (batch?, R, 1), ready for
+    ``gemm`` and ``gated``.  ``out``: the same pair of the caller's tensors.
+    ``stream`` as for ``gemm``."""
+    import torch
+    if x.dim() not in (2, 3):
+        raise ValueError("quantize_rows takes a matrix or a batch of matrices")
+    if out is None:
+        shape = x.shape[:-1]
+        make = lambda: (torch.empty(shape + ((x.shape[-1] + 15) // 16 * 16,), dtype=torch.int8, device=x.device),
+                        torch.empty(shape + (1,), dtype=torch.float32, device=x.device))
+        out = make() if stream is None else _allocated(stream, x.device, make)
+    elif len(out) != 2:
+        raise ValueError(f"out holds {len(out)} tensors, 2 are written")
+    args = sl_quantize_rows_args.from_buffer_copy(b"".join((_record(x), _record(out[0]), _record(out[1]))))
+    _check_one_device(x, *out)
+    sl_quantize_rows(args, stream)
+    return out
+
+
+def gated(x, w_gate, w_up, activation: str = "silu", sx=None, s_gate=None, s_up=None, keep: bool = False, out=None,
+          dtype=None, workspace=None, stream: Optional[int] = None):
+    """The gated feed-forward block h = act(x w_gate^T) (x w_up^T) of torch
+    tensors as include/sl.h states it: ``x`` (batch?, M, K), ``w_gate`` and
+    ``w_up`` (batch?, F, K) or, the same for every matrix of a batch, (F, K), fp16
+    or bf16 of any strides; or int8 codes with their scales ``sx`` (batch?, M,
+    1), ``s_gate`` and ``s_up`` (batch?, F, 1) as ``quantize_rows`` writes them.
+    ``activation``: "silu", "gelu", "gelu_tanh" or "relu".  Returns h (batch?,
+    M, F), of x's dtype, for int8 ``dtype`` (fp16 if None, or bf16 or
+    float32); with ``keep`` (h, gate, up), the two projections with it, for
+    ``gated_backward``.  ``out``: the caller's h, or with ``keep`` its three tensors.
+    ``workspace``: a device tensor of at least sl_gated_workspace_bytes, or
+    None for a torch allocation where one is needed.  ``stream`` as for ``gemm``."""
+    import torch
+    act = _activation(activation)
+    if out is None:
+        batch = max((t.shape[0] for t in (x, w_gate, w_up) if t.dim() == 3), default=None)
+        shape = (x.shape[-2], w_gate.shape[-2]) if batch is None else (batch, x.shape[-2], w_gate.shape[-2])
+        dtype = dtype or (torch.float16 if x.dtype == torch.int8 else x.dtype)
+        make = lambda: tuple(torch.empty(shape, dtype=dtype, device=x.device) for _ in range(3 if keep else 1))
+        out = make() if stream is None else _allocated(stream, x.device, make)
+    else:
+        out = tuple(out) if keep else (out,)
+        if len(out) != (3 if keep else 1):
+            raise ValueError(f"out holds {len(out)} tensors, 3 are written")
+    operands = (x, w_gate, w_up, sx, s_gate, s_up) + out
+    args = sl_gated_args.from_buffer_copy(b"".join([_record(t) for t in operands] + [_ABSENT] * (9 - len(operands)) +
+                                                   [_GATED_TAIL.pack(act, 0, 0)]))
+    _check_one_device(*operands, workspace)
+    set_workspace(args, _workspace(workspace, sl_gated_workspace_bytes(args) if workspace is None else 0, x.device, stream))
+    sl_gated(args, stream)
+    return out if keep else out[0]
+
+
+def gated_backward(dh, x, w_gate, w_up, gate, up, activation: str = "silu", need_dx: bool = True, need_dw: bool = True,
+                   out=None, workspace=None, stream: Optional[int] = None):
+    """The gradients of ``gated``'s inputs from h's, ``dh`` (batch?, M, F), its
+    inputs and the ``gate`` and ``up`` it kept: (dx, dw_gate, dw_up), dx shaped
+    (batch?, M, K) as dh is a batch or not, the others as the weights (summed over the
+    batch where those are (F, K)).  All fp16 or all bf16, any strides.
+    Without ``need_dx`` or ``need_dw`` those places hold None.  ``out``: the
+    same tuple of the caller's tensors.  ``workspace``: a device tensor of at least
+    sl_gated_backward_workspace_bytes, or None for a torch allocation.
+    ``stream`` as for ``gemm``."""
+    import torch
+    act = _activation(activation)
+    if not (need_dx or need_dw):
+        raise ValueError("nothing to compute: neither dx nor the weights' gradients")
+    if out is None:
+        # one buffer for both weights' gradients: they are then one product
+        make = lambda: (torch.empty(dh.shape[:-1] + (x.shape[-1],), dtype=x.dtype, device=x.device) if need_dx else None,
+                        torch.empty((2,) + tuple(w_gate.shape), dtype=x.dtype, device=x.device) if need_dw else None)
+        dx, dw = make() if stream is None else _allocated(stream, x.device, make)
+        out = (dx, None, None) if dw is None else (dx, dw[0], dw[1])
+    elif len(out) != 3 or (out[0] is not None) != need_dx or any((t is not None) != need_dw for t in out[1:]):
+        raise ValueError("out holds dx, dw_gate and dw_up, None where they are not wanted")
+    operands = (dh, x, w_gate, w_up, gate, up) + tuple(out)
+    args = sl_gated_backward_args.from_buffer_copy(b"".join([_record(t) for t in operands] + [_GATED_TAIL.pack(act, 0, 0)]))
+    _check_one_device(*operands, workspace)
+    set_workspace(args, _workspace(workspace, sl_gated_backward_workspace_bytes(args) if workspace is None else 0, x.device,
+                                   stream))
+    sl_gated_backward(args, stream)
     return out
 
 

@@ -633,6 +633,12 @@ sl_status sl_gemm_plan(const sl_gemm_args* args, sl_plan* plan) {
     if (s == SL_OK && plan) *plan = B.pub;
     return s;
   }
+  if (is_int8_gemm(args)) {
+    RowsPlan I;
+    const sl_status s = plan_int8(args, &I);
+    if (s == SL_OK && plan) *plan = I.pub;
+    return s;
+  }
   Plan P;
   const sl_status s = plan_gemm(args, &P);
   if (s != SL_OK) return s;
@@ -648,6 +654,12 @@ sl_status sl_gemm_workspace_bytes(const sl_gemm_args* args, int64_t* bytes) {
     if (s == SL_OK) *bytes = B.pub.workspace_bytes;
     return s;
   }
+  if (is_int8_gemm(args)) {
+    RowsPlan I;
+    const sl_status s = plan_int8(args, &I);
+    if (s == SL_OK) *bytes = 0;
+    return s;
+  }
   Plan P;
   const sl_status s = plan_gemm(args, &P);
   if (s != SL_OK) return s;
@@ -657,6 +669,7 @@ sl_status sl_gemm_workspace_bytes(const sl_gemm_args* args, int64_t* bytes) {
 
 sl_status sl_gemm(const sl_gemm_args* args, void* stream) {
   if (is_block_gemm(args)) return run_block(args, stream);
+  if (is_int8_gemm(args)) return run_int8(args, stream);
   Plan P;
   sl_status s = plan_gemm(args, &P);
   if (s != SL_OK) return s;
@@ -670,6 +683,7 @@ static_assert(sl::kScratchBytes == (size_t)SL_NO_ALLOC_SCRATCH_BYTES, "one scrat
 
 sl_status sl_gemm_no_alloc(const sl_gemm_args* args, void* stream) {
   if (is_block_gemm(args)) return run_block(args, stream);  // no workspace
+  if (is_int8_gemm(args)) return run_int8(args, stream);    // nor here
   Plan P;
   sl_status s = plan_gemm(args, &P, false);  // NVFP4: the fused kernels, no decoded copies
   if (s != SL_OK) return s;
@@ -904,8 +918,41 @@ static sl_status describe_block(const sl_gemm_args* args, char* out, int64_t cap
   return emit_description(in, out, capacity, needed);
 }
 
+static sl_status describe_int8(const sl_gemm_args* args, char* out, int64_t capacity, int64_t* needed) {
+  RowsPlan P;
+  const sl_status s = plan_int8(args, &P);
+  if (s != SL_OK) return s;
+  if (P.empty) return emit_text("# empty product: nothing is launched\n", out, capacity, needed);
+  const sl::DenseParams& p = P.p;
+  sl::DescribeInput in{};
+  in.kernel = P.pub.kernel;
+  in.a_load = P.pub.a_load, in.b_load = P.pub.b_load;
+  in.bm = P.pub.tile_m, in.bn = P.pub.tile_n, in.bk = P.pub.tile_k;
+  in.ring = P.tile.tile == sl::DT_RING;
+  in.wm = in.wn = P.tile.tile == sl::DT_RING || P.tile.tile == sl::DT_128 ? 2 : 1;
+  in.k_waves = P.pub.threads / 64 / (in.wm * in.wn);
+  in.from_memory = P.tile.tile == sl::DT_SKINNY;
+  in.stages = P.tile.stages;
+  in.splits = 1, in.group_m = p.group_m;
+  in.tiles_m = p.tiles_m, in.tiles_n = p.tiles_n;
+  in.workgroups = P.pub.workgroups, in.batch = P.pub.batch, in.M = p.M, in.N = p.N, in.K = p.K;
+  in.a_bs = p.a_bs, in.a_rs = p.a_rs, in.a_cs = 1;
+  in.b_bs = p.b_bs[0], in.b_rs = p.b_rs[0], in.b_cs = 1;
+  in.c_bs = p.c_bs, in.c_rs = p.c_rs, in.c_cs = p.c_cs;
+  in.d_bs = p.d_bs, in.d_rs = p.d_rs, in.d_cs = p.d_cs;
+  in.sa_rs = p.sa_rs, in.sb_rs = p.sb_rs[0];
+  in.d_bytes = elem_size(args->d.dtype);
+  in.a_batched = args->a.layout.rank == 3, in.b_batched = args->b.layout.rank == 3;
+  in.c_batched = args->c.layout.rank == 3, in.d_batched = args->d.layout.rank == 3;
+  in.has_c = p.c != nullptr;
+  in.flags = ((p.flags & sl::DF_D_VEC) ? sl::F_D_VEC : 0) | ((p.flags & sl::DF_C_VEC) ? sl::F_C_VEC : 0);
+  in.lds_bytes = P.pub.lds_bytes;
+  return emit_description(in, out, capacity, needed);
+}
+
 sl_status sl_describe_plan(const sl_gemm_args* args, char* out, int64_t capacity, int64_t* needed) {
   if (is_block_gemm(args)) return describe_block(args, out, capacity, needed);
+  if (is_int8_gemm(args)) return describe_int8(args, out, capacity, needed);
   Plan P;
   const sl_status s = plan_gemm(args, &P);
   if (s != SL_OK) return s;

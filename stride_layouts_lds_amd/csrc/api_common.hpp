@@ -12,6 +12,7 @@
 #include <string>
 
 #include "../../include/sl.h"
+#include "sl_ops.hpp"
 
 namespace sl {
 namespace host {
@@ -38,6 +39,7 @@ inline int elem_size(int32_t dt) {
     case SL_F8_E4M3: return 1;
     case SL_E8M0: return 1;
     case SL_F4_E2M1: return 1;  // two elements per byte: byte_range halves the span
+    case SL_I8: return 1;
     case SL_F6_E2M3:
     case SL_F6_E3M2: return 1;  // four elements per three bytes: byte_range scales the span
     default: return 0;
@@ -141,6 +143,44 @@ inline sl_status check_arch() {
   }
   if (known[dev] < 0) return fail(SL_ERR_ARCH, "device %d is not gfx950", dev);
   return SL_OK;
+}
+
+// ---- the operators next to the GEMM
+
+constexpr int64_t kLim = (int64_t)1 << 31;
+
+// OT_* of a 16- or 32-bit floating-point type, or -1
+inline int32_t op_type(int32_t dtype) {
+  switch (dtype) {
+    case SL_F16: return OT_F16;
+    case SL_BF16: return OT_BF16;
+    case SL_F32: return OT_F32;
+    default: return -1;
+  }
+}
+
+inline int64_t batch_stride(const View& v) { return v.t->layout.rank == 3 ? v.bs : 0; }
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// data present and aligned to its element
+inline sl_status check_data(const char* name, const sl_tensor& t) {
+  if (!t.data) return fail(SL_ERR_NULL, "%s.data is NULL", name);
+  if ((uintptr_t)t.data % elem_size(t.dtype)) return fail(SL_ERR_ALIGN, "%s.data is not aligned to its %d-byte element", name, elem_size(t.dtype));
+  return SL_OK;
+}
+
+// rows of one-byte codes: contiguous along the last axis, every row on a 16-byte
+// boundary
+inline bool code_rows(const View& v, int64_t batch) {
+  return v.cs == 1 && (v.rows <= 1 || v.rs % 16 == 0) && (uintptr_t)v.t->data % 16 == 0 &&
+         (v.t->layout.rank == 2 || batch <= 1 || v.bs % 16 == 0);
+}
+
+inline bool overlap(const View& x, const View& y, int64_t batch) {
+  uintptr_t xl, xh, yl, yh;
+  byte_range(x, batch, &xl, &xh);
+  byte_range(y, batch, &yl, &yh);
+  return xl < yh && yl < xh;
 }
 
 }  // namespace host

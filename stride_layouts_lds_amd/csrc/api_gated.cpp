@@ -1,0 +1,671 @@
+// api_gated.cpp -- host side of the gated feed-forward block and its backward
+// pass, of the int8 form of sl_gemm and of sl_quantize_rows.  Every check runs
+// before any HIP call.
+#include "api_common.hpp"
+#include "api_ops.hpp"
+#include "sl_kernels.hpp"
+
+namespace sl {
+
+// The tile (dense.hpp).  `N` columns of the result; a gated tile covers half as
+// many as it has rows of B.
+DensePlan dense_plan(int32_t kind, bool gated, int64_t batch, int64_t M, int64_t N, int64_t K) {
+  using host::ceil_div;
+  const int64_t B = gated ? 2 * N : N;  // rows of B
+  const int64_t tiles128 = batch * ceil_div(M, 128) * ceil_div(B, 128);
+  if (M <= 16) {
+    const int32_t bn = gated || batch * ceil_div(N, 32) >= kCUs ? 32 : 16;
+    return {DT_SKINNY, 16, bn, kDenseSkinnyWaves * 64, kDenseSkinnyWaves * bn / 16 * 1024, 0};
+  }
+  if (M <= 64 || tiles128 <= 64) {
+    const int32_t bm = M <= 32 ? 32 : 64;
+    const int32_t bn = batch * ceil_div(M, bm) * ceil_div(B, 64) >= kCUs ? 64 : 32;
+    const int32_t stages = bm == 32 ? (bn == 32 ? 4 : 3) : (bn == 32 ? 3 : 2);
+    return {DT_STREAM, bm, bn, kDenseStreamWaves * 64, kDenseStreamWaves * stages * (bm + bn) * 128, stages};
+  }
+  const int64_t tiles256 = batch * ceil_div(M, 256) * ceil_div(B, 256);
+  const double ring = (double)ceil_div(tiles256, kCUs) * 256 * 256, small = (double)ceil_div(tiles128, 2 * kCUs) * 2 * 128 * 128 / 0.7;
+  if (K > 0 && ring <= small) return {DT_RING, 256, 256, 256, 5 * 256 * 128, 0};
+  const int32_t stages = tiles128 > kCUs ? 2 : 4;
+  return {DT_128, 128, 128, 256, stages * 256 * 128, stages};
+}
+
+namespace host {
+
+// K (and the batch's stride) of rows that the kernels read as they lie
+static bool rows_ready(const View& v, int64_t batch, int64_t es) {
+  const int64_t vec = 16 / es;
+  return (v.cs == 1 || v.cols <= 1) && v.cols % vec == 0 && (v.rows <= 1 || v.rs % vec == 0) && (uintptr_t)v.t->data % 16 == 0 &&
+         (v.t->layout.rank == 2 || batch <= 1 || v.bs % vec == 0) && ((std::min<int64_t>(v.rows, 256) - 1) * v.rs + v.cols) * es < kLim;
+}
+static bool quad_rows(const View& v, int64_t batch) {
+  return v.cs == 1 && (v.rows <= 1 || v.rs % 4 == 0) && (uintptr_t)v.t->data % (4 * elem_size(v.t->dtype)) == 0 &&
+         (batch <= 1 || batch_stride(v) % 4 == 0);
+}
+
+// one scale per row: (batch?, rows, 1) f32
+static sl_status scale_view(const char* name, const sl_tensor& t, int64_t rows, int64_t batch, View* v) {
+  sl_status s;
+  if (t.dtype != SL_F32) return fail(SL_ERR_DTYPE, "%s must be f32", name);
+  if ((s = make_view(name, t, v)) != SL_OK) return s;
+  if (v->rows != rows || v->cols != 1)
+    return fail(SL_ERR_SHAPE, "%s is (%lld,%lld), expected (%lld,1)", name, (long long)v->rows, (long long)v->cols, (long long)rows);
+  if (t.layout.rank == 3 && v->batch != batch)
+    return fail(SL_ERR_SHAPE, "%s has batch %lld, expected %lld", name, (long long)v->batch, (long long)batch);
+  return SL_OK;
+}
+
+constexpr int64_t kInt8MaxK = 131072;  // 128 x 128 x K < 2^31
+
+// the tiles of a plan in p and whether they fit a grid
+static sl_status place_tiles(DenseParams* p, const DensePlan& t, bool gated) {
+  const int64_t cols = gated ? t.bn / 2 : t.bn;
+  const int64_t tm = ceil_div(p->M, t.bm), tn = ceil_div(p->N, cols);
+  if (!grid_fits(p->batch, tm, tn, t.threads))
+    return fail(SL_ERR_SHAPE, "too many output tiles (batch %d of %lld x %lld)", p->batch, (long long)tm, (long long)tn);
+  p->tiles_m = (int32_t)tm, p->tiles_n = (int32_t)tn, p->group_m = 8;
+  p->k_tiles = (int32_t)ceil_div(p->K, kDenseKBytes);
+  return SL_OK;
+}
+
+sl_status plan_int8(const sl_gemm_args* args, RowsPlan* out) {
+  g_msg.clear();
+  if (args->b.dtype != SL_I8) return fail(SL_ERR_DTYPE, "b must be i8 when a is");
+  const int32_t type = op_type(args->d.dtype);
+  if (type < 0) return fail(SL_ERR_DTYPE, "d must be f16, bf16 or f32");
+  const bool has_c = args->c.data != nullptr;
+  if (has_c && args->c.dtype != args->d.dtype) return fail(SL_ERR_DTYPE, "c must have d's dtype");
+  View A, B, C{}, D, SA, SB;
+  sl_status s;
+  if ((s = make_view("a", args->a, &A)) != SL_OK) return s;
+  if ((s = make_view("b", args->b, &B)) != SL_OK) return s;
+  if ((s = make_view("d", args->d, &D)) != SL_OK) return s;
+  if (has_c && (s = make_view("c", args->c, &C)) != SL_OK) return s;
+  const int64_t batch = D.batch, M = A.rows, K = A.cols, N = B.rows;
+  if (B.cols != K) return fail(SL_ERR_SHAPE, "b is (%lld,%lld) but a has K=%lld", (long long)B.rows, (long long)B.cols, (long long)K);
+  if (D.rows != M || D.cols != N)
+    return fail(SL_ERR_SHAPE, "d is (%lld,%lld), expected (%lld,%lld)", (long long)D.rows, (long long)D.cols, (long long)M, (long long)N);
+  if (has_c && (C.rows != M || C.cols != N))
+    return fail(SL_ERR_SHAPE, "c is (%lld,%lld), expected (%lld,%lld)", (long long)C.rows, (long long)C.cols, (long long)M, (long long)N);
+  if ((s = scale_view("sfa", args->sfa, M, batch, &SA)) != SL_OK) return s;
+  if ((s = scale_view("sfb", args->sfb, N, batch, &SB)) != SL_OK) return s;
+  const View* all[6] = {&A, &B, has_c ? &C : nullptr, &D, &SA, &SB};
+  const char* names[6] = {"a", "b", "c", "d", "sfa", "sfb"};
+  for (int i = 0; i < 3; ++i)
+    if (all[i] && all[i]->t->layout.rank == 3 && all[i]->batch != batch)
+      return fail(SL_ERR_SHAPE, "%s has batch %lld, d has %lld", names[i], (long long)all[i]->batch, (long long)batch);
+  if (M >= kLim || N >= kLim || batch >= kLim) return fail(SL_ERR_SHAPE, "a dimension exceeds 2^31-1");
+  if (K >= kInt8MaxK) return fail(SL_ERR_SHAPE, "K is %lld, below %lld are summed exactly", (long long)K, (long long)kInt8MaxK);
+  RowsPlan& P = *out;
+  memset(&P, 0, sizeof P);
+  P.pub.kernel = K_I8;
+  P.pub.batch = batch, P.pub.m = M, P.pub.n = N, P.pub.k = K;
+  P.pub.split_k = 1;
+  P.empty = batch == 0 || M == 0 || N == 0;
+  if (P.empty) return SL_OK;
+  for (int i = 0; i < 6; ++i) {
+    if (!all[i] || (!all[i]->t->data && i < 2 && K == 0)) continue;
+    if ((s = check_data(names[i], *all[i]->t)) != SL_OK) return s;
+  }
+  if (!injective(D, batch)) return fail(SL_ERR_LAYOUT, "d's strides map distinct elements to one address");
+  for (int i = 0; i < 6; ++i) {
+    if (!all[i] || i == 3 || (i < 2 && K == 0)) continue;
+    if (i == 2 && args->c.data == args->d.data && same_layout(args->c, args->d)) continue;
+    if (overlap(*all[i], D, batch)) return fail(SL_ERR_ALIAS, "d overlaps %s", names[i]);
+  }
+  if (K > 0 && (K % 16 != 0 || !code_rows(A, batch) || !code_rows(B, batch)))
+    return fail(SL_ERR_LAYOUT, "i8 operands must be K-contiguous with 16-byte aligned rows and K %% 16 == 0");
+  for (const View* X : {&A, &B})
+    if ((std::min<int64_t>(X->rows, 256) - 1) * X->rs + K >= kLim)
+      return fail(SL_ERR_SHAPE, "a 256-row tile of an operand spans 2^31 bytes or more");
+  DenseParams& p = P.p;
+  p.a = (const uint8_t*)args->a.data, p.b[0] = (const uint8_t*)args->b.data;
+  p.a_rs = A.rs, p.a_bs = batch_stride(A), p.b_rs[0] = B.rs, p.b_bs[0] = batch_stride(B);
+  p.M = M, p.N = N, p.K = K;
+  p.sa = (const float*)args->sfa.data, p.sb[0] = (const float*)args->sfb.data;
+  p.sa_rs = SA.rs, p.sa_bs = batch_stride(SA), p.sb_rs[0] = SB.rs, p.sb_bs[0] = batch_stride(SB);
+  p.c = has_c ? args->c.data : nullptr, p.d = args->d.data;
+  if (has_c) p.c_rs = C.rs, p.c_cs = C.cs, p.c_bs = batch_stride(C);
+  p.d_rs = D.rs, p.d_cs = D.cs, p.d_bs = batch_stride(D);
+  p.type = type, p.batch = (int32_t)batch;
+  p.flags = (quad_rows(D, batch) ? DF_D_VEC : 0) | (has_c && quad_rows(C, batch) ? DF_C_VEC : 0);
+  P.tile = dense_plan(EK_I8, false, batch, M, N, K);
+  if ((s = place_tiles(&p, P.tile, false)) != SL_OK) return s;
+  P.pub.a_load = P.pub.b_load = LOAD_KVEC;
+  P.pub.tile_m = P.tile.bm, P.pub.tile_n = P.tile.bn, P.pub.tile_k = (int32_t)kDenseKBytes;
+  P.pub.threads = P.tile.threads, P.pub.lds_bytes = P.tile.lds;
+  P.pub.workgroups = batch * p.tiles_m * p.tiles_n;
+  return SL_OK;
+}
+
+sl_status run_int8(const sl_gemm_args* args, void* stream) {
+  RowsPlan P;
+  sl_status s = plan_int8(args, &P);
+  if (s != SL_OK) return s;
+  if (P.empty) return SL_OK;
+  if ((s = check_arch()) != SL_OK) return s;
+  const hipError_t e = launch_gemm_i8(P.p, P.tile, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
+  return SL_OK;
+}
+
+}  // namespace host
+}  // namespace sl
+
+using namespace sl::host;
+
+extern "C" {
+
+sl_status sl_quantize_rows(const sl_quantize_rows_args* args, void* stream) {
+  g_msg.clear();
+  if (!args) return fail(SL_ERR_NULL, "args is NULL");
+  const int32_t type = op_type(args->x.dtype);
+  if (type < 0) return fail(SL_ERR_DTYPE, "x must be f16, bf16 or f32");
+  if (args->q.dtype != SL_I8) return fail(SL_ERR_DTYPE, "q must be i8");
+  View X, Q, S;
+  sl_status s;
+  if ((s = make_view("x", args->x, &X)) != SL_OK) return s;
+  if ((s = make_view("q", args->q, &Q)) != SL_OK) return s;
+  if ((s = scale_view("s", args->s, X.rows, X.batch, &S)) != SL_OK) return s;
+  const int64_t batch = X.batch, R = X.rows, C = X.cols;
+  if (Q.batch != batch || S.batch != batch) return fail(SL_ERR_SHAPE, "q and s must have x's batch of %lld", (long long)batch);
+  if (R >= kLim - 128 || C >= kLim - 128 || batch >= kLim) return fail(SL_ERR_SHAPE, "a dimension exceeds 2^31-129");
+  if (Q.rows != R || Q.cols < C || Q.cols > 128 * ceil_div(C, 128))
+    return fail(SL_ERR_SHAPE, "q is (%lld,%lld), expected %lld rows of %lld to %lld codes", (long long)Q.rows, (long long)Q.cols,
+                (long long)R, (long long)C, (long long)(128 * ceil_div(C, 128)));
+  if (batch == 0 || R == 0) return SL_OK;
+  if ((s = check_data("s", args->s)) != SL_OK) return s;
+  if (!injective(S, batch)) return fail(SL_ERR_LAYOUT, "s's strides map distinct elements to one address");
+  if (C > 0) {
+    if ((s = check_data("x", args->x)) != SL_OK) return s;
+    if ((s = check_data("q", args->q)) != SL_OK) return s;
+    if (!code_rows(Q, batch)) return fail(SL_ERR_LAYOUT, "q must be contiguous along its last axis with 16-byte aligned rows");
+    if (!injective(Q, batch)) return fail(SL_ERR_LAYOUT, "q's strides map distinct elements to one address");
+    if (overlap(Q, X, batch)) return fail(SL_ERR_ALIAS, "q overlaps x");
+    if (overlap(S, X, batch)) return fail(SL_ERR_ALIAS, "s overlaps x");
+    if (overlap(S, Q, batch)) return fail(SL_ERR_ALIAS, "s overlaps q");
+  }
+  sl::QuantizeRowsParams p{};
+  p.x = args->x.data, p.q = (int8_t*)args->q.data, p.s = (float*)args->s.data;
+  p.rows = R, p.cols = C, p.x_bs = batch_stride(X), p.x_rs = X.rs, p.x_cs = X.cs;
+  p.q_cols = Q.cols, p.q_bs = batch_stride(Q), p.q_rs = Q.rs, p.s_bs = batch_stride(S), p.s_rs = S.rs;
+  p.type = type, p.batch = (int32_t)batch;
+  if (!grid_fits(batch, R, 1, 1) || !grid_fits(sl::quantize_rows_groups(p), 1, 1, sl::quantize_rows_threads(p)))
+    return fail(SL_ERR_SHAPE, "too many rows (batch %lld of %lld)", (long long)batch, (long long)R);
+  if ((s = check_arch()) != SL_OK) return s;
+  const hipError_t e = sl::launch_quantize_rows(p, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
+  return SL_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// the caller's workspace against what a plan needs and the operands
+sl_status check_workspace(void* ws, int64_t given, int64_t needed, const View* const* views, const char* const* names, int n) {
+  if (!needed) return SL_OK;
+  if (!ws) return fail(SL_ERR_NULL, "workspace is NULL, %lld bytes are needed", (long long)needed);
+  if (given < needed) return fail(SL_ERR_SHAPE, "workspace of %lld bytes, %lld are needed", (long long)given, (long long)needed);
+  const uintptr_t lo = (uintptr_t)ws, hi = lo + (uintptr_t)needed;
+  if (lo % 16) return fail(SL_ERR_ALIGN, "workspace is not on a 16-byte boundary");
+  for (int i = 0; i < n; ++i) {
+    if (!views[i] || !views[i]->t->data) continue;
+    uintptr_t l, h;
+    byte_range(*views[i], views[i]->batch, &l, &h);
+    if (l < hi && lo < h) return fail(SL_ERR_ALIAS, "workspace overlaps %s", names[i]);
+  }
+  return SL_OK;
+}
+
+bool has_values(const View& v) { return v.batch > 0 && v.rows > 0 && v.cols > 0; }
+
+// Two views hold no element in common: their address ranges are apart, or they
+// are alike and one lies between the rows or columns of the other (the two
+// halves of a matrix that holds both).
+bool apart(const View& a, const View& b) {
+  uintptr_t al, ah, bl, bh;
+  byte_range(a, a.batch, &al, &ah);
+  byte_range(b, b.batch, &bl, &bh);
+  if (ah <= bl || bh <= al) return true;
+  if (a.t->dtype != b.t->dtype || a.batch != b.batch || a.rows != b.rows || a.cols != b.cols || a.bs != b.bs || a.rs != b.rs || a.cs != b.cs)
+    return false;
+  const int64_t es = elem_size(a.t->dtype);
+  const uintptr_t off = al > bl ? al - bl : bl - al;
+  if (off % es) return false;
+  struct Dim {
+    int64_t n, s;
+  } d[4] = {{a.batch, a.bs}, {a.rows, a.rs}, {a.cols, a.cs}, {2, (int64_t)(off / es)}};
+  std::sort(d, d + 4, [](const Dim& x, const Dim& y) { return x.s < y.s; });
+  int64_t span = 0;
+  for (const Dim& x : d) {
+    if (x.n <= 1) continue;
+    if (x.s <= span) return false;
+    span += x.s * (x.n - 1);
+  }
+  return true;
+}
+
+// The data of every view that is there and holds values, and the outputs (from
+// `first` on) apart from everything else.
+sl_status check_operands(const View* const* views, const char* const* names, int n, int first) {
+  sl_status s;
+  for (int i = 0; i < n; ++i)
+    if (views[i] && has_values(*views[i]) && (s = check_data(names[i], *views[i]->t)) != SL_OK) return s;
+  for (int i = first; i < n; ++i) {
+    if (!views[i] || !has_values(*views[i])) continue;
+    if (!injective(*views[i], views[i]->batch)) return fail(SL_ERR_LAYOUT, "%s's strides map distinct elements to one address", names[i]);
+    for (int j = 0; j < i; ++j) {
+      if (!views[j] || !has_values(*views[j])) continue;
+      if (!apart(*views[i], *views[j])) return fail(SL_ERR_ALIAS, "%s overlaps %s", names[i], names[j]);
+    }
+  }
+  return SL_OK;
+}
+
+bool valid_activation(int32_t a) { return a >= SL_SILU && a <= SL_RELU; }
+
+// shape (batch?, rows, cols) of a view: rank 3 with this batch, or rank 2 where
+// that is allowed
+sl_status check_shape(const char* name, const View& v, int64_t batch, int64_t rows, int64_t cols, bool shared, bool rank3) {
+  if (v.rows != rows || v.cols != cols)
+    return fail(SL_ERR_SHAPE, "%s is (%lld,%lld), expected (%lld,%lld)", name, (long long)v.rows, (long long)v.cols, (long long)rows,
+                (long long)cols);
+  if (v.t->layout.rank == 2 ? rank3 && !shared : !rank3 || v.batch != batch)
+    return fail(SL_ERR_SHAPE, "%s has another batch than the result's %lld", name, (long long)batch);
+  return SL_OK;
+}
+
+// A batch whose matrices follow each other is one matrix of all their rows.
+bool follows(const View& v) { return v.bs == v.rows * v.rs || v.rows == 1; }
+View flattened(View v) {
+  if (v.rows == 1) v.rs = v.bs;
+  v.rows *= v.batch, v.batch = 1, v.bs = 0;
+  return v;
+}
+
+struct GatedPlan {
+  sl::DenseParams p;
+  sl::DensePlan tile;
+  int32_t kind;
+  sl::PackParams pack[3];  // x, w_gate, w_up; rows 0: read as it lies
+  int64_t offset[3], ws_bytes;
+  bool empty;
+  View v[9];
+};
+
+// batch strides count for rank 3 alone
+int64_t bstride(const View& v) { return v.batch > 1 ? v.bs : 0; }
+
+sl_status plan_gated(const sl_gated_args* args, GatedPlan* out) {
+  g_msg.clear();
+  if (!args) return fail(SL_ERR_NULL, "args is NULL");
+  GatedPlan& P = *out;
+  memset((void*)&P, 0, sizeof P);
+  const bool i8 = args->x.dtype == SL_I8;
+  if (args->x.dtype != SL_F16 && args->x.dtype != SL_BF16 && !i8) return fail(SL_ERR_DTYPE, "x must be f16, bf16 or i8");
+  if (args->w_gate.dtype != args->x.dtype || args->w_up.dtype != args->x.dtype)
+    return fail(SL_ERR_DTYPE, "w_gate and w_up must have x's dtype");
+  const int32_t type = op_type(args->h.dtype);
+  if (type < 0 || (!i8 && args->h.dtype != args->x.dtype))
+    return fail(SL_ERR_DTYPE, i8 ? "h must be f16, bf16 or f32" : "h must have x's dtype");
+  const bool keep = args->gate.data || args->up.data;
+  if (keep && (args->gate.dtype != args->h.dtype || args->up.dtype != args->h.dtype))
+    return fail(SL_ERR_DTYPE, "gate and up must have h's dtype");
+  if (!i8 && (args->sx.data || args->s_gate.data || args->s_up.data)) return fail(SL_ERR_DTYPE, "scales given for 16-bit operands");
+  if (!valid_activation(args->activation)) return fail(SL_ERR_ARG, "activation %d", args->activation);
+  enum { X, WG, WU, SX, SG, SU, H, G, U, COUNT };
+  static const char* const names[COUNT] = {"x", "w_gate", "w_up", "sx", "s_gate", "s_up", "h", "gate", "up"};
+  const sl_tensor* t[COUNT] = {&args->x, &args->w_gate, &args->w_up, &args->sx, &args->s_gate, &args->s_up, &args->h, &args->gate, &args->up};
+  View* v = P.v;
+  const View* used[COUNT];
+  sl_status s;
+  for (int i = 0; i < COUNT; ++i) {
+    used[i] = nullptr;
+    if ((i >= SX && i <= SU && !i8) || (i >= G && !keep)) continue;
+    if ((s = make_view(names[i], *t[i], &v[i])) != SL_OK) return s;
+    used[i] = &v[i];
+  }
+  const bool rank3 = args->h.layout.rank == 3;
+  const int64_t batch = v[H].batch, M = v[H].rows, F = v[H].cols, K = v[X].cols;
+  if ((s = check_shape("x", v[X], batch, M, K, true, rank3)) != SL_OK) return s;
+  for (int i : {(int)WG, (int)WU})
+    if ((s = check_shape(names[i], v[i], batch, F, K, true, rank3)) != SL_OK) return s;
+  for (int i : {(int)G, (int)U})
+    if (used[i] && (s = check_shape(names[i], v[i], batch, M, F, false, rank3)) != SL_OK) return s;
+  if (i8) {
+    if ((s = scale_view("sx", args->sx, M, batch, &v[SX])) != SL_OK) return s;
+    if ((s = scale_view("s_gate", args->s_gate, F, batch, &v[SG])) != SL_OK) return s;
+    if ((s = scale_view("s_up", args->s_up, F, batch, &v[SU])) != SL_OK) return s;
+  }
+  if (M >= kLim || F >= kLim / 2 || K >= kLim / 2 || batch >= kLim) return fail(SL_ERR_SHAPE, "a dimension exceeds its limit");
+  if (i8 && K >= kInt8MaxK) return fail(SL_ERR_SHAPE, "K is %lld, below %lld are summed exactly", (long long)K, (long long)kInt8MaxK);
+  P.empty = batch == 0 || M == 0 || F == 0;
+  if (P.empty) return SL_OK;
+  if (keep && (!args->gate.data || !args->up.data)) return fail(SL_ERR_NULL, "gate and up are kept together");
+  if ((s = check_operands(used, names, COUNT, H)) != SL_OK) return s;
+
+  // one matrix of all tokens where the weights are shared: a token of each of
+  // many sequences is a batch of one row each
+  auto shared = [&](int i) { return !used[i] || v[i].t->layout.rank == 2 || v[i].bs == 0; };
+  bool flat = batch > 1 && shared(WG) && shared(WU) && shared(SG) && shared(SU) && batch * M < kLim;
+  for (int i : {(int)X, (int)SX, (int)H, (int)G, (int)U}) flat = flat && (!used[i] || (v[i].t->layout.rank == 3 && follows(v[i])));
+  View w[COUNT];
+  for (int i = 0; i < COUNT; ++i) {
+    w[i] = v[i];
+    if (!used[i]) continue;
+    if (flat && (i == X || i == SX || i >= H)) w[i] = flattened(v[i]);
+    else if (flat) w[i].batch = 1, w[i].bs = 0;
+    else if (w[i].t->layout.rank == 2) w[i].bs = 0;
+  }
+  sl::DenseParams& p = P.p;
+  p.batch = (int32_t)(flat ? 1 : batch);
+  p.M = flat ? batch * M : M, p.N = F;
+  const int64_t es = i8 ? 1 : 2;
+  int64_t k_bytes = K * es;
+  const uint8_t* data[3] = {(const uint8_t*)args->x.data, (const uint8_t*)args->w_gate.data, (const uint8_t*)args->w_up.data};
+  int64_t rs[3], bs[3];
+  for (int i = 0; i < 3; ++i) rs[i] = w[i].rs * es, bs[i] = bstride(w[i]) * es;
+  if (i8) {
+    for (int i = 0; i < 3; ++i)
+      if (K > 0 && (K % 16 != 0 || !code_rows(w[i], w[i].batch)))
+        return fail(SL_ERR_LAYOUT, "i8 operands must be K-contiguous with 16-byte aligned rows and K %% 16 == 0");
+    for (int i = 0; i < 3; ++i)
+      if ((std::min<int64_t>(w[i].rows, 256) - 1) * w[i].rs + K >= kLim)
+        return fail(SL_ERR_SHAPE, "a 256-row tile of an operand spans 2^31 bytes or more");
+  } else if (K > 0) {
+    const int64_t Kp = round_up(K, 8);
+    for (int i = 0; i < 3; ++i) {
+      if (rows_ready(w[i], w[i].batch, 2)) continue;
+      if ((std::min<int64_t>(w[i].rows, 256)) * Kp * 2 >= kLim) return fail(SL_ERR_SHAPE, "a 256-row tile of an operand spans 2^31 bytes or more");
+      sl::PackParams& q = P.pack[i];
+      q.x = (const uint16_t*)data[i];
+      q.rows = w[i].rows, q.cols = K, q.width = Kp;
+      q.batch = (int32_t)(bstride(w[i]) ? w[i].batch : 1);
+      q.x_bs = bstride(w[i]), q.x_rs = w[i].rs, q.x_cs = w[i].cs, q.out_rs = Kp, q.out_bs = w[i].rows * Kp;
+      if (!grid_fits(q.batch, q.rows, ceil_div(Kp, 8), 1) || !grid_fits(sl::pack_groups(q), 1, 1, sl::kPackThreads))
+        return fail(SL_ERR_SHAPE, "%s is too large to be copied", names[i]);
+      P.offset[i] = P.ws_bytes;
+      P.ws_bytes += round_up(q.batch * q.out_bs * 2, 256);
+      rs[i] = Kp * 2, bs[i] = q.batch > 1 ? q.out_bs * 2 : 0;
+    }
+    k_bytes = Kp * 2;
+  }
+  p.K = k_bytes;
+  p.a = data[0], p.a_rs = rs[0], p.a_bs = bs[0];
+  for (int i = 0; i < 2; ++i) p.b[i] = data[1 + i], p.b_rs[i] = rs[1 + i], p.b_bs[i] = bs[1 + i];
+  if (i8) {
+    p.sa = (const float*)args->sx.data, p.sa_rs = w[SX].rs, p.sa_bs = bstride(w[SX]);
+    p.sb[0] = (const float*)args->s_gate.data, p.sb_rs[0] = w[SG].rs, p.sb_bs[0] = bstride(w[SG]);
+    p.sb[1] = (const float*)args->s_up.data, p.sb_rs[1] = w[SU].rs, p.sb_bs[1] = bstride(w[SU]);
+  }
+  p.d = args->h.data, p.d_rs = w[H].rs, p.d_cs = w[H].cs, p.d_bs = bstride(w[H]);
+  p.flags = quad_rows(w[H], p.batch) ? sl::DF_D_VEC : 0;
+  if (keep)
+    for (int i = 0; i < 2; ++i) {
+      const View& k = w[G + i];
+      p.kept[i] = t[G + i]->data, p.kept_rs[i] = k.rs, p.kept_cs[i] = k.cs, p.kept_bs[i] = bstride(k);
+      if (quad_rows(k, p.batch)) p.flags |= sl::DF_KEPT_VEC << i;
+    }
+  p.type = type, p.act = args->activation - SL_SILU;
+  P.kind = i8 ? sl::EK_I8 : args->x.dtype == SL_F16 ? sl::EK_F16 : sl::EK_BF16;
+  P.tile = sl::dense_plan(P.kind, true, p.batch, p.M, F, k_bytes);
+  return place_tiles(&p, P.tile, true);
+}
+
+}  // namespace
+
+extern "C" {
+
+sl_status sl_gated_workspace_bytes(const sl_gated_args* args, int64_t* bytes) {
+  g_msg.clear();
+  if (!bytes) return fail(SL_ERR_NULL, "bytes is NULL");
+  GatedPlan P;
+  const sl_status s = plan_gated(args, &P);
+  if (s == SL_OK) *bytes = P.ws_bytes;
+  return s;
+}
+
+sl_status sl_gated(const sl_gated_args* args, void* stream) {
+  GatedPlan P;
+  sl_status s = plan_gated(args, &P);
+  if (s != SL_OK) return s;
+  if (P.empty) return SL_OK;
+  const bool i8 = args->x.dtype == SL_I8, keep = args->gate.data != nullptr;
+  const View* views[9] = {&P.v[0], &P.v[1], &P.v[2], i8 ? &P.v[3] : nullptr, i8 ? &P.v[4] : nullptr, i8 ? &P.v[5] : nullptr, &P.v[6],
+                          keep ? &P.v[7] : nullptr, keep ? &P.v[8] : nullptr};
+  const char* const names[9] = {"x", "w_gate", "w_up", "sx", "s_gate", "s_up", "h", "gate", "up"};
+  if ((s = check_workspace(args->workspace, args->workspace_bytes, P.ws_bytes, views, names, 9)) != SL_OK) return s;
+  if ((s = check_arch()) != SL_OK) return s;
+  hipError_t e = hipSuccess;
+  for (int i = 0; i < 3 && e == hipSuccess; ++i) {
+    if (!P.pack[i].rows) continue;
+    P.pack[i].out = (uint16_t*)((char*)args->workspace + P.offset[i]);
+    (i == 0 ? P.p.a : P.p.b[i - 1]) = (const uint8_t*)P.pack[i].out;
+    e = sl::launch_pack(P.pack[i], (hipStream_t)stream);
+  }
+  if (e == hipSuccess) e = sl::launch_gated(P.p, P.kind, P.tile, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
+  return SL_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+struct BackwardPlan {
+  sl::GatedSlopeParams slope;
+  sl::PackParams xt, wt[2];   // rows 0: not made
+  sl_gemm_args dx, dw[2];     // data pointers hold offsets into the workspace until the launch
+  int32_t dw_calls;           // 1: both weights' gradients as a batch of two
+  bool want_dx, want_dw, launch;
+  int64_t off_rows, off_t, off_xt, off_wt, off_gemm, ws_bytes, gemm_bytes;
+  View v[9];
+};
+
+sl_tensor matrix(void* data, int32_t dtype, int64_t batch, int64_t rows, int64_t cols, int64_t bs, int64_t rs, int64_t cs) {
+  sl_tensor t{};
+  t.data = data, t.dtype = dtype;
+  if (batch < 0) {
+    t.layout = sl_layout{2, {rows, cols, 0}, {rs, cs, 0}};
+  } else {
+    t.layout = sl_layout{3, {batch, rows, cols}, {bs, rs, cs}};
+  }
+  return t;
+}
+
+sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
+  g_msg.clear();
+  if (!args) return fail(SL_ERR_NULL, "args is NULL");
+  BackwardPlan& P = *out;
+  memset((void*)&P, 0, sizeof P);
+  const int32_t dt = args->dh.dtype;
+  if (dt != SL_F16 && dt != SL_BF16) return fail(SL_ERR_DTYPE, "dh must be f16 or bf16");
+  enum { DH, X, WG, WU, G, U, DX, DWG, DWU, COUNT };
+  static const char* const names[COUNT] = {"dh", "x", "w_gate", "w_up", "gate", "up", "dx", "dw_gate", "dw_up"};
+  const sl_tensor* t[COUNT] = {&args->dh, &args->x, &args->w_gate, &args->w_up, &args->gate, &args->up, &args->dx, &args->dw_gate, &args->dw_up};
+  View* v = P.v;
+  const View* used[COUNT];
+  sl_status s;
+  P.want_dx = args->dx.data, P.want_dw = args->dw_gate.data || args->dw_up.data;
+  if (!valid_activation(args->activation)) return fail(SL_ERR_ARG, "activation %d", args->activation);
+  for (int i = 0; i < COUNT; ++i) {
+    used[i] = nullptr;
+    if ((i == DX && !P.want_dx) || (i >= DWG && !P.want_dw)) continue;
+    if (t[i]->dtype != dt) return fail(SL_ERR_DTYPE, "%s must have dh's dtype", names[i]);
+    if ((s = make_view(names[i], *t[i], &v[i])) != SL_OK) return s;
+    used[i] = &v[i];
+  }
+  const bool rank3 = args->dh.layout.rank == 3;
+  const int64_t batch = v[DH].batch, M = v[DH].rows, F = v[DH].cols, K = v[X].cols;
+  if ((s = check_shape("x", v[X], batch, M, K, false, rank3)) != SL_OK) return s;
+  for (int i : {(int)WG, (int)WU})
+    if ((s = check_shape(names[i], v[i], batch, F, K, true, rank3)) != SL_OK) return s;
+  for (int i : {(int)G, (int)U})
+    if ((s = check_shape(names[i], v[i], batch, M, F, false, rank3)) != SL_OK) return s;
+  if (v[WG].t->layout.rank != v[WU].t->layout.rank) return fail(SL_ERR_SHAPE, "w_gate and w_up must have one rank");
+  const bool one_weight = v[WG].t->layout.rank == 2;  // for every matrix of the batch
+  if (P.want_dx && (s = check_shape("dx", v[DX], batch, M, K, false, rank3)) != SL_OK) return s;
+  for (int i : {(int)DWG, (int)DWU})
+    if (P.want_dw && (s = check_shape(names[i], v[i], batch, F, K, false, !one_weight)) != SL_OK) return s;
+  if (M >= kLim / 2 || F >= kLim / 4 || K >= kLim / 2 || batch >= kLim) return fail(SL_ERR_SHAPE, "a dimension exceeds its limit");
+  if (P.want_dw && K > 0 && F > 0 && (!args->dw_gate.data || !args->dw_up.data)) return fail(SL_ERR_NULL, "dw_gate and dw_up are wanted together");
+  P.want_dx = P.want_dx && has_values(v[DX]);
+  P.want_dw = P.want_dw && has_values(v[DWG]);
+  if (!P.want_dx && !P.want_dw) return SL_OK;
+  P.launch = true;
+  if ((s = check_operands(used, names, COUNT, DX)) != SL_OK) return s;
+
+  // one matrix of all tokens where the weights are shared
+  bool flat = rank3 && one_weight && batch > 0 && batch * M < kLim / 2;
+  for (int i : {(int)DH, (int)X, (int)G, (int)U, (int)DX}) flat = flat && (!used[i] || follows(v[i]));
+  View w[COUNT];
+  for (int i = 0; i < COUNT; ++i) {
+    w[i] = v[i];
+    if (!used[i]) continue;
+    if (flat && i != WG && i != WU && i < DWG) w[i] = flattened(v[i]);
+    if (w[i].t->layout.rank == 2) w[i].bs = 0;
+  }
+  const int64_t n = flat ? 1 : batch, rows = w[DH].rows;  // matrices, and rows of each
+  const int64_t Fp = round_up(F, 64), Mp = round_up(rows, 64);
+  const bool tokens = n > 0 && rows > 0 && F > 0;
+  const int64_t weights = one_weight ? 1 : n;          // matrices of weights
+  const int64_t across = one_weight ? n * Mp : Mp;     // values of a row of a transpose over the tokens
+  if (tokens && !grid_fits(n, ceil_div(rows, 64), ceil_div(F, 64), sl::kPackThreads)) return fail(SL_ERR_SHAPE, "dh is too large");
+  if (across >= kLim || n * rows >= kLim) return fail(SL_ERR_SHAPE, "too many rows in all");
+
+  sl::GatedSlopeParams& g = P.slope;
+  g.g = (const uint16_t*)args->gate.data, g.u = (const uint16_t*)args->up.data, g.dh = (const uint16_t*)args->dh.data;
+  g.M = rows, g.F = F, g.Fp = Fp, g.Mp = Mp;
+  g.g_bs = bstride(w[G]), g.g_rs = w[G].rs, g.g_cs = w[G].cs;
+  g.u_bs = bstride(w[U]), g.u_rs = w[U].rs, g.u_cs = w[U].cs;
+  g.dh_bs = bstride(w[DH]), g.dh_rs = w[DH].rs, g.dh_cs = w[DH].cs;
+  g.type = dt == SL_F16 ? sl::OT_F16 : sl::OT_BF16, g.act = args->activation - SL_SILU, g.batch = (int32_t)(tokens ? n : 0);
+  g.t_bs = one_weight ? Mp : 2 * Fp * Mp, g.t_rs = across, g.t_us = Fp * across;
+
+  auto take = [&](int64_t values) {
+    const int64_t at = P.ws_bytes;
+    P.ws_bytes += round_up(2 * values, 256);
+    return at;
+  };
+  // a transpose: out row r is x's column r
+  auto transpose = [&](sl::PackParams* q, const View& x, int64_t count, int64_t width, int64_t out_bs, int64_t out_rs) -> sl_status {
+    q->x = (const uint16_t*)x.t->data;
+    q->rows = x.cols, q->cols = x.rows, q->width = width;
+    q->x_bs = bstride(x), q->x_rs = x.cs, q->x_cs = x.rs, q->out_bs = out_bs, q->out_rs = out_rs;
+    q->batch = (int32_t)count;
+    if (!grid_fits(count, ceil_div(q->rows, 64), ceil_div(width, 64), sl::kPackThreads) ||
+        !grid_fits(count, q->rows, ceil_div(width, 8), 1) || !grid_fits(sl::pack_groups(*q), 1, 1, sl::kPackThreads))
+      return fail(SL_ERR_SHAPE, "an operand is too large to be transposed");
+    return SL_OK;
+  };
+  int64_t bytes;
+  auto product = [&](sl_gemm_args* a) -> sl_status {
+    const sl_status e = sl_gemm_workspace_bytes(a, &bytes);
+    if (e == SL_OK) P.gemm_bytes = std::max(P.gemm_bytes, bytes);
+    return e;
+  };
+  // operands in the workspace carry stand-in addresses through the plan: they
+  // are compared with nothing but 16-byte boundaries and the outputs
+  void* const stand_in = (void*)(uintptr_t)(uint64_t(1) << 62);
+  if (P.want_dx) {
+    if (tokens) {
+      P.off_rows = take(n * rows * 2 * Fp);
+      P.off_wt = take(weights * K * 2 * Fp);
+      for (int i = 0; i < 2; ++i)
+        if ((s = transpose(&P.wt[i], w[WG + i], weights, Fp, K * 2 * Fp, 2 * Fp)) != SL_OK) return s;
+    }
+    P.dx.a = matrix(tokens ? stand_in : nullptr, dt, n, rows, tokens ? 2 * Fp : 0, rows * 2 * Fp, 2 * Fp, 1);
+    P.dx.b = matrix(tokens ? stand_in : nullptr, dt, one_weight ? -1 : n, K, tokens ? 2 * Fp : 0, K * 2 * Fp, 2 * Fp, 1);
+    P.dx.c.layout.rank = 2;
+    P.dx.d = matrix(args->dx.data, dt, n, rows, K, w[DX].bs, w[DX].rs, w[DX].cs);
+    if ((s = product(&P.dx)) != SL_OK) return s;
+  }
+  if (P.want_dw) {
+    if (tokens) {
+      P.off_t = take(one_weight ? 2 * Fp * across : n * 2 * Fp * Mp);
+      P.off_xt = take(one_weight ? K * across : n * K * Mp);
+      if ((s = transpose(&P.xt, w[X], n, Mp, one_weight ? Mp : K * Mp, across)) != SL_OK) return s;
+    }
+    const int64_t depth = tokens ? across : 0;
+    const int64_t apart = ((intptr_t)args->dw_up.data - (intptr_t)args->dw_gate.data) / 2;
+    // both as a batch of two where dw_up lies behind dw_gate in the same strides
+    const bool pair = weights == 1 && v[DWG].rs == v[DWU].rs && v[DWG].cs == v[DWU].cs &&
+                      apart > (F - 1) * v[DWG].rs + (K - 1) * v[DWG].cs;
+    P.dw_calls = pair ? 1 : 2;
+    for (int i = 0; i < P.dw_calls; ++i) {
+      sl_gemm_args& a = P.dw[i];
+      const int64_t count = pair ? 2 : one_weight ? -1 : n;
+      void* const at = tokens ? stand_in : nullptr;
+      a.a = matrix(at, dt, count, F, depth, pair ? Fp * across : 2 * Fp * Mp, across, 1);
+      a.b = matrix(at, dt, pair || one_weight ? -1 : n, K, depth, K * Mp, across, 1);
+      a.c.layout.rank = 2;
+      const View& d = v[DWG + i];
+      a.d = matrix(t[DWG + i]->data, dt, count, F, K, pair ? apart : d.bs, d.rs, d.cs);
+      if ((s = product(&a)) != SL_OK) return s;
+    }
+  }
+  P.off_gemm = P.ws_bytes;
+  P.ws_bytes += P.gemm_bytes;
+  return SL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+sl_status sl_gated_backward_workspace_bytes(const sl_gated_backward_args* args, int64_t* bytes) {
+  g_msg.clear();
+  if (!bytes) return fail(SL_ERR_NULL, "bytes is NULL");
+  BackwardPlan P;
+  const sl_status s = plan_backward(args, &P);
+  if (s == SL_OK) *bytes = P.ws_bytes;
+  return s;
+}
+
+sl_status sl_gated_backward(const sl_gated_backward_args* args, void* stream) {
+  BackwardPlan P;
+  sl_status s = plan_backward(args, &P);
+  if (s != SL_OK) return s;
+  if (!P.launch) return SL_OK;
+  const View* views[9];
+  for (int i = 0; i < 9; ++i) views[i] = P.v[i].t ? &P.v[i] : nullptr;
+  static const char* const names[9] = {"dh", "x", "w_gate", "w_up", "gate", "up", "dx", "dw_gate", "dw_up"};
+  if ((s = check_workspace(args->workspace, args->workspace_bytes, P.ws_bytes, views, names, 9)) != SL_OK) return s;
+  if ((s = check_arch()) != SL_OK) return s;
+  const hipStream_t st = (hipStream_t)stream;
+  char* const ws = (char*)args->workspace;
+  auto at = [&](int64_t off) { return (uint16_t*)(ws + off); };
+  const bool tokens = P.slope.batch > 0;
+  hipError_t e = hipSuccess;
+  if (tokens) {
+    if (P.want_dx) P.slope.rows = at(P.off_rows);
+    if (P.want_dw) P.slope.t = at(P.off_t);
+    e = sl::launch_gated_slope(P.slope, st);
+    if (P.want_dx) {
+      for (int i = 0; i < 2 && e == hipSuccess; ++i) {
+        P.wt[i].out = at(P.off_wt) + i * P.slope.Fp;
+        e = sl::launch_pack(P.wt[i], st);
+      }
+      P.dx.a.data = at(P.off_rows), P.dx.b.data = at(P.off_wt);
+    }
+    if (P.want_dw && e == hipSuccess) {
+      P.xt.out = at(P.off_xt);
+      e = sl::launch_pack(P.xt, st);
+      for (int i = 0; i < P.dw_calls; ++i) P.dw[i].a.data = at(P.off_t) + i * P.slope.t_us, P.dw[i].b.data = at(P.off_xt);
+    }
+    if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
+  }
+  auto run = [&](sl_gemm_args* a) {
+    a->workspace = ws + P.off_gemm, a->workspace_bytes = P.gemm_bytes;
+    return sl_gemm(a, stream);
+  };
+  if (P.want_dx && (s = run(&P.dx)) != SL_OK) return s;
+  for (int i = 0; P.want_dw && i < P.dw_calls; ++i)
+    if ((s = run(&P.dw[i])) != SL_OK) return s;
+  return SL_OK;
+}
+
+}  // extern "C"

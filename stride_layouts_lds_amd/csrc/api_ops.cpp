@@ -11,41 +11,6 @@
 namespace sl {
 namespace host {
 
-constexpr int64_t kLim = (int64_t)1 << 31;
-
-static int32_t op_type(int32_t dtype) {
-  switch (dtype) {
-    case SL_F16: return OT_F16;
-    case SL_BF16: return OT_BF16;
-    case SL_F32: return OT_F32;
-    default: return -1;
-  }
-}
-
-static int64_t batch_stride(const View& v) { return v.t->layout.rank == 3 ? v.bs : 0; }
-static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// data present and aligned to its element
-static sl_status check_data(const char* name, const sl_tensor& t) {
-  if (!t.data) return fail(SL_ERR_NULL, "%s.data is NULL", name);
-  if ((uintptr_t)t.data % elem_size(t.dtype)) return fail(SL_ERR_ALIGN, "%s.data is not aligned to its %d-byte element", name, elem_size(t.dtype));
-  return SL_OK;
-}
-
-// rows of E4M3 codes: contiguous along the last axis, every row on a 16-byte
-// boundary
-static bool code_rows(const View& v, int64_t batch) {
-  return v.cs == 1 && (v.rows <= 1 || v.rs % 16 == 0) && (uintptr_t)v.t->data % 16 == 0 &&
-         (v.t->layout.rank == 2 || batch <= 1 || v.bs % 16 == 0);
-}
-
-static bool overlap(const View& x, const View& y, int64_t batch) {
-  uintptr_t xl, xh, yl, yh;
-  byte_range(x, batch, &xl, &xh);
-  byte_range(y, batch, &yl, &yh);
-  return xl < yh && yl < xh;
-}
-
 // The tile: up to 64 rows of A stream the weight once (the skinny kernels),
 // and so do products of up to 64 tiles of 128 x 128, which would leave most
 // CUs without work (128 x 512 x 8192: 54 us in those tiles, 14 us streamed in 64

@@ -1,5 +1,5 @@
-// api_ops.hpp -- the block-scaled 8-bit form of sl_gemm: api.cpp sends a call
-// with fp32 scales here.  Host only.
+// api_ops.hpp -- the 8-bit forms of sl_gemm with fp32 scales: api.cpp sends
+// such a call here.  Host only.
 #pragma once
 #include "../../include/sl.h"
 #include "sl_ops.hpp"
@@ -20,6 +20,18 @@ inline bool is_block_gemm(const sl_gemm_args* args) {
 }
 sl_status plan_block(const sl_gemm_args* args, BlockPlan* out);
 sl_status run_block(const sl_gemm_args* args, void* stream);
+
+struct RowsPlan {
+  sl_plan pub;
+  DenseParams p;
+  DensePlan tile;
+  bool empty;
+};
+
+// a and b int8 with one fp32 scale per row (api_gated.cpp)
+inline bool is_int8_gemm(const sl_gemm_args* args) { return args && args->a.dtype == SL_I8; }
+sl_status plan_int8(const sl_gemm_args* args, RowsPlan* out);
+sl_status run_int8(const sl_gemm_args* args, void* stream);
 
 }  // namespace host
 }  // namespace sl

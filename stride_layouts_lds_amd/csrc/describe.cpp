@@ -80,6 +80,8 @@ InstrInfo instr_of(const DescribeInput& in) {
   const bool bf16 = in.flags & F_BF16;
   switch (in.kernel) {
     case K_BLOCK8: return {MFMA16_F8, "v_mfma_scale_f32_16x16x128_f8f6f4 (E4M3 data, unit scales)", 16, 128, 16};
+    // (the fp16 instruction's map in bytes: 16 consecutive values a lane)
+    case K_I8: return {MFMA16_F16, "v_mfma_i32_16x16x64_i8", 16, 64, 16};
     case K_MX: return {MFMA16_F8, "v_mfma_scale_f32_16x16x128_f8f6f4 (E4M3 data, E8M0 scales)", 16, 128, 16};
     case K_MX_W8:
     case K_MX_W4R: return {MFMA32_F8, "v_mfma_scale_f32_32x32x64_f8f6f4 (E4M3 data, E8M0 scales)", 32, 64, 16};
@@ -104,7 +106,7 @@ Layout slot_modes(const InstrInfo& I, int64_t unit) {
     case MFMA32_F4:
     case MFMA16_F6:
     case MFMA32_F6: return T({S(32, unit)});
-    default: return T({S(8, unit)});
+    default: return T({S(I.kl, unit)});
   }
 }
 
@@ -144,6 +146,7 @@ const char* kernel_name(int32_t k) {
     case K_MXFP6: return "MXFP6 GEMM, scaled 32x32x64 instruction on 6-bit data";
     case K_MX_W4R: return "MXFP8 GEMM, 4 waves, scales loaded into registers";
     case K_BLOCK8: return "E4M3 GEMM with fp32 scales per 128 K";
+    case K_I8: return "int8 GEMM with fp32 scales per row";
     default: return "?";
   }
 }
@@ -166,7 +169,7 @@ void operand(Out& o, const DescribeInput& in, const InstrInfo& I, char name, int
   const int32_t KS = in.bk / I.k;                         // K slices per K-tile
   const bool fp4 = in.kernel == K_MXFP4;
   const bool fp6 = in.kernel == K_MXFP6;
-  const bool fp8 = in.kernel == K_MX || in.kernel == K_MX_W8 || in.kernel == K_MX_W4R || in.kernel == K_BLOCK8;
+  const bool fp8 = in.kernel == K_MX || in.kernel == K_MX_W8 || in.kernel == K_MX_W4R || in.kernel == K_BLOCK8 || in.kernel == K_I8;
   // the 4-wave MX kernel packs 6-bit K-tiles: rows 96 bytes apart in LDS
   // (LoaderFP6Packed); the 8-wave one pads them to 128-byte rows
   const bool packed = fp6 && in.ring;
@@ -181,7 +184,7 @@ void operand(Out& o, const DescribeInput& in, const InstrInfo& I, char name, int
               BR, in.bk));
   if (in.from_memory) {
     o.note(n + " loader: each lane's two 16-byte pieces of a row's K block straight from memory into registers");
-    o.line(n + "_frag", T({T({S(16, 1), S(2, 16)}), S(F, 32)}), fmt("registers: the lane's 32 codes of a K block (32 values x %d)", F));
+    o.line(n + "_frag", T({T({S(16, 1), S(2, 16)}), S(F, 32)}), fmt("registers: the lane's 32 codes of a K-tile (32 values x %d)", F));
     return;
   }
   o.note(n + " loader: " + load_name(load));
@@ -287,7 +290,8 @@ void accumulators(Out& o, const DescribeInput& in, const InstrInfo& I) {
   const int32_t regs = I.rows == 16 ? 4 : 16;
   o.line("D_instr", T({acc_lane(I, I.rows), acc_regs(I, I.rows)}),
          fmt("accumulator (lane, reg) -> m + %d n of the instruction tile", I.rows));
-  o.line("acc", T({S(regs, 1), S(FM, regs * FN), S(FN, regs)}), "fp32 registers acc[i][j][r] as (r, i, j)");
+  o.line("acc", T({S(regs, 1), S(FM, regs * FN), S(FN, regs)}),
+         fmt("%s registers acc[i][j][r] as (r, i, j)", in.kernel == K_I8 ? "int32" : "fp32"));
   const Layout dtile = T({R(in.bm, in.d_rs), R(in.bn, in.d_cs)});
   const Layout slice = T({acc_regs(I, in.bm), S(FM, I.rows), S(FN, (int64_t)I.rows * in.bm)});
   o.stage("D_lane0", [&] { return la::composition(dtile, slice); },
@@ -306,8 +310,8 @@ std::string describe_plan(const DescribeInput& in) {
   Out o;
   const InstrInfo I = instr_of(in);
   const int32_t NT = in.wm * in.wn * in.k_waves * 64;
-  if (in.kernel == K_BLOCK8 && in.k_waves > 1)
-    o.note(fmt("kernel %d: %s; tile %dx%dx%d, %d waves that split K (wave w takes K blocks w, w + %d, ...; their sums meet in "
+  if (in.k_waves > 1)
+    o.note(fmt("kernel %d: %s; tile %dx%dx%d, %d waves that split K (wave w takes K-tiles w, w + %d, ...; their sums meet in "
                "LDS)%s, %d LDS bytes",
                in.kernel, kernel_name(in.kernel), in.bm, in.bn, in.bk, in.k_waves, in.k_waves,
                in.from_memory ? "" : fmt(", each with %d LDS stages of its own", in.stages).c_str(), in.lds_bytes));
@@ -378,6 +382,11 @@ std::string describe_plan(const DescribeInput& in) {
     if (in.d_bytes == 4)
       o.note("fp32 D: the lane's 32 codes become fp16 in registers and four v_mfma_f32_16x16x32_f16 sum the block, 8 of them "
              "at a time");
+  }
+  if (in.kernel == K_I8) {
+    o.line("SFA", R(in.M, in.sa_rs), "fp32 scale of row m of A");
+    o.line("SFB", R(in.N, in.sb_rs), "fp32 scale of row n of B");
+    o.note("scales: the int32 sum, rounded to fp32, times SFA, then SFB, then + C");
   }
   accumulators(o, in, I);
   o.line("D", view(in.M, in.N, in.d_rs, in.d_cs, in.d_batched, in.batch, in.d_bs), "element (m, n[, batch])");

@@ -28,7 +28,8 @@ enum KernelKind : int32_t {
   K_MXFP4 = 6,        // MXFP4, 8 waves, v_mfma_scale 32x32x64 with E2M1 data
   K_MXFP6 = 7,        // MXFP6, 8 waves, v_mfma_scale 32x32x64 with E2M3 or E3M2 data
   K_MX_W4R = 8,       // MXFP8, 4 waves each 128x128, v_mfma_scale 32x32x64, LDS ring, scales in registers
-  K_BLOCK8 = 9        // E4M3 with fp32 scales per 128 K (sl_ops.hpp)
+  K_BLOCK8 = 9,       // E4M3 with fp32 scales per 128 K (sl_ops.hpp)
+  K_I8 = 10           // int8 with one fp32 scale per row of A and of B (sl_ops.hpp)
 };
 
 // Tile configurations the dispatcher can choose: rows of A, rows of B,

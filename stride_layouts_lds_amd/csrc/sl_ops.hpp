@@ -1,7 +1,8 @@
 // sl_ops.hpp -- parameters and launchers of the operators next to the GEMM:
-// block quantisation to E4M3, the block-scaled 8-bit product, and the
-// orthogonalised update.  Shared by the host side (api_ops.cpp) and their
-// kernel translation units.
+// block quantisation to E4M3, the block-scaled 8-bit product, the
+// orthogonalised update, row quantisation to int8, the int8 product, and the
+// gated feed-forward block with its backward pass.  Shared by the host side
+// (api_ops.cpp, api_gated.cpp) and their kernel translation units.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -115,6 +116,114 @@ struct OrthoGramPlan {
 OrthoGramPlan ortho_gram_plan(int64_t m, int64_t n);
 size_t ortho_gram_workspace(const OrthoParams& p);
 hipError_t launch_ortho_gram(const OrthoParams& p, hipStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Row quantisation of x (batch, rows, cols) to int8 codes with one fp32 scale
+// per row: q[b][r][c] at q + b q_bs + r q_rs + c, columns [cols, q_cols) zero;
+// s of row r at s + b s_bs + r s_rs.
+// ---------------------------------------------------------------------------
+struct QuantizeRowsParams {
+  const void* x;
+  int64_t rows, cols, x_bs, x_rs, x_cs;
+  int8_t* q;
+  float* s;
+  int64_t q_cols, q_bs, q_rs, s_bs, s_rs;
+  int32_t type;   // OT_*
+  int32_t batch;
+};
+int64_t quantize_rows_groups(const QuantizeRowsParams& p);
+int32_t quantize_rows_threads(const QuantizeRowsParams& p);  // of a workgroup
+hipError_t launch_quantize_rows(const QuantizeRowsParams& p, hipStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Products of K-contiguous rows (dense.hpp): the int8 product
+//   D[m,n] = C[m,n] + sa[m] sb[n] sum_k A[m,k] B[n,k]
+// and the gated pair, with B's rows n and those of a second matrix,
+//   h[m,n] = act(g) u,  g = sum_k A[m,k] B0[n,k],  u = sum_k A[m,k] B1[n,k]
+// (times the scales for int8), g and u kept where asked.
+// ---------------------------------------------------------------------------
+constexpr int EK_F16 = 0;   // the operands' element kinds (template arguments)
+constexpr int EK_BF16 = 1;
+constexpr int EK_I8 = 2;
+
+constexpr int32_t ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_RELU = 3;  // sl_activation - 1
+
+struct DenseParams {
+  // rows of K bytes: row m of A at a + b a_bs + m a_rs (bytes), row n of matrix
+  // s of B the same
+  const uint8_t* a;
+  const uint8_t* b[2];
+  int64_t a_rs, a_bs, b_rs[2], b_bs[2];
+  int64_t M, N, K;          // N: columns of the result; K in bytes, a multiple of 16
+  // int8: one scale per row of A and of each B
+  const float* sa;
+  const float* sb[2];
+  int64_t sa_rs, sa_bs, sb_rs[2], sb_bs[2];
+  const void* c;            // may be NULL (the product alone)
+  void* d;                  // the product's D, or h
+  void* kept[2];            // g and u; may be NULL
+  int64_t c_rs, c_cs, c_bs, d_rs, d_cs, d_bs, kept_rs[2], kept_cs[2], kept_bs[2];
+  int32_t type;             // OT_* of C, D, g and u
+  int32_t act;              // ACT_*
+  int32_t batch, tiles_m, tiles_n, group_m;
+  int32_t k_tiles;          // ceil(K / 128)
+  int32_t flags;            // DF_*
+};
+constexpr int32_t DF_D_VEC = 1;     // four consecutive n of D in one aligned access
+constexpr int32_t DF_C_VEC = 2;     // ... of C
+constexpr int32_t DF_KEPT_VEC = 4;  // ... of g, and 8: of u
+
+// tile configurations: rows of A x rows of B (for the gated pair, of both
+// matrices together)
+enum DenseTile : int32_t {
+  DT_RING = 0,     // 256 x 256: 4 waves, each 128 x 128
+  DT_128 = 1,      // 128 x 128: 4 waves, each 64 x 64
+  DT_STREAM = 2,   // 32 or 64 rows of A, 4 waves that split K
+  DT_SKINNY = 3,   // 16 rows of A, 8 waves that split K
+};
+constexpr int32_t kDenseSkinnyWaves = 8, kDenseStreamWaves = 4;
+constexpr int32_t kDenseKBytes = 128;  // of a row in a K-tile
+struct DensePlan {
+  int32_t tile;
+  int32_t bm, bn;       // rows of A and of B of a workgroup
+  int32_t threads, lds;
+  int32_t stages;       // LDS K-tiles of DT_128 and DT_STREAM
+};
+// `gated`: bn / 2 columns of the result to a workgroup
+DensePlan dense_plan(int32_t kind, bool gated, int64_t batch, int64_t M, int64_t N, int64_t K);
+hipError_t launch_gemm_i8(const DenseParams& p, const DensePlan& plan, hipStream_t stream);
+hipError_t launch_gated(const DenseParams& p, int32_t kind, const DensePlan& plan, hipStream_t stream);
+
+// ---------------------------------------------------------------------------
+// What the backward pass of the gated block does beside its products.
+// 16-bit matrices copied to rows of contiguous values: out row r (of `out_rs`
+// values; columns [cols, width) zero) from x's row r, any strides.
+// ---------------------------------------------------------------------------
+struct PackParams {
+  const uint16_t* x;
+  uint16_t* out;
+  int64_t rows, cols, width;   // width a multiple of 8
+  int64_t x_bs, x_rs, x_cs, out_bs, out_rs;  // out_rs, out_bs multiples of 8
+  int32_t batch;
+};
+int64_t pack_groups(const PackParams& p);
+hipError_t launch_pack(const PackParams& p, hipStream_t stream);
+
+// dg = dh u act'(g) and du = dh act(g), each rounded to 16 bits, as rows
+// (dg's columns at 0, du's at Fp of a row of 2 Fp) and as columns (row f of
+// dg's transpose at t + f t_rs, of du's at t + t_us more); padding zero.
+struct GatedSlopeParams {
+  const uint16_t *g, *u, *dh;
+  int64_t M, F, Fp, Mp;        // padded to multiples of 64
+  int64_t g_bs, g_rs, g_cs, u_bs, u_rs, u_cs, dh_bs, dh_rs, dh_cs;
+  uint16_t* rows;              // may be NULL; row m of batch b at rows + (b M + m) 2 Fp
+  uint16_t* t;                 // may be NULL
+  int64_t t_bs, t_rs, t_us;
+  int32_t type, act, batch;
+};
+int64_t gated_slope_groups(const GatedSlopeParams& p);
+hipError_t launch_gated_slope(const GatedSlopeParams& p, hipStream_t stream);
+constexpr int32_t kPackThreads = 256;
 
 template <int T>
 struct OrthoElem {
