@@ -128,7 +128,8 @@ sl_status plan_int8(const sl_gemm_args* args, RowsPlan* out) {
   if (has_c) p.c_rs = C.rs, p.c_cs = C.cs, p.c_bs = batch_stride(C);
   p.d_rs = D.rs, p.d_cs = D.cs, p.d_bs = batch_stride(D);
   p.type = type, p.batch = (int32_t)batch;
-  p.flags = (quad_rows(D, batch) ? DF_D_VEC : 0) | (has_c && quad_rows(C, batch) ? DF_C_VEC : 0);
+  p.flags = (quad_rows(D, batch) ? DF_D_VEC : 0) | (has_c && quad_rows(C, batch) ? DF_C_VEC : 0) |
+            (D.cs == 1 && (!has_c || C.cs == 1) ? DF_ROWS : 0);
   P.tile = dense_plan(EK_I8, false, batch, M, N, K);
   if ((s = place_tiles(&p, P.tile, false)) != SL_OK) return s;
   P.pub.a_load = P.pub.b_load = LOAD_KVEC;
@@ -403,6 +404,7 @@ sl_status plan_gated(const sl_gated_args* args, GatedPlan* out) {
   }
   p.d = args->h.data, p.d_rs = w[H].rs, p.d_cs = w[H].cs, p.d_bs = bstride(w[H]);
   p.flags = quad_rows(w[H], p.batch) ? sl::DF_D_VEC : 0;
+  if (w[H].cs == 1 && (!keep || (w[G].cs == 1 && w[U].cs == 1))) p.flags |= sl::DF_ROWS;
   if (keep)
     for (int i = 0; i < 2; ++i) {
       const View& k = w[G + i];

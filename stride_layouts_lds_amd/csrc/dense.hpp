@@ -101,7 +101,16 @@ struct RowLoader {
   __device__ __forceinline__ int32_t tile_row(int j) const { return (j * WAVES + wave) * 8 + lane / 8; }
   __device__ __forceinline__ int32_t chunk(int j) const { return (lane & 7) ^ swz(tile_row(j), 0); }
 
-  // copy j of a K-tile that lies inside K.  (Elements are copied to locals
+  // From here on the copies are of the last K-tile, of which `bytes` lie inside K
+  // (128 or fewer): the chunks past them read zero.
+  __device__ __forceinline__ void last_tile(int32_t bytes) {
+#pragma unroll
+    for (int j = 0; j < ITERS; ++j) voff[j] = 16 * chunk(j) < bytes ? voff[j] : kOutOfRange;
+  }
+
+  // copy j of a K-tile that lies inside K, or of the last one after last_tile.
+  // The lane's offset is voff[j] and the K-tile's start goes into the scalar
+  // offset: no vector arithmetic next to the products.  (Elements are copied to locals
   // first: the host compilation pass drops the launch stubs of kernels that
   // index a member array inside the builtin's argument list.)
   __device__ __forceinline__ void issue_full(int32_t t, char* lds, int j) const {
@@ -155,7 +164,8 @@ __device__ __forceinline__ u32x4 dense_frag(const char* tile, int32_t lane, int3
 // ---------------------------------------------------------------------------
 // What becomes of the sums: EPI::finish(batch, m, n, v) takes four consecutive
 // columns of one row, for the gated pair those of both products, with m < M
-// and n < N; columns from N on are not stored.  Defined by the including file.
+// and n < N; columns from N on are not stored.  EPI::rows: see dense_rows.
+// Defined by the including file.
 // ---------------------------------------------------------------------------
 
 // four values to a 16- or 32-bit row, `valid` of them
@@ -206,28 +216,76 @@ __device__ __forceinline__ floatx4 dense_load(const void* base, int32_t type, in
   return v;
 }
 
+// Eight values of a contiguous row, at any alignment of their type.
+template <int OT>
+__device__ __forceinline__ void dense_store8(void* at, const float (&v)[8]) {
+  typedef uint16_t halves __attribute__((ext_vector_type(8), aligned(2)));
+  typedef float floats __attribute__((ext_vector_type(4), aligned(4)));
+  if constexpr (OT == OT_F32) {
+    *(floats*)at = floats{v[0], v[1], v[2], v[3]};
+    *((floats*)at + 1) = floats{v[4], v[5], v[6], v[7]};
+  } else {
+    halves w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = from_f32<OT == OT_F16 ? DT_F16 : DT_BF16>(v[e]);
+    *(halves*)at = w;
+  }
+}
+template <int OT>
+__device__ __forceinline__ void dense_load8(const void* at, float (&v)[8]) {
+  typedef uint16_t halves __attribute__((ext_vector_type(8), aligned(2)));
+  typedef float floats __attribute__((ext_vector_type(4), aligned(4)));
+  if constexpr (OT == OT_F32) {
+    const floats a = *(const floats*)at, b = *((const floats*)at + 1);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+  } else {
+    const halves w = *(const halves*)at;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = to_f32<OT == OT_F16 ? DT_F16 : DT_BF16>(w[e]);
+  }
+}
+
 // A wave's 64 x COLS block of sums (COLS = 128 or 64) from its region of LDS,
 // in the chunk order of rows_chunk, row after row: whole rows of the block are
 // stored together.  GATED: the first half of the columns are g, the others u.
+//
+// Contiguous outputs (DF_ROWS) go eight columns a lane: EPI::rows<RPI>(batch, m,
+// n, count, get) finishes columns n .. n + 7 of rows m, m + RPI, ... as far as
+// `count` of them, get(it, s, v) being the sums of the it-th, s 0: g or the
+// product's, 1: u.  (A wave's LDS reads pair lanes 0-7 with 16-23, 8-15 with 24-31 and so
+// on; where eight lanes have a row, the rows of a pair differ in the lowest bit, so that
+// their chunks, all even or all odd in a row, lie on different banks.)  Others,
+// and the columns next to N where those are no eight: EPI::finish.
 template <int EK, bool GATED, int COLS, class EPI>
 __device__ __forceinline__ void dense_rows(const EPI& epi, const DenseParams& p, int64_t batch, int64_t m_base, int64_t n_base, int32_t lane,
                                            const char* region) {
   constexpr int OUT = GATED ? COLS / 2 : COLS;  // columns of the result
-  constexpr int LPR = OUT / 4, RPI = 64 / LPR;  // lanes to a row, rows at once
-  const int32_t q = lane % LPR;
-  const int64_t n = n_base + 4 * q;
-  if (n >= p.N) return;
-#pragma unroll 4
-  for (int it = 0; it < 64 / RPI; ++it) {
-    const int32_t r = RPI * it + lane / LPR;
-    if (m_base + r >= p.M) continue;
-    const floatx4 v = *(const floatx4*)(region + rows_chunk<COLS>(r, q));
-    if constexpr (GATED) {
-      const floatx4 u = *(const floatx4*)(region + rows_chunk<COLS>(r, q + LPR));
-      epi.finish(p, batch, m_base + r, n, dense_value<EK>(v), dense_value<EK>(u));
-    } else {
-      epi.finish(p, batch, m_base + r, n, dense_value<EK>(v));
-    }
+  constexpr int LPR = OUT / 8, RPI = 64 / LPR;  // lanes to a row, rows at once
+  const int32_t group = lane / LPR, l = lane % LPR;
+  // (the row bit that pairs of lane groups differ in goes last)
+  const int32_t r0 = LPR == 8 ? (group & 4) | (group & 1) << 1 | (group & 2) >> 1 : group;
+  const int64_t m = m_base + r0, n = n_base + 8 * l;
+  auto quad = [&](int32_t r, int32_t q) { return dense_value<EK>(*(const floatx4*)(region + rows_chunk<COLS>(r, q))); };
+  const int32_t count = m < p.M ? (int32_t)(p.M - m > 64 ? 64 / RPI : (p.M - m + RPI - 1) / RPI) : 0;
+  if (n >= p.N || count == 0) return;
+  if (p.flags & DF_ROWS && n + 8 <= p.N) {
+    auto get = [&](int32_t it, int s, float(&v)[8]) {
+      const int32_t r = RPI * it + r0, q = 2 * l + (s ? OUT / 4 : 0);
+      const floatx4 a = quad(r, q), b = quad(r, q + 1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+    };
+    epi.template rows<RPI>(p, batch, m, n, count, get);
+    return;
+  }
+#pragma unroll 1
+  for (int it = 0; it < 2 * count; ++it) {
+    const int32_t r = RPI * (it / 2) + r0, q = 2 * l + it % 2;
+    const int64_t nq = n + 4 * (it % 2);
+    if (nq >= p.N) continue;
+    if constexpr (GATED) epi.finish(p, batch, m_base + r, nq, quad(r, q), quad(r, q + OUT / 4));
+    else epi.finish(p, batch, m_base + r, nq, quad(r, q));
   }
 }
 
@@ -238,10 +296,9 @@ __device__ __forceinline__ void dense_rows(const EPI& epi, const DenseParams& p,
 // tile q (A of K-tile q / 2 for even q, B for odd q) in slot q % 5.  Per
 // K-tile: reads of its first slice beside the last products of the K-tile
 // before, the first slice's products beside the reads of the second, half of
-// the second's, one barrier.  KFULL: K a multiple of 128 bytes, copies without
-// vector arithmetic.  The gated pair's wave holds 64 rows of each matrix.
+// the second's, one barrier.  The gated pair's wave holds 64 rows of each matrix.
 // ---------------------------------------------------------------------------
-template <int EK, bool GATED, bool KFULL, class EPI>
+template <int EK, bool GATED, class EPI>
 __global__ __launch_bounds__(256, 1) void dense_ring_kernel(const DenseParams p) {
   constexpr int F = 8, SLOT = 256 * kRowBytes, LOADS = 8;
   constexpr int BN = kResultCols<GATED, 256>;
@@ -252,8 +309,8 @@ __global__ __launch_bounds__(256, 1) void dense_ring_kernel(const DenseParams p)
   const int64_t m0 = (int64_t)tc.tm * 256, n0 = (int64_t)tc.tn * BN;
   const int32_t rows_a = (int32_t)(p.M - m0 < 256 ? p.M - m0 : 256);
   const int32_t cols = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
-  const auto la = dense_a_loader<256, 256>(p, tc.batch, m0, rows_a, wave, lane);
-  const auto lb = dense_b_loader<GATED, 256, 256, GATED ? 64 : 0>(p, tc.batch, n0, cols, wave, lane);
+  auto la = dense_a_loader<256, 256>(p, tc.batch, m0, rows_a, wave, lane);
+  auto lb = dense_b_loader<GATED, 256, 256, GATED ? 64 : 0>(p, tc.batch, n0, cols, wave, lane);
   static_assert(decltype(la)::ITERS == LOADS && decltype(lb)::ITERS == LOADS, "copy layout");
 
   floatx4 acc[F][F];
@@ -264,18 +321,12 @@ __global__ __launch_bounds__(256, 1) void dense_ring_kernel(const DenseParams p)
   const int32_t a_row0 = (wave & 1) * 128, b_row0 = (wave >> 1) * 128;
   const int32_t T = p.k_tiles;  // at least 1
   __builtin_assume(T >= 1);
-  // past the last K-tile the look-ahead copies are not read: the last one
-  // again, or zeros
-  auto kt = [&](int32_t u) { return u < T ? u : (KFULL ? T - 1 : T); };
+  // past the last K-tile the look-ahead copies repeat it and are not read
+  auto kt = [&](int32_t u) { return u < T ? u : T - 1; };
   auto slot = [&](int32_t q) { return smem + q * SLOT; };
-  auto copy_a = [&](int32_t u, char* dst, int j) {
-    if constexpr (KFULL) la.issue_full(kt(u), dst, j);
-    else la.issue_one(kt(u), dst, j);
-  };
-  auto copy_b = [&](int32_t u, char* dst, int j) {
-    if constexpr (KFULL) lb.issue_full(kt(u), dst, j);
-    else lb.issue_one(kt(u), dst, j);
-  };
+  auto copy_a = [&](int32_t u, char* dst, int j) { la.issue_full(kt(u), dst, j); };
+  auto copy_b = [&](int32_t u, char* dst, int j) { lb.issue_full(kt(u), dst, j); };
+  const int32_t last_bytes = (int32_t)p.K - (T - 1) * kRowBytes;
   u32x4 fa0[F], fb0[F], fa1[F], fb1[F];
   typedef __attribute__((address_space(3))) const u32x4 lds_u4;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)smem;
@@ -309,12 +360,16 @@ __global__ __launch_bounds__(256, 1) void dense_ring_kernel(const DenseParams p)
 #pragma unroll
     for (int e = 2 * q; e < 2 * q + 2; ++e) dense_mfma_agpr<EK>(acc[i0 + e / F][e % F], fb[e % F], fa[i0 + e / F]);
   };
+  if (T == 1) la.last_tile(last_bytes), lb.last_tile(last_bytes);
 #pragma unroll
   for (int j = 0; j < LOADS; ++j) copy_a(0, slot(0), j);
 #pragma unroll
   for (int j = 0; j < LOADS; ++j) copy_b(0, slot(1), j);
+  if (T == 2) la.last_tile(last_bytes);
 #pragma unroll
   for (int j = 0; j < LOADS; ++j) copy_a(1, slot(2), j);
+  if (T == 2) lb.last_tile(last_bytes);
+  if (T == 3) la.last_tile(last_bytes);
   // the first K-tile's first part computes with zero fragments (adds nothing)
 #pragma unroll
   for (int i = 0; i < F; ++i) fa1[i] = fb1[i] = u32x4{0, 0, 0, 0};
@@ -347,6 +402,9 @@ __global__ __launch_bounds__(256, 1) void dense_ring_kernel(const DenseParams p)
     for (int q = 0; q < 16; ++q) products(0, q, fa1, fb1);
     const int32_t na = sa + 2 >= 5 ? sa - 3 : sa + 2;
     bases(na, na == 4 ? 0 : na + 1);
+    // the next copies are B(t + 2) and A(t + 3)
+    if (t + 2 == T - 1) lb.last_tile(last_bytes);
+    if (t + 3 == T - 1) la.last_tile(last_bytes);
     wait_vmem_n<LOADS>();  // in flight after this: A(t + 2)
     phase_barrier();
     sa = na;
@@ -622,8 +680,7 @@ hipError_t dense_launch(const DenseParams& p, const DensePlan& plan, hipStream_t
   typedef std::integral_constant<int, 4> c4;
   switch (plan.tile) {
     case DT_RING:
-      if (p.K % kRowBytes == 0) hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, true, EPI>), grid, block, 0, s, p);
-      else hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, false, EPI>), grid, block, 0, s, p);
+      hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, EPI>), grid, block, 0, s, p);
       break;
     case DT_128:
       if (plan.stages == 2) hipLaunchKernelGGL((dense_tile_kernel<EK, GATED, 2, EPI>), grid, block, 0, s, p);

@@ -26,6 +26,45 @@ struct ScaledSum {
     }
     dense_store(p.d, p.type, batch * p.d_bs + m * p.d_rs + n * p.d_cs, p.d_cs, p.flags & DF_D_VEC, valid, v);
   }
+  template <int OT, bool HAS_C, int RPI, class GET>
+  __device__ __forceinline__ void rows_of(const DenseParams& p, int64_t batch, int64_t m, int64_t n, int32_t count, const GET& get) const {
+    typedef typename OrthoElem<OT>::type E;
+    float b[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b[e] = sb[(n + e) * p.sb_rs[0]];
+    E* d = (E*)p.d + batch * p.d_bs + m * p.d_rs + n;
+    const E* c = HAS_C ? (const E*)p.c + batch * p.c_bs + m * p.c_rs + n : nullptr;
+    const float* a = sa + m * p.sa_rs;
+#pragma unroll 4
+    for (int it = 0; it < count; ++it) {
+      float v[8];
+      get(it, 0, v);
+      const float as = *a;
+      a += RPI * p.sa_rs;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * as * b[e];
+      if constexpr (HAS_C) {
+        float w[8];
+        dense_load8<OT>(c, w);
+        c += RPI * p.c_rs;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += w[e];
+      }
+      dense_store8<OT>(d, v);
+      d += RPI * p.d_rs;
+    }
+  }
+  template <int OT, int RPI, class GET>
+  __device__ __forceinline__ void rows_to(const DenseParams& p, int64_t batch, int64_t m, int64_t n, int32_t count, const GET& get) const {
+    if (p.c) rows_of<OT, true, RPI>(p, batch, m, n, count, get);
+    else rows_of<OT, false, RPI>(p, batch, m, n, count, get);
+  }
+  template <int RPI, class GET>
+  __device__ __forceinline__ void rows(const DenseParams& p, int64_t batch, int64_t m, int64_t n, int32_t count, const GET& get) const {
+    if (p.type == OT_F16) rows_to<OT_F16, RPI>(p, batch, m, n, count, get);
+    else if (p.type == OT_BF16) rows_to<OT_BF16, RPI>(p, batch, m, n, count, get);
+    else rows_to<OT_F32, RPI>(p, batch, m, n, count, get);
+  }
 };
 
 }  // namespace

@@ -172,6 +172,7 @@ struct DenseParams {
 constexpr int32_t DF_D_VEC = 1;     // four consecutive n of D in one aligned access
 constexpr int32_t DF_C_VEC = 2;     // ... of C
 constexpr int32_t DF_KEPT_VEC = 4;  // ... of g, and 8: of u
+constexpr int32_t DF_ROWS = 16;     // the columns of C and of every output contiguous
 
 // tile configurations: rows of A x rows of B (for the gated pair, of both
 // matrices together)
