@@ -21,7 +21,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libstride_layouts_lds.so")
 SOURCES = ["api.cpp", "api_ops.cpp", "api_gated.cpp", "describe.cpp", "layout_algebra.cpp", "gemm_f16.hip", "gemm_mx.hip",
            "gemm_block.hip", "quantize.hip", "orthogonalize.hip",
-           "ortho_gram.hip", "quantize_rows.hip", "gemm_i8.hip", "gated.hip", "gated_backward.hip", "probes.hip", "scratch.hip"]
+           "ortho_gram.hip", "quantize_rows.hip", "gemm_i8.hip", "gated.hip", "gated_prepare.hip", "gated_backward.hip", "probes.hip", "scratch.hip"]
 HEADERS = ["sl_maps.hpp", "sl_kernels.hpp", "sl_ops.hpp", "sl_device.hpp", "layout_algebra.hpp", "describe.hpp",
            "api_common.hpp", "api_ops.hpp", "ortho_device.hpp", "dense.hpp", "activation.hpp"]
 ARCH = "gfx950"

@@ -928,8 +928,8 @@ static sl_status describe_int8(const sl_gemm_args* args, char* out, int64_t capa
   in.kernel = P.pub.kernel;
   in.a_load = P.pub.a_load, in.b_load = P.pub.b_load;
   in.bm = P.pub.tile_m, in.bn = P.pub.tile_n, in.bk = P.pub.tile_k;
-  in.ring = P.tile.tile == sl::DT_RING;
-  in.wm = in.wn = P.tile.tile == sl::DT_RING || P.tile.tile == sl::DT_128 ? 2 : 1;
+  in.ring = P.tile.tile <= sl::DT_128x128;
+  in.wm = in.wn = in.ring ? 2 : 1;
   in.k_waves = P.pub.threads / 64 / (in.wm * in.wn);
   in.from_memory = P.tile.tile == sl::DT_SKINNY;
   in.stages = P.tile.stages;

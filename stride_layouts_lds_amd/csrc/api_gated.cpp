@@ -1,33 +1,54 @@
 // api_gated.cpp -- host side of the gated feed-forward block and its backward
 // pass, of the int8 form of sl_gemm and of sl_quantize_rows.  Every check runs
 // before any HIP call.
+#include <cmath>
+
 #include "api_common.hpp"
 #include "api_ops.hpp"
 #include "sl_kernels.hpp"
 
 namespace sl {
 
-// The tile (dense.hpp).  `N` columns of the result; a gated tile covers half as
-// many as it has rows of B.
-DensePlan dense_plan(int32_t kind, bool gated, int64_t batch, int64_t M, int64_t N, int64_t K) {
+// The tile (dense.hpp), by the least time of a plain model: rounds of workgroups
+// over the CUs times (start and end of a workgroup + K-tiles of 128 bytes x one's
+// time), in us, fitted to calls with each tile forced.  Some of them, gated bf16
+// (M x F, K 256 / 1024 / 4096; 256 x 256, 256 x 128, 128 x 128, streamed):
+//   256 x 1024   13 25 73     9 15 42     6 10 26     5  7  13
+//   512 x 1024   13 25 73     9 15 43     6 10 33     6  8  18
+//   1000 x 2000  14 26 74     9 16 43     7 11 37     22 36 101
+//   1000 x 2500  19 31 78     12 18 45    9 17 47     27 43 130
+//   2048 x 2048  15 27 75     10 20 56    9 19 58     42 55 130
+//   4096 x 2048  17 32 96     19 39 112   16 35 113   83 108 259
+//   4096 x 8192  59 126 372   68 145 432  53 129 446  324 458 1586
+// int8, 4096 x 4096: 19 27 58, 21 33 70, 17 27 66, 86 94 163.  Up to 64 rows of A go
+// streamed whatever it says (64 x 8192 x 4096 is read at 4.4 TB/s).
+DensePlan dense_plan(bool gated, int64_t batch, int64_t M, int64_t N, int64_t K) {
   using host::ceil_div;
-  const int64_t B = gated ? 2 * N : N;  // rows of B
-  const int64_t tiles128 = batch * ceil_div(M, 128) * ceil_div(B, 128);
+  const int64_t B = gated ? 2 * N : N;  // rows of B: a gated tile's columns of the result are half of its rows of B
   if (M <= 16) {
     const int32_t bn = gated || batch * ceil_div(N, 32) >= kCUs ? 32 : 16;
     return {DT_SKINNY, 16, bn, kDenseSkinnyWaves * 64, kDenseSkinnyWaves * bn / 16 * 1024, 0};
   }
-  if (M <= 64 || tiles128 <= 64) {
-    const int32_t bm = M <= 32 ? 32 : 64;
-    const int32_t bn = batch * ceil_div(M, bm) * ceil_div(B, 64) >= kCUs ? 64 : 32;
-    const int32_t stages = bm == 32 ? (bn == 32 ? 4 : 3) : (bn == 32 ? 3 : 2);
-    return {DT_STREAM, bm, bn, kDenseStreamWaves * 64, kDenseStreamWaves * stages * (bm + bn) * 128, stages};
+  const double T = (double)ceil_div(K, 128);
+  const int32_t bm = M <= 32 ? 32 : 64;
+  const int32_t bn = batch * ceil_div(M, bm) * ceil_div(B, 64) >= kCUs ? 64 : 32;
+  const int32_t stages = bm == 32 ? (bn == 32 ? 4 : 3) : (bn == 32 ? 3 : 2);
+  DensePlan best = {DT_STREAM, bm, bn, kDenseStreamWaves * 64, kDenseStreamWaves * stages * (bm + bn) * 128, stages};
+  if (M <= 64 || K == 0) return best;
+  const double groups = (double)batch * (double)ceil_div(M, bm) * (double)ceil_div(B, bn);
+  double least = std::ceil(groups / kCUs) * (5.0 + T * (bn == 64 ? 0.2 : 0.13));
+  constexpr struct {
+    int32_t tile, bm, bn, per_cu;
+    double start, k, k_alone;  // alone: one workgroup to a CU
+  } shapes[3] = {{DT_256x256, 256, 256, 1, 10.0, 1.3, 1.3}, {DT_256x128, 256, 128, 1, 7.0, 0.77, 0.77}, {DT_128x128, 128, 128, 2, 4.2, 0.8, 0.51}};
+  for (const auto& t : shapes) {
+    const double tiles = (double)batch * (double)ceil_div(M, t.bm) * (double)ceil_div(B, t.bn), slots = kCUs * t.per_cu;
+    const double whole = std::floor(tiles / slots), rest = tiles - whole * slots;
+    double cost = whole * (t.start + T * t.k);
+    if (rest > 0) cost += t.start + T * (rest <= kCUs ? t.k_alone : t.k);
+    if (cost < least) least = cost, best = {t.tile, t.bm, t.bn, 256, 5 * 128 * t.bm, 0};
   }
-  const int64_t tiles256 = batch * ceil_div(M, 256) * ceil_div(B, 256);
-  const double ring = (double)ceil_div(tiles256, kCUs) * 256 * 256, small = (double)ceil_div(tiles128, 2 * kCUs) * 2 * 128 * 128 / 0.7;
-  if (K > 0 && ring <= small) return {DT_RING, 256, 256, 256, 5 * 256 * 128, 0};
-  const int32_t stages = tiles128 > kCUs ? 2 : 4;
-  return {DT_128, 128, 128, 256, stages * 256 * 128, stages};
+  return best;
 }
 
 namespace host {
@@ -64,7 +85,7 @@ static sl_status place_tiles(DenseParams* p, const DensePlan& t, bool gated) {
   if (!grid_fits(p->batch, tm, tn, t.threads))
     return fail(SL_ERR_SHAPE, "too many output tiles (batch %d of %lld x %lld)", p->batch, (long long)tm, (long long)tn);
   p->tiles_m = (int32_t)tm, p->tiles_n = (int32_t)tn, p->group_m = 8;
-  p->k_tiles = (int32_t)ceil_div(p->K, kDenseKBytes);
+  p->k_tiles = (int32_t)ceil_div(p->K, 128);
   return SL_OK;
 }
 
@@ -130,10 +151,10 @@ sl_status plan_int8(const sl_gemm_args* args, RowsPlan* out) {
   p.type = type, p.batch = (int32_t)batch;
   p.flags = (quad_rows(D, batch) ? DF_D_VEC : 0) | (has_c && quad_rows(C, batch) ? DF_C_VEC : 0) |
             (D.cs == 1 && (!has_c || C.cs == 1) ? DF_ROWS : 0);
-  P.tile = dense_plan(EK_I8, false, batch, M, N, K);
+  P.tile = dense_plan(false, batch, M, N, K);
   if ((s = place_tiles(&p, P.tile, false)) != SL_OK) return s;
   P.pub.a_load = P.pub.b_load = LOAD_KVEC;
-  P.pub.tile_m = P.tile.bm, P.pub.tile_n = P.tile.bn, P.pub.tile_k = (int32_t)kDenseKBytes;
+  P.pub.tile_m = P.tile.bm, P.pub.tile_n = P.tile.bn, P.pub.tile_k = 128;
   P.pub.threads = P.tile.threads, P.pub.lds_bytes = P.tile.lds;
   P.pub.workgroups = batch * p.tiles_m * p.tiles_n;
   return SL_OK;
@@ -291,7 +312,7 @@ struct GatedPlan {
   sl::DenseParams p;
   sl::DensePlan tile;
   int32_t kind;
-  sl::PackParams pack[3];  // x, w_gate, w_up; rows 0: read as it lies
+  sl::GatedPrepareParams prepare;  // copies of x, w_gate, w_up; rows 0: read as it lies
   int64_t offset[3], ws_bytes;
   bool empty;
   View v[9];
@@ -381,12 +402,12 @@ sl_status plan_gated(const sl_gated_args* args, GatedPlan* out) {
     for (int i = 0; i < 3; ++i) {
       if (rows_ready(w[i], w[i].batch, 2)) continue;
       if ((std::min<int64_t>(w[i].rows, 256)) * Kp * 2 >= kLim) return fail(SL_ERR_SHAPE, "a 256-row tile of an operand spans 2^31 bytes or more");
-      sl::PackParams& q = P.pack[i];
+      sl::PackParams& q = P.prepare.pack[i];
       q.x = (const uint16_t*)data[i];
       q.rows = w[i].rows, q.cols = K, q.width = Kp;
       q.batch = (int32_t)(bstride(w[i]) ? w[i].batch : 1);
       q.x_bs = bstride(w[i]), q.x_rs = w[i].rs, q.x_cs = w[i].cs, q.out_rs = Kp, q.out_bs = w[i].rows * Kp;
-      if (!grid_fits(q.batch, q.rows, ceil_div(Kp, 8), 1) || !grid_fits(sl::pack_groups(q), 1, 1, sl::kPackThreads))
+      if (!grid_fits(q.batch, ceil_div(q.rows, 64), ceil_div(Kp, 64), sl::kPrepareThreads))
         return fail(SL_ERR_SHAPE, "%s is too large to be copied", names[i]);
       P.offset[i] = P.ws_bytes;
       P.ws_bytes += round_up(q.batch * q.out_bs * 2, 256);
@@ -394,6 +415,8 @@ sl_status plan_gated(const sl_gated_args* args, GatedPlan* out) {
     }
     k_bytes = Kp * 2;
   }
+  if (!grid_fits(sl::gated_prepare_groups(&P.prepare), 1, 1, sl::kPrepareThreads))
+    return fail(SL_ERR_SHAPE, "the operands are too large to be copied");
   p.K = k_bytes;
   p.a = data[0], p.a_rs = rs[0], p.a_bs = bs[0];
   for (int i = 0; i < 2; ++i) p.b[i] = data[1 + i], p.b_rs[i] = rs[1 + i], p.b_bs[i] = bs[1 + i];
@@ -413,7 +436,7 @@ sl_status plan_gated(const sl_gated_args* args, GatedPlan* out) {
     }
   p.type = type, p.act = args->activation - SL_SILU;
   P.kind = i8 ? sl::EK_I8 : args->x.dtype == SL_F16 ? sl::EK_F16 : sl::EK_BF16;
-  P.tile = sl::dense_plan(P.kind, true, p.batch, p.M, F, k_bytes);
+  P.tile = sl::dense_plan(true, p.batch, p.M, F, k_bytes);
   return place_tiles(&p, P.tile, true);
 }
 
@@ -441,13 +464,12 @@ sl_status sl_gated(const sl_gated_args* args, void* stream) {
   const char* const names[9] = {"x", "w_gate", "w_up", "sx", "s_gate", "s_up", "h", "gate", "up"};
   if ((s = check_workspace(args->workspace, args->workspace_bytes, P.ws_bytes, views, names, 9)) != SL_OK) return s;
   if ((s = check_arch()) != SL_OK) return s;
-  hipError_t e = hipSuccess;
-  for (int i = 0; i < 3 && e == hipSuccess; ++i) {
-    if (!P.pack[i].rows) continue;
-    P.pack[i].out = (uint16_t*)((char*)args->workspace + P.offset[i]);
-    (i == 0 ? P.p.a : P.p.b[i - 1]) = (const uint8_t*)P.pack[i].out;
-    e = sl::launch_pack(P.pack[i], (hipStream_t)stream);
+  for (int i = 0; i < 3; ++i) {
+    if (!P.prepare.pack[i].rows) continue;
+    P.prepare.pack[i].out = (uint16_t*)((char*)args->workspace + P.offset[i]);
+    (i == 0 ? P.p.a : P.p.b[i - 1]) = (const uint8_t*)P.prepare.pack[i].out;
   }
+  hipError_t e = sl::launch_gated_prepare(P.prepare, (hipStream_t)stream);
   if (e == hipSuccess) e = sl::launch_gated(P.p, P.kind, P.tile, (hipStream_t)stream);
   if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
   return SL_OK;
@@ -458,25 +480,14 @@ sl_status sl_gated(const sl_gated_args* args, void* stream) {
 namespace {
 
 struct BackwardPlan {
-  sl::GatedSlopeParams slope;
-  sl::PackParams xt, wt[2];   // rows 0: not made
-  sl_gemm_args dx, dw[2];     // data pointers hold offsets into the workspace until the launch
-  int32_t dw_calls;           // 1: both weights' gradients as a batch of two
+  sl::GatedPrepareParams prepare;  // copies: x's transpose, w_gate's, w_up's
+  sl::DenseParams dx, dw;
+  sl::DensePlan dx_tile, dw_tile;
+  int32_t kind;
   bool want_dx, want_dw, launch;
-  int64_t off_rows, off_t, off_xt, off_wt, off_gemm, ws_bytes, gemm_bytes;
+  int64_t off_rows, off_t, off_xt, off_wt, ws_bytes;
   View v[9];
 };
-
-sl_tensor matrix(void* data, int32_t dtype, int64_t batch, int64_t rows, int64_t cols, int64_t bs, int64_t rs, int64_t cs) {
-  sl_tensor t{};
-  t.data = data, t.dtype = dtype;
-  if (batch < 0) {
-    t.layout = sl_layout{2, {rows, cols, 0}, {rs, cs, 0}};
-  } else {
-    t.layout = sl_layout{3, {batch, rows, cols}, {bs, rs, cs}};
-  }
-  return t;
-}
 
 sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
   g_msg.clear();
@@ -535,10 +546,10 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
   const bool tokens = n > 0 && rows > 0 && F > 0;
   const int64_t weights = one_weight ? 1 : n;          // matrices of weights
   const int64_t across = one_weight ? n * Mp : Mp;     // values of a row of a transpose over the tokens
-  if (tokens && !grid_fits(n, ceil_div(rows, 64), ceil_div(F, 64), sl::kPackThreads)) return fail(SL_ERR_SHAPE, "dh is too large");
-  if (across >= kLim || n * rows >= kLim) return fail(SL_ERR_SHAPE, "too many rows in all");
+  if (across >= kLim / 2 || n * rows >= kLim) return fail(SL_ERR_SHAPE, "too many rows in all");
+  if (tokens && !grid_fits(n, ceil_div(rows, 64), ceil_div(F, 64), sl::kPrepareThreads)) return fail(SL_ERR_SHAPE, "dh is too large");
 
-  sl::GatedSlopeParams& g = P.slope;
+  sl::GatedSlopeParams& g = P.prepare.slope;
   g.g = (const uint16_t*)args->gate.data, g.u = (const uint16_t*)args->up.data, g.dh = (const uint16_t*)args->dh.data;
   g.M = rows, g.F = F, g.Fp = Fp, g.Mp = Mp;
   g.g_bs = bstride(w[G]), g.g_rs = w[G].rs, g.g_cs = w[G].cs;
@@ -558,59 +569,47 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
     q->rows = x.cols, q->cols = x.rows, q->width = width;
     q->x_bs = bstride(x), q->x_rs = x.cs, q->x_cs = x.rs, q->out_bs = out_bs, q->out_rs = out_rs;
     q->batch = (int32_t)count;
-    if (!grid_fits(count, ceil_div(q->rows, 64), ceil_div(width, 64), sl::kPackThreads) ||
-        !grid_fits(count, q->rows, ceil_div(width, 8), 1) || !grid_fits(sl::pack_groups(*q), 1, 1, sl::kPackThreads))
+    if (!grid_fits(count, ceil_div(q->rows, 64), ceil_div(width, 64), sl::kPrepareThreads))
       return fail(SL_ERR_SHAPE, "an operand is too large to be transposed");
     return SL_OK;
   };
-  int64_t bytes;
-  auto product = [&](sl_gemm_args* a) -> sl_status {
-    const sl_status e = sl_gemm_workspace_bytes(a, &bytes);
-    if (e == SL_OK) P.gemm_bytes = std::max(P.gemm_bytes, bytes);
-    return e;
+  // a product of `count` matrices (m, k) and (n, k) of the workspace, k values a row
+  auto product = [&](sl::DenseParams* p, sl::DensePlan* tile, int64_t count, int64_t m, int64_t n, int64_t k, int64_t a_bs, int64_t b_bs,
+                     int shift) -> sl_status {
+    p->M = m, p->N = n, p->K = 2 * k, p->batch = (int32_t)count, p->b_shift = shift;
+    p->a_rs = p->b_rs[0] = 2 * k, p->a_bs = 2 * a_bs, p->b_bs[0] = 2 * b_bs;
+    p->type = g.type;
+    if (256 * 2 * k >= kLim) return fail(SL_ERR_SHAPE, "a 256-row tile of an operand spans 2^31 bytes or more");
+    *tile = sl::dense_plan(false, count, m, n, 2 * k);
+    return place_tiles(p, *tile, false);
   };
-  // operands in the workspace carry stand-in addresses through the plan: they
-  // are compared with nothing but 16-byte boundaries and the outputs
-  void* const stand_in = (void*)(uintptr_t)(uint64_t(1) << 62);
+  auto output = [&](sl::DenseParams* p, int i, const sl_tensor& d, const View& v, int64_t count) {
+    p->kept[i] = d.data, p->kept_rs[i] = v.rs, p->kept_cs[i] = v.cs, p->kept_bs[i] = count > 1 ? v.bs : 0;
+    if (quad_rows(v, count)) p->flags |= sl::DF_KEPT_VEC << i;
+  };
+  P.kind = dt == SL_F16 ? sl::EK_F16 : sl::EK_BF16;
   if (P.want_dx) {
     if (tokens) {
       P.off_rows = take(n * rows * 2 * Fp);
       P.off_wt = take(weights * K * 2 * Fp);
       for (int i = 0; i < 2; ++i)
-        if ((s = transpose(&P.wt[i], w[WG + i], weights, Fp, K * 2 * Fp, 2 * Fp)) != SL_OK) return s;
+        if ((s = transpose(&P.prepare.pack[1 + i], w[WG + i], weights, Fp, K * 2 * Fp, 2 * Fp)) != SL_OK) return s;
     }
-    P.dx.a = matrix(tokens ? stand_in : nullptr, dt, n, rows, tokens ? 2 * Fp : 0, rows * 2 * Fp, 2 * Fp, 1);
-    P.dx.b = matrix(tokens ? stand_in : nullptr, dt, one_weight ? -1 : n, K, tokens ? 2 * Fp : 0, K * 2 * Fp, 2 * Fp, 1);
-    P.dx.c.layout.rank = 2;
-    P.dx.d = matrix(args->dx.data, dt, n, rows, K, w[DX].bs, w[DX].rs, w[DX].cs);
-    if ((s = product(&P.dx)) != SL_OK) return s;
+    if ((s = product(&P.dx, &P.dx_tile, n, rows, K, tokens ? 2 * Fp : 0, rows * 2 * Fp, one_weight ? 0 : K * 2 * Fp, 0)) != SL_OK) return s;
+    output(&P.dx, 0, args->dx, w[DX], n);
+    if (w[DX].cs == 1) P.dx.flags |= sl::DF_ROWS;
   }
   if (P.want_dw) {
     if (tokens) {
       P.off_t = take(one_weight ? 2 * Fp * across : n * 2 * Fp * Mp);
       P.off_xt = take(one_weight ? K * across : n * K * Mp);
-      if ((s = transpose(&P.xt, w[X], n, Mp, one_weight ? Mp : K * Mp, across)) != SL_OK) return s;
+      if ((s = transpose(&P.prepare.pack[0], w[X], n, Mp, one_weight ? Mp : K * Mp, across)) != SL_OK) return s;
     }
-    const int64_t depth = tokens ? across : 0;
-    const int64_t apart = ((intptr_t)args->dw_up.data - (intptr_t)args->dw_gate.data) / 2;
-    // both as a batch of two where dw_up lies behind dw_gate in the same strides
-    const bool pair = weights == 1 && v[DWG].rs == v[DWU].rs && v[DWG].cs == v[DWU].cs &&
-                      apart > (F - 1) * v[DWG].rs + (K - 1) * v[DWG].cs;
-    P.dw_calls = pair ? 1 : 2;
-    for (int i = 0; i < P.dw_calls; ++i) {
-      sl_gemm_args& a = P.dw[i];
-      const int64_t count = pair ? 2 : one_weight ? -1 : n;
-      void* const at = tokens ? stand_in : nullptr;
-      a.a = matrix(at, dt, count, F, depth, pair ? Fp * across : 2 * Fp * Mp, across, 1);
-      a.b = matrix(at, dt, pair || one_weight ? -1 : n, K, depth, K * Mp, across, 1);
-      a.c.layout.rank = 2;
-      const View& d = v[DWG + i];
-      a.d = matrix(t[DWG + i]->data, dt, count, F, K, pair ? apart : d.bs, d.rs, d.cs);
-      if ((s = product(&a)) != SL_OK) return s;
-    }
+    if ((s = product(&P.dw, &P.dw_tile, 2 * weights, F, K, tokens ? across : 0, Fp * across, K * across, 1)) != SL_OK) return s;
+    for (int i = 0; i < 2; ++i) output(&P.dw, i, *t[DWG + i], v[DWG + i], weights);
+    if (v[DWG].cs == 1 && v[DWU].cs == 1) P.dw.flags |= sl::DF_ROWS;
   }
-  P.off_gemm = P.ws_bytes;
-  P.ws_bytes += P.gemm_bytes;
+  if (!grid_fits(sl::gated_prepare_groups(&P.prepare), 1, 1, sl::kPrepareThreads)) return fail(SL_ERR_SHAPE, "the operands are too large");
   return SL_OK;
 }
 
@@ -639,34 +638,22 @@ sl_status sl_gated_backward(const sl_gated_backward_args* args, void* stream) {
   if ((s = check_arch()) != SL_OK) return s;
   const hipStream_t st = (hipStream_t)stream;
   char* const ws = (char*)args->workspace;
-  auto at = [&](int64_t off) { return (uint16_t*)(ws + off); };
-  const bool tokens = P.slope.batch > 0;
-  hipError_t e = hipSuccess;
-  if (tokens) {
-    if (P.want_dx) P.slope.rows = at(P.off_rows);
-    if (P.want_dw) P.slope.t = at(P.off_t);
-    e = sl::launch_gated_slope(P.slope, st);
+  if (P.prepare.slope.batch > 0) {  // (without tokens the products have K = 0 and read nothing)
     if (P.want_dx) {
-      for (int i = 0; i < 2 && e == hipSuccess; ++i) {
-        P.wt[i].out = at(P.off_wt) + i * P.slope.Fp;
-        e = sl::launch_pack(P.wt[i], st);
-      }
-      P.dx.a.data = at(P.off_rows), P.dx.b.data = at(P.off_wt);
+      P.prepare.slope.rows = (uint16_t*)(ws + P.off_rows);
+      for (int i = 0; i < 2; ++i) P.prepare.pack[1 + i].out = (uint16_t*)(ws + P.off_wt) + i * P.prepare.slope.Fp;
+      P.dx.a = (const uint8_t*)(ws + P.off_rows), P.dx.b[0] = (const uint8_t*)(ws + P.off_wt);
     }
-    if (P.want_dw && e == hipSuccess) {
-      P.xt.out = at(P.off_xt);
-      e = sl::launch_pack(P.xt, st);
-      for (int i = 0; i < P.dw_calls; ++i) P.dw[i].a.data = at(P.off_t) + i * P.slope.t_us, P.dw[i].b.data = at(P.off_xt);
+    if (P.want_dw) {
+      P.prepare.slope.t = (uint16_t*)(ws + P.off_t);
+      P.prepare.pack[0].out = (uint16_t*)(ws + P.off_xt);
+      P.dw.a = (const uint8_t*)(ws + P.off_t), P.dw.b[0] = (const uint8_t*)(ws + P.off_xt);
     }
-    if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
   }
-  auto run = [&](sl_gemm_args* a) {
-    a->workspace = ws + P.off_gemm, a->workspace_bytes = P.gemm_bytes;
-    return sl_gemm(a, stream);
-  };
-  if (P.want_dx && (s = run(&P.dx)) != SL_OK) return s;
-  for (int i = 0; P.want_dw && i < P.dw_calls; ++i)
-    if ((s = run(&P.dw[i])) != SL_OK) return s;
+  hipError_t e = sl::launch_gated_prepare(P.prepare, st);
+  if (e == hipSuccess && P.want_dx) e = sl::launch_gated_products(P.dx, P.kind, P.dx_tile, st);
+  if (e == hipSuccess && P.want_dw) e = sl::launch_gated_products(P.dw, P.kind, P.dw_tile, st);
+  if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
   return SL_OK;
 }
 

@@ -13,9 +13,8 @@
 // lane's accumulators hold g and u of the same (m, n): the activation and the
 // product with u cost no traffic, and A is read once for both.
 //
-// Tiles, from large to small (dense_plan):
-//   DT_RING    256 x 256, 4 waves, accumulators in AGPRs, LDS a ring of five
-//   DT_128     128 x 128, 4 waves, a few LDS stages
+// Tiles (dense_plan):
+//   256 x 256, 256 x 128, 128 x 128   4 waves, accumulators in AGPRs, LDS a ring of five
 //   DT_STREAM  up to 64 rows of A, the waves of a workgroup splitting K
 //   DT_SKINNY  up to 16 rows, K-tiles straight from memory into registers
 #pragma once
@@ -74,12 +73,13 @@ __device__ __forceinline__ floatx4 dense_value(floatx4 v) {
 // end, read zero: their offsets are out of range whatever the strides.
 template <int ROWS, int NT, int G>
 struct RowLoader {
-  static constexpr int WAVES = NT / 64;
-  static constexpr int ITERS = ROWS / (8 * WAVES);
+  static constexpr int WAVES = NT / 64, RB = kRowBytes;
+  static constexpr int CPR = RB / 16, RPI = 64 / CPR;  // 16-byte chunks of a row, rows of a copy
+  static constexpr int ITERS = ROWS / (RPI * WAVES);
   static constexpr int SRC = G > 0 ? 2 : 1;
-  static_assert(ITERS >= 1 && ROWS % (8 * WAVES) == 0, "copies of whole waves");
-  static_assert(G == 0 || G % (8 * WAVES) == 0, "a copy reads one matrix");
-  static constexpr int src(int j) { return G > 0 ? (j * WAVES * 8 / (G > 0 ? G : 1)) & 1 : 0; }
+  static_assert(ITERS >= 1 && ROWS % (RPI * WAVES) == 0, "copies of whole waves");
+  static_assert(G == 0 || G % (RPI * WAVES) == 0, "a copy reads one matrix");
+  static constexpr int src(int j) { return G > 0 ? (j * WAVES * RPI / (G > 0 ? G : 1)) & 1 : 0; }
 
   __amdgpu_buffer_rsrc_t rsrc[SRC];
   int32_t K, wave, lane;
@@ -98,8 +98,8 @@ struct RowLoader {
       voff[j] = r < rows ? (uint32_t)(r * rs[src(j)] + 16 * chunk(j)) : kOutOfRange;
     }
   }
-  __device__ __forceinline__ int32_t tile_row(int j) const { return (j * WAVES + wave) * 8 + lane / 8; }
-  __device__ __forceinline__ int32_t chunk(int j) const { return (lane & 7) ^ swz(tile_row(j), 0); }
+  __device__ __forceinline__ int32_t tile_row(int j) const { return (j * WAVES + wave) * RPI + lane / CPR; }
+  __device__ __forceinline__ int32_t chunk(int j) const { return (lane & (CPR - 1)) ^ swz(tile_row(j), 0, RB); }
 
   // From here on the copies are of the last K-tile, of which `bytes` lie inside K
   // (128 or fewer): the chunks past them read zero.
@@ -115,13 +115,13 @@ struct RowLoader {
   // index a member array inside the builtin's argument list.)
   __device__ __forceinline__ void issue_full(int32_t t, char* lds, int j) const {
     const uint32_t v = voff[j];
-    const uint32_t s = (uint32_t)(t * kRowBytes);
+    const uint32_t s = (uint32_t)(t * RB);
     const __amdgpu_buffer_rsrc_t from = rsrc[src(j)];
     __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void_t*)(lds + (j * WAVES + wave) * 1024), 16, v, s, 0, 0);
   }
   // copy j of any K-tile
   __device__ __forceinline__ void issue_one(int32_t t, char* lds, int j) const {
-    const uint32_t at = voff[j] == kOutOfRange || t * kRowBytes + 16 * chunk(j) >= K ? kOutOfRange : voff[j] + (uint32_t)(t * kRowBytes);
+    const uint32_t at = voff[j] == kOutOfRange || t * RB + 16 * chunk(j) >= K ? kOutOfRange : voff[j] + (uint32_t)(t * RB);
     const __amdgpu_buffer_rsrc_t from = rsrc[src(j)];
     __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void_t*)(lds + (j * WAVES + wave) * 1024), 16, at, 0, 0, 0);
   }
@@ -143,7 +143,7 @@ __device__ __forceinline__ RowLoader<BN, NT, G> dense_b_loader(const DenseParams
     const int64_t rs[2] = {p.b_rs[0], p.b_rs[1]};
     return RowLoader<BN, NT, G>(base, rs, cols, p.K, wave, lane);
   } else {
-    const uint8_t* const base[1] = {p.b[0] + batch * p.b_bs[0] + n0 * p.b_rs[0]};
+    const uint8_t* const base[1] = {p.b[0] + (batch >> p.b_shift) * p.b_bs[0] + n0 * p.b_rs[0]};
     const int64_t rs[1] = {p.b_rs[0]};
     return RowLoader<BN, NT, G>(base, rs, cols, p.K, wave, lane);
   }
@@ -290,35 +290,41 @@ __device__ __forceinline__ void dense_rows(const EPI& epi, const DenseParams& p,
 }
 
 // ---------------------------------------------------------------------------
-// 256 x 256: the schedule of gemm_f16_w4r_kernel (gemm_f16.hip), which see.
-// Four waves, one per SIMD, each a 128 x 128 block of 8 x 8 instruction tiles
-// with its accumulators in AGPRs; LDS a ring of five operand K-tiles, operand
-// tile q (A of K-tile q / 2 for even q, B for odd q) in slot q % 5.  Per
-// K-tile: reads of its first slice beside the last products of the K-tile
-// before, the first slice's products beside the reads of the second, half of
-// the second's, one barrier.  The gated pair's wave holds 64 rows of each matrix.
+// Large tiles, on the schedule of gemm_f16_w4r_kernel (gemm_f16.hip), which see:
+// four waves, each FM x FN instruction tiles with its accumulators in AGPRs,
+// LDS a ring of five operand K-tiles, operand tile q (A of K-tile q / 2 for even q, B for
+// odd q) in slot q % 5.  Per K-tile: reads of its first slice beside the last
+// products of the K-tile before, the first slice's products beside the reads of
+// the second, half of the second's, one barrier.  A copy has a K-tile of compute or
+// more to land.
+//   8 x 8  256 x 256, one workgroup to a CU
+//   8 x 4  256 x 128, the same
+//   4 x 4  128 x 128, two to a CU
+// The gated pair's wave holds 8 FN rows of each matrix.
 // ---------------------------------------------------------------------------
-template <int EK, bool GATED, class EPI>
-__global__ __launch_bounds__(256, 1) void dense_ring_kernel(const DenseParams p) {
-  constexpr int F = 8, SLOT = 256 * kRowBytes, LOADS = 8;
-  constexpr int BN = kResultCols<GATED, 256>;
+template <int EK, bool GATED, int FM, int FN, class EPI>
+__global__ __launch_bounds__(256, FM == 8 ? 1 : 2) void dense_ring_kernel(const DenseParams p) {
+  constexpr int ROWS_A = 32 * FM, ROWS_B = 32 * FN, SLOT = (FM > FN ? ROWS_A : ROWS_B) * kRowBytes;
+  constexpr int BN = kResultCols<GATED, ROWS_B>;
+  constexpr int NR = FM + FN;      // fragment reads of a slice
+  constexpr int NH = FM / 2 * FN;  // products of half a slice
   __shared__ __attribute__((aligned(1024))) char smem[5 * SLOT];
   const int32_t lane = threadIdx.x & 63;
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const TileCoord tc = map_tile(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.batch);
-  const int64_t m0 = (int64_t)tc.tm * 256, n0 = (int64_t)tc.tn * BN;
-  const int32_t rows_a = (int32_t)(p.M - m0 < 256 ? p.M - m0 : 256);
+  const int64_t m0 = (int64_t)tc.tm * ROWS_A, n0 = (int64_t)tc.tn * BN;
+  const int32_t rows_a = (int32_t)(p.M - m0 < ROWS_A ? p.M - m0 : ROWS_A);
   const int32_t cols = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
-  auto la = dense_a_loader<256, 256>(p, tc.batch, m0, rows_a, wave, lane);
-  auto lb = dense_b_loader<GATED, 256, 256, GATED ? 64 : 0>(p, tc.batch, n0, cols, wave, lane);
-  static_assert(decltype(la)::ITERS == LOADS && decltype(lb)::ITERS == LOADS, "copy layout");
+  auto la = dense_a_loader<ROWS_A, 256>(p, tc.batch, m0, rows_a, wave, lane);
+  auto lb = dense_b_loader<GATED, ROWS_B, 256, GATED ? 8 * FN : 0>(p, tc.batch, n0, cols, wave, lane);
+  static_assert(decltype(la)::ITERS == FM && decltype(lb)::ITERS == FN, "copy layout");
 
-  floatx4 acc[F][F];
+  floatx4 acc[FM][FN];
 #pragma unroll
-  for (int i = 0; i < F; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < F; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-  const int32_t a_row0 = (wave & 1) * 128, b_row0 = (wave >> 1) * 128;
+    for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  const int32_t a_row0 = (wave & 1) * 16 * FM, b_row0 = (wave >> 1) * 16 * FN;
   const int32_t T = p.k_tiles;  // at least 1
   __builtin_assume(T >= 1);
   // past the last K-tile the look-ahead copies repeat it and are not read
@@ -327,7 +333,7 @@ __global__ __launch_bounds__(256, 1) void dense_ring_kernel(const DenseParams p)
   auto copy_a = [&](int32_t u, char* dst, int j) { la.issue_full(kt(u), dst, j); };
   auto copy_b = [&](int32_t u, char* dst, int j) { lb.issue_full(kt(u), dst, j); };
   const int32_t last_bytes = (int32_t)p.K - (T - 1) * kRowBytes;
-  u32x4 fa0[F], fb0[F], fa1[F], fb1[F];
+  u32x4 fa0[FM], fb0[FN], fa1[FM], fb1[FN];
   typedef __attribute__((address_space(3))) const u32x4 lds_u4;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)smem;
   uint32_t offA[2][2], offB[2][2], bA[2][2], bB[2][2];
@@ -350,30 +356,34 @@ __global__ __launch_bounds__(256, 1) void dense_ring_kernel(const DenseParams p)
     asm volatile("" : "+v"(bA[0][0]), "+v"(bA[0][1]), "+v"(bA[1][0]), "+v"(bA[1][1]));
     asm volatile("" : "+v"(bB[0][0]), "+v"(bB[0][1]), "+v"(bB[1][0]), "+v"(bB[1][1]));
   };
-  auto read = [&](int r, int ks, u32x4(&fa)[F], u32x4(&fb)[F]) {
-    if (r < F)
+  // B's fragments first
+  auto read = [&](int r, int ks, u32x4(&fa)[FM], u32x4(&fb)[FN]) {
+    if (r < FN)
       fb[r] = *(lds_u4*)(uintptr_t)(bB[ks][r & 1] + 4096u * (uint32_t)(r >> 1));
     else
-      fa[r - F] = *(lds_u4*)(uintptr_t)(bA[ks][r & 1] + 4096u * (uint32_t)((r - F) >> 1));
+      fa[r - FN] = *(lds_u4*)(uintptr_t)(bA[ks][(r - FN) & 1] + 4096u * (uint32_t)((r - FN) >> 1));
   };
-  auto products = [&](int i0, int q, const u32x4(&fa)[F], const u32x4(&fb)[F]) {
+  // products [e0, e1) of the block's rows from i0 on
+  auto products = [&](int i0, int e0, int e1, const u32x4(&fa)[FM], const u32x4(&fb)[FN]) {
 #pragma unroll
-    for (int e = 2 * q; e < 2 * q + 2; ++e) dense_mfma_agpr<EK>(acc[i0 + e / F][e % F], fb[e % F], fa[i0 + e / F]);
+    for (int e = e0; e < e1; ++e) dense_mfma_agpr<EK>(acc[i0 + e / FN][e % FN], fb[e % FN], fa[i0 + e / FN]);
   };
   if (T == 1) la.last_tile(last_bytes), lb.last_tile(last_bytes);
 #pragma unroll
-  for (int j = 0; j < LOADS; ++j) copy_a(0, slot(0), j);
+  for (int j = 0; j < FM; ++j) copy_a(0, slot(0), j);
 #pragma unroll
-  for (int j = 0; j < LOADS; ++j) copy_b(0, slot(1), j);
+  for (int j = 0; j < FN; ++j) copy_b(0, slot(1), j);
   if (T == 2) la.last_tile(last_bytes);
 #pragma unroll
-  for (int j = 0; j < LOADS; ++j) copy_a(1, slot(2), j);
+  for (int j = 0; j < FM; ++j) copy_a(1, slot(2), j);
   if (T == 2) lb.last_tile(last_bytes);
   if (T == 3) la.last_tile(last_bytes);
   // the first K-tile's first part computes with zero fragments (adds nothing)
 #pragma unroll
-  for (int i = 0; i < F; ++i) fa1[i] = fb1[i] = u32x4{0, 0, 0, 0};
-  wait_vmem_n<LOADS>();
+  for (int i = 0; i < FM; ++i) fa1[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < FN; ++j) fb1[j] = u32x4{0, 0, 0, 0};
+  wait_vmem_n<FM>();
   phase_barrier();
   int32_t sa = 0;  // slot of A(t); B(t) in the next one
   int32_t t = 0;
@@ -384,127 +394,60 @@ __global__ __launch_bounds__(256, 1) void dense_ring_kernel(const DenseParams p)
   do {
     const int32_t s3 = sa + 3 >= 5 ? sa - 2 : sa + 3, s4 = sa == 0 ? 4 : sa - 1;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      read(q, 0, fa0, fb0);
-      if (!(q & 1)) copy_b(t + 1, slot(s3), q >> 1);
-      products(F / 2, q, fa1, fb1);  // K-tile t - 1's
+    for (int g = 0; g < NR; ++g) {
+      read(g, 0, fa0, fb0);
+#pragma unroll
+      for (int j = g * FN / NR; j < (g + 1) * FN / NR; ++j) copy_b(t + 1, slot(s3), j);
+      products(FM / 2, g * NH / NR, (g + 1) * NH / NR, fa1, fb1);  // K-tile t - 1's
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      read(q, 1, fa1, fb1);
-      if (q & 1) copy_a(t + 2, slot(s4), q >> 1);
-      products(q < 8 ? 0 : F / 2, 2 * (q & 7), fa0, fb0);
-      products(q < 8 ? 0 : F / 2, 2 * (q & 7) + 1, fa0, fb0);
+    for (int g = 0; g < NR; ++g) {
+      read(g, 1, fa1, fb1);
+#pragma unroll
+      for (int j = g * FM / NR; j < (g + 1) * FM / NR; ++j) copy_a(t + 2, slot(s4), j);
+      products(0, g * 2 * NH / NR, (g + 1) * 2 * NH / NR, fa0, fb0);
       __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int q = 0; q < 16; ++q) products(0, q, fa1, fb1);
+    products(0, 0, NH, fa1, fb1);
     const int32_t na = sa + 2 >= 5 ? sa - 3 : sa + 2;
     bases(na, na == 4 ? 0 : na + 1);
     // the next copies are B(t + 2) and A(t + 3)
     if (t + 2 == T - 1) lb.last_tile(last_bytes);
     if (t + 3 == T - 1) la.last_tile(last_bytes);
-    wait_vmem_n<LOADS>();  // in flight after this: A(t + 2)
+    wait_vmem_n<FM>();  // in flight after this: A(t + 2)
     phase_barrier();
     sa = na;
   } while (++t < T);
-#pragma unroll
-  for (int q = 0; q < 16; ++q) products(F / 2, q, fa1, fb1);
+  products(FM / 2, 0, NH, fa1, fb1);
   wait_vmem();
   // the products are inline assembly: an idle of 32 cycles between the last
   // of them and the first read of an accumulator, which the two statements
   // that re-define them all hold in place
   auto pin = [&] {
 #pragma unroll
-    for (int i = 0; i < F; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < F; j += 2) asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));
+      for (int j = 0; j < FN; j += 2) asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));
   };
   pin();
   asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
   pin();
   // every wave's copies have landed and its reads of the ring are done
   __syncthreads();
-  char* region = smem + wave * 32768;
+  constexpr int COLS = 16 * FN;
+  char* region = smem + wave * (64 * COLS * 4);
+  static_assert(4 * 64 * COLS * 4 <= 5 * SLOT, "the sums fit");
   const EPI epi(p, tc.batch);
-  const int64_t n_base = n0 + kResultCols<GATED, 128> * (wave >> 1);
+  const int64_t n_base = n0 + kResultCols<GATED, COLS> * (wave >> 1);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < FM / 4; ++h) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < F; ++j) *(floatx4*)(region + rows_chunk(16 * i + (lane & 15), 4 * j + (lane >> 4))) = acc[4 * h + i][j];
-    dense_rows<EK, GATED, 128>(epi, p, tc.batch, m0 + a_row0 + 64 * h, n_base, lane, region);
+      for (int j = 0; j < FN; ++j) *(floatx4*)(region + rows_chunk<COLS>(16 * i + (lane & 15), 4 * j + (lane >> 4))) = acc[4 * h + i][j];
+    dense_rows<EK, GATED, COLS>(epi, p, tc.batch, m0 + a_row0 + 64 * h, n_base, lane, region);
   }
-}
-
-// ---------------------------------------------------------------------------
-// 128 x 128: four waves, each 64 x 64, STAGES K-tiles of both operands in LDS
-// (two, and two workgroups to a CU; or four, where there is not more than one
-// for each).  The gated pair's wave holds 32 rows of each matrix.
-// ---------------------------------------------------------------------------
-template <int EK, bool GATED, int STAGES, class EPI>
-__global__ __launch_bounds__(256, STAGES == 2 ? 2 : 1) void dense_tile_kernel(const DenseParams p) {
-  constexpr int F = 4, HALF = 128 * kRowBytes, STAGE = 2 * HALF;
-  constexpr int BN = kResultCols<GATED, 128>;
-  __shared__ __attribute__((aligned(1024))) char smem[STAGES * STAGE];
-  const int32_t lane = threadIdx.x & 63;
-  const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const TileCoord tc = map_tile(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.batch);
-  const int64_t m0 = (int64_t)tc.tm * 128, n0 = (int64_t)tc.tn * BN;
-  const int32_t rows_a = (int32_t)(p.M - m0 < 128 ? p.M - m0 : 128);
-  const int32_t cols = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
-  const auto la = dense_a_loader<128, 256>(p, tc.batch, m0, rows_a, wave, lane);
-  const auto lb = dense_b_loader<GATED, 128, 256, GATED ? 32 : 0>(p, tc.batch, n0, cols, wave, lane);
-  constexpr int LOADS = decltype(la)::ITERS + decltype(lb)::ITERS;
-  const int32_t a_row0 = (wave & 1) * 64, b_row0 = (wave >> 1) * 64;
-  floatx4 acc[F][F];
-#pragma unroll
-  for (int i = 0; i < F; ++i)
-#pragma unroll
-    for (int j = 0; j < F; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-  const int32_t T = p.k_tiles;
-  auto request = [&](int32_t t, int d) {
-    la.issue(t, smem + d * STAGE);  // past the last K-tile: zeros, not read
-    lb.issue(t, smem + d * STAGE + HALF);
-  };
-#pragma unroll
-  for (int d = 0; d < STAGES - 1; ++d) request(d, d);
-  for (int32_t t = 0; t < T; t += STAGES) {
-#pragma unroll
-    for (int d = 0; d < STAGES; ++d) {
-      wait_vmem_n<(STAGES - 2) * LOADS>();  // K-tile t + d has landed
-      phase_barrier();                      // for every wave, and the one before is no longer read
-      request(t + d + STAGES - 1, (d + STAGES - 1) % STAGES);
-      if (t + d >= T) continue;
-      const char* cur = smem + d * STAGE;
-      u32x4 fa[2][F], fb[2][F];
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-#pragma unroll
-        for (int j = 0; j < F; ++j) fb[ks][j] = dense_frag(cur + HALF, lane, b_row0 + 16 * j, ks);
-#pragma unroll
-        for (int i = 0; i < F; ++i) fa[ks][i] = dense_frag(cur, lane, a_row0 + 16 * i, ks);
-      }
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-        for (int i = 0; i < F; ++i)
-#pragma unroll
-          for (int j = 0; j < F; ++j) acc[i][j] = dense_mfma<EK>(fb[ks][j], fa[ks][i], acc[i][j]);
-    }
-  }
-  wait_vmem();
-  __syncthreads();
-  static_assert(4 * 64 * 64 * 4 <= STAGES * STAGE, "the sums fit");
-  char* region = smem + wave * 16384;
-#pragma unroll
-  for (int i = 0; i < F; ++i)
-#pragma unroll
-    for (int j = 0; j < F; ++j) *(floatx4*)(region + rows_chunk<64>(16 * i + (lane & 15), 4 * j + (lane >> 4))) = acc[i][j];
-  const EPI epi(p, tc.batch);
-  dense_rows<EK, GATED, 64>(epi, p, tc.batch, m0 + a_row0, n0 + kResultCols<GATED, 64> * (wave >> 1), lane, region);
 }
 
 // The sums of a workgroup's W waves, each of FM x FN instruction tiles, meet
@@ -554,7 +497,7 @@ __global__ __launch_bounds__(kDenseSkinnyWaves * 64) void dense_skinny_kernel(co
   __amdgpu_buffer_rsrc_t rb[GATED ? 2 : 1];
 #pragma unroll
   for (int s = 0; s < (GATED ? 2 : 1); ++s)
-    rb[s] = make_rsrc(p.b[s] + batch * p.b_bs[s] + n0 * p.b_rs[s], (uint32_t)((cols - 1) * p.b_rs[s] + p.K));
+    rb[s] = make_rsrc(p.b[s] + (batch >> p.b_shift) * p.b_bs[s] + n0 * p.b_rs[s], (uint32_t)((cols - 1) * p.b_rs[s] + p.K));
   const int32_t kl = 16 * (lane >> 4), K = (int32_t)p.K;
   const uint32_t off_a = (lane & 15) < rows ? (uint32_t)((lane & 15) * p.a_rs + kl) : kOutOfRange;
   uint32_t off_b[FN];
@@ -679,13 +622,9 @@ hipError_t dense_launch(const DenseParams& p, const DensePlan& plan, hipStream_t
   typedef std::integral_constant<int, 3> c3;
   typedef std::integral_constant<int, 4> c4;
   switch (plan.tile) {
-    case DT_RING:
-      hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, EPI>), grid, block, 0, s, p);
-      break;
-    case DT_128:
-      if (plan.stages == 2) hipLaunchKernelGGL((dense_tile_kernel<EK, GATED, 2, EPI>), grid, block, 0, s, p);
-      else hipLaunchKernelGGL((dense_tile_kernel<EK, GATED, 4, EPI>), grid, block, 0, s, p);
-      break;
+    case DT_256x256: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 8, 8, EPI>), grid, block, 0, s, p); break;
+    case DT_256x128: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 8, 4, EPI>), grid, block, 0, s, p); break;
+    case DT_128x128: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 4, 4, EPI>), grid, block, 0, s, p); break;
     case DT_STREAM:
       if (plan.bm == 32) plan.bn == 32 ? stream(c2{}, c2{}, c4{}) : stream(c2{}, c4{}, c3{});
       else plan.bn == 32 ? stream(c4{}, c2{}, c3{}) : stream(c4{}, c4{}, c2{});

@@ -165,6 +165,7 @@ struct DenseParams {
   int64_t c_rs, c_cs, c_bs, d_rs, d_cs, d_bs, kept_rs[2], kept_cs[2], kept_bs[2];
   int32_t type;             // OT_* of C, D, g and u
   int32_t act;              // ACT_*
+  int32_t b_shift;          // matrix b of the batch takes B's matrix b >> b_shift
   int32_t batch, tiles_m, tiles_n, group_m;
   int32_t k_tiles;          // ceil(K / 128)
   int32_t flags;            // DF_*
@@ -177,38 +178,36 @@ constexpr int32_t DF_ROWS = 16;     // the columns of C and of every output cont
 // tile configurations: rows of A x rows of B (for the gated pair, of both
 // matrices together)
 enum DenseTile : int32_t {
-  DT_RING = 0,     // 256 x 256: 4 waves, each 128 x 128
-  DT_128 = 1,      // 128 x 128: 4 waves, each 64 x 64
-  DT_STREAM = 2,   // 32 or 64 rows of A, 4 waves that split K
-  DT_SKINNY = 3,   // 16 rows of A, 8 waves that split K
+  DT_256x256 = 0,  // 4 waves, each 128 x 128
+  DT_256x128 = 1,  // 4 waves, each 128 x 64
+  DT_128x128 = 2,  // 4 waves, each 64 x 64; two workgroups to a CU
+  DT_STREAM = 3,   // 32 or 64 rows of A, 4 waves that split K
+  DT_SKINNY = 4,   // 16 rows of A, 8 waves that split K
 };
 constexpr int32_t kDenseSkinnyWaves = 8, kDenseStreamWaves = 4;
-constexpr int32_t kDenseKBytes = 128;  // of a row in a K-tile
 struct DensePlan {
   int32_t tile;
   int32_t bm, bn;       // rows of A and of B of a workgroup
   int32_t threads, lds;
-  int32_t stages;       // LDS K-tiles of DT_128 and DT_STREAM
+  int32_t stages;       // LDS K-tiles of DT_STREAM
 };
 // `gated`: bn / 2 columns of the result to a workgroup
-DensePlan dense_plan(int32_t kind, bool gated, int64_t batch, int64_t M, int64_t N, int64_t K);
+DensePlan dense_plan(bool gated, int64_t batch, int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_i8(const DenseParams& p, const DensePlan& plan, hipStream_t stream);
 hipError_t launch_gated(const DenseParams& p, int32_t kind, const DensePlan& plan, hipStream_t stream);
 
 // ---------------------------------------------------------------------------
-// What the backward pass of the gated block does beside its products.
-// 16-bit matrices copied to rows of contiguous values: out row r (of `out_rs`
-// values; columns [cols, width) zero) from x's row r, any strides.
+// What the gated block's calls do ahead of their products (gated_prepare.hip),
+// one launch.  16-bit matrices copied to rows of contiguous values: out row r
+// (of `out_rs` values; columns [cols, width) zero) from x's row r, any strides.
 // ---------------------------------------------------------------------------
 struct PackParams {
   const uint16_t* x;
   uint16_t* out;
-  int64_t rows, cols, width;   // width a multiple of 8
+  int64_t rows, cols, width;   // rows 0: no copy; width a multiple of 8
   int64_t x_bs, x_rs, x_cs, out_bs, out_rs;  // out_rs, out_bs multiples of 8
   int32_t batch;
 };
-int64_t pack_groups(const PackParams& p);
-hipError_t launch_pack(const PackParams& p, hipStream_t stream);
 
 // dg = dh u act'(g) and du = dh act(g), each rounded to 16 bits, as rows
 // (dg's columns at 0, du's at Fp of a row of 2 Fp) and as columns (row f of
@@ -220,11 +219,21 @@ struct GatedSlopeParams {
   uint16_t* rows;              // may be NULL; row m of batch b at rows + (b M + m) 2 Fp
   uint16_t* t;                 // may be NULL
   int64_t t_bs, t_rs, t_us;
-  int32_t type, act, batch;
+  int32_t type, act, batch;    // batch 0: nothing to do
 };
-int64_t gated_slope_groups(const GatedSlopeParams& p);
-hipError_t launch_gated_slope(const GatedSlopeParams& p, hipStream_t stream);
-constexpr int32_t kPackThreads = 256;
+struct GatedPrepareParams {
+  GatedSlopeParams slope;
+  PackParams pack[3];
+  int64_t first[5];            // workgroups of the slopes, the copies; set by gated_prepare_groups
+};
+constexpr int32_t kPrepareThreads = 256;
+int64_t gated_prepare_groups(GatedPrepareParams* p);
+hipError_t launch_gated_prepare(const GatedPrepareParams& p, hipStream_t stream);
+
+// The products of the backward pass: 16-bit D = A B^T as DenseParams states it,
+// D in kept[0]; with pairs (b_shift 1) matrix 2 i + s of the batch takes B's
+// matrix i and goes to matrix i of kept[s].
+hipError_t launch_gated_products(const DenseParams& p, int32_t kind, const DensePlan& plan, hipStream_t stream);
 
 template <int T>
 struct OrthoElem {
