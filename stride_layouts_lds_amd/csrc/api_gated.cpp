@@ -37,17 +37,14 @@ DensePlan dense_plan(bool gated, int64_t batch, int64_t M, int64_t N, int64_t K)
   if (M <= 64 || K == 0) return best;
   const double groups = (double)batch * (double)ceil_div(M, bm) * (double)ceil_div(B, bn);
   double least = std::ceil(groups / kCUs) * (5.0 + T * (bn == 64 ? 0.2 : 0.13));
-  constexpr struct {
-    int32_t tile, bm, bn, per_cu;
-    double start, k, k_alone;  // alone: one workgroup to a CU
-  } shapes[3] = {{DT_256x256, 256, 256, 1, 10.0, 1.3, 1.3}, {DT_256x128, 256, 128, 1, 7.0, 0.77, 0.77}, {DT_128x128, 128, 128, 2, 4.2, 0.8, 0.51}};
-  for (const auto& t : shapes) {
-    const double tiles = (double)batch * (double)ceil_div(M, t.bm) * (double)ceil_div(B, t.bn), slots = kCUs * t.per_cu;
-    const double whole = std::floor(tiles / slots), rest = tiles - whole * slots;
-    double cost = whole * (t.start + T * t.k);
-    if (rest > 0) cost += t.start + T * (rest <= kCUs ? t.k_alone : t.k);
-    if (cost < least) least = cost, best = {t.tile, t.bm, t.bn, 256, 5 * 128 * t.bm, 0};
-  }
+  auto tiles = [&](int64_t rows_a, int64_t rows_b) { return (double)batch * (double)ceil_div(M, rows_a) * (double)ceil_div(B, rows_b); };
+  const double t0 = tiles(256, 256), t1 = tiles(256, 128), t2 = tiles(128, 128);
+  const double costs[3] = {std::ceil(t0 / kCUs) * (10.2 + 1.3 * T), std::ceil(t1 / kCUs) * (7.0 + 0.77 * T),
+                           t2 <= kCUs ? 4.4 + 0.51 * T : 2.4 + std::ceil(t2 / (2 * kCUs)) * (3.4 + 0.8 * T)};
+  constexpr DensePlan large[3] = {{DT_256x256, 256, 256, 256, 5 * 256 * 128, 0}, {DT_256x128, 256, 128, 256, 5 * 256 * 128, 0},
+                                  {DT_128x128, 128, 128, 256, 5 * 128 * 128, 0}};
+  for (int i = 0; i < 3; ++i)
+    if (costs[i] < least) least = costs[i], best = large[i];
   return best;
 }
 
@@ -481,10 +478,11 @@ namespace {
 
 struct BackwardPlan {
   sl::GatedPrepareParams prepare;  // copies: x's transpose, w_gate's, w_up's
-  sl::DenseParams dx, dw;
+  sl::GradParams dx, dw;
   sl::DensePlan dx_tile, dw_tile;
   int32_t kind;
   bool want_dx, want_dw, launch;
+  bool dx_ring, dw_ring;           // on operands as they lie (launch_grad_ring)
   int64_t off_rows, off_t, off_xt, off_wt, ws_bytes;
   View v[9];
 };
@@ -588,26 +586,52 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
     if (quad_rows(v, count)) p->flags |= sl::DF_KEPT_VEC << i;
   };
   P.kind = dt == SL_F16 ? sl::EK_F16 : sl::EK_BF16;
+  // a large product whose operands' rows lie on 16-byte boundaries reads them as they are
+  auto ring = [&](const sl::DensePlan& tile, const View& x, const View* y) {
+    bool ok = tokens && tile.tile == sl::DT_256x256;
+    for (const View* v : {&x, y ? y : &x})
+      ok = ok && v->cs == 1 && v->cols % 8 == 0 && v->rs % 8 == 0 && (uintptr_t)v->t->data % 16 == 0 && bstride(*v) % 8 == 0 &&
+           v->rows * v->rs * 2 + 1024 < kLim && v->rs == x.rs;
+    return ok;
+  };
+  const sl::DensePlan large = {sl::DT_256x256, 256, 256, 256, 5 * 256 * 128, 0};
   if (P.want_dx) {
-    if (tokens) {
-      P.off_rows = take(n * rows * 2 * Fp);
+    if (tokens) P.off_rows = take(n * rows * 2 * Fp);
+    if ((s = product(&P.dx.d, &P.dx_tile, n, rows, K, tokens ? 2 * Fp : 0, rows * 2 * Fp, one_weight ? 0 : K * 2 * Fp, 0)) != SL_OK) return s;
+    P.dx_ring = ring(P.dx_tile, w[WG], &w[WU]);
+    if (P.dx_ring) {
+      P.dx_tile = large;
+      if ((s = place_tiles(&P.dx.d, large, false)) != SL_OK) return s;
+      for (int i = 0; i < 2; ++i) P.dx.d.b[i] = (const uint8_t*)t[WG + i]->data, P.dx.d.b_bs[i] = 2 * bstride(w[WG + i]);
+      P.dx.d.b_rs[0] = 2 * w[WG].rs;
+      P.dx.rows = F, P.dx.parts = 2;
+    } else if (tokens) {
       P.off_wt = take(weights * K * 2 * Fp);
       for (int i = 0; i < 2; ++i)
         if ((s = transpose(&P.prepare.pack[1 + i], w[WG + i], weights, Fp, K * 2 * Fp, 2 * Fp)) != SL_OK) return s;
     }
-    if ((s = product(&P.dx, &P.dx_tile, n, rows, K, tokens ? 2 * Fp : 0, rows * 2 * Fp, one_weight ? 0 : K * 2 * Fp, 0)) != SL_OK) return s;
-    output(&P.dx, 0, args->dx, w[DX], n);
-    if (w[DX].cs == 1) P.dx.flags |= sl::DF_ROWS;
+    output(&P.dx.d, 0, args->dx, w[DX], n);
+    if (w[DX].cs == 1) P.dx.d.flags |= sl::DF_ROWS;
   }
   if (P.want_dw) {
-    if (tokens) {
+    if ((s = product(&P.dw.d, &P.dw_tile, 2 * weights, F, K, tokens ? across : 0, Fp * across, K * across, 1)) != SL_OK) return s;
+    P.dw_ring = (!one_weight || n == 1) && rows * 4 * Fp + 1024 < kLim && ring(P.dw_tile, w[X], nullptr);
+    if (P.dw_ring) {
+      if (!P.want_dx) P.off_rows = take(n * rows * 2 * Fp);
+      P.dw_tile = large;
+      if ((s = place_tiles(&P.dw.d, large, false)) != SL_OK) return s;
+      sl::DenseParams& d = P.dw.d;
+      d.a_rs = 4 * Fp, d.a_bs = rows * 4 * Fp;
+      for (int i = 0; i < 2; ++i) d.b[i] = (const uint8_t*)args->x.data, d.b_bs[i] = 2 * bstride(w[X]);
+      d.b_rs[0] = 2 * w[X].rs;
+      P.dw.rows = rows, P.dw.parts = 1, P.dw.a_second = 2 * Fp;
+    } else if (tokens) {
       P.off_t = take(one_weight ? 2 * Fp * across : n * 2 * Fp * Mp);
       P.off_xt = take(one_weight ? K * across : n * K * Mp);
       if ((s = transpose(&P.prepare.pack[0], w[X], n, Mp, one_weight ? Mp : K * Mp, across)) != SL_OK) return s;
     }
-    if ((s = product(&P.dw, &P.dw_tile, 2 * weights, F, K, tokens ? across : 0, Fp * across, K * across, 1)) != SL_OK) return s;
-    for (int i = 0; i < 2; ++i) output(&P.dw, i, *t[DWG + i], v[DWG + i], weights);
-    if (v[DWG].cs == 1 && v[DWU].cs == 1) P.dw.flags |= sl::DF_ROWS;
+    for (int i = 0; i < 2; ++i) output(&P.dw.d, i, *t[DWG + i], v[DWG + i], weights);
+    if (v[DWG].cs == 1 && v[DWU].cs == 1) P.dw.d.flags |= sl::DF_ROWS;
   }
   if (!grid_fits(sl::gated_prepare_groups(&P.prepare), 1, 1, sl::kPrepareThreads)) return fail(SL_ERR_SHAPE, "the operands are too large");
   return SL_OK;
@@ -638,21 +662,28 @@ sl_status sl_gated_backward(const sl_gated_backward_args* args, void* stream) {
   if ((s = check_arch()) != SL_OK) return s;
   const hipStream_t st = (hipStream_t)stream;
   char* const ws = (char*)args->workspace;
+  sl::DenseParams &dx = P.dx.d, &dw = P.dw.d;
   if (P.prepare.slope.batch > 0) {  // (without tokens the products have K = 0 and read nothing)
+    uint16_t* const rows = (uint16_t*)(ws + P.off_rows);
+    if (P.want_dx || P.dw_ring) P.prepare.slope.rows = rows;
     if (P.want_dx) {
-      P.prepare.slope.rows = (uint16_t*)(ws + P.off_rows);
-      for (int i = 0; i < 2; ++i) P.prepare.pack[1 + i].out = (uint16_t*)(ws + P.off_wt) + i * P.prepare.slope.Fp;
-      P.dx.a = (const uint8_t*)(ws + P.off_rows), P.dx.b[0] = (const uint8_t*)(ws + P.off_wt);
+      dx.a = (const uint8_t*)rows;
+      if (!P.dx_ring) {
+        for (int i = 0; i < 2; ++i) P.prepare.pack[1 + i].out = (uint16_t*)(ws + P.off_wt) + i * P.prepare.slope.Fp;
+        dx.b[0] = (const uint8_t*)(ws + P.off_wt);
+      }
     }
-    if (P.want_dw) {
+    if (P.want_dw && P.dw_ring) {
+      dw.a = (const uint8_t*)rows;
+    } else if (P.want_dw) {
       P.prepare.slope.t = (uint16_t*)(ws + P.off_t);
       P.prepare.pack[0].out = (uint16_t*)(ws + P.off_xt);
-      P.dw.a = (const uint8_t*)(ws + P.off_t), P.dw.b[0] = (const uint8_t*)(ws + P.off_xt);
+      dw.a = (const uint8_t*)(ws + P.off_t), dw.b[0] = (const uint8_t*)(ws + P.off_xt);
     }
   }
   hipError_t e = sl::launch_gated_prepare(P.prepare, st);
-  if (e == hipSuccess && P.want_dx) e = sl::launch_gated_products(P.dx, P.kind, P.dx_tile, st);
-  if (e == hipSuccess && P.want_dw) e = sl::launch_gated_products(P.dw, P.kind, P.dw_tile, st);
+  if (e == hipSuccess && P.want_dx) e = P.dx_ring ? sl::launch_grad_ring(P.dx, P.kind, false, st) : sl::launch_gated_products(dx, P.kind, P.dx_tile, st);
+  if (e == hipSuccess && P.want_dw) e = P.dw_ring ? sl::launch_grad_ring(P.dw, P.kind, true, st) : sl::launch_gated_products(dw, P.kind, P.dw_tile, st);
   if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
   return SL_OK;
 }

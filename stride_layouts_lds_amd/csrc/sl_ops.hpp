@@ -235,6 +235,19 @@ hipError_t launch_gated_prepare(const GatedPrepareParams& p, hipStream_t stream)
 // matrix i and goes to matrix i of kept[s].
 hipError_t launch_gated_products(const DenseParams& p, int32_t kind, const DensePlan& plan, hipStream_t stream);
 
+// The same products with B's rows (and, across, A's) contracted over: B is
+// `parts` matrices (b[0], b[1]) of `rows` rows of N contiguous values one after
+// the other, b_rs[0] bytes apart, N a multiple of 8, on 16-byte boundaries.  A: along its rows
+// (K-contiguous, each part's values padded with zeros to a multiple of 64), or
+// across, `rows` rows of M contiguous values, padded with zeros to a multiple of 64;
+// the odd matrices of pairs a_second bytes on.  256 x 256 tiles.
+struct GradParams {
+  DenseParams d;
+  int64_t rows, a_second;
+  int32_t parts;
+};
+hipError_t launch_grad_ring(const GradParams& g, int32_t kind, bool across, hipStream_t stream);
+
 template <int T>
 struct OrthoElem {
   typedef uint16_t type;
