@@ -216,14 +216,13 @@ def _record(x) -> bytes:
     absent operand) or a descriptor."""
     if x is None:
         return _ABSENT
-    if isinstance(x, sl_tensor):
-        return bytes(x)
-    if isinstance(x, PackedTensor):
-        return bytes(tensor_desc(x))
-    code = _codes.get(x.dtype)
+    code = _codes.get(x.dtype)  # (a PackedTensor's or a descriptor's is no key)
     if code is None:
-        return bytes(tensor_desc(x))
-    return _fields(x.data_ptr(), code, x.shape, x.stride())
+        return bytes(x) if isinstance(x, sl_tensor) else bytes(tensor_desc(x))
+    shape = x.shape
+    if len(shape) == 2:
+        return _pack(x.data_ptr(), code, 2, *shape, 0, *x.stride(), 0)
+    return _fields(x.data_ptr(), code, shape, x.stride())
 
 
 class PackedTensor:
@@ -271,19 +270,24 @@ def _check_devices(*operands) -> None:
             raise ValueError(f"an operand is on {x.device}: they are GPU tensors")
 
 
-def _check_one_device(*operands) -> None:
-    """GPU tensors of the current device: its stream is the one the call runs
-    on, and its address space the one the kernels see."""
-    _check_devices(*operands)
-    import torch
-    here = None
+def _one_device(*operands) -> Optional[int]:
+    """The current device's index, which every operand has to be on: its stream
+    is the one the call runs on, and its address space the one the kernels see.
+    (None where they are all descriptors.)"""
+    index = None
     for x in operands:
         if x is None or isinstance(x, sl_tensor):
             continue
-        if here is None:
-            here = torch.cuda.current_device()
-        if x.device.index != here:
-            raise ValueError(f"an operand is on {x.device}, the current device is cuda:{here}")
+        at = x.get_device()
+        if at < 0:
+            _check_devices(x)
+        if index is None:
+            import torch
+            current = getattr(torch._C, "_cuda_getDevice", None)
+            index = torch.cuda.current_device() if current is None else current()
+        if at != index:
+            raise ValueError(f"an operand is on {x.device}, the current device is cuda:{index}")
+    return index
 
 
 def make_args(a, b, c=None, d=None, sfa=None, sfb=None, block_k: int = 32, workspace=None) -> sl_gemm_args:
@@ -328,6 +332,29 @@ def _allocated(stream: int, device, make):
     with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
                            else torch.cuda.default_stream(device)):
         return make()
+
+
+_raw: dict = {}  # entry points that take their arguments as packed bytes
+
+
+def _status(name: str, record: bytes, index: Optional[int], stream: Optional[int]) -> int:
+    """The status of entry point ``name`` on packed arguments, on ``stream`` or
+    torch's current one on device ``index``.  (As bytes, without a ctypes structure in
+    between, the arguments of a call take 1 us less.)"""
+    call = _raw.get(name)
+    if call is None:
+        call = lib()[name]  # a function object of its own
+        call.restype, call.argtypes = ctypes.c_int32, [ctypes.c_char_p, ctypes.c_void_p]
+        _raw[name] = call
+    if stream is None:
+        import torch
+        handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        stream = torch.cuda.current_stream(index).cuda_stream if handle is None else handle(index)
+    return call(record, stream)
+
+
+def _run(name: str, records, index: Optional[int], stream: Optional[int]) -> None:
+    _check(_status(name, b"".join(records), index, stream))
 
 
 def sl_gemm(args: sl_gemm_args, stream: Optional[int] = None) -> None:
@@ -381,12 +408,12 @@ def gemm(a, b, c=None, out=None, sfa=None, sfb=None, block_k: int = 32, stream: 
         dtype = dtype or (torch.bfloat16 if a.dtype == torch.bfloat16 else torch.float16)
         out = (torch.empty(shape, dtype=dtype, device=a.device) if stream is None else
                _allocated(stream, a.device, lambda: torch.empty(shape, dtype=dtype, device=a.device)))
+    if a.dtype == torch.int8:  # plans without a workspace
+        _run("sl_gemm", (_record(a), _record(b), _record(c), _record(out), _record(sfa), _record(sfb), _GEMM_TAIL.pack(block_k, 0, 0)),
+             _one_device(a, b, c, out, sfa, sfb), stream)
+        return out
     args = make_args(a, b, c, out, sfa, sfb, block_k)
     _check_devices(a, b, c, out, sfa, sfb, workspace)
-    if args.a.dtype == SL_I8:  # plans without a workspace
-        _check_one_device(a, b, c, out, sfa, sfb)
-        sl_gemm(args, stream)
-        return out
     if workspace is None:
         workspace = (workspace_for(args, out.device) if stream is None else
                      _allocated(stream, out.device, lambda: workspace_for(args, out.device)))
@@ -513,13 +540,29 @@ def _activation(name: str) -> int:
     return ACTIVATIONS[name]
 
 
-def _workspace(workspace, n: int, device, stream: Optional[int]):
-    """The caller's workspace, or ``n`` bytes of the call's stream (0: none)."""
-    if workspace is not None or n == 0:
-        return workspace
-    import torch
-    make = lambda: torch.empty(n, dtype=torch.uint8, device=device)
-    return make() if stream is None else _allocated(stream, device, make)
+def _run_with_workspace(name: str, operands, tail: int, workspace, often: bool, device, stream: Optional[int]) -> None:
+    """Entry point ``name`` on the operands' descriptors and ``tail``'s first
+    field.  Without the caller's workspace its bytes are asked for, unless most
+    plans need none (not ``often``) and the call goes through without."""
+    records = b"".join([_record(t) for t in operands])
+    index = _one_device(*operands, workspace)
+    if workspace is None:
+        record = records + _GATED_TAIL.pack(tail, 0, 0)
+        if not often:
+            status = _status(name, record, index, stream)
+            if status != -1:  # SL_ERR_NULL: no workspace, or an operand without data
+                return _check(status)
+        query = name + "_workspace_bytes"
+        if query not in _raw:
+            _raw[query] = lib()[query]
+            _raw[query].restype, _raw[query].argtypes = ctypes.c_int32, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_int64)]
+        n = ctypes.c_int64(0)
+        _check(_raw[query](record, ctypes.byref(n)))
+        import torch
+        make = lambda: torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
+        workspace = make() if stream is None else _allocated(stream, device, make)
+    given = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _run(name, (records, _GATED_TAIL.pack(tail, *given)), index, stream)
 
 
 def quantize_rows(x, out=None, stream: Optional[int] = None):
@@ -539,9 +582,8 @@ def quantize_rows(x, out=None, stream: Optional[int] = None):
         out = make() if stream is None else _allocated(stream, x.device, make)
     elif len(out) != 2:
         raise ValueError(f"out holds {len(out)} tensors, 2 are written")
-    args = sl_quantize_rows_args.from_buffer_copy(b"".join((_record(x), _record(out[0]), _record(out[1]))))
-    _check_one_device(x, *out)
-    sl_quantize_rows(args, stream)
+    records = (_record(x), _record(out[0]), _record(out[1]))
+    _run("sl_quantize_rows", records, _one_device(x, *out), stream)
     return out
 
 
@@ -561,8 +603,9 @@ def gated(x, w_gate, w_up, activation: str = "silu", sx=None, s_gate=None, s_up=
     import torch
     act = _activation(activation)
     if out is None:
-        batch = max((t.shape[0] for t in (x, w_gate, w_up) if t.dim() == 3), default=None)
-        shape = (x.shape[-2], w_gate.shape[-2]) if batch is None else (batch, x.shape[-2], w_gate.shape[-2])
+        shape = (x.shape[-2], w_gate.shape[-2])
+        if x.dim() == 3 or w_gate.dim() == 3 or w_up.dim() == 3:
+            shape = (max(t.shape[0] for t in (x, w_gate, w_up) if t.dim() == 3),) + shape
         dtype = dtype or (torch.float16 if x.dtype == torch.int8 else x.dtype)
         make = lambda: tuple(torch.empty(shape, dtype=dtype, device=x.device) for _ in range(3 if keep else 1))
         out = make() if stream is None else _allocated(stream, x.device, make)
@@ -570,12 +613,8 @@ def gated(x, w_gate, w_up, activation: str = "silu", sx=None, s_gate=None, s_up=
         out = tuple(out) if keep else (out,)
         if len(out) != (3 if keep else 1):
             raise ValueError(f"out holds {len(out)} tensors, 3 are written")
-    operands = (x, w_gate, w_up, sx, s_gate, s_up) + out
-    args = sl_gated_args.from_buffer_copy(b"".join([_record(t) for t in operands] + [_ABSENT] * (9 - len(operands)) +
-                                                   [_GATED_TAIL.pack(act, 0, 0)]))
-    _check_one_device(*operands, workspace)
-    set_workspace(args, _workspace(workspace, sl_gated_workspace_bytes(args) if workspace is None else 0, x.device, stream))
-    sl_gated(args, stream)
+    operands = (x, w_gate, w_up, sx, s_gate, s_up) + out + (() if keep else (None, None))
+    _run_with_workspace("sl_gated", operands, act, workspace, False, x.device, stream)
     return out if keep else out[0]
 
 
@@ -594,19 +633,15 @@ def gated_backward(dh, x, w_gate, w_up, gate, up, activation: str = "silu", need
     if not (need_dx or need_dw):
         raise ValueError("nothing to compute: neither dx nor the weights' gradients")
     if out is None:
-        # one buffer for both weights' gradients: they are then one product
-        make = lambda: (torch.empty(dh.shape[:-1] + (x.shape[-1],), dtype=x.dtype, device=x.device) if need_dx else None,
-                        torch.empty((2,) + tuple(w_gate.shape), dtype=x.dtype, device=x.device) if need_dw else None)
-        dx, dw = make() if stream is None else _allocated(stream, x.device, make)
-        out = (dx, None, None) if dw is None else (dx, dw[0], dw[1])
+        def make():
+            like = lambda t: torch.empty_like(t, memory_format=torch.contiguous_format)
+            dx = None if not need_dx else like(x) if x.dim() == dh.dim() else x.new_empty(dh.shape[:-1] + x.shape[-1:])
+            return (dx, like(w_gate), like(w_up)) if need_dw else (dx, None, None)
+        out = make() if stream is None else _allocated(stream, x.device, make)
     elif len(out) != 3 or (out[0] is not None) != need_dx or any((t is not None) != need_dw for t in out[1:]):
         raise ValueError("out holds dx, dw_gate and dw_up, None where they are not wanted")
     operands = (dh, x, w_gate, w_up, gate, up) + tuple(out)
-    args = sl_gated_backward_args.from_buffer_copy(b"".join([_record(t) for t in operands] + [_GATED_TAIL.pack(act, 0, 0)]))
-    _check_one_device(*operands, workspace)
-    set_workspace(args, _workspace(workspace, sl_gated_backward_workspace_bytes(args) if workspace is None else 0, x.device,
-                                   stream))
-    sl_gated_backward(args, stream)
+    _run_with_workspace("sl_gated_backward", operands, act, workspace, True, x.device, stream)
     return out
 
 

@@ -27,24 +27,58 @@ DensePlan dense_plan(bool gated, int64_t batch, int64_t M, int64_t N, int64_t K)
   const int64_t B = gated ? 2 * N : N;  // rows of B: a gated tile's columns of the result are half of its rows of B
   if (M <= 16) {
     const int32_t bn = gated || batch * ceil_div(N, 32) >= kCUs ? 32 : 16;
-    return {DT_SKINNY, 16, bn, kDenseSkinnyWaves * 64, kDenseSkinnyWaves * bn / 16 * 1024, 0};
+    const double rounds = (double)batch * (double)ceil_div(B, bn) / (2.0 * kCUs);  // two workgroups to a CU
+    return {DT_SKINNY, 16, bn, kDenseSkinnyWaves * 64, kDenseSkinnyWaves * bn / 16 * 1024, 0, std::ceil(rounds) * (3.0 + 0.1 * (double)ceil_div(K, 128))};
   }
   const double T = (double)ceil_div(K, 128);
   const int32_t bm = M <= 32 ? 32 : 64;
   const int32_t bn = batch * ceil_div(M, bm) * ceil_div(B, 64) >= kCUs ? 64 : 32;
   const int32_t stages = bm == 32 ? (bn == 32 ? 4 : 3) : (bn == 32 ? 3 : 2);
-  DensePlan best = {DT_STREAM, bm, bn, kDenseStreamWaves * 64, kDenseStreamWaves * stages * (bm + bn) * 128, stages};
-  if (M <= 64 || K == 0) return best;
+  DensePlan best = {DT_STREAM, bm, bn, kDenseStreamWaves * 64, kDenseStreamWaves * stages * (bm + bn) * 128, stages, 0.0};
   const double groups = (double)batch * (double)ceil_div(M, bm) * (double)ceil_div(B, bn);
-  double least = std::ceil(groups / kCUs) * (5.0 + T * (bn == 64 ? 0.2 : 0.13));
+  best.us = std::ceil(groups / kCUs) * (5.0 + T * (bn == 64 ? 0.2 : 0.13));
+  if (M <= 64 || K == 0) return best;
   auto tiles = [&](int64_t rows_a, int64_t rows_b) { return (double)batch * (double)ceil_div(M, rows_a) * (double)ceil_div(B, rows_b); };
   const double t0 = tiles(256, 256), t1 = tiles(256, 128), t2 = tiles(128, 128);
   const double costs[3] = {std::ceil(t0 / kCUs) * (10.2 + 1.3 * T), std::ceil(t1 / kCUs) * (7.0 + 0.77 * T),
                            t2 <= kCUs ? 4.4 + 0.51 * T : 2.4 + std::ceil(t2 / (2 * kCUs)) * (3.4 + 0.8 * T)};
-  constexpr DensePlan large[3] = {{DT_256x256, 256, 256, 256, 5 * 256 * 128, 0}, {DT_256x128, 256, 128, 256, 5 * 256 * 128, 0},
-                                  {DT_128x128, 128, 128, 256, 5 * 128 * 128, 0}};
-  for (int i = 0; i < 3; ++i)
-    if (costs[i] < least) least = costs[i], best = large[i];
+  const DensePlan large[3] = {{DT_256x256, 256, 256, 256, 5 * 256 * 128, 0, costs[0]},
+                              {DT_256x128, 256, 128, 256, 5 * 256 * 128, 0, costs[1]},
+                              {DT_128x128, 128, 128, 256, 5 * 128 * 128, 0, costs[2]}};
+  for (const DensePlan& t : large)
+    if (t.us < best.us) best = t;
+  return best;
+}
+
+// One tile for two products in one launch, by the same model: the workgroups'
+// times over the slots there are, or the longest one's.  (512 x 1024 x 512
+// and its pair: 16 us one after the other, 9 at once.)
+DensePlan dense_pair_plan(const DenseParams& p, const DenseParams& q) {
+  using host::ceil_div;
+  constexpr struct {
+    DensePlan plan;
+    double slots, start, k;
+  } tiles[6] = {{{DT_256x256, 256, 256, 256, 5 * 256 * 128, 0, 0.0}, kCUs, 10.2, 1.3},
+                {{DT_256x128, 256, 128, 256, 5 * 256 * 128, 0, 0.0}, kCUs, 7.0, 0.77},
+                {{DT_128x128, 128, 128, 256, 5 * 128 * 128, 0, 0.0}, 2 * kCUs, 4.4, 0.8},
+                {{DT_STREAM, 64, 64, 256, 4 * 2 * 128 * 128, 2, 0.0}, kCUs, 5.0, 0.2},
+                {{DT_STREAM, 64, 32, 256, 4 * 3 * 96 * 128, 3, 0.0}, kCUs, 5.0, 0.13},
+                {{DT_STREAM, 32, 32, 256, 4 * 4 * 64 * 128, 4, 0.0}, kCUs, 4.5, 0.1}};
+  DensePlan best = tiles[0].plan;
+  best.us = 1e300;
+  for (const auto& t : tiles) {
+    double all = 0.0, longest = 0.0, groups = 0.0;
+    for (const DenseParams* x : {&p, &q}) {
+      if (x->K == 0 && t.plan.tile != DT_STREAM) longest = 1e30;  // the others want a K-tile
+      const double n = (double)x->batch * (double)ceil_div(x->M, t.plan.bm) * (double)ceil_div(x->N, t.plan.bn);
+      const double one = t.start + t.k * (double)ceil_div(x->K, 128);
+      all += n * one / t.slots, groups += n, longest = std::max(longest, one);
+    }
+    // (alone on a CU a 128 x 128 tile takes two thirds of its time)
+    if (t.plan.tile == DT_128x128 && groups <= kCUs) longest = 4.4 + (longest - 4.4) * 0.64;
+    const double cost = std::max(all, longest);
+    if (cost < best.us) best = t.plan, best.us = cost;
+  }
   return best;
 }
 
@@ -480,6 +514,7 @@ struct BackwardPlan {
   sl::GatedPrepareParams prepare;  // copies: x's transpose, w_gate's, w_up's
   sl::GradParams dx, dw;
   sl::DensePlan dx_tile, dw_tile;
+  bool pair;                       // both in one launch
   int32_t kind;
   bool want_dx, want_dw, launch;
   bool dx_ring, dw_ring;           // on operands as they lie (launch_grad_ring)
@@ -594,7 +629,7 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
            v->rows * v->rs * 2 + 1024 < kLim && v->rs == x.rs;
     return ok;
   };
-  const sl::DensePlan large = {sl::DT_256x256, 256, 256, 256, 5 * 256 * 128, 0};
+  const sl::DensePlan large = {sl::DT_256x256, 256, 256, 256, 5 * 256 * 128, 0, 0.0};
   if (P.want_dx) {
     if (tokens) P.off_rows = take(n * rows * 2 * Fp);
     if ((s = product(&P.dx.d, &P.dx_tile, n, rows, K, tokens ? 2 * Fp : 0, rows * 2 * Fp, one_weight ? 0 : K * 2 * Fp, 0)) != SL_OK) return s;
@@ -634,6 +669,14 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
     if (v[DWG].cs == 1 && v[DWU].cs == 1) P.dw.d.flags |= sl::DF_ROWS;
   }
   if (!grid_fits(sl::gated_prepare_groups(&P.prepare), 1, 1, sl::kPrepareThreads)) return fail(SL_ERR_SHAPE, "the operands are too large");
+  if (P.want_dx && P.want_dw && !P.dx_ring && !P.dw_ring) {
+    const sl::DensePlan both = sl::dense_pair_plan(P.dx.d, P.dw.d);
+    sl::DenseParams x = P.dx.d, y = P.dw.d;
+    P.pair = both.us < P.dx_tile.us + P.dw_tile.us && place_tiles(&x, both, false) == SL_OK && place_tiles(&y, both, false) == SL_OK &&
+             grid_fits((int64_t)x.batch * x.tiles_m * x.tiles_n + (int64_t)y.batch * y.tiles_m * y.tiles_n, 1, 1, both.threads);
+    if (P.pair) P.dx.d = x, P.dw.d = y, P.dx_tile = P.dw_tile = both;
+    g_msg.clear();
+  }
   return SL_OK;
 }
 
@@ -682,6 +725,12 @@ sl_status sl_gated_backward(const sl_gated_backward_args* args, void* stream) {
     }
   }
   hipError_t e = sl::launch_gated_prepare(P.prepare, st);
+  if (e == hipSuccess && P.pair) {
+    const sl::DensePair both = {{dx, dw}, (uint32_t)((int64_t)dx.batch * dx.tiles_m * dx.tiles_n)};
+    e = sl::launch_gated_products(both, P.kind, P.dx_tile, st);
+    if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
+    return SL_OK;
+  }
   if (e == hipSuccess && P.want_dx) e = P.dx_ring ? sl::launch_grad_ring(P.dx, P.kind, false, st) : sl::launch_gated_products(dx, P.kind, P.dx_tile, st);
   if (e == hipSuccess && P.want_dw) e = P.dw_ring ? sl::launch_grad_ring(P.dw, P.kind, true, st) : sl::launch_gated_products(dw, P.kind, P.dw_tile, st);
   if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));

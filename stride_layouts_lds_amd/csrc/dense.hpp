@@ -131,6 +131,18 @@ struct RowLoader {
   }
 };
 
+// The product that a workgroup belongs to, its number among that one's
+// workgroups, and theirs.
+__device__ __forceinline__ const DenseParams& dense_product(const DenseParams& p, uint32_t& id, uint32_t& total) {
+  id = blockIdx.x, total = gridDim.x;
+  return p;
+}
+__device__ __forceinline__ const DenseParams& dense_product(const DensePair& p, uint32_t& id, uint32_t& total) {
+  const bool second = blockIdx.x >= p.first;
+  id = blockIdx.x - (second ? p.first : 0u), total = second ? gridDim.x - p.first : p.first;
+  return second ? p.p[1] : p.p[0];
+}
+
 // rows of the gated pair that a tile of BN rows of B holds of each matrix
 template <bool GATED, int BN>
 constexpr int kResultCols = GATED ? BN / 2 : BN;
@@ -302,8 +314,10 @@ __device__ __forceinline__ void dense_rows(const EPI& epi, const DenseParams& p,
 //   4 x 4  128 x 128, two to a CU
 // The gated pair's wave holds 8 FN rows of each matrix.
 // ---------------------------------------------------------------------------
-template <int EK, bool GATED, int FM, int FN, class EPI>
-__global__ __launch_bounds__(256, FM == 8 ? 1 : 2) void dense_ring_kernel(const DenseParams p) {
+template <int EK, bool GATED, int FM, int FN, class EPI, class PRODUCTS>
+__global__ __launch_bounds__(256, FM == 8 ? 1 : 2) void dense_ring_kernel(const PRODUCTS products_) {
+  uint32_t id, total;
+  const DenseParams& p = dense_product(products_, id, total);
   constexpr int ROWS_A = 32 * FM, ROWS_B = 32 * FN, SLOT = (FM > FN ? ROWS_A : ROWS_B) * kRowBytes;
   constexpr int BN = kResultCols<GATED, ROWS_B>;
   constexpr int NR = FM + FN;      // fragment reads of a slice
@@ -311,7 +325,7 @@ __global__ __launch_bounds__(256, FM == 8 ? 1 : 2) void dense_ring_kernel(const 
   __shared__ __attribute__((aligned(1024))) char smem[5 * SLOT];
   const int32_t lane = threadIdx.x & 63;
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const TileCoord tc = map_tile(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.batch);
+  const TileCoord tc = map_tile((int32_t)id, (int32_t)total, p.tiles_m, p.tiles_n, p.group_m, p.batch);
   const int64_t m0 = (int64_t)tc.tm * ROWS_A, n0 = (int64_t)tc.tn * BN;
   const int32_t rows_a = (int32_t)(p.M - m0 < ROWS_A ? p.M - m0 : ROWS_A);
   const int32_t cols = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
@@ -481,14 +495,15 @@ __device__ __forceinline__ void dense_join(const DenseParams& p, int64_t batch, 
 // 16 FN rows of B (gated: 8 FN of each matrix); wave w of eight takes the
 // K-tiles w, w + 8, ... straight from memory into registers, DEPTH requested
 // ahead.
-template <int EK, bool GATED, int FN, class EPI>
-__global__ __launch_bounds__(kDenseSkinnyWaves * 64) void dense_skinny_kernel(const DenseParams p) {
+template <int EK, bool GATED, int FN, class EPI, class PRODUCTS>
+__global__ __launch_bounds__(kDenseSkinnyWaves * 64) void dense_skinny_kernel(const PRODUCTS products_) {
+  uint32_t id, total;
+  const DenseParams& p = dense_product(products_, id, total);
   constexpr int W = kDenseSkinnyWaves, DEPTH = 4;
   constexpr int OUT = GATED ? FN / 2 : FN;
   __shared__ floatx4 part[W * FN * 64];
   const int32_t lane = threadIdx.x & 63;
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t id = blockIdx.x;
   const int64_t tn = id % p.tiles_n, tm = id / p.tiles_n % p.tiles_m, batch = id / p.tiles_n / p.tiles_m;
   const int64_t m0 = tm * 16, n0 = tn * (16 * OUT);
   const int32_t rows = (int32_t)(p.M - m0 < 16 ? p.M - m0 : 16);
@@ -548,8 +563,10 @@ __global__ __launch_bounds__(kDenseSkinnyWaves * 64) void dense_skinny_kernel(co
 // straight into its own part of LDS, STAGES deep; no barrier until the sums
 // meet.  Also for more rows, 16 FM to a workgroup, where 128 x 128 tiles would
 // be few.
-template <int EK, bool GATED, int FM, int FN, int STAGES, class EPI>
-__global__ __launch_bounds__(kDenseStreamWaves * 64, 1) void dense_stream_kernel(const DenseParams p) {
+template <int EK, bool GATED, int FM, int FN, int STAGES, class EPI, class PRODUCTS>
+__global__ __launch_bounds__(kDenseStreamWaves * 64, 1) void dense_stream_kernel(const PRODUCTS products_) {
+  uint32_t id, total;
+  const DenseParams& p = dense_product(products_, id, total);
   constexpr int W = kDenseStreamWaves;
   constexpr int OUT = GATED ? FN / 2 : FN;
   constexpr int ABYTES = 16 * FM * kRowBytes, STAGE = ABYTES + 16 * FN * kRowBytes;
@@ -557,7 +574,6 @@ __global__ __launch_bounds__(kDenseStreamWaves * 64, 1) void dense_stream_kernel
   static_assert(W * FM * FN * 1024 <= (int)sizeof smem, "the sums fit");
   const int32_t lane = threadIdx.x & 63;
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t id = blockIdx.x;
   const int64_t tn = id % p.tiles_n, tm = id / p.tiles_n % p.tiles_m, batch = id / p.tiles_n / p.tiles_m;
   const int64_t m0 = tm * (16 * FM), n0 = tn * (16 * OUT);
   const int32_t rows = (int32_t)(p.M - m0 < 16 * FM ? p.M - m0 : 16 * FM);
@@ -611,31 +627,32 @@ __global__ __launch_bounds__(kDenseStreamWaves * 64, 1) void dense_stream_kernel
   dense_join<EK, GATED, FM, FN, W, EPI>(p, batch, m0, n0, lane, wave, acc, (floatx4*)smem);
 }
 
-template <int EK, bool GATED, class EPI>
-hipError_t dense_launch(const DenseParams& p, const DensePlan& plan, hipStream_t s) {
-  const dim3 grid((uint32_t)((int64_t)p.batch * p.tiles_m * p.tiles_n)), block(plan.threads);
+__host__ inline int64_t dense_groups(const DenseParams& p) { return (int64_t)p.batch * p.tiles_m * p.tiles_n; }
+__host__ inline int64_t dense_groups(const DensePair& p) { return dense_groups(p.p[0]) + dense_groups(p.p[1]); }
+
+template <int EK, bool GATED, class EPI, class PRODUCTS>
+hipError_t dense_launch(const PRODUCTS& p, const DensePlan& plan, hipStream_t s) {
+  const dim3 grid((uint32_t)dense_groups(p)), block(plan.threads);
   auto stream = [&](auto fm, auto fn, auto stages) {
-    hipLaunchKernelGGL((dense_stream_kernel<EK, GATED, decltype(fm)::value, decltype(fn)::value, decltype(stages)::value, EPI>), grid, block, 0,
-                       s, p);
+    hipLaunchKernelGGL((dense_stream_kernel<EK, GATED, decltype(fm)::value, decltype(fn)::value, decltype(stages)::value, EPI, PRODUCTS>), grid,
+                       block, 0, s, p);
   };
   typedef std::integral_constant<int, 2> c2;
   typedef std::integral_constant<int, 3> c3;
   typedef std::integral_constant<int, 4> c4;
   switch (plan.tile) {
-    case DT_256x256: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 8, 8, EPI>), grid, block, 0, s, p); break;
-    case DT_256x128: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 8, 4, EPI>), grid, block, 0, s, p); break;
-    case DT_128x128: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 4, 4, EPI>), grid, block, 0, s, p); break;
+    case DT_256x256: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 8, 8, EPI, PRODUCTS>), grid, block, 0, s, p); break;
+    case DT_256x128: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 8, 4, EPI, PRODUCTS>), grid, block, 0, s, p); break;
+    case DT_128x128: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 4, 4, EPI, PRODUCTS>), grid, block, 0, s, p); break;
     case DT_STREAM:
       if (plan.bm == 32) plan.bn == 32 ? stream(c2{}, c2{}, c4{}) : stream(c2{}, c4{}, c3{});
       else plan.bn == 32 ? stream(c4{}, c2{}, c3{}) : stream(c4{}, c4{}, c2{});
       break;
     case DT_SKINNY:
-      if (plan.bn == 16) {
-        if constexpr (GATED) return hipErrorInvalidValue;
-        else hipLaunchKernelGGL((dense_skinny_kernel<EK, GATED, 1, EPI>), grid, block, 0, s, p);
-      } else {
-        hipLaunchKernelGGL((dense_skinny_kernel<EK, GATED, 2, EPI>), grid, block, 0, s, p);
-      }
+      if constexpr (std::is_same<PRODUCTS, DensePair>::value) return hipErrorInvalidValue;  // no plan of two products
+      else if (plan.bn == 32) hipLaunchKernelGGL((dense_skinny_kernel<EK, GATED, 2, EPI, PRODUCTS>), grid, block, 0, s, p);
+      else if constexpr (GATED) return hipErrorInvalidValue;
+      else hipLaunchKernelGGL((dense_skinny_kernel<EK, GATED, 1, EPI, PRODUCTS>), grid, block, 0, s, p);
       break;
     default: return hipErrorInvalidValue;
   }

@@ -346,9 +346,12 @@ hipError_t launch_grad_ring(const GradParams& g, int32_t kind, bool across, hipS
   return hipGetLastError();
 }
 
-hipError_t launch_gated_products(const DenseParams& p, int32_t kind, const DensePlan& plan, hipStream_t s) {
+template <class PRODUCTS>
+static hipError_t products_of(const PRODUCTS& p, int32_t kind, const DensePlan& plan, hipStream_t s) {
   if (kind == EK_F16) return dense_launch<EK_F16, false, Gradient<OT_F16>>(p, plan, s);
   return dense_launch<EK_BF16, false, Gradient<OT_BF16>>(p, plan, s);
 }
+hipError_t launch_gated_products(const DenseParams& p, int32_t kind, const DensePlan& plan, hipStream_t s) { return products_of(p, kind, plan, s); }
+hipError_t launch_gated_products(const DensePair& p, int32_t kind, const DensePlan& plan, hipStream_t s) { return products_of(p, kind, plan, s); }
 
 }  // namespace sl

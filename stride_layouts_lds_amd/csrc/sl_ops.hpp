@@ -190,6 +190,7 @@ struct DensePlan {
   int32_t bm, bn;       // rows of A and of B of a workgroup
   int32_t threads, lds;
   int32_t stages;       // LDS K-tiles of DT_STREAM
+  double us;            // what the model of dense_plan gives it
 };
 // `gated`: bn / 2 columns of the result to a workgroup
 DensePlan dense_plan(bool gated, int64_t batch, int64_t M, int64_t N, int64_t K);
@@ -232,8 +233,15 @@ hipError_t launch_gated_prepare(const GatedPrepareParams& p, hipStream_t stream)
 
 // The products of the backward pass: 16-bit D = A B^T as DenseParams states it,
 // D in kept[0]; with pairs (b_shift 1) matrix 2 i + s of the batch takes B's
-// matrix i and goes to matrix i of kept[s].
+// matrix i and goes to matrix i of kept[s].  One of them, or two in one launch:
+// the first `first` workgroups are p[0]'s.
+struct DensePair {
+  DenseParams p[2];
+  uint32_t first;
+};
+DensePlan dense_pair_plan(const DenseParams& p, const DenseParams& q);
 hipError_t launch_gated_products(const DenseParams& p, int32_t kind, const DensePlan& plan, hipStream_t stream);
+hipError_t launch_gated_products(const DensePair& p, int32_t kind, const DensePlan& plan, hipStream_t stream);
 
 // The same products with B's rows (and, across, A's) contracted over: B is
 // `parts` matrices (b[0], b[1]) of `rows` rows of N contiguous values one after

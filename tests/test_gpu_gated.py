@@ -622,7 +622,9 @@ def test_gated_backward(api, shape, dtype):
     one = api.gated_backward(*s, "silu", need_dw=False)
     two = api.gated_backward(*s, "silu", need_dx=False)
     assert one[1] is None and one[2] is None and two[0] is None
-    assert torch.equal(one[0], got[0]) and torch.equal(two[1], got[1]) and torch.equal(two[2], got[2])
+    # (a call for one of them may take another tile, which adds in another order)
+    check_backward("silu", one, *s)
+    check_backward("silu", two, *s)
 
 
 @pytest.mark.parametrize("kind", ACTS)
