@@ -603,6 +603,8 @@ def gated(x, w_gate, w_up, activation: str = "silu", sx=None, s_gate=None, s_up=
     import torch
     act = _activation(activation)
     if out is None:
+        if x.dim() not in (2, 3) or w_gate.dim() not in (2, 3) or w_up.dim() not in (2, 3):
+            raise ValueError("gated takes matrices or batches of matrices")
         shape = (x.shape[-2], w_gate.shape[-2])
         if x.dim() == 3 or w_gate.dim() == 3 or w_up.dim() == 3:
             shape = (max(t.shape[0] for t in (x, w_gate, w_up) if t.dim() == 3),) + shape

@@ -645,8 +645,10 @@ hipError_t dense_launch(const PRODUCTS& p, const DensePlan& plan, hipStream_t s)
     case DT_256x128: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 8, 4, EPI, PRODUCTS>), grid, block, 0, s, p); break;
     case DT_128x128: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 4, 4, EPI, PRODUCTS>), grid, block, 0, s, p); break;
     case DT_STREAM:
-      if (plan.bm == 32) plan.bn == 32 ? stream(c2{}, c2{}, c4{}) : stream(c2{}, c4{}, c3{});
-      else plan.bn == 32 ? stream(c4{}, c2{}, c3{}) : stream(c4{}, c4{}, c2{});
+      if (plan.bm == 64) plan.bn == 32 ? stream(c4{}, c2{}, c3{}) : stream(c4{}, c4{}, c2{});
+      else if (plan.bn == 32) stream(c2{}, c2{}, c4{});
+      else if constexpr (std::is_same<PRODUCTS, DensePair>::value) return hipErrorInvalidValue;  // no plan of two products
+      else stream(c2{}, c4{}, c3{});
       break;
     case DT_SKINNY:
       if constexpr (std::is_same<PRODUCTS, DensePair>::value) return hipErrorInvalidValue;  // no plan of two products

@@ -1,0 +1,394 @@
+"""sl_quantize_rows, the int8 form of sl_gemm, sl_gated and sl_gated_backward on
+the host (no GPU): every check of their arguments runs before any HIP call, so a
+refusal is seen here; what passes the checks is planned, not run."""
+
+import ctypes
+
+import pytest
+
+from test_ops_abi import BF16, D, F16, F32, F8, Q, QT, S, ST, WS, X, api, gemm_args, refused, rm  # noqa: F401
+
+I8 = 9
+SILU, RELU = 1, 4
+Z = [i << 36 for i in range(10, 20)]   # further addresses, 64 GiB apart
+
+
+def filled(api, args, tensors):  # noqa: F811
+    for name, _ in args._fields_:
+        if _ is not api.sl_tensor:
+            continue
+        if tensors.get(name) is not None:
+            setattr(args, name, api.desc(*tensors[name]))
+        else:
+            getattr(args, name).layout.rank = 2
+    return args
+
+
+# --------------------------------------------------------------- quantize_rows
+
+def rows_args(api, **t):  # noqa: F811
+    return filled(api, api.sl_quantize_rows_args(), t)
+
+
+GOOD_R = dict(x=rm(X, (256, 500), F16), q=rm(Q, (256, 512), I8), s=rm(S, (256, 1), F32))
+
+
+@pytest.mark.parametrize("change,what", [
+    (dict(x=rm(X, (256, 500), I8)), "SL_ERR_DTYPE"),
+    (dict(q=rm(Q, (256, 512), F8)), "SL_ERR_DTYPE"),
+    (dict(s=rm(S, (256, 1), F16)), "SL_ERR_DTYPE"),
+    (dict(x=rm(X, (500,), F16)), "SL_ERR_LAYOUT"),
+    (dict(x=rm(X, (256, 500), F16, (500, -1))), "SL_ERR_LAYOUT"),
+    (dict(x=rm(X, (256, -500), F16, (512, 1))), "SL_ERR_SHAPE"),
+    (dict(q=rm(Q, (256, 496), I8)), "SL_ERR_SHAPE"),                     # fewer columns than x
+    (dict(q=rm(Q, (256, 528), I8)), "SL_ERR_SHAPE"),                     # past the next multiple of 128
+    (dict(q=rm(Q, (255, 512), I8)), "SL_ERR_SHAPE"),
+    (dict(s=rm(S, (255, 1), F32)), "SL_ERR_SHAPE"),
+    (dict(s=rm(S, (256, 4), F32)), "SL_ERR_SHAPE"),
+    (dict(s=rm(S, (1, 256), F32)), "SL_ERR_SHAPE"),
+    (dict(x=rm(X, (2, 256, 500), F16)), "SL_ERR_SHAPE"),                 # q and s have one matrix
+    (dict(x=rm(X, (2, 256, 500), F16), q=rm(Q, (2, 256, 512), I8)), "SL_ERR_SHAPE"),
+    (dict(s=rm(S, (2, 256, 1), F32)), "SL_ERR_SHAPE"),
+    (dict(x=rm(0, (256, 500), F16)), "SL_ERR_NULL"),
+    (dict(q=rm(0, (256, 512), I8)), "SL_ERR_NULL"),
+    (dict(s=rm(0, (256, 1), F32)), "SL_ERR_NULL"),
+    (dict(x=rm(X + 1, (256, 500), F16)), "SL_ERR_ALIGN"),
+    (dict(s=rm(S + 2, (256, 1), F32)), "SL_ERR_ALIGN"),
+    (dict(q=rm(Q, (256, 512), I8, (1, 256))), "SL_ERR_LAYOUT"),          # columns not contiguous
+    (dict(q=rm(Q, (256, 512), I8, (520, 1))), "SL_ERR_LAYOUT"),          # rows off 16 bytes
+    (dict(q=rm(Q + 8, (256, 512), I8)), "SL_ERR_LAYOUT"),
+    (dict(q=rm(Q, (256, 512), I8, (0, 1))), "SL_ERR_LAYOUT"),            # every row the same memory
+    (dict(s=rm(S, (256, 1), F32, (0, 1))), "SL_ERR_LAYOUT"),
+    (dict(q=rm(X, (256, 512), I8)), "SL_ERR_ALIAS"),
+    (dict(s=rm(X + 64, (256, 1), F32)), "SL_ERR_ALIAS"),
+    (dict(s=rm(Q + 512 * 256 - 4, (256, 1), F32)), "SL_ERR_ALIAS"),
+    (dict(x=rm(X, ((1 << 31) - 128, 1), F16), q=rm(Q, ((1 << 31) - 128, 16), I8), s=rm(S, ((1 << 31) - 128, 1), F32)), "SL_ERR_SHAPE"),
+    (dict(x=rm(X, (1 << 16, 1 << 16, 1), F16), q=rm(Q, (1 << 16, 1 << 16, 16), I8), s=rm(S, (1 << 16, 1 << 16, 1), F32)), "SL_ERR_SHAPE"),
+])
+def test_quantize_rows_refuses(api, change, what):  # noqa: F811
+    refused(api, api.sl_quantize_rows, rows_args(api, **{**GOOD_R, **change}), what)
+
+
+def test_quantize_rows_null_and_empty(api):  # noqa: F811
+    assert api.lib().sl_quantize_rows(None, None) == -1
+    # nothing to write: no memory either
+    api.sl_quantize_rows(rows_args(api, x=rm(0, (0, 512), F16), q=rm(0, (0, 512), I8), s=rm(0, (0, 1), F32)), 0)
+    api.sl_quantize_rows(rows_args(api, x=rm(0, (0, 4, 512), F16), q=rm(0, (0, 4, 512), I8), s=rm(0, (0, 4, 1), F32)), 0)
+    # rows without columns still have scales
+    refused(api, api.sl_quantize_rows, rows_args(api, x=rm(0, (4, 0), F16), q=rm(0, (4, 0), I8), s=rm(0, (4, 1), F32)), "SL_ERR_NULL")
+
+
+# ------------------------------------------------------------ the int8 product
+
+GOOD_I = dict(a=rm(X, (300, 512), I8), b=rm(Q, (200, 512), I8), d=rm(D, (300, 200), BF16),
+              sfa=rm(S, (300, 1), F32), sfb=rm(ST, (200, 1), F32), block_k=0)
+
+
+@pytest.mark.parametrize("change,what", [
+    (dict(b=rm(Q, (200, 512), F8)), "SL_ERR_DTYPE"),
+    (dict(d=rm(D, (300, 200), I8)), "SL_ERR_DTYPE"),
+    (dict(c=rm(QT, (300, 200), F32)), "SL_ERR_DTYPE"),
+    (dict(sfa=rm(S, (300, 1), BF16)), "SL_ERR_DTYPE"),
+    (dict(sfb=rm(ST, (200, 1), 4)), "SL_ERR_DTYPE"),
+    (dict(b=rm(Q, (200, 528), I8)), "SL_ERR_SHAPE"),
+    (dict(d=rm(D, (200, 300), BF16)), "SL_ERR_SHAPE"),
+    (dict(c=rm(QT, (300, 1), BF16)), "SL_ERR_SHAPE"),
+    (dict(sfa=rm(S, (300, 4), F32)), "SL_ERR_SHAPE"),                      # the block-scaled form's
+    (dict(sfb=rm(ST, (300, 1), F32)), "SL_ERR_SHAPE"),
+    (dict(a=rm(X, (2, 300, 512), I8)), "SL_ERR_SHAPE"),                    # d has one batch
+    (dict(sfb=rm(ST, (2, 200, 1), F32)), "SL_ERR_SHAPE"),
+    (dict(a=rm(X, (300, 131072), I8), b=rm(Q, (200, 131072), I8)), "SL_ERR_SHAPE"),   # sums past 31 bits
+    (dict(a=rm(0, (300, 512), I8)), "SL_ERR_NULL"),
+    (dict(sfa=rm(0, (300, 1), F32)), "SL_ERR_NULL"),
+    (dict(d=rm(0, (300, 200), BF16)), "SL_ERR_NULL"),
+    (dict(d=rm(D + 1, (300, 200), BF16)), "SL_ERR_ALIGN"),
+    (dict(sfb=rm(ST + 2, (200, 1), F32)), "SL_ERR_ALIGN"),
+    (dict(a=rm(X, (300, 512), I8, (1, 300))), "SL_ERR_LAYOUT"),
+    (dict(a=rm(X, (300, 512), I8, (520, 1))), "SL_ERR_LAYOUT"),
+    (dict(b=rm(Q + 8, (200, 512), I8)), "SL_ERR_LAYOUT"),
+    (dict(a=rm(X, (300, 504), I8, (512, 1)), b=rm(Q, (200, 504), I8, (512, 1))), "SL_ERR_LAYOUT"),
+    (dict(d=rm(D, (300, 200), BF16, (0, 1))), "SL_ERR_LAYOUT"),
+    (dict(d=rm(X, (300, 200), BF16)), "SL_ERR_ALIAS"),
+    (dict(d=rm(ST, (300, 200), BF16)), "SL_ERR_ALIAS"),
+    (dict(c=rm(D + 2, (300, 200), BF16)), "SL_ERR_ALIAS"),
+    (dict(a=rm(X, (300, 512), I8, (1 << 24, 1))), "SL_ERR_SHAPE"),         # a tile spans 2^31 bytes
+    (dict(a=rm(X, (1 << 25, 1, 16), I8), b=rm(Q, (16, 16), I8), sfa=rm(S, (1, 1), F32), sfb=rm(ST, (16, 1), F32),
+          d=rm(D, (1 << 25, 1, 16), BF16)), "SL_ERR_SHAPE"),               # more tiles than a grid holds
+])
+def test_int8_product_refuses(api, change, what):  # noqa: F811
+    args = gemm_args(api, **{**GOOD_I, **change})
+    for call in (api.sl_gemm, api.sl_gemm_no_alloc):
+        refused(api, call, args, what)
+    with pytest.raises(api.SLError) as e:
+        api.describe_plan(args)
+    assert e.value.name == what
+
+
+def test_int8_product_plans(api):  # noqa: F811
+    p = api.sl_gemm_plan(gemm_args(api, **GOOD_I))
+    assert p["kernel"] == api.K_I8 and p["tile_k"] == 128 and (p["m"], p["n"], p["k"]) == (300, 200, 512)
+    assert p["split_k"] == 1 and p["workspace_bytes"] == 0
+    api.sl_gemm_plan(gemm_args(api, **{**GOOD_I, "c": GOOD_I["d"]}))
+    api.sl_gemm_plan(gemm_args(api, **{**GOOD_I, "c": rm(QT, (300, 200), BF16, (0, 1))}))
+    # the longest sums that are exact
+    api.sl_gemm_plan(gemm_args(api, **{**GOOD_I, "a": rm(X, (300, 131056), I8), "b": rm(Q, (200, 131056), I8)}))
+    # K = 0 reads neither operand; an empty D is planned and nothing runs
+    api.sl_gemm_plan(gemm_args(api, **{**GOOD_I, "a": rm(0, (300, 0), I8), "b": rm(0, (200, 0), I8)}))
+    api.sl_gemm(gemm_args(api, rm(0, (0, 512), I8), GOOD_I["b"], rm(0, (0, 200), BF16), rm(0, (0, 1), F32), GOOD_I["sfb"], block_k=0), 0)
+
+
+@pytest.mark.parametrize("M,N,out", [(1, 4096, BF16), (48, 8192, F16), (64, 100, F32), (300, 200, F16), (1290, 1500, BF16), (1000, 2500, F32),
+                                     (8192, 8192, BF16), (4000, 1000, F32)])
+def test_int8_product_is_described(api, M, N, out):  # noqa: F811
+    K = 2064
+    args = gemm_args(api, rm(X, (M, K), I8), rm(Q, (N, K), I8), rm(D, (M, N), out), rm(S, (M, 1), F32), rm(ST, (N, 1), F32),
+                     c=rm(QT, (M, N), out), block_k=0)
+    plan = api.sl_gemm_plan(args)
+    text = api.describe_plan(args)
+    stages = api.describe_stages(text)
+    assert text.startswith(f"# kernel {api.K_I8}:") and "v_mfma_i32_16x16x64_i8" in text
+    assert f"{plan['workgroups']} workgroups of {plan['threads']} threads" in text
+    assert f"{plan['lds_bytes']} LDS bytes" in text
+    assert plan["lds_bytes"] <= 160 * 1024
+    for name in ("A", "B", "D", "C"):
+        api.layout_op("parse", stages[name])
+    size = lambda l: int(api.layout_op("size", l))
+    assert size(stages["A"]) == M * K and size(stages["B"]) == N * K and size(stages["D"]) == M * N
+    # tiles cover the product
+    tm, tn = -(-M // plan["tile_m"]), -(-N // plan["tile_n"])
+    assert plan["workgroups"] == tm * tn
+
+
+# -------------------------------------------------------------- the gated block
+
+def gated_args(api, activation=SILU, ws=0, ws_bytes=0, **t):  # noqa: F811
+    a = filled(api, api.sl_gated_args(), t)
+    a.activation, a.workspace, a.workspace_bytes = activation, ws, ws_bytes
+    return a
+
+
+M, F, K = 72, 96, 64
+GOOD_G = dict(x=rm(X, (M, K), BF16), w_gate=rm(Z[0], (F, K), BF16), w_up=rm(Z[1], (F, K), BF16), h=rm(D, (M, F), BF16),
+              gate=rm(Z[2], (M, F), BF16), up=rm(Z[3], (M, F), BF16))
+GOOD_G8 = dict(x=rm(X, (M, K), I8), w_gate=rm(Z[0], (F, K), I8), w_up=rm(Z[1], (F, K), I8), h=rm(D, (M, F), F16),
+               sx=rm(S, (M, 1), F32), s_gate=rm(ST, (F, 1), F32), s_up=rm(Z[4], (F, 1), F32))
+
+
+@pytest.mark.parametrize("change,what", [
+    (dict(x=rm(X, (M, K), F32)), "SL_ERR_DTYPE"),
+    (dict(x=rm(X, (M, K), F16)), "SL_ERR_DTYPE"),
+    (dict(w_up=rm(Z[1], (F, K), F16)), "SL_ERR_DTYPE"),
+    (dict(h=rm(D, (M, F), F32)), "SL_ERR_DTYPE"),
+    (dict(gate=rm(Z[2], (M, F), F32)), "SL_ERR_DTYPE"),
+    (dict(sx=rm(S, (M, 1), F32)), "SL_ERR_DTYPE"),                         # scales of 16-bit values
+    (dict(activation=0), "SL_ERR_ARG"),
+    (dict(activation=5), "SL_ERR_ARG"),
+    (dict(x=rm(X, (K,), BF16)), "SL_ERR_LAYOUT"),
+    (dict(w_gate=rm(Z[0], (F, K), BF16, (-64, 1))), "SL_ERR_LAYOUT"),
+    (dict(w_gate=rm(Z[0], (F, K + 8), BF16)), "SL_ERR_SHAPE"),
+    (dict(w_up=rm(Z[1], (F + 1, K), BF16)), "SL_ERR_SHAPE"),
+    (dict(x=rm(X, (M + 1, K), BF16)), "SL_ERR_SHAPE"),
+    (dict(up=rm(Z[3], (F, M), BF16)), "SL_ERR_SHAPE"),
+    (dict(x=rm(X, (2, M, K), BF16)), "SL_ERR_SHAPE"),                      # h is one matrix
+    (dict(h=rm(D, (2, M, F), BF16)), "SL_ERR_SHAPE"),                      # and so are gate and up
+    (dict(h=rm(D, (2, M, F), BF16), gate=rm(Z[2], (2, M, F), BF16), up=rm(Z[3], (2, M, F), BF16), x=rm(X, (3, M, K), BF16)), "SL_ERR_SHAPE"),
+    (dict(x=rm(0, (M, K), BF16)), "SL_ERR_NULL"),
+    (dict(w_up=rm(0, (F, K), BF16)), "SL_ERR_NULL"),
+    (dict(h=rm(0, (M, F), BF16)), "SL_ERR_NULL"),
+    (dict(gate=rm(0, (M, F), BF16)), "SL_ERR_NULL"),                       # one of the two
+    (dict(x=rm(X + 1, (M, K), BF16)), "SL_ERR_ALIGN"),
+    (dict(h=rm(D, (M, F), BF16, (0, 1))), "SL_ERR_LAYOUT"),
+    (dict(up=rm(Z[3], (M, F), BF16, (F, 0))), "SL_ERR_LAYOUT"),
+    (dict(h=rm(X, (M, F), BF16)), "SL_ERR_ALIAS"),
+    (dict(gate=rm(D, (M, F), BF16)), "SL_ERR_ALIAS"),
+    (dict(gate=rm(D + 2 * F, (M, F), BF16, (2 * F - 8, 1)), h=rm(D, (M, F), BF16, (2 * F - 8, 1))), "SL_ERR_ALIAS"),
+    (dict(up=rm(Z[1] + 128, (M, F), BF16)), "SL_ERR_ALIAS"),
+    (dict(x=rm(X, (M, 1 << 30), BF16), w_gate=rm(Z[0], (F, 1 << 30), BF16), w_up=rm(Z[1], (F, 1 << 30), BF16)), "SL_ERR_SHAPE"),
+    (dict(w_gate=rm(Z[0], (F, 1 << 24), BF16, (1, F)), x=rm(X, (M, 1 << 24), BF16), w_up=rm(Z[1], (F, 1 << 24), BF16)), "SL_ERR_SHAPE"),
+    # copies are needed
+    (dict(x=rm(X, (M, K), BF16, (1, M))), "SL_ERR_NULL"),
+    (dict(x=rm(X, (M, K), BF16, (1, M)), ws=WS, ws_bytes=M * K * 2 - 1), "SL_ERR_SHAPE"),
+    (dict(x=rm(X, (M, K), BF16, (1, M)), ws=WS + 8, ws_bytes=1 << 30), "SL_ERR_ALIGN"),
+    (dict(x=rm(X, (M, K), BF16, (1, M)), ws=D + 16, ws_bytes=1 << 30), "SL_ERR_ALIAS"),
+    (dict(x=rm(X, (M, K), BF16, (1, M)), ws=X - (1 << 12), ws_bytes=1 << 30), "SL_ERR_ALIAS"),
+])
+def test_gated_refuses(api, change, what):  # noqa: F811
+    refused(api, api.sl_gated, gated_args(api, **{**GOOD_G, **change}), what)
+
+
+@pytest.mark.parametrize("change,what", [
+    (dict(w_gate=rm(Z[0], (F, K), F16)), "SL_ERR_DTYPE"),
+    (dict(h=rm(D, (M, F), I8)), "SL_ERR_DTYPE"),
+    (dict(sx=rm(S, (M, 1), F16)), "SL_ERR_DTYPE"),
+    (dict(s_up=None), "SL_ERR_DTYPE"),
+    (dict(s_gate=rm(ST, (M, 1), F32)), "SL_ERR_SHAPE"),
+    (dict(s_gate=rm(0, (F, 1), F32)), "SL_ERR_NULL"),
+    (dict(s_gate=rm(ST + 2, (F, 1), F32)), "SL_ERR_ALIGN"),
+    (dict(x=rm(X, (M, K), I8, (1, M))), "SL_ERR_LAYOUT"),
+    (dict(x=rm(X, (M, K), I8, (72, 1))), "SL_ERR_LAYOUT"),
+    (dict(x=rm(X, (M, 40), I8, (64, 1)), w_gate=rm(Z[0], (F, 40), I8, (64, 1)), w_up=rm(Z[1], (F, 40), I8, (64, 1))), "SL_ERR_LAYOUT"),
+    (dict(x=rm(X, (M, 131072), I8), w_gate=rm(Z[0], (F, 131072), I8), w_up=rm(Z[1], (F, 131072), I8)), "SL_ERR_SHAPE"),
+    (dict(w_up=rm(Z[1], (F, K), I8, (1 << 25, 1))), "SL_ERR_SHAPE"),       # a tile spans 2^31 bytes
+    (dict(h=rm(S, (M, F), F16)), "SL_ERR_ALIAS"),
+])
+def test_gated_int8_refuses(api, change, what):  # noqa: F811
+    refused(api, api.sl_gated, gated_args(api, **{**GOOD_G8, **change}), what)
+
+
+def workspace(api, call, args):  # noqa: F811
+    n = ctypes.c_int64(-1)
+    api._check(call(ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def test_gated_plans(api):  # noqa: F811
+    L = api.lib()
+    assert L.sl_gated(None, None) == -1 and L.sl_gated_workspace_bytes(None, None) == -1
+    need = lambda **t: workspace(api, L.sl_gated_workspace_bytes, gated_args(api, **{**GOOD_G, **t}))
+    assert need() == 0 and need(gate=None, up=None) == 0
+    assert workspace(api, L.sl_gated_workspace_bytes, gated_args(api, **GOOD_G8)) == 0
+    # weights that are two parts of one matrix, one after the other or in turn: read as they lie
+    assert need(w_gate=rm(Z[0], (F, K), BF16), w_up=rm(Z[0] + 2 * F * K, (F, K), BF16)) == 0
+    assert need(w_gate=rm(Z[0], (F, K), BF16, (2 * K, 1)), w_up=rm(Z[0] + 2 * K, (F, K), BF16, (2 * K, 1))) == 0
+    # results that are two parts of one matrix
+    assert need(gate=rm(Z[2], (M, F), BF16, (2 * F, 1)), up=rm(Z[2] + 2 * F, (M, F), BF16, (2 * F, 1))) == 0
+    assert need(gate=rm(Z[2], (M, F), BF16, (2 * F, 2)), up=rm(Z[2] + 2, (M, F), BF16, (2 * F, 2))) == 0
+    # an operand that doesn't lie in rows is copied, K to a multiple of 8: 256-byte pieces
+    assert need(x=rm(X, (M, K), BF16, (1, M))) == M * K * 2
+    assert need(x=rm(X + 2, (M, K), BF16)) == M * K * 2
+    odd = dict(x=rm(X, (M, K - 1), BF16), w_gate=rm(Z[0], (F, K - 1), BF16), w_up=rm(Z[1], (F, K - 1), BF16))
+    assert need(**odd) == (M + 2 * F) * K * 2
+    # a broadcast weight once, a batch's own for every matrix
+    three = dict(h=rm(D, (3, M, F), BF16), gate=None, up=None, x=rm(X, (3, M, K), BF16))
+    assert need(**three, w_gate=rm(Z[0], (3, F, K), BF16, (0, 1, F))) == F * K * 2
+    assert need(**three, w_gate=rm(Z[0], (F, K), BF16, (1, F))) == F * K * 2
+    assert need(**three, w_gate=rm(Z[0], (3, F, K), BF16, (F * K, 1, F))) == 3 * F * K * 2
+    # empty: nothing is read, nothing is wanted
+    for m, f in ((0, F), (M, 0)):
+        e = gated_args(api, x=rm(0, (m, K), BF16), w_gate=rm(0, (f, K), BF16), w_up=rm(0, (f, K), BF16), h=rm(0, (m, f), BF16))
+        assert workspace(api, L.sl_gated_workspace_bytes, e) == 0
+        api.sl_gated(e, 0)
+
+
+# ------------------------------------------------------------ its backward pass
+
+def backward_args(api, activation=SILU, ws=WS, ws_bytes=1 << 33, **t):  # noqa: F811
+    a = filled(api, api.sl_gated_backward_args(), t)
+    a.activation, a.workspace, a.workspace_bytes = activation, ws, ws_bytes
+    return a
+
+
+GOOD_B = dict(dh=rm(D, (M, F), F16), x=rm(X, (M, K), F16), w_gate=rm(Z[0], (F, K), F16), w_up=rm(Z[1], (F, K), F16),
+              gate=rm(Z[2], (M, F), F16), up=rm(Z[3], (M, F), F16), dx=rm(Z[4], (M, K), F16), dw_gate=rm(Z[5], (F, K), F16),
+              dw_up=rm(Z[6], (F, K), F16))
+
+
+@pytest.mark.parametrize("change,what", [
+    (dict(dh=rm(D, (M, F), F32)), "SL_ERR_DTYPE"),
+    (dict(x=rm(X, (M, K), BF16)), "SL_ERR_DTYPE"),
+    (dict(up=rm(Z[3], (M, F), F32)), "SL_ERR_DTYPE"),
+    (dict(dw_up=rm(Z[6], (F, K), F32)), "SL_ERR_DTYPE"),
+    (dict(dx=rm(Z[4], (M, K), F32)), "SL_ERR_DTYPE"),
+    (dict(activation=0), "SL_ERR_ARG"),
+    (dict(activation=RELU + 1), "SL_ERR_ARG"),
+    (dict(dh=rm(D, (F,), F16)), "SL_ERR_LAYOUT"),
+    (dict(x=rm(X, (M, K), F16, (-K, 1))), "SL_ERR_LAYOUT"),
+    (dict(x=rm(X, (M + 1, K), F16)), "SL_ERR_SHAPE"),
+    (dict(w_up=rm(Z[1], (F, K + 8), F16)), "SL_ERR_SHAPE"),
+    (dict(gate=rm(Z[2], (F, M), F16)), "SL_ERR_SHAPE"),
+    (dict(dx=rm(Z[4], (K, M), F16)), "SL_ERR_SHAPE"),
+    (dict(dw_gate=rm(Z[5], (K, F), F16)), "SL_ERR_SHAPE"),
+    (dict(dw_gate=rm(Z[5], (1, F, K), F16)), "SL_ERR_SHAPE"),              # the weight is a matrix
+    (dict(x=rm(X, (1, M, K), F16)), "SL_ERR_SHAPE"),
+    (dict(w_gate=rm(Z[0], (1, F, K), F16)), "SL_ERR_SHAPE"),
+    (dict(dh=rm(0, (M, F), F16)), "SL_ERR_NULL"),
+    (dict(x=rm(0, (M, K), F16)), "SL_ERR_NULL"),
+    (dict(gate=rm(0, (M, F), F16)), "SL_ERR_NULL"),
+    (dict(dw_up=rm(0, (F, K), F16)), "SL_ERR_NULL"),
+    (dict(dw_gate=rm(0, (F, K), F16)), "SL_ERR_NULL"),
+    (dict(dx=rm(Z[4] + 1, (M, K), F16)), "SL_ERR_ALIGN"),
+    (dict(dx=rm(Z[4], (M, K), F16, (0, 1))), "SL_ERR_LAYOUT"),
+    (dict(dw_up=rm(Z[6], (F, K), F16, (1, 1))), "SL_ERR_LAYOUT"),
+    (dict(dx=rm(X, (M, K), F16)), "SL_ERR_ALIAS"),                         # not in place
+    (dict(dx=rm(D, (M, K), F16)), "SL_ERR_ALIAS"),
+    (dict(dw_gate=rm(Z[0], (F, K), F16)), "SL_ERR_ALIAS"),
+    (dict(dw_up=rm(Z[5], (F, K), F16)), "SL_ERR_ALIAS"),
+    (dict(dw_up=rm(Z[5] + 2 * K - 2, (F, K), F16, (2 * K, 1)), dw_gate=rm(Z[5], (F, K), F16, (2 * K, 1))), "SL_ERR_ALIAS"),
+    (dict(ws=0), "SL_ERR_NULL"),
+    (dict(ws_bytes=1024), "SL_ERR_SHAPE"),
+    (dict(ws=WS + 4), "SL_ERR_ALIGN"),
+    (dict(ws=Z[4]), "SL_ERR_ALIAS"),
+    (dict(ws=Z[6] - 256), "SL_ERR_ALIAS"),
+    (dict(ws=X), "SL_ERR_ALIAS"),
+])
+def test_gated_backward_refuses(api, change, what):  # noqa: F811
+    refused(api, api.sl_gated_backward, backward_args(api, **{**GOOD_B, **change}), what)
+
+
+def test_gated_backward_plans(api):  # noqa: F811
+    L = api.lib()
+    assert L.sl_gated_backward(None, None) == -1 and L.sl_gated_backward_workspace_bytes(None, None) == -1
+    need = lambda **t: workspace(api, L.sl_gated_backward_workspace_bytes, backward_args(api, **{**GOOD_B, **t}))
+    both, dx, dw = need(), need(dw_gate=None, dw_up=None), need(dx=None)
+    assert 0 < dx < both and 0 < dw < both and both <= dx + dw
+    assert need(dx=None, dw_gate=None, dw_up=None) == 0
+    api.sl_gated_backward(backward_args(api, **{**GOOD_B, "dx": None, "dw_gate": None, "dw_up": None}, ws=0, ws_bytes=0), 0)
+    # the two gradients as parts of one matrix
+    need(dw_gate=rm(Z[5], (F, K), F16, (2 * K, 1)), dw_up=rm(Z[5] + 2 * K, (F, K), F16, (2 * K, 1)))
+    need(dw_gate=rm(Z[5], (F, K), F16), dw_up=rm(Z[5] + 2 * F * K, (F, K), F16))
+    # without tokens the weights' gradients are zeros: no copies
+    none = {n: rm(0, (0, s), F16) for n, s in (("dh", F), ("x", K), ("gate", F), ("up", F), ("dx", K))}
+    assert need(**none) == 0
+    # nothing wanted is there
+    api.sl_gated_backward(backward_args(api, **{**GOOD_B, **none, "w_gate": rm(0, (0, K), F16), "w_up": rm(0, (0, K), F16),
+                                                "dh": rm(0, (0, 0), F16), "gate": rm(0, (0, 0), F16), "up": rm(0, (0, 0), F16),
+                                                "dw_gate": rm(0, (0, K), F16), "dw_up": rm(0, (0, K), F16)}, ws=0, ws_bytes=0), 0)
+
+
+def test_large_backward_reads_the_operands_as_they_lie(api):  # noqa: F811
+    """Its workspace holds dg and du alone, both together a row of 2 x F to a
+    multiple of 64; weights or activations off 16 bytes are copied again."""
+    m, f, k = 4096, 4088, 4096
+    big = dict(dh=rm(D, (m, f), BF16), x=rm(X, (m, k), BF16), w_gate=rm(Z[0], (f, k), BF16), w_up=rm(Z[1], (f, k), BF16),
+               gate=rm(Z[2], (m, f), BF16), up=rm(Z[3], (m, f), BF16), dx=rm(Z[4], (m, k), BF16), dw_gate=rm(Z[5], (f, k), BF16),
+               dw_up=rm(Z[6], (f, k), BF16))
+    need = lambda **t: workspace(api, api.lib().sl_gated_backward_workspace_bytes, backward_args(api, **{**big, **t}))
+    fp = -(-f // 64) * 64
+    assert need() == need(dx=None) == need(dw_gate=None, dw_up=None) == m * 2 * fp * 2
+    assert need(w_up=rm(Z[1] + 2, (f, k), BF16)) == m * 2 * fp * 2 + k * 2 * fp * 2
+    assert need(w_up=rm(Z[1], (f, k), BF16, (k + 8, 1))) == m * 2 * fp * 2 + k * 2 * fp * 2      # one stride for both
+    assert need(x=rm(X, (m, k), BF16, (1, m))) == m * 2 * fp * 2 + 2 * fp * m * 2 + k * m * 2
+
+
+# --------------------------------------------------------------------- Python
+
+def test_python_refuses(api):  # noqa: F811
+    import torch
+    h, w, q, s = torch.zeros(64, 128).half(), torch.zeros(32, 128).half(), torch.zeros(64, 128, dtype=torch.int8), torch.ones(64, 1)
+    kept = torch.zeros(64, 32).half()
+    # host tensors: a kernel that reads them faults the GPU
+    for call in (lambda **kw: api.quantize_rows(h, **kw), lambda **kw: api.gemm(q, q, sfa=s, sfb=s, **kw),
+                 lambda **kw: api.gated(h, w, w, **kw), lambda **kw: api.gated(h, w, w, keep=True, **kw),
+                 lambda **kw: api.gated(q, q, q, sx=s, s_gate=s, s_up=s, **kw),
+                 lambda **kw: api.gated_backward(kept, h, w, w, kept, kept, **kw)):
+        with pytest.raises(ValueError, match="GPU tensors"):
+            call()
+    with pytest.raises(ValueError, match="matrix"):
+        api.quantize_rows(h[0])
+    with pytest.raises(ValueError, match="2 are written"):
+        api.quantize_rows(h, out=(q,))
+    with pytest.raises(ValueError, match="activation"):
+        api.gated(h, w, w, activation="swish")
+    with pytest.raises(ValueError, match="activation"):
+        api.gated_backward(kept, h, w, w, kept, kept, activation=None)
+    with pytest.raises(ValueError, match="3 are written"):
+        api.gated(h, w, w, keep=True, out=(kept, kept))
+    with pytest.raises(ValueError, match="matri"):
+        api.gated(h[0], w, w)
+    with pytest.raises(ValueError, match="nothing to compute"):
+        api.gated_backward(kept, h, w, w, kept, kept, need_dx=False, need_dw=False)
+    for out in ((h, w), (None, w, w), (h, None, w), (h, w, None)):
+        with pytest.raises(ValueError, match="out holds"):
+            api.gated_backward(kept, h, w, w, kept, kept, out=out)
+    with pytest.raises(TypeError):
+        api.quantize_rows(torch.zeros(4, 128, dtype=torch.float64))

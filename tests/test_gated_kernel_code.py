@@ -1,0 +1,58 @@
+"""The compiled kernels of the int8 product and of the gated block and its
+backward pass, under the checks that test_kernel_code.py makes of the GEMM's
+ring kernels (MFMAs issued as inline assembly on accumulators in AGPRs,
+barriers that the LDS reads before them have ended at) and test_ops_kernel_code.py
+of kernels whose waves each wait for their own copies by counting."""
+
+import pytest
+
+import test_kernel_code as K
+import test_ops_kernel_code as O
+from test_kernel_code import code_objects  # noqa: F401
+
+RING = "_ZN2sl12_GLOBAL__N_117dense_ring_kernelILi{ek}ELb{gated}ELi{fm}ELi{fn}ENS0_{epi}ENS_{params}EEEvT4_"
+EPILOGUE = {"product": "9ScaledSum", "gated": "4GateILi{ek}EE", "backward": "8GradientILi{ek}EE"}
+TYPES = {0: "fp16", 1: "bf16", 2: "int8"}
+
+# symbol, MFMAs of one K-loop iteration, MFMAs after the loop
+NAMES = {}
+for what, eks, params in (("product", (2,), "11DenseParams"), ("gated", (0, 1, 2), "11DenseParams"),
+                          ("backward", (0, 1), "11DenseParams"), ("backward", (0, 1), "9DensePair")):
+    for ek in eks:
+        for fm, fn, loop, after in ((8, 8, 128, 32), (8, 4, 64, 16), (4, 4, 32, 8)):
+            name = f"{what}{'_pair' if params == '9DensePair' else ''}_{TYPES[ek]}_{fm}{fn}"
+            NAMES[name] = (RING.format(ek=ek, gated=int(what == "gated"), fm=fm, fn=fn, epi=EPILOGUE[what].format(ek=ek),
+                                       params=params), loop, after)
+NAMES.update({f"across_{TYPES[ek]}_{a}": (f"_ZN2sl12_GLOBAL__N_116grad_ring_kernelILi{ek}ELb{a}EEEvNS_10GradParamsE", 128, 64)
+              for ek in (0, 1) for a in (0, 1)})
+K.KERNELS.update(NAMES)
+
+
+@pytest.mark.parametrize("name", sorted(NAMES))
+def test_accumulator_discipline(code_objects, name):  # noqa: F811
+    K.test_ring_kernel_accumulator_discipline(code_objects, name)
+
+
+@pytest.mark.parametrize("name", sorted(NAMES))
+def test_barriers_follow_lds_waits(code_objects, name):  # noqa: F811
+    K.test_ring_kernel_barriers_follow_lds_waits(code_objects, name)
+
+
+# waves that stream K-tiles of their own: (symbol, stages, copies of a K-tile, K-tiles in flight at a wait)
+STREAM = "_ZN2sl12_GLOBAL__N_119dense_stream_kernelILi{ek}ELb{gated}ELi{fm}ELi{fn}ELi{stages}ENS0_{epi}ENS_{params}EEEvT5_"
+COUNTED = {}
+for what, eks, params in (("product", (2,), "11DenseParams"), ("gated", (0, 1, 2), "11DenseParams"),
+                          ("backward", (0, 1), "11DenseParams"), ("backward", (0, 1), "9DensePair")):
+    for ek in eks:
+        for fm, fn, stages in ((2, 2, 4), (2, 4, 3), (4, 2, 3), (4, 4, 2)):
+            if params == "9DensePair" and (fm, fn) == (2, 4):
+                continue
+            COUNTED[f"{what}{'_pair' if params == '9DensePair' else ''}_stream_{TYPES[ek]}_{fm}{fn}"] = (
+                STREAM.format(ek=ek, gated=int(what == "gated"), fm=fm, fn=fn, stages=stages,
+                              epi=EPILOGUE[what].format(ek=ek), params=params), stages, 2 * (fm + fn), stages - 1)
+O.COUNTED.update(COUNTED)
+
+
+@pytest.mark.parametrize("name", sorted(COUNTED))
+def test_counted_waits(code_objects, name):  # noqa: F811
+    O.test_counted_waits(code_objects, name)

@@ -895,3 +895,163 @@ def test_calls_do_not_vary(api):
     for _ in range(3):
         for a, b in zip(api.gated(*s[1:4], keep=True) + tuple(api.gated_backward(*s)), first):
             assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
+# large products: operands read as they lie, and the tiles that only they take
+# ---------------------------------------------------------------------------
+
+def backward_workspace(api, s, got):
+    args = api.sl_gated_backward_args()
+    for name, t in zip(("dh", "x", "w_gate", "w_up", "gate", "up", "dx", "dw_gate", "dw_up"), tuple(s) + tuple(got)):
+        if t is not None:
+            setattr(args, name, api.tensor_desc(t))
+        else:
+            getattr(args, name).layout.rank = 2
+    args.activation = 1
+    return api.sl_gated_backward_workspace_bytes(args)
+
+
+def as_they_lie(M, F, n=1):
+    """Bytes of dg and du side by side: the workspace of a call that copies nothing."""
+    return -(-n * M * 2 * (-(-F // 64) * 64) * 2 // 256) * 256
+
+
+# x's gradient on a large tile: F and the output's sides end inside tiles
+@pytest.mark.parametrize("shape", [(4096, 200, 2304), (3900, 264, 2344), (4090, 65, 2312), (4000, 323, 4096)])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_large_input_gradient(api, shape, dtype):
+    M, F, K = shape
+    s = state(1, shape, dtype, "silu")
+    got = api.gated_backward(*s, need_dw=False)
+    assert backward_workspace(api, s, got) == as_they_lie(M, F)
+    check_backward("silu", got, *s)
+    # the same values in rows further apart, and a result in such rows
+    wide = [strided(v, "wide") for v in s]
+    out = strided(got[0].clone().zero_(), "wide")
+    api.gated_backward(*wide, need_dw=False, out=(out, None, None))
+    assert backward_workspace(api, wide, (out, None, None)) == as_they_lie(M, F)
+    assert (out == got[0]).all()
+    # weights that cannot be read as they lie: the other way, whose sums run in another order
+    off = [strided(v, "padded") if i in (2, 3) else v for i, v in enumerate(s)]
+    assert backward_workspace(api, off, got) > as_they_lie(M, F)
+    check_backward("silu", api.gated_backward(*off, need_dw=False), *s)
+
+
+# the weights' gradients on a large tile: tokens that end inside a K-tile
+@pytest.mark.parametrize("shape", [(384, 2200, 2048), (330, 2304, 2056), (1, 2208, 2048), (67, 4090, 2296)])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_large_weight_gradients(api, shape, dtype):
+    import torch
+    M, F, K = shape
+    s = state(1, shape, dtype, "gelu")
+    got = api.gated_backward(*s, "gelu", need_dx=False)
+    check_backward("gelu", got, *s)
+    lies = backward_workspace(api, s, got) == as_they_lie(M, F)
+    assert lies == (M > 256)  # few tokens take smaller tiles
+    both = torch.zeros((F, 2, K), dtype=s[1].dtype, device="cuda")
+    wide = [strided(v, "wide") for v in s]
+    api.gated_backward(*wide, "gelu", need_dx=False, out=(None, both[:, 0], both[:, 1]))
+    assert (both[:, 0] == got[1]).all() and (both[:, 1] == got[2]).all()
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_large_backward_of_a_batch(api, shared):
+    """Experts, each with tokens and weights of its own, and sequences that share them."""
+    M, F, K, n = 1030, 1024, 2040, 4
+    s = state(1, (M, F, K), "bfloat16", "silu", (n,), shared=shared)
+    check_backward("silu", api.gated_backward(*s), *s)
+    one = api.gated_backward(*s, need_dw=False)
+    two = api.gated_backward(*s, need_dx=False)
+    assert backward_workspace(api, s, one) == as_they_lie(M, F, n)
+    assert (backward_workspace(api, s, two) == as_they_lie(M, F, n)) == (not shared)
+    check_backward("silu", one, *s)
+    check_backward("silu", two, *s)
+
+
+def test_large_backward_integers_bit_for_bit(api):
+    """relu with small integers: dg, du and every sum are exact, on whichever way."""
+    import torch
+    for M, F, K in ((4096, 330, 2304), (330, 2312, 2048), (2300, 2100, 2056)):
+        x, w = integers(1, -2, 2, M, K).bfloat16(), integers(2, -2, 2, 2, F, K).bfloat16()
+        g, u, dh = integers(3, -3, 3, M, F).bfloat16(), integers(4, -3, 3, M, F).bfloat16(), integers(5, -2, 2, M, F).bfloat16()
+        dg, du = (dh * u * (g > 0)).double(), (dh * g.clamp_min(0)).double()
+        for wg, wu, v in ((w[0], w[1], x), (strided(w[0], "padded"), strided(w[1], "padded"), strided(x, "cols"))):
+            dx, dwg, dwu = api.gated_backward(dh, v, wg, wu, g, u, "relu")
+            assert torch.equal(dx, (dg @ w[0].double() + du @ w[1].double()).float().bfloat16())
+            assert torch.equal(dwg, (dg.t() @ x.double()).float().bfloat16()) and torch.equal(dwu, (du.t() @ x.double()).float().bfloat16())
+
+
+def test_large_backward_infinities_stay_in_their_rows(api):
+    """Rows and columns past an operand's end are not read as its values: what is
+    next to a view in memory is NaN throughout."""
+    import torch
+    M, F, K = 4001, 202, 2304
+
+    def among_nans(v):
+        store = torch.full((v.shape[0] + 200, v.shape[1] + 64), float("nan"), dtype=v.dtype, device="cuda")
+        view = store[100:100 + v.shape[0], 32:32 + v.shape[1]]
+        view.copy_(v)
+        return view
+    s = state(1, (M, F, K), "bfloat16", "silu")
+    got = api.gated_backward(*(among_nans(v) for v in s))
+    check_backward("silu", got, *s)
+    s = state(2, (330, 2304, 2056), "float16", "silu")
+    got = api.gated_backward(*(among_nans(v) for v in s))
+    check_backward("silu", got, *s)
+
+
+# the 256 x 128 tile and tiles of two products in one launch, next to each alone
+@pytest.mark.parametrize("shape", [(512, 1024, 512), (64, 360, 256), (700, 130, 2500), (1000, 1000, 1000), (2050, 1030, 1030), (33, 40, 2000)])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_gated_backward_tiles(api, shape, dtype):
+    s = state(1, shape, dtype, "gelu_tanh")
+    check_backward("gelu_tanh", api.gated_backward(*s, "gelu_tanh"), *s)
+    check_backward("gelu_tanh", api.gated_backward(*s, "gelu_tanh", need_dx=False), *s)
+    check_backward("gelu_tanh", api.gated_backward(*s, "gelu_tanh", need_dw=False), *s)
+
+
+@pytest.mark.parametrize("shape", [(1000, 2500, 256), (1000, 2500, 4100), (256, 4096, 1000), (2048, 2048, 1032)])
+def test_middle_tiles(api, shape):
+    x, wg, wu = block(1, shape, "bfloat16")
+    check_gated("silu", api.gated(x, wg, wu, keep=True), x, wg, wu)
+    M, N, K = shape
+    K = -(-K // 16) * 16
+    check_int8(api, codes(1, M, K), codes(2, N, K), scales(3, M), scales(4, N), c=normal(5, M, N).bfloat16())
+
+
+def test_two_streams_at_once(api):
+    """Calls in flight on two streams, each with its own allocations, give what they give alone."""
+    import torch
+    s, r = state(1, (300, 520, 264), "bfloat16", "silu"), state(2, (257, 1100, 520), "bfloat16", "silu")
+
+    def steps(v):
+        q, sc = api.quantize_rows(v[1])
+        return api.gated(*v[1:4], keep=True) + tuple(api.gated_backward(*v)) + (api.gemm(q, q, sfa=sc, sfb=sc),)
+    want = steps(s), steps(r)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        with torch.cuda.stream(one):
+            a = steps(s)
+        with torch.cuda.stream(two):
+            b = steps(r)
+        got.append((a, b))
+    torch.cuda.synchronize()
+    for a, b in got:
+        for x, y in zip(a + b, want[0] + want[1]):
+            assert torch.equal(x, y)
+
+
+def test_the_same_operand_twice(api):
+    """One tensor in several places that are only read."""
+    import torch
+    x = normal(1, 130, 136).bfloat16()
+    w = (normal(2, 200, 136) * 0.1).bfloat16()
+    check_gated("silu", api.gated(x, w, w, keep=True), x, w, w)
+    check_gated("gelu", api.gated(w, w, w, "gelu"), w, w, w)
+    g = matmul(x.double(), w.double()).bfloat16()
+    check_backward("silu", api.gated_backward(g, x, w, w, g, g), g, x, w, w, g, g)
+    q, s = api.quantize_rows(w)
+    check_int8(api, q, q, s, s)
