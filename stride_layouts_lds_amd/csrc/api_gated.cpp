@@ -13,15 +13,32 @@ namespace sl {
 // over the CUs times (start and end of a workgroup + K-tiles of 128 bytes x one's
 // time), in us, fitted to calls with each tile forced.  Some of them, gated bf16
 // (M x F, K 256 / 1024 / 4096; 256 x 256, 256 x 128, 128 x 128, streamed):
-//   256 x 1024   13 25 73     9 15 42     6 10 26     5  7  13
-//   512 x 1024   13 25 73     9 15 43     6 10 33     6  8  18
+//   256 x 1024   14 26 73     9 16 42     6 10 26     5  7  13
+//   512 x 1024   14 26 73     9 16 43     6 10 33     6  8  18
 //   1000 x 2000  14 26 74     9 16 43     7 11 37     22 36 101
 //   1000 x 2500  19 31 78     12 18 45    9 17 47     27 43 130
 //   2048 x 2048  15 27 75     10 20 56    9 19 58     42 55 130
 //   4096 x 2048  17 32 96     19 39 112   16 35 113   83 108 259
 //   4096 x 8192  59 126 372   68 145 432  53 129 446  324 458 1586
-// int8, 4096 x 4096: 19 27 58, 21 33 70, 17 27 66, 86 94 163.  Up to 64 rows of A go
-// streamed whatever it says (64 x 8192 x 4096 is read at 4.4 TB/s).
+// int8 (256 x 256, 256 x 192, 128 x 128): 4000 x 3000 x 256 / 2064 / 8192 16 14 13, 35 33 39,
+// 83 79 93; 3000 x 3000 x 2048 31 26 29; 4096 x 6144 x 4096 100 89 96; 8192 x 8192 x 2048
+// 133 155 141.  Up to 64 rows of A go streamed whatever it says (64 x 8192 x 4096 is read at
+// 4.4 TB/s).
+//
+// A 128 x 128 tile alone on its CU waits for its copies where many K-tiles meet many
+// others': the deep ring has two K-tiles more on their way (gated bf16 512 x 1024 x 4096 33 ->
+// 27, 1000 x 1900 x 4096 37 -> 32, x 2048 23 -> 21; int8 2048 x 1024 x 8192 34 -> 28), and
+// takes longer to fill where there are few (256 x 1024 x 2048 14.9 -> 15.7, 512 x 1024 x 1024
+// 10.0 -> 10.4).
+static DensePlan ring_plan(int32_t tile, int32_t bm, int32_t bn, int32_t slots) {
+  return {tile, bm, bn, 256, slots * std::max(bm, bn) * 128, slots, 0.0};
+}
+// 256 x 256 tiles of a product (rows of B: N)
+static double dense_large_us(int64_t batch, int64_t M, int64_t N, int64_t K) {
+  using host::ceil_div;
+  const double tiles = (double)batch * (double)ceil_div(M, 256) * (double)ceil_div(N, 256);
+  return std::ceil(tiles / kCUs) * (10.2 + 1.3 * (double)ceil_div(K, 128));
+}
 DensePlan dense_plan(bool gated, int64_t batch, int64_t M, int64_t N, int64_t K) {
   using host::ceil_div;
   const int64_t B = gated ? 2 * N : N;  // rows of B: a gated tile's columns of the result are half of its rows of B
@@ -39,12 +56,14 @@ DensePlan dense_plan(bool gated, int64_t batch, int64_t M, int64_t N, int64_t K)
   best.us = std::ceil(groups / kCUs) * (5.0 + T * (bn == 64 ? 0.2 : 0.13));
   if (M <= 64 || K == 0) return best;
   auto tiles = [&](int64_t rows_a, int64_t rows_b) { return (double)batch * (double)ceil_div(M, rows_a) * (double)ceil_div(B, rows_b); };
-  const double t0 = tiles(256, 256), t1 = tiles(256, 128), t2 = tiles(128, 128);
-  const double costs[3] = {std::ceil(t0 / kCUs) * (10.2 + 1.3 * T), std::ceil(t1 / kCUs) * (7.0 + 0.77 * T),
-                           t2 <= kCUs ? 4.4 + 0.51 * T : 2.4 + std::ceil(t2 / (2 * kCUs)) * (3.4 + 0.8 * T)};
-  const DensePlan large[3] = {{DT_256x256, 256, 256, 256, 5 * 256 * 128, 0, costs[0]},
-                              {DT_256x128, 256, 128, 256, 5 * 256 * 128, 0, costs[1]},
-                              {DT_128x128, 128, 128, 256, 5 * 128 * 128, 0, costs[2]}};
+  const double t2 = tiles(128, 128);
+  const bool deep = t2 <= kCUs && t2 * T >= 3500.0;
+  DensePlan large[4] = {ring_plan(DT_256x256, 256, 256, kRing), ring_plan(DT_256x192, 256, 192, kRing),
+                        ring_plan(DT_256x128, 256, 128, kRing), ring_plan(DT_128x128, 128, 128, deep ? kDeepRing : kRing)};
+  large[0].us = dense_large_us(batch, M, B, K);
+  large[1].us = gated ? best.us : std::ceil(tiles(256, 192) / kCUs) * (8.6 + 1.1 * T);
+  large[2].us = std::ceil(tiles(256, 128) / kCUs) * (7.0 + 0.77 * T);
+  large[3].us = deep ? 4.8 + 0.4 * T : t2 <= kCUs ? 4.4 + 0.51 * T : 2.4 + std::ceil(t2 / (2 * kCUs)) * (3.4 + 0.8 * T);
   for (const DensePlan& t : large)
     if (t.us < best.us) best = t;
   return best;
@@ -55,12 +74,12 @@ DensePlan dense_plan(bool gated, int64_t batch, int64_t M, int64_t N, int64_t K)
 // and its pair: 16 us one after the other, 9 at once.)
 DensePlan dense_pair_plan(const DenseParams& p, const DenseParams& q) {
   using host::ceil_div;
-  constexpr struct {
+  const struct {
     DensePlan plan;
     double slots, start, k;
-  } tiles[6] = {{{DT_256x256, 256, 256, 256, 5 * 256 * 128, 0, 0.0}, kCUs, 10.2, 1.3},
-                {{DT_256x128, 256, 128, 256, 5 * 256 * 128, 0, 0.0}, kCUs, 7.0, 0.77},
-                {{DT_128x128, 128, 128, 256, 5 * 128 * 128, 0, 0.0}, 2 * kCUs, 4.4, 0.8},
+  } tiles[6] = {{ring_plan(DT_256x256, 256, 256, kRing), kCUs, 10.2, 1.3},
+                {ring_plan(DT_256x128, 256, 128, kRing), kCUs, 7.0, 0.77},
+                {ring_plan(DT_128x128, 128, 128, kRing), 2 * kCUs, 4.4, 0.8},
                 {{DT_STREAM, 64, 64, 256, 4 * 2 * 128 * 128, 2, 0.0}, kCUs, 5.0, 0.2},
                 {{DT_STREAM, 64, 32, 256, 4 * 3 * 96 * 128, 3, 0.0}, kCUs, 5.0, 0.13},
                 {{DT_STREAM, 32, 32, 256, 4 * 4 * 64 * 128, 4, 0.0}, kCUs, 4.5, 0.1}};
@@ -621,19 +640,23 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
     if (quad_rows(v, count)) p->flags |= sl::DF_KEPT_VEC << i;
   };
   P.kind = dt == SL_F16 ? sl::EK_F16 : sl::EK_BF16;
-  // a large product whose operands' rows lie on 16-byte boundaries reads them as they are
-  auto ring = [&](const sl::DensePlan& tile, const View& x, const View* y) {
-    bool ok = tokens && tile.tile == sl::DT_256x256;
+  // A large product whose operands' rows lie on 16-byte boundaries reads them as they are,
+  // unless the copies (bytes read and written, at 4 TB/s) cost less than a better tile
+  // saves.  (us as they lie and with copies: 4000 x 500 x 3000's dx 43 and 39, 4096 x 4096 x
+  // 2048's two 281 and 248, 8 of 1024 x 1000 x 1024's dw 56 and 57, 4000 x 2000 x 3000's two 194
+  // and 207, 4096 x 8192 x 4096's two 871 and 925.)
+  const sl::DensePlan large = sl::ring_plan(sl::DT_256x256, 256, 256, sl::kRing);
+  auto ring = [&](const sl::DenseParams& p, const sl::DensePlan& tile, double copies, const View& x, const View* y) {
+    bool ok = tokens && sl::dense_large_us(p.batch, p.M, p.N, p.K) <= tile.us + copies / 4e6;
     for (const View* v : {&x, y ? y : &x})
       ok = ok && v->cs == 1 && v->cols % 8 == 0 && v->rs % 8 == 0 && (uintptr_t)v->t->data % 16 == 0 && bstride(*v) % 8 == 0 &&
            v->rows * v->rs * 2 + 1024 < kLim && v->rs == x.rs;
     return ok;
   };
-  const sl::DensePlan large = {sl::DT_256x256, 256, 256, 256, 5 * 256 * 128, 0, 0.0};
   if (P.want_dx) {
     if (tokens) P.off_rows = take(n * rows * 2 * Fp);
     if ((s = product(&P.dx.d, &P.dx_tile, n, rows, K, tokens ? 2 * Fp : 0, rows * 2 * Fp, one_weight ? 0 : K * 2 * Fp, 0)) != SL_OK) return s;
-    P.dx_ring = ring(P.dx_tile, w[WG], &w[WU]);
+    P.dx_ring = ring(P.dx.d, P.dx_tile, 8.0 * (double)weights * (double)F * (double)K, w[WG], &w[WU]);
     if (P.dx_ring) {
       P.dx_tile = large;
       if ((s = place_tiles(&P.dx.d, large, false)) != SL_OK) return s;
@@ -650,7 +673,7 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
   }
   if (P.want_dw) {
     if ((s = product(&P.dw.d, &P.dw_tile, 2 * weights, F, K, tokens ? across : 0, Fp * across, K * across, 1)) != SL_OK) return s;
-    P.dw_ring = (!one_weight || n == 1) && rows * 4 * Fp + 1024 < kLim && ring(P.dw_tile, w[X], nullptr);
+    P.dw_ring = (!one_weight || n == 1) && rows * 4 * Fp + 1024 < kLim && ring(P.dw.d, P.dw_tile, 4.0 * (double)n * (double)rows * (double)K, w[X], nullptr);
     if (P.dw_ring) {
       if (!P.want_dx) P.off_rows = take(n * rows * 2 * Fp);
       P.dw_tile = large;

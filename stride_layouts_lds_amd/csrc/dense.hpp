@@ -269,18 +269,22 @@ __device__ __forceinline__ void dense_load8(const void* at, float (&v)[8]) {
 // on; where eight lanes have a row, the rows of a pair differ in the lowest bit, so that
 // their chunks, all even or all odd in a row, lie on different banks.)  Others,
 // and the columns next to N where those are no eight: EPI::finish.
+template <int COLS>
+constexpr int kRowsPitch = COLS == 96 ? 128 : COLS;
 template <int EK, bool GATED, int COLS, class EPI>
 __device__ __forceinline__ void dense_rows(const EPI& epi, const DenseParams& p, int64_t batch, int64_t m_base, int64_t n_base, int32_t lane,
                                            const char* region) {
+  static_assert(!GATED || COLS != 96, "halves of whole lanes");
   constexpr int OUT = GATED ? COLS / 2 : COLS;  // columns of the result
-  constexpr int LPR = OUT / 8, RPI = 64 / LPR;  // lanes to a row, rows at once
+  constexpr int PITCH = kRowsPitch<COLS>;
+  constexpr int LPR = (GATED ? PITCH / 2 : PITCH) / 8, RPI = 64 / LPR;  // lanes to a row (of 96 columns: four of them idle), rows at once
   const int32_t group = lane / LPR, l = lane % LPR;
   // (the row bit that pairs of lane groups differ in goes last)
   const int32_t r0 = LPR == 8 ? (group & 4) | (group & 1) << 1 | (group & 2) >> 1 : group;
   const int64_t m = m_base + r0, n = n_base + 8 * l;
-  auto quad = [&](int32_t r, int32_t q) { return dense_value<EK>(*(const floatx4*)(region + rows_chunk<COLS>(r, q))); };
+  auto quad = [&](int32_t r, int32_t q) { return dense_value<EK>(*(const floatx4*)(region + rows_chunk<PITCH>(r, q))); };
   const int32_t count = m < p.M ? (int32_t)(p.M - m > 64 ? 64 / RPI : (p.M - m + RPI - 1) / RPI) : 0;
-  if (n >= p.N || count == 0) return;
+  if (n >= p.N || count == 0 || l >= OUT / 8) return;
   if (p.flags & DF_ROWS && n + 8 <= p.N) {
     auto get = [&](int32_t it, int s, float(&v)[8]) {
       const int32_t r = RPI * it + r0, q = 2 * l + (s ? OUT / 4 : 0);
@@ -304,25 +308,27 @@ __device__ __forceinline__ void dense_rows(const EPI& epi, const DenseParams& p,
 // ---------------------------------------------------------------------------
 // Large tiles, on the schedule of gemm_f16_w4r_kernel (gemm_f16.hip), which see:
 // four waves, each FM x FN instruction tiles with its accumulators in AGPRs,
-// LDS a ring of five operand K-tiles, operand tile q (A of K-tile q / 2 for even q, B for
-// odd q) in slot q % 5.  Per K-tile: reads of its first slice beside the last
+// LDS a ring of S operand K-tiles, operand tile q (A of K-tile q / 2 for even q, B for
+// odd q) in slot q % S.  Per K-tile: reads of its first slice beside the last
 // products of the K-tile before, the first slice's products beside the reads of
 // the second, half of the second's, one barrier.  A copy has a K-tile of compute or
 // more to land.
 //   8 x 8  256 x 256, one workgroup to a CU
+//   8 x 6  256 x 192, the same
 //   8 x 4  256 x 128, the same
 //   4 x 4  128 x 128, two to a CU
 // The gated pair's wave holds 8 FN rows of each matrix.
 // ---------------------------------------------------------------------------
-template <int EK, bool GATED, int FM, int FN, class EPI, class PRODUCTS>
-__global__ __launch_bounds__(256, FM == 8 ? 1 : 2) void dense_ring_kernel(const PRODUCTS products_) {
+template <int EK, bool GATED, int FM, int FN, int AHEAD, class EPI, class PRODUCTS>
+__global__ __launch_bounds__(256, FM == 8 || AHEAD > 0 ? 1 : 2) void dense_ring_kernel(const PRODUCTS products_) {
   uint32_t id, total;
   const DenseParams& p = dense_product(products_, id, total);
   constexpr int ROWS_A = 32 * FM, ROWS_B = 32 * FN, SLOT = (FM > FN ? ROWS_A : ROWS_B) * kRowBytes;
   constexpr int BN = kResultCols<GATED, ROWS_B>;
   constexpr int NR = FM + FN;      // fragment reads of a slice
   constexpr int NH = FM / 2 * FN;  // products of half a slice
-  __shared__ __attribute__((aligned(1024))) char smem[5 * SLOT];
+  constexpr int S = kRing + 2 * AHEAD;  // operand K-tiles in LDS
+  __shared__ __attribute__((aligned(1024))) char smem[S * SLOT];
   const int32_t lane = threadIdx.x & 63;
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const TileCoord tc = map_tile((int32_t)id, (int32_t)total, p.tiles_m, p.tiles_n, p.group_m, p.batch);
@@ -341,11 +347,9 @@ __global__ __launch_bounds__(256, FM == 8 ? 1 : 2) void dense_ring_kernel(const 
   const int32_t a_row0 = (wave & 1) * 16 * FM, b_row0 = (wave >> 1) * 16 * FN;
   const int32_t T = p.k_tiles;  // at least 1
   __builtin_assume(T >= 1);
-  // past the last K-tile the look-ahead copies repeat it and are not read
-  auto kt = [&](int32_t u) { return u < T ? u : T - 1; };
   auto slot = [&](int32_t q) { return smem + q * SLOT; };
-  auto copy_a = [&](int32_t u, char* dst, int j) { la.issue_full(kt(u), dst, j); };
-  auto copy_b = [&](int32_t u, char* dst, int j) { lb.issue_full(kt(u), dst, j); };
+  auto copy_a = [&](int32_t u, char* dst, int j) { la.issue_full(u, dst, j); };
+  auto copy_b = [&](int32_t u, char* dst, int j) { lb.issue_full(u, dst, j); };
   const int32_t last_bytes = (int32_t)p.K - (T - 1) * kRowBytes;
   u32x4 fa0[FM], fb0[FN], fa1[FM], fb1[FN];
   typedef __attribute__((address_space(3))) const u32x4 lds_u4;
@@ -382,22 +386,30 @@ __global__ __launch_bounds__(256, FM == 8 ? 1 : 2) void dense_ring_kernel(const 
 #pragma unroll
     for (int e = e0; e < e1; ++e) dense_mfma_agpr<EK>(acc[i0 + e / FN][e % FN], fb[e % FN], fa[i0 + e / FN]);
   };
-  if (T == 1) la.last_tile(last_bytes), lb.last_tile(last_bytes);
+  // ahead of a copy of K-tile u: the last one ends at K, those behind it read zeros
+  auto ends_a = [&](int32_t u) {
+    if (u >= T - 1) la.last_tile(u == T - 1 ? last_bytes : 0);
+  };
+  auto ends_b = [&](int32_t u) {
+    if (u >= T - 1) lb.last_tile(u == T - 1 ? last_bytes : 0);
+  };
 #pragma unroll
-  for (int j = 0; j < FM; ++j) copy_a(0, slot(0), j);
+  for (int u = 0; u <= AHEAD + 1; ++u) {
+    ends_a(u);
 #pragma unroll
-  for (int j = 0; j < FN; ++j) copy_b(0, slot(1), j);
-  if (T == 2) la.last_tile(last_bytes);
+    for (int j = 0; j < FM; ++j) copy_a(u, slot(2 * u), j);
+    ends_b(u);
 #pragma unroll
-  for (int j = 0; j < FM; ++j) copy_a(1, slot(2), j);
-  if (T == 2) lb.last_tile(last_bytes);
-  if (T == 3) la.last_tile(last_bytes);
+    for (int j = 0; j < FN && u <= AHEAD; ++j) copy_b(u, slot(2 * u + 1), j);
+  }
+  ends_a(AHEAD + 2);
   // the first K-tile's first part computes with zero fragments (adds nothing)
 #pragma unroll
   for (int i = 0; i < FM; ++i) fa1[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
   for (int j = 0; j < FN; ++j) fb1[j] = u32x4{0, 0, 0, 0};
-  wait_vmem_n<FM>();
+  constexpr int FLIGHT = FM * (AHEAD + 1) + FN * AHEAD;  // copies of the K-tiles behind the next one
+  wait_vmem_n<FLIGHT>();
   phase_barrier();
   int32_t sa = 0;  // slot of A(t); B(t) in the next one
   int32_t t = 0;
@@ -406,12 +418,12 @@ __global__ __launch_bounds__(256, FM == 8 ? 1 : 2) void dense_ring_kernel(const 
   // accumulators a second path to what follows
 #pragma clang loop unroll(disable)
   do {
-    const int32_t s3 = sa + 3 >= 5 ? sa - 2 : sa + 3, s4 = sa == 0 ? 4 : sa - 1;
+    const int32_t s3 = sa < 2 ? sa + S - 2 : sa - 2, s4 = sa == 0 ? S - 1 : sa - 1;
 #pragma unroll
     for (int g = 0; g < NR; ++g) {
       read(g, 0, fa0, fb0);
 #pragma unroll
-      for (int j = g * FN / NR; j < (g + 1) * FN / NR; ++j) copy_b(t + 1, slot(s3), j);
+      for (int j = g * FN / NR; j < (g + 1) * FN / NR; ++j) copy_b(t + AHEAD + 1, slot(s3), j);
       products(FM / 2, g * NH / NR, (g + 1) * NH / NR, fa1, fb1);  // K-tile t - 1's
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -419,17 +431,16 @@ __global__ __launch_bounds__(256, FM == 8 ? 1 : 2) void dense_ring_kernel(const 
     for (int g = 0; g < NR; ++g) {
       read(g, 1, fa1, fb1);
 #pragma unroll
-      for (int j = g * FM / NR; j < (g + 1) * FM / NR; ++j) copy_a(t + 2, slot(s4), j);
+      for (int j = g * FM / NR; j < (g + 1) * FM / NR; ++j) copy_a(t + AHEAD + 2, slot(s4), j);
       products(0, g * 2 * NH / NR, (g + 1) * 2 * NH / NR, fa0, fb0);
       __builtin_amdgcn_sched_barrier(0);
     }
     products(0, 0, NH, fa1, fb1);
-    const int32_t na = sa + 2 >= 5 ? sa - 3 : sa + 2;
-    bases(na, na == 4 ? 0 : na + 1);
-    // the next copies are B(t + 2) and A(t + 3)
-    if (t + 2 == T - 1) lb.last_tile(last_bytes);
-    if (t + 3 == T - 1) la.last_tile(last_bytes);
-    wait_vmem_n<FM>();  // in flight after this: A(t + 2)
+    const int32_t na = sa + 2 >= S ? sa + 2 - S : sa + 2;
+    bases(na, na == S - 1 ? 0 : na + 1);
+    ends_b(t + AHEAD + 2);
+    ends_a(t + AHEAD + 3);
+    wait_vmem_n<FLIGHT>();  // K-tile t + 1 has landed
     phase_barrier();
     sa = na;
   } while (++t < T);
@@ -450,8 +461,9 @@ __global__ __launch_bounds__(256, FM == 8 ? 1 : 2) void dense_ring_kernel(const 
   // every wave's copies have landed and its reads of the ring are done
   __syncthreads();
   constexpr int COLS = 16 * FN;
-  char* region = smem + wave * (64 * COLS * 4);
-  static_assert(4 * 64 * COLS * 4 <= 5 * SLOT, "the sums fit");
+  constexpr int PITCH = kRowsPitch<COLS>;
+  char* region = smem + wave * (64 * PITCH * 4);
+  static_assert(4 * 64 * PITCH * 4 <= S * SLOT, "the sums fit");
   const EPI epi(p, tc.batch);
   const int64_t n_base = n0 + kResultCols<GATED, COLS> * (wave >> 1);
 #pragma unroll
@@ -459,7 +471,7 @@ __global__ __launch_bounds__(256, FM == 8 ? 1 : 2) void dense_ring_kernel(const 
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) *(floatx4*)(region + rows_chunk<COLS>(16 * i + (lane & 15), 4 * j + (lane >> 4))) = acc[4 * h + i][j];
+      for (int j = 0; j < FN; ++j) *(floatx4*)(region + rows_chunk<PITCH>(16 * i + (lane & 15), 4 * j + (lane >> 4))) = acc[4 * h + i][j];
     dense_rows<EK, GATED, COLS>(epi, p, tc.batch, m0 + a_row0 + 64 * h, n_base, lane, region);
   }
 }
@@ -641,9 +653,16 @@ hipError_t dense_launch(const PRODUCTS& p, const DensePlan& plan, hipStream_t s)
   typedef std::integral_constant<int, 3> c3;
   typedef std::integral_constant<int, 4> c4;
   switch (plan.tile) {
-    case DT_256x256: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 8, 8, EPI, PRODUCTS>), grid, block, 0, s, p); break;
-    case DT_256x128: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 8, 4, EPI, PRODUCTS>), grid, block, 0, s, p); break;
-    case DT_128x128: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 4, 4, EPI, PRODUCTS>), grid, block, 0, s, p); break;
+    case DT_256x256: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 8, 8, 0, EPI, PRODUCTS>), grid, block, 0, s, p); break;
+    case DT_256x192:  // no plan of the gated pair or of two products
+      if constexpr (GATED || std::is_same<PRODUCTS, DensePair>::value) return hipErrorInvalidValue;
+      else hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 8, 6, 0, EPI, PRODUCTS>), grid, block, 0, s, p);
+      break;
+    case DT_256x128: hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 8, 4, 0, EPI, PRODUCTS>), grid, block, 0, s, p); break;
+    case DT_128x128:
+      if (plan.stages == kDeepRing) hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 4, 4, (kDeepRing - kRing) / 2, EPI, PRODUCTS>), grid, block, 0, s, p);
+      else hipLaunchKernelGGL((dense_ring_kernel<EK, GATED, 4, 4, 0, EPI, PRODUCTS>), grid, block, 0, s, p);
+      break;
     case DT_STREAM:
       if (plan.bm == 64) plan.bn == 32 ? stream(c4{}, c2{}, c3{}) : stream(c4{}, c4{}, c2{});
       else if (plan.bn == 32) stream(c2{}, c2{}, c4{});

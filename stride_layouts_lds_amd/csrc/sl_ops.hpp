@@ -179,17 +179,19 @@ constexpr int32_t DF_ROWS = 16;     // the columns of C and of every output cont
 // matrices together)
 enum DenseTile : int32_t {
   DT_256x256 = 0,  // 4 waves, each 128 x 128
-  DT_256x128 = 1,  // 4 waves, each 128 x 64
-  DT_128x128 = 2,  // 4 waves, each 64 x 64; two workgroups to a CU
-  DT_STREAM = 3,   // 32 or 64 rows of A, 4 waves that split K
-  DT_SKINNY = 4,   // 16 rows of A, 8 waves that split K
+  DT_256x192 = 1,  // 4 waves, each 128 x 96
+  DT_256x128 = 2,  // 4 waves, each 128 x 64
+  DT_128x128 = 3,  // 4 waves, each 64 x 64; two workgroups to a CU, or one of the deep ring's
+  DT_STREAM = 4,   // 32 or 64 rows of A, 4 waves that split K
+  DT_SKINNY = 5,   // 16 rows of A, 8 waves that split K
 };
 constexpr int32_t kDenseSkinnyWaves = 8, kDenseStreamWaves = 4;
+constexpr int32_t kRing = 5, kDeepRing = 9;  // operand K-tiles in the ring of the first four
 struct DensePlan {
   int32_t tile;
   int32_t bm, bn;       // rows of A and of B of a workgroup
   int32_t threads, lds;
-  int32_t stages;       // LDS K-tiles of DT_STREAM
+  int32_t stages;       // LDS K-tiles of a wave of DT_STREAM, operand K-tiles of a ring
   double us;            // what the model of dense_plan gives it
 };
 // `gated`: bn / 2 columns of the result to a workgroup

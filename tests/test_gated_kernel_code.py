@@ -10,7 +10,7 @@ import test_kernel_code as K
 import test_ops_kernel_code as O
 from test_kernel_code import code_objects  # noqa: F401
 
-RING = "_ZN2sl12_GLOBAL__N_117dense_ring_kernelILi{ek}ELb{gated}ELi{fm}ELi{fn}ENS0_{epi}ENS_{params}EEEvT4_"
+RING = "_ZN2sl12_GLOBAL__N_117dense_ring_kernelILi{ek}ELb{gated}ELi{fm}ELi{fn}ELi{ahead}ENS0_{epi}ENS_{params}EEEvT5_"
 EPILOGUE = {"product": "9ScaledSum", "gated": "4GateILi{ek}EE", "backward": "8GradientILi{ek}EE"}
 TYPES = {0: "fp16", 1: "bf16", 2: "int8"}
 
@@ -19,9 +19,11 @@ NAMES = {}
 for what, eks, params in (("product", (2,), "11DenseParams"), ("gated", (0, 1, 2), "11DenseParams"),
                           ("backward", (0, 1), "11DenseParams"), ("backward", (0, 1), "9DensePair")):
     for ek in eks:
-        for fm, fn, loop, after in ((8, 8, 128, 32), (8, 4, 64, 16), (4, 4, 32, 8)):
-            name = f"{what}{'_pair' if params == '9DensePair' else ''}_{TYPES[ek]}_{fm}{fn}"
-            NAMES[name] = (RING.format(ek=ek, gated=int(what == "gated"), fm=fm, fn=fn, epi=EPILOGUE[what].format(ek=ek),
+        for fm, fn, ahead, loop, after in ((8, 8, 0, 128, 32), (8, 6, 0, 96, 24), (8, 4, 0, 64, 16), (4, 4, 0, 32, 8), (4, 4, 2, 32, 8)):
+            if fn == 6 and (what == "gated" or params == "9DensePair"):
+                continue
+            name = f"{what}{'_pair' if params == '9DensePair' else ''}_{TYPES[ek]}_{fm}{fn}{ahead}"
+            NAMES[name] = (RING.format(ek=ek, gated=int(what == "gated"), fm=fm, fn=fn, ahead=ahead, epi=EPILOGUE[what].format(ek=ek),
                                        params=params), loop, after)
 NAMES.update({f"across_{TYPES[ek]}_{a}": (f"_ZN2sl12_GLOBAL__N_116grad_ring_kernelILi{ek}ELb{a}EEEvNS_10GradParamsE", 128, 64)
               for ek in (0, 1) for a in (0, 1)})
