@@ -33,7 +33,13 @@ namespace sl {
 static DensePlan ring_plan(int32_t tile, int32_t bm, int32_t bn, int32_t slots) {
   return {tile, bm, bn, 256, slots * std::max(bm, bn) * 128, slots, 0.0};
 }
-// 256 x 256 tiles of a product (rows of B: N)
+// 128 x 128 tiles of a product (rows of B: N): alone on their CU the more of them the
+// longer a K-tile takes, two to a CU by rounds; and 256 x 256 ones.
+static double alone_k(double tiles, bool deep) { return 0.33 + (deep ? 0.1 : 0.2) * tiles / kCUs; }
+static double dense_small_us(double tiles, double T, bool deep) {
+  if (tiles > kCUs) return 2.4 + std::ceil(tiles / (2 * kCUs)) * (3.4 + 0.8 * T);
+  return (deep ? 4.8 : 4.4) + alone_k(tiles, deep) * T;
+}
 static double dense_large_us(int64_t batch, int64_t M, int64_t N, int64_t K) {
   using host::ceil_div;
   const double tiles = (double)batch * (double)ceil_div(M, 256) * (double)ceil_div(N, 256);
@@ -63,39 +69,53 @@ DensePlan dense_plan(bool gated, int64_t batch, int64_t M, int64_t N, int64_t K)
   large[0].us = dense_large_us(batch, M, B, K);
   large[1].us = gated ? best.us : std::ceil(tiles(256, 192) / kCUs) * (8.6 + 1.1 * T);
   large[2].us = std::ceil(tiles(256, 128) / kCUs) * (7.0 + 0.77 * T);
-  large[3].us = deep ? 4.8 + 0.4 * T : t2 <= kCUs ? 4.4 + 0.51 * T : 2.4 + std::ceil(t2 / (2 * kCUs)) * (3.4 + 0.8 * T);
+  large[3].us = dense_small_us(t2, T, deep);
   for (const DensePlan& t : large)
     if (t.us < best.us) best = t;
   return best;
 }
 
-// One tile for two products in one launch, by the same model: the workgroups'
-// times over the slots there are, or the longest one's.  (512 x 1024 x 512
-// and its pair: 16 us one after the other, 9 at once.)
-DensePlan dense_pair_plan(const DenseParams& p, const DenseParams& q) {
+// 128 x 128 tiles of the backward pass on operands as they lie: transposing reads take
+// LDS twice as long, which bounds these tiles (1024 x 2048 x 1024's dx 37 us, with
+// copies, made in 3 us more, 18; 8 of 300 x 1000 x 520's 21 and 15.5; two to a CU 2048 tiles of 8
+// K-tiles 43 both ways).
+static double lying_k(double tiles) { return 0.5 + 0.11 * tiles / kCUs; }
+static double grad_tiles_us(double tiles, double T) {
+  return tiles > kCUs ? 2.4 + std::ceil(tiles / (2 * kCUs)) * (3.4 + 0.85 * T) : 4.4 + lying_k(tiles) * T;
+}
+
+// Two products in one launch, by the same model: the workgroups' times over the
+// slots there are, or the longest one's.
+namespace {
+struct PairTile {
+  DensePlan plan;
+  double slots, start, k;
+};
+double pair_us(const PairTile& t, const DenseParams& p, const DenseParams& q, bool lying) {
   using host::ceil_div;
-  const struct {
-    DensePlan plan;
-    double slots, start, k;
-  } tiles[6] = {{ring_plan(DT_256x256, 256, 256, kRing), kCUs, 10.2, 1.3},
-                {ring_plan(DT_256x128, 256, 128, kRing), kCUs, 7.0, 0.77},
-                {ring_plan(DT_128x128, 128, 128, kRing), 2 * kCUs, 4.4, 0.8},
-                {{DT_STREAM, 64, 64, 256, 4 * 2 * 128 * 128, 2, 0.0}, kCUs, 5.0, 0.2},
-                {{DT_STREAM, 64, 32, 256, 4 * 3 * 96 * 128, 3, 0.0}, kCUs, 5.0, 0.13},
-                {{DT_STREAM, 32, 32, 256, 4 * 4 * 64 * 128, 4, 0.0}, kCUs, 4.5, 0.1}};
+  double all = 0.0, longest = 0.0, groups = 0.0;
+  for (const DenseParams* x : {&p, &q}) {
+    if (x->K == 0 && t.plan.tile != DT_STREAM) return 1e30;  // the others want a K-tile
+    const double n = (double)x->batch * (double)ceil_div(x->M, t.plan.bm) * (double)ceil_div(x->N, t.plan.bn);
+    const double one = t.start + t.k * (double)ceil_div(x->K, 128);
+    all += n * one / t.slots, groups += n, longest = std::max(longest, one);
+  }
+  if (t.plan.tile == DT_128x128 && groups <= kCUs) longest = 4.4 + (longest - 4.4) * (lying ? lying_k(groups) : alone_k(groups, false)) / t.k;
+  return std::max(all, longest);
+}
+PairTile pair_128x128() { return {ring_plan(DT_128x128, 128, 128, kRing), 2 * kCUs, 4.4, 0.8}; }
+}  // namespace
+DensePlan dense_pair_plan(const DenseParams& p, const DenseParams& q) {
+  const PairTile tiles[6] = {{ring_plan(DT_256x256, 256, 256, kRing), kCUs, 10.2, 1.3},
+                             {ring_plan(DT_256x128, 256, 128, kRing), kCUs, 7.0, 0.77},
+                             pair_128x128(),
+                             {{DT_STREAM, 64, 64, 256, 4 * 2 * 128 * 128, 2, 0.0}, kCUs, 5.0, 0.2},
+                             {{DT_STREAM, 64, 32, 256, 4 * 3 * 96 * 128, 3, 0.0}, kCUs, 5.0, 0.13},
+                             {{DT_STREAM, 32, 32, 256, 4 * 4 * 64 * 128, 4, 0.0}, kCUs, 4.5, 0.1}};
   DensePlan best = tiles[0].plan;
   best.us = 1e300;
-  for (const auto& t : tiles) {
-    double all = 0.0, longest = 0.0, groups = 0.0;
-    for (const DenseParams* x : {&p, &q}) {
-      if (x->K == 0 && t.plan.tile != DT_STREAM) longest = 1e30;  // the others want a K-tile
-      const double n = (double)x->batch * (double)ceil_div(x->M, t.plan.bm) * (double)ceil_div(x->N, t.plan.bn);
-      const double one = t.start + t.k * (double)ceil_div(x->K, 128);
-      all += n * one / t.slots, groups += n, longest = std::max(longest, one);
-    }
-    // (alone on a CU a 128 x 128 tile takes two thirds of its time)
-    if (t.plan.tile == DT_128x128 && groups <= kCUs) longest = 4.4 + (longest - 4.4) * 0.64;
-    const double cost = std::max(all, longest);
+  for (const PairTile& t : tiles) {
+    const double cost = pair_us(t, p, q, false);
     if (cost < best.us) best = t.plan, best.us = cost;
   }
   return best;
@@ -536,7 +556,7 @@ struct BackwardPlan {
   bool pair;                       // both in one launch
   int32_t kind;
   bool want_dx, want_dw, launch;
-  bool dx_ring, dw_ring;           // on operands as they lie (launch_grad_ring)
+  bool dx_lies, dw_lies;           // on operands as they lie (launch_grad_ring, launch_grad_tiles)
   int64_t off_rows, off_t, off_xt, off_wt, ws_bytes;
   View v[9];
 };
@@ -633,33 +653,66 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
     p->type = g.type;
     if (256 * 2 * k >= kLim) return fail(SL_ERR_SHAPE, "a 256-row tile of an operand spans 2^31 bytes or more");
     *tile = sl::dense_plan(false, count, m, n, 2 * k);
-    return place_tiles(p, *tile, false);
+    return SL_OK;
   };
   auto output = [&](sl::DenseParams* p, int i, const sl_tensor& d, const View& v, int64_t count) {
     p->kept[i] = d.data, p->kept_rs[i] = v.rs, p->kept_cs[i] = v.cs, p->kept_bs[i] = count > 1 ? v.bs : 0;
     if (quad_rows(v, count)) p->flags |= sl::DF_KEPT_VEC << i;
   };
   P.kind = dt == SL_F16 ? sl::EK_F16 : sl::EK_BF16;
-  // A large product whose operands' rows lie on 16-byte boundaries reads them as they are,
-  // unless the copies (bytes read and written, at 4 TB/s) cost less than a better tile
-  // saves.  (us as they lie and with copies: 4000 x 500 x 3000's dx 43 and 39, 4096 x 4096 x
-  // 2048's two 281 and 248, 8 of 1024 x 1000 x 1024's dw 56 and 57, 4000 x 2000 x 3000's two 194
-  // and 207, 4096 x 8192 x 4096's two 871 and 925.)
-  const sl::DensePlan large = sl::ring_plan(sl::DT_256x256, 256, 256, sl::kRing);
-  auto ring = [&](const sl::DenseParams& p, const sl::DensePlan& tile, double copies, const View& x, const View* y) {
-    bool ok = tokens && sl::dense_large_us(p.batch, p.M, p.N, p.K) <= tile.us + copies / 4e6;
-    for (const View* v : {&x, y ? y : &x})
+  // Operands whose rows lie on 16-byte boundaries can be read as they are; others, and where
+  // a better tile saves more than the copies (bytes read and written, at 7 TB/s:
+  // much of it never leaves the caches) cost, are copied.  us as they lie and with copies: 4000 x 500 x 3000's dx 43 and 39, 4096 x
+  // 4096 x 2048's two 281 and 248, 8 of 1024 x 1000 x 1024's two 91 and 97, 1024 x 4096 x 4096's
+  // 141 and 159, 4000 x 2000 x 3000's 194 and 207, 4096 x 8192 x 4096's 871 and 925.
+  constexpr double COPIED = 7e6;  // bytes a us
+  auto readable = [&](const View& x, const View& y) {
+    bool ok = tokens && x.rs == y.rs;
+    for (const View* v : {&x, &y})
       ok = ok && v->cs == 1 && v->cols % 8 == 0 && v->rs % 8 == 0 && (uintptr_t)v->t->data % 16 == 0 && bstride(*v) % 8 == 0 &&
-           v->rows * v->rs * 2 + 1024 < kLim && v->rs == x.rs;
+           v->rows * v->rs * 2 + 1024 < kLim;
     return ok;
   };
+  auto choose = [&](const sl::DenseParams& p, bool ok, double copies, sl::DensePlan* tile) {
+    sl::DensePlan large = sl::ring_plan(sl::DT_256x256, 256, 256, sl::kRing), small = sl::ring_plan(sl::DT_128x128, 128, 128, sl::kRing);
+    large.us = sl::dense_large_us(p.batch, p.M, p.N, p.K);
+    small.us = sl::grad_tiles_us((double)p.batch * (double)ceil_div(p.M, 128) * (double)ceil_div(p.N, 128), (double)ceil_div(p.K, 128));
+    const sl::DensePlan& best = small.us < large.us ? small : large;
+    tile->us += copies / COPIED;
+    if (!ok || best.us > tile->us) return false;
+    *tile = best;
+    return true;
+  };
+  bool dx_ok = false, dw_ok = false;
+  double dx_copies = 0.0, dw_copies = 0.0;
   if (P.want_dx) {
-    if (tokens) P.off_rows = take(n * rows * 2 * Fp);
     if ((s = product(&P.dx.d, &P.dx_tile, n, rows, K, tokens ? 2 * Fp : 0, rows * 2 * Fp, one_weight ? 0 : K * 2 * Fp, 0)) != SL_OK) return s;
-    P.dx_ring = ring(P.dx.d, P.dx_tile, 8.0 * (double)weights * (double)F * (double)K, w[WG], &w[WU]);
-    if (P.dx_ring) {
-      P.dx_tile = large;
-      if ((s = place_tiles(&P.dx.d, large, false)) != SL_OK) return s;
+    dx_ok = readable(w[WG], w[WU]);
+    if (tokens) dx_copies = 8.0 * (double)weights * (double)F * (double)K;
+    P.dx_lies = choose(P.dx.d, dx_ok, dx_copies, &P.dx_tile);
+  }
+  if (P.want_dw) {
+    if ((s = product(&P.dw.d, &P.dw_tile, 2 * weights, F, K, tokens ? across : 0, Fp * across, K * across, 1)) != SL_OK) return s;
+    dw_ok = (!one_weight || n == 1) && rows * 4 * Fp + 1024 < kLim && readable(w[X], w[X]);
+    // (with dx wanted too dg and du are written both ways where they are not read as they lie)
+    if (tokens) dw_copies = 4.0 * (double)n * (double)rows * (double)(K + (P.want_dx ? F : 0));
+    P.dw_lies = choose(P.dw.d, dw_ok, dw_copies, &P.dw_tile);
+  }
+  if (P.want_dx && P.want_dw) {
+    sl::DensePlan copied = sl::dense_pair_plan(P.dx.d, P.dw.d), lying = sl::ring_plan(sl::DT_128x128, 128, 128, sl::kRing);
+    copied.us += (dx_copies + dw_copies) / COPIED;
+    lying.us = dx_ok && dw_ok ? sl::pair_us(sl::pair_128x128(), P.dx.d, P.dw.d, true) : 1e30;
+    const sl::DensePlan& both = lying.us < copied.us ? lying : copied;
+    sl::DenseParams x = P.dx.d, y = P.dw.d;
+    P.pair = both.us < P.dx_tile.us + P.dw_tile.us && place_tiles(&x, both, false) == SL_OK && place_tiles(&y, both, false) == SL_OK &&
+             grid_fits((int64_t)x.batch * x.tiles_m * x.tiles_n + (int64_t)y.batch * y.tiles_m * y.tiles_n, 1, 1, both.threads);
+    if (P.pair) P.dx_tile = P.dw_tile = both, P.dx_lies = P.dw_lies = lying.us < copied.us;
+    g_msg.clear();
+  }
+  if (P.want_dx || P.dw_lies) P.off_rows = tokens ? take(n * rows * 2 * Fp) : 0;
+  if (P.want_dx) {
+    if ((s = place_tiles(&P.dx.d, P.dx_tile, false)) != SL_OK) return s;
+    if (P.dx_lies) {
       for (int i = 0; i < 2; ++i) P.dx.d.b[i] = (const uint8_t*)t[WG + i]->data, P.dx.d.b_bs[i] = 2 * bstride(w[WG + i]);
       P.dx.d.b_rs[0] = 2 * w[WG].rs;
       P.dx.rows = F, P.dx.parts = 2;
@@ -672,12 +725,8 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
     if (w[DX].cs == 1) P.dx.d.flags |= sl::DF_ROWS;
   }
   if (P.want_dw) {
-    if ((s = product(&P.dw.d, &P.dw_tile, 2 * weights, F, K, tokens ? across : 0, Fp * across, K * across, 1)) != SL_OK) return s;
-    P.dw_ring = (!one_weight || n == 1) && rows * 4 * Fp + 1024 < kLim && ring(P.dw.d, P.dw_tile, 4.0 * (double)n * (double)rows * (double)K, w[X], nullptr);
-    if (P.dw_ring) {
-      if (!P.want_dx) P.off_rows = take(n * rows * 2 * Fp);
-      P.dw_tile = large;
-      if ((s = place_tiles(&P.dw.d, large, false)) != SL_OK) return s;
+    if ((s = place_tiles(&P.dw.d, P.dw_tile, false)) != SL_OK) return s;
+    if (P.dw_lies) {
       sl::DenseParams& d = P.dw.d;
       d.a_rs = 4 * Fp, d.a_bs = rows * 4 * Fp;
       for (int i = 0; i < 2; ++i) d.b[i] = (const uint8_t*)args->x.data, d.b_bs[i] = 2 * bstride(w[X]);
@@ -692,14 +741,6 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
     if (v[DWG].cs == 1 && v[DWU].cs == 1) P.dw.d.flags |= sl::DF_ROWS;
   }
   if (!grid_fits(sl::gated_prepare_groups(&P.prepare), 1, 1, sl::kPrepareThreads)) return fail(SL_ERR_SHAPE, "the operands are too large");
-  if (P.want_dx && P.want_dw && !P.dx_ring && !P.dw_ring) {
-    const sl::DensePlan both = sl::dense_pair_plan(P.dx.d, P.dw.d);
-    sl::DenseParams x = P.dx.d, y = P.dw.d;
-    P.pair = both.us < P.dx_tile.us + P.dw_tile.us && place_tiles(&x, both, false) == SL_OK && place_tiles(&y, both, false) == SL_OK &&
-             grid_fits((int64_t)x.batch * x.tiles_m * x.tiles_n + (int64_t)y.batch * y.tiles_m * y.tiles_n, 1, 1, both.threads);
-    if (P.pair) P.dx.d = x, P.dw.d = y, P.dx_tile = P.dw_tile = both;
-    g_msg.clear();
-  }
   return SL_OK;
 }
 
@@ -731,15 +772,15 @@ sl_status sl_gated_backward(const sl_gated_backward_args* args, void* stream) {
   sl::DenseParams &dx = P.dx.d, &dw = P.dw.d;
   if (P.prepare.slope.batch > 0) {  // (without tokens the products have K = 0 and read nothing)
     uint16_t* const rows = (uint16_t*)(ws + P.off_rows);
-    if (P.want_dx || P.dw_ring) P.prepare.slope.rows = rows;
+    if (P.want_dx || P.dw_lies) P.prepare.slope.rows = rows;
     if (P.want_dx) {
       dx.a = (const uint8_t*)rows;
-      if (!P.dx_ring) {
+      if (!P.dx_lies) {
         for (int i = 0; i < 2; ++i) P.prepare.pack[1 + i].out = (uint16_t*)(ws + P.off_wt) + i * P.prepare.slope.Fp;
         dx.b[0] = (const uint8_t*)(ws + P.off_wt);
       }
     }
-    if (P.want_dw && P.dw_ring) {
+    if (P.want_dw && P.dw_lies) {
       dw.a = (const uint8_t*)rows;
     } else if (P.want_dw) {
       P.prepare.slope.t = (uint16_t*)(ws + P.off_t);
@@ -748,14 +789,16 @@ sl_status sl_gated_backward(const sl_gated_backward_args* args, void* stream) {
     }
   }
   hipError_t e = sl::launch_gated_prepare(P.prepare, st);
-  if (e == hipSuccess && P.pair) {
-    const sl::DensePair both = {{dx, dw}, (uint32_t)((int64_t)dx.batch * dx.tiles_m * dx.tiles_n)};
-    e = sl::launch_gated_products(both, P.kind, P.dx_tile, st);
-    if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
-    return SL_OK;
-  }
-  if (e == hipSuccess && P.want_dx) e = P.dx_ring ? sl::launch_grad_ring(P.dx, P.kind, false, st) : sl::launch_gated_products(dx, P.kind, P.dx_tile, st);
-  if (e == hipSuccess && P.want_dw) e = P.dw_ring ? sl::launch_grad_ring(P.dw, P.kind, true, st) : sl::launch_gated_products(dw, P.kind, P.dw_tile, st);
+  const uint32_t first = (uint32_t)((int64_t)dx.batch * dx.tiles_m * dx.tiles_n);
+  if (e == hipSuccess && P.pair)
+    e = P.dx_lies ? sl::launch_grad_tiles(sl::GradPair{P.dx, P.dw, first}, P.kind, st)
+                  : sl::launch_gated_products(sl::DensePair{{dx, dw}, first}, P.kind, P.dx_tile, st);
+  auto one = [&](const sl::GradParams& g, const sl::DensePlan& tile, bool lies, bool across) {
+    return !lies ? sl::launch_gated_products(g.d, P.kind, tile, st)
+                 : tile.tile == sl::DT_256x256 ? sl::launch_grad_ring(g, P.kind, across, st) : sl::launch_grad_tiles(g, P.kind, across, st);
+  };
+  if (e == hipSuccess && P.want_dx && !P.pair) e = one(P.dx, P.dx_tile, P.dx_lies, false);
+  if (e == hipSuccess && P.want_dw && !P.pair) e = one(P.dw, P.dw_tile, P.dw_lies, true);
   if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
   return SL_OK;
 }

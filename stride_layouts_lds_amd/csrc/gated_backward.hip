@@ -35,12 +35,14 @@ struct Gradient {
   }
 };
 
-// A K-tile of an operand whose rows are contracted over: 64 rows of 256 of its
-// columns into the M-major LDS tile (mn_lds_offset), copy j of a wave 2 rows.
+// A K-tile of an operand whose rows are contracted over: 64 rows of W of its
+// columns into the M-major LDS tile (mn_lds_offset), copy j of a wave 512 / W rows.
+template <int W>
 struct AcrossLoader {
+  static constexpr int CPR = W / 8, RPC = 64 / CPR, ITERS = 16 / RPC;  // 16-byte chunks of a row, rows of a copy, copies
   int32_t wave, lane, cols;
-  uint32_t step;     // bytes between rows
-  uint32_t voff[8];  // the lane's offset in copy j of a K-tile
+  uint32_t step;         // bytes between rows
+  uint32_t voff[ITERS];  // the lane's offset in copy j of a K-tile
   // `cols` valid columns, a multiple of 8, of rows `step_` bytes apart
   __device__ __forceinline__ AcrossLoader(int32_t cols_, int64_t step_, int32_t wave_, int32_t lane_)
       : wave(wave_), lane(lane_), cols(cols_), step((uint32_t)step_) {
@@ -49,8 +51,8 @@ struct AcrossLoader {
   // of the K-tiles copied from here on `valid` rows are there (others read zero)
   __device__ __forceinline__ void rows(int32_t valid) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int32_t k = 2 * (4 * j + wave) + (lane >> 5), c = (lane & 31) ^ mn_swz(k);
+    for (int j = 0; j < ITERS; ++j) {
+      const int32_t k = RPC * (4 * j + wave) + lane / CPR, c = lane % CPR ^ mn_swz(k);
       voff[j] = k < valid && 8 * c < cols ? (uint32_t)k * step + (uint32_t)(16 * c) : kOutOfRange;
     }
   }
@@ -146,6 +148,47 @@ __device__ __forceinline__ void products_reads_copies(floatx4 (&acc)[8][8], cons
   for (int n = 0; n < NF; ++n) to[n] = __builtin_shufflevector(o[n][0], o[n][1], 0, 1, 2, 3);
 }
 #undef SL_STATEMENT
+
+// The same for a wave's 4 x 4 block: its 16 products, NF = 4 or 8 fragments (B's
+// four, then A's) and four copies.
+#define SL_PRODUCTS16(op, r0, r1, r2, r3, r4, r5, r6, r7, c8, c9, c10, c11, c12, c13, c14, c15)                     \
+  r0 SL_MFMA(op, 0, 0, 0) r1 SL_MFMA(op, 1, 1, 0) r2 SL_MFMA(op, 2, 2, 0) r3 SL_MFMA(op, 3, 3, 0)                   \
+  r4 SL_MFMA(op, 4, 0, 1) r5 SL_MFMA(op, 5, 1, 1) r6 SL_MFMA(op, 6, 2, 1) r7 SL_MFMA(op, 7, 3, 1)                   \
+  c8 SL_MFMA(op, 8, 0, 2) c9 SL_MFMA(op, 9, 1, 2) c10 SL_MFMA(op, 10, 2, 2) c11 SL_MFMA(op, 11, 3, 2)               \
+  c12 SL_MFMA(op, 12, 0, 3) c13 SL_MFMA(op, 13, 1, 3) c14 SL_MFMA(op, 14, 2, 3) c15 SL_MFMA(op, 15, 3, 3) "s_waitcnt lgkmcnt(0)"
+#define SL_ALL16(...) SL_PRODUCTS16(__VA_ARGS__)
+#define SL_FIRST4 SL_READ(0), SL_READ(1), SL_READ(2), SL_READ(3), "", "", "", ""
+#define SL_COPIES16 SL_TO(0), SL_COPY(0), SL_TO(1), SL_COPY(1), SL_TO(2), SL_COPY(2), SL_TO(3), SL_COPY(3)
+#define SL_ROW4(i, n0, n1, n2, n3) [c##n0] "+a"(acc[i][0]), [c##n1] "+a"(acc[i][1]), [c##n2] "+a"(acc[i][2]), [c##n3] "+a"(acc[i][3])
+#define SL_ACC16 SL_ROW4(0, 0, 1, 2, 3), SL_ROW4(1, 4, 5, 6, 7), SL_ROW4(2, 8, 9, 10, 11), SL_ROW4(3, 12, 13, 14, 15)
+#define SL_OPERANDS16                                                                                                        \
+  [b0] "v"(fb[0]), [b1] "v"(fb[1]), [b2] "v"(fb[2]), [b3] "v"(fb[3]), [a0] "v"(fa[0]), [a1] "v"(fa[1]), [a2] "v"(fa[2]),      \
+      [a3] "v"(fa[3]), [k0] "n"(K0), [k1] "n"(K0 + 1024)
+#define SL_STATEMENT16(op)                                                                                                   \
+  if constexpr (NF == 8)                                                                                                     \
+    asm volatile(SL_ALL16(op, SL_READS8, SL_COPIES16) : SL_ACC16, SL_OUT8 : SL_OPERANDS16, SL_COPY4, SL_AT8 : "memory", "m0", "scc"); \
+  else                                                                                                                       \
+    asm volatile(SL_ALL16(op, SL_FIRST4, SL_COPIES16) : SL_ACC16, SL_OUT4 : SL_OPERANDS16, SL_COPY4, SL_AT4 : "memory", "m0", "scc");
+template <int EK, int NF, int K0>
+__device__ __forceinline__ void products16(floatx4 (&acc)[4][4], const u32x4 (&fb)[4], const u32x4 (&fa)[4], const uint32_t (&at)[8],
+                                           u32x4 (&to_b)[4], u32x4 (&to_a)[4], const Copies& copy, const uint32_t (&voff)[4]) {
+  u32x2 o[NF][2];
+  if constexpr (EK == EK_F16) {
+    SL_STATEMENT16("v_mfma_f32_16x16x32_f16")
+  } else {
+    SL_STATEMENT16("v_mfma_f32_16x16x32_bf16")
+  }
+#pragma unroll
+  for (int n = 0; n < NF; ++n) (n < 4 ? to_b[n & 3] : to_a[n & 3]) = __builtin_shufflevector(o[n][0], o[n][1], 0, 1, 2, 3);
+}
+#undef SL_STATEMENT16
+#undef SL_OPERANDS16
+#undef SL_ACC16
+#undef SL_ROW4
+#undef SL_COPIES16
+#undef SL_FIRST4
+#undef SL_ALL16
+#undef SL_PRODUCTS16
 #undef SL_AT8
 #undef SL_AT4
 #undef SL_AT
@@ -191,7 +234,7 @@ __global__ __launch_bounds__(256, 1) void grad_ring_kernel(const GradParams g) {
   const uint8_t* const a_base[1] = {a};
   const int64_t a_rs[1] = {p.a_rs};
   RowLoader<256, 256, 0> la(a_base, a_rs, ACROSS ? 0 : rows_a, ACROSS ? 0 : (int64_t)T * kRowBytes, wave, lane);
-  AcrossLoader xa(ACROSS ? (rows_a + 7) / 8 * 8 : 0, p.a_rs, wave, lane), xb(rows_b, p.b_rs[0], wave, lane);
+  AcrossLoader<256> xa(ACROSS ? (rows_a + 7) / 8 * 8 : 0, p.a_rs, wave, lane), xb(rows_b, p.b_rs[0], wave, lane);
   const uint32_t a_bytes = ACROSS ? (uint32_t)((part - 1) * p.a_rs + 512) : (uint32_t)((rows_a - 1) * p.a_rs + (int64_t)T * kRowBytes);
   const uint32_t b_bytes = (uint32_t)((part - 1) * p.b_rs[0] + 2 * rows_b);
   const u32x4 ra = rsrc_words(a, a_bytes);
@@ -332,6 +375,166 @@ __global__ __launch_bounds__(256, 1) void grad_ring_kernel(const GradParams g) {
   }
 }
 
+// 128 x 128 tiles of the same, two workgroups to a CU, on the schedule of dense_ring_kernel's.
+template <int EK, bool ACROSS>
+__device__ __forceinline__ void grad_tile(const GradParams& g, uint32_t id, uint32_t total, char* smem) {
+  constexpr int F = 4, W = 128, SLOT = W * kRowBytes;
+  const DenseParams& p = g.d;
+  const int32_t lane = threadIdx.x & 63;
+  const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const TileCoord tc = map_tile((int32_t)id, (int32_t)total, p.tiles_m, p.tiles_n, p.group_m, p.batch);
+  const int64_t m0 = (int64_t)tc.tm * W, n0 = (int64_t)tc.tn * W;
+  const int32_t rows_a = (int32_t)(p.M - m0 < W ? p.M - m0 : W), rows_b = (int32_t)(p.N - n0 < W ? p.N - n0 : W);
+  const int64_t matrix = tc.batch >> p.b_shift;
+  const int32_t second = tc.batch & p.b_shift;
+  const uint8_t* a = p.a + matrix * p.a_bs + second * g.a_second + (ACROSS ? 2 * m0 : m0 * p.a_rs);
+  // (columns of A past the result's rows hold zeros)
+  const int32_t part = (int32_t)g.rows, parts = g.parts;  // rows of B to a part, parts
+  const int32_t PT = (part + 63) / 64, T = parts * PT;    // K-tiles
+  __builtin_assume(T >= 1);
+  const uint8_t* const a_base[1] = {a};
+  const int64_t a_rs[1] = {p.a_rs};
+  RowLoader<W, 256, 0> la(a_base, a_rs, ACROSS ? 0 : rows_a, ACROSS ? 0 : (int64_t)T * kRowBytes, wave, lane);
+  AcrossLoader<W> xa(ACROSS ? (rows_a + 7) / 8 * 8 : 0, p.a_rs, wave, lane), xb(rows_b, p.b_rs[0], wave, lane);
+  const uint32_t a_bytes = ACROSS ? (uint32_t)((part - 1) * p.a_rs + 2 * W) : (uint32_t)((rows_a - 1) * p.a_rs + (int64_t)T * kRowBytes);
+  const uint32_t b_bytes = (uint32_t)((part - 1) * p.b_rs[0] + 2 * rows_b);
+  const u32x4 ra = rsrc_words(a, a_bytes);
+  const uint8_t* const b0 = p.b[0] + matrix * p.b_bs[0] + 2 * n0;
+  const uint8_t* const b1 = p.b[1] + matrix * p.b_bs[1] + 2 * n0;
+  const u32x4 rb0 = rsrc_words(b0, b_bytes), rb1 = rsrc_words(b1, b_bytes);
+  floatx4 acc[F][F];
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < F; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  const int32_t a_row0 = (wave & 1) * 64, b_row0 = (wave >> 1) * 64;
+  auto kt = [&](int32_t u) { return u < T ? u : T - 1; };
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)smem;
+  // ahead of K-tile u's copies: the last one of a part may have fewer than 64 rows, and
+  // those past the last read zeros
+  const int32_t last = part - 64 * (PT - 1);
+  auto before_a = [&](int32_t u) {
+    if constexpr (ACROSS) {
+      if (u >= T - 1) xa.rows(u == T - 1 ? last : 0);
+    } else {
+      if (u >= T) la.last_tile(0);
+    }
+  };
+  auto before_b = [&](int32_t u) {
+    const int32_t at = u >= PT ? u - PT : u;
+    if (u >= T) xb.rows(0);
+    else if (at == PT - 1) xb.rows(last);
+    else if (at == 0 && u > 0) xb.rows(64);
+  };
+  auto copies_a = [&](int32_t u, int32_t q) {
+    return Copies{lds0 + (uint32_t)(q * SLOT + wave * 1024), ra, (uint32_t)kt(u) * (ACROSS ? 64u * xa.step : (uint32_t)kRowBytes)};
+  };
+  auto copies_b = [&](int32_t u, int32_t q) {
+    const int32_t v = kt(u);
+    return Copies{lds0 + (uint32_t)(q * SLOT + wave * 1024), v >= PT ? rb1 : rb0, (uint32_t)(v >= PT ? v - PT : v) * 64u * xb.step};
+  };
+  const uint32_t(&va)[4] = ACROSS ? xa.voff : la.voff;
+  const uint32_t(&vb)[4] = xb.voff;
+  // all four at once, ahead of the loop
+  auto copy_all = [&](const uint8_t* base, uint32_t bytes, const uint32_t(&voff)[4], const Copies& c) {
+    const __amdgpu_buffer_rsrc_t from = make_rsrc(base, bytes);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t v = voff[j];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void_t*)(uintptr_t)(c.to + 4096u * (uint32_t)j), 16, v, c.start, 0, 0);
+    }
+  };
+  u32x4 fa0[F], fb0[F], fa1[F], fb1[F];
+  typedef __attribute__((address_space(3))) const u32x4 lds_u4;
+  // LDS addresses: of an operand read across, one for each fragment (slices 8192
+  // apart); of A read along its rows, for either slice and parity of the fragment (pairs
+  // of fragments 4096 apart)
+  uint32_t off[8], at[8];  // B's, then A's
+#pragma unroll
+  for (int j = 0; j < F; ++j) {
+    off[j] = lds0 + (uint32_t)tr_read_offset(lane, 0, b_row0 + 16 * j, 0, W);
+    off[F + j] = ACROSS ? lds0 + (uint32_t)tr_read_offset(lane, 0, a_row0 + 16 * j, 0, W)
+                        : lds0 + (uint32_t)fragment_lds_offset(MFMA16_F16, lane, 0, a_row0 + 16 * (j & 1), j >> 1, 0);
+  }
+  auto bases = [&](int32_t qa, int32_t qb) {
+#pragma unroll
+    for (int j = 0; j < F; ++j) at[j] = off[j] + (uint32_t)(qb * SLOT), at[F + j] = off[F + j] + (uint32_t)(qa * SLOT);
+  };
+  auto read_a = [&](int ks, u32x4(&fa)[F]) {
+    if constexpr (!ACROSS) {
+#pragma unroll
+      for (int e = 0; e < F; ++e) fa[e] = *(lds_u4*)(uintptr_t)(at[F + 2 * ks + (e & 1)] + 4096u * (uint32_t)(e >> 1));
+    }
+  };
+  before_a(0), before_b(0);
+  copy_all(a, a_bytes, va, copies_a(0, 0));
+  copy_all(b0, b_bytes, vb, copies_b(0, 1));
+  before_a(1);
+  copy_all(a, a_bytes, va, copies_a(1, 2));
+  before_b(1), before_a(2);
+  // the first K-tile's first products are of zero fragments (add nothing)
+#pragma unroll
+  for (int i = 0; i < F; ++i) fa1[i] = fb1[i] = u32x4{0, 0, 0, 0};
+  wait_vmem_n<4>();
+  phase_barrier();
+  int32_t sa = 0;  // slot of A(t); B(t) in the next one
+  int32_t t = 0;
+  bases(0, 1);
+#pragma clang loop unroll(disable)
+  do {
+    const int32_t s3 = sa + 3 >= 5 ? sa - 2 : sa + 3, s4 = sa == 0 ? 4 : sa - 1;
+    // K-tile t - 1's second slice; slice 0 read; B(t + 1) copied.  Then its first
+    // slice; slice 1 read; A(t + 2) copied.
+    read_a(0, fa0);
+    __builtin_amdgcn_sched_barrier(0);
+    products16<EK, ACROSS ? 8 : 4, 0>(acc, fb1, fa1, at, fb0, fa0, copies_b(t + 1, s3), vb);
+    __builtin_amdgcn_sched_barrier(0);
+    read_a(1, fa1);
+    __builtin_amdgcn_sched_barrier(0);
+    products16<EK, ACROSS ? 8 : 4, 8192>(acc, fb0, fa0, at, fb1, fa1, copies_a(t + 2, s4), va);
+    __builtin_amdgcn_sched_barrier(0);
+    const int32_t na = sa + 2 >= 5 ? sa - 3 : sa + 2;
+    bases(na, na == 4 ? 0 : na + 1);
+    before_b(t + 2), before_a(t + 3);  // the next copies
+    wait_vmem_n<4>();  // in flight after this: A(t + 2)
+    phase_barrier();
+    sa = na;
+  } while (++t < T);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) dense_mfma_agpr<EK>(acc[e / F][e % F], fb1[e % F], fa1[e / F]);
+  wait_vmem();
+  auto pin = [&] {
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; j += 2) asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i][j + 1]));
+  };
+  pin();
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+  pin();
+  __syncthreads();
+  char* region = smem + wave * 16384;
+  const Gradient<EK == EK_F16 ? OT_F16 : OT_BF16> epi(p, tc.batch);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < F; ++j) *(floatx4*)(region + rows_chunk<64>(16 * i + (lane & 15), 4 * j + (lane >> 4))) = acc[i][j];
+  dense_rows<EK, false, 64>(epi, p, tc.batch, m0 + a_row0, n0 + b_row0, lane, region);
+}
+
+template <int EK, bool ACROSS>
+__global__ __launch_bounds__(256, 2) void grad_tile_kernel(const GradParams g) {
+  __shared__ __attribute__((aligned(1024))) char smem[kRing * 128 * kRowBytes];
+  grad_tile<EK, ACROSS>(g, blockIdx.x, gridDim.x, smem);
+}
+// x's gradient and the weights' in one launch
+template <int EK>
+__global__ __launch_bounds__(256, 2) void grad_pair_kernel(const GradPair g) {
+  __shared__ __attribute__((aligned(1024))) char smem[kRing * 128 * kRowBytes];
+  if (blockIdx.x < g.first) grad_tile<EK, false>(g.dx, blockIdx.x, g.first, smem);
+  else grad_tile<EK, true>(g.dw, blockIdx.x - g.first, gridDim.x - g.first, smem);
+}
+
 }  // namespace
 
 hipError_t launch_grad_ring(const GradParams& g, int32_t kind, bool across, hipStream_t s) {
@@ -343,6 +546,24 @@ hipError_t launch_grad_ring(const GradParams& g, int32_t kind, bool across, hipS
     if (across) hipLaunchKernelGGL((grad_ring_kernel<EK_BF16, true>), grid, block, 0, s, g);
     else hipLaunchKernelGGL((grad_ring_kernel<EK_BF16, false>), grid, block, 0, s, g);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_tiles(const GradParams& g, int32_t kind, bool across, hipStream_t s) {
+  const dim3 grid((uint32_t)dense_groups(g.d)), block(256);
+  if (kind == EK_F16) {
+    if (across) hipLaunchKernelGGL((grad_tile_kernel<EK_F16, true>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((grad_tile_kernel<EK_F16, false>), grid, block, 0, s, g);
+  } else {
+    if (across) hipLaunchKernelGGL((grad_tile_kernel<EK_BF16, true>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((grad_tile_kernel<EK_BF16, false>), grid, block, 0, s, g);
+  }
+  return hipGetLastError();
+}
+hipError_t launch_grad_tiles(const GradPair& g, int32_t kind, hipStream_t s) {
+  const dim3 grid((uint32_t)(g.first + dense_groups(g.dw.d))), block(256);
+  if (kind == EK_F16) hipLaunchKernelGGL((grad_pair_kernel<EK_F16>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((grad_pair_kernel<EK_BF16>), grid, block, 0, s, g);
   return hipGetLastError();
 }
 

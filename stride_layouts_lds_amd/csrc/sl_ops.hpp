@@ -250,13 +250,20 @@ hipError_t launch_gated_products(const DensePair& p, int32_t kind, const DensePl
 // the other, b_rs[0] bytes apart, N a multiple of 8, on 16-byte boundaries.  A: along its rows
 // (K-contiguous, each part's values padded with zeros to a multiple of 64), or
 // across, `rows` rows of M contiguous values, padded with zeros to a multiple of 64;
-// the odd matrices of pairs a_second bytes on.  256 x 256 tiles.
+// the odd matrices of pairs a_second bytes on.
 struct GradParams {
   DenseParams d;
   int64_t rows, a_second;
   int32_t parts;
 };
-hipError_t launch_grad_ring(const GradParams& g, int32_t kind, bool across, hipStream_t stream);
+// x's gradient, A along its rows, by the first `first` workgroups, and the weights'
+struct GradPair {
+  GradParams dx, dw;
+  uint32_t first;
+};
+hipError_t launch_grad_ring(const GradParams& g, int32_t kind, bool across, hipStream_t stream);  // 256 x 256 tiles
+hipError_t launch_grad_tiles(const GradParams& g, int32_t kind, bool across, hipStream_t stream); // 128 x 128 tiles
+hipError_t launch_grad_tiles(const GradPair& g, int32_t kind, hipStream_t stream);
 
 template <int T>
 struct OrthoElem {

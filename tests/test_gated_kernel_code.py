@@ -27,6 +27,8 @@ for what, eks, params in (("product", (2,), "11DenseParams"), ("gated", (0, 1, 2
                                        params=params), loop, after)
 NAMES.update({f"across_{TYPES[ek]}_{a}": (f"_ZN2sl12_GLOBAL__N_116grad_ring_kernelILi{ek}ELb{a}EEEvNS_10GradParamsE", 128, 64)
               for ek in (0, 1) for a in (0, 1)})
+NAMES.update({f"across_tile_{TYPES[ek]}_{a}": (f"_ZN2sl12_GLOBAL__N_116grad_tile_kernelILi{ek}ELb{a}EEEvNS_10GradParamsE", 32, 16)
+              for ek in (0, 1) for a in (0, 1)})
 K.KERNELS.update(NAMES)
 
 

