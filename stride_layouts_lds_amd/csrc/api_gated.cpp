@@ -661,11 +661,12 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
   };
   P.kind = dt == SL_F16 ? sl::EK_F16 : sl::EK_BF16;
   // Operands whose rows lie on 16-byte boundaries can be read as they are; others, and where
-  // a better tile saves more than the copies (bytes read and written, at 7 TB/s:
-  // much of it never leaves the caches) cost, are copied.  us as they lie and with copies: 4000 x 500 x 3000's dx 43 and 39, 4096 x
+  // a better tile saves more than the copies (bytes read and written, at 7 TB/s as
+  // long as the caches hold them, else 4.5) cost, are copied.  us as they lie and with copies: 4000 x 500 x 3000's dx 43 and 39, 4096 x
   // 4096 x 2048's two 281 and 248, 8 of 1024 x 1000 x 1024's two 91 and 97, 1024 x 4096 x 4096's
-  // 141 and 159, 4000 x 2000 x 3000's 194 and 207, 4096 x 8192 x 4096's 871 and 925.
-  constexpr double COPIED = 7e6;  // bytes a us
+  // 134 and 159, 4000 x 2000 x 3000's 194 and 207, 4096 x 8192 x 4096's 871 and 925, 1024 x 8192 x
+  // 4096's dx 160 and 219 (251 with the workspace's rows 128 bytes off powers of two).
+  auto copied_us = [](double bytes) { return bytes / (bytes < 1.5e8 ? 7e6 : 4.5e6); };
   auto readable = [&](const View& x, const View& y) {
     bool ok = tokens && x.rs == y.rs;
     for (const View* v : {&x, &y})
@@ -678,7 +679,7 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
     large.us = sl::dense_large_us(p.batch, p.M, p.N, p.K);
     small.us = sl::grad_tiles_us((double)p.batch * (double)ceil_div(p.M, 128) * (double)ceil_div(p.N, 128), (double)ceil_div(p.K, 128));
     const sl::DensePlan& best = small.us < large.us ? small : large;
-    tile->us += copies / COPIED;
+    tile->us += copied_us(copies);
     if (!ok || best.us > tile->us) return false;
     *tile = best;
     return true;
@@ -700,7 +701,7 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
   }
   if (P.want_dx && P.want_dw) {
     sl::DensePlan copied = sl::dense_pair_plan(P.dx.d, P.dw.d), lying = sl::ring_plan(sl::DT_128x128, 128, 128, sl::kRing);
-    copied.us += (dx_copies + dw_copies) / COPIED;
+    copied.us += copied_us(dx_copies + dw_copies);
     lying.us = dx_ok && dw_ok ? sl::pair_us(sl::pair_128x128(), P.dx.d, P.dw.d, true) : 1e30;
     const sl::DensePlan& both = lying.us < copied.us ? lying : copied;
     sl::DenseParams x = P.dx.d, y = P.dw.d;
