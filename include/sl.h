@@ -365,7 +365,7 @@ sl_status sl_quantize_rows(const sl_quantize_rows_args* args, void* stream);
  *   activation  SL_SILU v / (1 + e^-v), SL_GELU v Phi(v), SL_GELU_TANH 0.5 v (1 +
  *           tanh(sqrt(2/pi) (v + 0.044715 v^3))), SL_RELU max(v, 0)
  * Sums, scales, activation and product are in fp32 (i8 sums exact); g, u and h
- * are each rounded once (SL_SILU and SL_GELU_TANH are v s with an s between 0 and
+ * are each rounded once (the smooth activations are v s with an s between 0 and
  * 1, taken as 0 below 2^-126).  16-bit operands may have any strides: those whose
  * rows are not K-contiguous on 16-byte boundaries (all of them, where K is not a
  * multiple of 8) are first copied to such rows in the workspace
@@ -373,8 +373,8 @@ sl_status sl_quantize_rows(const sl_quantize_rows_args* args, void* stream);
  * are K-contiguous with rows on 16-byte boundaries and K % 16 == 0.
  * Outputs may have any strides that do not broadcast and overlap nothing; gate
  * and up may be the two halves of one matrix (of its rows or its columns).
- * M or F or the batch 0: a no-op; K 0: zeros.  Asynchronous on `stream`; errors
- * as sl_gemm, SL_ERR_ARG for another activation.
+ * M or F or the batch 0: a no-op; K 0: zeros.  F and K are below 2^30 (else
+ * SL_ERR_SHAPE).  Asynchronous on `stream`; errors as sl_gemm, SL_ERR_ARG for another activation.
  */
 typedef enum { SL_SILU = 1, SL_GELU = 2, SL_GELU_TANH = 3, SL_RELU = 4 } sl_activation;
 
@@ -406,10 +406,11 @@ sl_status sl_gated_workspace_bytes(const sl_gated_args* args, int64_t* bytes);
  * The batch is dh's; x's rank is dh's.  Gradients may have any strides that do
  * not broadcast and overlap nothing (dw_gate and dw_up may be halves as gate and
  * up).  Without tokens (M or the batch 0) the
- * weights' gradients are zeros; with F 0 dx is.  Workspace as sl_gated: 16-bit
- * copies of dg and du both ways and of x's and the weights' transposes, and what
- * sl_gemm's plan for the three products asks for.  Asynchronous on `stream`;
- * results do not vary from call to call.
+ * weights' gradients are zeros; with F 0 dx is.  M and K are below 2^30, F below
+ * 2^29 (else SL_ERR_SHAPE).  Workspace as sl_gated: dg and du, 4 bytes for each
+ * (m, f), F to a multiple of 64; where a product does not read its operands as they lie
+ * also their transposes: of dg and du, of x, of the weights.
+ * Asynchronous on `stream`; results do not vary from call to call.
  */
 typedef struct {
   sl_tensor dh;

@@ -577,8 +577,8 @@ def quantize_rows(x, out=None, stream: Optional[int] = None):
         raise ValueError("quantize_rows takes a matrix or a batch of matrices")
     if out is None:
         shape = x.shape[:-1]
-        make = lambda: (torch.empty(shape + ((x.shape[-1] + 15) // 16 * 16,), dtype=torch.int8, device=x.device),
-                        torch.empty(shape + (1,), dtype=torch.float32, device=x.device))
+        make = lambda: (x.new_empty(shape + ((x.shape[-1] + 15) // 16 * 16,), dtype=torch.int8),
+                        x.new_empty(shape + (1,), dtype=torch.float32))
         out = make() if stream is None else _allocated(stream, x.device, make)
     elif len(out) != 2:
         raise ValueError(f"out holds {len(out)} tensors, 2 are written")
@@ -609,7 +609,7 @@ def gated(x, w_gate, w_up, activation: str = "silu", sx=None, s_gate=None, s_up=
         if x.dim() == 3 or w_gate.dim() == 3 or w_up.dim() == 3:
             shape = (max(t.shape[0] for t in (x, w_gate, w_up) if t.dim() == 3),) + shape
         dtype = dtype or (torch.float16 if x.dtype == torch.int8 else x.dtype)
-        make = lambda: tuple(torch.empty(shape, dtype=dtype, device=x.device) for _ in range(3 if keep else 1))
+        make = lambda: tuple([x.new_empty(shape, dtype=dtype) for _ in range(3 if keep else 1)])
         out = make() if stream is None else _allocated(stream, x.device, make)
     else:
         out = tuple(out) if keep else (out,)

@@ -1053,3 +1053,55 @@ def test_the_same_operand_twice(api):
     check_backward("silu", api.gated_backward(g, x, w, w, g, g), g, x, w, w, g, g)
     q, s = api.quantize_rows(w)
     check_int8(api, q, q, s, s)
+
+
+# ---------------------------------------------------------------------------
+# offsets past 32 bits, gradients that broadcast
+# ---------------------------------------------------------------------------
+
+def test_large_offsets(api):
+    """Operands and results of more than 2^32 bytes, their last rows against the formula."""
+    import torch
+    K, n = 8192, 300
+    rows = (1 << 32) // K + n
+    a = torch.zeros((rows, K), dtype=torch.int8, device="cuda")
+    a[-n:] = codes(1, n, K)
+    b, sa, sb = codes(2, 64, K), scales(3, rows), scales(4, 64)
+    got = api.gemm(a, b, sfa=sa, sfb=sb, dtype=torch.float32)
+    part = a[-n:].double() @ b.double().t() * sa[-n:].double() * sb.double().t()
+    within(got[-n:], part, 3.01 * U * part.abs())
+    assert not got[:-n].any()
+    # and as the weight
+    got = api.gemm(b, a, sfa=sb, sfb=sa, dtype=torch.float32)
+    within(got[:, -n:], part.t(), 3.01 * U * part.abs().t())
+    del a, got
+    rows = (1 << 31) // K + n
+    x, wg, wu = block(5, (n, 64, K), "bfloat16")
+    big = torch.zeros((rows, K), dtype=torch.bfloat16, device="cuda")
+    big[-n:] = x
+    h, g, u = api.gated(big, wg, wu, keep=True)
+    check_gated("silu", (h[-n:], g[-n:], u[-n:]), x, wg, wu)
+    assert not h[:-n].any()
+    # backward: the other rows' gradients are zero
+    dh = torch.zeros_like(h)
+    dh[-n:] = normal(6, n, 64).bfloat16()
+    dx, dwg, dwu = api.gated_backward(dh, big, wg, wu, g, u)
+    check_backward("silu", (dx[-n:], dwg, dwu), dh[-n:], x, wg, wu, g[-n:], u[-n:])
+    assert not dx[:-n].any()
+    # as the weights
+    few = normal(7, 20, K).bfloat16()
+    h = api.gated(few, big, big)
+    check_gated("silu", h[:, -n:], few, x, x)
+
+
+@pytest.mark.parametrize("shape", [(40, 100, 72), (300, 520, 264), (1100, 1000, 520)])
+def test_gated_backward_of_a_sum(api, shape):
+    """h's gradient as a sum gives it, one value for all (strides 0), and a row for all."""
+    import torch
+    M, F, K = shape
+    for batch in ((), (3,)):
+        for shared in (False, True):
+            s = state(1, shape, "bfloat16", "silu", batch, shared and bool(batch))
+            for dh in (torch.ones((), device="cuda", dtype=torch.bfloat16).expand(s[0].shape),
+                       s[0][..., :1, :].expand(s[0].shape)):
+                check_backward("silu", api.gated_backward(dh, *s[1:]), dh, *s[1:])
