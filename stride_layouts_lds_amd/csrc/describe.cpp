@@ -320,6 +320,12 @@ std::string describe_plan(const DescribeInput& in) {
                "K-tiles t and t + 1, and a free one), %d LDS bytes",
                in.kernel, kernel_name(in.kernel), in.bm, in.bn, in.bk, NT / 64, in.wm, in.wn, in.bm / in.wm, in.bn / in.wn,
                in.lds_bytes));
+  else if (in.kernel == K_I8)
+    o.note(fmt("kernel %d: %s; tile %dx%dx%d, %d waves (%d x %d), wave tile %dx%d with accumulators in AGPRs; LDS "
+               "a ring of %d operand K-tiles (operand tile q = A of K-tile q/2 for even q, B for odd q, in slot "
+               "q %% %d), %d LDS bytes",
+               in.kernel, kernel_name(in.kernel), in.bm, in.bn, in.bk, NT / 64, in.wm, in.wn, in.bm / in.wm,
+               in.bn / in.wn, in.stages, in.stages, in.lds_bytes));
   else if (in.ring)
     o.note(fmt("kernel %d: %s; tile %dx%dx%d, %d waves (%d x %d), wave tile %dx%d with accumulators in AGPRs; LDS "
                "a ring of five operand K-tiles (operand tile q = A of K-tile q/2 for even q, B for odd q, in slot "

@@ -138,9 +138,10 @@ def test_int8_product_plans(api):  # noqa: F811
 
 
 @pytest.mark.parametrize("M,N,out", [(1, 4096, BF16), (48, 8192, F16), (64, 100, F32), (300, 200, F16), (1290, 1500, BF16), (1000, 2500, F32),
-                                     (8192, 8192, BF16), (4000, 1000, F32)])
-def test_int8_product_is_described(api, M, N, out):  # noqa: F811
-    K = 2064
+                                     (8192, 8192, BF16), (4000, 1000, F32),
+                                     (4000, 3000, F16), (512, 1024, BF16)])
+@pytest.mark.parametrize("K", [2064, 16384])
+def test_int8_product_is_described(api, M, N, out, K):  # noqa: F811
     args = gemm_args(api, rm(X, (M, K), I8), rm(Q, (N, K), I8), rm(D, (M, N), out), rm(S, (M, 1), F32), rm(ST, (N, 1), F32),
                      c=rm(QT, (M, N), out), block_k=0)
     plan = api.sl_gemm_plan(args)
@@ -150,6 +151,9 @@ def test_int8_product_is_described(api, M, N, out):  # noqa: F811
     assert f"{plan['workgroups']} workgroups of {plan['threads']} threads" in text
     assert f"{plan['lds_bytes']} LDS bytes" in text
     assert plan["lds_bytes"] <= 160 * 1024
+    if plan["tile_m"] >= 128:  # a ring of five operand K-tiles, or of nine
+        slots = plan["lds_bytes"] // (128 * plan["tile_m"])
+        assert slots in (5, 9) and f"a ring of {slots} operand K-tiles" in text
     for name in ("A", "B", "D", "C"):
         api.layout_op("parse", stages[name])
     size = lambda l: int(api.layout_op("size", l))
