@@ -409,7 +409,8 @@ sl_status sl_gated_workspace_bytes(const sl_gated_args* args, int64_t* bytes);
  * weights' gradients are zeros; with F 0 dx is.  M and K are below 2^30, F below
  * 2^29 (else SL_ERR_SHAPE).  Workspace as sl_gated: dg and du, 4 bytes for each
  * (m, f), F to a multiple of 64; where a product does not read its operands as they lie
- * also their transposes: of dg and du, of x, of the weights.
+ * also their transposes: of dg and du, of x, of the weights; for few rows dx's
+ * fp32 sums of up to 256 workgroups' shares.
  * Asynchronous on `stream`; results do not vary from call to call.
  */
 typedef struct {

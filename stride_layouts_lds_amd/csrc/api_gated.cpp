@@ -93,15 +93,22 @@ struct PairTile {
 };
 double pair_us(const PairTile& t, const DenseParams& p, const DenseParams& q, bool lying) {
   using host::ceil_div;
-  double all = 0.0, longest = 0.0, groups = 0.0;
-  for (const DenseParams* x : {&p, &q}) {
-    if (x->K == 0 && t.plan.tile != DT_STREAM) return 1e30;  // the others want a K-tile
-    const double n = (double)x->batch * (double)ceil_div(x->M, t.plan.bm) * (double)ceil_div(x->N, t.plan.bn);
-    const double one = t.start + t.k * (double)ceil_div(x->K, 128);
-    all += n * one / t.slots, groups += n, longest = std::max(longest, one);
+  double work[2], T[2], groups = 0.0;
+  for (int i = 0; i < 2; ++i) {
+    const DenseParams& x = i ? q : p;
+    if (x.K == 0 && t.plan.tile != DT_STREAM) return 1e30;  // the others want a K-tile
+    const double n = (double)x.batch * (double)ceil_div(x.M, t.plan.bm) * (double)ceil_div(x.N, t.plan.bn);
+    T[i] = (double)ceil_div(x.K, 128), work[i] = n * (t.start + t.k * T[i]) / t.slots, groups += n;
   }
-  if (t.plan.tile == DT_128x128 && groups <= kCUs) longest = 4.4 + (longest - 4.4) * (lying ? lying_k(groups) : alone_k(groups, false)) / t.k;
-  return std::max(all, longest);
+  double longest = 0.0;
+  for (int i = 0; i < 2; ++i) {
+    double k = t.k;
+    if (t.plan.tile == DT_128x128 && groups <= kCUs) k = lying ? lying_k(groups) : alone_k(groups, false);
+    // as they lie: faster while no neighbour is there (400 x 1000 x 2304's two 30 us, 512 x 8192 x 4096's 260)
+    else if (lying) k = 0.65 + 0.35 * std::min(1.0, work[1 - i] / (t.start + 0.65 * T[i]));
+    longest = std::max(longest, t.start + k * T[i]);
+  }
+  return std::max(work[0] + work[1], longest);
 }
 PairTile pair_128x128() { return {ring_plan(DT_128x128, 128, 128, kRing), 2 * kCUs, 4.4, 0.8}; }
 }  // namespace
@@ -557,6 +564,8 @@ struct BackwardPlan {
   int32_t kind;
   bool want_dx, want_dw, launch;
   bool dx_lies, dw_lies;           // on operands as they lie (launch_grad_ring, launch_grad_tiles)
+  bool dx_few;                     // on launch_grad_few, as they lie too
+  int64_t off_partial;
   int64_t off_rows, off_t, off_xt, off_wt, ws_bytes;
   View v[9];
 };
@@ -662,10 +671,11 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
   P.kind = dt == SL_F16 ? sl::EK_F16 : sl::EK_BF16;
   // Operands whose rows lie on 16-byte boundaries can be read as they are; others, and where
   // a better tile saves more than the copies (bytes read and written, at 7 TB/s as
-  // long as the caches hold them, else 4.5) cost, are copied.  us as they lie and with copies: 4000 x 500 x 3000's dx 43 and 39, 4096 x
-  // 4096 x 2048's two 281 and 248, 8 of 1024 x 1000 x 1024's two 91 and 97, 1024 x 4096 x 4096's
-  // 134 and 159, 4000 x 2000 x 3000's 194 and 207, 4096 x 8192 x 4096's 871 and 925, 1024 x 8192 x
-  // 4096's dx 160 and 219 (251 with the workspace's rows 128 bytes off powers of two).
+  // long as the caches hold them, else 4.5) cost, are copied.  us as they lie and with copies:
+  // 4000 x 500 x 3000's dx 43 and 39, 4096 x 4096 x 2048's two 281 and 248, 8 of 1024 x 1000 x
+  // 1024's two 91 and 97, 1024 x 4096 x 4096's 134 and 159, 4000 x 2000 x 3000's 194 and 207, 4096
+  // x 8192 x 4096's 871 and 925, 1024 x 8192 x 4096's dx 160 and 219 (251 with the workspace's
+  // rows 128 bytes off powers of two).
   auto copied_us = [](double bytes) { return bytes / (bytes < 1.5e8 ? 7e6 : 4.5e6); };
   auto readable = [&](const View& x, const View& y) {
     bool ok = tokens && x.rs == y.rs;
@@ -691,6 +701,22 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
     dx_ok = readable(w[WG], w[WU]);
     if (tokens) dx_copies = 8.0 * (double)weights * (double)F * (double)K;
     P.dx_lies = choose(P.dx.d, dx_ok, dx_copies, &P.dx_tile);
+    // Few rows: the weights read once (8192 x 4096's two, 134 MB in 24 to 29 us for up to 64 rows) and the
+    // workgroups' sums joined, by the same kind of model.  us so and otherwise, from Python: 1 x 8192 x
+    // 4096 31 and 69, 64 x 8192 x 4096 35 and 82, 512 x 8192 x 4096 111 and 147; 1 x 2048 x 2048 13
+    // and 17; 512 x 4096 x 8192 108 and 76; 40 x 1000 x 520 19 and 13.
+    if (dx_ok) {
+      sl::DensePlan few = {sl::DT_256x256, sl::kFewRows, 128, sl::kFewThreads, 0, 0, 0.0};
+      const double tiles = (double)n * (double)ceil_div(rows, sl::kFewRows) * (double)ceil_div(K, 128), steps = 2.0 * (double)ceil_div(F, 32);
+      const double splits = std::max(1.0, std::min(std::floor(sl::kCUs / tiles), std::floor(steps / 32)));
+      const double fm = rows <= 16 ? 1.0 : rows <= 32 ? 2.0 : 4.0;
+      const double work = std::ceil(tiles * splits / sl::kCUs) * (0.6 * fm + std::ceil(steps / (8.0 * splits)) * (0.3 + 0.3 * fm));
+      const double join = splits > 1.0 ? 3.5 + 8.0 * splits * (double)n * (double)rows * (double)K / 4e6 : 0.0;
+      few.us = 3.0 + join + std::max(work, 4.0 * (double)n * (double)F * (double)K / 5.5e6);
+      P.dx.splits = (int32_t)splits;
+      P.dx_few = few.us < P.dx_tile.us;
+      if (P.dx_few) P.dx_tile = few, P.dx_lies = true;
+    }
   }
   if (P.want_dw) {
     if ((s = product(&P.dw.d, &P.dw_tile, 2 * weights, F, K, tokens ? across : 0, Fp * across, K * across, 1)) != SL_OK) return s;
@@ -707,7 +733,7 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
     sl::DenseParams x = P.dx.d, y = P.dw.d;
     P.pair = both.us < P.dx_tile.us + P.dw_tile.us && place_tiles(&x, both, false) == SL_OK && place_tiles(&y, both, false) == SL_OK &&
              grid_fits((int64_t)x.batch * x.tiles_m * x.tiles_n + (int64_t)y.batch * y.tiles_m * y.tiles_n, 1, 1, both.threads);
-    if (P.pair) P.dx_tile = P.dw_tile = both, P.dx_lies = P.dw_lies = lying.us < copied.us;
+    if (P.pair) P.dx_tile = P.dw_tile = both, P.dx_lies = P.dw_lies = lying.us < copied.us, P.dx_few = false;
     g_msg.clear();
   }
   if (P.want_dx || P.dw_lies) P.off_rows = tokens ? take(n * rows * 2 * Fp) : 0;
@@ -717,6 +743,7 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
       for (int i = 0; i < 2; ++i) P.dx.d.b[i] = (const uint8_t*)t[WG + i]->data, P.dx.d.b_bs[i] = 2 * bstride(w[WG + i]);
       P.dx.d.b_rs[0] = 2 * w[WG].rs;
       P.dx.rows = F, P.dx.parts = 2;
+      if (P.dx_few && P.dx.splits > 1) P.off_partial = take(2 * P.dx.splits * n * rows * K);  // fp32
     } else if (tokens) {
       P.off_wt = take(weights * K * 2 * Fp);
       for (int i = 0; i < 2; ++i)
@@ -798,7 +825,11 @@ sl_status sl_gated_backward(const sl_gated_backward_args* args, void* stream) {
     return !lies ? sl::launch_gated_products(g.d, P.kind, tile, st)
                  : tile.tile == sl::DT_256x256 ? sl::launch_grad_ring(g, P.kind, across, st) : sl::launch_grad_tiles(g, P.kind, across, st);
   };
-  if (e == hipSuccess && P.want_dx && !P.pair) e = one(P.dx, P.dx_tile, P.dx_lies, false);
+  if (P.dx_few) {
+    P.dx.partial = (float*)(ws + P.off_partial);
+    if (e == hipSuccess) e = sl::launch_grad_few(P.dx, P.kind, st);
+  }
+  if (e == hipSuccess && P.want_dx && !P.pair && !P.dx_few) e = one(P.dx, P.dx_tile, P.dx_lies, false);
   if (e == hipSuccess && P.want_dw && !P.pair) e = one(P.dw, P.dw_tile, P.dw_lies, true);
   if (e != hipSuccess) return fail(SL_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
   return SL_OK;

@@ -255,6 +255,8 @@ struct GradParams {
   DenseParams d;
   int64_t rows, a_second;
   int32_t parts;
+  int32_t splits;  // launch_grad_few: workgroups that share the rows of B; more than one leave
+  float* partial;  // their sums here, [split][batch][M][N]
 };
 // x's gradient, A along its rows, by the first `first` workgroups, and the weights'
 struct GradPair {
@@ -263,6 +265,8 @@ struct GradPair {
 };
 hipError_t launch_grad_ring(const GradParams& g, int32_t kind, bool across, hipStream_t stream);  // 256 x 256 tiles
 hipError_t launch_grad_tiles(const GradParams& g, int32_t kind, bool across, hipStream_t stream); // 128 x 128 tiles
+constexpr int32_t kFewRows = 64, kFewThreads = 512;
+hipError_t launch_grad_few(const GradParams& g, int32_t kind, hipStream_t stream);  // x's, few rows: kFewRows x 128 tiles
 hipError_t launch_grad_tiles(const GradPair& g, int32_t kind, hipStream_t stream);
 
 template <int T>

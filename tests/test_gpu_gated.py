@@ -791,7 +791,7 @@ def test_a_served_block_captured(api, tokens):
         assert torch.equal(y, want)
 
 
-@pytest.mark.parametrize("shape", [(40, 100, 65), (300, 520, 264)])
+@pytest.mark.parametrize("shape", [(40, 100, 65), (300, 520, 264), (20, 2048, 2048), (1000, 2304, 2048)])
 def test_a_training_step_captured(api, shape):
     """Forward and backward in one graph, its workspaces the graph's own."""
     import torch
@@ -1105,3 +1105,43 @@ def test_gated_backward_of_a_sum(api, shape):
             for dh in (torch.ones((), device="cuda", dtype=torch.bfloat16).expand(s[0].shape),
                        s[0][..., :1, :].expand(s[0].shape)):
                 check_backward("silu", api.gated_backward(dh, *s[1:]), dh, *s[1:])
+
+
+# few rows, large weights: x's gradient straight from the weights, the rows of them shared by workgroups
+@pytest.mark.parametrize("shape", [(1, 2048, 2048), (16, 2100, 2056), (17, 4096, 1032), (33, 3001, 2312), (64, 2048, 2048), (65, 4100, 1032),
+                                   (150, 4096, 1032), (40, 8192, 4104)])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_input_gradient_of_few_rows(api, shape, dtype):
+    import torch
+    M, F, K = shape
+    s = state(1, shape, dtype, "silu")
+    got = api.gated_backward(*s, need_dw=False)
+    lies = as_they_lie(M, F)
+    assert lies < backward_workspace(api, s, got) <= lies + 16 * 4 * M * K  # sums of up to 16 workgroups, no copies
+    check_backward("silu", got, *s)
+    check_backward("silu", api.gated_backward(*s), *s)
+    for a in (api.gated_backward(*s, need_dw=False), api.gated_backward(*(strided(v, "wide") for v in s), need_dw=False)):
+        assert torch.equal(a[0], got[0])
+    out = strided(torch.zeros_like(got[0]), "sparse")
+    api.gated_backward(*s, need_dw=False, out=(out, None, None))
+    assert torch.equal(out, got[0])
+
+
+def test_input_gradient_of_few_rows_of_a_batch(api):
+    """Experts of a few rows each; weights among NaNs; integers bit for bit."""
+    import torch
+    s = state(1, (20, 1500, 2056), "bfloat16", "silu", (3,))
+    check_backward("silu", api.gated_backward(*s, need_dw=False), *s)
+    s = state(2, (7, 2048, 2056), "float16", "silu")
+    store = torch.full((2, 2300, 2200), float("nan"), dtype=torch.float16, device="cuda")
+    w = store[:, 100:2148, 64:2120]
+    w[0].copy_(s[2]), w[1].copy_(s[3])
+    s = s[:2] + (w[0], w[1]) + s[4:]
+    check_backward("silu", api.gated_backward(*s, need_dw=False), *s)
+    for M in (1, 30, 60, 100):
+        F, K = 2080, 2056
+        x, w = integers(1, -2, 2, M, K).bfloat16(), integers(2, -2, 2, 2, F, K).bfloat16()
+        g, u, dh = integers(3, -3, 3, M, F).bfloat16(), integers(4, -3, 3, M, F).bfloat16(), integers(5, -2, 2, M, F).bfloat16()
+        dg, du = (dh * u * (g > 0)).double(), (dh * g.clamp_min(0)).double()
+        dx, _, _ = api.gated_backward(dh, x, w[0], w[1], g, u, "relu", need_dw=False)
+        assert torch.equal(dx, (dg @ w[0].double() + du @ w[1].double()).float().bfloat16())
