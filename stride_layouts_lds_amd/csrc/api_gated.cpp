@@ -2,6 +2,7 @@
 // pass, of the int8 form of sl_gemm and of sl_quantize_rows.  Every check runs
 // before any HIP call.
 #include <cmath>
+#include <initializer_list>
 
 #include "api_common.hpp"
 #include "api_ops.hpp"
@@ -23,7 +24,8 @@ namespace sl {
 // int8 (256 x 256, 256 x 192, 128 x 128): 4000 x 3000 x 256 / 2064 / 8192 16 14 13, 35 33 39,
 // 83 79 93; 3000 x 3000 x 2048 31 26 29; 4096 x 6144 x 4096 100 89 96; 8192 x 8192 x 2048
 // 133 155 141.  Up to 64 rows of A go streamed whatever it says (64 x 8192 x 4096 is read at
-// 4.4 TB/s).
+// 4.4 TB/s), but up to 16 rows of few K-tiles, whose many workgroups only start and end
+// (gated, 15 of 4 x 4171 x 32: 21 us, in 128 x 128 tiles 10; 16 of 16 x 8192 x 128 47 and 22).
 //
 // A 128 x 128 tile alone on its CU waits for its copies where many K-tiles meet many
 // others': the deep ring has two K-tiles more on their way (gated bf16 512 x 1024 x 4096 33 ->
@@ -48,11 +50,6 @@ static double dense_large_us(int64_t batch, int64_t M, int64_t N, int64_t K) {
 DensePlan dense_plan(bool gated, int64_t batch, int64_t M, int64_t N, int64_t K) {
   using host::ceil_div;
   const int64_t B = gated ? 2 * N : N;  // rows of B: a gated tile's columns of the result are half of its rows of B
-  if (M <= 16) {
-    const int32_t bn = gated || batch * ceil_div(N, 32) >= kCUs ? 32 : 16;
-    const double rounds = (double)batch * (double)ceil_div(B, bn) / (2.0 * kCUs);  // two workgroups to a CU
-    return {DT_SKINNY, 16, bn, kDenseSkinnyWaves * 64, kDenseSkinnyWaves * bn / 16 * 1024, 0, std::ceil(rounds) * (3.0 + 0.1 * (double)ceil_div(K, 128))};
-  }
   const double T = (double)ceil_div(K, 128);
   const int32_t bm = M <= 32 ? 32 : 64;
   const int32_t bn = batch * ceil_div(M, bm) * ceil_div(B, 64) >= kCUs ? 64 : 32;
@@ -60,7 +57,12 @@ DensePlan dense_plan(bool gated, int64_t batch, int64_t M, int64_t N, int64_t K)
   DensePlan best = {DT_STREAM, bm, bn, kDenseStreamWaves * 64, kDenseStreamWaves * stages * (bm + bn) * 128, stages, 0.0};
   const double groups = (double)batch * (double)ceil_div(M, bm) * (double)ceil_div(B, bn);
   best.us = std::ceil(groups / kCUs) * (5.0 + T * (bn == 64 ? 0.2 : 0.13));
-  if (M <= 64 || K == 0) return best;
+  if (M <= 16) {
+    const int32_t cols = gated || batch * ceil_div(N, 32) >= kCUs ? 32 : 16;
+    const double rounds = (double)batch * (double)ceil_div(B, cols) / (2.0 * kCUs);  // two workgroups to a CU
+    best = {DT_SKINNY, 16, cols, kDenseSkinnyWaves * 64, kDenseSkinnyWaves * cols / 16 * 1024, 0, std::ceil(rounds) * (3.0 + 0.1 * T)};
+  }
+  if (K == 0 || (M <= 64 && (best.tile == DT_STREAM || T > 4))) return best;
   auto tiles = [&](int64_t rows_a, int64_t rows_b) { return (double)batch * (double)ceil_div(M, rows_a) * (double)ceil_div(B, rows_b); };
   const double t2 = tiles(128, 128);
   const bool deep = t2 <= kCUs && t2 * T >= 3500.0;
@@ -139,6 +141,17 @@ static bool rows_ready(const View& v, int64_t batch, int64_t es) {
 static bool quad_rows(const View& v, int64_t batch) {
   return v.cs == 1 && (v.rows <= 1 || v.rs % 4 == 0) && (uintptr_t)v.t->data % (4 * elem_size(v.t->dtype)) == 0 &&
          (batch <= 1 || batch_stride(v) % 4 == 0);
+}
+
+// how a product's kernel may write (and read C) along the rows of these, all of one type
+static int32_t row_flags(std::initializer_list<const View*> outs, int64_t batch) {
+  bool rows = true, four = true, eight = true;
+  for (const View* v : outs) {
+    rows = rows && v->cs == 1, four = four && quad_rows(*v, batch);
+    eight = eight && elem_size(v->t->dtype) == 2 && (v->rows <= 1 || v->rs % 8 == 0) && (uintptr_t)v->t->data % 16 == 0 &&
+            (batch <= 1 || batch_stride(*v) % 8 == 0);
+  }
+  return !rows ? 0 : DF_ROWS | (four ? DF_ROWS4 : 0) | (four && eight ? DF_ROWS8 : 0);
 }
 
 // one scale per row: (batch?, rows, 1) f32
@@ -227,7 +240,7 @@ sl_status plan_int8(const sl_gemm_args* args, RowsPlan* out) {
   p.d_rs = D.rs, p.d_cs = D.cs, p.d_bs = batch_stride(D);
   p.type = type, p.batch = (int32_t)batch;
   p.flags = (quad_rows(D, batch) ? DF_D_VEC : 0) | (has_c && quad_rows(C, batch) ? DF_C_VEC : 0) |
-            (D.cs == 1 && (!has_c || C.cs == 1) ? DF_ROWS : 0);
+            row_flags({&D, has_c ? &C : &D}, batch);
   P.tile = dense_plan(false, batch, M, N, K);
   if ((s = place_tiles(&p, P.tile, false)) != SL_OK) return s;
   P.pub.a_load = P.pub.b_load = LOAD_KVEC;
@@ -504,7 +517,7 @@ sl_status plan_gated(const sl_gated_args* args, GatedPlan* out) {
   }
   p.d = args->h.data, p.d_rs = w[H].rs, p.d_cs = w[H].cs, p.d_bs = bstride(w[H]);
   p.flags = quad_rows(w[H], p.batch) ? sl::DF_D_VEC : 0;
-  if (w[H].cs == 1 && (!keep || (w[G].cs == 1 && w[U].cs == 1))) p.flags |= sl::DF_ROWS;
+  p.flags |= row_flags({&w[H], &w[keep ? G : H], &w[keep ? U : H]}, p.batch);
   if (keep)
     for (int i = 0; i < 2; ++i) {
       const View& k = w[G + i];
@@ -750,7 +763,7 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
         if ((s = transpose(&P.prepare.pack[1 + i], w[WG + i], weights, Fp, K * 2 * Fp, 2 * Fp)) != SL_OK) return s;
     }
     output(&P.dx.d, 0, args->dx, w[DX], n);
-    if (w[DX].cs == 1) P.dx.d.flags |= sl::DF_ROWS;
+    P.dx.d.flags |= row_flags({&w[DX]}, n);
   }
   if (P.want_dw) {
     if ((s = place_tiles(&P.dw.d, P.dw_tile, false)) != SL_OK) return s;
@@ -766,7 +779,7 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
       if ((s = transpose(&P.prepare.pack[0], w[X], n, Mp, one_weight ? Mp : K * Mp, across)) != SL_OK) return s;
     }
     for (int i = 0; i < 2; ++i) output(&P.dw.d, i, *t[DWG + i], v[DWG + i], weights);
-    if (v[DWG].cs == 1 && v[DWU].cs == 1) P.dw.d.flags |= sl::DF_ROWS;
+    P.dw.d.flags |= row_flags({&v[DWG], &v[DWU]}, weights);
   }
   if (!grid_fits(sl::gated_prepare_groups(&P.prepare), 1, 1, sl::kPrepareThreads)) return fail(SL_ERR_SHAPE, "the operands are too large");
   return SL_OK;

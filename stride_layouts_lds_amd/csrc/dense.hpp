@@ -228,47 +228,60 @@ __device__ __forceinline__ floatx4 dense_load(const void* base, int32_t type, in
   return v;
 }
 
-// Eight values of a contiguous row, at any alignment of their type.
-template <int OT>
-__device__ __forceinline__ void dense_store8(void* at, const float (&v)[8]) {
-  typedef uint16_t halves __attribute__((ext_vector_type(8), aligned(2)));
-  typedef float floats __attribute__((ext_vector_type(4), aligned(4)));
-  if constexpr (OT == OT_F32) {
-    *(floats*)at = floats{v[0], v[1], v[2], v[3]};
-    *((floats*)at + 1) = floats{v[4], v[5], v[6], v[7]};
+// V consecutive values of a row that starts on a boundary of V of them (16-bit types: one,
+// four or eight; fp32: one or four).
+template <int OT, int V>
+__device__ __forceinline__ void dense_store_cols(void* at, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    if constexpr (OT == OT_F32) *(float*)at = v[0];
+    else *(uint16_t*)at = from_f32<OT == OT_F16 ? DT_F16 : DT_BF16>(v[0]);
+  } else if constexpr (OT == OT_F32) {
+    typedef float floats __attribute__((ext_vector_type(V)));
+    floats w;
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] = v[e];
+    *(floats*)at = w;
   } else {
+    typedef uint16_t halves __attribute__((ext_vector_type(V)));
     halves w;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = from_f32<OT == OT_F16 ? DT_F16 : DT_BF16>(v[e]);
+    for (int e = 0; e < V; ++e) w[e] = from_f32<OT == OT_F16 ? DT_F16 : DT_BF16>(v[e]);
     *(halves*)at = w;
   }
 }
-template <int OT>
-__device__ __forceinline__ void dense_load8(const void* at, float (&v)[8]) {
-  typedef uint16_t halves __attribute__((ext_vector_type(8), aligned(2)));
-  typedef float floats __attribute__((ext_vector_type(4), aligned(4)));
-  if constexpr (OT == OT_F32) {
-    const floats a = *(const floats*)at, b = *((const floats*)at + 1);
+template <int OT, int V>
+__device__ __forceinline__ void dense_load_cols(const void* at, float (&v)[V]) {
+  if constexpr (V == 1) {
+    if constexpr (OT == OT_F32) v[0] = *(const float*)at;
+    else v[0] = to_f32<OT == OT_F16 ? DT_F16 : DT_BF16>(*(const uint16_t*)at);
+  } else if constexpr (OT == OT_F32) {
+    typedef float floats __attribute__((ext_vector_type(V)));
+    const floats w = *(const floats*)at;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+    for (int e = 0; e < V; ++e) v[e] = w[e];
   } else {
+    typedef uint16_t halves __attribute__((ext_vector_type(V)));
     const halves w = *(const halves*)at;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = to_f32<OT == OT_F16 ? DT_F16 : DT_BF16>(w[e]);
+    for (int e = 0; e < V; ++e) v[e] = to_f32<OT == OT_F16 ? DT_F16 : DT_BF16>(w[e]);
   }
 }
 
-// A wave's 64 x COLS block of sums (COLS = 128 or 64) from its region of LDS,
-// in the chunk order of rows_chunk, row after row: whole rows of the block are
-// stored together.  GATED: the first half of the columns are g, the others u.
+// A wave's 64 x COLS block of sums (COLS = 128, 96 or 64) from its region of LDS,
+// in the chunk order of rows_chunk (96 columns in rows of 128), row after row: whole
+// rows of the block are stored together.  GATED: the first half of the columns are
+// g, the others u.
 //
-// Contiguous outputs (DF_ROWS) go eight columns a lane: EPI::rows<RPI>(batch, m,
-// n, count, get) finishes columns n .. n + 7 of rows m, m + RPI, ... as far as
-// `count` of them, get(it, s, v) being the sums of the it-th, s 0: g or the
-// product's, 1: u.  (A wave's LDS reads pair lanes 0-7 with 16-23, 8-15 with 24-31 and so
-// on; where eight lanes have a row, the rows of a pair differ in the lowest bit, so that
-// their chunks, all even or all odd in a row, lie on different banks.)  Others,
-// and the columns next to N where those are no eight: EPI::finish.
+// Contiguous outputs go V columns a lane: EPI::rows<RPI, V>(batch, m, n, count, get)
+// finishes columns n .. n + V - 1 of rows m, m + RPI, ... as far as `count` of
+// them, get(it, s, v) being the sums of the it-th, s 0: g or the product's, 1: u.
+// V is eight (DF_ROWS8) or four (DF_ROWS4) where every row starts on a boundary of so many,
+// else one (DF_ROWS): an access off its boundaries is taken apart by the hardware (us, int8 528
+// x 870 x 48 + C 20 by eights and 8 by ones; 528 x 868 x 48, rows on 8 bytes, 12 by eights, 8 by
+// ones, 7 by fours; 4000 x 3004 x 2064 + C 66, 47 and 40).  (Of eights, where eight lanes have a row, a wave's LDS reads pair lanes 0-7 with 16-23, 8-15 with 24-31 and so
+// on: the rows of a pair differ in the lowest bit, so that their chunks, all even or all
+// odd in a row, lie on different banks.)  Other outputs, and the columns next to N
+// where those are no V: EPI::finish.
 template <int COLS>
 constexpr int kRowsPitch = COLS == 96 ? 128 : COLS;
 template <int EK, bool GATED, int COLS, class EPI>
@@ -277,32 +290,52 @@ __device__ __forceinline__ void dense_rows(const EPI& epi, const DenseParams& p,
   static_assert(!GATED || COLS != 96, "halves of whole lanes");
   constexpr int OUT = GATED ? COLS / 2 : COLS;  // columns of the result
   constexpr int PITCH = kRowsPitch<COLS>;
-  constexpr int LPR = (GATED ? PITCH / 2 : PITCH) / 8, RPI = 64 / LPR;  // lanes to a row (of 96 columns: four of them idle), rows at once
-  const int32_t group = lane / LPR, l = lane % LPR;
-  // (the row bit that pairs of lane groups differ in goes last)
-  const int32_t r0 = LPR == 8 ? (group & 4) | (group & 1) << 1 | (group & 2) >> 1 : group;
-  const int64_t m = m_base + r0, n = n_base + 8 * l;
   auto quad = [&](int32_t r, int32_t q) { return dense_value<EK>(*(const floatx4*)(region + rows_chunk<PITCH>(r, q))); };
-  const int32_t count = m < p.M ? (int32_t)(p.M - m > 64 ? 64 / RPI : (p.M - m + RPI - 1) / RPI) : 0;
-  if (n >= p.N || count == 0 || l >= OUT / 8) return;
-  if (p.flags & DF_ROWS && n + 8 <= p.N) {
-    auto get = [&](int32_t it, int s, float(&v)[8]) {
-      const int32_t r = RPI * it + r0, q = 2 * l + (s ? OUT / 4 : 0);
-      const floatx4 a = quad(r, q), b = quad(r, q + 1);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
-    };
-    epi.template rows<RPI>(p, batch, m, n, count, get);
-    return;
-  }
+  auto by = [&](auto columns, bool whole) {
+    constexpr int V = decltype(columns)::value;
+    constexpr int PAD = GATED ? PITCH / 2 : PITCH;  // (of 96 columns a quarter of the lanes is idle)
+    constexpr int LPR = PAD / V < 64 ? PAD / V : 64, RPI = 64 / LPR;  // lanes to a row, rows at once
+    const int32_t group = lane / LPR;
+    // (the row bit that pairs of lane groups differ in goes last)
+    const int32_t r0 = V == 8 && LPR == 8 ? (group & 4) | (group & 1) << 1 | (group & 2) >> 1 : group;
+    const int64_t m = m_base + r0;
+    const int32_t count = m < p.M ? (int32_t)(p.M - m > 64 ? 64 / RPI : (p.M - m + RPI - 1) / RPI) : 0;
 #pragma unroll 1
-  for (int it = 0; it < 2 * count; ++it) {
-    const int32_t r = RPI * (it / 2) + r0, q = 2 * l + it % 2;
-    const int64_t nq = n + 4 * (it % 2);
-    if (nq >= p.N) continue;
-    if constexpr (GATED) epi.finish(p, batch, m_base + r, nq, quad(r, q), quad(r, q + OUT / 4));
-    else epi.finish(p, batch, m_base + r, nq, quad(r, q));
-  }
+    for (int32_t c = V * (lane % LPR); c < OUT; c += V * LPR) {
+      const int64_t n = n_base + c;
+      if (n >= p.N || count == 0) return;
+      if (whole && n + V <= p.N) {
+        auto get = [&](int32_t it, int s, float(&v)[V]) {
+          const int32_t r = RPI * it + r0, at = c + (s ? OUT : 0);
+          if constexpr (V == 1) {
+            const char* from = region + rows_chunk<PITCH>(r, at / 4) + 4 * (at % 4);
+            if constexpr (EK == EK_I8) v[0] = (float)*(const int32_t*)from;
+            else v[0] = *(const float*)from;
+          } else {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+              const floatx4 a = quad(r, at / 4 + i);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[4 * i + e] = a[e];
+            }
+          }
+        };
+        epi.template rows<RPI, V>(p, batch, m, n, count, get);
+      } else if constexpr (V > 1) {
+#pragma unroll 1
+        for (int it = 0; it < V / 4 * count; ++it) {
+          const int32_t r = RPI * (it / (V / 4)) + r0, q = c / 4 + it % (V / 4);
+          const int64_t nq = n + 4 * (it % (V / 4));
+          if (nq >= p.N) continue;
+          if constexpr (GATED) epi.finish(p, batch, m_base + r, nq, quad(r, q), quad(r, q + OUT / 4));
+          else epi.finish(p, batch, m_base + r, nq, quad(r, q));
+        }
+      }
+    }
+  };
+  if (p.flags & DF_ROWS8) by(std::integral_constant<int, 8>{}, true);
+  else if ((p.flags & (DF_ROWS | DF_ROWS4)) == DF_ROWS) by(std::integral_constant<int, 1>{}, true);
+  else by(std::integral_constant<int, 4>{}, p.flags & DF_ROWS4);
 }
 
 // ---------------------------------------------------------------------------

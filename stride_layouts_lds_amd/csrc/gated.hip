@@ -39,15 +39,15 @@ struct Gate {
     for (int r = 0; r < 4; ++r) h[r] = activate(p.act, g[r]) * u[r];
     dense_store(p.d, p.type, batch * p.d_bs + m * p.d_rs + n * p.d_cs, p.d_cs, p.flags & DF_D_VEC, valid, h);
   }
-  template <int OT, int ACT, int RPI, class GET>
+  template <int OT, int ACT, int RPI, int V, class GET>
   __device__ __forceinline__ void rows_of(const DenseParams& p, int64_t batch, int64_t m, int64_t n, int32_t count, const GET& get) const {
     typedef typename OrthoElem<OT>::type E;
-    float bg[8], bu[8];
+    float bg[V], bu[V];
     const float* a = nullptr;
     if constexpr (SCALED) {
       a = sa + m * p.sa_rs;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) bg[e] = sg[(n + e) * p.sb_rs[0]], bu[e] = su[(n + e) * p.sb_rs[1]];
+      for (int e = 0; e < V; ++e) bg[e] = sg[(n + e) * p.sb_rs[0]], bu[e] = su[(n + e) * p.sb_rs[1]];
     }
     E* d = (E*)p.d + batch * p.d_bs + m * p.d_rs + n;
     const bool keep = p.kept[0];
@@ -55,42 +55,42 @@ struct Gate {
     E* ku = (E*)p.kept[1] + batch * p.kept_bs[1] + m * p.kept_rs[1] + n;
 #pragma unroll 2
     for (int it = 0; it < count; ++it) {
-      float g[8], u[8], h[8];
+      float g[V], u[V], h[V];
       get(it, 0, g);
       get(it, 1, u);
       if constexpr (SCALED) {
         const float as = *a;
         a += RPI * p.sa_rs;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = g[e] * as * bg[e], u[e] = u[e] * as * bu[e];
+        for (int e = 0; e < V; ++e) g[e] = g[e] * as * bg[e], u[e] = u[e] * as * bu[e];
       }
       if (keep) {
-        dense_store8<OT>(kg, g);
-        dense_store8<OT>(ku, u);
+        dense_store_cols<OT, V>(kg, g);
+        dense_store_cols<OT, V>(ku, u);
         kg += RPI * p.kept_rs[0], ku += RPI * p.kept_rs[1];
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = activate(ACT, g[e]) * u[e];
-      dense_store8<OT>(d, h);
+      for (int e = 0; e < V; ++e) h[e] = activate(ACT, g[e]) * u[e];
+      dense_store_cols<OT, V>(d, h);
       d += RPI * p.d_rs;
     }
   }
-  template <int OT, int RPI, class GET>
+  template <int OT, int RPI, int V, class GET>
   __device__ __forceinline__ void rows_by_act(const DenseParams& p, int64_t batch, int64_t m, int64_t n, int32_t count, const GET& get) const {
     switch (p.act) {
-      case ACT_SILU: rows_of<OT, ACT_SILU, RPI>(p, batch, m, n, count, get); break;
-      case ACT_GELU: rows_of<OT, ACT_GELU, RPI>(p, batch, m, n, count, get); break;
-      case ACT_GELU_TANH: rows_of<OT, ACT_GELU_TANH, RPI>(p, batch, m, n, count, get); break;
-      default: rows_of<OT, ACT_RELU, RPI>(p, batch, m, n, count, get);
+      case ACT_SILU: rows_of<OT, ACT_SILU, RPI, V>(p, batch, m, n, count, get); break;
+      case ACT_GELU: rows_of<OT, ACT_GELU, RPI, V>(p, batch, m, n, count, get); break;
+      case ACT_GELU_TANH: rows_of<OT, ACT_GELU_TANH, RPI, V>(p, batch, m, n, count, get); break;
+      default: rows_of<OT, ACT_RELU, RPI, V>(p, batch, m, n, count, get);
     }
   }
-  template <int RPI, class GET>
+  template <int RPI, int V, class GET>
   __device__ __forceinline__ void rows(const DenseParams& p, int64_t batch, int64_t m, int64_t n, int32_t count, const GET& get) const {
-    if constexpr (EK == EK_F16) rows_by_act<OT_F16, RPI>(p, batch, m, n, count, get);
-    else if constexpr (EK == EK_BF16) rows_by_act<OT_BF16, RPI>(p, batch, m, n, count, get);
-    else if (p.type == OT_F16) rows_by_act<OT_F16, RPI>(p, batch, m, n, count, get);
-    else if (p.type == OT_F32) rows_by_act<OT_F32, RPI>(p, batch, m, n, count, get);
-    else rows_by_act<OT_BF16, RPI>(p, batch, m, n, count, get);
+    if constexpr (EK == EK_F16) rows_by_act<OT_F16, RPI, V>(p, batch, m, n, count, get);
+    else if constexpr (EK == EK_BF16) rows_by_act<OT_BF16, RPI, V>(p, batch, m, n, count, get);
+    else if (p.type == OT_F16) rows_by_act<OT_F16, RPI, V>(p, batch, m, n, count, get);
+    else if (p.type == OT_BF16) rows_by_act<OT_BF16, RPI, V>(p, batch, m, n, count, get);
+    else if constexpr (V < 8) rows_by_act<OT_F32, RPI, V>(p, batch, m, n, count, get);  // (DF_ROWS8 is of 16-bit types)
   }
 };
 

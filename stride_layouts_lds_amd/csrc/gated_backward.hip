@@ -23,14 +23,14 @@ struct Gradient {
     const int64_t off = (batch >> p.b_shift) * p.kept_bs[s] + m * p.kept_rs[s] + n * p.kept_cs[s];
     dense_store(p.kept[s], OT, off, p.kept_cs[s], s ? p.flags & (2 * DF_KEPT_VEC) : p.flags & DF_KEPT_VEC, p.N - n, v);
   }
-  template <int RPI, class GET>
+  template <int RPI, int V, class GET>
   __device__ __forceinline__ void rows(const DenseParams& p, int64_t batch, int64_t m, int64_t n, int32_t count, const GET& get) const {
     uint16_t* d = (uint16_t*)p.kept[s] + (batch >> p.b_shift) * p.kept_bs[s] + m * p.kept_rs[s] + n;
 #pragma unroll 4
     for (int it = 0; it < count; ++it) {
-      float v[8];
+      float v[V];
       get(it, 0, v);
-      dense_store8<OT>(d, v);
+      dense_store_cols<OT, V>(d, v);
       d += RPI * p.kept_rs[s];
     }
   }

@@ -26,12 +26,58 @@ struct ScaledSum {
     }
     dense_store(p.d, p.type, batch * p.d_bs + m * p.d_rs + n * p.d_cs, p.d_cs, p.flags & DF_D_VEC, valid, v);
   }
-  template <int OT, bool HAS_C, int RPI, class GET>
-  __device__ __forceinline__ void rows_of(const DenseParams& p, int64_t batch, int64_t m, int64_t n, int32_t count, const GET& get) const {
-    typedef typename OrthoElem<OT>::type E;
-    float b[8];
+  // V values of a row as they are stored.  (Where V is eight fp16 and bf16 each have their copy of
+  // the code; otherwise ANY16 is either: with copies of all of it the kernel's
+  // registers went to memory, and told apart row by row eights take 2 of 33 us more, 4000 x
+  // 3000 x 2064 + C.)
+  static constexpr int ANY16 = -1;
+  template <int OT, int V>
+  struct Stored {
+    static constexpr bool F32 = OT == OT_F32;
+    typedef typename std::conditional<F32, float, uint16_t>::type E;
+    typedef E vec __attribute__((ext_vector_type(V == 1 ? 2 : V)));
+    vec w;
+    __device__ __forceinline__ void load(const E* at) {
+      if constexpr (V == 1) w[0] = *at;
+      else w = *(const vec*)at;
+    }
+    __device__ __forceinline__ void store(E* at) const {
+      if constexpr (V == 1) *at = w[0];
+      else *(vec*)at = w;
+    }
+    template <int DT>
+    __device__ __forceinline__ void add_as(float (&v)[V]) const {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) b[e] = sb[(n + e) * p.sb_rs[0]];
+      for (int e = 0; e < V; ++e) {
+        if constexpr (F32) v[e] += w[e];
+        else v[e] += to_f32<DT>((uint16_t)w[e]);
+      }
+    }
+    template <int DT>
+    __device__ __forceinline__ void set_as(const float (&v)[V]) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if constexpr (F32) w[e] = v[e];
+        else w[e] = from_f32<DT>(v[e]);
+      }
+    }
+    __device__ __forceinline__ void add_to(float (&v)[V], bool bf16) const {
+      if (OT == OT_BF16 || (OT == ANY16 && bf16)) add_as<DT_BF16>(v);
+      else add_as<DT_F16>(v);
+    }
+    __device__ __forceinline__ void set(const float (&v)[V], bool bf16) {
+      if (OT == OT_BF16 || (OT == ANY16 && bf16)) set_as<DT_BF16>(v);
+      else set_as<DT_F16>(v);
+    }
+  };
+  template <int OT, bool HAS_C, int RPI, int V, class GET>
+  __device__ __forceinline__ void rows_of(const DenseParams& p, int64_t batch, int64_t m, int64_t n, int32_t count, const GET& get) const {
+    typedef Stored<OT, V> S;
+    typedef typename S::E E;
+    const bool bf16 = p.type == OT_BF16;
+    float b[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) b[e] = sb[(n + e) * p.sb_rs[0]];
     E* d = (E*)p.d + batch * p.d_bs + m * p.d_rs + n;
     const E* c = HAS_C ? (const E*)p.c + batch * p.c_bs + m * p.c_rs + n : nullptr;
     const float* a = sa + m * p.sa_rs;
@@ -39,19 +85,24 @@ struct ScaledSum {
     // other each waited for memory (4000 x 3000 x 2064 + C: 12 of 48 us)
     auto some = [&](int32_t it0, auto many) {
       constexpr int N = decltype(many)::value;
-      float as[N], w[HAS_C ? N : 1][8];
+      float as[N];
+      S w[HAS_C ? N : 1];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         as[i] = a[(it0 + i) * RPI * p.sa_rs];
-        if constexpr (HAS_C) dense_load8<OT>(c + (it0 + i) * RPI * p.c_rs, w[i]);
+        if constexpr (HAS_C) w[i].load(c + (it0 + i) * RPI * p.c_rs);
       }
+      if constexpr (HAS_C) __builtin_amdgcn_sched_barrier(0);  // (or each load moves next to its use)
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        float v[8];
+        float v[V];
+        S out;
         get(it0 + i, 0, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = HAS_C ? v[e] * as[i] * b[e] + w[HAS_C ? i : 0][e] : v[e] * as[i] * b[e];
-        dense_store8<OT>(d, v);
+        for (int e = 0; e < V; ++e) v[e] = v[e] * as[i] * b[e];
+        if constexpr (HAS_C) w[i].add_to(v, bf16);
+        out.set(v, bf16);
+        out.store(d);
         d += RPI * p.d_rs;
       }
     };
@@ -61,16 +112,20 @@ struct ScaledSum {
 #pragma unroll 1
     for (; it < count; ++it) some(it, std::integral_constant<int, 1>{});
   }
-  template <int OT, int RPI, class GET>
+  template <int OT, int RPI, int V, class GET>
   __device__ __forceinline__ void rows_to(const DenseParams& p, int64_t batch, int64_t m, int64_t n, int32_t count, const GET& get) const {
-    if (p.c) rows_of<OT, true, RPI>(p, batch, m, n, count, get);
-    else rows_of<OT, false, RPI>(p, batch, m, n, count, get);
+    if (p.c) rows_of<OT, true, RPI, V>(p, batch, m, n, count, get);
+    else rows_of<OT, false, RPI, V>(p, batch, m, n, count, get);
   }
-  template <int RPI, class GET>
+  template <int RPI, int V, class GET>
   __device__ __forceinline__ void rows(const DenseParams& p, int64_t batch, int64_t m, int64_t n, int32_t count, const GET& get) const {
-    if (p.type == OT_F16) rows_to<OT_F16, RPI>(p, batch, m, n, count, get);
-    else if (p.type == OT_BF16) rows_to<OT_BF16, RPI>(p, batch, m, n, count, get);
-    else rows_to<OT_F32, RPI>(p, batch, m, n, count, get);
+    if constexpr (V == 8) {  // (DF_ROWS8 is of 16-bit types)
+      if (p.type == OT_F16) rows_to<OT_F16, RPI, V>(p, batch, m, n, count, get);
+      else rows_to<OT_BF16, RPI, V>(p, batch, m, n, count, get);
+    } else {
+      if (p.type == OT_F32) rows_to<OT_F32, RPI, V>(p, batch, m, n, count, get);
+      else rows_to<ANY16, RPI, V>(p, batch, m, n, count, get);
+    }
   }
 };
 

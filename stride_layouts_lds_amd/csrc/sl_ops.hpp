@@ -174,6 +174,8 @@ constexpr int32_t DF_D_VEC = 1;     // four consecutive n of D in one aligned ac
 constexpr int32_t DF_C_VEC = 2;     // ... of C
 constexpr int32_t DF_KEPT_VEC = 4;  // ... of g, and 8: of u
 constexpr int32_t DF_ROWS = 16;     // the columns of C and of every output contiguous
+constexpr int32_t DF_ROWS4 = 32;    // ... and rows of them start on boundaries of four
+constexpr int32_t DF_ROWS8 = 64;    // ... of eight, and are of 16-bit types
 
 // tile configurations: rows of A x rows of B (for the gated pair, of both
 // matrices together)

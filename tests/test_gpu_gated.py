@@ -1145,3 +1145,35 @@ def test_input_gradient_of_few_rows_of_a_batch(api):
         dg, du = (dh * u * (g > 0)).double(), (dh * g.clamp_min(0)).double()
         dx, _, _ = api.gated_backward(dh, x, w[0], w[1], g, u, "relu", need_dw=False)
         assert torch.equal(dx, (dg @ w[0].double() + du @ w[1].double()).float().bfloat16())
+
+
+# how results are written: by eights, fours and single columns, and what is left of a row
+@pytest.mark.parametrize("N", [129, 130, 132, 136, 267, 1036])
+@pytest.mark.parametrize("how", ["rows", "wide", "padded", "sparse"])
+def test_result_rows(api, N, how):
+    import torch
+    M, K = 300, 272
+    a, b, sa, sb = codes(1, M, K), codes(2, N, K), scales(3, M), scales(4, N)
+    for dtype in ("float16", "bfloat16", "float32"):
+        t = dtype_of(dtype)
+        c = strided(normal(5, M, N).to(t), how)
+        for given in (None, c):
+            out = strided(torch.full((M, N), 9, dtype=t, device="cuda"), how)
+            check_int8(api, a, b, sa, sb, given, dtype, out=out)
+    x, wg, wu = block(6, (M, N, K), "bfloat16")
+    outs = tuple(strided(torch.full((M, N), 9, dtype=torch.bfloat16, device="cuda"), how) for _ in range(3))
+    check_gated("gelu", api.gated(x, wg, wu, "gelu", keep=True, out=outs), x, wg, wu)
+    check_gated("gelu", api.gated(x, wg, wu, "gelu"), x, wg, wu)
+    s = state(7, (M, 200, N), "float16", "silu")
+    outs = tuple(strided(torch.full_like(v, 9), how) for v in s[1:4])
+    check_backward("silu", api.gated_backward(*s, out=outs), *s)
+
+
+@pytest.mark.parametrize("K", [30, 64, 128, 200])
+def test_many_experts_of_few_rows(api, K):
+    """Few K-tiles and many matrices: larger tiles than few rows alone would take."""
+    x, wg, wu = block(1, (4, 4171, K), "float16", (15,))
+    check_gated("silu", api.gated(x, wg, wu, keep=True), x, wg, wu)
+    n = -(-K // 16) * 16
+    a, b = codes(1, 15, 16, n), codes(2, 15, 5000, n)
+    check_int8(api, a, b, scales(3, 15, 16), scales(4, 15, 5000))
