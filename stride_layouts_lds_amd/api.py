@@ -543,7 +543,7 @@ def _activation(name: str) -> int:
 def _run_with_workspace(name: str, operands, tail: int, workspace, often: bool, device, stream: Optional[int]) -> None:
     """Entry point ``name`` on the operands' descriptors and ``tail``'s first
     field.  Without the caller's workspace its bytes are asked for, unless most
-    plans need none (not ``often``) and the call goes through without."""
+    such plans need none (not ``often``) and the call goes through without."""
     records = b"".join([_record(t) for t in operands])
     index = _one_device(*operands, workspace)
     if workspace is None:
@@ -616,7 +616,8 @@ def gated(x, w_gate, w_up, activation: str = "silu", sx=None, s_gate=None, s_up=
         if len(out) != (3 if keep else 1):
             raise ValueError(f"out holds {len(out)} tensors, 3 are written")
     operands = (x, w_gate, w_up, sx, s_gate, s_up) + out + (() if keep else (None, None))
-    _run_with_workspace("sl_gated", operands, act, workspace, False, x.device, stream)
+    copies = x.shape[-1] % 8 != 0 and x.dtype != torch.int8  # of all operands (others may want some too)
+    _run_with_workspace("sl_gated", operands, act, workspace, copies, x.device, stream)
     return out if keep else out[0]
 
 
