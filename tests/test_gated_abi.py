@@ -396,3 +396,28 @@ def test_python_refuses(api):  # noqa: F811
             api.gated_backward(kept, h, w, w, kept, kept, out=out)
     with pytest.raises(TypeError):
         api.quantize_rows(torch.zeros(4, 128, dtype=torch.float64))
+
+
+def test_operands_of_another_device_are_refused(api, monkeypatch):  # noqa: F811
+    """The call runs on the current device's stream: an operand of another one's memory
+    would fault the GPU."""
+    import torch
+
+    class Operand:
+        is_cuda = True
+
+        def __init__(self, index):
+            self.index, self.device = index, f"cuda:{index}"
+
+        def get_device(self):
+            return self.index
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    assert api._one_device(Operand(1), None, Operand(1)) == 1
+    for operands in ((Operand(0),), (Operand(1), Operand(0)), (None, Operand(2), Operand(1))):
+        with pytest.raises(ValueError, match="the current device is cuda:1"):
+            api._one_device(*operands)
+    monkeypatch.delattr(torch._C, "_cuda_getDevice")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    assert api._one_device(Operand(3)) == 3
+    # descriptors alone: nothing to check
+    assert api._one_device(None, api.sl_tensor()) is None
