@@ -1177,3 +1177,21 @@ def test_many_experts_of_few_rows(api, K):
     n = -(-K // 16) * 16
     a, b = codes(1, 15, 16, n), codes(2, 15, 5000, n)
     check_int8(api, a, b, scales(3, 15, 16), scales(4, 15, 5000))
+
+
+def test_input_gradient_of_few_rows_of_shared_weights(api):
+    """Sequences that share their weights, as one matrix of all rows and as rows apart."""
+    import torch
+    s = state(1, (20, 2048, 2056), "bfloat16", "gelu", (3,), shared=True)
+    got = api.gated_backward(*s, "gelu", need_dw=False)
+    check_backward("gelu", got, *s)
+    apart = [torch.zeros((3, 24, v.shape[2]), dtype=v.dtype, device="cuda")[:, 1:21] for v in (s[0], s[1], s[4], s[5])]
+    for a, v in zip(apart, (s[0], s[1], s[4], s[5])):
+        a.copy_(v)
+    t = (apart[0], apart[1], s[2], s[3], apart[2], apart[3])
+    check_backward("gelu", api.gated_backward(*t, "gelu", need_dw=False), *s)
+    check_backward("gelu", api.gated_backward(*t, "gelu"), *s)
+    out = torch.full((3, 30, 2056), 7, dtype=s[1].dtype, device="cuda")
+    api.gated_backward(*t, "gelu", need_dw=False, out=(out[:, 5:25], None, None))
+    check_backward("gelu", (out[:, 5:25], None, None), *s)
+    assert (out[:, :5] == 7).all() and (out[:, 25:] == 7).all()
