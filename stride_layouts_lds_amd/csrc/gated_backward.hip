@@ -541,9 +541,9 @@ __global__ __launch_bounds__(256, 2) void grad_pair_kernel(const GradPair g) {
 }
 
 // x's gradient of few rows, 16 FM to a tile: the weights are read as they lie, from
-// memory once, and bound the call.  A wave takes 32 rows of a weight and 128 of its columns straight into
-// registers, a lane eight values of each of eight rows: turned within the lane,
-// eight fragments (fragment j holds columns j, 8 + j, 16 + j, ...), so that neither LDS nor
+// memory once, and bound the call.  A wave takes 32 rows of a weight and 128 of its
+// columns straight into registers, a lane eight values of each of eight rows: turned
+// within the lane, eight fragments (fragment j holds columns j, 8 + j, 16 + j, ...), so that neither LDS nor
 // copies are needed.  The eight waves of a workgroup and `splits` workgroups share the
 // rows; waves' sums meet in LDS, workgroups' in the workspace (grad_few_join_kernel), always
 // in one order.  Two weights of 8192 x 4096 (134 MB) for one row: 24 us, 5.5 TB/s; for 64 rows 29.

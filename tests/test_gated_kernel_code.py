@@ -60,3 +60,32 @@ O.COUNTED.update(COUNTED)
 @pytest.mark.parametrize("name", sorted(COUNTED))
 def test_counted_waits(code_objects, name):  # noqa: F811
     O.test_counted_waits(code_objects, name)
+
+
+# both products in one launch: the two bodies of the kernels above in one
+PAIRS = {f"across_pair_{TYPES[ek]}": (f"_ZN2sl12_GLOBAL__N_116grad_pair_kernelILi{ek}EEEvNS_8GradPairE", 64, 32) for ek in (0, 1)}
+K.KERNELS.update(PAIRS)
+
+
+@pytest.mark.parametrize("name", sorted(PAIRS))
+def test_pair_of_products(code_objects, name):  # noqa: F811
+    symbol, in_loops, after = PAIRS[name]
+    L = K.disassemble(code_objects, symbol)
+    ops = [l.replace(",", " ").split() for l in L]
+    mf = [k for k, o in enumerate(ops) if o[0].startswith("v_mfma")]
+    assert len(mf) == in_loops + after
+    assert not [l for l in L if l.startswith("scratch_")], "scratch traffic"
+    assert all(ops[k][1] == ops[k][4] for k in mf), "not accumulating in place"
+    # runs of MFMAs (a loop's two statements, the products after it) hold no accumulator moves
+    for a, b in zip(mf, mf[1:]):
+        if b - a < 8:
+            assert not [L[k] for k in range(a, b) if ops[k][0].startswith("v_accvgpr")], L[a]
+    K.test_ring_kernel_barriers_follow_lds_waits(code_objects, name)
+
+
+@pytest.mark.parametrize("ek", [0, 1])
+@pytest.mark.parametrize("fm", [1, 2, 4])
+def test_few_rows_kernel_stays_in_registers(code_objects, ek, fm):  # noqa: F811
+    L = K.disassemble(code_objects, f"_ZN2sl12_GLOBAL__N_115grad_few_kernelILi{ek}ELi{fm}EEEvNS_10GradParamsE")
+    assert not [l for l in L if l.startswith("scratch_")], "scratch traffic"
+    assert [l for l in L if l.startswith("v_mfma")]
