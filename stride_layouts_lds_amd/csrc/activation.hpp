@@ -74,7 +74,9 @@ __device__ __forceinline__ void activate_with_slope(int32_t act, float v, float&
       return;
     }
     case ACT_GELU_TANH: {
-      const float q = kGeluCubic * v * v;
+      // (bounded: from 8.7e19 on v^2 leaves fp32, and infinity times the s (1 - s) = 0 that
+      // |v| above 10 has is no number; at the bound, |v| = 150, s is 0 or 1 to the last bit)
+      const float q = __builtin_fminf(kGeluCubic * v * v, 1e3f);
       const float s = sigmoid_of(kGeluTwoC * v * (1.f + q));
       a = v * s;
       slope = __builtin_fmaf(v * s * (1.f - s), kGeluTwoC * __builtin_fmaf(3.f, q, 1.f), s);

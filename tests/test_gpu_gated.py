@@ -1195,3 +1195,22 @@ def test_input_gradient_of_few_rows_of_shared_weights(api):
     api.gated_backward(*t, "gelu", need_dw=False, out=(out[:, 5:25], None, None))
     check_backward("gelu", (out[:, 5:25], None, None), *s)
     assert (out[:, :5] == 7).all() and (out[:, 25:] == 7).all()
+
+
+@pytest.mark.parametrize("kind", ACTS)
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_gated_backward_far_out(api, kind, dtype):
+    """Gates as large as the type holds, where the slope is 0 or 1 to the last
+    bit: with x and w_gate identities the gradients are dg and du themselves, and
+    with dh and u powers of two those are exact."""
+    import torch
+    t = dtype_of(dtype)
+    top = [1e3, 3e4, 65504.0] if dtype == "float16" else [1e3, 1e10, 8e18, 9e19, 1e30, 3e38]
+    v = torch.tensor((top + [-a for a in top] + [0.0] * 16)[:16], dtype=torch.float64, device="cuda").to(t)
+    g = v.expand(16, 16).contiguous()
+    dh, u = torch.full_like(g, 2.0 ** -3), torch.full_like(g, 2.0 ** -5)
+    eye, zero = torch.eye(16, device="cuda", dtype=t), torch.zeros(16, 16, device="cuda", dtype=t)
+    a, slope = activation(kind, g.double())
+    dg, du = (dh.double() * u.double() * slope).to(t), (dh.double() * a).to(t)
+    dx, dwg, dwu = api.gated_backward(dh, eye, eye, zero, g, u, kind)
+    assert torch.equal(dwg, dg.t()) and torch.equal(dwu, du.t()) and torch.equal(dx, dg)
