@@ -407,7 +407,14 @@ sl_status sl_gated_workspace_bytes(const sl_gated_args* args, int64_t* bytes);
  * not broadcast and overlap nothing (dw_gate and dw_up may be halves as gate and
  * up).  Without tokens (M or the batch 0) the
  * weights' gradients are zeros; with F 0 dx is.  M and K are below 2^30, F below
- * 2^29 (else SL_ERR_SHAPE).  Workspace as sl_gated: dg and du, 4 bytes for each
+ * 2^29, and 256 rows of what a product reads (all, where there are fewer) span less
+ * than 2^31 bytes.  For dx that is dg and du, 4 bytes for each f, F to a multiple of 64 (F
+ * below 2^21 - 63 from 256 tokens on), and, where the weights are not read as they lie, the
+ * K rows of their transposes, as long.  For the weights' gradients it is the F rows of
+ * dg's and du's transposes and the K rows of x's, 2 bytes for each token (fewer than 2^22 -
+ * 63 tokens with F or K from 256 on; of sequences that do not follow each other, each
+ * counted to a multiple of 64).  Else, and for more tiles than a launch holds (sl_gemm's
+ * sizes), SL_ERR_SHAPE.  Workspace as sl_gated: dg and du, 4 bytes for each
  * (m, f), F to a multiple of 64; where a product does not read its operands as they lie
  * also their transposes: of dg and du, of x, of the weights; for few rows dx's
  * fp32 sums of up to 256 workgroups' shares.

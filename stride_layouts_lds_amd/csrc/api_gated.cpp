@@ -669,14 +669,15 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
   };
   // a product of `count` matrices (m, k) and (n, k) of the workspace, k values a row
   auto product = [&](sl::DenseParams* p, sl::DensePlan* tile, int64_t count, int64_t m, int64_t n, int64_t k, int64_t a_bs, int64_t b_bs,
-                     int shift) -> sl_status {
+                     int shift) {
     p->M = m, p->N = n, p->K = 2 * k, p->batch = (int32_t)count, p->b_shift = shift;
     p->a_rs = p->b_rs[0] = 2 * k, p->a_bs = 2 * a_bs, p->b_bs[0] = 2 * b_bs;
     p->type = g.type;
-    if (256 * 2 * k >= kLim) return fail(SL_ERR_SHAPE, "a 256-row tile of an operand spans 2^31 bytes or more");
     *tile = sl::dense_plan(false, count, m, n, 2 * k);
-    return SL_OK;
   };
+  // the rows of a tile that are there span less than 2^31 bytes, of k values each
+  auto fits = [](int64_t rows, int64_t k) { return std::min<int64_t>(rows, 256) * 2 * k < kLim; };
+  auto too_long = [] { return fail(SL_ERR_SHAPE, "a 256-row tile of an operand spans 2^31 bytes or more"); };
   auto output = [&](sl::DenseParams* p, int i, const sl_tensor& d, const View& v, int64_t count) {
     p->kept[i] = d.data, p->kept_rs[i] = v.rs, p->kept_cs[i] = v.cs, p->kept_bs[i] = count > 1 ? v.bs : 0;
     if (quad_rows(v, count)) p->flags |= sl::DF_KEPT_VEC << i;
@@ -697,23 +698,25 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
            v->rows * v->rs * 2 + 1024 < kLim;
     return ok;
   };
-  auto choose = [&](const sl::DenseParams& p, bool ok, double copies, sl::DensePlan* tile) {
+  auto choose = [&](const sl::DenseParams& p, bool ok, bool copy, double copies, sl::DensePlan* tile) {
     sl::DensePlan large = sl::ring_plan(sl::DT_256x256, 256, 256, sl::kRing), small = sl::ring_plan(sl::DT_128x128, 128, 128, sl::kRing);
     large.us = sl::dense_large_us(p.batch, p.M, p.N, p.K);
     small.us = sl::grad_tiles_us((double)p.batch * (double)ceil_div(p.M, 128) * (double)ceil_div(p.N, 128), (double)ceil_div(p.K, 128));
     const sl::DensePlan& best = small.us < large.us ? small : large;
     tile->us += copied_us(copies);
-    if (!ok || best.us > tile->us) return false;
+    if (!ok || (copy && best.us > tile->us)) return false;
     *tile = best;
     return true;
   };
-  bool dx_ok = false, dw_ok = false;
+  bool dx_ok = false, dw_ok = false, dx_copy = true, dw_copy = true;  // on operands as they lie, with copies: possible
   double dx_copies = 0.0, dw_copies = 0.0;
   if (P.want_dx) {
-    if ((s = product(&P.dx.d, &P.dx_tile, n, rows, K, tokens ? 2 * Fp : 0, rows * 2 * Fp, one_weight ? 0 : K * 2 * Fp, 0)) != SL_OK) return s;
-    dx_ok = readable(w[WG], w[WU]);
+    if (tokens && !fits(rows, 2 * Fp)) return too_long();  // dg and du
+    product(&P.dx.d, &P.dx_tile, n, rows, K, tokens ? 2 * Fp : 0, rows * 2 * Fp, one_weight ? 0 : K * 2 * Fp, 0);
+    dx_ok = readable(w[WG], w[WU]), dx_copy = !tokens || fits(K, 2 * Fp);
+    if (!dx_ok && !dx_copy) return too_long();
     if (tokens) dx_copies = 8.0 * (double)weights * (double)F * (double)K;
-    P.dx_lies = choose(P.dx.d, dx_ok, dx_copies, &P.dx_tile);
+    P.dx_lies = choose(P.dx.d, dx_ok, dx_copy, dx_copies, &P.dx_tile);
     // Few rows: the weights read once (8192 x 4096's two, 134 MB in 24 to 29 us for up to 64 rows) and the
     // workgroups' sums joined, by the same kind of model.  us so and otherwise, from Python: 1 x 8192 x
     // 4096 31 and 69, 64 x 8192 x 4096 35 and 82, 512 x 8192 x 4096 111 and 147; 1 x 2048 x 2048 13
@@ -732,15 +735,17 @@ sl_status plan_backward(const sl_gated_backward_args* args, BackwardPlan* out) {
     }
   }
   if (P.want_dw) {
-    if ((s = product(&P.dw.d, &P.dw_tile, 2 * weights, F, K, tokens ? across : 0, Fp * across, K * across, 1)) != SL_OK) return s;
+    product(&P.dw.d, &P.dw_tile, 2 * weights, F, K, tokens ? across : 0, Fp * across, K * across, 1);
     dw_ok = (!one_weight || n == 1) && rows * 4 * Fp + 1024 < kLim && readable(w[X], w[X]);
+    dw_copy = !tokens || fits(std::max(F, K), across);
+    if (!dw_ok && !dw_copy) return too_long();
     // (with dx wanted too dg and du are written both ways where they are not read as they lie)
     if (tokens) dw_copies = 4.0 * (double)n * (double)rows * (double)(K + (P.want_dx ? F : 0));
-    P.dw_lies = choose(P.dw.d, dw_ok, dw_copies, &P.dw_tile);
+    P.dw_lies = choose(P.dw.d, dw_ok, dw_copy, dw_copies, &P.dw_tile);
   }
   if (P.want_dx && P.want_dw) {
     sl::DensePlan copied = sl::dense_pair_plan(P.dx.d, P.dw.d), lying = sl::ring_plan(sl::DT_128x128, 128, 128, sl::kRing);
-    copied.us += copied_us(dx_copies + dw_copies);
+    copied.us += dx_copy && dw_copy ? copied_us(dx_copies + dw_copies) : 1e30;
     lying.us = dx_ok && dw_ok ? sl::pair_us(sl::pair_128x128(), P.dx.d, P.dw.d, true) : 1e30;
     const sl::DensePlan& both = lying.us < copied.us ? lying : copied;
     sl::DenseParams x = P.dx.d, y = P.dw.d;

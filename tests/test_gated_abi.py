@@ -421,3 +421,59 @@ def test_operands_of_another_device_are_refused(api, monkeypatch):  # noqa: F811
     assert api._one_device(Operand(3)) == 3
     # descriptors alone: nothing to check
     assert api._one_device(None, api.sl_tensor()) is None
+
+
+def sized(m, f, k, batch=(), pitch=None, off=0, **wanted):
+    """A backward call of that size (sequences ``pitch`` rows apart), ``off`` bytes
+    behind a boundary of 16 where the weights and x start."""
+    wide = lambda at, rows, cols: rm(at, (*batch, rows, cols), BF16, *([((pitch or rows) * cols, cols, 1)] if batch else []))
+    apart = lambda i: i << 42  # 4 TiB
+    t = dict(dh=wide(apart(1), m, f), x=wide(apart(2) + off, m, k), w_gate=rm(apart(3) + off, (f, k), BF16), w_up=rm(apart(4) + off, (f, k), BF16),
+             gate=wide(apart(5), m, f), up=wide(apart(6), m, f), dx=wide(apart(7), m, k), dw_gate=rm(apart(8), (f, k), BF16),
+             dw_up=rm(apart(9), (f, k), BF16))
+    return {**t, **wanted}
+
+
+NO_DX, NO_DW = dict(dx=None), dict(dw_gate=None, dw_up=None)
+
+
+@pytest.mark.parametrize("call,accepted", [
+    # many tokens: the transposes' 64 rows span 2^29 bytes
+    (sized(1 << 22, 64, 64), True),
+    (sized(1 << 22, 64, 64, off=2), True),
+    (sized(1 << 24, 64, 64, off=2), False),
+    (sized((1 << 24) - 64, 64, 64, off=2), True),
+    # ... 256 of them 2^31; read as they lie nothing of the kind
+    (sized((1 << 22) - 64, 256, 256), True),
+    (sized((1 << 22) - 63, 256, 256), False),
+    (sized(1 << 22, 256, 256), False),
+    (sized(1 << 22, 256, 256, **NO_DW), True),
+    (sized(1 << 22, 64, 256), False),   # (x itself spans 2^31)
+    (sized(1 << 22, 64, 256, x=rm(2 << 42, (1 << 22, 256), BF16, (0, 1))), True),
+    # a wide block: rows of dg and du
+    (sized(64, 1 << 21, 64), True),
+    (sized(255, 1 << 21, 64), True),
+    (sized(256, (1 << 21) - 64, 64), True),
+    (sized(256, (1 << 21) - 63, 64), False),
+    (sized(256, 1 << 21, 64, **NO_DX), True),
+    # ... and the weights' transposes
+    (sized(1, 1 << 21, 256), True),
+    (sized(1, 1 << 21, 256, off=2), False),
+    (sized(1, (1 << 21) - 64, 256, off=2), True),
+    (sized(1, 1 << 21, 255, off=2), True),
+    (sized(1, 1 << 28, 8, **NO_DW), False),
+    (sized(1, (1 << 29) - 1, 1), False),
+    # sequences of two tokens that do not follow each other, 64 each; that do
+    (sized(2, 64, 64, (1 << 16,), 3), True),
+    (sized(2, 256, 64, (1 << 16,), 3), False),
+    (sized(2, 256, 64, ((1 << 16) - 1,), 3), True),
+    (sized(2, 256, 64, (1 << 16,)), True),
+])
+def test_gated_backward_sizes(api, call, accepted):  # noqa: F811
+    """256 rows of what a product reads, or all of fewer, span less than 2^31 bytes."""
+    L, args = api.lib(), backward_args(api, **call)
+    if accepted:
+        assert workspace(api, L.sl_gated_backward_workspace_bytes, args) > 0
+    else:
+        n = ctypes.c_int64(0)
+        assert api.STATUS[L.sl_gated_backward_workspace_bytes(ctypes.byref(args), ctypes.byref(n))] == "SL_ERR_SHAPE"

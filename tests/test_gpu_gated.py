@@ -1214,3 +1214,31 @@ def test_gated_backward_far_out(api, kind, dtype):
     dg, du = (dh.double() * u.double() * slope).to(t), (dh.double() * a).to(t)
     dx, dwg, dwu = api.gated_backward(dh, eye, eye, zero, g, u, kind)
     assert torch.equal(dwg, dg.t()) and torch.equal(dwu, du.t()) and torch.equal(dx, dg)
+
+
+@pytest.mark.parametrize("size", [(1 << 22, 64, 64), (1 << 22, 40, 61), (64, 1 << 21, 64), (3, (1 << 21) + 40, 61)])
+def test_gated_backward_of_many_tokens_and_wide_blocks(api, size):
+    """Whole numbers whose sums fp32 holds exactly (below 2^24): bit for bit."""
+    import torch
+    M, F, K = size
+    bits = lambda seed, *shape: integers(seed, -1, 1, *shape).to(torch.int8).bfloat16()
+    dh, x, wg, wu = bits(1, M, F), bits(2, M, K), bits(3, F, K), bits(4, F, K)
+    g, u = bits(5, M, F), bits(6, M, F)
+    dx, dwg, dwu = api.gated_backward(dh, x, wg, wu, g, u, "relu")
+    dg, du = (dh * u * (g > 0)).double(), (dh * g.clamp_min(0)).double()
+    assert torch.equal(dwg, (dg.t() @ x.double()).bfloat16()) and torch.equal(dwu, (du.t() @ x.double()).bfloat16())
+    assert torch.equal(dx, (dg @ wg.double() + du @ wu.double()).bfloat16())
+
+
+def test_gated_backward_of_many_sequences_apart(api):
+    """2^16 sequences of two tokens with a row between them, weights shared."""
+    import torch
+    B, M, F, K = 1 << 16, 2, 64, 48
+    bits = lambda seed, *shape: integers(seed, -1, 1, *shape).to(torch.int8).bfloat16()
+    dh, wg, wu, g, u = bits(1, B, M, F), bits(3, F, K), bits(4, F, K), bits(5, B, M, F), bits(6, B, M, F)
+    x = bits(2, B, M + 1, K)[:, 1:]
+    dx, dwg, dwu = api.gated_backward(dh, x, wg, wu, g, u, "relu")
+    dg, du = ((dh * u * (g > 0)).double().view(-1, F), (dh * g.clamp_min(0)).double().view(-1, F))
+    flat = x.double().reshape(-1, K)
+    assert torch.equal(dwg, (dg.t() @ flat).bfloat16()) and torch.equal(dwu, (du.t() @ flat).bfloat16())
+    assert torch.equal(dx, (dg @ wg.double() + du @ wu.double()).bfloat16().view(B, M, K))
