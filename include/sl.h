@@ -373,8 +373,11 @@ sl_status sl_quantize_rows(const sl_quantize_rows_args* args, void* stream);
  * are K-contiguous with rows on 16-byte boundaries and K % 16 == 0.
  * Outputs may have any strides that do not broadcast and overlap nothing; gate
  * and up may be the two halves of one matrix (of its rows or its columns).
- * M or F or the batch 0: a no-op; K 0: zeros.  F and K are below 2^30 (else
- * SL_ERR_SHAPE).  Asynchronous on `stream`; errors as sl_gemm, SL_ERR_ARG for another activation.
+ * M or F or the batch 0: a no-op; K 0: zeros.  F and K are below 2^30, and 256 rows
+ * of an operand as it is read (all, where it has fewer) span less than 2^31 bytes (16-bit K
+ * below 2^22 - 7 from 256 rows on; rows of 16-bit values that lie farther apart are
+ * copied); else, and for more tiles than a launch holds (sl_gemm's sizes),
+ * SL_ERR_SHAPE.  Asynchronous on `stream`; errors as sl_gemm, SL_ERR_ARG for another activation.
  */
 typedef enum { SL_SILU = 1, SL_GELU = 2, SL_GELU_TANH = 3, SL_RELU = 4 } sl_activation;
 

@@ -477,3 +477,32 @@ def test_gated_backward_sizes(api, call, accepted):  # noqa: F811
     else:
         n = ctypes.c_int64(0)
         assert api.STATUS[L.sl_gated_backward_workspace_bytes(ctypes.byref(args), ctypes.byref(n))] == "SL_ERR_SHAPE"
+
+
+@pytest.mark.parametrize("m,f,k,pitch,ws,dtype", [
+    (300, 8, (1 << 22) - 8, None, 0, BF16),
+    (300, 8, (1 << 22) - 7, None, None, BF16),                 # rows of 2^22 values, copied
+    (300, 8, 1 << 22, None, None, BF16),
+    (8, 256, 1 << 22, None, None, BF16),
+    (255, 255, 1 << 22, None, 0, BF16),
+    (1, 1, (1 << 30) - 8, None, 0, BF16),
+    (1, 1, (1 << 30) - 1, None, None, BF16),
+    (1, 1, 1 << 30, None, None, BF16),
+    (300, 8, 64, 1 << 23, 300 * 64 * 2, BF16),                 # rows 2^24 bytes apart: copied
+    (300, 8, 64, 1 << 23, 0, I8),                              # ... 2^23
+    (300, 8, 64, 1 << 24, None, I8),                           # int8 codes are not
+    (100, 8, 64, 1 << 24, 0, I8),
+])
+def test_gated_sizes(api, m, f, k, pitch, ws, dtype):  # noqa: F811
+    """256 rows of what is read, or all of fewer, span less than 2^31 bytes."""
+    apart = lambda i: i << 42
+    t = dict(x=rm(apart(1), (m, k), dtype, (pitch or k, 1)), w_gate=rm(apart(2), (f, k), dtype), w_up=rm(apart(3), (f, k), dtype),
+             h=rm(apart(4), (m, f), BF16))
+    if dtype == I8:
+        t.update(sx=rm(apart(5), (m, 1), F32), s_gate=rm(apart(6), (f, 1), F32), s_up=rm(apart(7), (f, 1), F32))
+    args = gated_args(api, **t)
+    if ws is None:
+        n = ctypes.c_int64(0)
+        assert api.STATUS[api.lib().sl_gated_workspace_bytes(ctypes.byref(args), ctypes.byref(n))] == "SL_ERR_SHAPE"
+    else:
+        assert workspace(api, api.lib().sl_gated_workspace_bytes, args) == ws
