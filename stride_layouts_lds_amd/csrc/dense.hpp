@@ -115,13 +115,15 @@ struct RowLoader {
   // index a member array inside the builtin's argument list.)
   __device__ __forceinline__ void issue_full(int32_t t, char* lds, int j) const {
     const uint32_t v = voff[j];
-    const uint32_t s = (uint32_t)(t * RB);
+    const uint32_t s = (uint32_t)t * RB;
     const __amdgpu_buffer_rsrc_t from = rsrc[src(j)];
     __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void_t*)(lds + (j * WAVES + wave) * 1024), 16, v, s, 0, 0);
   }
-  // copy j of any K-tile
+  // copy j of any K-tile (counted in 32 bits without a sign: K is below 2^31, a K-tile
+  // requested ahead of the last one may start past that)
   __device__ __forceinline__ void issue_one(int32_t t, char* lds, int j) const {
-    const uint32_t at = voff[j] == kOutOfRange || t * RB + 16 * chunk(j) >= K ? kOutOfRange : voff[j] + (uint32_t)(t * RB);
+    const uint32_t s = (uint32_t)t * RB;
+    const uint32_t at = voff[j] == kOutOfRange || s + (uint32_t)(16 * chunk(j)) >= (uint32_t)K ? kOutOfRange : voff[j] + s;
     const __amdgpu_buffer_rsrc_t from = rsrc[src(j)];
     __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void_t*)(lds + (j * WAVES + wave) * 1024), 16, at, 0, 0, 0);
   }
@@ -561,7 +563,7 @@ __global__ __launch_bounds__(kDenseSkinnyWaves * 64) void dense_skinny_kernel(co
 #pragma unroll
   for (int s = 0; s < (GATED ? 2 : 1); ++s)
     rb[s] = make_rsrc(p.b[s] + (batch >> p.b_shift) * p.b_bs[s] + n0 * p.b_rs[s], (uint32_t)((cols - 1) * p.b_rs[s] + p.K));
-  const int32_t kl = 16 * (lane >> 4), K = (int32_t)p.K;
+  const uint32_t kl = 16 * (lane >> 4), K = (uint32_t)p.K;
   const uint32_t off_a = (lane & 15) < rows ? (uint32_t)((lane & 15) * p.a_rs + kl) : kOutOfRange;
   uint32_t off_b[FN];
 #pragma unroll
@@ -573,11 +575,11 @@ __global__ __launch_bounds__(kDenseSkinnyWaves * 64) void dense_skinny_kernel(co
     u32x4 a[2], b[FN][2];
   };
   auto load = [&](int32_t t, Regs& x) {
-    const int32_t k = t * kRowBytes;
+    const uint32_t k = (uint32_t)t * kRowBytes;  // (may pass 2^31, as in RowLoader::issue_one)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const bool in = k + kl + 64 * h < K;
-      const uint32_t at = (uint32_t)(k + 64 * h);
+      const uint32_t at = k + 64 * h;
+      const bool in = at + kl < K;
 #pragma unroll
       for (int j = 0; j < FN; ++j)
         x.b[j][h] = __builtin_amdgcn_raw_buffer_load_b128(rb[j / OUT], in && off_b[j] != kOutOfRange ? off_b[j] + at : kOutOfRange, 0, 0);

@@ -1242,3 +1242,25 @@ def test_gated_backward_of_many_sequences_apart(api):
     flat = x.double().reshape(-1, K)
     assert torch.equal(dwg, (dg.t() @ flat).bfloat16()) and torch.equal(dwu, (du.t() @ flat).bfloat16())
     assert torch.equal(dx, (dg @ wg.double() + du @ wu.double()).bfloat16().view(B, M, K))
+
+
+def test_gated_longest_rows(api):
+    """K of 2^30 - 8: rows that end 16 bytes short of 2^31.  Whole numbers whose
+    sums fp32 holds exactly."""
+    import torch
+    K = (1 << 30) - 8
+
+    def bits(seed):
+        out = torch.empty(1, K, dtype=torch.bfloat16, device="cuda")
+        generator = gen(seed)
+        for part in out[0].split(1 << 26):
+            part.copy_(torch.randint(-1, 2, part.shape, generator=generator, device="cuda", dtype=torch.int8))
+        return out
+    x, wg, wu = bits(1), bits(2), bits(3)
+    x[0, -8:], wg[0, -8:], wu[0, -8:] = 1, 30, 60      # the last chunk counts
+    h, g, u = api.gated(x, wg, wu, "relu", keep=True)
+    dot = lambda w: sum(int((a.int() * b.int()).sum()) for a, b in zip(x[0].split(1 << 26), w[0].split(1 << 26)))
+    G, V = dot(wg), dot(wu)
+    assert abs(G) < 1 << 20 and abs(V) < 1 << 20
+    of = lambda v: float(torch.tensor(v, dtype=torch.float32).bfloat16())
+    assert float(g) == of(G) and float(u) == of(V) and float(h) == of(float(max(G, 0) * V))
