@@ -32,8 +32,8 @@ struct RowScale {
   typedef typename std::conditional<T == OT_F32, double, float>::type R;
   R d, r;   // 2^-7 top and its reciprocal (no overflow at the largest top)
   float s;
-  __device__ __forceinline__ explicit RowScale(uint32_t top_bits) {
-    const bool bad = top_bits >= kInfBits;
+  bool bad; // the row holds a NaN or an infinity: its codes are 0, and code() is not asked (a NaN has no integer)
+  __device__ __forceinline__ explicit RowScale(uint32_t top_bits) : bad(top_bits >= kInfBits) {
     const float top = fmaxf(__builtin_bit_cast(float, bad ? 0x3F800000u : top_bits), 0x1p-100f);
     constexpr float k = 1.f / 127.f;
     const float s0 = top * k;
@@ -45,7 +45,6 @@ struct RowScale {
       const float r0 = __builtin_amdgcn_rcpf(d);
       r = __builtin_fmaf(__builtin_fmaf(-d, r0, 1.f), r0, r0);
     }
-    if (bad) r = 0, d = 0;  // codes 0
   }
   __device__ __forceinline__ int32_t code(float x) const {
     const R v = (R)x * (R)0.9921875f;  // 127 / 128
@@ -75,7 +74,6 @@ __device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* lds) {
   return m;
 }
 
-template <int T>
 __device__ __forceinline__ void store8(int8_t* q, int64_t c, int64_t q_cols, const int32_t (&w)[8]) {
   uint32_t lo = 0, hi = 0;
 #pragma unroll
@@ -87,6 +85,12 @@ __device__ __forceinline__ void store8(int8_t* q, int64_t c, int64_t q_cols, con
     for (int e = 0; e < 8; ++e)
       if (c + e < q_cols) q[c + e] = (int8_t)w[e];
   }
+}
+
+// the codes of a row without numbers, a thread's: columns c0 .. + 7 of every `step`
+__device__ __forceinline__ void store_zeros(int8_t* q, int64_t c0, int64_t step, int64_t q_cols) {
+  const int32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int64_t c = c0; c < q_cols; c += step) store8(q, c, q_cols, w);
 }
 
 // Rows contiguous: TPR threads to a row, which holds it in registers (VPT
@@ -124,7 +128,7 @@ __global__ __launch_bounds__(256) void quantize_whole_rows_kernel(const Quantize
     int32_t w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = s.code(widen<T>(v[e]));
-    store8<T>(Q, c, p.q_cols, w);
+    store8(Q, c, p.q_cols, w);
   };
   uint32_t m = 0;
   if constexpr (VPT > 0) {
@@ -133,8 +137,9 @@ __global__ __launch_bounds__(256) void quantize_whole_rows_kernel(const Quantize
     for (int i = 0; i < VPT; ++i) v[i] = load(8 * (t + (int64_t)TPR * i));
 #pragma unroll
     for (int i = 0; i < VPT; ++i) m = top(v[i], m);
-    const RowScale<T> s(row_max<TPR>(m, lds));
+    const RowScale<T> s((uint32_t)__builtin_amdgcn_readfirstlane((int)row_max<TPR>(m, lds)));  // one for the wave
     if (t == 0) p.s[b * p.s_bs + row * p.s_rs] = s.s;
+    if (s.bad) return store_zeros(Q, 8 * t, 8 * TPR, p.q_cols);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int64_t c = 8 * (t + (int64_t)TPR * i);
@@ -142,8 +147,9 @@ __global__ __launch_bounds__(256) void quantize_whole_rows_kernel(const Quantize
     }
   } else {
     for (int64_t c = 8 * t; c < p.cols; c += 8 * TPR) m = top(load(c), m);
-    const RowScale<T> s(row_max<TPR>(m, lds));
+    const RowScale<T> s((uint32_t)__builtin_amdgcn_readfirstlane((int)row_max<TPR>(m, lds)));  // one for the wave
     if (t == 0) p.s[b * p.s_bs + row * p.s_rs] = s.s;
+    if (s.bad) return store_zeros(Q, 8 * t, 8 * TPR, p.q_cols);
     for (int64_t c = 8 * t; c < p.q_cols; c += 8 * TPR) write(s, load(c), c);
   }
 }
@@ -174,6 +180,10 @@ __global__ __launch_bounds__(64 * kStridedWaves) void quantize_strided_rows_kern
   const RowScale<T> s(m);
   if (wave == 0) p.s[b * p.s_bs + row * p.s_rs] = s.s;
   int8_t* Q = p.q + b * p.q_bs + row * p.q_rs;
+  if (s.bad) {
+    for (int32_t h = 0; h < 16; h += 8) store_zeros(Q, 16 * wave + h, 16 * kStridedWaves, p.q_cols);
+    return;
+  }
   for (int64_t c = 16 * wave; c < p.q_cols; c += 16 * kStridedWaves) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -183,7 +193,7 @@ __global__ __launch_bounds__(64 * kStridedWaves) void quantize_strided_rows_kern
         const int64_t at = c + 8 * h + e;
         w[e] = at < p.cols ? s.code(widen<T>(X[at * p.x_cs])) : 0;
       }
-      if (c + 8 * h < p.q_cols) store8<T>(Q, c + 8 * h, p.q_cols, w);
+      if (c + 8 * h < p.q_cols) store8(Q, c + 8 * h, p.q_cols, w);
     }
   }
 }

@@ -1264,3 +1264,16 @@ def test_gated_longest_rows(api):
     assert abs(G) < 1 << 20 and abs(V) < 1 << 20
     of = lambda v: float(torch.tensor(v, dtype=torch.float32).bfloat16())
     assert float(g) == of(G) and float(u) == of(V) and float(h) == of(float(max(G, 0) * V))
+
+
+@pytest.mark.parametrize("rows,cols,how", [(5, 100, "rows"), (5, 3000, "rows"), (1100, 3000, "rows"), (5, 9000, "rows"), (5, 20000, "rows"), (70, 100, "cols")])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16", "float32"])
+def test_quantize_rows_of_no_numbers(api, dtype, rows, cols, how):
+    """Rows of NaN alone, of infinities alone and of both among numbers: scale NaN, codes 0."""
+    import torch
+    x = normal(6, rows, cols).to(dtype_of(dtype))
+    clean = api.quantize_rows(x)
+    x[0], x[1], x[2, ::2], x[2, 1::4], x[3, cols // 2] = float("nan"), -float("inf"), float("inf"), float("nan"), float("inf")
+    q, s = api.quantize_rows(strided(x, how))
+    assert torch.isnan(s[:4]).all() and not q[:4].any()
+    assert torch.equal(q[4:], clean[0][4:]) and torch.equal(s[4:], clean[1][4:])
