@@ -278,7 +278,7 @@ def _one_device(*operands) -> Optional[int]:
     for x in operands:
         if x is None or isinstance(x, sl_tensor):
             continue
-        at = x.get_device()
+        at = x.get_device() if not isinstance(x, PackedTensor) else x.storage.get_device()
         if at < 0:
             _check_devices(x)
         if index is None:

@@ -506,3 +506,29 @@ def test_gated_sizes(api, m, f, k, pitch, ws, dtype):  # noqa: F811
         assert api.STATUS[api.lib().sl_gated_workspace_bytes(ctypes.byref(args), ctypes.byref(n))] == "SL_ERR_SHAPE"
     else:
         assert workspace(api, api.lib().sl_gated_workspace_bytes, args) == ws
+
+
+def test_packed_operands_are_refused_with_a_reason(api, monkeypatch):  # noqa: F811
+    """Packed 6-bit data beside other operands: the library's
+    refusal of its type, and host memory before that."""
+    import torch
+
+    class OnGpu(torch.Tensor):   # a host tensor that says it is on device 1
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    gpu = lambda *shape, dtype: torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+    q, s, d = gpu(64, 128, dtype=torch.int8), gpu(64, 1, dtype=torch.float32), gpu(64, 64, dtype=torch.bfloat16)
+    h, w = gpu(64, 128, dtype=torch.float16), gpu(32, 128, dtype=torch.float16)
+    packed = lambda make: api.PackedTensor(make(64 * 96, dtype=torch.uint8), api.SL_F6_E2M3, (64, 128), (128, 1))
+    here, host = packed(gpu), packed(torch.zeros)
+    with pytest.raises(ValueError, match="GPU tensors"):
+        api._one_device(host)
+    assert api._one_device(here, q) == 1
+    for call in (lambda: api.gemm(q, here, out=d, sfa=s, sfb=s, stream=0), lambda: api.gemm(q, q, here, out=d, sfa=s, sfb=s, stream=0),
+                 lambda: api.gemm(q, q, out=d, sfa=here, sfb=s, stream=0), lambda: api.gated(h, here, w, out=d, stream=0)):
+        with pytest.raises(api.SLError) as e:
+            call()
+        assert e.value.name == "SL_ERR_DTYPE"
