@@ -292,7 +292,7 @@ def _one_device(*operands) -> Optional[int]:
 
 def make_args(a, b, c=None, d=None, sfa=None, sfb=None, block_k: int = 32, workspace=None) -> sl_gemm_args:
     """Arguments from descriptors (sl_tensor) or torch tensors; ``workspace``
-    is a device tensor (its bytes) or None."""
+    is a contiguous device tensor (its bytes) or None."""
     args = sl_gemm_args.from_buffer_copy(b"".join((_record(a), _record(b), _record(c), _record(d), _record(sfa),
                                                    _record(sfb), _GEMM_TAIL.pack(block_k, 0, 0))))
     if workspace is not None:
@@ -300,13 +300,20 @@ def make_args(a, b, c=None, d=None, sfa=None, sfb=None, block_k: int = 32, works
     return args
 
 
-def set_workspace(args, workspace) -> None:
-    """Point args at a device tensor's bytes as the call's workspace (None: none)."""
+def _workspace_bytes(workspace) -> tuple:
+    """Address and size of a workspace.  A tensor with gaps has other values between
+    its own, an expanded one fewer bytes than elements: neither is a buffer."""
     if workspace is None:
-        args.workspace, args.workspace_bytes = None, 0
-    else:
-        args.workspace = workspace.data_ptr() or None
-        args.workspace_bytes = workspace.numel() * workspace.element_size()
+        return 0, 0
+    if not workspace.is_contiguous():
+        raise ValueError("workspace is not contiguous: its bytes are used as one buffer")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def set_workspace(args, workspace) -> None:
+    """Point args at a contiguous device tensor's bytes as the call's workspace (None: none)."""
+    at, args.workspace_bytes = _workspace_bytes(workspace)
+    args.workspace = at or None
 
 
 # ---------------------------------------------------------------------------
@@ -397,7 +404,7 @@ def gemm(a, b, c=None, out=None, sfa=None, sfb=None, block_k: int = 32, stream: 
     C may be fp16, bf16 or float32 (``dtype``, or ``out``'s).  int8 ``a`` and
     ``b`` take one float32 scale per row, (batch?, rows, 1), as
     ``quantize_rows`` writes them; D and C as with those.  A plan's workspace (split-K partial sums, or NVFP4
-    operands decoded to fp16) is ``workspace`` (a device tensor) or, when
+    operands decoded to fp16) is ``workspace`` (a contiguous device tensor) or, when
     None, a torch allocation of the size the library asks for.  Returns ``out`` (allocated by torch if None).
     With ``stream`` (a stream's handle) the call runs there, and what it
     allocates belongs to that stream, as under ``torch.cuda.stream``."""
@@ -481,7 +488,7 @@ def orthogonalize(x, out=None, steps: int = 5, coefficients=None, workspace=None
     """Newton-Schulz orthogonalisation of each matrix of ``x`` ((batch?, M,
     N), fp16, bf16 or float32, any strides) as include/sl.h states it.
     ``coefficients``: (a, b, c) for every step or one triple per step (None:
-    the library's).  ``workspace``: a device tensor of at least
+    the library's).  ``workspace``: a contiguous device tensor of at least
     sl_orthogonalize_workspace_bytes, or None for a torch allocation.
     Returns ``out`` (x's dtype, bf16 for float32, if None).  ``stream`` as for
     ``gemm``."""
@@ -561,8 +568,7 @@ def _run_with_workspace(name: str, operands, tail: int, workspace, often: bool, 
         import torch
         make = lambda: torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
         workspace = make() if stream is None else _allocated(stream, device, make)
-    given = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _run(name, (records, _GATED_TAIL.pack(tail, *given)), index, stream)
+    _run(name, (records, _GATED_TAIL.pack(tail, *_workspace_bytes(workspace))), index, stream)
 
 
 def quantize_rows(x, out=None, stream: Optional[int] = None):
@@ -598,7 +604,7 @@ def gated(x, w_gate, w_up, activation: str = "silu", sx=None, s_gate=None, s_up=
     M, F), of x's dtype, for int8 ``dtype`` (fp16 if None, or bf16 or
     float32); with ``keep`` (h, gate, up), the two projections with it, for
     ``gated_backward``.  ``out``: the caller's h, or with ``keep`` its three tensors.
-    ``workspace``: a device tensor of at least sl_gated_workspace_bytes, or
+    ``workspace``: a contiguous device tensor of at least sl_gated_workspace_bytes, or
     None for a torch allocation where one is needed.  ``stream`` as for ``gemm``."""
     import torch
     act = _activation(activation)
@@ -628,7 +634,7 @@ def gated_backward(dh, x, w_gate, w_up, gate, up, activation: str = "silu", need
     (batch?, M, K) as dh is a batch or not, the others as the weights (summed over the
     batch where those are (F, K)).  All fp16 or all bf16, any strides.
     Without ``need_dx`` or ``need_dw`` those places hold None.  ``out``: the
-    same tuple of the caller's tensors.  ``workspace``: a device tensor of at least
+    same tuple of the caller's tensors.  ``workspace``: a contiguous device tensor of at least
     sl_gated_backward_workspace_bytes, or None for a torch allocation.
     ``stream`` as for ``gemm``."""
     import torch

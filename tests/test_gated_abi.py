@@ -532,3 +532,27 @@ def test_packed_operands_are_refused_with_a_reason(api, monkeypatch):  # noqa: F
         with pytest.raises(api.SLError) as e:
             call()
         assert e.value.name == "SL_ERR_DTYPE"
+
+
+def test_a_workspace_is_one_buffer(api, monkeypatch):  # noqa: F811
+    """A view with gaps holds other data between its bytes, an expanded tensor has
+    fewer than its elements say: a call would write memory that is not its own."""
+    import torch
+    monkeypatch.setattr(api, "_one_device", lambda *operands: 0)
+    monkeypatch.setattr(api, "_check_devices", lambda *operands: None)
+    rows = lambda *shape: torch.zeros(*shape, dtype=torch.float16)
+    kept, x, w, m = rows(64, 32), rows(64, 128), rows(32, 128), rows(64, 64)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 24), torch.zeros(1 << 12, 2, dtype=torch.float32)[:, 0],
+               torch.zeros(64, 256, dtype=torch.uint8)[:, :128]):
+        for call in (lambda **kw: api.gated(x[:, 1:8], w[:, 1:8], w[:, 1:8], stream=0, out=rows(64, 32), **kw),
+                     lambda **kw: api.gated_backward(kept, x, w, w, kept, kept, stream=0, out=(rows(64, 128), rows(32, 128), rows(32, 128)), **kw),
+                     lambda **kw: api.orthogonalize(m, out=rows(64, 64), stream=0, **kw),
+                     lambda **kw: api.gemm(x, w, out=rows(64, 32), stream=0, **kw)):
+            with pytest.raises(ValueError, match="contiguous"):
+                call(workspace=ws)
+    at = torch.zeros(8, 512, dtype=torch.uint8)[2:6]
+    args = api.sl_gated_args()
+    api.set_workspace(args, at)
+    assert (args.workspace, args.workspace_bytes) == (at.data_ptr(), 2048)
+    api.set_workspace(args, None)
+    assert (args.workspace, args.workspace_bytes) == (None, 0)
