@@ -23,9 +23,13 @@ namespace sl {
 //   4096 x 8192  59 126 372   68 145 432  53 129 446  324 458 1586
 // int8 (256 x 256, 256 x 192, 128 x 128): 4000 x 3000 x 256 / 2064 / 8192 16 14 13, 35 33 39,
 // 83 79 93; 3000 x 3000 x 2048 31 26 29; 4096 x 6144 x 4096 100 89 96; 8192 x 8192 x 2048
-// 133 155 141.  Up to 64 rows of A go streamed whatever it says (64 x 8192 x 4096 is read at
-// 4.4 TB/s), but up to 16 rows of few K-tiles, whose many workgroups only start and end
-// (gated, 15 of 4 x 4171 x 32: 21 us, in 128 x 128 tiles 10; 16 of 16 x 8192 x 128 47 and 22).
+// 133 155 141.  Up to 64 rows of A the streamed tiles read B once, and where that bounds the
+// call they stay (int8 16 of 17 x 8192 x 4096 120 us, in larger tiles 126; 64 x 8192 x 4096 is
+// read at 4.4 TB/s).  Elsewhere many workgroups only start and end (int8, streamed and in 128 x 128
+// tiles: 16 of 17 x 8192 x 128 31 and 10, 16 of 64 x 8192 x 256 45 and 15, 16 of 16 x 8192 x 1024 61
+// and 26; gated bf16 64 of 33 x 4096 x 64 148 and 35).  From 17 rows on a larger tile has to be
+// a fifth better than streamed ones in parts of a round: a last round that is not full costs less than
+// one (gated bf16 2 of 24 x 3744 x 1216 11 us streamed, by the model 15, and 13).
 //
 // A 128 x 128 tile alone on its CU waits for its copies where many K-tiles meet many
 // others': the deep ring has two K-tiles more on their way (gated bf16 512 x 1024 x 4096 33 ->
@@ -55,14 +59,17 @@ DensePlan dense_plan(bool gated, int64_t batch, int64_t M, int64_t N, int64_t K)
   const int32_t bn = batch * ceil_div(M, bm) * ceil_div(B, 64) >= kCUs ? 64 : 32;
   const int32_t stages = bm == 32 ? (bn == 32 ? 4 : 3) : (bn == 32 ? 3 : 2);
   DensePlan best = {DT_STREAM, bm, bn, kDenseStreamWaves * 64, kDenseStreamWaves * stages * (bm + bn) * 128, stages, 0.0};
-  const double groups = (double)batch * (double)ceil_div(M, bm) * (double)ceil_div(B, bn);
-  best.us = std::ceil(groups / kCUs) * (5.0 + T * (bn == 64 ? 0.2 : 0.13));
+  const double groups = (double)batch * (double)ceil_div(M, bm) * (double)ceil_div(B, bn), one = 5.0 + T * (bn == 64 ? 0.2 : 0.13);
+  best.us = std::ceil(groups / kCUs) * one;
+  double limit = M <= 64 ? 0.8 * std::max(1.0, groups / kCUs) * one : best.us;  // what a larger tile has to be below
   if (M <= 16) {
     const int32_t cols = gated || batch * ceil_div(N, 32) >= kCUs ? 32 : 16;
     const double rounds = (double)batch * (double)ceil_div(B, cols) / (2.0 * kCUs);  // two workgroups to a CU
     best = {DT_SKINNY, 16, cols, kDenseSkinnyWaves * 64, kDenseSkinnyWaves * cols / 16 * 1024, 0, std::ceil(rounds) * (3.0 + 0.1 * T)};
+    limit = best.us;
   }
-  if (K == 0 || (M <= 64 && (best.tile == DT_STREAM || T > 4))) return best;
+  const bool once = M <= 64 && best.us <= (double)batch * (double)B * (double)K / 4.5e6;  // one pass over B bounds it
+  if (K == 0 || once) return best;
   auto tiles = [&](int64_t rows_a, int64_t rows_b) { return (double)batch * (double)ceil_div(M, rows_a) * (double)ceil_div(B, rows_b); };
   const double t2 = tiles(128, 128);
   const bool deep = t2 <= kCUs && t2 * T >= 3500.0;
@@ -73,7 +80,7 @@ DensePlan dense_plan(bool gated, int64_t batch, int64_t M, int64_t N, int64_t K)
   large[2].us = std::ceil(tiles(256, 128) / kCUs) * (7.0 + 0.77 * T);
   large[3].us = dense_small_us(t2, T, deep);
   for (const DensePlan& t : large)
-    if (t.us < best.us) best = t;
+    if (t.us < limit) best = t, limit = t.us;
   return best;
 }
 

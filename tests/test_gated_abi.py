@@ -556,3 +556,21 @@ def test_a_workspace_is_one_buffer(api, monkeypatch):  # noqa: F811
     assert (args.workspace, args.workspace_bytes) == (at.data_ptr(), 2048)
     api.set_workspace(args, None)
     assert (args.workspace, args.workspace_bytes) == (None, 0)
+
+
+@pytest.mark.parametrize("batch,m,n,k,tile", [
+    # many matrices of few K-tiles: 128 x 128 on either side of 16 and of 64 rows
+    (16, 16, 8192, 128, (128, 128)), (16, 17, 8192, 128, (128, 128)), (16, 32, 8192, 128, (128, 128)), (16, 64, 8192, 128, (128, 128)),
+    (16, 65, 8192, 128, (128, 128)), (16, 16, 8192, 1024, (128, 128)), (16, 17, 8192, 1024, (128, 128)), (16, 64, 8192, 1024, (128, 128)),
+    (64, 32, 8192, 512, (128, 128)), (1, 16, 131072, 1024, (128, 128)), (1, 17, 131072, 1024, (128, 128)),
+    # one pass over B bounds the call
+    (16, 16, 8192, 4096, (16, 32)), (16, 17, 8192, 4096, (32, 64)), (16, 64, 8192, 8192, (64, 64)), (1, 48, 8192, 4096, (64, 32)),
+    (1, 1, 4096, 8192, (16, 16)),
+    # one round of workgroups, or little more
+    (1, 17, 1024, 2048, (32, 32)), (1, 24, 9440, 1664, (32, 32)), (2, 24, 7488, 2432, (32, 32)),
+])
+def test_few_rows_take_the_tile_that_is_less(api, batch, m, n, k, tile):  # noqa: F811
+    r3 = lambda at, dt, *s: rm(at, (batch, *s) if batch > 1 else s, dt)
+    p = api.sl_gemm_plan(gemm_args(api, a=r3(Z[0], I8, m, k), b=r3(Z[1], I8, n, k), d=r3(Z[2], BF16, m, n), sfa=r3(Z[3], F32, m, 1),
+                                   sfb=r3(Z[4], F32, n, 1), block_k=0))
+    assert (p["tile_m"], p["tile_n"]) == tile
