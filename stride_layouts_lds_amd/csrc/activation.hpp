@@ -5,7 +5,7 @@
 // distribution's (gelu, normal_of): no difference of nearly equal numbers where v is far
 // below zero.  The hardware's
 // exponential and reciprocal (one unit in the last place each) on t log2(e)
-// rounded: off by about (1 + |t|) 2^-23 of s, an eighth of fp16's rounding at
+// rounded: off by about (1 + |t|) 2^-23 of s, a fortieth of fp16's rounding at
 // |t| = 100.  They give zero for results below 2^-126: s is 0 for t below -87.
 #pragma once
 #include "sl_ops.hpp"
@@ -25,8 +25,10 @@ __device__ __forceinline__ float sigmoid_of(float t) {
 // for v below zero s = e t P(t), t = 1 / (1 + 0.35 |v|), above 1 less that.  P is
 // erfc(u / sqrt 2) e^(u^2 / 2) / (2 t) fitted on 0 <= u <= 14 (e is zero beyond) by least squares
 // whose weights move to the largest errors (Lawson's method): off by 0.5 2^-24 of
-// itself, 5.2 2^-24 as summed in fp32.  (With the library's erfcf dg and du of 8 experts of
-// 300 x 1000, 2.4 M of each, took 12 us, so 10.)
+// itself, 5.2 2^-24 as summed in fp32.  s below zero is off by up to (7 + v^2) 2^-24 of itself (9 at
+// -2, 18 at -4, 65 at -8, 127 at -12.4, before the hardware's e and t): e's argument is
+// rounded, which counts v^2 / 2 times; fp16's own rounding is 8192 2^-24.  (With the library's
+// erfcf dg and du of 8 experts of 300 x 1000, 2.4 M of each, took 12 us, so 10.)
 __device__ __forceinline__ void normal_of(float v, float& s, float& e) {
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.35f, __builtin_fabsf(v), 1.f));
   e = __builtin_amdgcn_exp2f(-0.5f * kLog2e * (v * v));

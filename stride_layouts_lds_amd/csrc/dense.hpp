@@ -353,9 +353,9 @@ __device__ __forceinline__ void dense_rows(const EPI& epi, const DenseParams& p,
 //   8 x 4  256 x 128, the same
 //   4 x 4  128 x 128, two to a CU
 // AHEAD K-tiles more on their way (dense_plan) take a CU's LDS.  The gated pair's wave
-// holds 8 FN rows of each matrix.  int8 8192^3 takes 392 us (2.8 POP/s), gated bf16 4096 x
-// 8192 x 4096 with both projections kept 400 us (1.37 PFLOP/s): the matrix cores are busy 70%
-// of the time, at 1.9 GHz (power).
+// holds 8 FN rows of each matrix.  int8 8192^3 takes 383 to 395 us (2.8 POP/s), gated bf16 4096 x
+// 8192 x 4096 with both projections kept 396 to 412 us (1.36 PFLOP/s), back to back on several
+// cards: the matrix cores are busy 70% of the time, at 1.9 GHz (power).
 // ---------------------------------------------------------------------------
 template <int EK, bool GATED, int FM, int FN, int AHEAD, class EPI, class PRODUCTS>
 __global__ __launch_bounds__(256, FM == 8 || AHEAD > 0 ? 1 : 2) void dense_ring_kernel(const PRODUCTS products_) {

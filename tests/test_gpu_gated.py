@@ -1277,3 +1277,19 @@ def test_quantize_rows_of_no_numbers(api, dtype, rows, cols, how):
     q, s = api.quantize_rows(strided(x, how))
     assert torch.isnan(s[:4]).all() and not q[:4].any()
     assert torch.equal(q[4:], clean[0][4:]) and torch.equal(s[4:], clean[1][4:])
+
+
+def test_gated_backward_past_fp16(api):
+    """A dg past 65504 is infinite: with it go its row of dx and its row of
+    dw_gate, and nothing else."""
+    import torch
+    for shape in ((5, 40, 72), (300, 520, 264)):
+        s = list(state(3, shape, "float16", "relu"))
+        s[4][2, 7], s[0][2, 7], s[5][2, 7] = 0.5, 0.25, 0.125
+        want = api.gated_backward(*s, "relu")
+        s[0][2, 7], s[5][2, 7] = 300.0, 300.0        # dg 90000, du 150
+        dx, dwg, dwu = api.gated_backward(*s, "relu")
+        m, f = torch.arange(shape[0], device="cuda") != 2, torch.arange(shape[1], device="cuda") != 7
+        assert not torch.isfinite(dx[2]).any() and not torch.isfinite(dwg[7]).any()
+        assert torch.equal(dx[m], want[0][m]) and torch.equal(dwg[f], want[1][f]) and torch.equal(dwu[f], want[2][f])
+        assert torch.isfinite(dwu).all()
