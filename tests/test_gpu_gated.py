@@ -1293,3 +1293,21 @@ def test_gated_backward_past_fp16(api):
         assert not torch.isfinite(dx[2]).any() and not torch.isfinite(dwg[7]).any()
         assert torch.equal(dx[m], want[0][m]) and torch.equal(dwg[f], want[1][f]) and torch.equal(dwu[f], want[2][f])
         assert torch.isfinite(dwu).all()
+
+
+@pytest.mark.parametrize("batch,M,N,K", [(16, 1, 8190, 1040), (16, 16, 8190, 1040), (16, 17, 8190, 144), (24, 33, 2100, 528), (16, 64, 8190, 1040),
+                                         (1, 17, 70001, 256), (1, 64, 140000, 80)])
+def test_few_rows_in_large_tiles(api, batch, M, N, K):
+    """Up to 64 rows where reading B once does not bound the call."""
+    a, b, sa, sb = codes(1, batch, M, K), codes(2, batch, N, K), scales(3, batch, M), scales(4, batch, N)
+    d = normal(5, batch, M, N).bfloat16()
+    args = api.make_args(a, b, None, d, sa, sb)
+    assert api.sl_gemm_plan(args)["tile_m"] >= 128
+    check_int8(api, a, b, sa, sb)
+    check_int8(api, a, b, sa, sb, d)
+    if batch > 1:
+        for dtype in ("float16", "bfloat16"):
+            x, wg, wu = block(1, (M, N // 2, K // 2), dtype, (batch,))
+            check_gated("gelu", api.gated(x, wg, wu, "gelu", keep=True), x, wg, wu)
+            s = state(2, (M, N // 8, K // 2), dtype, "silu", (batch,))
+            check_backward("silu", api.gated_backward(*s, "silu"), *s)
