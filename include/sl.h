@@ -401,7 +401,7 @@ sl_status sl_gated_workspace_bytes(const sl_gated_args* args, int64_t* bytes);
  *     dx = dg w_gate + du w_up,   dw_gate = dg^T x,   dw_up = du^T x,
  * act' being 0 at 0 for SL_RELU.  dg and du are rounded to the operands' type, in
  * which they are multiplied; sums are in fp32, each gradient rounded once.  In f16 a
- * dg or du past 65504 is infinite, and with it its row of dx and its row of dw_gate or
+ * dg or du from 65520 on is infinite, and with it its row of dx and its row of dw_gate or
  * dw_up infinite or NaN, whatever their sums would have been, and one up to 2^-25 is zero: a
  * loss scaled for f16 gradients keeps both in range.
  *   dh, gate, up  (batch?, M, F), x (batch?, M, K), w_gate and w_up (batch?, F,
@@ -423,9 +423,10 @@ sl_status sl_gated_workspace_bytes(const sl_gated_args* args, int64_t* bytes);
  * sizes), SL_ERR_SHAPE.  Workspace as sl_gated: dg and du, 4 bytes for each
  * (m, f), F to a multiple of 64; where a product does not read its operands as they lie
  * also their transposes: of dg and du, of x, of the weights; for few rows dx's
- * fp32 sums of up to 256 workgroups' shares.  With shared weights a batch whose matrices do
- * not follow each other (in dh, x, gate, up or dx) is always transposed, each matrix's tokens
- * to a multiple of 64: short sequences with rows between them are better copied together first.
+ * fp32 sums of up to 256 workgroups' shares.  For shared weights' gradients of a batch whose
+ * matrices do not follow each other (in dh, x, gate, up or dx) those of dg, du and x are always
+ * made, each matrix's tokens to a multiple of 64: short sequences with rows between them are
+ * better copied together first.
  * Asynchronous on `stream`; results do not vary from call to call.
  */
 typedef struct {

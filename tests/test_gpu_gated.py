@@ -1280,7 +1280,7 @@ def test_quantize_rows_of_no_numbers(api, dtype, rows, cols, how):
 
 
 def test_gated_backward_past_fp16(api):
-    """A dg past 65504 is infinite: with it go its row of dx and its row of
+    """A dg from 65520 on is infinite: with it go its row of dx and its row of
     dw_gate, and nothing else."""
     import torch
     for shape in ((5, 40, 72), (300, 520, 264)):
